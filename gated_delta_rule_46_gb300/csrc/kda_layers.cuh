@@ -1,0 +1,98 @@
+// kda_layers.cuh -- what the translation units of the layer operators
+// (include/kda_layers.h) share: parameter blocks, launchers, small helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_common.cuh"
+#include "kda_layers.h"
+
+namespace kda {
+
+struct LinearParams {
+    const __nv_bfloat16 *x;
+    int64_t ldx;
+    const __nv_bfloat16 *w;
+    const float *bias;
+    const void *residual;
+    void *out;
+    int64_t M, N, K;
+    kda_act_t act;
+    bool out_f32;
+    uint32_t *status;
+};
+cudaError_t launch_linear_simt(const LinearParams &p, cudaStream_t st);
+
+struct DecayParams {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;          // row strides, elements
+    const float *log_decay;         // [H]
+    const int32_t *cu_seqlens;
+    int num_seqs, H;
+    int64_t total;
+    float scale;
+    const float *init;
+    float *fin;
+    void *out;
+    uint32_t *status;
+};
+cudaError_t launch_decay_prefill_simt(const DecayParams &p, int dk, int dv, bool bf16, cudaStream_t st);
+
+struct DecayStepParams {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *log_decay;
+    float *pool;
+    int pool_size;
+    const int32_t *slots;
+    void *out;
+    int N, H;
+    float scale;
+    uint32_t *status;
+};
+cudaError_t launch_decay_decode(const DecayStepParams &p, int dk, int dv, bool bf16, cudaStream_t st);
+
+struct AppendParams {
+    const void *k, *v;
+    int64_t ldk, ldv;               // row strides, bytes
+    void *kc, *vc;
+    int num_pages, page_shift;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *start, *cu_seqlens;
+    int num_seqs, Hkv;
+    int64_t total;
+    int row_bytes;                  // d x element size: one head of one token
+    uint32_t *status;
+};
+cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t st);
+
+struct PagedParams {
+    const void *q;
+    int64_t ldq;
+    const void *kc, *vc;
+    int num_pages, page_shift;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *lens;
+    int N, Hq, Hkv, G;              // G = Hq / Hkv query heads per key-value head
+    float scale;
+    void *out;
+    float *lse;
+    float *part;                    // partial results (workspace)
+    uint32_t *status;
+};
+size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d);
+cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st);
+
+// Number of SMs of the current device.
+int sm_count();
+
+// lambda^n from the base-2 logarithm of lambda; lambda = 0 (l2 = -inf) gives 1 at n = 0.
+__device__ __forceinline__ float decay_pow(float l2, int n) { return n == 0 ? 1.f : exp2f(l2 * (float)n); }
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+}  // namespace kda

@@ -1,0 +1,372 @@
+// kda_paged.cu -- the paged key-value cache of a full-attention layer: writing
+// new tokens into their pages, and softmax attention of one token per sequence
+// over the cache, split over its length and joined.
+//
+// With scores s_t = scale q . k_t over any part of the cache, a part is
+// summed up by m = max s_t, l = sum e^{s_t - m} and a = sum e^{s_t - m} v_t; two
+// parts join as m = max(m1, m2), l = l1 e^{m1-m} + l2 e^{m2-m}, a likewise, and
+// the whole gives out = a / l, lse = m + log l.
+#include "kda_layers.cuh"
+#include "kda_tc_util.cuh"
+
+namespace kda {
+
+// ---------------------------------------------------------------------------
+// Append: one warp per token.
+// ---------------------------------------------------------------------------
+template <typename V>
+__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= p.total) return;
+    int seq = (int)t;
+    int64_t off = 0;
+    if (p.cu_seqlens) {   // the last sequence that starts at or before t
+        int lo = 0, hi = p.num_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cu_seqlens[mid] <= t) lo = mid; else hi = mid;
+        }
+        seq = lo;
+        off = t - p.cu_seqlens[seq];
+        if (off < 0 || t >= p.cu_seqlens[seq + 1]) {   // offsets that do not cover t
+            if (lane == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+            return;
+        }
+    }
+    const int start = p.start[seq];
+    const int64_t pos = start + off;
+    const int64_t pi = pos >> p.page_shift;
+    const int page = (start < 0 || pi >= p.max_pages) ? -1 : p.table[(int64_t)seq * p.max_pages + pi];
+    if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    const int at = (int)(pos & ((1 << p.page_shift) - 1));
+    const int per = p.row_bytes / (int)sizeof(V);          // vectors per head
+    const int n = p.Hkv * per;
+    const V *k = reinterpret_cast<const V *>(static_cast<const uint8_t *>(p.k) + t * p.ldk);
+    const V *v = reinterpret_cast<const V *>(static_cast<const uint8_t *>(p.v) + t * p.ldv);
+    V *kc = static_cast<V *>(p.kc), *vc = static_cast<V *>(p.vc);
+    for (int i = lane; i < n; i += 32) {
+        const int h = i / per;
+        const int64_t to = (((((int64_t)page * p.Hkv + h) << p.page_shift) + at) * per) + (i - h * per);
+        kc[to] = k[i];
+        vc[to] = v[i];
+    }
+}
+
+cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t st) {
+    const unsigned grid = (unsigned)((p.total + 7) / 8);
+    if (vec16) paged_append_kernel<uint4><<<grid, 256, 0, st>>>(p);
+    else paged_append_kernel<uint16_t><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The split.  An item is a (sequence, key-value head, block of at most HB query
+// heads); its cache is cut into tiles of TILE tokens.  All tiles of all items
+// in order are dealt out evenly: CTA b of g takes tiles [b W / g, (b + 1) W / g)
+// of W, whatever the lengths are, so ragged batches and one long row both fill
+// the GPU.  An item that one CTA has whole is finished there; of the others
+// each CTA leaves at most two partial results (slot 0: it does not start the
+// item, slot 1: it starts it), which the join kernel adds up in order.
+// ---------------------------------------------------------------------------
+struct Split {
+    int64_t W;        // tiles in all
+    int g;            // CTAs that have any
+    int64_t cum;      // tiles of one head of the sequences before `n`
+    int n;            // sequence
+};
+
+__device__ __forceinline__ int clamp_len(const PagedParams &p, int n, bool tell) {
+    int len = p.lens[n];
+    const int64_t cap = (int64_t)p.max_pages << p.page_shift;
+    const int c = len < 0 ? 0 : (len > cap ? (int)cap : len);
+    if (tell && c != len) report_status(p.status, KDA_ERR_INVALID_ARG);
+    return c;
+}
+
+// Tiles of one item of sequence n.
+template <int TILE>
+__device__ __forceinline__ int64_t tiles_of(const PagedParams &p, int n) {
+    return (clamp_len(p, n, false) + TILE - 1) / TILE;
+}
+
+// Block-wide (256 threads): the totals, and with b >= 0 the sequence in which
+// CTA b's first tile lies; with b < 0 the sums before sequence `n`.
+template <int TILE>
+__device__ Split find_split(const PagedParams &p, int items, int grid, int b, int n, int64_t *s_sum /* 258 */,
+                            int *s_n) {
+    const int tid = threadIdx.x;
+    const int per = (p.N + 255) / 256, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    int64_t mine = 0;
+    for (int i = n0; i < n1; ++i) mine += tiles_of<TILE>(p, i);
+    // inclusive scan over the 256 threads: within warps, then over the 8 warp sums
+    int64_t x = mine;
+    const int lane = tid & 31, w = tid >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[w] = x;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < 8; ++i) {
+        if (i < w) before += s_sum[i];
+        total += s_sum[i];
+    }
+    int64_t c = before + x - mine;                 // tiles of one item of every sequence before n0
+    Split r;
+    r.W = total * items;
+    r.g = (int)(r.W < grid ? r.W : grid);
+    r.n = n;
+    r.cum = 0;
+    if (b >= 0 && b >= r.g) return r;
+    const int64_t w0 = b >= 0 ? (int64_t)b * r.W / r.g : 0;
+    for (int i = n0; i < n1; ++i) {
+        const int64_t ti = tiles_of<TILE>(p, i);
+        if (b >= 0 ? (w0 >= c * items && w0 < (c + ti) * items) : i == n) {
+            s_sum[256] = c;
+            *s_n = i;
+        }
+        c += ti;
+    }
+    __syncthreads();
+    r.cum = s_sum[256];
+    r.n = *s_n;
+    __syncthreads();
+    return r;
+}
+
+constexpr int kHB = 16;        // query heads per item
+
+// One partial result: m, l (base-2 logarithms) and a[d] per query head.
+__host__ __device__ constexpr int part_floats(int d) { return kHB * (d + 2); }
+
+static int split_grid() { return 2 * sm_count(); }
+
+size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d) {
+    (void)Hq, (void)Hkv;
+    return sizeof(float) * (size_t)split_grid() * 2 * part_floats(d);
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core form: tiles of 64 tokens in shared memory as float32.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParams p) {
+    constexpr int TILE = 64, LD = D + 4, NG = 256 / D, NA = kHB / NG;
+    extern __shared__ float sm[];
+    float *sK = sm, *sV = sK + TILE * LD, *sQ = sV + TILE * D, *sS = sQ + kHB * D;   // sS [kHB][TILE]
+    float *sM = sS + kHB * TILE, *sL = sM + kHB, *sC = sL + kHB;                     // max, sum, correction
+    __shared__ int64_t s_sum[258];
+    __shared__ int s_n;
+    const int tid = threadIdx.x, lane = tid & 31, wy = tid >> 5;
+    const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
+    const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    if ((int)blockIdx.x >= sp.g) return;
+    int64_t w = (int64_t)blockIdx.x * sp.W / sp.g;
+    const int64_t w1 = (int64_t)(blockIdx.x + 1) * sp.W / sp.g;
+    int n = sp.n;
+    int64_t nt = tiles_of<TILE>(p, n);
+    int item = (int)((w - sp.cum * items) / nt);
+    int64_t tile = (w - sp.cum * items) - item * nt;
+    const float sc2 = p.scale * kLog2E;
+    const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
+    const int col = tid % D, hg = tid / D;
+
+    while (w < w1) {
+        const int len = clamp_len(p, n, tid == 0 && item == 0 && tile == 0);
+        const int kvh = item / nb, g0 = (item % nb) * kHB, hb = min(kHB, p.G - g0);
+        const int hq0 = kvh * p.G + g0;
+        const int64_t first = tile, last = min(nt, tile + (w1 - w));      // tiles [first, last) of the item
+        __syncthreads();
+        for (int i = tid; i < hb * D; i += 256)
+            sQ[i] = to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)hq0 * D + i]) * sc2;
+        if (tid < kHB) { sM[tid] = -INFINITY; sL[tid] = 0.f; }
+        float acc[NA];
+#pragma unroll
+        for (int i = 0; i < NA; ++i) acc[i] = 0.f;
+        for (; tile < last; ++tile) {
+            const int t0 = (int)(tile * TILE);
+            __syncthreads();
+            for (int i = tid; i < TILE * (D / 4); i += 256) {
+                const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+                float kk[4] = {}, vv[4] = {};
+                if (t0 + r < len) {
+                    const int pg = p.table[(int64_t)n * p.max_pages + ((t0 + r) >> p.page_shift)];
+                    if (pg >= 0 && pg < p.num_pages) {
+                        const int64_t at = (((((int64_t)pg * p.Hkv + kvh) << p.page_shift) +
+                                             ((t0 + r) & ((1 << p.page_shift) - 1))) * D) + c;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) { kk[e] = to_f32(kc[at + e]); vv[e] = to_f32(vc[at + e]); }
+                    } else {
+                        if (c == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { sK[r * LD + c + e] = kk[e]; sV[r * D + c + e] = vv[e]; }
+            }
+            __syncthreads();
+            {   // scores: thread = token x every fourth head
+                const int j = tid & 63;
+                bool ok = t0 + j < len;
+                if (ok) {
+                    const int pg = p.table[(int64_t)n * p.max_pages + ((t0 + j) >> p.page_shift)];
+                    ok = pg >= 0 && pg < p.num_pages;
+                }
+                for (int g = tid >> 6; g < hb; g += 4) {
+                    float a = 0.f;
+#pragma unroll 8
+                    for (int c = 0; c < D; c += 4) {
+                        float x[4], y[4];
+                        tc::ld4(sQ + g * D + c, x);
+                        tc::ld4(sK + j * LD + c, y);
+                        a = fmaf(x[0], y[0], a); a = fmaf(x[1], y[1], a);
+                        a = fmaf(x[2], y[2], a); a = fmaf(x[3], y[3], a);
+                    }
+                    sS[g * TILE + j] = ok ? a : -INFINITY;
+                }
+            }
+            __syncthreads();
+            for (int g = wy; g < hb; g += 8) {   // softmax of one head per warp
+                const float s0 = sS[g * TILE + lane], s1 = sS[g * TILE + 32 + lane];
+                float m = fmaxf(s0, s1);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float mo = sM[g], mn = fmaxf(mo, m);
+                // a tile with nothing in it leaves everything as it is
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                const float p0 = exp2f(s0 - mu), p1 = exp2f(s1 - mu);
+                float l = p0 + p1;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                sS[g * TILE + lane] = p0;
+                sS[g * TILE + 32 + lane] = p1;
+                __syncwarp();
+                if (lane == 0) {
+                    const float f = exp2f(mo - mu);
+                    sC[g] = f;
+                    sM[g] = mn;
+                    sL[g] = sL[g] * f + l;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int g = hg + i * NG;
+                if (g >= hb) break;
+                float a = acc[i] * sC[g];
+#pragma unroll 8
+                for (int j = 0; j < TILE; ++j) a = fmaf(sS[g * TILE + j], sV[j * D + col], a);
+                acc[i] = a;
+            }
+        }
+        __syncthreads();
+        if (first == 0 && last == nt) {
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int g = hg + i * NG;
+                if (g >= hb) break;
+                const float l = sL[g];
+                static_cast<T *>(p.out)[((int64_t)n * p.Hq + hq0 + g) * D + col] =
+                    from_f32<T>(l > 0.f ? acc[i] / l : (l == 0.f ? 0.f : l));
+                if (col == 0 && p.lse) p.lse[(int64_t)n * p.Hq + hq0 + g] = (sM[g] + log2f(l)) / kLog2E;
+            }
+        } else {
+            float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D);
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int g = hg + i * NG;
+                if (g >= hb) break;
+                part[kHB * 2 + g * D + col] = acc[i];
+                if (col == 0) { part[2 * g] = sM[g]; part[2 * g + 1] = sL[g]; }
+            }
+        }
+        w += last - first;
+        if (w < w1) {   // the next item
+            tile = 0;
+            if (++item == items) {
+                item = 0;
+                do { ++n; nt = tiles_of<TILE>(p, n); } while (nt == 0);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join: one CTA per sequence, one warp per query head.  Heads whose item one
+// CTA had whole are done already; a sequence without tokens gets zeros.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int TILE>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int grid) {
+    __shared__ int64_t s_sum[258];
+    __shared__ int s_n;
+    const int n = blockIdx.x, lane = threadIdx.x & 31;
+    const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
+    constexpr int E = D / 32;
+    T *out = static_cast<T *>(p.out);
+    const int64_t nt = tiles_of<TILE>(p, n);
+    if (nt == 0) {
+        clamp_len(p, n, threadIdx.x == 0);
+        for (int i = threadIdx.x; i < p.Hq * D; i += 256) out[(int64_t)n * p.Hq * D + i] = from_f32<T>(0.f);
+        if (p.lse)
+            for (int i = threadIdx.x; i < p.Hq; i += 256) p.lse[(int64_t)n * p.Hq + i] = -INFINITY;
+        return;
+    }
+    const Split sp = find_split<TILE>(p, items, grid, -1, n, s_sum, &s_n);
+    for (int hq = threadIdx.x >> 5; hq < p.Hq; hq += 8) {
+        const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / kHB, g = gi % kHB;
+        const int64_t s = sp.cum * items + item * nt, e = s + nt;
+        const int b0 = (int)(((s + 1) * sp.g - 1) / sp.W), b1 = (int)((e * sp.g - 1) / sp.W);
+        if (b0 == b1) continue;
+        float m = -INFINITY, l = 0.f, a[E] = {};
+        for (int b = b0; b <= b1; ++b) {
+            const float *part = p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D);
+            const float mb = part[2 * g], lb = part[2 * g + 1];
+            const float mn = fmaxf(m, mb), mu = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m - mu), fb = exp2f(mb - mu);
+            m = mn;
+            l = l * f + lb * fb;
+#pragma unroll
+            for (int i = 0; i < E; ++i) a[i] = a[i] * f + part[kHB * 2 + g * D + lane * E + i] * fb;
+        }
+        const int64_t row = (int64_t)n * p.Hq + hq;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            out[row * D + lane * E + i] = from_f32<T>(l > 0.f ? a[i] / l : (l == 0.f ? 0.f : l));
+        if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) / kLog2E;
+    }
+}
+
+template <typename T, int D>
+static cudaError_t paged_simt(const PagedParams &p, cudaStream_t st) {
+    constexpr int TILE = 64;
+    const size_t smem = sizeof(float) * (TILE * (D + 4) + TILE * D + kHB * D + kHB * TILE + 3 * kHB);
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = split_grid();
+    paged_decode_simt_kernel<T, D><<<grid, 256, smem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    paged_join_kernel<T, D, TILE><<<p.N, 256, 0, st>>>(p, grid);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) {
+    switch (d) {
+        case 32: return paged_simt<T, 32>(p, st);
+        case 64: return paged_simt<T, 64>(p, st);
+        case 128: return paged_simt<T, 128>(p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
+    return bf16 ? paged_dispatch<__nv_bfloat16>(p, d, st) : paged_dispatch<float>(p, d, st);
+}
+
+}  // namespace kda
