@@ -23,7 +23,7 @@ struct LinearParams {
     bool out_f32;
     uint32_t *status;
 };
-cudaError_t launch_linear_simt(const LinearParams &p, cudaStream_t st);
+cudaError_t launch_linear(const LinearParams &p, cudaStream_t st);
 
 struct DecayParams {
     const void *q, *k, *v;

@@ -50,7 +50,7 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
         return KDA_ERR_INVALID_ARG;
     const kda::LinearParams p{static_cast<const __nv_bfloat16 *>(x), ldx, static_cast<const __nv_bfloat16 *>(w),
                               bias, residual, out, M, N, K, act, out_dtype == KDA_F32, status};
-    return from_cuda(kda::launch_linear_simt(p, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(kda::launch_linear(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,

@@ -1,77 +1,575 @@
-// kda_linear.cu -- out = act(x w^T + bias) + residual.
+// kda_linear.cu -- out = act(x w^T + bias) + residual on the tensor cores.
+//
+// Two kernels.  `linear_pair_kernel` (many rows): a pair of CTAs works on one
+// 256 x 256 tile of out at a time.  `linear_rows_kernel` (few rows): the roles
+// of x and w are swapped, so that 128 output features lie on the MMA's rows and
+// the rows of x, however few, on its columns; K is split over a cluster.
+#include <cuda.h>
+
 #include "kda_layers.cuh"
+#include "kda_tc_util.cuh"
+#include "kda_tmap.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr long long kWaitBudget = 2000000000LL;   // cycles (about one second)
+constexpr long long kDrain = 20000000LL;          // cycles (about ten milliseconds)
 
 // The activation on the float32 sum.  sigmoid and silu are written with
 // exp(-y): it overflows to +inf for very negative y, where both then give 0.
-__device__ __forceinline__ float activate(float y, int act) {
-    switch (act) {
-        case KDA_ACT_RELU: return y > 0.f ? y : (y != y ? y : 0.f);
-        case KDA_ACT_GELU: return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
-        case KDA_ACT_SILU: return y / (1.f + expf(-y));
-        case KDA_ACT_SIGMOID: return 1.f / (1.f + expf(-y));
-        default: return y;
+template <int ACT>
+__device__ __forceinline__ float activate(float y) {
+    if constexpr (ACT == KDA_ACT_RELU) return y > 0.f ? y : (y != y ? y : 0.f);
+    if constexpr (ACT == KDA_ACT_GELU) return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
+    if constexpr (ACT == KDA_ACT_SILU) return __fdividef(y, 1.f + __expf(-y));
+    if constexpr (ACT == KDA_ACT_SIGMOID) return __fdividef(1.f, 1.f + __expf(-y));
+    return y;
+}
+
+// After an expired wait: long enough for every copy and MMA in flight to land
+// before shared and tensor memory are given back.
+__device__ __forceinline__ void drain() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrain) {}
+}
+
+struct Tail {   // what the epilogue needs
+    const float *bias;
+    const void *residual;
+    void *out;
+    int M, N, K;
+    uint32_t *status;
+};
+
+// ---------------------------------------------------------------------------
+// Few rows.  One CTA: 128 features (rows of w, the MMA's M) x NT rows of x (the
+// MMA's N, a multiple of 16), over its share of K; the S CTAs of a cluster
+// share one tile and add their sums up in order of rank, each for its part of
+// the rows.  Warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-5 read TMEM.
+// With LOAD = 1 (rows that no TMA copy can start on) warps 6-13 load instead,
+// element by element, into the same swizzled layout.
+// ---------------------------------------------------------------------------
+constexpr int kBK = 64;                     // K per stage: one 128-byte swizzled row
+constexpr uint32_t kABytes = 128 * 128;     // 128 rows
+
+struct RowsParams {
+    Tail t;
+    const __nv_bfloat16 *x, *w;   // LOAD = 1
+    int64_t ldx;
+    int NT, stages, S;
+};
+
+template <int ACT, bool F32>
+__device__ __forceinline__ void put(const Tail &t, int64_t m, int64_t n, float y) {
+    y = activate<ACT>(y);
+    const int64_t at = m * t.N + n;
+    if constexpr (F32) {
+        if (t.residual) y += static_cast<const float *>(t.residual)[at];
+        static_cast<float *>(t.out)[at] = y;
+    } else {
+        if (t.residual) y += to_f32(static_cast<const __nv_bfloat16 *>(t.residual)[at]);
+        static_cast<__nv_bfloat16 *>(t.out)[at] = __float2bfloat16_rn(y);
     }
 }
 
-// CUDA-core form for rows that no TMA copy can start on (K not a multiple of 8
-// or misaligned rows): a 64 x 64 tile per CTA, K in steps of 16, 4 x 4 sums
-// per thread in float32.
-__global__ void __launch_bounds__(256) linear_simt_kernel(const LinearParams p) {
-    constexpr int BK = 16;
-    __shared__ float xs[BK][68], ws[BK][68];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += BK) {
-        for (int i = tid; i < 64 * BK; i += 256) {
-            const int r = i / BK, c = i % BK;
-            const int64_t kk = k0 + c;
-            xs[c][r] = (m0 + r < p.M && kk < p.K) ? to_f32(p.x[(m0 + r) * p.ldx + kk]) : 0.f;
-            ws[c][r] = (n0 + r < p.N && kk < p.K) ? to_f32(p.w[(n0 + r) * p.K + kk]) : 0.f;
+template <int ACT, bool F32, int LOAD>
+__global__ void __launch_bounds__(LOAD ? 448 : 192)
+    linear_rows_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                       const RowsParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[12], empty[12], done;
+    __shared__ uint32_t s_tmem, s_abort;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage_bytes = kABytes + (uint32_t)p.NT * 128u;
+    const int rank = p.S > 1 ? (int)ptx::cluster_rank() : 0;
+    const int f0 = (int)(blockIdx.x / p.S) * 128, m0 = (int)blockIdx.y * p.NT;
+    const int kb_all = (p.t.K + kBK - 1) / kBK;
+    const int kb0 = (int)((int64_t)kb_all * rank / p.S), kb1 = (int)((int64_t)kb_all * (rank + 1) / p.S);
+    uint32_t cols = 32;
+    while (cols < (uint32_t)p.NT) cols <<= 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            ptx::mbar_init(&full[i], LOAD ? 256 : 1);
+            ptx::mbar_init(&empty[i], 1);
         }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < BK; ++c) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { a[i] = xs[c][ty * 4 + i]; b[i] = ws[c][tx * 4 + i]; }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        ptx::mbar_init(&done, 1);
+        ptx::fence_mbar_init();
+        s_abort = 0;
+        if (!LOAD) {
+            ptx::prefetch_tensormap(&mw);
+            ptx::prefetch_tensormap(&mx);
         }
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= p.M || n >= p.N) continue;
-            const float y = activate(acc[i][j] + (p.bias ? p.bias[n] : 0.f), p.act);
-            const int64_t at = m * p.N + n;
-            if (p.out_f32) {
-                const float r = p.residual ? static_cast<const float *>(p.residual)[at] : 0.f;
-                static_cast<float *>(p.out)[at] = y + r;
-            } else {
-                const float r = p.residual ? to_f32(static_cast<const __nv_bfloat16 *>(p.residual)[at]) : 0.f;
-                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y + r);
+    if (warp == 1) {
+        ptx::tmem_alloc(&s_tmem, cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+
+    if (warp == 0 && !LOAD) {
+        if (lane == 0) {
+            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+                const int s = i % p.stages;
+                if (i >= p.stages && !ptx::mbar_wait(&empty[s], ((i / p.stages) - 1) & 1, kWaitBudget)) { ok = false; break; }
+                uint8_t *a = sm + s * stage_bytes;
+                ptx::mbar_arrive_expect_tx(&full[s], stage_bytes);
+                ptx::tma_load_2d(a, &mw, kb * kBK, f0, &full[s]);
+                ptx::tma_load_2d(a + kABytes, &mx, kb * kBK, m0, &full[s]);
             }
         }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = ptx::idesc_bf16_f32(128, p.NT);
+            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+                const int s = i % p.stages;
+                if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kWaitBudget)) { ok = false; break; }
+                ptx::tc_fence_after_sync();
+                const uint32_t a = ptx::smem_addr(sm + s * stage_bytes);
+                mma_k<4>(tmem, a, 0, a + kABytes, 0, idesc, i > 0);
+                ptx::mma_commit(&empty[s]);
+            }
+            ptx::mma_commit(&done);
+        }
+    } else if (LOAD && warp >= 6) {
+        const int tid = threadIdx.x - 192, chunks = (128 + p.NT) * 8;
+        for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            const int s = i % p.stages;
+            uint4 v[12];
+#pragma unroll
+            for (int j = 0; j < 12; ++j) {
+                const int id = tid + j * 256;
+                if (id >= chunks) break;
+                const int row = id >> 3;
+                const int64_t k0 = (int64_t)kb * kBK + (id & 7) * 8;
+                const bool isw = row < 128;
+                const int64_t r = isw ? f0 + row : m0 + row - 128;
+                const __nv_bfloat16 *src = isw ? p.w + r * p.t.K : p.x + r * p.ldx;
+                const bool in = r < (isw ? p.t.N : p.t.M);
+                uint16_t e[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    e[c] = in && k0 + c < p.t.K ? __bfloat16_as_ushort(src[k0 + c]) : (uint16_t)0;
+                v[j] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                  e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+            }
+            if (i >= p.stages && !ptx::mbar_wait(&empty[s], ((i / p.stages) - 1) & 1, kWaitBudget)) { ok = false; break; }
+#pragma unroll
+            for (int j = 0; j < 12; ++j) {
+                const int id = tid + j * 256;
+                if (id >= chunks) break;
+                const int row = id >> 3;
+                uint8_t *dst = row < 128 ? sm + s * stage_bytes + swz(row, id & 7)
+                                         : sm + s * stage_bytes + kABytes + swz(row - 128, id & 7);
+                *reinterpret_cast<uint4 *>(dst) = v[j];
+            }
+            ptx::fence_async_smem();
+            ptx::mbar_arrive(&full[s]);
+        }
+    }
+    const bool reader = warp >= 2 && warp < 6;
+    const int q = warp & 3;                      // TMEM lane quarter of this warp
+    float bias = 0.f;
+    const int f = f0 + q * 32 + lane;
+    if (reader) {
+        if (p.t.bias && f < p.t.N) bias = p.t.bias[f];
+        ok = ptx::mbar_wait(&done, 0, kWaitBudget);
+        ptx::tc_fence_after_sync();
+    }
+    if (!ok) {
+        s_abort = 1;
+        report_status(p.t.status, KDA_ERR_DEVICE_TIMEOUT);
+    }
+    __syncthreads();
+    if (s_abort) drain();
+    const int rows = min(p.NT, p.t.M - m0);
+    if (p.S == 1) {
+        if (reader && !s_abort) {
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                float d[16];
+                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
+                ptx::tmem_ld_wait();
+                if (f < p.t.N)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (c0 + c < rows) put<ACT, F32>(p.t, m0 + c0 + c, f, d[c] + bias);
+            }
+        }
+    } else {
+        // this CTA's sums as [row][128] float32 over the stages (all consumed), then each CTA of the
+        // cluster adds up every S-th row over the ranks
+        float *part = reinterpret_cast<float *>(sm);
+        if (reader) {
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                float d[16];
+                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (c0 + c < rows) part[(c0 + c) * 128 + q * 32 + lane] = d[c];
+            }
+        }
+        ptx::cluster_sync();
+        if (!s_abort) {
+            float b[4];
+            const int n0 = f0 + lane * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = p.t.bias && n0 + e < p.t.N ? p.t.bias[n0 + e] : 0.f;
+            for (int r = rank + p.S * warp; r < rows; r += p.S * (int)(blockDim.x >> 5)) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int o = 0; o < p.S; ++o) {
+                    const float4 v = ptx::ld_cluster_f4(ptx::map_to_rank(part + r * 128 + lane * 4, (uint32_t)o));
+                    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+                }
+                const float y[4] = {a.x + b[0], a.y + b[1], a.z + b[2], a.w + b[3]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n0 + e < p.t.N) put<ACT, F32>(p.t, m0 + r, n0 + e, y[e]);
+            }
+        }
+        ptx::cluster_sync();     // no CTA leaves while another reads its shared memory
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, cols);
+    }
 }
 
-cudaError_t launch_linear_simt(const LinearParams &p, cudaStream_t st) {
-    const int64_t gx = (p.N + 63) / 64;
-    // M in slices of 65,535 row tiles (the grid's limit in y)
-    for (int64_t m0 = 0; m0 < p.M; m0 += 65535 * 64) {
+// ---------------------------------------------------------------------------
+// Many rows.  A pair of CTAs per 256 x 256 tile: each loads its 128 rows of x
+// and 128 of the 256 rows of w per K step (32 KB; the MMA reads the halves of w
+// from both, so each SM fetches half of what a lone CTA would), accumulates
+// 128 x 256 float32 in TMEM, two tiles' worth, so that the epilogue of one tile
+// runs beside the next one's MMAs.  Persistent: pair i takes tiles i, i + pairs, ...
+// Warp 0 loads, warp 1 issues (rank 0 of the pair only), warps 2-9 are the
+// epilogue: two groups of four, 128 columns each, by way of a 16 KB staging
+// tile and TMA stores; a residual tile comes in by TMA through the same buffer.
+// ---------------------------------------------------------------------------
+constexpr int kStages = 6;
+constexpr uint32_t kStageBytes = 2 * kABytes, kStaging = 16384;
+constexpr uint32_t kPairSmem = kStages * kStageBytes + 2 * kStaging + 1024;
+
+struct PairParams {
+    Tail t;
+    int tiles_m, tiles_n, group;    // tiles are walked `group` row tiles at a time, column by column
+};
+
+__device__ __forceinline__ void tile_at(const PairParams &p, int i, int &tm, int &tn) {
+    const int per = p.group * p.tiles_n, g = i / per, m0 = g * p.group;
+    const int h = min(p.group, p.tiles_m - m0), r = i - g * per;
+    tm = m0 + r % h;
+    tn = r / h;
+}
+
+template <int ACT, bool F32>
+__global__ void __launch_bounds__(320)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                       const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
+                       const PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], rbar[2];
+    __shared__ uint32_t s_tmem, s_abort;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int tiles = p.tiles_m * p.tiles_n, kbs = (p.t.K + kBK - 1) / kBK;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&tfull[i], 1);
+            ptx::mbar_init(&tempty[i], 16);      // the epilogue warps of both CTAs
+            ptx::mbar_init(&rbar[i], 1);
+        }
+        ptx::fence_mbar_init();
+        s_abort = 0;
+        ptx::prefetch_tensormap(&mx);
+        ptx::prefetch_tensormap(&mw);
+        ptx::prefetch_tensormap(&mo);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(&s_tmem, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int i = pair; i < tiles && ok; i += pairs) {
+                int tm, tn;
+                tile_at(p, i, tm, tn);
+                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !ptx::mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, kWaitBudget)) { ok = false; break; }
+                    uint8_t *a = sm + s * kStageBytes;
+                    // rank 0's barrier counts the bytes of both CTAs
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    const uint32_t bar = ptx::map_to_rank(&full[s], 0);
+                    ptx::tma_load_2d_pair(a, &mx, kb * kBK, m0, bar);
+                    ptx::tma_load_2d_pair(a + kABytes, &mw, kb * kBK, n0, bar);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = ptx::idesc_bf16_f32(256, 256);
+            int it = 0, n = 0;
+            for (int i = pair; i < tiles && ok; i += pairs, ++n) {
+                const int b = n & 1;
+                if (n >= 2 && !ptx::mbar_wait_cluster(&tempty[b], ((n >> 1) - 1) & 1, kWaitBudget)) { ok = false; break; }
+                ptx::tc_fence_after_sync();
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!ptx::mbar_wait_cluster(&full[s], (it / kStages) & 1, kWaitBudget)) { ok = false; break; }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t a = ptx::smem_addr(sm + s * kStageBytes);
+                    const uint64_t da = ptx::sdesc_kmajor_sw128(a), db = ptx::sdesc_kmajor_sw128(a + kABytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_bf16_ss_pair(tmem + b * 256, da + k * 2, db + k * 2, idesc, kb > 0 || k > 0);
+                    ptx::mma_commit_pair(&empty[s]);
+                }
+                if (ok) ptx::mma_commit_pair(&tfull[b]);
+            }
+        }
+    } else {
+        const int g = (warp - 2) >> 2, q = warp & 3, row = q * 32 + lane;
+        const bool lead = ((warp - 2) & 3) == 0 && lane == 0;      // the group's thread for TMA
+        uint8_t *st = sm + kStages * kStageBytes + g * kStaging;
+        constexpr int CW = F32 ? 32 : 64, CHUNKS = 128 / CW;       // columns of a 128-byte staging row
+        int n = 0;
+        uint32_t rphase = 0;
+        for (int i = pair; i < tiles && ok; i += pairs, ++n) {
+            const int b = n & 1;
+            int tm, tn;
+            tile_at(p, i, tm, tn);
+            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + g * 128;
+            // the group goes on, or gives up, as one
+            ok = !ptx::bar_any(g + 1, 128, !ptx::mbar_wait_cluster(&tfull[b], (n >> 1) & 1, kWaitBudget));
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int nc = n0 + c * CW;
+                // the staging tile is free once its last store has read it
+                if (lead) {
+                    ptx::bulk_wait_read();
+                    if (p.t.residual) {
+                        ptx::mbar_arrive_expect_tx(&rbar[g], kStaging);
+                        ptx::tma_load_2d(st, &mr, nc, m0, &rbar[g]);
+                    }
+                }
+                float d[CW];
+                ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * 256 + g * 128 + c * CW, *reinterpret_cast<float(*)[32]>(d));
+                if constexpr (!F32)
+                    ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * 256 + g * 128 + c * CW + 32,
+                                   *reinterpret_cast<float(*)[32]>(d + 32));
+                ptx::tmem_ld_wait();
+                if (c == CHUNKS - 1) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&tempty[b], 0));
+                }
+#pragma unroll
+                for (int j = 0; j < CW; j += 4) {
+                    float bb[4] = {};
+                    if (p.t.bias) {
+                        if (nc + j + 4 <= p.t.N) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) bb[e] = __ldg(p.t.bias + nc + j + e);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) bb[e] = nc + j + e < p.t.N ? p.t.bias[nc + j + e] : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[j + e] = activate<ACT>(d[j + e] + bb[e]);
+                }
+                if (p.t.residual) {
+                    ok = ptx::mbar_wait(&rbar[g], rphase, kWaitBudget);
+                    rphase ^= 1;
+                } else {
+                    asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory");
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint8_t *at = st + swz(row, j);
+                    if constexpr (F32) {
+                        float4 v = make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
+                        if (p.t.residual) {
+                            const float4 r = *reinterpret_cast<float4 *>(at);
+                            v.x += r.x; v.y += r.y; v.z += r.z; v.w += r.w;
+                        }
+                        *reinterpret_cast<float4 *>(at) = v;
+                    } else {
+                        if (p.t.residual) {
+                            float r[8];
+                            ld_chunk(st, swz(row, j), r);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) d[8 * j + e] += r[e];
+                        }
+                        st_chunk(st, swz(row, j), d + 8 * j);
+                    }
+                }
+                ptx::fence_async_smem();
+                ok = !ptx::bar_any(g + 1, 128, !ok);
+                if (!ok) break;
+                if (lead) {
+                    ptx::tma_store_2d(&mo, nc, m0, st);
+                    ptx::bulk_commit();
+                }
+            }
+        }
+        if (lead) ptx::bulk_wait_all();
+    }
+    if (!ok) {
+        s_abort = 1;
+        report_status(p.t.status, KDA_ERR_DEVICE_TIMEOUT);
+    }
+    __syncthreads();
+    if (s_abort) drain();
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync();         // neither CTA leaves while the other's MMAs or barriers use it
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+template <int ACT, bool F32>
+cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
+    CUtensorMap mx, mw, mo, mr;
+    const uint64_t eb = F32 ? 4 : 2;
+    if (!make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, 128) || !make_map_2d(&mw, p.w, true, p.N, p.K, p.K * 2, 128) ||
+        !make_map_2d(&mo, p.out, !F32, p.M, p.N, p.N * eb, 128) ||
+        !make_map_2d(&mr, p.residual ? p.residual : p.out, !F32, p.M, p.N, p.N * eb, 128))
+        return cudaErrorInvalidValue;
+    PairParams pp{{p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status}, (int)((p.M + 255) / 256),
+                  (int)((p.N + 255) / 256), 8};
+    auto *kernel = linear_pair_kernel<ACT, F32>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)pp.tiles_m * pp.tiles_n;
+    const int pairs = sm_count() / 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
+    cfg.blockDim = dim3(320);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, mo, mr, pp);
+}
+
+template <int ACT, bool F32, int LOAD>
+cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
+    RowsParams rp{};
+    rp.t = {p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status};
+    rp.x = p.x;
+    rp.w = p.w;
+    rp.ldx = p.ldx;
+    rp.NT = p.M < 256 ? (int)((p.M + 15) / 16) * 16 : 256;
+    const uint32_t stage = kABytes + rp.NT * 128;
+    // two CTAs per SM where the stages allow it: one's epilogue beside the other's loads
+    const int per_sm = rp.NT <= 128 && !LOAD ? 2 : 1;
+    const uint32_t room = per_sm == 2 ? 104 * 1024 : 200 * 1024;
+    rp.stages = (int)(room / stage) < 12 ? (int)(room / stage) : 12;
+    const int64_t tiles = ((p.N + 127) / 128) * ((p.M + rp.NT - 1) / rp.NT);
+    // split K while that still adds CTAs to the GPU and leaves each at least four stages of work
+    const int64_t slots = (int64_t)sm_count() * per_sm, kbs = (p.K + kBK - 1) / kBK;
+    rp.S = 1;
+    while (rp.S < 8 && tiles * rp.S * 2 <= slots && kbs / (rp.S * 2) >= 4) rp.S *= 2;
+    uint32_t smem = rp.stages * stage;
+    if (rp.S > 1 && smem < (uint32_t)rp.NT * 512u) smem = rp.NT * 512u;
+    smem += 1024;
+    CUtensorMap mw{}, mx{};
+    if (!LOAD && (!make_map_2d(&mw, p.w, true, p.N, p.K, p.K * 2, 128) ||
+                  !make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, rp.NT)))
+        return cudaErrorInvalidValue;
+    auto *kernel = linear_rows_kernel<ACT, F32, LOAD>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t mt = (p.M + rp.NT - 1) / rp.NT;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(LOAD ? 448 : 192);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = rp.S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = rp.S > 1 ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt);
+    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, rp);
+}
+
+template <int ACT, bool F32>
+cudaError_t launch_act(const LinearParams &p, cudaStream_t st) {
+    const bool tma = p.K % 8 == 0 && p.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
+    if (!tma) return launch_rows<ACT, F32, 1>(p, st);
+    const uint64_t eb = F32 ? 4 : 2;
+    const bool store = p.N * eb % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.residual) % 16 == 0;
+    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+    if (store && p.M > 256 && tiles * 2 >= sm_count() / 2) return launch_pair<ACT, F32>(p, st);
+    return launch_rows<ACT, F32, 0>(p, st);
+}
+
+template <int ACT>
+cudaError_t launch_type(const LinearParams &p, cudaStream_t st) {
+    return p.out_f32 ? launch_act<ACT, true>(p, st) : launch_act<ACT, false>(p, st);
+}
+
+cudaError_t launch_slice(const LinearParams &p, cudaStream_t st) {
+    switch (p.act) {
+        case KDA_ACT_RELU: return launch_type<KDA_ACT_RELU>(p, st);
+        case KDA_ACT_GELU: return launch_type<KDA_ACT_GELU>(p, st);
+        case KDA_ACT_SILU: return launch_type<KDA_ACT_SILU>(p, st);
+        case KDA_ACT_SIGMOID: return launch_type<KDA_ACT_SIGMOID>(p, st);
+        default: return launch_type<KDA_ACT_NONE>(p, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearParams &p, cudaStream_t st) {
+    // M in slices of 2^23 rows: the grid's limit in y, and 32-bit tile coordinates
+    constexpr int64_t kSlice = int64_t(1) << 23;
+    for (int64_t m0 = 0; m0 < p.M; m0 += kSlice) {
         LinearParams s = p;
-        s.M = p.M - m0 < 65535 * 64 ? p.M - m0 : 65535 * 64;
+        s.M = p.M - m0 < kSlice ? p.M - m0 : kSlice;
         s.x = p.x + m0 * p.ldx;
         const int64_t off = m0 * p.N * (p.out_f32 ? 4 : 2);
         s.out = static_cast<uint8_t *>(p.out) + off;
         if (p.residual) s.residual = static_cast<const uint8_t *>(p.residual) + off;
-        linear_simt_kernel<<<dim3((unsigned)gx, (unsigned)((s.M + 63) / 64)), 256, 0, st>>>(s);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_slice(s, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
