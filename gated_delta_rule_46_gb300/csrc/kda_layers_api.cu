@@ -55,8 +55,10 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,
                                         kda_dtype_t dtype) {
-    (void)total_tokens, (void)num_seqs, (void)H, (void)dk, (void)dv, (void)dtype;
-    return 0;
+    if (total_tokens <= 0 || total_tokens >= kMax31 || num_seqs <= 0 || H <= 0 || dtype != KDA_BF16 || dk != 128 ||
+        dv != 128)
+        return 0;
+    return kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H);
 }
 
 kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
@@ -77,9 +79,13 @@ kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_
         !aligned(out, elem(dtype)) || !aligned(initial_state, 16) || !aligned(final_state, 16) ||
         !aligned(workspace, 16))
         return KDA_ERR_INVALID_ARG;
-    (void)workspace_bytes;
     const kda::DecayParams p{q, k, v, ldq, ldk, ldv, log_decay, cu_seqlens, num_seqs, H, total_tokens, scale,
                              initial_state, final_state, out, status};
+    // TMA copies start on 16-byte boundaries
+    if (dtype == KDA_BF16 && dk == 128 && dv == 128 && total_tokens > 0 && aligned(q, 16) && aligned(k, 16) &&
+        aligned(v, 16) && aligned(out, 16) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0)
+        return from_cuda(kda::launch_decay_prefill_tc(p, workspace, workspace_bytes,
+                                                      reinterpret_cast<cudaStream_t>(stream)));
     return from_cuda(kda::launch_decay_prefill_simt(p, dk, dv, dtype == KDA_BF16,
                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
