@@ -148,7 +148,7 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
         return KDA_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || !dim_ok(d) || page_shift(page_size) < 0) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)num_seqs * Hq >= kMax31 || (int64_t)Hq * d >= kMax31 ||
-        (int64_t)max_pages * page_size >= kMax31)
+        (int64_t)max_pages * page_size > (int64_t(1) << 30))
         return KDA_ERR_UNSUPPORTED;
     if (ldq < (int64_t)Hq * d) return KDA_ERR_INVALID_ARG;
     if (num_seqs == 0) return KDA_OK;

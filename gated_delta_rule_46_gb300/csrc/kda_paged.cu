@@ -6,8 +6,9 @@
 // summed up by m = max s_t, l = sum e^{s_t - m} and a = sum e^{s_t - m} v_t; two
 // parts join as m = max(m1, m2), l = l1 e^{m1-m} + l2 e^{m2-m}, a likewise, and
 // the whole gives out = a / l, lse = m + log l.
-#include "kda_layers.cuh"
+#include "kda_paged.cuh"
 #include "kda_tc_util.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 
@@ -64,107 +65,22 @@ cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t 
 }
 
 // ---------------------------------------------------------------------------
-// The split.  An item is a (sequence, key-value head, block of at most HB query
-// heads); its cache is cut into tiles of TILE tokens.  All tiles of all items
-// in order are dealt out evenly: CTA b of g takes tiles [b W / g, (b + 1) W / g)
-// of W, whatever the lengths are, so ragged batches and one long row both fill
-// the GPU.  An item that one CTA has whole is finished there; of the others
-// each CTA leaves at most two partial results (slot 0: it does not start the
-// item, slot 1: it starts it), which the join kernel adds up in order.
-// ---------------------------------------------------------------------------
-struct Split {
-    int64_t W;        // tiles in all
-    int g;            // CTAs that have any
-    int64_t cum;      // tiles of one head of the sequences before `n`
-    int n;            // sequence
-};
-
-__device__ __forceinline__ int clamp_len(const PagedParams &p, int n, bool tell) {
-    int len = p.lens[n];
-    const int64_t cap = (int64_t)p.max_pages << p.page_shift;
-    const int c = len < 0 ? 0 : (len > cap ? (int)cap : len);
-    if (tell && c != len) report_status(p.status, KDA_ERR_INVALID_ARG);
-    return c;
-}
-
-// Tiles of one item of sequence n.
-template <int TILE>
-__device__ __forceinline__ int64_t tiles_of(const PagedParams &p, int n) {
-    return (clamp_len(p, n, false) + TILE - 1) / TILE;
-}
-
-// Block-wide (256 threads): the totals, and with b >= 0 the sequence in which
-// CTA b's first tile lies; with b < 0 the sums before sequence `n`.
-template <int TILE>
-__device__ Split find_split(const PagedParams &p, int items, int grid, int b, int n, int64_t *s_sum /* 258 */,
-                            int *s_n) {
-    const int tid = threadIdx.x;
-    const int per = (p.N + 255) / 256, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
-    int64_t mine = 0;
-    for (int i = n0; i < n1; ++i) mine += tiles_of<TILE>(p, i);
-    // inclusive scan over the 256 threads: within warps, then over the 8 warp sums
-    int64_t x = mine;
-    const int lane = tid & 31, w = tid >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_sum[w] = x;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int i = 0; i < 8; ++i) {
-        if (i < w) before += s_sum[i];
-        total += s_sum[i];
-    }
-    int64_t c = before + x - mine;                 // tiles of one item of every sequence before n0
-    Split r;
-    r.W = total * items;
-    r.g = (int)(r.W < grid ? r.W : grid);
-    r.n = n;
-    r.cum = 0;
-    if (b >= 0 && b >= r.g) return r;
-    const int64_t w0 = b >= 0 ? (int64_t)b * r.W / r.g : 0;
-    for (int i = n0; i < n1; ++i) {
-        const int64_t ti = tiles_of<TILE>(p, i);
-        if (b >= 0 ? (w0 >= c * items && w0 < (c + ti) * items) : i == n) {
-            s_sum[256] = c;
-            *s_n = i;
-        }
-        c += ti;
-    }
-    __syncthreads();
-    r.cum = s_sum[256];
-    r.n = *s_n;
-    __syncthreads();
-    return r;
-}
-
-constexpr int kHB = 16;        // query heads per item
-
-// One partial result: m, l (base-2 logarithms) and a[d] per query head.
-__host__ __device__ constexpr int part_floats(int d) { return kHB * (d + 2); }
-
-static int split_grid() { return 2 * sm_count(); }
-
-size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d) {
-    (void)Hq, (void)Hkv;
-    return sizeof(float) * (size_t)split_grid() * 2 * part_floats(d);
-}
-
-// ---------------------------------------------------------------------------
 // CUDA-core form: tiles of 64 tokens in shared memory as float32.
 // ---------------------------------------------------------------------------
+constexpr int kHB = 16;        // query heads per item
+constexpr int kTile = 64;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParams p) {
-    constexpr int TILE = 64, LD = D + 4, NG = 256 / D, NA = kHB / NG;
+    constexpr int TILE = kTile, LD = D + 4, NG = 256 / D, NA = kHB / NG;
     extern __shared__ float sm[];
     float *sK = sm, *sV = sK + TILE * LD, *sQ = sV + TILE * D, *sS = sQ + kHB * D;   // sS [kHB][TILE]
     float *sM = sS + kHB * TILE, *sL = sM + kHB, *sC = sL + kHB;                     // max, sum, correction
-    __shared__ int64_t s_sum[258];
+    __shared__ int64_t s_sum[257];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, wy = tid >> 5;
     const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
+    ptx::pdl_launch_dependents();     // the join kernel may start its setup
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
     if ((int)blockIdx.x >= sp.g) return;
     int64_t w = (int64_t)blockIdx.x * sp.W / sp.g;
@@ -276,7 +192,7 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
                 if (col == 0 && p.lse) p.lse[(int64_t)n * p.Hq + hq0 + g] = (sM[g] + log2f(l)) / kLog2E;
             }
         } else {
-            float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D);
+            float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, kHB);
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
                 const int g = hg + i * NG;
@@ -300,16 +216,17 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
 // Join: one CTA per sequence, one warp per query head.  Heads whose item one
 // CTA had whole are done already; a sequence without tokens gets zeros.
 // ---------------------------------------------------------------------------
-template <typename T, int D, int TILE>
+template <typename T, int D, int TILE, int HB>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int grid) {
-    __shared__ int64_t s_sum[258];
+    __shared__ int64_t s_sum[257];
     __shared__ int s_n;
     const int n = blockIdx.x, lane = threadIdx.x & 31;
-    const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
+    const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     constexpr int E = D / 32;
     T *out = static_cast<T *>(p.out);
     const int64_t nt = tiles_of<TILE>(p, n);
     if (nt == 0) {
+        ptx::pdl_wait();         // this grid's end stands for the one before it too
         clamp_len(p, n, threadIdx.x == 0);
         for (int i = threadIdx.x; i < p.Hq * D; i += 256) out[(int64_t)n * p.Hq * D + i] = from_f32<T>(0.f);
         if (p.lse)
@@ -317,21 +234,22 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
         return;
     }
     const Split sp = find_split<TILE>(p, items, grid, -1, n, s_sum, &s_n);
+    ptx::pdl_wait();             // the partial results
     for (int hq = threadIdx.x >> 5; hq < p.Hq; hq += 8) {
-        const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / kHB, g = gi % kHB;
+        const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / HB, g = gi % HB;
         const int64_t s = sp.cum * items + item * nt, e = s + nt;
         const int b0 = (int)(((s + 1) * sp.g - 1) / sp.W), b1 = (int)((e * sp.g - 1) / sp.W);
         if (b0 == b1) continue;
         float m = -INFINITY, l = 0.f, a[E] = {};
         for (int b = b0; b <= b1; ++b) {
-            const float *part = p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D);
+            const float *part = p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB);
             const float mb = part[2 * g], lb = part[2 * g + 1];
             const float mn = fmaxf(m, mb), mu = mn == -INFINITY ? 0.f : mn;
             const float f = exp2f(m - mu), fb = exp2f(mb - mu);
             m = mn;
             l = l * f + lb * fb;
 #pragma unroll
-            for (int i = 0; i < E; ++i) a[i] = a[i] * f + part[kHB * 2 + g * D + lane * E + i] * fb;
+            for (int i = 0; i < E; ++i) a[i] = a[i] * f + part[HB * 2 + g * D + lane * E + i] * fb;
         }
         const int64_t row = (int64_t)n * p.Hq + hq;
 #pragma unroll
@@ -341,18 +259,46 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     }
 }
 
+template <typename T, int D, int TILE, int HB>
+static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.N);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, TILE, HB>, p, grid);
+}
+
+// Query heads per item of the tensor-core form: one pass over the cache for up to 32 of them.
+static int heads_tc(int G) { return G <= 16 ? 16 : 32; }
+
+// The tensor-core form: its TMA copies take whole 8-row groups of a page, and
+// their row coordinates are 32-bit.
+static bool use_tc(const PagedParams &p, int d, bool bf16) {
+    return bf16 && d >= 64 && p.page_shift >= 3 && p.num_pages > 0 && p.max_pages > 0 &&
+           ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
+}
+
+size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d) {
+    const size_t tc = (size_t)sm_count() * 2 * part_floats(d, heads_tc(Hq / Hkv));
+    const size_t simt = (size_t)2 * sm_count() * 2 * part_floats(d, kHB);
+    return sizeof(float) * (tc > simt ? tc : simt);
+}
+
 template <typename T, int D>
 static cudaError_t paged_simt(const PagedParams &p, cudaStream_t st) {
-    constexpr int TILE = 64;
-    const size_t smem = sizeof(float) * (TILE * (D + 4) + TILE * D + kHB * D + kHB * TILE + 3 * kHB);
+    const size_t smem = sizeof(float) * (kTile * (D + 4) + kTile * D + kHB * D + kHB * kTile + 3 * kHB);
     cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = split_grid();
+    const int grid = 2 * sm_count();
     paged_decode_simt_kernel<T, D><<<grid, 256, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    paged_join_kernel<T, D, TILE><<<p.N, 256, 0, st>>>(p, grid);
-    return cudaGetLastError();
+    return launch_join<T, D, kTile, kHB>(p, grid, st);
 }
 
 template <typename T>
@@ -366,7 +312,15 @@ static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) 
 }
 
 cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
-    return bf16 ? paged_dispatch<__nv_bfloat16>(p, d, st) : paged_dispatch<float>(p, d, st);
+    if (!use_tc(p, d, bf16)) return bf16 ? paged_dispatch<__nv_bfloat16>(p, d, st) : paged_dispatch<float>(p, d, st);
+    const int HB = heads_tc(p.G), grid = sm_count();
+    const cudaError_t e = launch_paged_decode_tc(p, d, HB, grid, st);
+    if (e != cudaSuccess) return e;
+    if (d == 64)
+        return HB == 16 ? launch_join<__nv_bfloat16, 64, kTileTc, 16>(p, grid, st)
+                        : launch_join<__nv_bfloat16, 64, kTileTc, 32>(p, grid, st);
+    return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16>(p, grid, st)
+                    : launch_join<__nv_bfloat16, 128, kTileTc, 32>(p, grid, st);
 }
 
 }  // namespace kda

@@ -147,6 +147,7 @@ size_t kda_paged_decode_workspace_size(int num_seqs, int Hq, int Hkv, int d, kda
  *   lse          [num_seqs, Hq] float32 (written), or NULL
  *   workspace    16-byte aligned, kda_paged_decode_workspace_size() bytes
  * Tokens on a page whose id lies outside the cache are recorded and left out.
+ * A table covers at most 2^30 tokens per sequence.
  */
 kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, const void *v_cache,
                               int num_pages, int page_size, const int32_t *page_table,
