@@ -16,10 +16,11 @@
 // are split into three bf16 terms (24 bits) whose products accumulate in
 // float32, from zero in every chunk, before one float32 addition to the state.
 //
-// Roles of the 20 warps of a CTA (one CTA per SM): 0 loads by TMA, two chunks
-// ahead; 1 issues Q K^T, S^T Q^T and V^T P^T; 2 issues the state's product; 4-7
-// take P out of TMEM and later the output; 8-11 split the decayed keys; 12-19
-// hold the state, 64 of its columns of one row per thread.  mbarriers link them.
+// Roles of the 20 warps of a CTA (one CTA per SM): 0 and 1 take P out of TMEM; 2
+// loads by TMA, two chunks ahead, and issues the state's product; 3 issues
+// Q K^T, S^T Q^T and V^T P^T; 4-7 write the output; 8-11 split the decayed keys;
+// 12-19 hold the state, 64 of its columns of one row per thread.  mbarriers link
+// them.
 #include <cuda.h>
 
 #include "kda_layers.cuh"
@@ -51,8 +52,9 @@ constexpr uint32_t R_P = R_T + 6 * kTile;                 // P [i][j], two buffe
 constexpr uint32_t R_S = R_P + 2 * kTile;                 // S bf16 [dk][dv]: two halves of 128 rows
 constexpr uint32_t kSHalf = 128 * 128;
 constexpr uint32_t R_O = R_S + 2 * kSHalf;                // output staging [token][dv]
-constexpr uint32_t R_PW = R_O + 2 * kTile;                // lambda^1 .. lambda^64
-constexpr uint32_t kSmem = R_PW + C * 4 + 1024;
+constexpr uint32_t R_PW = R_O + 2 * kTile;                // lambda^1 .. lambda^64, of two items in turn
+constexpr uint32_t R_KW = R_PW + 2 * C * 4;                // lambda^0 .. lambda^63, one copy for each key warp
+constexpr uint32_t kSmem = R_KW + 4 * C * 4 + 1024;
 static_assert(kSmem <= 231000, "shared memory");
 
 // ---- tensor memory columns (512)
@@ -61,7 +63,7 @@ __device__ __forceinline__ uint32_t tm_qs(int b) { return 128 + b * 128; }    //
 __device__ __forceinline__ uint32_t tm_pv(int b) { return 192 + b * 128; }    // V^T P^T
 constexpr uint32_t TM_DS = 384;
 
-enum Bar { LD, LD1, FREE, FREE1, QK, QK1, PREADY, PREADY1, OD, OD1, OFREE, OFREE1, QS, SREADY, TFULL, TFULL1, DS, DSFREE, NBAR };
+enum Bar { LD, LD1, FREE, FREE1, QK, QK1, PREADY, PREADY1, OD, OD1, OFREE, OFREE1, QS, SREADY, TF, DSH = TF + 4, DS = DSH + 2, DSFREE, NBAR };
 
 struct Params {
     const float *log_decay;
@@ -72,22 +74,25 @@ struct Params {
     const float *init;          // initial states, or nullptr
     float *fin;                 // final states, or nullptr
     __nv_bfloat16 *out;
+    const __nv_bfloat16 *v;     // (the values again, for the rare path)
+    int64_t ldv;
     const int32_t *order;       // longest-first order of the sequences, or nullptr
     uint32_t *status;
     int seg_len;                // 0: a chain is one item; else tokens per segment
     float *seg;                 // [segment][H][D][D]
-    int64_t seg_cap;            // segments that seg has room for (more only if the offsets overlap)
+    int seg_cap;                // segments that seg has room for (more only if the offsets overlap)
 };
 
 // One piece of a chain: tokens [t0, t1) of one head.
 struct Item {
-    int64_t t0, t1;
+    int t0, t1;
     int head;
     const float *from;          // start state, nullptr for zeros
     float *to;                  // end state, nullptr for none
 };
 
-__device__ __forceinline__ void bounds(const Params &p, int seq, int64_t &bos, int64_t &eos, bool tell) {
+// Offsets are below 2^31 (the entry point sees to it), so token counts are int.
+__device__ __forceinline__ void bounds(const Params &p, int seq, int &bos, int &eos, bool tell) {
     bos = p.cu[seq];
     eos = p.cu[seq + 1];
     if (bos < 0 || eos < bos || eos > p.total) {
@@ -96,74 +101,94 @@ __device__ __forceinline__ void bounds(const Params &p, int seq, int64_t &bos, i
     }
 }
 
+// Segments of a sequence; an empty one has one empty segment (its state is copied).
+__device__ __forceinline__ int segments(const Params &p, int len) {
+    return len > 0 ? (int)((unsigned)(len - 1) / (unsigned)p.seg_len) + 1 : 1;
+}
+
 // Walks this CTA's items in order; every role walks its own copy.
 template <bool OUT>
 struct Walk {
-    int it = 0;
-    __device__ bool next(const Params &p, Item &x, bool tell) {
-        const int64_t chain_floats = (int64_t)D * D;
+    unsigned it = 0;
+    __device__ __noinline__ bool next(const Params &p, Item &x, bool tell) {
+        constexpr int64_t kState = (int64_t)D * D;
+        const unsigned H = (unsigned)p.H;
         if (p.seg_len == 0) {
             // rows of gridDim.x chains, dealt out forwards and backwards in turn: with the longest first, every
             // CTA gets about the same number of tokens
-            const int64_t i = (int64_t)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const unsigned chains = (unsigned)p.N * H, row = it * gridDim.x;
+            if (row >= chains) return false;
+            const unsigned i = row + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             ++it;
-            if ((int64_t)(it - 1) * gridDim.x >= (int64_t)p.N * p.H) return false;
-            if (i >= (int64_t)p.N * p.H) {      // the last row is shorter
-                x.t0 = x.t1 = 0; x.head = 0; x.from = nullptr; x.to = nullptr;
-                return true;
-            }
-            const int k = (int)(i / p.H), seq = p.order ? p.order[k] : k;
-            x.head = (int)(i % p.H);
+            x.t0 = x.t1 = x.head = 0;
+            x.from = nullptr;
+            x.to = nullptr;
+            if (i >= chains) return true;       // the last row is shorter
+            const unsigned k = i / H;
+            const int seq = p.order ? p.order[k] : (int)k;
+            x.head = (int)(i - k * H);
             bounds(p, seq, x.t0, x.t1, tell);
-            const int64_t at = ((int64_t)seq * p.H + x.head) * chain_floats;
-            x.from = p.init ? p.init + at : nullptr;
-            x.to = p.fin ? p.fin + at : nullptr;
+            const int64_t at = ((int64_t)seq * H + x.head) * kState;
+            if (p.init) x.from = p.init + at;
+            if (p.fin) x.to = p.fin + at;
             return true;
         }
         // segments of all sequences in order, heads fastest; the state pass (OUT = false) skips each last one
-        int64_t i = (int64_t)it * gridDim.x + blockIdx.x;
+        unsigned i = it * gridDim.x + blockIdx.x;
         ++it;
-        x.head = (int)(i % p.H);
-        i /= p.H;
-        int64_t before = 0;                     // segments of the sequences before
+        const unsigned seg = i / H;
+        x.head = (int)(i - seg * H);
+        int before = 0;                         // segments of the sequences before
+#pragma unroll 1
         for (int n = 0; n < p.N; ++n) {
-            int64_t bos, eos;
+            int bos, eos;
             bounds(p, n, bos, eos, tell && it == 1);
-            // an empty sequence is one empty segment: its state is copied
-            const int64_t segs = eos > bos ? (eos - bos + p.seg_len - 1) / p.seg_len : 1;
-            if (i < before + segs) {
-                if (i >= p.seg_cap) {
-                    if (tell) report_status(p.status, kDevBadSeqlens);
-                    return false;
-                }
-                const int64_t g = i - before;
-                const int64_t at = ((int64_t)n * p.H + x.head) * chain_floats;
-                float *cell = p.seg + (i * p.H + x.head) * chain_floats;
-                x.t0 = bos + g * p.seg_len;
-                x.t1 = x.t0 + p.seg_len < eos ? x.t0 + p.seg_len : eos;
-                if (OUT) {
-                    x.from = cell;
-                    x.to = g == segs - 1 && p.fin ? p.fin + at : nullptr;
-                } else {
-                    x.from = nullptr;
-                    x.to = cell;
-                    if (g == segs - 1) { x.t1 = x.t0; x.to = nullptr; }
-                }
-                return true;
-            }
+            const int segs = segments(p, eos - bos), g = (int)seg - before;
             before += segs;
+            if (g >= segs) continue;
+            if (seg >= (unsigned)p.seg_cap) {
+                if (tell) report_status(p.status, kDevBadSeqlens);
+                return false;
+            }
+            const int64_t at = ((int64_t)n * H + x.head) * kState;
+            float *cell = p.seg + ((int64_t)seg * H + x.head) * kState;
+            x.t0 = bos + g * p.seg_len;
+            x.t1 = eos - x.t0 > p.seg_len ? x.t0 + p.seg_len : eos;
+            if (OUT) {
+                x.from = cell;
+                x.to = g == segs - 1 && p.fin ? p.fin + at : nullptr;
+            } else {
+                x.from = nullptr;
+                x.to = cell;
+                if (g == segs - 1) { x.t1 = x.t0; x.to = nullptr; }
+            }
+            return true;
         }
         return false;
     }
 };
+
+// Chunks of all of a CTA's items.
+template <bool OUT>
+__device__ __noinline__ int chunks_of(const Params &p, bool tell) {
+    Walk<OUT> walk;
+    Item x;
+    int total = 0;
+    while (walk.next(p, x, tell)) total += (x.t1 - x.t0 + C - 1) / C;
+    return total;
+}
 
 __device__ __forceinline__ float log2_decay(const Params &p, int head) {
     // 2^(l2 n) with l2 no lower than -16384: exactly 0 for n >= 1 there, and 1 for n = 0
     return fmaxf(p.log_decay[head] * kLog2E, -16384.f);
 }
 
+// The bounded wait, out of line: the roles' loops run side by side, and what
+// they cost is instruction fetches as much as issue slots.
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t phase) { return ptx::mbar_wait(bar, phase & 1, kWaitBudget); }
+
 // Wait by all lanes of a warp; false for all if it ran out for any.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
+__device__ __noinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, kWaitBudget));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -179,22 +204,61 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead)
 }
 constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;      // instruction descriptor: operand is M- / N-major
 
+// x = k w of eight bf16 k, as three bf16 terms of eight bits each: x cut after
+// eight bits of its significand, the exact remainder cut likewise, and the
+// rest, which has at most eight bits left.
+__device__ __forceinline__ void split3(const uint4 &k, float w, uint4 &t1, uint4 &t2, uint4 &t3) {
+    const uint32_t u[4] = {k.x, k.y, k.z, k.w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16) * w;
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * w;
+    }
+    auto cut = [&](uint4 &t) {
+        uint32_t b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(x[i]);
+        t.x = __byte_perm(b[0], b[1], 0x7632);
+        t.y = __byte_perm(b[2], b[3], 0x7632);
+        t.z = __byte_perm(b[4], b[5], 0x7632);
+        t.w = __byte_perm(b[6], b[7], 0x7632);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] -= __uint_as_float(b[i] & 0xffff0000u);
+    };
+    cut(t1);
+    cut(t2);
+    cut(t3);
+}
+
+// sum_{s <= i} P_is v_sj for token i and channel j of the chunk at token t, v
+// from global memory.
+__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, const Item &x, int i, int j) {
+    float y = 0.f;
+    if (t + i >= x.t1) return y;
+#pragma unroll 1
+    for (int s = 0; s <= i; ++s)
+        y = fmaf(to_f32(*reinterpret_cast<const __nv_bfloat16 *>(sp + swz(i, s >> 3) + (s & 7) * 2)),
+                 to_f32(p.v[(int64_t)(t + s) * p.ldv + (int64_t)x.head * D + j]), y);
+    return y;
+}
+
 template <bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[NBAR];
-    __shared__ uint32_t s_tmem, s_abort, s_bad[2];
+    __shared__ uint32_t s_tmem, s_abort;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(sm);
 
     if (threadIdx.x == 0) {
-        const uint8_t counts[NBAR] = {1, 1, OUT ? 3 : 1, OUT ? 3 : 1, 1, 1, 2, 2, 1, 1, 4, 4, 1, 8, 4, 4, 1, 8};
+        const uint8_t counts[NBAR] = {1, 1, OUT ? 2 : 1, OUT ? 2 : 1, 1, 1, 2, 2, 1, 1, 4, 4, 1, 8, 4, 4, 4, 4, 1, 1, 1, 8};
         for (int i = 0; i < NBAR; ++i) ptx::mbar_init(&bar[i], counts[i]);
         ptx::fence_mbar_init();
-        s_abort = s_bad[0] = s_bad[1] = 0;
+        s_abort = 0;
         if (OUT) ptx::prefetch_tensormap(&mq);
         ptx::prefetch_tensormap(&mk);
         ptx::prefetch_tensormap(&mv);
@@ -204,6 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(&s_tmem, 512);
         ptx::tmem_relinquish();
     }
+    if (OUT)                           // P's masked quarter stays zero
+        for (int i = threadIdx.x; i < 2 * (int)kTile / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(sm + R_P)[i] = make_uint4(0, 0, 0, 0);
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
@@ -213,275 +280,283 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk<OUT> walk;
     Item x;
 
-    if (warp == 0) {                                              // ---- loads
-        if (lane == 0) {
-            int c = 0;
-            while (ok && walk.next(p, x, true)) {
-                for (int64_t t = x.t0; t < x.t1; t += C, ++c) {
-                    const int s = c & 1;
-                    if (c >= 2 && !ptx::mbar_wait(&bar[FREE + s], ((c >> 1) - 1) & 1, kWaitBudget)) { ok = false; break; }
-                    uint8_t *st = sm + R_STAGE + s * kStage;
-                    ptx::mbar_arrive_expect_tx(&bar[LD + s], (OUT ? 6 : 4) * kTile);
+    if (warp == 2) {                                              // ---- loads, and the state's product
+        // one thread does whichever of the two can go ahead
+        const int total = chunks_of<OUT>(p, true);
+        if (ptx::elect_one()) {
+            const uint32_t id = ptx::idesc_bf16_f32(128, 128) | kAMn | kBMn;
+            const uint64_t dt = sdesc_mn_sw128(base + R_T, kTile);
+            int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
+            int t = 0;
+            x.t1 = 0;
+            long long since = clock64();
+            while (dc < total) {
+                bool did = false;
+                if (lc < total && (lc < 2 || ptx::mbar_try_wait(&bar[FREE + (lc & 1)], ((lc >> 1) - 1) & 1))) {
+                    while (t >= x.t1) {
+                        walk.next(p, x, false);
+                        t = x.t0;
+                    }
+                    uint64_t *full = &bar[LD + (lc & 1)];
+                    uint8_t *st = sm + R_STAGE + (lc & 1) * kStage;
+                    ptx::mbar_arrive_expect_tx(full, (OUT ? 6 : 4) * kTile);
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const int col = x.head * D + h * 64;
-                        if (OUT) ptx::tma_load_2d(st + O_Q + h * kHalf, &mq, col, (int)t, &bar[LD + s]);
-                        ptx::tma_load_2d(st + O_K + h * kHalf, &mk, col, (int)t, &bar[LD + s]);
-                        ptx::tma_load_2d(st + O_V + h * kTile, &mv, col, (int)t, &bar[LD + s]);
+                        ptx::tma_load_2d(st + O_K + h * kHalf, &mk, col, t, full);
+                        if (OUT) ptx::tma_load_2d(st + O_Q + h * kHalf, &mq, col, t, full);
+                        ptx::tma_load_2d(st + O_V + h * kTile, &mv, col, t, full);
                     }
+                    t += C;
+                    ++lc;
+                    did = true;
                 }
+                const int b = dc & 1;
+                if (ptx::mbar_try_wait(&bar[TF + 2 * b + half], (dc >> 1) & 1) &&
+                    (half == 1 || dc == 0 || ptx::mbar_try_wait(&bar[DSFREE], (dc - 1) & 1))) {
+                    ptx::tc_fence_after_sync();
+                    const uint64_t a = dt + half * (4096 >> 4);
+                    const uint64_t v = sdesc_mn_sw128(base + R_STAGE + b * kStage + O_V, kTile) + half * (4096 >> 4);
+#pragma unroll 2
+                    for (int e = 0; e < 6; ++e)
+                        ptx::mma_bf16_ss(tmem + TM_DS, a + ((e >> 1) * 2 * kTile + (e & 1) * 2048) / 16,
+                                         v + (e & 1) * (2048 >> 4), id, half > 0 || e > 0);
+                    ptx::mma_commit(&bar[DSH + half]);
+                    if (half == 1) {
+                        ptx::mma_commit(&bar[DS]);
+                        ptx::mma_commit(&bar[FREE + b]);
+                        ++dc;
+                    }
+                    half ^= 1;
+                    did = true;
+                }
+                const long long now = clock64();
+                if (did) since = now;
+                else if (now - since > kWaitBudget) { ok = false; break; }
             }
         }
-    } else if (warp == 1) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
-        if (OUT && lane == 0) {
-            // chunks in all
-            int total = 0;
-            while (walk.next(p, x, false)) total += (int)((x.t1 - x.t0 + C - 1) / C);
-            const uint32_t id_qk = ptx::idesc_bf16_f32(128, 64), id_qs = ptx::idesc_bf16_f32(128, 64) | kAMn;
-            auto qk = [&](int c) {
-                const int b = c & 1;
-                if (!ptx::mbar_wait(&bar[LD + b], (c >> 1) & 1, kWaitBudget)) return false;
-                // P's TMEM buffer was read two chunks ago
-                if (c >= 2 && !ptx::mbar_wait(&bar[PREADY + b], ((c >> 1) - 1) & 1, kWaitBudget)) return false;
-                ptx::tc_fence_after_sync();
-                const uint32_t st = base + R_STAGE + b * kStage;
-                // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
-                mma_k<8>(tmem + tm_p(b), st + O_Q, kHalf, st + O_K, kHalf, id_qk, false);
-                ptx::mma_commit(&bar[QK + b]);
-                return true;
-            };
-            ok = total == 0 || qk(0);
-            for (int c = 0; c < total && ok; ++c) {
-                if (c + 1 < total && !qk(c + 1)) { ok = false; break; }
-                const int b = c & 1;
-                const uint32_t st = base + R_STAGE + b * kStage;
-                if (!ptx::mbar_wait(&bar[SREADY], c & 1, kWaitBudget) ||
-                    (c >= 2 && !ptx::mbar_wait(&bar[OFREE + b], ((c >> 1) - 1) & 1, kWaitBudget))) { ok = false; break; }
-                ptx::tc_fence_after_sync();
-                {
-                    const uint64_t a = sdesc_mn_sw128(base + R_S, kSHalf), q = ptx::sdesc_kmajor_sw128(st + O_Q);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        ptx::mma_bf16_ss(tmem + tm_qs(b), a + k * (2048 >> 4), q + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
-                                         id_qs, k > 0);
-                }
-                ptx::mma_commit(&bar[QS]);
-                if (!ptx::mbar_wait(&bar[PREADY + b], (c >> 1) & 1, kWaitBudget) ||
-                    !ptx::mbar_wait(&bar[TFULL + b], (c >> 1) & 1, kWaitBudget)) { ok = false; break; }    // (V's tail is clean)
-                ptx::tc_fence_after_sync();
-                {
-                    const uint64_t a = sdesc_mn_sw128(st + O_V, kTile), q = ptx::sdesc_kmajor_sw128(base + R_P + b * kTile);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), q + k * 2, id_qs, k > 0);
-                }
-                ptx::mma_commit(&bar[OD + b]);
-                ptx::mma_commit(&bar[FREE + b]);
-            }
-        }
-    } else if (warp == 2) {                                       // ---- the state's product
-        if (lane == 0) {
-            const uint32_t id = ptx::idesc_bf16_f32(128, 128) | kAMn | kBMn;
+    } else if (warp < 2) {                                        // ---- P: thread = token of the chunk
+        if (OUT) {
+            const int i = threadIdx.x;
+            const float fi = (float)i;
             int c = 0;
             while (ok && walk.next(p, x, false)) {
-                for (int64_t t = x.t0; t < x.t1; t += C, ++c) {
+                const float l2 = log2_decay(p, x.head);
+                for (int t = x.t0; t < x.t1; t += C, ++c) {
                     const int b = c & 1;
-                    if (!ptx::mbar_wait(&bar[TFULL + b], (c >> 1) & 1, kWaitBudget) ||
-                        (c >= 1 && !ptx::mbar_wait(&bar[DSFREE], (c - 1) & 1, kWaitBudget))) { ok = false; break; }
+                    // the output products of two chunks ago have read this buffer, and so has their output if it had to
+                    ok = warp_wait(&bar[QK + b], c >> 1) && (c < 2 || warp_wait(&bar[OFREE + b], (c >> 1) - 1));
+                    if (!ok) break;
                     ptx::tc_fence_after_sync();
-                    const uint64_t v = sdesc_mn_sw128(base + R_STAGE + b * kStage + O_V, kTile);
+                    uint8_t *sp = sm + R_P + b * kTile;
+                    // (columns 32-63 of rows 0-31 are never written: zero from the start)
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 16) {
+                        float d[16];
+                        ptx::tmem_ld16(tmem + ((uint32_t)warp << 21) + tm_p(b) + j0, d);
+                        const float f0 = fi - (float)j0;
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        const uint64_t a = sdesc_mn_sw128(base + R_T + e * 2 * kTile, kTile);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_bf16_ss(tmem + TM_DS, a + k * (2048 >> 4), v + k * (2048 >> 4), id, e > 0 || k > 0);
+                        for (int e = 0; e < 16; ++e) {
+                            const float gap = f0 - (float)e;
+                            d[e] = gap >= 0.f ? d[e] * ex2(l2 * gap) : 0.f;
+                        }
+                        st_chunk(sp, swz(i, j0 >> 3), d);
+                        st_chunk(sp, swz(i, (j0 >> 3) + 1), d + 8);
                     }
-                    ptx::mma_commit(&bar[DS]);
+                    ptx::fence_async_smem();
+                    ptx::tc_fence_before_sync();
+                    warp_arrive(&bar[PREADY + b]);
+                }
+            }
+        }
+    } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
+        const int total = OUT ? chunks_of<OUT>(p, false) : 0;
+        if (OUT && ptx::elect_one()) {
+            const uint32_t id_qk = ptx::idesc_bf16_f32(128, 64), id_qs = id_qk | kAMn;
+            const uint64_t ds = sdesc_mn_sw128(base + R_S, kSHalf);
+            for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
+                const int b = c & 1, phase = (c >> 1) & 1;
+                const uint32_t st = base + R_STAGE + b * kStage;
+                if (c >= 0) {
+                    if (!wait_on(&bar[SREADY], c & 1) ||
+                        (c >= 2 && !wait_on(&bar[OFREE + b], phase ^ 1))) { ok = false; break; }
+                    ptx::tc_fence_after_sync();
+                    const uint64_t q = ptx::sdesc_kmajor_sw128(st + O_Q);
+#pragma unroll 2
+                    for (int k = 0; k < 8; ++k)
+                        ptx::mma_bf16_ss(tmem + tm_qs(b), ds + k * (2048 >> 4), q + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
+                                         id_qs, k > 0);
+                    ptx::mma_commit(&bar[QS]);
+                }
+                // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
+                // load may be waiting for this very chunk's stage.
+                bool todo = c + 1 < total;
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    const int nb = b ^ 1, np = ((c + 1) >> 1) & 1;
+                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[LD + nb], np))) {
+                        todo = false;
+                        if (!wait_on(&bar[LD + nb], np) ||
+                            // P's TMEM buffer was read two chunks ago
+                            (c >= 1 && !wait_on(&bar[PREADY + nb], np ^ 1))) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                        const uint32_t sn = base + R_STAGE + nb * kStage;
+                        // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
+                        const uint64_t q = ptx::sdesc_kmajor_sw128(sn + O_Q), kd = ptx::sdesc_kmajor_sw128(sn + O_K);
+#pragma unroll 2
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                            ptx::mma_bf16_ss(tmem + tm_p(nb), q + at, kd + at, id_qk, k > 0);
+                        }
+                        ptx::mma_commit(&bar[QK + nb]);
+                    }
+                    if (c < 0 || pass == 1) continue;
+                    if (!wait_on(&bar[PREADY + b], phase) ||
+                        !wait_on(&bar[TF + 2 * b], phase) ||           // (V's tail is clean)
+                        !wait_on(&bar[TF + 2 * b + 1], phase)) { ok = false; break; }
+                    ptx::tc_fence_after_sync();
+                    const uint64_t a = sdesc_mn_sw128(st + O_V, kTile), pb = ptx::sdesc_kmajor_sw128(base + R_P + b * kTile);
+#pragma unroll 2
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id_qs, k > 0);
+                    ptx::mma_commit(&bar[OD + b]);
                     ptx::mma_commit(&bar[FREE + b]);
                 }
             }
         }
-    } else if (warp >= 4 && warp < 8) {                           // ---- P, then the output
+    } else if (warp >= 4 && warp < 8) {                           // ---- the output
         if (OUT) {
             const int tid = threadIdx.x - 128, q = warp & 3;
             float *pw = reinterpret_cast<float *>(sm + R_PW);
             uint8_t *so = sm + R_O;
-            // the chunk whose output is still to come
-            int64_t ot = 0;
-            int on = 0, ohead = 0, head = -1;
-            float l2 = 0.f;
-            auto output = [&](int c) {      // false: gave up (all 128 threads alike)
-                const int b = c & 1;
-                bool good = ptx::mbar_wait(&bar[OD + b], (c >> 1) & 1, kWaitBudget);
-                if (tid == 0) ptx::bulk_wait_read();                 // the staging tile's last store
-                const bool bad = *static_cast<volatile uint32_t *>(&s_bad[b]) != 0;   // an infinity or NaN in V
-                if (ptx::bar_any(1, 128, !good || !ok)) return false;
-                ptx::tc_fence_after_sync();
-                if (!bad && tid == 0) ptx::mbar_arrive(&bar[FREE + b]);
-                const int j = q * 32 + lane;                         // value channel
-                const uint8_t *sp = sm + R_P + b * kTile, *sv = sm + R_STAGE + b * kStage + O_V + (j >> 6) * kTile;
-                auto cell = [](const uint8_t *tile, int row, int col) {
-                    return to_f32(*reinterpret_cast<const __nv_bfloat16 *>(tile + swz(row, (col & 63) >> 3) + (col & 7) * 2));
-                };
-#pragma unroll
-                for (int i0 = 0; i0 < C; i0 += 16) {
-                    float a[16], o[16];
-                    ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + tm_qs(b) + i0, a);
-                    ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + tm_pv(b) + i0, o);
-                    ptx::tmem_ld_wait();
-                    if (bad) {
-                        // P's zeros would turn a later token's infinity into NaN: sum the real pairs alone
-#pragma unroll 1
-                        for (int i = 0; i < 16; ++i) {
-                            float y = 0.f;
-                            for (int s = 0; s <= i0 + i; ++s) y = fmaf(cell(sp, i0 + i, s), cell(sv, s, j), y);
-                            o[0] = i == 0 ? y : o[0];
-#pragma unroll
-                            for (int e = 1; e < 16; ++e) o[e] = i == e ? y : o[e];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float y = fmaf(a[i], pw[i0 + i], o[i]) * p.scale;
-                        *reinterpret_cast<__nv_bfloat16 *>(so + (j >> 6) * kTile + swz(i0 + i, (j & 63) >> 3) + (j & 7) * 2) =
-                            __float2bfloat16_rn(y);
-                    }
-                }
-                ptx::tc_fence_before_sync();
-                warp_arrive(&bar[OFREE + b]);
-                ptx::fence_async_smem();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (bad && tid == 0) ptx::mbar_arrive(&bar[FREE + b]);
-                if (on == C) {
-                    if (tid == 0) {
-                        ptx::tma_store_2d(&mo, ohead * D, (int)ot, so);
-                        ptx::tma_store_2d(&mo, ohead * D + 64, (int)ot, so + kTile);
-                        ptx::bulk_commit();
-                    }
-                } else {
-                    for (int i = tid; i < on * 16; i += 128) {
-                        const int r = i >> 4, ch = i & 15;
-                        *reinterpret_cast<uint4 *>(p.out + ((ot + r) * p.H + ohead) * D + ch * 8) =
-                            *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
-                    }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");   // read before the next chunk's tile
-                }
-                return true;
-            };
-            int c = 0;
+            int c = 0, item = 0;
             while (ok && walk.next(p, x, false)) {
-                for (int64_t t = x.t0; t < x.t1; t += C, ++c) {
+                if (x.t1 > x.t0) {                                   // (read after the first chunk's barrier)
+                    ++item;
+                    if (tid < C) pw[(item & 1) * C + tid] = exp2f(log2_decay(p, x.head) * (float)(tid + 1));
+                }
+                for (int t = x.t0; t < x.t1; t += C, ++c) {
                     const int b = c & 1;
-                    // the chunk before leaves first where its powers differ from this chunk's
-                    if (x.head != head && c > 0) {
-                        if (!output(c - 1)) { ok = false; break; }
-                        on = 0;
-                    }
-                    if (x.head != head) {
-                        head = x.head;
-                        l2 = log2_decay(p, head);
-                        asm volatile("bar.sync 1, 128;" ::: "memory");
-                        if (tid < C) pw[tid] = exp2f(l2 * (float)(tid + 1));
-                    }
-                    ok = warp_wait(&bar[QK + b], c >> 1);
-                    if (ok && q < 2) {
-                        ptx::tc_fence_after_sync();
-                        const int i = q * 32 + lane;
-                        uint8_t *sp = sm + R_P + b * kTile;
+                    const bool good = wait_on(&bar[OD + b], (c >> 1) & 1);
+                    if (tid == 0) ptx::bulk_wait_read();             // the staging tile's last store
+                    ok = !ptx::bar_any(1, 128, !good);        // all 128 threads go on or give up alike
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint8_t *sp = sm + R_P + b * kTile;
+                    const float *pwo = pw + (item & 1) * C;
+                    // 16 value channels x 32 tokens at a time, as 8 x 8 tiles that are stored transposed
+#pragma unroll 1
+                    for (int part = 0; part < 4; ++part) {
+                        const int j0 = q * 32 + (part & 1) * 16, i0 = (part >> 1) * 32;
+                        const uint32_t at = tmem + ((uint32_t)j0 << 16) + i0;
+                        float a[16], o[16];
+                        ptx::tmem_ld_tiles4(at + tm_qs(b), a);
+                        ptx::tmem_ld_tiles4(at + tm_pv(b), o);
+                        ptx::tmem_ld_wait();
+                        const int ic = i0 + 2 * (lane & 3);          // this thread's first token
+                        // an infinity or NaN in v shows in its channel at every token, as P's zeros for later tokens turn
+                        // it into NaN: there the sums are taken again over the real pairs
+                        float probe = 0.f;
 #pragma unroll
-                        for (int j0 = 0; j0 < C; j0 += 16) {
-                            float d[16];
-                            ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + tm_p(b) + j0, d);
-                            ptx::tmem_ld_wait();
+                        for (int e = 0; e < 16; ++e) probe = fmaf(o[e], 0.f, probe);
+                        if (probe != 0.f)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int gap = i - (j0 + e);
-                                d[e] = gap >= 0 ? d[e] * ex2(l2 * (float)gap) : 0.f;
-                            }
-                            st_chunk(sp, swz(i, j0 >> 3), d);
-                            st_chunk(sp, swz(i, (j0 >> 3) + 1), d + 8);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = real_pairs(p, sp, t, x, ic + (e >> 2) * 8 + (e & 1), j0 + (lane >> 2) + ((e >> 1) & 1) * 8);
+                        uint32_t u[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = *reinterpret_cast<const float2 *>(pwo + ic + e * 8);
+                            u[2 * e] = pack_bf16(fmaf(a[4 * e], f.x, o[4 * e]) * p.scale, fmaf(a[4 * e + 1], f.y, o[4 * e + 1]) * p.scale);
+                            u[2 * e + 1] = pack_bf16(fmaf(a[4 * e + 2], f.x, o[4 * e + 2]) * p.scale,
+                                                     fmaf(a[4 * e + 3], f.y, o[4 * e + 3]) * p.scale);
                         }
-                        ptx::fence_async_smem();
-                        ptx::tc_fence_before_sync();
-                        warp_arrive(&bar[PREADY + b]);
+                        // tile lane / 8: tokens + 8 (tile / 2), channels + 8 (tile % 2); row lane % 8
+                        const int r = i0 + (lane >> 4) * 8 + (lane & 7), ch = (j0 & 63) / 8 + ((lane >> 3) & 1);
+                        const uint32_t to = ptx::smem_addr(so) + (j0 >> 6) * kTile;
+                        ptx::stmatrix4_trans(to + swz(r, ch), u[0], u[1], u[2], u[3]);
+                        ptx::stmatrix4_trans(to + swz(r + 16, ch), u[4], u[5], u[6], u[7]);
                     }
-                    if (c > 0 && on > 0) {
-                        if (!output(c - 1)) { ok = false; break; }
-                    } else if (ptx::bar_any(1, 128, !ok)) {
-                        ok = false;
-                        break;
+                    ptx::tc_fence_before_sync();
+                    warp_arrive(&bar[OFREE + b]);
+                    ptx::fence_async_smem();
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    const int on = min(x.t1 - t, C);
+                    if (on == C) {
+                        if (tid == 0) {
+                            ptx::tma_store_2d(&mo, x.head * D, t, so);
+                            ptx::tma_store_2d(&mo, x.head * D + 64, t, so + kTile);
+                            ptx::bulk_commit();
+                        }
+                    } else {
+                        for (int i = tid; i < on * 16; i += 128) {
+                            const int r = i >> 4, ch = i & 15;
+                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.H + x.head) * D + ch * 8) =
+                                *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
+                        }
+                        asm volatile("bar.sync 1, 128;" ::: "memory");   // read before the next chunk's tile
                     }
-                    ot = t;
-                    on = (int)(x.t1 - t < C ? x.t1 - t : C);
-                    ohead = head;
                 }
             }
-            if (ok && c > 0 && !output(c - 1)) ok = false;
             if (tid == 0) ptx::bulk_wait_all();
         }
     } else if (warp >= 8 && warp < 12) {                          // ---- the decayed keys in three terms
-        const int tid = threadIdx.x - 256;
+        const int tid = threadIdx.x - 256, r0 = tid >> 4, ch = tid & 15;     // rows r0, r0 + 8, ...; 16-byte column
+        const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
+        float *kw = reinterpret_cast<float *>(sm + R_KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
         int c = 0;
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
-            for (int64_t t = x.t0; t < x.t1; t += C, ++c) {
-                const int b = c & 1, n = (int)(x.t1 - t < C ? x.t1 - t : C);
-                ok = warp_wait(&bar[LD + b], c >> 1) && (c == 0 || warp_wait(&bar[DS], c - 1));
+            __syncwarp();
+            kw[lane] = exp2f(l2 * (float)lane);
+            kw[lane + 32] = exp2f(l2 * (float)(lane + 32));
+            __syncwarp();
+            for (int t = x.t0; t < x.t1; t += C, ++c) {
+                const int b = c & 1, n = min(x.t1 - t, C);
+                ok = warp_wait(&bar[LD + b], c >> 1);
                 if (!ok) break;
                 uint8_t *st = sm + R_STAGE + b * kStage;
-                uint32_t top = 0;                                 // largest magnitudes of V's pairs
-                const int ch = tid & 15;
-                const uint32_t half = (ch >> 3), cc = ch & 7;
-#pragma unroll 2
-                for (int r = tid >> 4; r < C; r += 8) {
-                    float k[8], hi[8];
-                    ld_chunk(st + O_K + half * kHalf, swz(r, cc), k);
-                    const float w = r < n ? exp2f(l2 * (float)(n - 1 - r)) : 0.f;
-                    uint8_t *dst = sm + R_T + half * kTile;
-                    const uint32_t at = swz(r, cc);
+                const float *w = kw + max(n - 1 - r0, 0);         // row r0 + 8 i: lambda^{n - 1 - r0 - 8 i}
+                const int most = max(n - 1 - r0, 0) >> 3;
+                const uint8_t *kp = st + O_K + half * kHalf + at0;
+                uint8_t *dst = sm + R_T + half * kTile + at0;
+                if (n < C)                                        // rows of the next sequence
+                    for (int i = 0; i < 8; ++i)
+                        if (r0 + 8 * i >= n)
+                            *reinterpret_cast<uint4 *>(st + O_V + half * kTile + at0 + i * 1024) = make_uint4(0, 0, 0, 0);
+                // The loads of the next 32 tokens go before the stores of these: beside the MMAs' own reads a load
+                // from shared memory takes some 200 cycles.
+                uint4 kn[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) k[e] = r < n ? k[e] * w : 0.f;
+                for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + i * 1024);
+#pragma unroll 1
+                for (int th = 0; th < 2; ++th) {                  // 32 tokens at a time
+                    uint4 k[4];
+                    float wi[4];
 #pragma unroll
-                    for (int term = 0; term < 3; ++term) {
-                        uint4 u;
-                        u.x = pack_bf16(k[0], k[1]); u.y = pack_bf16(k[2], k[3]);
-                        u.z = pack_bf16(k[4], k[5]); u.w = pack_bf16(k[6], k[7]);
-                        *reinterpret_cast<uint4 *>(dst + term * 2 * kTile + at) = u;
-                        if (term < 2) {
-                            const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = bf2_to_f2(uu[e]);
-                                hi[2 * e] = f.x; hi[2 * e + 1] = f.y;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) k[e] -= hi[e];
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        k[i] = kn[i];
+                        wi[i] = w[-8 * min(th * 4 + i, most)];
+                        if (r0 + 8 * (th * 4 + i) >= n) k[i] = make_uint4(0, 0, 0, 0);
                     }
-                    uint4 *pv = reinterpret_cast<uint4 *>(st + O_V + half * kTile + at);
-                    if (r < n) {
-                        if (OUT) {
-                            const uint4 u = *pv;
-                            const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+                    if (th == 0)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                // a lane of all-ones exponent, in either half
-                                const uint32_t m = uu[e] & 0x7f807f80u;
-                                top |= (uint32_t)((m & 0xffff0000u) == 0x7f800000u) | (uint32_t)((m & 0xffffu) == 0x7f80u);
-                            }
-                        }
-                    } else {
-                        *pv = make_uint4(0, 0, 0, 0);             // rows of the next sequence
+                        for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + (i + 4) * 1024);
+                    if (c > 0 && !(ok = warp_wait(&bar[DSH + th], c - 1))) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 t1, t2, t3;
+                        split3(k[i], wi[i], t1, t2, t3);
+                        *reinterpret_cast<uint4 *>(dst + i * 1024) = t1;
+                        *reinterpret_cast<uint4 *>(dst + i * 1024 + 2 * kTile) = t2;
+                        *reinterpret_cast<uint4 *>(dst + i * 1024 + 4 * kTile) = t3;
                     }
+                    dst += 4096;
+                    ptx::fence_async_smem();
+                    warp_arrive(&bar[TF + 2 * b + th]);
                 }
-                if (OUT) {
-                    // the flag of two chunks ago was read before its stage was handed back
-                    const bool any = __any_sync(0xffffffffu, top != 0);
-                    if (lane == 0 && any) atomicOr(&s_bad[b], 1u << (warp - 8));
-                    if (lane == 0 && !any) atomicAnd(&s_bad[b], ~(1u << (warp - 8)));
-                }
-                ptx::fence_async_smem();
-                warp_arrive(&bar[TFULL + b]);
+                if (!ok) break;
             }
         }
     } else if (warp >= 12) {                                      // ---- the state
@@ -497,34 +572,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (x.from) f = *reinterpret_cast<const float4 *>(x.from + mine + e);
                 s[e] = f.x; s[e + 1] = f.y; s[e + 2] = f.z; s[e + 3] = f.w;
             }
-            auto copy_out = [&](int e) {       // 16 columns as bf16
-                uint8_t *ss = sm + R_S + (col0 >> 6) * kSHalf;
-                st_chunk(ss, swz(row, e >> 3), s + e);
-                st_chunk(ss, swz(row, (e >> 3) + 1), s + e + 8);
+            auto copy_out = [&](int e) {       // 8 columns as bf16
+                st_chunk(sm + R_S + (col0 >> 6) * kSHalf, swz(row, e >> 3), s + e);
             };
             if (OUT && x.t1 > x.t0) {
                 if (c > 0) ok = warp_wait(&bar[QS], c - 1);
                 if (!ok) break;
 #pragma unroll
-                for (int e = 0; e < 64; e += 16) copy_out(e);
+                for (int e = 0; e < 64; e += 8) copy_out(e);
                 ptx::fence_async_smem();
                 warp_arrive(&bar[SREADY]);
             }
-            for (int64_t t = x.t0; t < x.t1; t += C, ++c) {
-                const int n = (int)(x.t1 - t < C ? x.t1 - t : C);
+            for (int t = x.t0; t < x.t1; t += C, ++c) {
+                const int n = min(x.t1 - t, C);
                 const bool more = t + C < x.t1;
                 const float f = exp2f(l2 * (float)n);
                 ok = warp_wait(&bar[DS], c) && (!OUT || !more || warp_wait(&bar[QS], c));
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
+                const uint32_t at = tmem + ((uint32_t)q << 21) + TM_DS + col0;
 #pragma unroll
                 for (int e = 0; e < 64; e += 16) {
                     float d[16];
-                    ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + TM_DS + col0 + e, d);
+                    ptx::tmem_ld16(at + e, d);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
-                    if (OUT && more) copy_out(e);
+                    if (OUT && more) {
+                        copy_out(e);
+                        copy_out(e + 8);
+                    }
                 }
                 ptx::tc_fence_before_sync();
                 warp_arrive(&bar[DSFREE]);
@@ -564,23 +641,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) decay_segments_kernel(const Params p) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    const int n = blockIdx.y / p.H, h = blockIdx.y % p.H;
-    int64_t bos, eos, before = 0;
+    const int n = (int)((unsigned)blockIdx.y / (unsigned)p.H), h = (int)blockIdx.y - n * p.H;
+    int bos, eos, before = 0;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         bounds(p, i, bos, eos, false);
-        before += eos > bos ? (eos - bos + p.seg_len - 1) / p.seg_len : 1;
+        before += segments(p, eos - bos);
     }
     bounds(p, n, bos, eos, false);
-    int64_t segs = eos > bos ? (eos - bos + p.seg_len - 1) / p.seg_len : 1;
+    int segs = segments(p, eos - bos);
     if (before + segs > p.seg_cap) segs = p.seg_cap - before;
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, step = (int64_t)p.H * D * D;
     const float f = exp2f(log2_decay(p, h) * (float)p.seg_len);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.init) s = *reinterpret_cast<const float4 *>(p.init + (int64_t)blockIdx.y * D * D + at);
-    float4 *cell = reinterpret_cast<float4 *>(p.seg + (before * p.H + h) * D * D + at);
+    float4 *cell = reinterpret_cast<float4 *>(p.seg + ((int64_t)before * p.H + h) * D * D + at);
     // (the first segment's start state is copied too: its buffer may be the one that the last segment writes)
 #pragma unroll 4
-    for (int64_t g = 0; g + 1 < segs; ++g) {
+    for (int g = 0; g + 1 < segs; ++g) {
         const float4 b = cell[g * (step / 4)];
         cell[g * (step / 4)] = s;
         s.x = fmaf(f, s.x, b.x); s.y = fmaf(f, s.y, b.y); s.z = fmaf(f, s.z, b.z); s.w = fmaf(f, s.w, b.w);
@@ -623,7 +701,7 @@ cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_
         return cudaErrorInvalidValue;
     const int sms = sm_count();
     Params p{d.log_decay, d.cu_seqlens, d.num_seqs, d.H, d.total, d.scale, d.init, d.fin,
-             static_cast<__nv_bfloat16 *>(d.out), nullptr, d.status, 0, nullptr, 0};
+             static_cast<__nv_bfloat16 *>(d.out), static_cast<const __nv_bfloat16 *>(d.v), d.ldv, nullptr, d.status, 0, nullptr, 0};
     cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(decay_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -643,8 +721,8 @@ cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_
     if (len) {
         p.seg_len = len;
         p.seg = reinterpret_cast<float *>(ws + ((kOrderAt + sizeof(int32_t) * (size_t)d.num_seqs + 1023) & ~size_t(1023)));
-        p.seg_cap = d.total / len + d.num_seqs;
-        const int64_t items = p.seg_cap * d.H;
+        p.seg_cap = (int)(d.total / len) + d.num_seqs;
+        const int64_t items = (int64_t)p.seg_cap * d.H;
         cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
         cfg.numAttrs = 0;
         if ((e = cudaLaunchKernelEx(&cfg, decay_chunk_kernel<false>, mq, mk, mv, mo, p)) != cudaSuccess) return e;
