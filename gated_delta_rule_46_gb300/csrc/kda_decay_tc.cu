@@ -40,6 +40,7 @@ using namespace tc;
 constexpr int C = 64, D = 128;
 constexpr int kThreads = 640;
 constexpr long long kWaitBudget = 2000000000LL;   // cycles (about one second)
+constexpr int kWaitTries = 1 << 24;               // attempts of a wait, at least some 20 cycles each
 constexpr long long kDrain = 20000000LL;
 
 // ---- shared memory, bytes from a 1024-aligned base.  Tiles have 128-byte rows
@@ -183,13 +184,19 @@ __device__ __forceinline__ float log2_decay(const Params &p, int head) {
     return fmaxf(p.log_decay[head] * kLog2E, -16384.f);
 }
 
-// The bounded wait, out of line: the roles' loops run side by side, and what
-// they cost is instruction fetches as much as issue slots.
-__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t phase) { return ptx::mbar_wait(bar, phase & 1, kWaitBudget); }
+// The bounded wait in few instructions (each attempt suspends for a while by
+// itself).  The roles' loops run side by side, so what they cost is instruction
+// fetches as much as issue slots; and a call would spill the state's registers.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t phase) {
+#pragma unroll 1
+    for (int i = 0; i < kWaitTries; ++i)
+        if (ptx::mbar_try_wait(bar, phase & 1)) return true;
+    return false;
+}
 
 // Wait by all lanes of a warp; false for all if it ran out for any.
-__device__ __noinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, kWaitBudget));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, wait_on(bar, phase));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
