@@ -5,7 +5,7 @@
 // start state S and lambda = exp(log_decay):
 //   P_ij = lambda^{i-j} q_i . k_j  (j <= i, else 0)
 //   O^T  = (S^T Q^T) diag(lambda^{i+1}) + V^T P^T
-//   S   <- lambda^n S + sum_j (lambda^{n-1-j} k_j) v_j^T
+//   S^T <- lambda^n S^T + sum_j v_j (lambda^{n-1-j} k_j)^T
 // Only the state links the chunks, and it takes part in one product (S^T Q^T)
 // and one update, so everything else of the next chunk runs ahead of it.
 //
@@ -17,10 +17,10 @@
 // float32, from zero in every chunk, before one float32 addition to the state.
 //
 // Roles of the 20 warps of a CTA (one CTA per SM): 0 and 1 take P out of TMEM; 2
-// loads by TMA, two chunks ahead, and issues the state's product; 3 issues
+// loads by TMA, up to three chunks ahead, and issues the state's product; 3 issues
 // Q K^T, S^T Q^T and V^T P^T; 4-7 write the output; 8-11 split the decayed keys;
-// 12-19 hold the state, 64 of its columns of one row per thread.  mbarriers link
-// them.
+// 12-19 hold the state, 64 key channels of one value channel per thread, and leave
+// its bf16 copy in TMEM, where the MMA takes it from.  mbarriers link them.
 #include <cuda.h>
 
 #include "kda_layers.cuh"
@@ -48,23 +48,24 @@ constexpr long long kDrain = 20000000LL;
 constexpr uint32_t kTile = C * 128;                       // 64 rows x 64 channels
 constexpr uint32_t R_STAGE = 0;                           // per stage: [Q0 K0 Q1 K1 V0 V1]
 constexpr uint32_t kStage = 6 * kTile, O_Q = 0, O_K = kTile, O_V = 4 * kTile, kHalf = 2 * kTile;
-constexpr uint32_t R_T = 2 * kStage;                      // three terms of the decayed keys, [token][channel]
+constexpr int NS = 3;                                     // stages
+constexpr uint32_t R_T = NS * kStage;                     // three terms of the decayed keys, [token][channel]
 constexpr uint32_t R_P = R_T + 6 * kTile;                 // P [i][j], two buffers
-constexpr uint32_t R_S = R_P + 2 * kTile;                 // S bf16 [dk][dv]: two halves of 128 rows
-constexpr uint32_t kSHalf = 128 * 128;
-constexpr uint32_t R_O = R_S + 2 * kSHalf;                // output staging [token][dv]
+constexpr uint32_t R_O = R_P + 2 * kTile;                 // output staging [token][dv]
 constexpr uint32_t R_PW = R_O + 2 * kTile;                // lambda^1 .. lambda^64, of two items in turn
 constexpr uint32_t R_KW = R_PW + 2 * C * 4;                // lambda^0 .. lambda^63, one copy for each key warp
 constexpr uint32_t kSmem = R_KW + 4 * C * 4 + 1024;
-static_assert(kSmem <= 231000, "shared memory");
+static_assert(kSmem <= 232448 - 256, "shared memory");
 
 // ---- tensor memory columns (512)
-__device__ __forceinline__ uint32_t tm_p(int b) { return b * 64; }            // Q K^T, lanes 0-63
+constexpr uint32_t TM_P = 0;                                                  // Q K^T, lanes 0-63
+constexpr uint32_t TM_S = 64;                                                 // S^T as bf16 pairs: lane = dv, 64 columns
 __device__ __forceinline__ uint32_t tm_qs(int b) { return 128 + b * 128; }    // S^T Q^T
 __device__ __forceinline__ uint32_t tm_pv(int b) { return 192 + b * 128; }    // V^T P^T
-constexpr uint32_t TM_DS = 384;
+constexpr uint32_t TM_DS = 384;                                               // what the chunk adds to S^T
 
-enum Bar { LD, LD1, FREE, FREE1, QK, QK1, PREADY, PREADY1, OD, OD1, OFREE, OFREE1, QS, SREADY, TF, DSH = TF + 4, DS = DSH + 2, DSFREE, NBAR };
+enum Bar { LD, FREE = LD + NS, QK = FREE + NS, PREADY = QK + 2, OD = PREADY + 2, OFREE = OD + 2, QS = OFREE + 2, SREADY,
+           TF, DSH = TF + 2 * NS, DS = DSH + 2, DSFREE, NBAR };
 
 struct Params {
     const float *log_decay;
@@ -240,13 +241,13 @@ __device__ __forceinline__ void split3(const uint4 &k, float w, uint4 &t1, uint4
 
 // sum_{s <= i} P_is v_sj for token i and channel j of the chunk at token t, v
 // from global memory.
-__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, const Item &x, int i, int j) {
+__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int head, int i, int j) {
     float y = 0.f;
-    if (t + i >= x.t1) return y;
+    if (t + i >= t1) return y;
 #pragma unroll 1
     for (int s = 0; s <= i; ++s)
         y = fmaf(to_f32(*reinterpret_cast<const __nv_bfloat16 *>(sp + swz(i, s >> 3) + (s & 7) * 2)),
-                 to_f32(p.v[(int64_t)(t + s) * p.ldv + (int64_t)x.head * D + j]), y);
+                 to_f32(p.v[(int64_t)(t + s) * p.ldv + (int64_t)head * D + j]), y);
     return y;
 }
 
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = ptx::smem_addr(sm);
 
     if (threadIdx.x == 0) {
-        const uint8_t counts[NBAR] = {1, 1, OUT ? 2 : 1, OUT ? 2 : 1, 1, 1, 2, 2, 1, 1, 4, 4, 1, 8, 4, 4, 4, 4, 1, 1, 1, 8};
+        const uint8_t counts[NBAR] = {1, 1, 1, OUT ? 2 : 1, OUT ? 2 : 1, OUT ? 2 : 1, 1, 1, 2, 2, 1, 1, 4, 4, 1, 8, 4, 4, 4, 4, 4, 4, 1, 1, 1, 8};
         for (int i = 0; i < NBAR; ++i) ptx::mbar_init(&bar[i], counts[i]);
         ptx::fence_mbar_init();
         s_abort = 0;
@@ -294,45 +295,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t id = ptx::idesc_bf16_f32(128, 128) | kAMn | kBMn;
             const uint64_t dt = sdesc_mn_sw128(base + R_T, kTile);
             int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
-            int t = 0;
-            x.t1 = 0;
+            int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
+            int t = 0, t1 = 0, col0 = 0;
             long long since = clock64();
             while (dc < total) {
                 bool did = false;
-                if (lc < total && (lc < 2 || ptx::mbar_try_wait(&bar[FREE + (lc & 1)], ((lc >> 1) - 1) & 1))) {
-                    while (t >= x.t1) {
+                if (lc < total && (lp == 0 || ptx::mbar_try_wait(&bar[FREE + ls], (lp - 1) & 1))) {
+                    while (t >= t1) {
                         walk.next(p, x, false);
                         t = x.t0;
+                        t1 = x.t1;
+                        col0 = x.head * D;
                     }
-                    uint64_t *full = &bar[LD + (lc & 1)];
-                    uint8_t *st = sm + R_STAGE + (lc & 1) * kStage;
+                    uint64_t *full = &bar[LD + ls];
+                    uint8_t *st = sm + R_STAGE + ls * kStage;
                     ptx::mbar_arrive_expect_tx(full, (OUT ? 6 : 4) * kTile);
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        const int col = x.head * D + h * 64;
+                        const int col = col0 + h * 64;
                         ptx::tma_load_2d(st + O_K + h * kHalf, &mk, col, t, full);
                         if (OUT) ptx::tma_load_2d(st + O_Q + h * kHalf, &mq, col, t, full);
                         ptx::tma_load_2d(st + O_V + h * kTile, &mv, col, t, full);
                     }
                     t += C;
                     ++lc;
+                    if (++ls == NS) { ls = 0; ++lp; }
                     did = true;
                 }
-                const int b = dc & 1;
-                if (ptx::mbar_try_wait(&bar[TF + 2 * b + half], (dc >> 1) & 1) &&
+                if (ptx::mbar_try_wait(&bar[TF + 2 * ds + half], dp & 1) &&
                     (half == 1 || dc == 0 || ptx::mbar_try_wait(&bar[DSFREE], (dc - 1) & 1))) {
                     ptx::tc_fence_after_sync();
                     const uint64_t a = dt + half * (4096 >> 4);
-                    const uint64_t v = sdesc_mn_sw128(base + R_STAGE + b * kStage + O_V, kTile) + half * (4096 >> 4);
+                    const uint64_t v = sdesc_mn_sw128(base + R_STAGE + ds * kStage + O_V, kTile) + half * (4096 >> 4);
 #pragma unroll 2
                     for (int e = 0; e < 6; ++e)
-                        ptx::mma_bf16_ss(tmem + TM_DS, a + ((e >> 1) * 2 * kTile + (e & 1) * 2048) / 16,
-                                         v + (e & 1) * (2048 >> 4), id, half > 0 || e > 0);
+                        ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * 2 * kTile + (e & 1) * 2048) / 16,
+                                         id, half > 0 || e > 0);
                     ptx::mma_commit(&bar[DSH + half]);
                     if (half == 1) {
                         ptx::mma_commit(&bar[DS]);
-                        ptx::mma_commit(&bar[FREE + b]);
+                        ptx::mma_commit(&bar[FREE + ds]);
                         ++dc;
+                        if (++ds == NS) { ds = 0; ++dp; }
                     }
                     half ^= 1;
                     did = true;
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int c = 0;
             while (ok && walk.next(p, x, false)) {
                 const float l2 = log2_decay(p, x.head);
-                for (int t = x.t0; t < x.t1; t += C, ++c) {
+                for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
                     const int b = c & 1;
                     // the output products of two chunks ago have read this buffer, and so has their output if it had to
                     ok = warp_wait(&bar[QK + b], c >> 1) && (c < 2 || warp_wait(&bar[OFREE + b], (c >> 1) - 1));
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 16) {
                         float d[16];
-                        ptx::tmem_ld16(tmem + ((uint32_t)warp << 21) + tm_p(b) + j0, d);
+                        ptx::tmem_ld16(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
                         const float f0 = fi - (float)j0;
                         ptx::tmem_ld_wait();
 #pragma unroll
@@ -380,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
         const int total = OUT ? chunks_of<OUT>(p, false) : 0;
         if (OUT && ptx::elect_one()) {
-            const uint32_t id_qk = ptx::idesc_bf16_f32(128, 64), id_qs = id_qk | kAMn;
-            const uint64_t ds = sdesc_mn_sw128(base + R_S, kSHalf);
+            const uint32_t id = ptx::idesc_bf16_f32(128, 64);
+            int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
             for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
                 const int b = c & 1, phase = (c >> 1) & 1;
-                const uint32_t st = base + R_STAGE + b * kStage;
+                const uint32_t st = base + R_STAGE + s * kStage;
                 if (c >= 0) {
                     if (!wait_on(&bar[SREADY], c & 1) ||
                         (c >= 2 && !wait_on(&bar[OFREE + b], phase ^ 1))) { ok = false; break; }
@@ -392,44 +396,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t q = ptx::sdesc_kmajor_sw128(st + O_Q);
 #pragma unroll 2
                     for (int k = 0; k < 8; ++k)
-                        ptx::mma_bf16_ss(tmem + tm_qs(b), ds + k * (2048 >> 4), q + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
-                                         id_qs, k > 0);
+                        ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
+                                         id, k > 0);
                     ptx::mma_commit(&bar[QS]);
+                    if (!wait_on(&bar[PREADY + b], phase)) { ok = false; break; }
+                    ptx::tc_fence_after_sync();
                 }
                 // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
                 // load may be waiting for this very chunk's stage.
                 bool todo = c + 1 < total;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
-                    const int nb = b ^ 1, np = ((c + 1) >> 1) & 1;
-                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[LD + nb], np))) {
+                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[LD + ns], np & 1))) {
                         todo = false;
-                        if (!wait_on(&bar[LD + nb], np) ||
-                            // P's TMEM buffer was read two chunks ago
-                            (c >= 1 && !wait_on(&bar[PREADY + nb], np ^ 1))) { ok = false; break; }
+                        if (!wait_on(&bar[LD + ns], np)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
-                        const uint32_t sn = base + R_STAGE + nb * kStage;
+                        const uint32_t sn = base + R_STAGE + ns * kStage;
                         // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
                         const uint64_t q = ptx::sdesc_kmajor_sw128(sn + O_Q), kd = ptx::sdesc_kmajor_sw128(sn + O_K);
 #pragma unroll 2
                         for (int k = 0; k < 8; ++k) {
                             const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                            ptx::mma_bf16_ss(tmem + tm_p(nb), q + at, kd + at, id_qk, k > 0);
+                            ptx::mma_bf16_ss(tmem + TM_P, q + at, kd + at, id, k > 0);
                         }
-                        ptx::mma_commit(&bar[QK + nb]);
+                        ptx::mma_commit(&bar[QK + (b ^ 1)]);
                     }
                     if (c < 0 || pass == 1) continue;
-                    if (!wait_on(&bar[PREADY + b], phase) ||
-                        !wait_on(&bar[TF + 2 * b], phase) ||           // (V's tail is clean)
-                        !wait_on(&bar[TF + 2 * b + 1], phase)) { ok = false; break; }
+                    if (!wait_on(&bar[TF + 2 * s], sp) ||                  // (V's tail is clean)
+                        !wait_on(&bar[TF + 2 * s + 1], sp)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
                     const uint64_t a = sdesc_mn_sw128(st + O_V, kTile), pb = ptx::sdesc_kmajor_sw128(base + R_P + b * kTile);
 #pragma unroll 2
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id_qs, k > 0);
+                        ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
                     ptx::mma_commit(&bar[OD + b]);
-                    ptx::mma_commit(&bar[FREE + b]);
+                    ptx::mma_commit(&bar[FREE + s]);
                 }
+                s = ns;
+                sp = np;
+                if (++ns == NS) { ns = 0; ++np; }
             }
         }
     } else if (warp >= 4 && warp < 8) {                           // ---- the output
@@ -439,11 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *so = sm + R_O;
             int c = 0, item = 0;
             while (ok && walk.next(p, x, false)) {
-                if (x.t1 > x.t0) {                                   // (read after the first chunk's barrier)
+                const int t1 = x.t1, head = x.head;
+                if (t1 > x.t0) {                                     // (read after the first chunk's barrier)
                     ++item;
-                    if (tid < C) pw[(item & 1) * C + tid] = exp2f(log2_decay(p, x.head) * (float)(tid + 1));
+                    if (tid < C) pw[(item & 1) * C + tid] = exp2f(log2_decay(p, head) * (float)(tid + 1));
                 }
-                for (int t = x.t0; t < x.t1; t += C, ++c) {
+                for (int t = x.t0; t < t1; t += C, ++c) {
                     const int b = c & 1;
                     const bool good = wait_on(&bar[OD + b], (c >> 1) & 1);
                     if (tid == 0) ptx::bulk_wait_read();             // the staging tile's last store
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (probe != 0.f)
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                o[e] = real_pairs(p, sp, t, x, ic + (e >> 2) * 8 + (e & 1), j0 + (lane >> 2) + ((e >> 1) & 1) * 8);
+                                o[e] = real_pairs(p, sp, t, t1, head, ic + (e >> 2) * 8 + (e & 1), j0 + (lane >> 2) + ((e >> 1) & 1) * 8);
                         uint32_t u[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -489,17 +495,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     warp_arrive(&bar[OFREE + b]);
                     ptx::fence_async_smem();
                     asm volatile("bar.sync 1, 128;" ::: "memory");
-                    const int on = min(x.t1 - t, C);
+                    const int on = min(t1 - t, C);
                     if (on == C) {
                         if (tid == 0) {
-                            ptx::tma_store_2d(&mo, x.head * D, t, so);
-                            ptx::tma_store_2d(&mo, x.head * D + 64, t, so + kTile);
+                            ptx::tma_store_2d(&mo, head * D, t, so);
+                            ptx::tma_store_2d(&mo, head * D + 64, t, so + kTile);
                             ptx::bulk_commit();
                         }
                     } else {
                         for (int i = tid; i < on * 16; i += 128) {
                             const int r = i >> 4, ch = i & 15;
-                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.H + x.head) * D + ch * 8) =
+                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.H + head) * D + ch * 8) =
                                 *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
                         }
                         asm volatile("bar.sync 1, 128;" ::: "memory");   // read before the next chunk's tile
@@ -512,18 +518,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tid = threadIdx.x - 256, r0 = tid >> 4, ch = tid & 15;     // rows r0, r0 + 8, ...; 16-byte column
         const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
         float *kw = reinterpret_cast<float *>(sm + R_KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
-        int c = 0;
+        int c = 0, s = 0, round = 0;
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
             __syncwarp();
             kw[lane] = exp2f(l2 * (float)lane);
             kw[lane + 32] = exp2f(l2 * (float)(lane + 32));
             __syncwarp();
-            for (int t = x.t0; t < x.t1; t += C, ++c) {
-                const int b = c & 1, n = min(x.t1 - t, C);
-                ok = warp_wait(&bar[LD + b], c >> 1);
+            for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
+                const int n = min(t1 - t, C);
+                ok = warp_wait(&bar[LD + s], round);
                 if (!ok) break;
-                uint8_t *st = sm + R_STAGE + b * kStage;
+                uint8_t *st = sm + R_STAGE + s * kStage;
+                uint64_t *full = &bar[TF + 2 * s];
+                if (++s == NS) { s = 0; ++round; }
                 const float *w = kw + max(n - 1 - r0, 0);         // row r0 + 8 i: lambda^{n - 1 - r0 - 8 i}
                 const int most = max(n - 1 - r0, 0) >> 3;
                 const uint8_t *kp = st + O_K + half * kHalf + at0;
@@ -561,68 +569,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     dst += 4096;
                     ptx::fence_async_smem();
-                    warp_arrive(&bar[TF + 2 * b + th]);
+                    warp_arrive(full + th);
                 }
                 if (!ok) break;
             }
         }
-    } else if (warp >= 12) {                                      // ---- the state
-        const int q = warp & 3, col0 = ((warp - 12) >> 2) * 64, row = q * 32 + lane;
-        const int64_t mine = (int64_t)row * D + col0;
+    } else if (warp >= 12) {                                      // ---- the state: lane = value channel
+        const int q = warp & 3, k0 = ((warp - 12) >> 2) * 64;         // key channels k0 .. k0 + 63
+        const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
+        const uint32_t at = tmem + ((uint32_t)q << 21);
         int c = 0;
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
+            const float *from = x.from;
             float s[64];
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (x.from) f = *reinterpret_cast<const float4 *>(x.from + mine + e);
-                s[e] = f.x; s[e + 1] = f.y; s[e + 2] = f.z; s[e + 3] = f.w;
-            }
-            auto copy_out = [&](int e) {       // 8 columns as bf16
-                st_chunk(sm + R_S + (col0 >> 6) * kSHalf, swz(row, e >> 3), s + e);
+            for (int e = 0; e < 64; ++e) s[e] = from ? from[mine + e * D] : 0.f;
+            auto copy_out = [&](int e) {       // 16 channels as bf16 pairs
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = pack_bf16(s[e + 2 * i], s[e + 2 * i + 1]);
+                ptx::tmem_st8(at + TM_S + (k0 + e) / 2, u);
             };
-            if (OUT && x.t1 > x.t0) {
+            const int t0 = x.t0, t1 = x.t1;
+            if (OUT && t1 > t0) {
                 if (c > 0) ok = warp_wait(&bar[QS], c - 1);
                 if (!ok) break;
+                ptx::tc_fence_after_sync();
 #pragma unroll
-                for (int e = 0; e < 64; e += 8) copy_out(e);
-                ptx::fence_async_smem();
+                for (int e = 0; e < 64; e += 16) copy_out(e);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
                 warp_arrive(&bar[SREADY]);
             }
-            for (int t = x.t0; t < x.t1; t += C, ++c) {
-                const int n = min(x.t1 - t, C);
-                const bool more = t + C < x.t1;
-                const float f = exp2f(l2 * (float)n);
-                ok = warp_wait(&bar[DS], c) && (!OUT || !more || warp_wait(&bar[QS], c));
+            for (int t = t0; t < t1; t += C, ++c) {
+                const bool more = OUT && t + C < t1;
+                const float f = exp2f(l2 * (float)min(t1 - t, C));
+                ok = warp_wait(&bar[DS], c) && (!more || warp_wait(&bar[QS], c));
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t at = tmem + ((uint32_t)q << 21) + TM_DS + col0;
 #pragma unroll
                 for (int e = 0; e < 64; e += 16) {
                     float d[16];
-                    ptx::tmem_ld16(at + e, d);
+                    ptx::tmem_ld16(at + TM_DS + k0 + e, d);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
-                    if (OUT && more) {
-                        copy_out(e);
-                        copy_out(e + 8);
-                    }
+                    if (more) copy_out(e);
                 }
+                if (more) ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
                 warp_arrive(&bar[DSFREE]);
-                if (OUT && more) {
-                    ptx::fence_async_smem();
-                    warp_arrive(&bar[SREADY]);
-                }
+                if (more) warp_arrive(&bar[SREADY]);
             }
             if (!ok) break;
-            if (x.to) {
+            if (x.to)
 #pragma unroll
-                for (int e = 0; e < 64; e += 4)
-                    *reinterpret_cast<float4 *>(x.to + mine + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
-            }
+                for (int e = 0; e < 64; ++e) x.to[mine + e * D] = s[e];
         }
     }
     if (!ok) {
