@@ -85,9 +85,10 @@ struct PagedParams {
     void *out;
     float *lse;
     float *part;                    // partial results (workspace)
+    bool lone;                      // no item has more than one tile: nothing to join
     uint32_t *status;
 };
-size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d);
+size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
 cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st);
 
 // Number of SMs of the current device.

@@ -134,9 +134,10 @@ kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t
     return from_cuda(kda::launch_paged_append(p, vec16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t kda_paged_decode_workspace_size(int num_seqs, int Hq, int Hkv, int d, kda_dtype_t dtype) {
-    if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !dim_ok(d) || !dtype_ok(dtype)) return 0;
-    return (kda::paged_decode_workspace_bytes(Hq, Hkv, d) + 255) & ~size_t(255);
+size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq, int Hkv, int d,
+                                       kda_dtype_t dtype) {
+    if (num_seqs <= 0 || max_tokens < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !dim_ok(d) || !dtype_ok(dtype)) return 0;
+    return (kda::paged_decode_workspace_bytes(num_seqs, max_tokens, Hq, Hkv, d) + 255) & ~size_t(255);
 }
 
 kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, const void *v_cache,
@@ -158,11 +159,11 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
     if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return KDA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < kda_paged_decode_workspace_size(num_seqs, Hq, Hkv, d, dtype))
+        workspace_bytes < kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype))
         return KDA_ERR_INVALID_ARG;
-    const kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
+    kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
                              seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
-                             static_cast<float *>(workspace), status};
+                             static_cast<float *>(workspace), false, status};
     return from_cuda(kda::launch_paged_decode(p, d, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 

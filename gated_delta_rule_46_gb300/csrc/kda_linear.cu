@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_f32(128, p.NT);
             for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
                 const int s = i % p.stages;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(320)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && ptx::elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_f32(256, 256);
             int it = 0, n = 0;
             for (int i = pair; i < tiles && ok; i += pairs, ++n) {

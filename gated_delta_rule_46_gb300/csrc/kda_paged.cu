@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
     const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
     ptx::pdl_launch_dependents();     // the join kernel may start its setup
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    empty_sequences<T, TILE>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
     int64_t w = (int64_t)blockIdx.x * sp.W / sp.g;
     const int64_t w1 = (int64_t)(blockIdx.x + 1) * sp.W / sp.g;
@@ -227,10 +228,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     const int64_t nt = tiles_of<TILE>(p, n);
     if (nt == 0) {
         ptx::pdl_wait();         // this grid's end stands for the one before it too
-        clamp_len(p, n, threadIdx.x == 0);
-        for (int i = threadIdx.x; i < p.Hq * D; i += 256) out[(int64_t)n * p.Hq * D + i] = from_f32<T>(0.f);
-        if (p.lse)
-            for (int i = threadIdx.x; i < p.Hq; i += 256) p.lse[(int64_t)n * p.Hq + i] = -INFINITY;
+        empty_sequence<T>(p, n, D);
         return;
     }
     const Split sp = find_split<TILE>(p, items, grid, -1, n, s_sum, &s_n);
@@ -261,6 +259,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
 
 template <typename T, int D, int TILE, int HB>
 static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) {
+    if (p.lone) return cudaSuccess;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -283,19 +282,34 @@ static bool use_tc(const PagedParams &p, int d, bool bf16) {
            ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
 }
 
-size_t paged_decode_workspace_bytes(int Hq, int Hkv, int d) {
-    const size_t tc = (size_t)sm_count() * 2 * part_floats(d, heads_tc(Hq / Hkv));
-    const size_t simt = (size_t)2 * sm_count() * 2 * part_floats(d, kHB);
+// CTAs that can have work: at most one per tile of the longest possible batch.
+static int grid_for(int N, int64_t max_tokens, int items, int tile, int most) {
+    const int64_t tiles = (int64_t)N * items * ((max_tokens + tile - 1) / tile);
+    return (int)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
+}
+static int grid_tc(int N, int64_t max_tokens, int Hkv, int G) {
+    const int HB = heads_tc(G);
+    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc, sm_count());
+}
+static int grid_simt(int N, int64_t max_tokens, int Hkv, int G) {
+    return grid_for(N, max_tokens, Hkv * ((G + kHB - 1) / kHB), kTile, 2 * sm_count());
+}
+
+size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
+    const int G = Hq / Hkv;
+    const size_t tc = (size_t)grid_tc(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_tc(G));
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G) * 2 * part_floats(d, kHB);
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 
 template <typename T, int D>
-static cudaError_t paged_simt(const PagedParams &p, cudaStream_t st) {
+static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
+    p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile;
     const size_t smem = sizeof(float) * (kTile * (D + 4) + kTile * D + kHB * D + kHB * kTile + 3 * kHB);
     cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = 2 * sm_count();
+    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
     paged_decode_simt_kernel<T, D><<<grid, 256, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_join<T, D, kTile, kHB>(p, grid, st);
@@ -313,14 +327,16 @@ static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) 
 
 cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
     if (!use_tc(p, d, bf16)) return bf16 ? paged_dispatch<__nv_bfloat16>(p, d, st) : paged_dispatch<float>(p, d, st);
-    const int HB = heads_tc(p.G), grid = sm_count();
-    const cudaError_t e = launch_paged_decode_tc(p, d, HB, grid, st);
+    const int HB = heads_tc(p.G), grid = grid_tc(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
+    PagedParams pt = p;
+    pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc;
+    const cudaError_t e = launch_paged_decode_tc(pt, d, HB, grid, st);
     if (e != cudaSuccess) return e;
     if (d == 64)
-        return HB == 16 ? launch_join<__nv_bfloat16, 64, kTileTc, 16>(p, grid, st)
-                        : launch_join<__nv_bfloat16, 64, kTileTc, 32>(p, grid, st);
-    return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16>(p, grid, st)
-                    : launch_join<__nv_bfloat16, 128, kTileTc, 32>(p, grid, st);
+        return HB == 16 ? launch_join<__nv_bfloat16, 64, kTileTc, 16>(pt, grid, st)
+                        : launch_join<__nv_bfloat16, 64, kTileTc, 32>(pt, grid, st);
+    return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16>(pt, grid, st)
+                    : launch_join<__nv_bfloat16, 128, kTileTc, 32>(pt, grid, st);
 }
 
 }  // namespace kda

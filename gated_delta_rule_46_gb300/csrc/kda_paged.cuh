@@ -82,6 +82,24 @@ __device__ Split find_split(const PagedParams &p, int items, int grid, int b, in
     return r;
 }
 
+// Zero outputs and lse = -inf of sequence n, which has no tokens (block-wide).
+template <typename T>
+__device__ __forceinline__ void empty_sequence(const PagedParams &p, int n, int D) {
+    clamp_len(p, n, threadIdx.x == 0);
+    T *out = static_cast<T *>(p.out) + (int64_t)n * p.Hq * D;
+    for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x) out[i] = from_f32<T>(0.f);
+    if (p.lse)
+        for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) p.lse[(int64_t)n * p.Hq + i] = -INFINITY;
+}
+
+// Those of all empty sequences, where no join kernel follows to write them.
+template <typename T, int TILE>
+__device__ __forceinline__ void empty_sequences(const PagedParams &p, int D) {
+    if (p.lone)
+        for (int n = blockIdx.x; n < p.N; n += gridDim.x)
+            if (tiles_of<TILE>(p, n) == 0) empty_sequence<T>(p, n, D);
+}
+
 // One partial result of an item of HB query heads: m, l (base-2 logarithms) per
 // head, then a[d] per head.
 __host__ __device__ constexpr int part_floats(int d, int HB) { return HB * (d + 2); }

@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(384, 1)
 
     ptx::pdl_launch_dependents();     // the join kernel may start its setup
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    empty_sequences<__nv_bfloat16, TILE>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBAR; ++i) {
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(384, 1)
             wk.next_item(p, last - first);
         }
     } else if (warp == 1) {                                       // ---- MMAs
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             const int total = (int)(wk.w1 - wk.w);
             // the tile that the S^T products have reached, one ahead of the O^T products
             int item_no = 0;

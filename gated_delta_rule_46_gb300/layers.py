@@ -12,7 +12,6 @@ stream it runs on.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -27,10 +26,13 @@ _SIGNATURES = {
     "kda_decay_prefill": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _L, _I, _I, _I, _I, _F, _P, _P, _P, _P, _Z, _P, _P]),
     "kda_decay_decode": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
     "kda_paged_append": (_I, [_P, _L, _P, _L, _P, _P, _I, _I, _P, _I, _P, _P, _I, _L, _I, _I, _I, _P, _P]),
-    "kda_paged_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "kda_paged_decode_workspace_size": (_Z, [_I, _L, _I, _I, _I, _I]),
     "kda_paged_decode": (_I, [_P, _L, _P, _P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _Z, _P, _P]),
 }
 _fns: dict = {}
+# torch's current stream of a device as an integer, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _fn(name):
@@ -43,44 +45,58 @@ def _fn(name):
 
 
 def _dense(t, name, shape, dtype, device):
-    """`t` is a contiguous tensor of this shape (-1: any), dtype and device; its pointer (None for None)."""
+    """`t` is a contiguous tensor of this shape, dtype and device; its pointer (None for None)."""
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(a != b and b >= 0 for a, b in zip(t.shape, shape))):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name, shape, dtype, device):
-    """`t` is a tensor of this shape whose rows (all axes but the first) are dense; its row stride."""
+def _rows(t, name, shape, width, dtype, device):
+    """`t` is a tensor of this shape whose rows (all axes but the first, `width` elements) are dense; its row stride."""
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
-        return math.prod(t.shape[1:])
-    width = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != width:
+        return width
+    inner = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != inner:
             raise ValueError(f"{name}: the rows of [T, ...] must be dense")
-        width *= n
+        inner *= n
     if t.shape[0] > 1 and t.stride(0) < width:
         raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)}, {width} elements)")
     return max(t.stride(0), width)
+
+
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} axes")
+    return t.shape
 
 
 def _code(dtype, name):
@@ -93,17 +109,19 @@ def _code(dtype, name):
 def _call(name, device, stream, allocated, *args):
     """Runs `name` on `device` and `stream` (torch's current one by default) and
     hands what was allocated for the call over to that stream."""
-    cur = torch.cuda.current_stream(device)
-    if stream is not None and stream != cur:
-        for t in allocated:
-            t.record_stream(stream)
+    index = device.index
+    if stream is None:
+        raw = _raw_stream(index)
     else:
-        stream = cur
-    if device.index == torch.cuda.current_device():
-        st = _fn(name)(*args, stream.cuda_stream)
+        raw = stream.cuda_stream
+        if raw != _raw_stream(index):
+            for t in allocated:
+                t.record_stream(stream)
+    if index == torch.cuda.current_device():
+        st = _fn(name)(*args, raw)
     else:
         with torch.cuda.device(device):
-            st = _fn(name)(*args, stream.cuda_stream)
+            st = _fn(name)(*args, raw)
     if st != KDA_OK:
         raise KDAError(st, name)
 
@@ -120,24 +138,22 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, out_dtype=None,
     """act(x w^T + bias) + residual for x [M, K] bf16 (rows any stride apart), w
     [N, K] bf16, bias [N] f32, residual [M, N] of the output's dtype (bf16, or
     out_dtype=torch.float32).  act: one of ACTIVATIONS."""
-    ldx = _rows(x, "x", None, torch.bfloat16, None)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
-    dev = x.device
-    M, K = x.shape
-    wp = _dense(w, "w", (-1, K), torch.bfloat16, dev)
-    N = w.shape[0]
+    dev = _cuda(x, "x")
+    M, K = _dims(x, "x", 2)
+    ldx = _rows(x, "x", (M, K), K, torch.bfloat16, dev)
+    N = _dims(w, "w", 2)[0]
+    wp = _dense(w, "w", (N, K), torch.bfloat16, dev)
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     new = []
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = x.new_empty((M, N), dtype=out_dtype)
         new.append(out)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     code = _code(out.dtype, "out")
     _call("kda_linear", dev, stream, new, x.data_ptr(), ldx, wp, _dense(bias, "bias", (N,), torch.float32, dev),
-          _dense(residual, "residual", (M, N), out.dtype, dev), _dense(out, "out", (M, N), None, dev), M, N, K,
+          _dense(residual, "residual", (M, N), out.dtype, dev), _dense(out, "out", (M, N), out.dtype, dev), M, N, K,
           ACTIVATIONS[act], code, _status(status, dev))
     return out
 
@@ -153,34 +169,35 @@ def decay_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, final_stat
     q, k [T, H, dk], v [T, H, dv] (bf16 or f32, all the same; rows any stride
     apart); log_decay [H] f32; cu_seqlens [N + 1] int32; initial_state
     [N, H, dk, dv] f32 or None.  Returns (out [T, H, dv], final_state or None)."""
-    code = _code(q.dtype, "q")
-    ldq = _rows(q, "q", None, q.dtype, None)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and v must be [T, H, d]")
-    T, H, dk = q.shape
-    dv, dev = v.shape[2], q.device
-    ldk = _rows(k, "k", (T, H, dk), q.dtype, dev)
-    ldv = _rows(v, "v", (T, H, dv), q.dtype, dev)
+    dev = _cuda(q, "q")
+    dt = q.dtype
+    code = _code(dt, "q")
+    T, H, dk = _dims(q, "q", 3)
+    dv = _dims(v, "v", 3)[2]
+    ldq = _rows(q, "q", (T, H, dk), H * dk, dt, dev)
+    ldk = _rows(k, "k", (T, H, dk), H * dk, dt, dev)
+    ldv = _rows(v, "v", (T, H, dv), H * dv, dt, dev)
     lp = _dense(log_decay, "log_decay", (H,), torch.float32, dev)
-    cp = _dense(cu_seqlens, "cu_seqlens", (-1,), torch.int32, dev)
-    N = cu_seqlens.shape[0] - 1
+    N = _dims(cu_seqlens, "cu_seqlens", 1)[0] - 1
+    cp = _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
     new = []
     if final_state is None and want_final_state:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = log_decay.new_empty((N, H, dk, dv))
         new.append(final_state)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+        out = q.new_empty((T, H, dv))
         new.append(out)
     if workspace is None:
         size = _fn("kda_decay_prefill_workspace_size")(T, N, H, dk, dv, code)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(size, dtype=torch.uint8)
             new.append(workspace)
-    wp = _dense(workspace, "workspace", (-1,), torch.uint8, dev)
+    size = 0 if workspace is None else _dims(workspace, "workspace", 1)[0]
+    wp = _dense(workspace, "workspace", (size,), torch.uint8, dev)
     _call("kda_decay_prefill", dev, stream, new, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, lp, cp, N, T,
           H, dk, dv, code, scale, _dense(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev),
           _dense(final_state, "final_state", (N, H, dk, dv), torch.float32, dev),
-          _dense(out, "out", (T, H, dv), q.dtype, dev), wp, workspace.numel() if workspace is not None else 0,
+          _dense(out, "out", (T, H, dv), dt, dev), wp, size,
           _status(status, dev))
     return out, final_state
 
@@ -189,22 +206,23 @@ def decay_decode(q, k, v, log_decay, state_pool, slot_ids=None, out=None, scale=
     """One token per sequence of the same mixer; the states in the pool [P, H,
     dk, dv] f32 are updated in place.  q, k [N, H, dk], v [N, H, dv]; slot_ids
     [N] int32 (negative: padding row) or None for slot i = i.  Returns out [N, H, dv]."""
-    code = _code(q.dtype, "q")
-    ldq = _rows(q, "q", None, q.dtype, None)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and v must be [N, H, d]")
-    N, H, dk = q.shape
-    dv, dev = v.shape[2], q.device
-    ldk = _rows(k, "k", (N, H, dk), q.dtype, dev)
-    ldv = _rows(v, "v", (N, H, dv), q.dtype, dev)
+    dev = _cuda(q, "q")
+    dt = q.dtype
+    code = _code(dt, "q")
+    N, H, dk = _dims(q, "q", 3)
+    dv = _dims(v, "v", 3)[2]
+    ldq = _rows(q, "q", (N, H, dk), H * dk, dt, dev)
+    ldk = _rows(k, "k", (N, H, dk), H * dk, dt, dev)
+    ldv = _rows(v, "v", (N, H, dv), H * dv, dt, dev)
+    P = _dims(state_pool, "state_pool", 4)[0]
     new = []
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
+        out = q.new_empty((N, H, dv))
         new.append(out)
     _call("kda_decay_decode", dev, stream, new, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
           _dense(log_decay, "log_decay", (H,), torch.float32, dev),
-          _dense(state_pool, "state_pool", (-1, H, dk, dv), torch.float32, dev), state_pool.shape[0],
-          _dense(slot_ids, "slot_ids", (N,), torch.int32, dev), _dense(out, "out", (N, H, dv), q.dtype, dev), N, H, dk,
+          _dense(state_pool, "state_pool", (P, H, dk, dv), torch.float32, dev), P,
+          _dense(slot_ids, "slot_ids", (N,), torch.int32, dev), _dense(out, "out", (N, H, dv), dt, dev), N, H, dk,
           dv, code, scale, _status(status, dev))
     return out
 
@@ -213,24 +231,24 @@ def paged_append(k, v, k_cache, v_cache, page_table, start_pos, cu_seqlens=None,
     """Writes new tokens' k and v [T, Hkv, d] into the pages [P, Hkv, page_size, d]
     of a cache: token t of sequence i goes to position start_pos[i] + t -
     cu_seqlens[i] (cu_seqlens None: one token per sequence)."""
-    code = _code(k.dtype, "k")
-    ldk = _rows(k, "k", None, k.dtype, None)
-    if k.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("k must be [T, Hkv, d] and k_cache [P, Hkv, page_size, d]")
-    T, H, d = k.shape
-    dev = k.device
-    ldv = _rows(v, "v", (T, H, d), k.dtype, dev)
-    kp = _dense(k_cache, "k_cache", (-1, H, -1, d), k.dtype, dev)
-    vp = _dense(v_cache, "v_cache", k_cache.shape, k.dtype, dev)
-    tp = _dense(page_table, "page_table", (-1, -1), torch.int32, dev)
-    N = page_table.shape[0]
-    _call("kda_paged_append", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, k_cache.shape[0],
-          k_cache.shape[2], tp, page_table.shape[1], _dense(start_pos, "start_pos", (N,), torch.int32, dev),
+    dev = _cuda(k, "k")
+    dt = k.dtype
+    code = _code(dt, "k")
+    T, H, d = _dims(k, "k", 3)
+    ldk = _rows(k, "k", (T, H, d), H * d, dt, dev)
+    ldv = _rows(v, "v", (T, H, d), H * d, dt, dev)
+    P, _, ps, _ = _dims(k_cache, "k_cache", 4)
+    kp = _dense(k_cache, "k_cache", (P, H, ps, d), dt, dev)
+    vp = _dense(v_cache, "v_cache", (P, H, ps, d), dt, dev)
+    N, cols = _dims(page_table, "page_table", 2)
+    tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
+    _call("kda_paged_append", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, P, ps, tp, cols, _dense(start_pos, "start_pos", (N,), torch.int32, dev),
           _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, d, code, _status(status, dev))
 
 
-def paged_decode_workspace_size(num_seqs, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
-    return int(_fn("kda_paged_decode_workspace_size")(num_seqs, Hq, Hkv, d, _code(dtype, "dtype")))
+def paged_decode_workspace_size(num_seqs, max_tokens, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of paged_decode for tables of max_tokens = max_pages * page_size tokens."""
+    return int(_fn("kda_paged_decode_workspace_size")(num_seqs, max_tokens, Hq, Hkv, d, _code(dtype, "dtype")))
 
 
 def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None, lse=None, return_lse=False,
@@ -239,30 +257,30 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
     its paged cache.  q [N, Hq, d]; caches [P, Hkv, page_size, d]; page_table
     [N, max_pages] int32; seq_lens [N] int32; scale defaults to d^-1/2.  Returns
     out [N, Hq, d], or (out, lse [N, Hq] f32) with return_lse."""
-    code = _code(q.dtype, "q")
-    ldq = _rows(q, "q", None, q.dtype, None)
-    if q.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("q must be [N, Hq, d] and k_cache [P, Hkv, page_size, d]")
-    N, Hq, d = q.shape
-    dev = q.device
-    kp = _dense(k_cache, "k_cache", (-1, -1, -1, d), q.dtype, dev)
-    vp = _dense(v_cache, "v_cache", k_cache.shape, q.dtype, dev)
-    P, Hkv, ps, _ = k_cache.shape
-    tp = _dense(page_table, "page_table", (N, -1), torch.int32, dev)
+    dev = _cuda(q, "q")
+    dt = q.dtype
+    code = _code(dt, "q")
+    N, Hq, d = _dims(q, "q", 3)
+    ldq = _rows(q, "q", (N, Hq, d), Hq * d, dt, dev)
+    P, Hkv, ps, _ = _dims(k_cache, "k_cache", 4)
+    kp = _dense(k_cache, "k_cache", (P, Hkv, ps, d), dt, dev)
+    vp = _dense(v_cache, "v_cache", (P, Hkv, ps, d), dt, dev)
+    cols = _dims(page_table, "page_table", 2)[1]
+    tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
     new = []
     if out is None:
-        out = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+        out = q.new_empty((N, Hq, d))
         new.append(out)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((N, Hq), dtype=torch.float32)
         new.append(lse)
     if workspace is None:
-        workspace = torch.empty(_fn("kda_paged_decode_workspace_size")(N, Hq, Hkv, d, code), dtype=torch.uint8,
-                                device=dev)
+        workspace = q.new_empty(_fn("kda_paged_decode_workspace_size")(N, cols * ps, Hq, Hkv, d, code), dtype=torch.uint8)
         new.append(workspace)
-    _call("kda_paged_decode", dev, stream, new, q.data_ptr(), ldq, kp, vp, P, ps, tp, page_table.shape[1],
+    size = _dims(workspace, "workspace", 1)[0]
+    _call("kda_paged_decode", dev, stream, new, q.data_ptr(), ldq, kp, vp, P, ps, tp, cols,
           _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
-          d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), q.dtype, dev),
-          _dense(lse, "lse", (N, Hq), torch.float32, dev), _dense(workspace, "workspace", (-1,), torch.uint8, dev),
-          workspace.numel(), _status(status, dev))
+          d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),
+          _dense(lse, "lse", (N, Hq), torch.float32, dev), _dense(workspace, "workspace", (size,), torch.uint8, dev),
+          size, _status(status, dev))
     return (out, lse) if return_lse else out

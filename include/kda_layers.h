@@ -129,8 +129,10 @@ kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t
                               const int32_t *cu_seqlens, int num_seqs, int64_t total_tokens, int Hkv,
                               int d, kda_dtype_t dtype, uint32_t *status, kda_stream_t stream);
 
-/* Workspace of kda_paged_decode (its partial results). */
-size_t kda_paged_decode_workspace_size(int num_seqs, int Hq, int Hkv, int d, kda_dtype_t dtype);
+/* Workspace of kda_paged_decode (its partial results) for sequences of up to
+ * max_tokens = max_pages page_size tokens. */
+size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq, int Hkv, int d,
+                                       kda_dtype_t dtype);
 
 /*
  * kda_paged_decode -- softmax attention of one token per sequence over the

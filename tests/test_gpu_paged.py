@@ -150,7 +150,7 @@ def test_row_stride_workspace_stream_and_repeats():
     qs, = ref.fused_rows([q], dev)
     c = [t.to(dev) for t in (kc, vc, table)]
     n = torch.tensor(lens, dtype=torch.int32, device=dev)
-    ws = torch.full((paged_decode_workspace_size(4, 8, 2, 128),), 255, dtype=torch.uint8, device=dev)
+    ws = torch.full((paged_decode_workspace_size(4, table.shape[1] * 64, 8, 2, 128),), 255, dtype=torch.uint8, device=dev)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     o2, l2 = paged_decode(qs, *c, n, return_lse=True, workspace=ws, stream=s)
