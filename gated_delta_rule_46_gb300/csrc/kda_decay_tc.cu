@@ -1,5 +1,5 @@
 // kda_decay_tc.cu -- the chunked form of linear attention with one decay per
-// head (bf16, dk = dv = 128) on the tensor cores.
+// head (bf16, dk = dv = 128 or 64) on the tensor cores.
 //
 // Per chain (sequence, head), in chunks of C = 64 tokens with n of them real,
 // start state S and lambda = exp(log_decay):
@@ -37,25 +37,35 @@ namespace {
 
 using namespace tc;
 
-constexpr int C = 64, D = 128;
+constexpr int C = 64;
 constexpr int kThreads = 640;
 constexpr long long kWaitBudget = 2000000000LL;   // cycles (about one second)
 constexpr int kWaitTries = 1 << 24;               // attempts of a wait, at least some 20 cycles each
 constexpr long long kDrain = 20000000LL;
 
 // ---- shared memory, bytes from a 1024-aligned base.  Tiles have 128-byte rows
-// with the 128-byte swizzle; a 128-channel row is two tiles (halves).
+// with the 128-byte swizzle; a row of 128 channels is two tiles (halves).
 constexpr uint32_t kTile = C * 128;                       // 64 rows x 64 channels
-constexpr uint32_t R_STAGE = 0;                           // per stage: [Q0 K0 Q1 K1 V0 V1]
-constexpr uint32_t kStage = 6 * kTile, O_Q = 0, O_K = kTile, O_V = 4 * kTile, kHalf = 2 * kTile;
-constexpr int NS = 3;                                     // stages
-constexpr uint32_t R_T = NS * kStage;                     // three terms of the decayed keys, [token][channel]
-constexpr uint32_t R_P = R_T + 6 * kTile;                 // P [i][j], two buffers
-constexpr uint32_t R_O = R_P + 2 * kTile;                 // output staging [token][dv]
-constexpr uint32_t R_PW = R_O + 2 * kTile;                // lambda^1 .. lambda^64, of two items in turn
-constexpr uint32_t R_KW = R_PW + 2 * C * 4;                // lambda^0 .. lambda^63, one copy for each key warp
-constexpr uint32_t kSmem = R_KW + 4 * C * 4 + 1024;
-static_assert(kSmem <= 232448 - 256, "shared memory");
+template <int D>
+struct Lay {
+    static constexpr int HV = D / 64;                     // halves
+    static constexpr int NS = D == 128 ? 3 : 6;           // stages of loads
+    static constexpr uint32_t half = 2 * kTile;           // from Q0 to Q1, from K0 to K1
+    static constexpr uint32_t q = 0, k = kTile, v = HV * half;            // in a stage: [Q0 K0 (Q1 K1) V0 (V1)]
+    static constexpr uint32_t stage = 3 * HV * kTile;
+    static constexpr uint32_t T = NS * stage;             // three terms of the decayed keys, [token][channel]
+    static constexpr uint32_t term = HV * kTile;
+    static constexpr uint32_t P = T + 3 * term;           // P [i][j], two buffers
+    static constexpr uint32_t O = P + 2 * kTile;          // output staging [token][dv]
+    static constexpr uint32_t PW = O + HV * kTile;        // lambda^1 .. lambda^64, of two items in turn
+    static constexpr uint32_t KW = PW + 2 * C * 4;        // lambda^0 .. lambda^63, one copy for each key warp
+    static constexpr uint32_t bytes = KW + 4 * C * 4 + 1024;
+    static_assert(bytes <= 232448 - 256, "shared memory");
+    // with 64 channels the MMAs' upper 64 rows (M = 128) are whatever lies one tile on: rows that no one reads
+    // barriers
+    enum Bar { LD, FREE = LD + NS, QK = FREE + NS, PREADY = QK + 2, OD = PREADY + 2, OFREE = OD + 2, QS = OFREE + 2, SREADY,
+               TF, DSH = TF + 2 * NS, DS = DSH + 2, DSFREE, NBAR };
+};
 
 // ---- tensor memory columns (512)
 constexpr uint32_t TM_P = 0;                                                  // Q K^T, lanes 0-63
@@ -64,8 +74,6 @@ __device__ __forceinline__ uint32_t tm_qs(int b) { return 128 + b * 128; }    //
 __device__ __forceinline__ uint32_t tm_pv(int b) { return 192 + b * 128; }    // V^T P^T
 constexpr uint32_t TM_DS = 384;                                               // what the chunk adds to S^T
 
-enum Bar { LD, FREE = LD + NS, QK = FREE + NS, PREADY = QK + 2, OD = PREADY + 2, OFREE = OD + 2, QS = OFREE + 2, SREADY,
-           TF, DSH = TF + 2 * NS, DS = DSH + 2, DSFREE, NBAR };
 
 struct Params {
     const float *log_decay;
@@ -109,7 +117,7 @@ __device__ __forceinline__ int segments(const Params &p, int len) {
 }
 
 // Walks this CTA's items in order; every role walks its own copy.
-template <bool OUT>
+template <int D, bool OUT>
 struct Walk {
     unsigned it = 0;
     __device__ __noinline__ bool next(const Params &p, Item &x, bool tell) {
@@ -171,9 +179,9 @@ struct Walk {
 };
 
 // Chunks of all of a CTA's items.
-template <bool OUT>
+template <int D, bool OUT>
 __device__ __noinline__ int chunks_of(const Params &p, bool tell) {
-    Walk<OUT> walk;
+    Walk<D, OUT> walk;
     Item x;
     int total = 0;
     while (walk.next(p, x, tell)) total += (x.t1 - x.t0 + C - 1) / C;
@@ -239,32 +247,40 @@ __device__ __forceinline__ void split3(const uint4 &k, float w, uint4 &t1, uint4
     cut(t3);
 }
 
-// sum_{s <= i} P_is v_sj for token i and channel j of the chunk at token t, v
-// from global memory.
-__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int head, int i, int j) {
+// sum_{s <= i} P_is v_sj for token i of the chunk at token t and the channel that
+// is element `at` of a row, v from global memory.
+__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int at, int i) {
     float y = 0.f;
     if (t + i >= t1) return y;
 #pragma unroll 1
     for (int s = 0; s <= i; ++s)
         y = fmaf(to_f32(*reinterpret_cast<const __nv_bfloat16 *>(sp + swz(i, s >> 3) + (s & 7) * 2)),
-                 to_f32(p.v[(int64_t)(t + s) * p.ldv + (int64_t)head * D + j]), y);
+                 to_f32(p.v[(int64_t)(t + s) * p.ldv + at]), y);
     return y;
 }
 
-template <bool OUT>
+template <int D, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Params p) {
+    using L = Lay<D>;
+    constexpr int NS = L::NS, HV = L::HV;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar[NBAR];
+    __shared__ uint64_t bar[L::NBAR];
     __shared__ uint32_t s_tmem, s_abort;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(sm);
 
     if (threadIdx.x == 0) {
-        const uint8_t counts[NBAR] = {1, 1, 1, OUT ? 2 : 1, OUT ? 2 : 1, OUT ? 2 : 1, 1, 1, 2, 2, 1, 1, 4, 4, 1, 8, 4, 4, 4, 4, 4, 4, 1, 1, 1, 8};
-        for (int i = 0; i < NBAR; ++i) ptx::mbar_init(&bar[i], counts[i]);
+        for (int i = 0; i < L::NBAR; ++i) {
+            int n = 1;
+            if (i >= L::FREE && i < L::QK) n = OUT ? 2 : 1;             // the two issuers
+            if (i >= L::PREADY && i < L::OD) n = 2;                     // warps 0, 1
+            if ((i >= L::OFREE && i < L::QS) || (i >= L::TF && i < L::DSH)) n = 4;   // the output's, the keys' warps
+            if (i == L::SREADY || i == L::DSFREE) n = 4 * HV;           // the state's warps
+            ptx::mbar_init(&bar[i], n);
+        }
         ptx::fence_mbar_init();
         s_abort = 0;
         if (OUT) ptx::prefetch_tensormap(&mq);
@@ -278,63 +294,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (OUT)                           // P's masked quarter stays zero
         for (int i = threadIdx.x; i < 2 * (int)kTile / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(sm + R_P)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm + L::P)[i] = make_uint4(0, 0, 0, 0);
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
     if (OUT) ptx::pdl_wait();          // the segments' start states
     bool ok = true;
-    Walk<OUT> walk;
+    Walk<D, OUT> walk;
     Item x;
 
     if (warp == 2) {                                              // ---- loads, and the state's product
         // one thread does whichever of the two can go ahead
-        const int total = chunks_of<OUT>(p, true);
+        const int total = chunks_of<D, OUT>(p, true);
         if (ptx::elect_one()) {
-            const uint32_t id = ptx::idesc_bf16_f32(128, 128) | kAMn | kBMn;
-            const uint64_t dt = sdesc_mn_sw128(base + R_T, kTile);
+            const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
+            const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
             int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
             int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
             int t = 0, t1 = 0, col0 = 0;
             long long since = clock64();
             while (dc < total) {
                 bool did = false;
-                if (lc < total && (lp == 0 || ptx::mbar_try_wait(&bar[FREE + ls], (lp - 1) & 1))) {
+                if (lc < total && (lp == 0 || ptx::mbar_try_wait(&bar[L::FREE + ls], (lp - 1) & 1))) {
                     while (t >= t1) {
                         walk.next(p, x, false);
                         t = x.t0;
                         t1 = x.t1;
                         col0 = x.head * D;
                     }
-                    uint64_t *full = &bar[LD + ls];
-                    uint8_t *st = sm + R_STAGE + ls * kStage;
-                    ptx::mbar_arrive_expect_tx(full, (OUT ? 6 : 4) * kTile);
+                    uint64_t *full = &bar[L::LD + ls];
+                    uint8_t *st = sm + ls * L::stage;
+                    ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < HV; ++h) {
                         const int col = col0 + h * 64;
-                        ptx::tma_load_2d(st + O_K + h * kHalf, &mk, col, t, full);
-                        if (OUT) ptx::tma_load_2d(st + O_Q + h * kHalf, &mq, col, t, full);
-                        ptx::tma_load_2d(st + O_V + h * kTile, &mv, col, t, full);
+                        ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, t, full);
+                        if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, t, full);
+                        ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, t, full);
                     }
                     t += C;
                     ++lc;
                     if (++ls == NS) { ls = 0; ++lp; }
                     did = true;
                 }
-                if (ptx::mbar_try_wait(&bar[TF + 2 * ds + half], dp & 1) &&
-                    (half == 1 || dc == 0 || ptx::mbar_try_wait(&bar[DSFREE], (dc - 1) & 1))) {
+                if (ptx::mbar_try_wait(&bar[L::TF + 2 * ds + half], dp & 1) &&
+                    (half == 1 || dc == 0 || ptx::mbar_try_wait(&bar[L::DSFREE], (dc - 1) & 1))) {
                     ptx::tc_fence_after_sync();
                     const uint64_t a = dt + half * (4096 >> 4);
-                    const uint64_t v = sdesc_mn_sw128(base + R_STAGE + ds * kStage + O_V, kTile) + half * (4096 >> 4);
+                    const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
 #pragma unroll 2
                     for (int e = 0; e < 6; ++e)
-                        ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * 2 * kTile + (e & 1) * 2048) / 16,
+                        ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
                                          id, half > 0 || e > 0);
-                    ptx::mma_commit(&bar[DSH + half]);
+                    ptx::mma_commit(&bar[L::DSH + half]);
                     if (half == 1) {
-                        ptx::mma_commit(&bar[DS]);
-                        ptx::mma_commit(&bar[FREE + ds]);
+                        ptx::mma_commit(&bar[L::DS]);
+                        ptx::mma_commit(&bar[L::FREE + ds]);
                         ++dc;
                         if (++ds == NS) { ds = 0; ++dp; }
                     }
@@ -356,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
                     const int b = c & 1;
                     // the output products of two chunks ago have read this buffer, and so has their output if it had to
-                    ok = warp_wait(&bar[QK + b], c >> 1) && (c < 2 || warp_wait(&bar[OFREE + b], (c >> 1) - 1));
+                    ok = warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
-                    uint8_t *sp = sm + R_P + b * kTile;
+                    uint8_t *sp = sm + L::P + b * kTile;
                     // (columns 32-63 of rows 0-31 are never written: zero from the start)
 #pragma unroll 1
                     for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 16) {
@@ -377,29 +393,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ptx::fence_async_smem();
                     ptx::tc_fence_before_sync();
-                    warp_arrive(&bar[PREADY + b]);
+                    warp_arrive(&bar[L::PREADY + b]);
                 }
             }
         }
     } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
-        const int total = OUT ? chunks_of<OUT>(p, false) : 0;
+        const int total = OUT ? chunks_of<D, OUT>(p, false) : 0;
         if (OUT && ptx::elect_one()) {
             const uint32_t id = ptx::idesc_bf16_f32(128, 64);
             int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
             for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
                 const int b = c & 1, phase = (c >> 1) & 1;
-                const uint32_t st = base + R_STAGE + s * kStage;
+                const uint32_t st = base + s * L::stage;
                 if (c >= 0) {
-                    if (!wait_on(&bar[SREADY], c & 1) ||
-                        (c >= 2 && !wait_on(&bar[OFREE + b], phase ^ 1))) { ok = false; break; }
+                    if (!wait_on(&bar[L::SREADY], c & 1) ||
+                        (c >= 2 && !wait_on(&bar[L::OFREE + b], phase ^ 1))) { ok = false; break; }
                     ptx::tc_fence_after_sync();
-                    const uint64_t q = ptx::sdesc_kmajor_sw128(st + O_Q);
+                    const uint64_t q = ptx::sdesc_kmajor_sw128(st + L::q);
 #pragma unroll 2
-                    for (int k = 0; k < 8; ++k)
-                        ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
+                    for (int k = 0; k < D / 16; ++k)
+                        ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * L::half + (k & 3) * 32) >> 4),
                                          id, k > 0);
-                    ptx::mma_commit(&bar[QS]);
-                    if (!wait_on(&bar[PREADY + b], phase)) { ok = false; break; }
+                    ptx::mma_commit(&bar[L::QS]);
+                    if (!wait_on(&bar[L::PREADY + b], phase)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
                 }
                 // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
@@ -407,30 +423,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool todo = c + 1 < total;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
-                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[LD + ns], np & 1))) {
+                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[L::LD + ns], np & 1))) {
                         todo = false;
-                        if (!wait_on(&bar[LD + ns], np)) { ok = false; break; }
+                        if (!wait_on(&bar[L::LD + ns], np)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
-                        const uint32_t sn = base + R_STAGE + ns * kStage;
+                        const uint32_t sn = base + ns * L::stage;
                         // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
-                        const uint64_t q = ptx::sdesc_kmajor_sw128(sn + O_Q), kd = ptx::sdesc_kmajor_sw128(sn + O_K);
+                        const uint64_t q = ptx::sdesc_kmajor_sw128(sn + L::q), kd = ptx::sdesc_kmajor_sw128(sn + L::k);
 #pragma unroll 2
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
                             ptx::mma_bf16_ss(tmem + TM_P, q + at, kd + at, id, k > 0);
                         }
-                        ptx::mma_commit(&bar[QK + (b ^ 1)]);
+                        ptx::mma_commit(&bar[L::QK + (b ^ 1)]);
                     }
                     if (c < 0 || pass == 1) continue;
-                    if (!wait_on(&bar[TF + 2 * s], sp) ||                  // (V's tail is clean)
-                        !wait_on(&bar[TF + 2 * s + 1], sp)) { ok = false; break; }
+                    if (!wait_on(&bar[L::TF + 2 * s], sp) ||                  // (V's tail is clean)
+                        !wait_on(&bar[L::TF + 2 * s + 1], sp)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
-                    const uint64_t a = sdesc_mn_sw128(st + O_V, kTile), pb = ptx::sdesc_kmajor_sw128(base + R_P + b * kTile);
+                    const uint64_t a = sdesc_mn_sw128(st + L::v, kTile), pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
 #pragma unroll 2
                     for (int k = 0; k < 4; ++k)
                         ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
-                    ptx::mma_commit(&bar[OD + b]);
-                    ptx::mma_commit(&bar[FREE + s]);
+                    ptx::mma_commit(&bar[L::OD + b]);
+                    ptx::mma_commit(&bar[L::FREE + s]);
                 }
                 s = ns;
                 sp = np;
@@ -440,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4 && warp < 8) {                           // ---- the output
         if (OUT) {
             const int tid = threadIdx.x - 128, q = warp & 3;
-            float *pw = reinterpret_cast<float *>(sm + R_PW);
-            uint8_t *so = sm + R_O;
+            float *pw = reinterpret_cast<float *>(sm + L::PW);
+            uint8_t *so = sm + L::O;
             int c = 0, item = 0;
             while (ok && walk.next(p, x, false)) {
                 const int t1 = x.t1, head = x.head;
@@ -451,16 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int t = x.t0; t < t1; t += C, ++c) {
                     const int b = c & 1;
-                    const bool good = wait_on(&bar[OD + b], (c >> 1) & 1);
+                    const bool good = wait_on(&bar[L::OD + b], (c >> 1) & 1);
                     if (tid == 0) ptx::bulk_wait_read();             // the staging tile's last store
                     ok = !ptx::bar_any(1, 128, !good);        // all 128 threads go on or give up alike
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
-                    const uint8_t *sp = sm + R_P + b * kTile;
+                    const uint8_t *sp = sm + L::P + b * kTile;
                     const float *pwo = pw + (item & 1) * C;
                     // 16 value channels x 32 tokens at a time, as 8 x 8 tiles that are stored transposed
 #pragma unroll 1
-                    for (int part = 0; part < 4; ++part) {
+                    for (int part = q * 32 < D ? 0 : 4; part < 4; ++part) {    // (64 channels: two warps)
                         const int j0 = q * 32 + (part & 1) * 16, i0 = (part >> 1) * 32;
                         const uint32_t at = tmem + ((uint32_t)j0 << 16) + i0;
                         float a[16], o[16];
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (probe != 0.f)
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                o[e] = real_pairs(p, sp, t, t1, head, ic + (e >> 2) * 8 + (e & 1), j0 + (lane >> 2) + ((e >> 1) & 1) * 8);
+                                o[e] = real_pairs(p, sp, t, t1, head * D + j0 + (lane >> 2) + ((e >> 1) & 1) * 8, ic + (e >> 2) * 8 + (e & 1));
                         uint32_t u[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -492,19 +508,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::stmatrix4_trans(to + swz(r + 16, ch), u[4], u[5], u[6], u[7]);
                     }
                     ptx::tc_fence_before_sync();
-                    warp_arrive(&bar[OFREE + b]);
+                    warp_arrive(&bar[L::OFREE + b]);
                     ptx::fence_async_smem();
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     const int on = min(t1 - t, C);
                     if (on == C) {
                         if (tid == 0) {
                             ptx::tma_store_2d(&mo, head * D, t, so);
-                            ptx::tma_store_2d(&mo, head * D + 64, t, so + kTile);
+                            if (HV == 2) ptx::tma_store_2d(&mo, head * D + 64, t, so + kTile);
                             ptx::bulk_commit();
                         }
                     } else {
-                        for (int i = tid; i < on * 16; i += 128) {
-                            const int r = i >> 4, ch = i & 15;
+                        for (int i = tid; i < on * (D / 8); i += 128) {
+                            const int r = i / (D / 8), ch = i % (D / 8);
                             *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.H + head) * D + ch * 8) =
                                 *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
                         }
@@ -515,9 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tid == 0) ptx::bulk_wait_all();
         }
     } else if (warp >= 8 && warp < 12) {                          // ---- the decayed keys in three terms
-        const int tid = threadIdx.x - 256, r0 = tid >> 4, ch = tid & 15;     // rows r0, r0 + 8, ...; 16-byte column
+        constexpr int RP = 128 / (D / 8), NR = 32 / RP;                       // rows at a time; times per half chunk
+        const int tid = threadIdx.x - 256, r0 = tid / (D / 8), ch = tid % (D / 8);   // rows r0, r0 + RP, ...; 16-byte column
         const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
-        float *kw = reinterpret_cast<float *>(sm + R_KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
+        float *kw = reinterpret_cast<float *>(sm + L::KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
         int c = 0, s = 0, round = 0;
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
@@ -527,45 +544,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
                 const int n = min(t1 - t, C);
-                ok = warp_wait(&bar[LD + s], round);
+                ok = warp_wait(&bar[L::LD + s], round);
                 if (!ok) break;
-                uint8_t *st = sm + R_STAGE + s * kStage;
-                uint64_t *full = &bar[TF + 2 * s];
+                uint8_t *st = sm + s * L::stage;
+                uint64_t *full = &bar[L::TF + 2 * s];
                 if (++s == NS) { s = 0; ++round; }
-                const float *w = kw + max(n - 1 - r0, 0);         // row r0 + 8 i: lambda^{n - 1 - r0 - 8 i}
-                const int most = max(n - 1 - r0, 0) >> 3;
-                const uint8_t *kp = st + O_K + half * kHalf + at0;
-                uint8_t *dst = sm + R_T + half * kTile + at0;
+                const float *w = kw + max(n - 1 - r0, 0);         // row r0 + RP i: lambda^{n - 1 - r0 - RP i}
+                const int most = max(n - 1 - r0, 0) / RP;
+                const uint8_t *kp = st + L::k + half * L::half + at0;
+                uint8_t *dst = sm + L::T + half * kTile + at0;
                 if (n < C)                                        // rows of the next sequence
-                    for (int i = 0; i < 8; ++i)
-                        if (r0 + 8 * i >= n)
-                            *reinterpret_cast<uint4 *>(st + O_V + half * kTile + at0 + i * 1024) = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 2 * NR; ++i)
+                        if (r0 + RP * i >= n)
+                            *reinterpret_cast<uint4 *>(st + L::v + half * kTile + at0 + i * RP * 128) = make_uint4(0, 0, 0, 0);
                 // The loads of the next 32 tokens go before the stores of these: beside the MMAs' own reads a load
                 // from shared memory takes some 200 cycles.
-                uint4 kn[4];
+                uint4 kn[NR];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + i * 1024);
+                for (int i = 0; i < NR; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + i * RP * 128);
 #pragma unroll 1
                 for (int th = 0; th < 2; ++th) {                  // 32 tokens at a time
-                    uint4 k[4];
-                    float wi[4];
+                    uint4 k[NR];
+                    float wi[NR];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < NR; ++i) {
                         k[i] = kn[i];
-                        wi[i] = w[-8 * min(th * 4 + i, most)];
-                        if (r0 + 8 * (th * 4 + i) >= n) k[i] = make_uint4(0, 0, 0, 0);
+                        wi[i] = w[-RP * min(th * NR + i, most)];
+                        if (r0 + RP * (th * NR + i) >= n) k[i] = make_uint4(0, 0, 0, 0);
                     }
                     if (th == 0)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + (i + 4) * 1024);
-                    if (c > 0 && !(ok = warp_wait(&bar[DSH + th], c - 1))) break;
+                        for (int i = 0; i < NR; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + (i + NR) * RP * 128);
+                    if (c > 0 && !(ok = warp_wait(&bar[L::DSH + th], c - 1))) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < NR; ++i) {
                         uint4 t1, t2, t3;
                         split3(k[i], wi[i], t1, t2, t3);
-                        *reinterpret_cast<uint4 *>(dst + i * 1024) = t1;
-                        *reinterpret_cast<uint4 *>(dst + i * 1024 + 2 * kTile) = t2;
-                        *reinterpret_cast<uint4 *>(dst + i * 1024 + 4 * kTile) = t3;
+                        *reinterpret_cast<uint4 *>(dst + i * RP * 128) = t1;
+                        *reinterpret_cast<uint4 *>(dst + i * RP * 128 + L::term) = t2;
+                        *reinterpret_cast<uint4 *>(dst + i * RP * 128 + 2 * L::term) = t3;
                     }
                     dst += 4096;
                     ptx::fence_async_smem();
@@ -574,17 +591,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
         }
-    } else if (warp >= 12) {                                      // ---- the state: lane = value channel
-        const int q = warp & 3, k0 = ((warp - 12) >> 2) * 64;         // key channels k0 .. k0 + 63
+    } else if (warp >= 12 && (warp & 3) * 32 < D) {               // ---- the state: lane = value channel
+        constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
+        const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;
         const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
         const uint32_t at = tmem + ((uint32_t)q << 21);
         int c = 0;
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
             const float *from = x.from;
-            float s[64];
+            float s[KC];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) s[e] = from ? from[mine + e * D] : 0.f;
+            for (int e = 0; e < KC; ++e) s[e] = from ? from[mine + e * D] : 0.f;
             auto copy_out = [&](int e) {       // 16 channels as bf16 pairs
                 uint32_t u[8];
 #pragma unroll
@@ -593,23 +611,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int t0 = x.t0, t1 = x.t1;
             if (OUT && t1 > t0) {
-                if (c > 0) ok = warp_wait(&bar[QS], c - 1);
+                if (c > 0) ok = warp_wait(&bar[L::QS], c - 1);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
-                for (int e = 0; e < 64; e += 16) copy_out(e);
+                for (int e = 0; e < KC; e += 16) copy_out(e);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
-                warp_arrive(&bar[SREADY]);
+                warp_arrive(&bar[L::SREADY]);
             }
             for (int t = t0; t < t1; t += C, ++c) {
                 const bool more = OUT && t + C < t1;
                 const float f = exp2f(l2 * (float)min(t1 - t, C));
-                ok = warp_wait(&bar[DS], c) && (!more || warp_wait(&bar[QS], c));
+                ok = warp_wait(&bar[L::DS], c) && (!more || warp_wait(&bar[L::QS], c));
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
-                for (int e = 0; e < 64; e += 16) {
+                for (int e = 0; e < KC; e += 16) {
                     float d[16];
                     ptx::tmem_ld16(at + TM_DS + k0 + e, d);
                     ptx::tmem_ld_wait();
@@ -619,13 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (more) ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
-                warp_arrive(&bar[DSFREE]);
-                if (more) warp_arrive(&bar[SREADY]);
+                warp_arrive(&bar[L::DSFREE]);
+                if (more) warp_arrive(&bar[L::SREADY]);
             }
             if (!ok) break;
             if (x.to)
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x.to[mine + e * D] = s[e];
+                for (int e = 0; e < KC; ++e) x.to[mine + e * D] = s[e];
         }
     }
     if (!ok) {
@@ -648,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Start states of the segments: S(0) = initial state, S(g + 1) = lambda^{seg_len}
 // S(g) + b(g), in place over the b that the state pass left; one CTA column per
 // (sequence, head), one float4 per thread.
+template <int D>
 __global__ void __launch_bounds__(256) decay_segments_kernel(const Params p) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
@@ -695,7 +714,7 @@ int segment_tokens(int64_t total, int N, int H, int sms) {
 
 }  // namespace
 
-size_t decay_prefill_tc_workspace(int64_t total, int N, int H) {
+size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D) {
     const int len = segment_tokens(total, N, H, sm_count());
     size_t bytes = kOrderAt + sizeof(int32_t) * (size_t)N;
     bytes = (bytes + 1023) & ~size_t(1023);
@@ -703,7 +722,9 @@ size_t decay_prefill_tc_workspace(int64_t total, int N, int H) {
     return bytes;
 }
 
-cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_t workspace_bytes, cudaStream_t st) {
+template <int D>
+static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t workspace_bytes, cudaStream_t st) {
+    constexpr uint32_t kSmem = Lay<D>::bytes;
     CUtensorMap mq, mk, mv, mo;
     const uint64_t T = (uint64_t)d.total, cols = (uint64_t)d.H * D;
     if (!make_map_2d(&mq, d.q, true, T, cols, d.ldq * 2, C) || !make_map_2d(&mk, d.k, true, T, cols, d.ldk * 2, C) ||
@@ -712,12 +733,12 @@ cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_
     const int sms = sm_count();
     Params p{d.log_decay, d.cu_seqlens, d.num_seqs, d.H, d.total, d.scale, d.init, d.fin,
              static_cast<__nv_bfloat16 *>(d.out), static_cast<const __nv_bfloat16 *>(d.v), d.ldv, nullptr, d.status, 0, nullptr, 0};
-    cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decay_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H);
+    const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -735,15 +756,15 @@ cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_
         const int64_t items = (int64_t)p.seg_cap * d.H;
         cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
         cfg.numAttrs = 0;
-        if ((e = cudaLaunchKernelEx(&cfg, decay_chunk_kernel<false>, mq, mk, mv, mo, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, false>, mq, mk, mv, mo, p)) != cudaSuccess) return e;
         cudaLaunchConfig_t c2 = cfg;
         c2.gridDim = dim3(D * D / 1024, (unsigned)chains);
         c2.blockDim = dim3(256);
         c2.dynamicSmemBytes = 0;
         c2.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&c2, decay_segments_kernel, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&c2, decay_segments_kernel<D>, p)) != cudaSuccess) return e;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<true>, mq, mk, mv, mo, p);
+        return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, true>, mq, mk, mv, mo, p);
     }
     if (room && chains > sms && d.num_seqs > 1) {
         int32_t *order = reinterpret_cast<int32_t *>(ws + kOrderAt);
@@ -754,7 +775,11 @@ cudaError_t launch_decay_prefill_tc(const DecayParams &d, void *workspace, size_
         cfg.numAttrs = 1;
     }
     cfg.gridDim = dim3((unsigned)(chains < sms ? chains : sms));
-    return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<true>, mq, mk, mv, mo, p);
+    return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, true>, mq, mk, mv, mo, p);
+}
+
+cudaError_t launch_decay_prefill_tc(const DecayParams &d, int D, void *workspace, size_t workspace_bytes, cudaStream_t st) {
+    return D == 64 ? launch_tc<64>(d, workspace, workspace_bytes, st) : launch_tc<128>(d, workspace, workspace_bytes, st);
 }
 
 }  // namespace kda

@@ -55,10 +55,10 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,
                                         kda_dtype_t dtype) {
-    if (total_tokens <= 0 || total_tokens >= kMax31 || num_seqs <= 0 || H <= 0 || dtype != KDA_BF16 || dk != 128 ||
-        dv != 128)
+    if (total_tokens <= 0 || total_tokens >= kMax31 || num_seqs <= 0 || H <= 0 || dtype != KDA_BF16 || dk != dv ||
+        (dk != 128 && dk != 64))
         return 0;
-    return kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H);
+    return kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H, dk);
 }
 
 kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
@@ -82,9 +82,9 @@ kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_
     const kda::DecayParams p{q, k, v, ldq, ldk, ldv, log_decay, cu_seqlens, num_seqs, H, total_tokens, scale,
                              initial_state, final_state, out, status};
     // TMA copies start on 16-byte boundaries
-    if (dtype == KDA_BF16 && dk == 128 && dv == 128 && total_tokens > 0 && aligned(q, 16) && aligned(k, 16) &&
+    if (dtype == KDA_BF16 && dk == dv && dk >= 64 && total_tokens > 0 && aligned(q, 16) && aligned(k, 16) &&
         aligned(v, 16) && aligned(out, 16) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0)
-        return from_cuda(kda::launch_decay_prefill_tc(p, workspace, workspace_bytes,
+        return from_cuda(kda::launch_decay_prefill_tc(p, dk, workspace, workspace_bytes,
                                                       reinterpret_cast<cudaStream_t>(stream)));
     return from_cuda(kda::launch_decay_prefill_simt(p, dk, dv, dtype == KDA_BF16,
                                                     reinterpret_cast<cudaStream_t>(stream)));

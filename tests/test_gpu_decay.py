@@ -248,3 +248,20 @@ def test_refusals():
         decay_decode(d["q"], d["k"], d["v"], d["ld"], pool[:, :, :, :32])
     with pytest.raises(KDAError):
         decay_decode(d["q"], d["k"], d["v"], d["ld"], pool)             # 8 rows, 4 slots, no ids
+
+
+@pytest.mark.parametrize("d_", [64, 128])
+@pytest.mark.parametrize("lens,H", [([3000], 3), ([700, 0, 1800], 2), ([64 * 30 + 1], 1)])
+def test_segments_of_few_chains(d_, lens, H):
+    """bf16 chains cut into segments, with and without the workspace that this takes; slow decays."""
+    dev = need_gpu()
+    d = _inputs(lens, H, d_, d_, BF, seed=21)
+    d["ld"] = -torch.exp2(-9 - 3 * torch.rand(H, generator=torch.Generator().manual_seed(4)))
+    out, fin = _prefill(d, dev)
+    _check(d, out, fin)
+    one, last = _prefill(d, dev, workspace=torch.zeros(16, dtype=torch.uint8, device=dev))
+    _check(d, one, last)
+    state = d["init"].to(dev)                                     # the start state's buffer takes the end state
+    d["init"] = state
+    again, same = _prefill(d, dev, final_state=state)
+    assert same is state and torch.equal(again, out) and torch.equal(state, fin)
