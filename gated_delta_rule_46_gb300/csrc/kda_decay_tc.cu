@@ -23,7 +23,7 @@
 // its bf16 copy in TMEM, where the MMA takes it from.  mbarriers link them.
 #include <cuda.h>
 
-#include "kda_layers.cuh"
+#include "kda_decay.cuh"
 #include "kda_tc_util.cuh"
 #include "kda_tmap.cuh"
 #include "sm100_ptx.cuh"
@@ -76,10 +76,8 @@ constexpr uint32_t TM_DS = 384;                                               //
 
 
 struct Params {
+    DecaySegs g;
     const float *log_decay;
-    const int32_t *cu;
-    int N, H;
-    int64_t total;
     float scale;
     const float *init;          // initial states, or nullptr
     float *fin;                 // final states, or nullptr
@@ -87,10 +85,6 @@ struct Params {
     const __nv_bfloat16 *v;     // (the values again, for the rare path)
     int64_t ldv;
     const int32_t *order;       // longest-first order of the sequences, or nullptr
-    uint32_t *status;
-    int seg_len;                // 0: a chain is one item; else tokens per segment
-    float *seg;                 // [segment][H][D][D]
-    int seg_cap;                // segments that seg has room for (more only if the offsets overlap)
 };
 
 // One piece of a chain: tokens [t0, t1) of one head.
@@ -101,32 +95,17 @@ struct Item {
     float *to;                  // end state, nullptr for none
 };
 
-// Offsets are below 2^31 (the entry point sees to it), so token counts are int.
-__device__ __forceinline__ void bounds(const Params &p, int seq, int &bos, int &eos, bool tell) {
-    bos = p.cu[seq];
-    eos = p.cu[seq + 1];
-    if (bos < 0 || eos < bos || eos > p.total) {
-        if (tell) report_status(p.status, kDevBadSeqlens);
-        bos = eos = 0;
-    }
-}
-
-// Segments of a sequence; an empty one has one empty segment (its state is copied).
-__device__ __forceinline__ int segments(const Params &p, int len) {
-    return len > 0 ? (int)((unsigned)(len - 1) / (unsigned)p.seg_len) + 1 : 1;
-}
-
 // Walks this CTA's items in order; every role walks its own copy.
 template <int D, bool OUT>
 struct Walk {
     unsigned it = 0;
     __device__ __noinline__ bool next(const Params &p, Item &x, bool tell) {
         constexpr int64_t kState = (int64_t)D * D;
-        const unsigned H = (unsigned)p.H;
-        if (p.seg_len == 0) {
+        const unsigned H = (unsigned)p.g.H;
+        if (p.g.len == 0) {
             // rows of gridDim.x chains, dealt out forwards and backwards in turn: with the longest first, every
             // CTA gets about the same number of tokens
-            const unsigned chains = (unsigned)p.N * H, row = it * gridDim.x;
+            const unsigned chains = (unsigned)p.g.N * H, row = it * gridDim.x;
             if (row >= chains) return false;
             const unsigned i = row + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             ++it;
@@ -137,44 +116,26 @@ struct Walk {
             const unsigned k = i / H;
             const int seq = p.order ? p.order[k] : (int)k;
             x.head = (int)(i - k * H);
-            bounds(p, seq, x.t0, x.t1, tell);
+            seq_range(p.g, seq, x.t0, x.t1, tell);
             const int64_t at = ((int64_t)seq * H + x.head) * kState;
             if (p.init) x.from = p.init + at;
             if (p.fin) x.to = p.fin + at;
             return true;
         }
         // segments of all sequences in order, heads fastest; the state pass (OUT = false) skips each last one
-        unsigned i = it * gridDim.x + blockIdx.x;
+        const unsigned i = it * gridDim.x + blockIdx.x, seg = i / H;
         ++it;
-        const unsigned seg = i / H;
         x.head = (int)(i - seg * H);
-        int before = 0;                         // segments of the sequences before
-#pragma unroll 1
-        for (int n = 0; n < p.N; ++n) {
-            int bos, eos;
-            bounds(p, n, bos, eos, tell && it == 1);
-            const int segs = segments(p, eos - bos), g = (int)seg - before;
-            before += segs;
-            if (g >= segs) continue;
-            if (seg >= (unsigned)p.seg_cap) {
-                if (tell) report_status(p.status, kDevBadSeqlens);
-                return false;
-            }
-            const int64_t at = ((int64_t)n * H + x.head) * kState;
-            float *cell = p.seg + ((int64_t)seg * H + x.head) * kState;
-            x.t0 = bos + g * p.seg_len;
-            x.t1 = eos - x.t0 > p.seg_len ? x.t0 + p.seg_len : eos;
-            if (OUT) {
-                x.from = cell;
-                x.to = g == segs - 1 && p.fin ? p.fin + at : nullptr;
-            } else {
-                x.from = nullptr;
-                x.to = cell;
-                if (g == segs - 1) { x.t1 = x.t0; x.to = nullptr; }
-            }
-            return true;
-        }
-        return false;
+        Segment sg;
+        if (!find_segment(p.g, seg, sg, tell && it == 1)) return false;
+        x.t0 = sg.t0;
+        x.t1 = sg.t1;
+        float *cell = p.g.cells + ((int64_t)seg * H + x.head) * kState;
+        x.from = OUT ? cell : nullptr;
+        x.to = cell;
+        if (OUT) x.to = sg.last && p.fin ? p.fin + ((int64_t)sg.n * H + x.head) * kState : nullptr;
+        else if (sg.last) { x.t1 = x.t0; x.to = nullptr; }
+        return true;
     }
 };
 
@@ -188,10 +149,7 @@ __device__ __noinline__ int chunks_of(const Params &p, bool tell) {
     return total;
 }
 
-__device__ __forceinline__ float log2_decay(const Params &p, int head) {
-    // 2^(l2 n) with l2 no lower than -16384: exactly 0 for n >= 1 there, and 1 for n = 0
-    return fmaxf(p.log_decay[head] * kLog2E, -16384.f);
-}
+__device__ __forceinline__ float log2_decay(const Params &p, int head) { return decay_log2(p.log_decay, head); }
 
 // The bounded wait in few instructions (each attempt suspends for a while by
 // itself).  The roles' loops run side by side, so what they cost is instruction
@@ -521,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         for (int i = tid; i < on * (D / 8); i += 128) {
                             const int r = i / (D / 8), ch = i % (D / 8);
-                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.H + head) * D + ch * 8) =
+                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.g.H + head) * D + ch * 8) =
                                 *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
                         }
                         asm volatile("bar.sync 1, 128;" ::: "memory");   // read before the next chunk's tile
@@ -648,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
         s_abort = 1;
-        report_status(p.status, KDA_ERR_DEVICE_TIMEOUT);
+        report_status(p.g.status, KDA_ERR_DEVICE_TIMEOUT);
     }
     __syncthreads();
     if (s_abort) {      // every copy and MMA in flight lands before the memory is given back
@@ -663,63 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Start states of the segments: S(0) = initial state, S(g + 1) = lambda^{seg_len}
-// S(g) + b(g), in place over the b that the state pass left; one CTA column per
-// (sequence, head), one float4 per thread.
-template <int D>
-__global__ void __launch_bounds__(256) decay_segments_kernel(const Params p) {
-    ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
-    const int n = (int)((unsigned)blockIdx.y / (unsigned)p.H), h = (int)blockIdx.y - n * p.H;
-    int bos, eos, before = 0;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        bounds(p, i, bos, eos, false);
-        before += segments(p, eos - bos);
-    }
-    bounds(p, n, bos, eos, false);
-    int segs = segments(p, eos - bos);
-    if (before + segs > p.seg_cap) segs = p.seg_cap - before;
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, step = (int64_t)p.H * D * D;
-    const float f = exp2f(log2_decay(p, h) * (float)p.seg_len);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.init) s = *reinterpret_cast<const float4 *>(p.init + (int64_t)blockIdx.y * D * D + at);
-    float4 *cell = reinterpret_cast<float4 *>(p.seg + ((int64_t)before * p.H + h) * D * D + at);
-    // (the first segment's start state is copied too: its buffer may be the one that the last segment writes)
-#pragma unroll 4
-    for (int g = 0; g + 1 < segs; ++g) {
-        const float4 b = cell[g * (step / 4)];
-        cell[g * (step / 4)] = s;
-        s.x = fmaf(f, s.x, b.x); s.y = fmaf(f, s.y, b.y); s.z = fmaf(f, s.z, b.z); s.w = fmaf(f, s.w, b.w);
-    }
-    if (segs > 0) cell[(segs - 1) * (step / 4)] = s;
-}
-
 constexpr size_t kOrderAt = 256;
-
-// Tokens per segment, or 0 for whole chains.  Segments cost a second pass over
-// k and v, so they are taken only where the chains fill at most half of the
-// SMs; then one segment per SM, in whole chunks.
-int segment_tokens(int64_t total, int N, int H, int sms) {
-    const int64_t chains = (int64_t)N * H;
-    if (chains * 2 > sms || N > 64) return 0;
-    const int64_t per_chain_slots = (sms - chains) * C;           // sum over the sequences of len / m below it
-    int64_t m = (total * H + per_chain_slots - 1) / per_chain_slots;
-    if (N == 1) m = ((total + C - 1) / C + sms / H - 1) / (sms / H);
-    if (m < 4) m = 4;
-    const int64_t len = m * C;
-    if (len * 2 > total) return 0;
-    return (int)len;
-}
+size_t cells_at(int N) { return (kOrderAt + sizeof(int32_t) * (size_t)N + 1023) & ~size_t(1023); }
 
 }  // namespace
 
 size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D) {
-    const int len = segment_tokens(total, N, H, sm_count());
-    size_t bytes = kOrderAt + sizeof(int32_t) * (size_t)N;
-    bytes = (bytes + 1023) & ~size_t(1023);
-    if (len) bytes += (size_t)((total / len + N) * H) * D * D * sizeof(float);
-    return bytes;
+    return cells_at(N) + decay_cells_bytes(total, N, H, decay_segment_tokens(total, N, H, sm_count(), C), D, D);
 }
 
 template <int D>
@@ -731,8 +639,15 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
         !make_map_2d(&mv, d.v, true, T, cols, d.ldv * 2, C) || !make_map_2d(&mo, d.out, true, T, cols, cols * 2, C))
         return cudaErrorInvalidValue;
     const int sms = sm_count();
-    Params p{d.log_decay, d.cu_seqlens, d.num_seqs, d.H, d.total, d.scale, d.init, d.fin,
-             static_cast<__nv_bfloat16 *>(d.out), static_cast<const __nv_bfloat16 *>(d.v), d.ldv, nullptr, d.status, 0, nullptr, 0};
+    Params p{{d.cu_seqlens, d.num_seqs, d.H, d.total, 0, 0, nullptr, d.status},
+             d.log_decay,
+             d.scale,
+             d.init,
+             d.fin,
+             static_cast<__nv_bfloat16 *>(d.out),
+             static_cast<const __nv_bfloat16 *>(d.v),
+             d.ldv,
+             nullptr};
     cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -748,21 +663,16 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
     cfg.stream = st;
     cfg.attrs = &attr;
     const int64_t chains = (int64_t)d.num_seqs * d.H;
-    const int len = room ? segment_tokens(d.total, d.num_seqs, d.H, sms) : 0;
+    const int len = room ? decay_segment_tokens(d.total, d.num_seqs, d.H, sms, C) : 0;
     if (len) {
-        p.seg_len = len;
-        p.seg = reinterpret_cast<float *>(ws + ((kOrderAt + sizeof(int32_t) * (size_t)d.num_seqs + 1023) & ~size_t(1023)));
-        p.seg_cap = (int)(d.total / len) + d.num_seqs;
-        const int64_t items = (int64_t)p.seg_cap * d.H;
+        p.g.len = len;
+        p.g.cells = reinterpret_cast<float *>(ws + cells_at(d.num_seqs));
+        p.g.cap = (int)(d.total / len) + d.num_seqs;
+        const int64_t items = (int64_t)p.g.cap * d.H;
         cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
         cfg.numAttrs = 0;
         if ((e = cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, false>, mq, mk, mv, mo, p)) != cudaSuccess) return e;
-        cudaLaunchConfig_t c2 = cfg;
-        c2.gridDim = dim3(D * D / 1024, (unsigned)chains);
-        c2.blockDim = dim3(256);
-        c2.dynamicSmemBytes = 0;
-        c2.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&c2, decay_segments_kernel<D>, p)) != cudaSuccess) return e;
+        if ((e = launch_decay_segments(p.g, d.log_decay, d.init, D, D, st)) != cudaSuccess) return e;
         cfg.numAttrs = 1;
         return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, true>, mq, mk, mv, mo, p);
     }

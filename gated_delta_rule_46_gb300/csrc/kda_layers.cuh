@@ -41,7 +41,9 @@ struct DecayParams {
 // bf16, dk = dv = D = 64 or 128, total > 0, rows that start on 16-byte boundaries
 size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D);
 cudaError_t launch_decay_prefill_tc(const DecayParams &p, int D, void *workspace, size_t workspace_bytes, cudaStream_t st);
-cudaError_t launch_decay_prefill_simt(const DecayParams &p, int dk, int dv, bool bf16, cudaStream_t st);
+size_t decay_prefill_simt_workspace(int64_t total, int N, int H, int dk, int dv);
+cudaError_t launch_decay_prefill_simt(const DecayParams &p, int dk, int dv, bool bf16, void *workspace,
+                                      size_t workspace_bytes, cudaStream_t st);
 
 struct DecayStepParams {
     const void *q, *k, *v;
@@ -93,9 +95,6 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
 
 // Number of SMs of the current device.
 int sm_count();
-
-// lambda^n from the base-2 logarithm of lambda; lambda = 0 (l2 = -inf) gives 1 at n = 0.
-__device__ __forceinline__ float decay_pow(float l2, int n) { return n == 0 ? 1.f : exp2f(l2 * (float)n); }
 
 constexpr float kLog2E = 1.4426950408889634f;
 

@@ -55,10 +55,15 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,
                                         kda_dtype_t dtype) {
-    if (total_tokens <= 0 || total_tokens >= kMax31 || num_seqs <= 0 || H <= 0 || dtype != KDA_BF16 || dk != dv ||
-        (dk != 128 && dk != 64))
+    if (total_tokens <= 0 || total_tokens >= kMax31 || num_seqs <= 0 || H <= 0 || (int64_t)num_seqs * H >= kMax31 ||
+        !dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv))
         return 0;
-    return kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H, dk);
+    size_t bytes = kda::decay_prefill_simt_workspace(total_tokens, num_seqs, H, dk, dv);
+    if (dtype == KDA_BF16 && dk == dv && dk >= 64) {
+        const size_t tc = kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H, dk);
+        if (tc > bytes) bytes = tc;
+    }
+    return (bytes + 255) & ~size_t(255);
 }
 
 kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
@@ -86,7 +91,7 @@ kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_
         aligned(v, 16) && aligned(out, 16) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0)
         return from_cuda(kda::launch_decay_prefill_tc(p, dk, workspace, workspace_bytes,
                                                       reinterpret_cast<cudaStream_t>(stream)));
-    return from_cuda(kda::launch_decay_prefill_simt(p, dk, dv, dtype == KDA_BF16,
+    return from_cuda(kda::launch_decay_prefill_simt(p, dk, dv, dtype == KDA_BF16, workspace, workspace_bytes,
                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -265,3 +265,41 @@ def test_segments_of_few_chains(d_, lens, H):
     d["init"] = state
     again, same = _prefill(d, dev, final_state=state)
     assert same is state and torch.equal(again, out) and torch.equal(state, fin)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(F32, 128, 128), (F32, 64, 32), (BF, 32, 64), (F32, 32, 128)])
+@pytest.mark.parametrize("lens,H", [([2500], 3), ([600, 0, 1500], 2), ([32 * 40 + 5], 1)])
+def test_segments_on_the_cuda_cores(dtype, dk, dv, lens, H):
+    dev = need_gpu()
+    d = _inputs(lens, H, dk, dv, dtype, seed=22)
+    d["ld"] = -torch.exp2(-9 - 3 * torch.rand(H, generator=torch.Generator().manual_seed(5)))
+    out, fin = _prefill(d, dev, fused=True)
+    _check(d, out, fin)
+    one, last = _prefill(d, dev, workspace=torch.zeros(16, dtype=torch.uint8, device=dev))
+    _check(d, one, last)
+
+
+@pytest.mark.parametrize("dtype,d_", [(BF, 128), (BF, 64), (F32, 64)])
+def test_unaligned_rows(dtype, d_):
+    """q, k, v that start on odd elements of wider rows: no 16-byte copies possible."""
+    dev = need_gpu()
+    d = _inputs([100, 33], 2, d_, d_, dtype, seed=23)
+    wide = {n: torch.zeros(133, 2 * d_ + 7, dtype=dtype, device=dev) for n in "qkv"}
+    views = {}
+    for i, n in enumerate("qkv"):
+        wide[n][:, i + 1:i + 1 + 2 * d_] = d[n].reshape(133, -1).to(dev)
+        views[n] = wide[n][:, i + 1:i + 1 + 2 * d_].unflatten(1, (2, d_))
+    out, fin = decay_prefill(views["q"], views["k"], views["v"], d["ld"].to(dev), d["cu"].to(dev), d["init"].to(dev))
+    _check(d, out, fin)
+
+
+@pytest.mark.parametrize("dtype,d_", [(BF, 128), (F32, 64)])
+def test_overlapping_offsets_stay_inside_the_workspace(dtype, d_):
+    """Offsets that go back and forth name more tokens than there are: reported, nothing out of range."""
+    dev = need_gpu()
+    d = _inputs([3000], 1, d_, d_, dtype, seed=24, init=False)
+    cu = [0, 3000, 0, 3000, 0, 3000, 0, 3000]
+    d["cu"] = torch.tensor(cu, dtype=torch.int32)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, fin = _prefill(d, dev, status=status)
+    assert check_device_status(status) == kda.KDA_ERR_INVALID_ARG
