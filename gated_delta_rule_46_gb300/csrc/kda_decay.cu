@@ -34,13 +34,22 @@ __global__ void __launch_bounds__(256) decay_segments_kernel(const DecaySegs p, 
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) s = *reinterpret_cast<const float4 *>(init + (int64_t)blockIdx.y * state + at);
     float4 *cell = reinterpret_cast<float4 *>(p.cells + ((int64_t)before * p.H + h) * state + at);
-#pragma unroll 4
-    for (int g = 0; g + 1 < segs; ++g) {
-        const float4 b = cell[g * (step / 4)];
-        cell[g * (step / 4)] = s;
-        s.x = fmaf(f, s.x, b.x); s.y = fmaf(f, s.y, b.y); s.z = fmaf(f, s.z, b.z); s.w = fmaf(f, s.w, b.w);
+    // eight loads under way at a time: a store may not be overtaken by the loads after it
+    constexpr int B = 8;
+    for (int g0 = 0; g0 < segs; g0 += B) {
+        float4 b[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (g0 + i + 1 < segs) b[i] = cell[(g0 + i) * (step / 4)];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (g0 + i >= segs) break;
+            cell[(g0 + i) * (step / 4)] = s;
+            if (g0 + i + 1 < segs) {
+                s.x = fmaf(f, s.x, b[i].x); s.y = fmaf(f, s.y, b[i].y); s.z = fmaf(f, s.z, b[i].z); s.w = fmaf(f, s.w, b[i].w);
+            }
+        }
     }
-    if (segs > 0) cell[(segs - 1) * (step / 4)] = s;
 }
 
 static cudaLaunchConfig_t dependent(cudaLaunchAttribute &attr, dim3 grid, size_t smem, cudaStream_t st) {

@@ -214,47 +214,60 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
 }
 
 // ---------------------------------------------------------------------------
-// Join: one CTA per sequence, one warp per query head.  Heads whose item one
-// CTA had whole are done already; a sequence without tokens gets zeros.
+// Join: one warp per sequence and query head, eight heads per CTA.  Heads whose
+// item one CTA had whole are done already; a sequence without tokens gets
+// zeros.  A long row has a part from nearly every CTA: their maxima and sums
+// are read a part per lane and joined by shuffles, then the weighted rows are
+// summed in order, with as many loads under way as the unrolling gives.
 // ---------------------------------------------------------------------------
 template <typename T, int D, int TILE, int HB>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int grid) {
     __shared__ int64_t s_sum[257];
     __shared__ int s_n;
-    const int n = blockIdx.x, lane = threadIdx.x & 31;
+    const int n = blockIdx.x, hq = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     constexpr int E = D / 32;
     T *out = static_cast<T *>(p.out);
     const int64_t nt = tiles_of<TILE>(p, n);
     if (nt == 0) {
         ptx::pdl_wait();         // this grid's end stands for the one before it too
-        empty_sequence<T>(p, n, D);
+        if (blockIdx.y == 0) empty_sequence<T>(p, n, D);
         return;
     }
     const Split sp = find_split<TILE>(p, items, grid, -1, n, s_sum, &s_n);
     ptx::pdl_wait();             // the partial results
-    for (int hq = threadIdx.x >> 5; hq < p.Hq; hq += 8) {
-        const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / HB, g = gi % HB;
-        const int64_t s = sp.cum * items + item * nt, e = s + nt;
-        const int b0 = (int)(((s + 1) * sp.g - 1) / sp.W), b1 = (int)((e * sp.g - 1) / sp.W);
-        if (b0 == b1) continue;
-        float m = -INFINITY, l = 0.f, a[E] = {};
-        for (int b = b0; b <= b1; ++b) {
-            const float *part = p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB);
-            const float mb = part[2 * g], lb = part[2 * g + 1];
-            const float mn = fmaxf(m, mb), mu = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m - mu), fb = exp2f(mb - mu);
-            m = mn;
-            l = l * f + lb * fb;
+    if (hq >= p.Hq) return;
+    const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / HB, g = gi % HB;
+    const int64_t s = sp.cum * items + item * nt, e = s + nt;
+    const int b0 = (int)(((s + 1) * sp.g - 1) / sp.W), b1 = (int)((e * sp.g - 1) / sp.W);
+    if (b0 == b1) return;
+    // CTA b0 starts the item (slot 1), the others go on with it (slot 0)
+    auto part = [&](int b) { return p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB); };
+    float m = -INFINITY;
+    for (int b = b0 + lane; b <= b1; b += 32) m = fmaxf(m, part(b)[2 * g]);
 #pragma unroll
-            for (int i = 0; i < E; ++i) a[i] = a[i] * f + part[HB * 2 + g * D + lane * E + i] * fb;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mu = m == -INFINITY ? 0.f : m;
+    float l = 0.f, a[E] = {};
+    for (int c0 = b0; c0 <= b1; c0 += 32) {
+        const int b = c0 + lane;
+        const float f = b <= b1 ? exp2f(part(b)[2 * g] - mu) : 0.f;
+        l += b <= b1 ? part(b)[2 * g + 1] * f : 0.f;
+        const int cnt = min(32, b1 - c0 + 1);
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+            const float *x = part(c0 + i) + HB * 2 + g * D + lane * E;
+            const float w = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+            for (int j = 0; j < E; ++j) a[j] = fmaf(x[j], w, a[j]);
         }
-        const int64_t row = (int64_t)n * p.Hq + hq;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            out[row * D + lane * E + i] = from_f32<T>(l > 0.f ? a[i] / l : (l == 0.f ? 0.f : l));
-        if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) / kLog2E;
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int64_t row = (int64_t)n * p.Hq + hq;
+#pragma unroll
+    for (int i = 0; i < E; ++i) out[row * D + lane * E + i] = from_f32<T>(l > 0.f ? a[i] / l : (l == 0.f ? 0.f : l));
+    if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) / kLog2E;
 }
 
 template <typename T, int D, int TILE, int HB>
@@ -264,7 +277,7 @@ static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.N);
+    cfg.gridDim = dim3((unsigned)p.N, (unsigned)((p.Hq + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = &attr;
