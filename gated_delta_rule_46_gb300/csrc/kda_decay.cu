@@ -52,24 +52,10 @@ __global__ void __launch_bounds__(256) decay_segments_kernel(const DecaySegs p, 
     }
 }
 
-static cudaLaunchConfig_t dependent(cudaLaunchAttribute &attr, dim3 grid, size_t smem, cudaStream_t st) {
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
 cudaError_t launch_decay_segments(const DecaySegs &p, const float *log_decay, const float *init, int dk, int dv,
                                   cudaStream_t st) {
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = dependent(attr, dim3(dk * dv / 1024, (unsigned)(p.N * p.H)), 0, st);
-    return cudaLaunchKernelEx(&cfg, decay_segments_kernel, p, log_decay, init, dk * dv);
+    return launch_dependent(decay_segments_kernel, dim3(dk * dv / 1024, (unsigned)(p.N * p.H)), 256, 0, st, 1, p, log_decay,
+                            init, dk * dv);
 }
 
 // ---------------------------------------------------------------------------
@@ -130,7 +116,8 @@ __global__ void __launch_bounds__(256, 2) decay_simt_kernel(const DecaySimtParam
     float *pw = sR + (G - 1) * C * JB;                         // lambda^0 .. lambda^C
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j0 = blockIdx.y * JB;
-    if (OUT) ptx::pdl_wait();                                  // the segments' start states
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const int item = (int)((unsigned)blockIdx.x / (unsigned)p.g.H), h = (int)blockIdx.x - item * p.g.H;
     const int64_t state = (int64_t)DK * dv;
     int t0, t1;
@@ -351,18 +338,15 @@ static cudaError_t decay_simt(DecaySimtParams &p, int dv, int64_t chains, cudaSt
     const size_t smem = sizeof(float) * (2 * C * (DK + 4) + C * JB + DK * JB + C * (C + 4) + (G - 1) * C * JB + C + 1);
     cudaError_t e = cudaFuncSetAttribute(decay_simt_kernel<T, DK, JB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    cudaLaunchConfig_t cfg = dependent(attr, dim3((unsigned)chains, dv / JB), smem, st);
-    cfg.numAttrs = 0;
+    dim3 grid((unsigned)chains, dv / JB);
     if (p.g.len) {
         e = cudaFuncSetAttribute(decay_simt_kernel<T, DK, JB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        cfg.gridDim.x = (unsigned)((int64_t)p.g.cap * p.g.H);
-        if ((e = cudaLaunchKernelEx(&cfg, decay_simt_kernel<T, DK, JB, false>, p, dv)) != cudaSuccess) return e;
+        grid.x = (unsigned)((int64_t)p.g.cap * p.g.H);
+        if ((e = launch_dependent(decay_simt_kernel<T, DK, JB, false>, grid, 256, smem, st, 1, p, dv)) != cudaSuccess) return e;
         if ((e = launch_decay_segments(p.g, p.log_decay, p.init, DK, dv, st)) != cudaSuccess) return e;
-        cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, decay_simt_kernel<T, DK, JB, true>, p, dv);
+    return launch_dependent(decay_simt_kernel<T, DK, JB, true>, grid, 256, smem, st, 1, p, dv);
 }
 
 template <typename T>
@@ -409,6 +393,8 @@ __global__ void __launch_bounds__(256) decay_decode_kernel(const DecayStepParams
     static_assert(DK % RPP == 0, "decode tiling");
     __shared__ float s_k[DK], s_q[DK];
     __shared__ float s_red[RPP][DV + 4];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const int nh = blockIdx.x, n = nh / p.H, h = nh % p.H, tid = threadIdx.x;
     T *out = static_cast<T *>(p.out) + (int64_t)nh * DV;
     int slot = p.slots ? p.slots[n] : n;
@@ -456,14 +442,14 @@ __global__ void __launch_bounds__(256) decay_decode_kernel(const DecayStepParams
 
 template <typename T>
 static cudaError_t decay_decode_dispatch(const DecayStepParams &p, int dk, int dv, cudaStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)p.N * p.H);
+    const dim3 grid((unsigned)((int64_t)p.N * p.H));
 #define KDA_DECAY_CASE(DK_, DV_) \
-    if (dk == DK_ && dv == DV_) decay_decode_kernel<T, DK_, DV_><<<grid, 256, 0, st>>>(p);
+    if (dk == DK_ && dv == DV_) return launch_dependent(decay_decode_kernel<T, DK_, DV_>, grid, 256, 0, st, 1, p);
     KDA_DECAY_CASE(32, 32) KDA_DECAY_CASE(32, 64) KDA_DECAY_CASE(32, 128)
     KDA_DECAY_CASE(64, 32) KDA_DECAY_CASE(64, 64) KDA_DECAY_CASE(64, 128)
     KDA_DECAY_CASE(128, 32) KDA_DECAY_CASE(128, 64) KDA_DECAY_CASE(128, 128)
 #undef KDA_DECAY_CASE
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decay_decode(const DecayStepParams &p, int dk, int dv, bool bf16, cudaStream_t st) {

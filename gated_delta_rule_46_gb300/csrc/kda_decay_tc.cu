@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
-    if (OUT) ptx::pdl_wait();          // the segments' start states
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     bool ok = true;
     Walk<D, OUT> walk;
     Item x;
@@ -654,14 +655,6 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
     if (e != cudaSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
     const int64_t chains = (int64_t)d.num_seqs * d.H;
     const int len = room ? decay_segment_tokens(d.total, d.num_seqs, d.H, sms, C) : 0;
     if (len) {
@@ -669,12 +662,11 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
         p.g.cells = reinterpret_cast<float *>(ws + cells_at(d.num_seqs));
         p.g.cap = (int)(d.total / len) + d.num_seqs;
         const int64_t items = (int64_t)p.g.cap * d.H;
-        cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
-        cfg.numAttrs = 0;
-        if ((e = cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, false>, mq, mk, mv, mo, p)) != cudaSuccess) return e;
+        const dim3 grid((unsigned)(items < sms ? items : sms));
+        if ((e = launch_dependent(decay_chunk_kernel<D, false>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
+            return e;
         if ((e = launch_decay_segments(p.g, d.log_decay, d.init, D, D, st)) != cudaSuccess) return e;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, true>, mq, mk, mv, mo, p);
+        return launch_dependent(decay_chunk_kernel<D, true>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
     }
     if (room && chains > sms && d.num_seqs > 1) {
         int32_t *order = reinterpret_cast<int32_t *>(ws + kOrderAt);
@@ -682,10 +674,9 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
                                  reinterpret_cast<uint32_t *>(ws), st)) != cudaSuccess)
             return e;
         p.order = order;
-        cfg.numAttrs = 1;
     }
-    cfg.gridDim = dim3((unsigned)(chains < sms ? chains : sms));
-    return cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, true>, mq, mk, mv, mo, p);
+    return launch_dependent(decay_chunk_kernel<D, true>, dim3((unsigned)(chains < sms ? chains : sms)), kThreads, kSmem, st, 1, mq,
+                            mk, mv, mo, p);
 }
 
 cudaError_t launch_decay_prefill_tc(const DecayParams &d, int D, void *workspace, size_t workspace_bytes, cudaStream_t st) {

@@ -96,6 +96,29 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
 // Number of SMs of the current device.
 int sm_count();
 
+// Launches `kernel` so that its start may overlap the end of the kernel before
+// it in the stream: the kernel calls griddepcontrol.wait before it touches
+// anything that another kernel writes, and so does every one of its blocks
+// before it ends.  cluster: CTAs of a cluster along x, or 1.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
+                                    unsigned cluster, const A &...args) {
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr float kLog2E = 1.4426950408889634f;
 
 }  // namespace kda

@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
     bool ok = true;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
 
     if (warp == 0 && !LOAD) {
         if (lane == 0) {
@@ -247,18 +249,23 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  A pair of CTAs per 256 x 256 tile: each loads its 128 rows of x
-// and 128 of the 256 rows of w per K step (32 KB; the MMA reads the halves of w
-// from both, so each SM fetches half of what a lone CTA would), accumulates
-// 128 x 256 float32 in TMEM, two tiles' worth, so that the epilogue of one tile
+// Many rows.  A pair of CTAs per 256 x BN tile: each loads its 128 rows of x and
+// half of the BN rows of w per K step (32 KB for BN = 256; the MMA reads the
+// halves of w from both, so each SM fetches half of what a lone CTA would),
+// accumulates 128 x BN float32 in TMEM, two tiles' worth, so that the epilogue of one tile
 // runs beside the next one's MMAs.  Persistent: pair i takes tiles i, i + pairs, ...
 // Warp 0 loads, warp 1 issues (rank 0 of the pair only), warps 2-9 are the
-// epilogue: two groups of four, 128 columns each, by way of a 16 KB staging
+// epilogue: two groups of four, BN / 2 columns each, by way of a 16 KB staging
 // tile and TMA stores; a residual tile comes in by TMA through the same buffer.
 // ---------------------------------------------------------------------------
-constexpr int kStages = 6;
-constexpr uint32_t kStageBytes = 2 * kABytes, kStaging = 16384;
-constexpr uint32_t kPairSmem = kStages * kStageBytes + 2 * kStaging + 1024;
+constexpr uint32_t kStaging = 16384;
+template <int BN>
+struct PairLay {
+    static constexpr int stages = BN == 256 ? 6 : 8;
+    static constexpr uint32_t stage = kABytes + (BN / 2) * 128;
+    static constexpr uint32_t staging = stages * stage;
+    static constexpr uint32_t bytes = staging + 2 * kStaging + 1024;
+};
 
 struct PairParams {
     Tail t;
@@ -272,11 +279,13 @@ __device__ __forceinline__ void tile_at(const PairParams &p, int i, int &tm, int
     tn = r / h;
 }
 
-template <int ACT, bool F32>
+template <int ACT, bool F32, int BN>
 __global__ void __launch_bounds__(320)
     linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                        const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
                        const PairParams p) {
+    using L = PairLay<BN>;
+    constexpr int kStages = L::stages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], rbar[2];
     __shared__ uint32_t s_tmem, s_abort;
@@ -303,7 +312,7 @@ __global__ void __launch_bounds__(320)
         ptx::prefetch_tensormap(&mo);
     }
     if (warp == 1) {
-        ptx::tmem_alloc_pair(&s_tmem, 512);
+        ptx::tmem_alloc_pair(&s_tmem, 2 * BN);
         ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before_sync();
@@ -311,6 +320,8 @@ __global__ void __launch_bounds__(320)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
     bool ok = true;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -318,13 +329,13 @@ __global__ void __launch_bounds__(320)
             for (int i = pair; i < tiles && ok; i += pairs) {
                 int tm, tn;
                 tile_at(p, i, tm, tn);
-                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
+                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < kbs; ++kb, ++it) {
                     const int s = it % kStages;
                     if (it >= kStages && !ptx::mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, kWaitBudget)) { ok = false; break; }
-                    uint8_t *a = sm + s * kStageBytes;
+                    uint8_t *a = sm + s * L::stage;
                     // rank 0's barrier counts the bytes of both CTAs
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::stage);
                     const uint32_t bar = ptx::map_to_rank(&full[s], 0);
                     ptx::tma_load_2d_pair(a, &mx, kb * kBK, m0, bar);
                     ptx::tma_load_2d_pair(a + kABytes, &mw, kb * kBK, n0, bar);
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(320)
         }
     } else if (warp == 1) {
         if (rank == 0 && ptx::elect_one()) {
-            const uint32_t idesc = ptx::idesc_bf16_f32(256, 256);
+            const uint32_t idesc = ptx::idesc_bf16_f32(256, BN);
             int it = 0, n = 0;
             for (int i = pair; i < tiles && ok; i += pairs, ++n) {
                 const int b = n & 1;
@@ -343,11 +354,11 @@ __global__ void __launch_bounds__(320)
                     const int s = it % kStages;
                     if (!ptx::mbar_wait_cluster(&full[s], (it / kStages) & 1, kWaitBudget)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
-                    const uint32_t a = ptx::smem_addr(sm + s * kStageBytes);
+                    const uint32_t a = ptx::smem_addr(sm + s * L::stage);
                     const uint64_t da = ptx::sdesc_kmajor_sw128(a), db = ptx::sdesc_kmajor_sw128(a + kABytes);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16_ss_pair(tmem + b * 256, da + k * 2, db + k * 2, idesc, kb > 0 || k > 0);
+                        ptx::mma_bf16_ss_pair(tmem + b * BN, da + k * 2, db + k * 2, idesc, kb > 0 || k > 0);
                     ptx::mma_commit_pair(&empty[s]);
                 }
                 if (ok) ptx::mma_commit_pair(&tfull[b]);
@@ -356,15 +367,15 @@ __global__ void __launch_bounds__(320)
     } else {
         const int g = (warp - 2) >> 2, q = warp & 3, row = q * 32 + lane;
         const bool lead = ((warp - 2) & 3) == 0 && lane == 0;      // the group's thread for TMA
-        uint8_t *st = sm + kStages * kStageBytes + g * kStaging;
-        constexpr int CW = F32 ? 32 : 64, CHUNKS = 128 / CW;       // columns of a 128-byte staging row
+        uint8_t *st = sm + L::staging + g * kStaging;
+        constexpr int CW = F32 ? 32 : 64, CHUNKS = BN / 2 / CW;    // columns of a 128-byte staging row
         int n = 0;
         uint32_t rphase = 0;
         for (int i = pair; i < tiles && ok; i += pairs, ++n) {
             const int b = n & 1;
             int tm, tn;
             tile_at(p, i, tm, tn);
-            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + g * 128;
+            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * BN + g * (BN / 2);
             // the group goes on, or gives up, as one
             ok = !ptx::bar_any(g + 1, 128, !ptx::mbar_wait_cluster(&tfull[b], (n >> 1) & 1, kWaitBudget));
             if (!ok) break;
@@ -381,9 +392,9 @@ __global__ void __launch_bounds__(320)
                     }
                 }
                 float d[CW];
-                ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * 256 + g * 128 + c * CW, *reinterpret_cast<float(*)[32]>(d));
+                ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c * CW, *reinterpret_cast<float(*)[32]>(d));
                 if constexpr (!F32)
-                    ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * 256 + g * 128 + c * CW + 32,
+                    ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c * CW + 32,
                                    *reinterpret_cast<float(*)[32]>(d + 32));
                 ptx::tmem_ld_wait();
                 if (c == CHUNKS - 1) {
@@ -453,37 +464,27 @@ __global__ void __launch_bounds__(320)
     ptx::cluster_sync();         // neither CTA leaves while the other's MMAs or barriers use it
     if (warp == 1) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc_pair(tmem, 512);
+        ptx::tmem_dealloc_pair(tmem, 2 * BN);
     }
 }
 
-template <int ACT, bool F32>
+template <int ACT, bool F32, int BN>
 cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
+    using L = PairLay<BN>;
     CUtensorMap mx, mw, mo, mr;
     const uint64_t eb = F32 ? 4 : 2;
-    if (!make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, 128) || !make_map_2d(&mw, p.w, true, p.N, p.K, p.K * 2, 128) ||
+    if (!make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, 128) || !make_map_2d(&mw, p.w, true, p.N, p.K, p.K * 2, BN / 2) ||
         !make_map_2d(&mo, p.out, !F32, p.M, p.N, p.N * eb, 128) ||
         !make_map_2d(&mr, p.residual ? p.residual : p.out, !F32, p.M, p.N, p.N * eb, 128))
         return cudaErrorInvalidValue;
     PairParams pp{{p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status}, (int)((p.M + 255) / 256),
-                  (int)((p.N + 255) / 256), 8};
-    auto *kernel = linear_pair_kernel<ACT, F32>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+                  (int)((p.N + BN - 1) / BN), 8};
+    auto *kernel = linear_pair_kernel<ACT, F32, BN>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)pp.tiles_m * pp.tiles_n;
     const int pairs = sm_count() / 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
-    cfg.blockDim = dim3(320);
-    cfg.dynamicSmemBytes = kPairSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, mo, mr, pp);
+    return launch_dependent(kernel, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), 320, L::bytes, st, 2, mx, mw, mo, mr, pp);
 }
 
 template <int ACT, bool F32, int LOAD>
@@ -495,13 +496,12 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     rp.ldx = p.ldx;
     rp.NT = p.M < 256 ? (int)((p.M + 15) / 16) * 16 : 256;
     const uint32_t stage = kABytes + rp.NT * 128;
-    // two CTAs per SM where the stages allow it: one's epilogue beside the other's loads
-    const int per_sm = rp.NT <= 128 && !LOAD ? 2 : 1;
-    const uint32_t room = per_sm == 2 ? 104 * 1024 : 200 * 1024;
-    rp.stages = (int)(room / stage) < 12 ? (int)(room / stage) : 12;
+    constexpr uint32_t kRoom = 200 * 1024;      // all of an SM's: the weights under way are what hides HBM's latency
+    rp.stages = (int)(kRoom / stage) < 12 ? (int)(kRoom / stage) : 12;
     const int64_t tiles = ((p.N + 127) / 128) * ((p.M + rp.NT - 1) / rp.NT);
-    // split K while that still adds CTAs to the GPU and leaves each at least four stages of work
-    const int64_t slots = (int64_t)sm_count() * per_sm, kbs = (p.K + kBK - 1) / kBK;
+    // Split K over a cluster while one CTA per SM still has room for it and each keeps at least four steps.  64 x 4096
+    // x 4096 (32 tiles): S = 4 takes 10.6 us; with two smaller CTAs per SM S = 4 takes 11.2 and S = 8 11.9.
+    const int64_t slots = sm_count(), kbs = (p.K + kBK - 1) / kBK;
     rp.S = 1;
     while (rp.S < 8 && tiles * rp.S * 2 <= slots && kbs / (rp.S * 2) >= 4) rp.S *= 2;
     uint32_t smem = rp.stages * stage;
@@ -515,18 +515,7 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t mt = (p.M + rp.NT - 1) / rp.NT;
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(LOAD ? 448 : 192);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = rp.S;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = rp.S > 1 ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt);
-    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, rp);
+    return launch_dependent(kernel, dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt), LOAD ? 448 : 192, smem, st, rp.S, mw, mx, rp);
 }
 
 template <int ACT, bool F32>
@@ -537,8 +526,12 @@ cudaError_t launch_act(const LinearParams &p, cudaStream_t st) {
     const uint64_t eb = F32 ? 4 : 2;
     const bool store = p.N * eb % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(p.residual) % 16 == 0;
-    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-    if (store && p.M > 256 && tiles * 2 >= sm_count() / 2) return launch_pair<ACT, F32>(p, st);
+    // Tiles of 256 x 256 where they give more than half of the pairs work (256 x 16384 x 4096: 31 us, 38 by rows; 1024 x
+    // 4096 x 4096: 25 us, 32 by rows), of 256 x 128 where those do (512 x 4096 x 4096: 21 us, 24 either way; 1024^3: 8.5
+    // us, 10.4 by rows).  With fewer, splitting K beats both (256 x 4096 x 4096: 16 us, 20 in pairs).
+    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256), pairs = sm_count() / 2;
+    if (store && p.M > 128 && tiles * 2 > pairs) return launch_pair<ACT, F32, 256>(p, st);
+    if (store && p.M > 256 && tiles * 5 > pairs) return launch_pair<ACT, F32, 128>(p, st);
     return launch_rows<ACT, F32, 0>(p, st);
 }
 

@@ -17,6 +17,8 @@ namespace kda {
 // ---------------------------------------------------------------------------
 template <typename V>
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= p.total) return;
@@ -59,9 +61,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p)
 
 cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t st) {
     const unsigned grid = (unsigned)((p.total + 7) / 8);
-    if (vec16) paged_append_kernel<uint4><<<grid, 256, 0, st>>>(p);
-    else paged_append_kernel<uint16_t><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(vec16 ? paged_append_kernel<uint4> : paged_append_kernel<uint16_t>, dim3(grid), 256, 0, st, 1, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, wy = tid >> 5;
     const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
-    ptx::pdl_launch_dependents();     // the join kernel may start its setup
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
     empty_sequences<T, TILE>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
@@ -273,16 +274,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
 template <typename T, int D, int TILE, int HB>
 static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) {
     if (p.lone) return cudaSuccess;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.N, (unsigned)((p.Hq + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, TILE, HB>, p, grid);
+    return launch_dependent(paged_join_kernel<T, D, TILE, HB>, dim3((unsigned)p.N, (unsigned)((p.Hq + 7) / 8)), 256, 0, st, 1,
+                            p, grid);
 }
 
 // Query heads per item of the tensor-core form: one pass over the cache for up to 32 of them.
@@ -323,8 +316,7 @@ static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
-    paged_decode_simt_kernel<T, D><<<grid, 256, smem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_dependent(paged_decode_simt_kernel<T, D>, dim3(grid), 256, smem, st, 1, p)) != cudaSuccess) return e;
     return launch_join<T, D, kTile, kHB>(p, grid, st);
 }
 

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(384, 1)
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     constexpr uint32_t kCols = HB == 16 ? 64 : 128;
 
-    ptx::pdl_launch_dependents();     // the join kernel may start its setup
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
     empty_sequences<__nv_bfloat16, TILE>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
@@ -443,8 +444,7 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     static_assert(smem <= 229000, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, 384, smem, st>>>(mk, mv, p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), 384, smem, st, 1, mk, mv, p);
 }
 
 }  // namespace

@@ -155,3 +155,11 @@ def test_refusals():
         linear(x, w.cpu())
     with pytest.raises(KDAError):
         linear(x[:, :0], w[:, :0].contiguous())
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 2056, 200), (1024, 1032, 136), (260, 6000, 64), (200, 10240, 264), (2304, 2304, 72)])
+@pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_pair_tiles(M, N, K, odt, residual):
+    """Sizes that the CTA-pair kernel takes, both tile widths, edges in every direction."""
+    _run(M, N, K, True, residual, "gelu", odt, seed=11)
