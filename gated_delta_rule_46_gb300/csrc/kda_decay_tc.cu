@@ -99,7 +99,7 @@ struct Item {
 template <int D, bool OUT>
 struct Walk {
     unsigned it = 0;
-    __device__ __noinline__ bool next(const Params &p, Item &x, bool tell) {
+    __device__ __forceinline__ bool next(const Params &p, Item &x, bool tell) {
         constexpr int64_t kState = (int64_t)D * D;
         const unsigned H = (unsigned)p.g.H;
         if (p.g.len == 0) {
@@ -141,7 +141,7 @@ struct Walk {
 
 // Chunks of all of a CTA's items.
 template <int D, bool OUT>
-__device__ __noinline__ int chunks_of(const Params &p, bool tell) {
+__device__ __forceinline__ int chunks_of(const Params &p, bool tell) {
     Walk<D, OUT> walk;
     Item x;
     int total = 0;
@@ -207,7 +207,7 @@ __device__ __forceinline__ void split3(const uint4 &k, float w, uint4 &t1, uint4
 
 // sum_{s <= i} P_is v_sj for token i of the chunk at token t and the channel that
 // is element `at` of a row, v from global memory.
-__device__ __noinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int at, int i) {
+__device__ __forceinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int at, int i) {
     float y = 0.f;
     if (t + i >= t1) return y;
 #pragma unroll 1
@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Walk<D, OUT> walk;
     Item x;
-
+    // 96 registers a thread at launch; of the five warpgroups' 480 the state's two take 120 each
+    if (warp < 4) {
+    ptx::regs_dec<80>();
     if (warp == 2) {                                              // ---- loads, and the state's product
         // one thread does whichever of the two can go ahead
         const int total = chunks_of<D, OUT>(p, true);
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             long long since = clock64();
             while (dc < total) {
                 bool did = false;
-                if (lc < total && (lp == 0 || ptx::mbar_try_wait(&bar[L::FREE + ls], (lp - 1) & 1))) {
+                if (lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
                     while (t >= t1) {
                         walk.next(p, x, false);
                         t = x.t0;
@@ -297,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++ls == NS) { ls = 0; ++lp; }
                     did = true;
                 }
-                if (ptx::mbar_try_wait(&bar[L::TF + 2 * ds + half], dp & 1) &&
-                    (half == 1 || dc == 0 || ptx::mbar_try_wait(&bar[L::DSFREE], (dc - 1) & 1))) {
+                if (ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
+                    (half == 1 || dc == 0 || ptx::mbar_test(&bar[L::DSFREE], (dc - 1) & 1))) {
                     ptx::tc_fence_after_sync();
                     const uint64_t a = dt + half * (4096 >> 4);
                     const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool todo = c + 1 < total;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
-                    if (todo && (pass == 1 || c < 0 || ptx::mbar_try_wait(&bar[L::LD + ns], np & 1))) {
+                    if (todo && (pass == 1 || c < 0 || ptx::mbar_test(&bar[L::LD + ns], np & 1))) {
                         todo = false;
                         if (!wait_on(&bar[L::LD + ns], np)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
@@ -412,7 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++ns == NS) { ns = 0; ++np; }
             }
         }
-    } else if (warp >= 4 && warp < 8) {                           // ---- the output
+    }
+    } else if (warp < 8) {                                        // ---- the output
+        ptx::regs_dec<80>();
         if (OUT) {
             const int tid = threadIdx.x - 128, q = warp & 3;
             float *pw = reinterpret_cast<float *>(sm + L::PW);
@@ -489,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (tid == 0) ptx::bulk_wait_all();
         }
-    } else if (warp >= 8 && warp < 12) {                          // ---- the decayed keys in three terms
+    } else if (warp < 12) {                                       // ---- the decayed keys in three terms
+        ptx::regs_dec<80>();
         constexpr int RP = 128 / (D / 8), NR = 32 / RP;                       // rows at a time; times per half chunk
         const int tid = threadIdx.x - 256, r0 = tid / (D / 8), ch = tid % (D / 8);   // rows r0, r0 + RP, ...; 16-byte column
         const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
@@ -550,7 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
         }
-    } else if (warp >= 12 && (warp & 3) * 32 < D) {               // ---- the state: lane = value channel
+    } else {                                                      // ---- the state: lane = value channel
+        ptx::regs_inc<120>();
+        if ((warp & 3) * 32 < D) {
         constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
         const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;
         const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
@@ -582,27 +589,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = t0; t < t1; t += C, ++c) {
                 const bool more = OUT && t + C < t1;
                 const float f = exp2f(l2 * (float)min(t1 - t, C));
-                ok = warp_wait(&bar[L::DS], c) && (!more || warp_wait(&bar[L::QS], c));
+                ok = warp_wait(&bar[L::DS], c);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
+                // 32 columns at a time: the next product may overwrite them as soon as the last have been read
 #pragma unroll
-                for (int e = 0; e < KC; e += 16) {
-                    float d[16];
-                    ptx::tmem_ld16(at + TM_DS + k0 + e, d);
+                for (int e = 0; e < KC; e += 32) {
+                    float d[32];
+                    ptx::tmem_ld16(at + TM_DS + k0 + e, *reinterpret_cast<float(*)[16]>(d));
+                    ptx::tmem_ld16(at + TM_DS + k0 + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
                     ptx::tmem_ld_wait();
+                    if (e + 32 == KC) {
+                        ptx::tc_fence_before_sync();
+                        warp_arrive(&bar[L::DSFREE]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
-                    if (more) copy_out(e);
+                    for (int i = 0; i < 32; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
                 }
-                if (more) ptx::tmem_st_wait();
-                ptx::tc_fence_before_sync();
-                warp_arrive(&bar[L::DSFREE]);
-                if (more) warp_arrive(&bar[L::SREADY]);
+                if (more) {
+                    ok = warp_wait(&bar[L::QS], c);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+#pragma unroll
+                    for (int e = 0; e < KC; e += 16) copy_out(e);
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before_sync();
+                    warp_arrive(&bar[L::SREADY]);
+                }
             }
             if (!ok) break;
             if (x.to)
 #pragma unroll
                 for (int e = 0; e < KC; ++e) x.to[mine + e * D] = s[e];
+        }
         }
     }
     if (!ok) {
