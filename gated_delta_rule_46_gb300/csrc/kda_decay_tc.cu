@@ -326,7 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 2) {                                        // ---- P: thread = token of the chunk
         if (OUT) {
             const int i = threadIdx.x;
-            const float fi = (float)i;
             int c = 0;
             while (ok && walk.next(p, x, false)) {
                 const float l2 = log2_decay(p, x.head);
@@ -339,18 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t *sp = sm + L::P + b * kTile;
                     // (columns 32-63 of rows 0-31 are never written: zero from the start)
 #pragma unroll 1
-                    for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 16) {
-                        float d[16];
-                        ptx::tmem_ld16(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
-                        const float f0 = fi - (float)j0;
+                    for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 32) {
+                        float d[32];
+                        ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
+                        const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float gap = f0 - (float)e;
-                            d[e] = gap >= 0.f ? d[e] * ex2(l2 * gap) : 0.f;
-                        }
-                        st_chunk(sp, swz(i, j0 >> 3), d);
-                        st_chunk(sp, swz(i, (j0 >> 3) + 1), d + 8);
+                        for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
+                        if (j0 == 32 * warp)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) d[e] = e <= lane ? d[e] : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) st_chunk(sp, swz(i, (j0 + e) >> 3), d + e);
                     }
                     ptx::fence_async_smem();
                     ptx::tc_fence_before_sync();
