@@ -51,11 +51,26 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p)
     const V *k = reinterpret_cast<const V *>(static_cast<const uint8_t *>(p.k) + t * p.ldk);
     const V *v = reinterpret_cast<const V *>(static_cast<const uint8_t *>(p.v) + t * p.ldv);
     V *kc = static_cast<V *>(p.kc), *vc = static_cast<V *>(p.vc);
-    for (int i = lane; i < n; i += 32) {
-        const int h = i / per;
-        const int64_t to = (((((int64_t)page * p.Hkv + h) << p.page_shift) + at) * per) + (i - h * per);
-        kc[to] = k[i];
-        vc[to] = v[i];
+    // loads of eight vectors go before their stores (the compiler may not swap them)
+    for (int i0 = lane; i0 < n; i0 += 128) {
+        V x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 32;
+            if (i < n) {
+                x[u] = k[i];
+                y[u] = v[i];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 32;
+            if (i >= n) break;
+            const int h = i / per;
+            const int64_t to = (((((int64_t)page * p.Hkv + h) << p.page_shift) + at) * per) + (i - h * per);
+            kc[to] = x[u];
+            vc[to] = y[u];
+        }
     }
 }
 
