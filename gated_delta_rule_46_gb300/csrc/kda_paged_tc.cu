@@ -90,6 +90,14 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead)
     return (ptx::sdesc_kmajor_sw128(addr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)((lead >> 4) & 0x3FFF) << 16);
 }
 
+// Eight bf16 from any even address.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p) {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __bfloat16_as_ushort(p[i]);
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
 // 16 values per lane, combined over the warp: lane i ends with value i / 2.
 template <typename Op>
 __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
@@ -243,11 +251,14 @@ __global__ void __launch_bounds__(384, 1)
                 const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[t & 7]);
                 const int left = len - (int)(i * TILE);
                 if (left < TILE || __popc(mask) < pieces) {
-                    for (int r = 0; r < TILE; ++r) {
+                    // 16 bytes a lane and step, from the first row that may be without a token on
+                    const int from = __popc(mask) < pieces ? 0 : min(max(left, 0), TILE);
+                    for (int j = from * 8 + lane; j < TILE * 8; j += 32) {
+                        const int r = j >> 3;
                         if (r < left && (mask >> (r / rows) & 1)) continue;
-                        if (lane < 8 * HALVES)
-                            *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + (lane >> 3) * kSub + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + h * kSub + j * 16) = make_uint4(0, 0, 0, 0);
                     }
                     ptx::fence_async_smem();
                 }
@@ -257,6 +268,7 @@ __global__ void __launch_bounds__(384, 1)
         }
     } else if (warp == 3) {                                       // ---- Q
         int item_no = 0;
+        const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
@@ -264,13 +276,22 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
-            // two channels per lane and step (q rows may start on any even address)
-            for (int j = lane; j < HB * D / 2; j += 32) {
-                const int h = j / (D / 2), c = (j % (D / 2)) * 2;
-                uint32_t u = 0;
-                if (h < hb)
-                    u = (uint32_t)__bfloat16_as_ushort(q[h * D + c]) | (uint32_t)__bfloat16_as_ushort(q[h * D + c + 1]) << 16;
-                *reinterpret_cast<uint32_t *>(dst + (c >> 6) * (HB * 128) + swz(h, (c & 63) >> 3) + (c & 7) * 2) = u;
+            // eight channels per lane and step, all loads first
+            constexpr int PER = HB * D / 256;
+            uint4 u[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int j = lane + i * 32, h = j / (D / 8);
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (h < hb) {
+                    if (q16) u[i] = *reinterpret_cast<const uint4 *>(q + j * 8);
+                    else u[i] = load8(q + j * 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int j = lane + i * 32, h = j / (D / 8), c = j % (D / 8);
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * (HB * 128) + swz(h, c & 7)) = u[i];
             }
             ptx::fence_async_smem();
             warp_arrive(&bar[QFULL + (item_no & 1)]);

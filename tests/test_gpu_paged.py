@@ -279,3 +279,33 @@ def test_refusals():
         paged_append(k, k, kc[:, :1].contiguous(), vc, table, n)
     with pytest.raises(KDAError):
         paged_append(k[:0].expand(0, 2, 64), k[:0], kc, vc, table, n)      # one token per sequence, none given
+
+
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 20)])
+def test_query_rows_off_16_byte_boundaries(d, G):
+    dev = need_gpu()
+    lens = [300, 77]
+    q, kc, vc, table = _cache(lens, 2, G, d, 16, BF, seed=15)
+    wide = torch.zeros(2, 2 * G * d + 5, dtype=BF, device=dev)
+    wide[:, 3:3 + 2 * G * d] = q.reshape(2, -1).to(dev)
+    view = wide[:, 3:3 + 2 * G * d].unflatten(1, (2 * G, d))
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    out, lse = paged_decode(view, kc.to(dev), vc.to(dev), table.to(dev), n, return_lse=True)
+    ro, rl = ref.paged(q, kc, vc, table, lens, d ** -0.5)
+    ref.close("out", out, ro)
+    ref.close("lse", lse, rl)
+
+
+@pytest.mark.parametrize("ps", [8, 16, 64])
+def test_one_bad_page_among_good_ones(ps):
+    """A page outside the cache in the middle of a tile, V garbage in the slot that held its place before."""
+    dev = need_gpu()
+    lens = [512, 512]
+    q, kc, vc, table = _cache(lens, 2, 4, 128, ps, BF, seed=16)
+    vc[torch.isnan(vc)] = math.inf
+    for j in (1, 128 // ps + 1, 3):
+        table[0, j] = -1
+    ro, rl = ref.paged(q, kc, vc, table, lens, 128 ** -0.5)
+    out, lse = _decode(q, kc, vc, table, lens, dev)
+    ref.close("out", out, ro)
+    ref.close("lse", lse, rl)
