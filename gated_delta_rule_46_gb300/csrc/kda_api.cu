@@ -35,6 +35,7 @@ cudaError_t launch_prefill_tc_logdecay(const void *q, const void *k, const void 
                                        void *workspace, size_t workspace_bytes, cudaStream_t st);
 int prefill_tc_launches(int64_t total, int num_seqs, int H, size_t workspace_bytes);
 void set_test_expire(int mask);
+void set_layers_expire(int mask);
 size_t segment_map_workspace_bytes(int64_t total, int num_seqs, int H);
 cudaError_t launch_segment_map(const void *q, const void *k, const void *v, const void *z,
                                const float *A, const float *beta, const int32_t *cu, int num_seqs,
@@ -263,7 +264,11 @@ kda_status_t kda_state_slots_copy(float *state_pool, int pool_size, const int32_
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
-void kda_testing_expire_next_wait(int kernels) { kda::set_test_expire(kernels); }
+void kda_testing_expire_next_wait(int kernels) {
+    constexpr int kLayers = KDA_TESTING_LINEAR | KDA_TESTING_DECAY | KDA_TESTING_PAGED;
+    kda::set_test_expire(kernels & ~kLayers);
+    kda::set_layers_expire(kernels & kLayers);
+}
 
 size_t kda_segment_map_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,
                                       kda_dtype_t dtype) {

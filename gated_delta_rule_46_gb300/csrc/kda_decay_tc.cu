@@ -25,6 +25,7 @@
 
 #include "kda_decay.cuh"
 #include "kda_tc_util.cuh"
+#include "kda_testing.h"
 #include "kda_tmap.cuh"
 #include "sm100_ptx.cuh"
 
@@ -40,7 +41,6 @@ using namespace tc;
 constexpr int C = 64;
 constexpr int kThreads = 640;
 constexpr long long kWaitBudget = 2000000000LL;   // cycles (about one second)
-constexpr int kWaitTries = 1 << 24;               // attempts of a wait, at least some 20 cycles each
 constexpr long long kDrain = 20000000LL;
 
 // ---- shared memory, bytes from a 1024-aligned base.  Tiles have 128-byte rows
@@ -85,6 +85,7 @@ struct Params {
     const __nv_bfloat16 *v;     // (the values again, for the rare path)
     int64_t ldv;
     const int32_t *order;       // longest-first order of the sequences, or nullptr
+    int expire;                 // test support
 };
 
 // One piece of a chain: tokens [t0, t1) of one head.
@@ -151,14 +152,14 @@ __device__ __forceinline__ int chunks_of(const Params &p, bool tell) {
 
 __device__ __forceinline__ float log2_decay(const Params &p, int head) { return decay_log2(p.log_decay, head); }
 
-// The bounded wait in few instructions (each attempt suspends for a while by
-// itself).  The roles' loops run side by side, so what they cost is instruction
-// fetches as much as issue slots; and a call would spill the state's registers.
+// The bounded wait in few instructions (about a second on the 32-bit clock).
+// The roles' loops run side by side, so what they cost is instruction fetches as
+// much as issue slots; and a call would spill the state's registers.
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t phase) {
-#pragma unroll 1
-    for (int i = 0; i < kWaitTries; ++i)
-        if (ptx::mbar_try_wait(bar, phase & 1)) return true;
-    return false;
+    const unsigned t0 = (unsigned)clock();
+    while (!ptx::mbar_try_wait(bar, phase & 1))
+        if ((unsigned)clock() - t0 > (unsigned)kWaitBudget) return false;
+    return true;
 }
 
 // Wait by all lanes of a warp; false for all if it ran out for any.
@@ -499,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
         float *kw = reinterpret_cast<float *>(sm + L::KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
         int c = 0, s = 0, round = 0;
+        if (p.expire && blockIdx.x == 0)
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bar[L::DSH], 0, kTestWait));
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
             __syncwarp();
@@ -666,7 +669,8 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
              static_cast<__nv_bfloat16 *>(d.out),
              static_cast<const __nv_bfloat16 *>(d.v),
              d.ldv,
-             nullptr};
+             nullptr,
+             take_layers_expire(KDA_TESTING_DECAY)};
     cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);

@@ -88,6 +88,7 @@ struct PagedParams {
     float *lse;
     float *part;                    // partial results (workspace)
     bool lone;                      // no item has more than one tile: nothing to join
+    int expire;                     // test support
     uint32_t *status;
 };
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
@@ -95,6 +96,11 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
 
 // Number of SMs of the current device.
 int sm_count();
+
+// Test support: whether kda_testing_expire_next_wait armed this operator's bit,
+// which is cleared; a kernel so called has CTA 0 fail one wait.
+bool take_layers_expire(int bit);
+constexpr long long kTestWait = 1LL << 21;    // cycles (about a millisecond)
 
 // Launches `kernel` so that its start may overlap the end of the kernel before
 // it in the stream: the kernel calls griddepcontrol.wait before it touches

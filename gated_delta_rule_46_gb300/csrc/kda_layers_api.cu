@@ -4,9 +4,15 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_layers.cuh"
 
 namespace kda {
+static std::atomic<int> g_layers_expire{0};
+void set_layers_expire(int mask) { g_layers_expire.store(mask); }
+bool take_layers_expire(int bit) { return g_layers_expire.fetch_and(~bit) & bit; }
+
 int sm_count() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -168,7 +174,7 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
         return KDA_ERR_INVALID_ARG;
     kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
                              seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
-                             static_cast<float *>(workspace), false, status};
+                             static_cast<float *>(workspace), false, 0, status};
     return from_cuda(kda::launch_paged_decode(p, d, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 

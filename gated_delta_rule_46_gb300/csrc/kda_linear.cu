@@ -8,6 +8,7 @@
 
 #include "kda_layers.cuh"
 #include "kda_tc_util.cuh"
+#include "kda_testing.h"
 #include "kda_tmap.cuh"
 #include "sm100_ptx.cuh"
 
@@ -43,6 +44,7 @@ struct Tail {   // what the epilogue needs
     void *out;
     int M, N, K;
     uint32_t *status;
+    int expire;           // test support
 };
 
 // ---------------------------------------------------------------------------
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     } else if (warp == 1) {
         if (ptx::elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_f32(128, p.NT);
-            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            if (p.t.expire && blockIdx.x + blockIdx.y == 0) ok = ptx::mbar_wait(&done, 0, kTestWait);
+            for (int kb = kb0, i = 0; kb < kb1 && ok; ++kb, ++i) {
                 const int s = i % p.stages;
                 if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kWaitBudget)) { ok = false; break; }
                 ptx::tc_fence_after_sync();
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
                 mma_k<4>(tmem, a, 0, a + kABytes, 0, idesc, i > 0);
                 ptx::mma_commit(&empty[s]);
             }
-            ptx::mma_commit(&done);
+            if (ok) ptx::mma_commit(&done);
         }
     } else if (LOAD && warp >= 6) {
         const int tid = threadIdx.x - 192, chunks = (128 + p.NT) * 8;
@@ -349,6 +352,7 @@ __global__ void __launch_bounds__(320)
         if (rank == 0 && ptx::elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_f32(256, BN);
             int it = 0, n = 0;
+            if (p.t.expire && pair == 0) ok = ptx::mbar_wait(&tfull[0], 0, kTestWait);
             for (int i = pair; i < tiles && ok; i += pairs, ++n) {
                 const int b = n & 1;
                 if (n >= 2 && !ptx::mbar_wait_cluster(&tempty[b], ((n >> 1) - 1) & 1, kWaitBudget)) { ok = false; break; }
@@ -480,7 +484,7 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
         !make_map_2d(&mo, p.out, !F32, p.M, p.N, p.N * eb, 128) ||
         !make_map_2d(&mr, p.residual ? p.residual : p.out, !F32, p.M, p.N, p.N * eb, 128))
         return cudaErrorInvalidValue;
-    PairParams pp{{p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status}, (int)((p.M + 255) / 256),
+    PairParams pp{{p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status, take_layers_expire(KDA_TESTING_LINEAR)}, (int)((p.M + 255) / 256),
                   (int)((p.N + BN - 1) / BN), 8};
     auto *kernel = linear_pair_kernel<ACT, F32, BN>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
@@ -493,7 +497,7 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
 template <int ACT, bool F32, int LOAD>
 cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     RowsParams rp{};
-    rp.t = {p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status};
+    rp.t = {p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status, take_layers_expire(KDA_TESTING_LINEAR)};
     rp.x = p.x;
     rp.w = p.w;
     rp.ldx = p.ldx;

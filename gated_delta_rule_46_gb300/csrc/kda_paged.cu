@@ -8,6 +8,7 @@
 // the whole gives out = a / l, lse = m + log l.
 #include "kda_paged.cuh"
 #include "kda_tc_util.cuh"
+#include "kda_testing.h"
 #include "sm100_ptx.cuh"
 
 namespace kda {
@@ -349,6 +350,7 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
     if (!use_tc(p, d, bf16)) return bf16 ? paged_dispatch<__nv_bfloat16>(p, d, st) : paged_dispatch<float>(p, d, st);
     const int HB = heads_tc(p.G), grid = grid_tc(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
     PagedParams pt = p;
+    pt.expire = take_layers_expire(KDA_TESTING_PAGED);
     pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc;
     const cudaError_t e = launch_paged_decode_tc(pt, d, HB, grid, st);
     if (e != cudaSuccess) return e;

@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 return true;
             };
-            ok = scores(0);
+            if (p.expire && blockIdx.x == 0) ok = ptx::mbar_wait(&bar[PVD], 0, kTestWait);
+            ok = ok && scores(0);
             for (int t = 0; t < total && ok; ++t) {
                 if (t + 1 < total && !scores(t + 1)) { ok = false; break; }
                 const int b = t & 1, s = t % NS;

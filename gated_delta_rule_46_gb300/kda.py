@@ -21,6 +21,8 @@ KDA_F32, KDA_BF16 = 0, 1
 # kernels of the tensor-core prefill, as named by include/kda_testing.h
 KDA_TESTING_FUSED, KDA_TESTING_INTRA, KDA_TESTING_SEGMENT, KDA_TESTING_SCAN, KDA_TESTING_STATE = (
     1, 2, 4, 8, 16)
+# and of the operators in include/kda_layers.h
+KDA_TESTING_LINEAR, KDA_TESTING_DECAY, KDA_TESTING_PAGED = 32, 64, 128
 
 _lock = threading.Lock()
 _lib = None
@@ -362,6 +364,7 @@ def chunk_prefill_noalloc(q, k, v, z, A, beta, cu_seqlens, initial_state=None, f
 
 def testing_expire_next_wait(kernels: int) -> None:
     """Test support (include/kda_testing.h): the next bf16 d=128 prefill call's
+    (or the next tensor-core linear's, decay_prefill's, paged_decode's)
     kernels named by the KDA_TESTING_* mask `kernels` see one bounded wait in
     their first CTA run out, and take their timeout path."""
     lib().kda_testing_expire_next_wait(int(kernels))

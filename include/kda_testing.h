@@ -10,13 +10,17 @@
 extern "C" {
 #endif
 
-/* Bits of kda_testing_expire_next_wait(): the kernels of the tensor-core
- * prefill whose first CTA is to see a wait run out. */
+/* Bits of kda_testing_expire_next_wait(): the kernels whose first CTA is to see
+ * a wait run out; of the tensor-core prefill: */
 #define KDA_TESTING_FUSED 1        /* one-kernel plan (many chains) */
 #define KDA_TESTING_INTRA 2        /* chunk-parallel kernel of the few-chain plans */
 #define KDA_TESTING_SEGMENT 4      /* segment maps of the segment-scan plan */
 #define KDA_TESTING_SCAN 8         /* the scan over segments */
 #define KDA_TESTING_STATE 16       /* state pass of the few-chain plans */
+/* and of the operators in kda_layers.h, where they run on the tensor cores: */
+#define KDA_TESTING_LINEAR 32      /* kda_linear */
+#define KDA_TESTING_DECAY 64       /* kda_decay_prefill */
+#define KDA_TESTING_PAGED 128      /* kda_paged_decode */
 
 /*
  * kda_testing_expire_next_wait -- arms a simulated wait expiry for the next
@@ -30,6 +34,9 @@ extern "C" {
  * tensor-core operations in flight complete, frees its tensor memory and
  * returns, leaving that call's outputs incomplete and the CUDA context
  * usable.  kernels = 0 disarms.  Not for production use.
+ * The last three bits are consumed, each by itself, by the next tensor-core
+ * call of their operator; there one role of the kernel gives up and the others'
+ * waits for it run out in earnest, after about a second.
  */
 void kda_testing_expire_next_wait(int kernels);
 
