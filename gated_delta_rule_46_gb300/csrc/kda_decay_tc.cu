@@ -265,156 +265,156 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item x;
     // 96 registers a thread at launch; of the five warpgroups' 480 the state's two take 120 each
     if (warp < 4) {
-    ptx::regs_dec<80>();
-    if (warp == 2) {                                              // ---- loads, and the state's product
-        // one thread does whichever of the two can go ahead
-        const int total = chunks_of<D, OUT>(p, true);
-        if (ptx::elect_one()) {
-            const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
-            const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
-            int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
-            int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
-            int t = 0, t1 = 0, col0 = 0;
-            long long since = clock64();
-            while (dc < total) {
-                bool did = false;
-                if (lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
-                    while (t >= t1) {
-                        walk.next(p, x, false);
-                        t = x.t0;
-                        t1 = x.t1;
-                        col0 = x.head * D;
-                    }
-                    uint64_t *full = &bar[L::LD + ls];
-                    uint8_t *st = sm + ls * L::stage;
-                    ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
-#pragma unroll 1
-                    for (int h = 0; h < HV; ++h) {
-                        const int col = col0 + h * 64;
-                        ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, t, full);
-                        if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, t, full);
-                        ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, t, full);
-                    }
-                    t += C;
-                    ++lc;
-                    if (++ls == NS) { ls = 0; ++lp; }
-                    did = true;
-                }
-                if (ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
-                    (half == 1 || dc == 0 || ptx::mbar_test(&bar[L::DSFREE], (dc - 1) & 1))) {
-                    ptx::tc_fence_after_sync();
-                    const uint64_t a = dt + half * (4096 >> 4);
-                    const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
-#pragma unroll 2
-                    for (int e = 0; e < 6; ++e)
-                        ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
-                                         id, half > 0 || e > 0);
-                    ptx::mma_commit(&bar[L::DSH + half]);
-                    if (half == 1) {
-                        ptx::mma_commit(&bar[L::DS]);
-                        ptx::mma_commit(&bar[L::FREE + ds]);
-                        ++dc;
-                        if (++ds == NS) { ds = 0; ++dp; }
-                    }
-                    half ^= 1;
-                    did = true;
-                }
-                const long long now = clock64();
-                if (did) since = now;
-                else if (now - since > kWaitBudget) { ok = false; break; }
-            }
-        }
-    } else if (warp < 2) {                                        // ---- P: thread = token of the chunk
-        if (OUT) {
-            const int i = threadIdx.x;
-            int c = 0;
-            while (ok && walk.next(p, x, false)) {
-                const float l2 = log2_decay(p, x.head);
-                for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
-                    const int b = c & 1;
-                    // the output products of two chunks ago have read this buffer, and so has their output if it had to
-                    ok = warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
-                    if (!ok) break;
-                    ptx::tc_fence_after_sync();
-                    uint8_t *sp = sm + L::P + b * kTile;
-                    // (columns 32-63 of rows 0-31 are never written: zero from the start)
-#pragma unroll 1
-                    for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 32) {
-                        float d[32];
-                        ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
-                        const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
-                        if (j0 == 32 * warp)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) d[e] = e <= lane ? d[e] : 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) st_chunk(sp, swz(i, (j0 + e) >> 3), d + e);
-                    }
-                    ptx::fence_async_smem();
-                    ptx::tc_fence_before_sync();
-                    warp_arrive(&bar[L::PREADY + b]);
-                }
-            }
-        }
-    } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
-        const int total = OUT ? chunks_of<D, OUT>(p, false) : 0;
-        if (OUT && ptx::elect_one()) {
-            const uint32_t id = ptx::idesc_bf16_f32(128, 64);
-            int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
-            for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
-                const int b = c & 1, phase = (c >> 1) & 1;
-                const uint32_t st = base + s * L::stage;
-                if (c >= 0) {
-                    if (!wait_on(&bar[L::SREADY], c & 1) ||
-                        (c >= 2 && !wait_on(&bar[L::OFREE + b], phase ^ 1))) { ok = false; break; }
-                    ptx::tc_fence_after_sync();
-                    const uint64_t q = ptx::sdesc_kmajor_sw128(st + L::q);
-#pragma unroll 2
-                    for (int k = 0; k < D / 16; ++k)
-                        ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * L::half + (k & 3) * 32) >> 4),
-                                         id, k > 0);
-                    ptx::mma_commit(&bar[L::QS]);
-                    if (!wait_on(&bar[L::PREADY + b], phase)) { ok = false; break; }
-                    ptx::tc_fence_after_sync();
-                }
-                // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
-                // load may be waiting for this very chunk's stage.
-                bool todo = c + 1 < total;
-#pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (todo && (pass == 1 || c < 0 || ptx::mbar_test(&bar[L::LD + ns], np & 1))) {
-                        todo = false;
-                        if (!wait_on(&bar[L::LD + ns], np)) { ok = false; break; }
-                        ptx::tc_fence_after_sync();
-                        const uint32_t sn = base + ns * L::stage;
-                        // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
-                        const uint64_t q = ptx::sdesc_kmajor_sw128(sn + L::q), kd = ptx::sdesc_kmajor_sw128(sn + L::k);
-#pragma unroll 2
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
-                            ptx::mma_bf16_ss(tmem + TM_P, q + at, kd + at, id, k > 0);
+        ptx::regs_dec<80>();
+        if (warp == 2) {                                              // ---- loads, and the state's product
+            // one thread does whichever of the two can go ahead
+            const int total = chunks_of<D, OUT>(p, true);
+            if (ptx::elect_one()) {
+                const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
+                const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
+                int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
+                int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
+                int t = 0, t1 = 0, col0 = 0;
+                long long since = clock64();
+                while (dc < total) {
+                    bool did = false;
+                    if (lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
+                        while (t >= t1) {
+                            walk.next(p, x, false);
+                            t = x.t0;
+                            t1 = x.t1;
+                            col0 = x.head * D;
                         }
-                        ptx::mma_commit(&bar[L::QK + (b ^ 1)]);
+                        uint64_t *full = &bar[L::LD + ls];
+                        uint8_t *st = sm + ls * L::stage;
+                        ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
+    #pragma unroll 1
+                        for (int h = 0; h < HV; ++h) {
+                            const int col = col0 + h * 64;
+                            ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, t, full);
+                            if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, t, full);
+                            ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, t, full);
+                        }
+                        t += C;
+                        ++lc;
+                        if (++ls == NS) { ls = 0; ++lp; }
+                        did = true;
                     }
-                    if (c < 0 || pass == 1) continue;
-                    if (!wait_on(&bar[L::TF + 2 * s], sp) ||                  // (V's tail is clean)
-                        !wait_on(&bar[L::TF + 2 * s + 1], sp)) { ok = false; break; }
-                    ptx::tc_fence_after_sync();
-                    const uint64_t a = sdesc_mn_sw128(st + L::v, kTile), pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
-#pragma unroll 2
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
-                    ptx::mma_commit(&bar[L::OD + b]);
-                    ptx::mma_commit(&bar[L::FREE + s]);
+                    if (ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
+                        (half == 1 || dc == 0 || ptx::mbar_test(&bar[L::DSFREE], (dc - 1) & 1))) {
+                        ptx::tc_fence_after_sync();
+                        const uint64_t a = dt + half * (4096 >> 4);
+                        const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
+    #pragma unroll 2
+                        for (int e = 0; e < 6; ++e)
+                            ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
+                                             id, half > 0 || e > 0);
+                        ptx::mma_commit(&bar[L::DSH + half]);
+                        if (half == 1) {
+                            ptx::mma_commit(&bar[L::DS]);
+                            ptx::mma_commit(&bar[L::FREE + ds]);
+                            ++dc;
+                            if (++ds == NS) { ds = 0; ++dp; }
+                        }
+                        half ^= 1;
+                        did = true;
+                    }
+                    const long long now = clock64();
+                    if (did) since = now;
+                    else if (now - since > kWaitBudget) { ok = false; break; }
                 }
-                s = ns;
-                sp = np;
-                if (++ns == NS) { ns = 0; ++np; }
+            }
+        } else if (warp < 2) {                                        // ---- P: thread = token of the chunk
+            if (OUT) {
+                const int i = threadIdx.x;
+                int c = 0;
+                while (ok && walk.next(p, x, false)) {
+                    const float l2 = log2_decay(p, x.head);
+                    for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
+                        const int b = c & 1;
+                        // the output products of two chunks ago have read this buffer, and so has their output if it had to
+                        ok = warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
+                        if (!ok) break;
+                        ptx::tc_fence_after_sync();
+                        uint8_t *sp = sm + L::P + b * kTile;
+                        // (columns 32-63 of rows 0-31 are never written: zero from the start)
+    #pragma unroll 1
+                        for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 32) {
+                            float d[32];
+                            ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
+                            const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
+                            ptx::tmem_ld_wait();
+    #pragma unroll
+                            for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
+                            if (j0 == 32 * warp)
+    #pragma unroll
+                                for (int e = 0; e < 32; ++e) d[e] = e <= lane ? d[e] : 0.f;
+    #pragma unroll
+                            for (int e = 0; e < 32; e += 8) st_chunk(sp, swz(i, (j0 + e) >> 3), d + e);
+                        }
+                        ptx::fence_async_smem();
+                        ptx::tc_fence_before_sync();
+                        warp_arrive(&bar[L::PREADY + b]);
+                    }
+                }
+            }
+        } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
+            const int total = OUT ? chunks_of<D, OUT>(p, false) : 0;
+            if (OUT && ptx::elect_one()) {
+                const uint32_t id = ptx::idesc_bf16_f32(128, 64);
+                int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
+                for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
+                    const int b = c & 1, phase = (c >> 1) & 1;
+                    const uint32_t st = base + s * L::stage;
+                    if (c >= 0) {
+                        if (!wait_on(&bar[L::SREADY], c & 1) ||
+                            (c >= 2 && !wait_on(&bar[L::OFREE + b], phase ^ 1))) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                        const uint64_t q = ptx::sdesc_kmajor_sw128(st + L::q);
+    #pragma unroll 2
+                        for (int k = 0; k < D / 16; ++k)
+                            ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * L::half + (k & 3) * 32) >> 4),
+                                             id, k > 0);
+                        ptx::mma_commit(&bar[L::QS]);
+                        if (!wait_on(&bar[L::PREADY + b], phase)) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                    }
+                    // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
+                    // load may be waiting for this very chunk's stage.
+                    bool todo = c + 1 < total;
+    #pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (todo && (pass == 1 || c < 0 || ptx::mbar_test(&bar[L::LD + ns], np & 1))) {
+                            todo = false;
+                            if (!wait_on(&bar[L::LD + ns], np)) { ok = false; break; }
+                            ptx::tc_fence_after_sync();
+                            const uint32_t sn = base + ns * L::stage;
+                            // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
+                            const uint64_t q = ptx::sdesc_kmajor_sw128(sn + L::q), kd = ptx::sdesc_kmajor_sw128(sn + L::k);
+    #pragma unroll 2
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
+                                ptx::mma_bf16_ss(tmem + TM_P, q + at, kd + at, id, k > 0);
+                            }
+                            ptx::mma_commit(&bar[L::QK + (b ^ 1)]);
+                        }
+                        if (c < 0 || pass == 1) continue;
+                        if (!wait_on(&bar[L::TF + 2 * s], sp) ||                  // (V's tail is clean)
+                            !wait_on(&bar[L::TF + 2 * s + 1], sp)) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                        const uint64_t a = sdesc_mn_sw128(st + L::v, kTile), pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
+    #pragma unroll 2
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
+                        ptx::mma_commit(&bar[L::OD + b]);
+                        ptx::mma_commit(&bar[L::FREE + s]);
+                    }
+                    s = ns;
+                    sp = np;
+                    if (++ns == NS) { ns = 0; ++np; }
+                }
             }
         }
-    }
     } else if (warp < 8) {                                        // ---- the output
         ptx::regs_dec<80>();
         if (OUT) {
@@ -560,70 +560,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {                                                      // ---- the state: lane = value channel
         ptx::regs_inc<120>();
         if ((warp & 3) * 32 < D) {
-        constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
-        const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;
-        const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
-        const uint32_t at = tmem + ((uint32_t)q << 21);
-        int c = 0;
-        while (ok && walk.next(p, x, false)) {
-            const float l2 = log2_decay(p, x.head);
-            const float *from = x.from;
-            float s[KC];
-#pragma unroll
-            for (int e = 0; e < KC; ++e) s[e] = from ? from[mine + e * D] : 0.f;
-            auto copy_out = [&](int e) {       // 16 channels as bf16 pairs
-                uint32_t u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = pack_bf16(s[e + 2 * i], s[e + 2 * i + 1]);
-                ptx::tmem_st8(at + TM_S + (k0 + e) / 2, u);
-            };
-            const int t0 = x.t0, t1 = x.t1;
-            if (OUT && t1 > t0) {
-                if (c > 0) ok = warp_wait(&bar[L::QS], c - 1);
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
-#pragma unroll
-                for (int e = 0; e < KC; e += 16) copy_out(e);
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before_sync();
-                warp_arrive(&bar[L::SREADY]);
-            }
-            for (int t = t0; t < t1; t += C, ++c) {
-                const bool more = OUT && t + C < t1;
-                const float f = exp2f(l2 * (float)min(t1 - t, C));
-                ok = warp_wait(&bar[L::DS], c);
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
-                // 32 columns at a time: the next product may overwrite them as soon as the last have been read
-#pragma unroll
-                for (int e = 0; e < KC; e += 32) {
-                    float d[32];
-                    ptx::tmem_ld16(at + TM_DS + k0 + e, *reinterpret_cast<float(*)[16]>(d));
-                    ptx::tmem_ld16(at + TM_DS + k0 + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
-                    ptx::tmem_ld_wait();
-                    if (e + 32 == KC) {
-                        ptx::tc_fence_before_sync();
-                        warp_arrive(&bar[L::DSFREE]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
-                }
-                if (more) {
-                    ok = warp_wait(&bar[L::QS], c);
+            constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
+            const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;
+            const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
+            const uint32_t at = tmem + ((uint32_t)q << 21);
+            int c = 0;
+            while (ok && walk.next(p, x, false)) {
+                const float l2 = log2_decay(p, x.head);
+                const float *from = x.from;
+                float s[KC];
+    #pragma unroll
+                for (int e = 0; e < KC; ++e) s[e] = from ? from[mine + e * D] : 0.f;
+                auto copy_out = [&](int e) {       // 16 channels as bf16 pairs
+                    uint32_t u[8];
+    #pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = pack_bf16(s[e + 2 * i], s[e + 2 * i + 1]);
+                    ptx::tmem_st8(at + TM_S + (k0 + e) / 2, u);
+                };
+                const int t0 = x.t0, t1 = x.t1;
+                if (OUT && t1 > t0) {
+                    if (c > 0) ok = warp_wait(&bar[L::QS], c - 1);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
-#pragma unroll
+    #pragma unroll
                     for (int e = 0; e < KC; e += 16) copy_out(e);
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before_sync();
                     warp_arrive(&bar[L::SREADY]);
                 }
+                for (int t = t0; t < t1; t += C, ++c) {
+                    const bool more = OUT && t + C < t1;
+                    const float f = exp2f(l2 * (float)min(t1 - t, C));
+                    ok = warp_wait(&bar[L::DS], c);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    // 32 columns at a time: the next product may overwrite them as soon as the last have been read
+    #pragma unroll
+                    for (int e = 0; e < KC; e += 32) {
+                        float d[32];
+                        ptx::tmem_ld16(at + TM_DS + k0 + e, *reinterpret_cast<float(*)[16]>(d));
+                        ptx::tmem_ld16(at + TM_DS + k0 + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
+                        ptx::tmem_ld_wait();
+                        if (e + 32 == KC) {
+                            ptx::tc_fence_before_sync();
+                            warp_arrive(&bar[L::DSFREE]);
+                        }
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
+                    }
+                    if (more) {
+                        ok = warp_wait(&bar[L::QS], c);
+                        if (!ok) break;
+                        ptx::tc_fence_after_sync();
+    #pragma unroll
+                        for (int e = 0; e < KC; e += 16) copy_out(e);
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before_sync();
+                        warp_arrive(&bar[L::SREADY]);
+                    }
+                }
+                if (!ok) break;
+                if (x.to)
+    #pragma unroll
+                    for (int e = 0; e < KC; ++e) x.to[mine + e * D] = s[e];
             }
-            if (!ok) break;
-            if (x.to)
-#pragma unroll
-                for (int e = 0; e < KC; ++e) x.to[mine + e * D] = s[e];
-        }
         }
     }
     if (!ok) {

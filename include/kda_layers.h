@@ -54,8 +54,9 @@ typedef enum {
  *             as out
  *   out       [M, N] of out_dtype (KDA_BF16 or KDA_F32), dense (written)
  * Products are summed in float32 and rounded once, after the residual.  Any
- * M, N >= 0 and K >= 1 below 2^31; K a multiple of 8 with 16-byte aligned rows
- * runs on the tensor cores, anything else on the CUDA cores.
+ * M, N >= 0 and K >= 1 below 2^31, any row stride and alignment of elements; K a
+ * multiple of 8 with 16-byte aligned rows is loaded by TMA, anything else element
+ * by element.
  */
 kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *bias,
                         const void *residual, void *out, int64_t M, int64_t N, int64_t K,
@@ -76,8 +77,7 @@ size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int 
  *     S_t = exp(log_decay) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
  *   q, k           [total_tokens, H, dk], v [total_tokens, H, dv], of dtype, row
  *                  strides ldq, ldk, ldv
- *   log_decay      [H] float32, device, <= 0 (-inf: no memory); larger values
- *                  are taken as 0
+ *   log_decay      [H] float32, device; <= 0 for a decay, -inf for no memory
  *   cu_seqlens     [num_seqs + 1] int32, device, as for kda_chunk_prefill
  *   initial_state  [num_seqs, H, dk, dv] float32, or NULL for zeros
  *   final_state    [num_seqs, H, dk, dv] float32 (written), or NULL; it may be
@@ -120,8 +120,8 @@ kda_status_t kda_decay_decode(const void *q, int64_t ldq, const void *k, int64_t
  *   cu_seqlens       [num_seqs + 1] int32, device, or NULL for one token per
  *                    sequence (total_tokens = num_seqs)
  * Token t of sequence i goes to position start_pos[i] + t - cu_seqlens[i].
- * page_size is a power of two up to 1024, d in {32, 64, 128}.  A position past the table, or a
- * page id outside the cache, is recorded in *status and skipped.
+ * page_size is a power of two up to 1024, d in {32, 64, 128}.  A position past
+ * the table, or a page id outside the cache, is recorded in *status and skipped.
  */
 kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t ldv, void *k_cache,
                               void *v_cache, int num_pages, int page_size,
