@@ -46,25 +46,26 @@ constexpr long long kDrain = 20000000LL;
 // ---- shared memory, bytes from a 1024-aligned base.  Tiles have 128-byte rows
 // with the 128-byte swizzle; a row of 128 channels is two tiles (halves).
 constexpr uint32_t kTile = C * 128;                       // 64 rows x 64 channels
-template <int D>
+template <int D, bool OUT>
 struct Lay {
     static constexpr int HV = D / 64;                     // halves
-    static constexpr int NS = D == 128 ? 3 : 6;           // stages of loads
-    static constexpr uint32_t half = 2 * kTile;           // from Q0 to Q1, from K0 to K1
-    static constexpr uint32_t q = 0, k = kTile, v = HV * half;            // in a stage: [Q0 K0 (Q1 K1) V0 (V1)]
-    static constexpr uint32_t stage = 3 * HV * kTile;
+    static constexpr int NS = (OUT ? 3 : 4) * (2 / HV);   // stages of loads
+    static constexpr int NB = OUT ? 1 : 2;                // buffers of the terms and of their product
+    static constexpr uint32_t half = (OUT ? 2 : 1) * kTile;               // from Q0 to Q1, from K0 to K1
+    static constexpr uint32_t q = 0, k = OUT ? kTile : 0, v = HV * half;  // in a stage: [(Q0) K0 (Q1) (K1) V0 (V1)]
+    static constexpr uint32_t stage = v + HV * kTile;
     static constexpr uint32_t T = NS * stage;             // three terms of the decayed keys, [token][channel]
     static constexpr uint32_t term = HV * kTile;
-    static constexpr uint32_t P = T + 3 * term;           // P [i][j], two buffers
+    static constexpr uint32_t P = T + NB * 3 * term;      // P [i][j], two buffers
     static constexpr uint32_t O = P + 2 * kTile;          // output staging [token][dv]
     static constexpr uint32_t PW = O + HV * kTile;        // lambda^1 .. lambda^64, of two items in turn
     static constexpr uint32_t KW = PW + 2 * C * 4;        // lambda^0 .. lambda^63, one copy for each key warp
-    static constexpr uint32_t bytes = KW + 4 * C * 4 + 1024;
+    static constexpr uint32_t bytes = (OUT ? KW + 4 * C * 4 : P) + 1024;
     static_assert(bytes <= 232448 - 256, "shared memory");
     // with 64 channels the MMAs' upper 64 rows (M = 128) are whatever lies one tile on: rows that no one reads
     // barriers
     enum Bar { LD, FREE = LD + NS, QK = FREE + NS, PREADY = QK + 2, OD = PREADY + 2, OFREE = OD + 2, QS = OFREE + 2, SREADY,
-               TF, DSH = TF + 2 * NS, DS = DSH + 2, DSFREE, NBAR };
+               TF, DSH = TF + 2 * NS, DS = DSH + 2 * NB, DSFREE = DS + NB, NBAR = DSFREE + NB };
 };
 
 // ---- tensor memory columns (512)
@@ -72,8 +73,7 @@ constexpr uint32_t TM_P = 0;                                                  //
 constexpr uint32_t TM_S = 64;                                                 // S^T as bf16 pairs: lane = dv, 64 columns
 __device__ __forceinline__ uint32_t tm_qs(int b) { return 128 + b * 128; }    // S^T Q^T
 __device__ __forceinline__ uint32_t tm_pv(int b) { return 192 + b * 128; }    // V^T P^T
-constexpr uint32_t TM_DS = 384;                                               // what the chunk adds to S^T
-
+__device__ __forceinline__ uint32_t tm_ds(int b) { return 384 - b * 128; }    // what the chunk adds to S^T
 
 struct Params {
     DecaySegs g;
@@ -222,8 +222,8 @@ template <int D, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Params p) {
-    using L = Lay<D>;
-    constexpr int NS = L::NS, HV = L::HV;
+    using L = Lay<D, OUT>;
+    constexpr int NS = L::NS, HV = L::HV, NB = L::NB;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[L::NBAR];
     __shared__ uint32_t s_tmem, s_abort;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= L::FREE && i < L::QK) n = OUT ? 2 : 1;             // the two issuers
             if (i >= L::PREADY && i < L::OD) n = 2;                     // warps 0, 1
             if ((i >= L::OFREE && i < L::QS) || (i >= L::TF && i < L::DSH)) n = 4;   // the output's, the keys' warps
-            if (i == L::SREADY || i == L::DSFREE) n = 4 * HV;           // the state's warps
+            if (i == L::SREADY || i >= L::DSFREE) n = 4 * HV;           // the state's warps
             ptx::mbar_init(&bar[i], n);
         }
         ptx::fence_mbar_init();
@@ -266,19 +266,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 96 registers a thread at launch; of the five warpgroups' 480 the state's two take 120 each
     if (warp < 4) {
         ptx::regs_dec<80>();
-        if (warp == 2) {                                              // ---- loads, and the state's product
-            // one thread does whichever of the two can go ahead
-            const int total = chunks_of<D, OUT>(p, true);
+        if (warp == 2 || (!OUT && warp == 3)) {                       // ---- loads, and the state's product
+            // one thread does whichever of the two can go ahead; without the output's products, one thread each
+            const bool loads = OUT || warp == 2, mults = OUT || warp == 3;
+            const int total = chunks_of<D, OUT>(p, loads);
             if (ptx::elect_one()) {
                 const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
                 const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
                 int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
                 int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
+                int b = 0, bp = 0;                                    // the product's buffer and round
                 int t = 0, t1 = 0, col0 = 0;
                 long long since = clock64();
-                while (dc < total) {
+                while ((mults ? dc : lc) < total) {
                     bool did = false;
-                    if (lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
+                    if (loads && lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
                         while (t >= t1) {
                             walk.next(p, x, false);
                             t = x.t0;
@@ -300,21 +302,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (++ls == NS) { ls = 0; ++lp; }
                         did = true;
                     }
-                    if (ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
-                        (half == 1 || dc == 0 || ptx::mbar_test(&bar[L::DSFREE], (dc - 1) & 1))) {
+                    if (mults && ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
+                        (half == 1 || bp == 0 || ptx::mbar_test(&bar[L::DSFREE + b], (bp - 1) & 1))) {
                         ptx::tc_fence_after_sync();
-                        const uint64_t a = dt + half * (4096 >> 4);
+                        const uint64_t a = dt + (b * 3 * L::term + half * 4096) / 16;
                         const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
     #pragma unroll 2
                         for (int e = 0; e < 6; ++e)
-                            ptx::mma_bf16_ss(tmem + TM_DS, v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
+                            ptx::mma_bf16_ss(tmem + tm_ds(b), v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
                                              id, half > 0 || e > 0);
-                        ptx::mma_commit(&bar[L::DSH + half]);
+                        ptx::mma_commit(&bar[L::DSH + 2 * b + half]);
                         if (half == 1) {
-                            ptx::mma_commit(&bar[L::DS]);
+                            ptx::mma_commit(&bar[L::DS + b]);
                             ptx::mma_commit(&bar[L::FREE + ds]);
                             ++dc;
                             if (++ds == NS) { ds = 0; ++dp; }
+                            if (++b == NB) { b = 0; ++bp; }
                         }
                         half ^= 1;
                         did = true;
@@ -358,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-        } else if (warp == 3) {                                       // ---- Q K^T, S^T Q^T, V^T P^T
-            const int total = OUT ? chunks_of<D, OUT>(p, false) : 0;
-            if (OUT && ptx::elect_one()) {
+        } else if (OUT && warp == 3) {                                // ---- Q K^T, S^T Q^T, V^T P^T
+            const int total = chunks_of<D, OUT>(p, false);
+            if (ptx::elect_one()) {
                 const uint32_t id = ptx::idesc_bf16_f32(128, 64);
                 int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
                 for (int c = -1; c < total && ok; ++c) {              // (step -1: the first chunk's scores alone)
@@ -415,9 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp < 8) {                                        // ---- the output
+    } else if (OUT && warp < 8) {                                 // ---- the output
         ptx::regs_dec<80>();
-        if (OUT) {
+        {
             const int tid = threadIdx.x - 128, q = warp & 3;
             float *pw = reinterpret_cast<float *>(sm + L::PW);
             uint8_t *so = sm + L::O;
@@ -496,18 +499,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 12) {                                       // ---- the decayed keys in three terms
         ptx::regs_dec<80>();
         constexpr int RP = 128 / (D / 8), NR = 32 / RP;                       // rows at a time; times per half chunk
-        const int tid = threadIdx.x - 256, r0 = tid / (D / 8), ch = tid % (D / 8);   // rows r0, r0 + RP, ...; 16-byte column
+        // both halves of a chunk, or (where no output is written) one half by warps 4-7 and one by 8-11
+        const int th0 = OUT || warp < 8 ? 0 : 1, th1 = OUT || warp >= 8 ? 2 : 1;
+        const int tid = threadIdx.x & 127, r0 = tid / (D / 8), ch = tid % (D / 8);   // rows r0, r0 + RP, ...; 16-byte column
         const uint32_t half = ch >> 3, at0 = swz(r0, ch & 7);                 // (8 rows on: 1024 bytes on)
-        float *kw = reinterpret_cast<float *>(sm + L::KW) + (warp - 8) * C;    // lambda^0 .. lambda^63
+        float *kw = reinterpret_cast<float *>(sm + L::KW) + (warp & 7) * C;    // lambda^0 .. lambda^63
         int c = 0, s = 0, round = 0;
         if (p.expire && blockIdx.x == 0)
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bar[L::DSH], 0, kTestWait));
         while (ok && walk.next(p, x, false)) {
             const float l2 = log2_decay(p, x.head);
-            __syncwarp();
-            kw[lane] = exp2f(l2 * (float)lane);
-            kw[lane + 32] = exp2f(l2 * (float)(lane + 32));
-            __syncwarp();
+            if (OUT) {
+                __syncwarp();
+                kw[lane] = exp2f(l2 * (float)lane);
+                kw[lane + 32] = exp2f(l2 * (float)(lane + 32));
+                __syncwarp();
+            }
             for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
                 const int n = min(t1 - t, C);
                 ok = warp_wait(&bar[L::LD + s], round);
@@ -517,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++s == NS) { s = 0; ++round; }
                 const float *w = kw + max(n - 1 - r0, 0);         // row r0 + RP i: lambda^{n - 1 - r0 - RP i}
                 const int most = max(n - 1 - r0, 0) / RP;
-                const uint8_t *kp = st + L::k + half * L::half + at0;
-                uint8_t *dst = sm + L::T + half * kTile + at0;
+                const uint8_t *kp = st + L::k + half * L::half + at0 + th0 * 4096;
+                uint8_t *dst = sm + L::T + (c & (NB - 1)) * 3 * L::term + half * kTile + at0 + th0 * 4096;
                 if (n < C)                                        // rows of the next sequence
-                    for (int i = 0; i < 2 * NR; ++i)
+                    for (int i = th0 * NR; i < th1 * NR; ++i)
                         if (r0 + RP * i >= n)
                             *reinterpret_cast<uint4 *>(st + L::v + half * kTile + at0 + i * RP * 128) = make_uint4(0, 0, 0, 0);
                 // The loads of the next 32 tokens go before the stores of these: beside the MMAs' own reads a load
@@ -529,19 +536,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + i * RP * 128);
 #pragma unroll 1
-                for (int th = 0; th < 2; ++th) {                  // 32 tokens at a time
+                for (int th = th0; th < th1; ++th) {              // 32 tokens at a time
                     uint4 k[NR];
                     float wi[NR];
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         k[i] = kn[i];
-                        wi[i] = w[-RP * min(th * NR + i, most)];
+                        wi[i] = OUT ? w[-RP * min(th * NR + i, most)]
+                                    : exp2f(l2 * (float)max(n - 1 - r0 - RP * (th * NR + i), 0));
                         if (r0 + RP * (th * NR + i) >= n) k[i] = make_uint4(0, 0, 0, 0);
                     }
-                    if (th == 0)
+                    if (OUT && th == 0)
 #pragma unroll
                         for (int i = 0; i < NR; ++i) kn[i] = *reinterpret_cast<const uint4 *>(kp + (i + NR) * RP * 128);
-                    if (c > 0 && !(ok = warp_wait(&bar[L::DSH + th], c - 1))) break;
+                    if (c >= NB && !(ok = warp_wait(&bar[L::DSH + 2 * (c & (NB - 1)) + th], c / NB - 1))) break;
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         uint4 t1, t2, t3;
@@ -591,19 +599,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = t0; t < t1; t += C, ++c) {
                     const bool more = OUT && t + C < t1;
                     const float f = exp2f(l2 * (float)min(t1 - t, C));
-                    ok = warp_wait(&bar[L::DS], c);
+                    ok = warp_wait(&bar[L::DS + (c & (NB - 1))], c / NB);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
+                    const uint32_t ds = at + tm_ds(c & (NB - 1)) + k0;
                     // 32 columns at a time: the next product may overwrite them as soon as the last have been read
     #pragma unroll
                     for (int e = 0; e < KC; e += 32) {
                         float d[32];
-                        ptx::tmem_ld16(at + TM_DS + k0 + e, *reinterpret_cast<float(*)[16]>(d));
-                        ptx::tmem_ld16(at + TM_DS + k0 + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
+                        ptx::tmem_ld16(ds + e, *reinterpret_cast<float(*)[16]>(d));
+                        ptx::tmem_ld16(ds + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
                         ptx::tmem_ld_wait();
                         if (e + 32 == KC) {
                             ptx::tc_fence_before_sync();
-                            warp_arrive(&bar[L::DSFREE]);
+                            warp_arrive(&bar[L::DSFREE + (c & (NB - 1))]);
                         }
     #pragma unroll
                         for (int i = 0; i < 32; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
@@ -654,7 +663,7 @@ size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D) {
 
 template <int D>
 static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t workspace_bytes, cudaStream_t st) {
-    constexpr uint32_t kSmem = Lay<D>::bytes;
+    constexpr uint32_t kSmem = Lay<D, true>::bytes, kSmemState = Lay<D, false>::bytes;
     CUtensorMap mq, mk, mv, mo;
     const uint64_t T = (uint64_t)d.total, cols = (uint64_t)d.H * D;
     if (!make_map_2d(&mq, d.q, true, T, cols, d.ldq * 2, C) || !make_map_2d(&mk, d.k, true, T, cols, d.ldk * 2, C) ||
@@ -673,7 +682,7 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
              take_layers_expire(KDA_TESTING_DECAY)};
     cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemState);
     if (e != cudaSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);
@@ -685,7 +694,7 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
         p.g.cap = (int)(d.total / len) + d.num_seqs;
         const int64_t items = (int64_t)p.g.cap * d.H;
         const dim3 grid((unsigned)(items < sms ? items : sms));
-        if ((e = launch_dependent(decay_chunk_kernel<D, false>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
+        if ((e = launch_dependent(decay_chunk_kernel<D, false>, grid, kThreads, kSmemState, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
             return e;
         if ((e = launch_decay_segments(p.g, d.log_decay, d.init, D, D, st)) != cudaSuccess) return e;
         return launch_dependent(decay_chunk_kernel<D, true>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
