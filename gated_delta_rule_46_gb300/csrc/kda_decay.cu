@@ -325,11 +325,12 @@ __global__ void __launch_bounds__(256, 2) decay_simt_kernel(const DecaySimtParam
 }
 
 constexpr int kSimtChunk = 32;
+constexpr SegmentCost kSimtCost{kSimtChunk, 2, 2.25f, 2.f};
 // CTAs that run at a time (two per SM), by blocks of up to 64 value channels
 static int simt_slots(int dv) { return 2 * sm_count() / (dv > 64 ? 2 : 1); }
 
 size_t decay_prefill_simt_workspace(int64_t total, int N, int H, int dk, int dv) {
-    return decay_cells_bytes(total, N, H, decay_segment_tokens(total, N, H, simt_slots(dv), kSimtChunk), dk, dv);
+    return decay_cells_bytes(total, N, H, decay_segment_tokens(total, N, H, simt_slots(dv), kSimtCost), dk, dv);
 }
 
 template <typename T, int DK, int JB>
@@ -373,7 +374,7 @@ cudaError_t launch_decay_prefill_simt(const DecayParams &d, int dk, int dv, bool
     DecaySimtParams p{{d.cu_seqlens, d.num_seqs, d.H, d.total, 0, 0, nullptr, d.status}, d.q, d.k, d.v, d.ldq, d.ldk, d.ldv,
                       d.log_decay, d.init, d.fin, d.out, d.scale,
                       four(d.q, d.ldq) && four(d.k, d.ldk) && four(d.v, d.ldv) && four(d.out, 4)};
-    const int len = decay_segment_tokens(d.total, d.num_seqs, d.H, simt_slots(dv), kSimtChunk);
+    const int len = decay_segment_tokens(d.total, d.num_seqs, d.H, simt_slots(dv), kSimtCost);
     if (len && workspace && workspace_bytes >= decay_prefill_simt_workspace(d.total, d.num_seqs, d.H, dk, dv)) {
         p.g.len = len;
         p.g.cap = (int)(d.total / len) + d.num_seqs;

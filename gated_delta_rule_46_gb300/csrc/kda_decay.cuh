@@ -71,19 +71,34 @@ __device__ __forceinline__ float decay_log2(const float *log_decay, int head) {
     return fmaxf(log_decay[head] * kLog2E, -16384.f);
 }
 
-// Tokens per segment in whole chunks of C, or 0 for whole chains.  Segments cost
-// a second pass over k and v, so they are taken only where the chains fill at
-// most half of the `slots` (CTAs that run at a time); then one segment per slot.
-inline int decay_segment_tokens(int64_t total, int N, int H, int slots, int C) {
-    const int64_t chains = (int64_t)N * H;
+// Tokens per segment in whole chunks, or 0 for whole chains.  Segments cost a
+// second pass over k and v and two more launches: in units of a chunk's time in a
+// whole chain, a segment of m chunks takes per m + fixed.  So they are taken where
+// the chains fill at most half of the `slots` (CTAs that run at a time), one
+// segment per slot, and only where that is less than the longest chain's chunks,
+// guessed at 3/2 of the mean (the lengths are on the device; the mean itself where
+// there is one sequence).
+//   Measured, in segments / whole (us).  bf16, d = 128, 16 heads: 512 tokens 24.0 /
+// 18.6, 1024 25.3 / 32.7, 4096 39.7 / 117; 64 heads: 2048 tokens 63.9 / 62.7, 4096
+// 108 / 120; 4 sequences of 1024 tokens, 16 heads, 54.5 / 33.4.  f32, d = 128, 16
+// heads: 256 tokens 41.4 / 64.9, 4096 268 / 1056; 64 heads: 4096 tokens 1110 / 1074.
+// The guess costs most with few long sequences of one length: 4 of 4096 tokens, 16
+// heads, 153 / 119.
+struct SegmentCost {
+    int chunk, least;           // tokens of a chunk; fewest chunks of a segment
+    float per, fixed;
+};
+
+inline int decay_segment_tokens(int64_t total, int N, int H, int slots, const SegmentCost &cost) {
+    const int64_t chains = (int64_t)N * H, C = cost.chunk;
     if (chains * 2 > slots || N > 64) return 0;
     // sum over the sequences of ceil(len / m) stays within the slots
     const int64_t room = (slots - chains) * C;
     int64_t m = (total * H + room - 1) / room;
     if (N == 1) m = ((total + C - 1) / C + slots / H - 1) / (slots / H);
-    if (m < 4) m = 4;
-    const int64_t len = m * C;
-    return len * 2 > total ? 0 : (int)len;
+    if (m < cost.least) m = cost.least;
+    const float longest = (float)total / (float)(N * C) * (N > 1 ? 1.5f : 1.f);
+    return cost.per * (float)m + cost.fixed < longest ? (int)(m * C) : 0;
 }
 
 inline size_t decay_cells_bytes(int64_t total, int N, int H, int len, int dk, int dv) {

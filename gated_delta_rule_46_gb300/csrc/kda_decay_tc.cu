@@ -653,12 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr size_t kOrderAt = 256;
+constexpr SegmentCost kCost{C, 4, 1.6f, 9.f};
 size_t cells_at(int N) { return (kOrderAt + sizeof(int32_t) * (size_t)N + 1023) & ~size_t(1023); }
 
 }  // namespace
 
 size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D) {
-    return cells_at(N) + decay_cells_bytes(total, N, H, decay_segment_tokens(total, N, H, sm_count(), C), D, D);
+    const int len = decay_segment_tokens(total, N, H, sm_count(), kCost);
+    if (len == 0 && (N == 1 || (int64_t)N * H <= sm_count())) return 0;
+    return cells_at(N) + decay_cells_bytes(total, N, H, len, D, D);
 }
 
 template <int D>
@@ -687,7 +690,7 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);
     const int64_t chains = (int64_t)d.num_seqs * d.H;
-    const int len = room ? decay_segment_tokens(d.total, d.num_seqs, d.H, sms, C) : 0;
+    const int len = room ? decay_segment_tokens(d.total, d.num_seqs, d.H, sms, kCost) : 0;
     if (len) {
         p.g.len = len;
         p.g.cells = reinterpret_cast<float *>(ws + cells_at(d.num_seqs));

@@ -38,7 +38,7 @@ def test_linear(M, N, K, ld):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("lens,H", [([900, 300], 2), ([70] * 100, 2)])
+@pytest.mark.parametrize("lens,H", [([3000, 900], 2), ([70] * 100, 2)])
 def test_decay_prefill(d, lens, H):
     """With segments and without."""
     dev = need_gpu()
