@@ -21,6 +21,16 @@
 // Q K^T, S^T Q^T and V^T P^T; 4-7 write the output; 8-11 split the decayed keys;
 // 12-19 hold the state, 64 key channels of one value channel per thread, and leave
 // its bf16 copy in TMEM, where the MMA takes it from.  mbarriers link them.
+//
+// What bounds it: a token of one head moves 4 d bf16 values and no more; with 128
+// channels that is 64 KB per chunk, 1.5 us at a CTA's share of the copy rate.  It
+// takes 1.8: 133k ragged tokens of 32 heads run in 805 us, 5.5 TB/s.  No unit is full
+// (tensor pipe 38 %, issue slots 57 %, shared memory 36 %): what is left is each
+// chunk's chain from the state through its product with q to the next state, and the
+// roles in each other's way.  d = 64: 697 us for as many tokens and heads.  Measured
+// before, at that batch: S's copy in shared memory, which leaves room for two stages
+// of loads, 1034 us (917 in TMEM); waits that are calls, 1173; all warps at 96
+// registers, 918 (810).
 #include <cuda.h>
 
 #include "kda_decay.cuh"
@@ -263,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Walk<D, OUT> walk;
     Item x;
-    // 96 registers a thread at launch; of the five warpgroups' 480 the state's two take 120 each
+    // 96 registers a thread at launch (61,440); of the five warpgroups' 480 the state's two take 120 each
     if (warp < 4) {
         ptx::regs_dec<80>();
         if (warp == 2 || (!OUT && warp == 3)) {                       // ---- loads, and the state's product

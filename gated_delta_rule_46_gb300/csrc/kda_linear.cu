@@ -4,6 +4,14 @@
 // 256 x 256 tile of out at a time.  `linear_rows_kernel` (few rows): the roles
 // of x and w are swapped, so that 128 output features lie on the MMA's rows and
 // the rows of x, however few, on its columns; K is split over a cluster.
+//
+// Many rows are bound by the tensor pipe: 8192 x 16384 x 4096 (M x N x K) takes
+// 555-565 us, 1.95-1.98 PFLOP/s, as long as the power cap does not set in (then
+// 663); the pipe is 90 % busy at 4096 x 9728 x 4096 (175 us).  Few rows are bound
+// by reading w: 64 x 16384 x 8192 takes 46 us (5.9 TB/s), 64 x 4096 x 4096 11.5 us,
+// of which the 34 MB are 5; launch, the first load and the join are the rest.
+// Every sum is held in float32 (TMEM, and the join of a cluster's parts in order
+// of rank, so that results do not depend on timing); the one rounding is out's own.
 #include <cuda.h>
 
 #include "kda_layers.cuh"
@@ -46,6 +54,10 @@ struct Tail {   // what the epilogue needs
     uint32_t *status;
     int expire;           // test support
 };
+
+Tail tail(const LinearParams &p) {
+    return {p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status, take_layers_expire(KDA_TESTING_LINEAR)};
+}
 
 // ---------------------------------------------------------------------------
 // Few rows.  One CTA: 128 features (rows of w, the MMA's M) x NT rows of x (the
@@ -338,7 +350,10 @@ __global__ void __launch_bounds__(320)
                 const int m0 = tm * 256 + (int)rank * 128, n0 = tn * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < kbs; ++kb, ++it) {
                     const int s = it % kStages;
-                    if (it >= kStages && !ptx::mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, kWaitBudget)) { ok = false; break; }
+                    if (it >= kStages && !ptx::mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, kWaitBudget)) {
+                        ok = false;
+                        break;
+                    }
                     uint8_t *a = sm + s * L::stage;
                     // rank 0's barrier counts the bytes of both CTAs
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::stage);
@@ -484,8 +499,7 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
         !make_map_2d(&mo, p.out, !F32, p.M, p.N, p.N * eb, 128) ||
         !make_map_2d(&mr, p.residual ? p.residual : p.out, !F32, p.M, p.N, p.N * eb, 128))
         return cudaErrorInvalidValue;
-    PairParams pp{{p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status, take_layers_expire(KDA_TESTING_LINEAR)}, (int)((p.M + 255) / 256),
-                  (int)((p.N + BN - 1) / BN), 8};
+    PairParams pp{tail(p), (int)((p.M + 255) / 256), (int)((p.N + BN - 1) / BN), 8};
     auto *kernel = linear_pair_kernel<ACT, F32, BN>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
@@ -497,7 +511,7 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
 template <int ACT, bool F32, int LOAD>
 cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     RowsParams rp{};
-    rp.t = {p.bias, p.residual, p.out, (int)p.M, (int)p.N, (int)p.K, p.status, take_layers_expire(KDA_TESTING_LINEAR)};
+    rp.t = tail(p);
     rp.x = p.x;
     rp.w = p.w;
     rp.ldx = p.ldx;
@@ -522,7 +536,8 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t mt = (p.M + rp.NT - 1) / rp.NT;
-    return launch_dependent(kernel, dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt), LOAD ? 448 : 192, smem, st, rp.S, mw, mx, rp);
+    return launch_dependent(kernel, dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt), LOAD ? 448 : 192, smem, st,
+                            rp.S, mw, mx, rp);
 }
 
 template <int ACT, bool F32>
