@@ -340,11 +340,11 @@ template <typename T, int DK, int JB>
 static cudaError_t decay_simt(DecaySimtParams &p, int dv, int64_t chains, cudaStream_t st) {
     constexpr int C = kSimtChunk, G = 256 / (2 * JB);
     const size_t smem = sizeof(float) * (2 * C * (DK + 4) + C * JB + DK * JB + C * (C + 4) + (G - 1) * C * JB + C + 1);
-    cudaError_t e = cudaFuncSetAttribute(decay_simt_kernel<T, DK, JB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<decay_simt_kernel<T, DK, JB, true>>((uint32_t)smem);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)chains, dv / JB);
     if (p.g.len) {
-        e = cudaFuncSetAttribute(decay_simt_kernel<T, DK, JB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_smem<decay_simt_kernel<T, DK, JB, false>>((uint32_t)smem);
         if (e != cudaSuccess) return e;
         grid.x = (unsigned)((int64_t)p.g.cap * p.g.H);
         if ((e = launch_dependent(decay_simt_kernel<T, DK, JB, false>, grid, 256, smem, st, 1, p, dv)) != cudaSuccess) return e;

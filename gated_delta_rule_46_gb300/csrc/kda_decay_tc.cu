@@ -693,9 +693,8 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
              d.ldv,
              nullptr,
              take_layers_expire(KDA_TESTING_DECAY)};
-    cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemState);
+    cudaError_t e = allow_smem<decay_chunk_kernel<D, true>>(kSmem);
+    if (e == cudaSuccess) e = allow_smem<decay_chunk_kernel<D, false>>(kSmemState);
     if (e != cudaSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);

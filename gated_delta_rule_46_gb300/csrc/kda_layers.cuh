@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_common.cuh"
 #include "kda_layers.h"
 
@@ -101,6 +103,20 @@ int sm_count();
 // which is cleared; a kernel so called has CTA 0 fail one wait.
 bool take_layers_expire(int bit);
 constexpr long long kTestWait = 1LL << 21;    // cycles (about a millisecond)
+
+// Opts `Kernel` in to dynamic shared memory of up to `bytes` on the current device, once (the call takes 2 us).
+template <auto Kernel>
+inline cudaError_t allow_smem(uint32_t bytes) {
+    static std::atomic<uint64_t> done{0};         // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launches `kernel` so that its start may overlap the end of the kernel before
 // it in the stream: the kernel calls griddepcontrol.wait before it touches

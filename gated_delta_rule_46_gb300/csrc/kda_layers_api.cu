@@ -14,10 +14,12 @@ void set_layers_expire(int mask) { g_layers_expire.store(mask); }
 bool take_layers_expire(int bit) { return g_layers_expire.fetch_and(~bit) & bit; }
 
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 }  // namespace kda
@@ -169,9 +171,9 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
     const int64_t e = elem(dtype);
     if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return KDA_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype))
-        return KDA_ERR_INVALID_ARG;
+    const size_t need =
+        kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype);
+    if (!aligned(workspace, 16) || (need > 0 && (!workspace || workspace_bytes < need))) return KDA_ERR_INVALID_ARG;
     kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
                              seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
                              static_cast<float *>(workspace), false, 0, status};

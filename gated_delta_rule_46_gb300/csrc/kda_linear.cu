@@ -501,7 +501,7 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
         return cudaErrorInvalidValue;
     PairParams pp{tail(p), (int)((p.M + 255) / 256), (int)((p.N + BN - 1) / BN), 8};
     auto *kernel = linear_pair_kernel<ACT, F32, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
+    const cudaError_t e = allow_smem<linear_pair_kernel<ACT, F32, BN>>(L::bytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)pp.tiles_m * pp.tiles_n;
     const int pairs = sm_count() / 2;
@@ -533,7 +533,7 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
                   !make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, rp.NT)))
         return cudaErrorInvalidValue;
     auto *kernel = linear_rows_kernel<ACT, F32, LOAD>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem<linear_rows_kernel<ACT, F32, LOAD>>(kRoom + 1024);
     if (e != cudaSuccess) return e;
     const int64_t mt = (p.M + rp.NT - 1) / rp.NT;
     return launch_dependent(kernel, dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt), LOAD ? 448 : 192, smem, st,

@@ -322,6 +322,7 @@ static int grid_simt(int N, int64_t max_tokens, int Hkv, int G) {
 
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
     const int G = Hq / Hkv;
+    if (max_tokens <= (kTile < kTileTc ? kTile : kTileTc)) return 0;      // one tile: nothing to join
     const size_t tc = (size_t)grid_tc(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_tc(G));
     const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G) * 2 * part_floats(d, kHB);
     return sizeof(float) * (tc > simt ? tc : simt);
@@ -331,8 +332,7 @@ template <typename T, int D>
 static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
     p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile;
     const size_t smem = sizeof(float) * (kTile * (D + 4) + kTile * D + kHB * D + kHB * kTile + 3 * kHB);
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<paged_decode_simt_kernel<T, D>>((uint32_t)smem);
     if (e != cudaSuccess) return e;
     const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
     if ((e = launch_dependent(paged_decode_simt_kernel<T, D>, dim3(grid), 256, smem, st, 1, p)) != cudaSuccess) return e;

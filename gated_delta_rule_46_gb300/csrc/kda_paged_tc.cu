@@ -470,7 +470,7 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     constexpr uint32_t smem = Lay<D, HB>::bytes + (D == 64 ? kSub : 0) + 1024;
     auto *kernel = paged_decode_tc_kernel<D, HB>;
     static_assert(smem <= 229000, "shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem<paged_decode_tc_kernel<D, HB>>(smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(grid), 384, smem, st, 1, mk, mv, p);
 }

@@ -147,7 +147,7 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, out_dtype=None,
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     new = []
     if out is None:
-        out = x.new_empty((M, N), dtype=out_dtype)
+        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
         new.append(out)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -182,15 +182,15 @@ def decay_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, final_stat
     cp = _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
     new = []
     if final_state is None and want_final_state:
-        final_state = log_decay.new_empty((N, H, dk, dv))
+        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
         new.append(final_state)
     if out is None:
-        out = q.new_empty((T, H, dv))
+        out = torch.empty((T, H, dv), dtype=dt, device=dev)
         new.append(out)
     if workspace is None:
         size = _fn("kda_decay_prefill_workspace_size")(T, N, H, dk, dv, code)
         if size:
-            workspace = q.new_empty(size, dtype=torch.uint8)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
             new.append(workspace)
     size = 0 if workspace is None else _dims(workspace, "workspace", 1)[0]
     wp = _dense(workspace, "workspace", (size,), torch.uint8, dev)
@@ -217,7 +217,7 @@ def decay_decode(q, k, v, log_decay, state_pool, slot_ids=None, out=None, scale=
     P = _dims(state_pool, "state_pool", 4)[0]
     new = []
     if out is None:
-        out = q.new_empty((N, H, dv))
+        out = torch.empty((N, H, dv), dtype=dt, device=dev)
         new.append(out)
     _call("kda_decay_decode", dev, stream, new, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
           _dense(log_decay, "log_decay", (H,), torch.float32, dev),
@@ -242,7 +242,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, start_pos, cu_seqlens=None,
     vp = _dense(v_cache, "v_cache", (P, H, ps, d), dt, dev)
     N, cols = _dims(page_table, "page_table", 2)
     tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
-    _call("kda_paged_append", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, P, ps, tp, cols, _dense(start_pos, "start_pos", (N,), torch.int32, dev),
+    _call("kda_paged_append", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, P, ps, tp, cols,
+          _dense(start_pos, "start_pos", (N,), torch.int32, dev),
           _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, d, code, _status(status, dev))
 
 
@@ -269,15 +270,17 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
     tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
     new = []
     if out is None:
-        out = q.new_empty((N, Hq, d))
+        out = torch.empty((N, Hq, d), dtype=dt, device=dev)
         new.append(out)
     if lse is None and return_lse:
-        lse = q.new_empty((N, Hq), dtype=torch.float32)
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
         new.append(lse)
     if workspace is None:
-        workspace = q.new_empty(_fn("kda_paged_decode_workspace_size")(N, cols * ps, Hq, Hkv, d, code), dtype=torch.uint8)
-        new.append(workspace)
-    size = _dims(workspace, "workspace", 1)[0]
+        size = _fn("kda_paged_decode_workspace_size")(N, cols * ps, Hq, Hkv, d, code)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            new.append(workspace)
+    size = 0 if workspace is None else _dims(workspace, "workspace", 1)[0]
     _call("kda_paged_decode", dev, stream, new, q.data_ptr(), ldq, kp, vp, P, ps, tp, cols,
           _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
           d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),
