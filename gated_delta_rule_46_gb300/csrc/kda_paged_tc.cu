@@ -20,9 +20,11 @@
 //
 // Bound by reading the cache: a ragged batch with 2.1 GB of it takes 317 us (6.75
 // TB/s, the rate of a plain copy), one row of 131072 tokens (537 MB, split over all
-// SMs and joined) 91 us (5.9 TB/s; 79 at the copy rate, the rest is the launch, the
-// first pages' latency and the join).  With d = 64 a tile is half as large and the
-// softmax warps, which take about as long for it, hold it to 79 % of the copy rate.
+// SMs and joined) 88 us (6.1 TB/s; 79 at the copy rate, the rest is the launch, the
+// first pages' latency and the join).  With d = 64 a tile is half as large and takes
+// the softmax warps about as long: 64 rows of 8192 tokens, 8 key-value heads, 4 query
+// heads each, run at 94 % of the copy rate, and at 79 % if the softmax works on all 16
+// of the MMA's columns.
 #include <cuda.h>
 
 #include "kda_paged.cuh"
@@ -104,11 +106,11 @@ __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p) {
     return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
-// 16 values per lane, combined over the warp: lane i ends with value i / 2.
-template <typename Op>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
+// N = 8 or 16 values per lane, combined over the warp: lane i ends with value i / (32 / N).
+template <int N, typename Op>
+__device__ __forceinline__ float reduce_lanes(float (&v)[N], int lane, Op op) {
 #pragma unroll
-    for (int n = 8, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
+    for (int n = N / 2, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
         const bool up = lane & bit;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -116,15 +118,24 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
             v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
         }
     }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+#pragma unroll
+    for (int bit = 16 / N; bit >= 1; bit >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+    return v[0];
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
+    if constexpr (N == 8) ptx::tmem_ld8(addr, v);
+    else ptx::tmem_ld16(addr, v);
 }
 
-template <int D, int HB>
+// HB heads are the MMAs' columns (their least is 16), the first HR of them are worked on: the others' columns hold
+// whatever is there and reach no one.
+template <int D, int HB, int HR>
 __global__ void __launch_bounds__(384, 1)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedParams p) {
     using L = Lay<D, HB>;
     constexpr int NS = L::NS;
-    constexpr int HALVES = D / 64;
+    constexpr int HALVES = D / 64, W = HR < 16 ? HR : 16;       // heads at a time
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[NBAR];
     __shared__ int64_t s_sum[257];
@@ -284,7 +295,7 @@ __global__ void __launch_bounds__(384, 1)
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
             // eight channels per lane and step, all loads first
-            constexpr int PER = HB * D / 256;
+            constexpr int PER = HR * D / 256;
             uint4 u[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -314,34 +325,34 @@ __global__ void __launch_bounds__(384, 1)
         while (ok && wk.more()) {
             const int len = clamp_len(p, wk.n, false);
             const int64_t first = wk.tile, last = wk.last();
-            float m[HB], l[HB];
+            float m[HR], l[HR];
 #pragma unroll
-            for (int h = 0; h < HB; ++h) { m[h] = -INFINITY; l[h] = 0.f; }
+            for (int h = 0; h < HR; ++h) { m[h] = -INFINITY; l[h] = 0.f; }
             for (int64_t i = first; i < last; ++i, ++t) {
                 const int b = t & 1;
                 // the factors and weights of two tiles ago have been used
                 ok = warp_wait(&bar[SD + b], t >> 1) && (t < 2 || warp_wait(&bar[OFREE + b], (t >> 1) - 1));
-                float s[HB];
+                float s[HR];
                 if (ok) {
                     ptx::tc_fence_after_sync();
 #pragma unroll
-                    for (int h = 0; h < HB; h += 16) {
-                        float v[16];
-                        ptx::tmem_ld16(tm_s(b) + ((uint32_t)q << 21) + h, v);
+                    for (int h = 0; h < HR; h += W) {
+                        float v[W];
+                        tmem_load(tm_s(b) + ((uint32_t)q << 21) + h, v);
                         ptx::tmem_ld_wait();
                         const bool in = (int)(i * TILE) + j < len &&
                                         (*static_cast<volatile uint32_t *>(&s_mask[t & 7]) >> (j / rows) & 1);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) s[h + e] = v[e] = in ? v[e] * sc2 : -INFINITY;
-                        const float mx = reduce16(v, lane, [](float x, float y) { return fmaxf(x, y); });
-                        if (!(lane & 1)) red[(b * 4 + q) * HB + h + (lane >> 1)] = mx;
+                        for (int e = 0; e < W; ++e) s[h + e] = v[e] = in ? v[e] * sc2 : -INFINITY;
+                        const float mx = reduce_lanes(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                        if (lane % (32 / W) == 0) red[(b * 4 + q) * HB + h + lane / (32 / W)] = mx;
                     }
                 }
                 ok = !ptx::bar_any(1, 128, !ok);
                 if (!ok) break;
                 uint8_t *sp_ = sm + L::P + b * L::p_bytes + (j >> 6) * (HB * 128) + (j & 7) * 2;
 #pragma unroll
-                for (int h = 0; h < HB; h += 4) {
+                for (int h = 0; h < HR; h += 4) {
                     float mt[4], f[4];
                     ld4(red + (b * 4) * HB + h, mt);
 #pragma unroll
@@ -371,16 +382,16 @@ __global__ void __launch_bounds__(384, 1)
             if (item_no >= 2) ok = warp_wait(&bar[IFREE + ib], (item_no >> 1) - 1);
             if (!ok) break;
 #pragma unroll
-            for (int h = 0; h < HB; h += 16) {
-                float v[16];
+            for (int h = 0; h < HR; h += W) {
+                float v[W];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = l[h + e];
-                const float sum = reduce16(v, lane, [](float x, float y) { return x + y; });
-                if (!(lane & 1)) sums[(ib * 4 + q) * HB + h + (lane >> 1)] = sum;
+                for (int e = 0; e < W; ++e) v[e] = l[h + e];
+                const float sum = reduce_lanes(v, lane, [](float x, float y) { return x + y; });
+                if (lane % (32 / W) == 0) sums[(ib * 4 + q) * HB + h + lane / (32 / W)] = sum;
             }
             if (j == 0)
 #pragma unroll
-                for (int h = 0; h < HB; ++h) maxs[ib * HB + h] = m[h];
+                for (int h = 0; h < HR; ++h) maxs[ib * HB + h] = m[h];
             warp_arrive(&bar[IREADY + ib]);
             ++item_no;
             wk.next_item(p, last - first);
@@ -394,23 +405,23 @@ __global__ void __launch_bounds__(384, 1)
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
             const int64_t row0 = (int64_t)wk.n * p.Hq + (int64_t)kvh * p.G + g0;
-            float acc[HB];
+            float acc[HR];
 #pragma unroll
-            for (int h = 0; h < HB; ++h) acc[h] = 0.f;
+            for (int h = 0; h < HR; ++h) acc[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
                 const int b = t & 1;
                 ok = warp_wait(&bar[PVD + b], t >> 1);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
-                for (int h = 0; h < HB; h += 16) {
-                    float v[16], f[16];
-                    ptx::tmem_ld16(tm_o(b) + ((uint32_t)q << 21) + h, v);
-                    ld8(sf + b * HB + h, f);
-                    ld8(sf + b * HB + h + 8, f + 8);
+                for (int h = 0; h < HR; h += W) {
+                    float v[W], f[W];
+                    tmem_load(tm_o(b) + ((uint32_t)q << 21) + h, v);
+#pragma unroll
+                    for (int e = 0; e < W; e += 8) ld8(sf + b * HB + h + e, f + e);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[h + e] = fmaf(acc[h + e], f[e], v[e]);
+                    for (int e = 0; e < W; ++e) acc[h + e] = fmaf(acc[h + e], f[e], v[e]);
                 }
                 ptx::tc_fence_before_sync();
                 warp_arrive(&bar[OFREE + b]);
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(384, 1)
             const bool whole = first == 0 && last == wk.nt;
             float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
 #pragma unroll
-            for (int h = 0; h < HB; ++h) {
+            for (int h = 0; h < HR; ++h) {
                 if (h >= hb) break;
                 const float l = (sums[ib * 4 * HB + h] + sums[(ib * 4 + 1) * HB + h]) +
                                 (sums[(ib * 4 + 2) * HB + h] + sums[(ib * 4 + 3) * HB + h]);
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-template <int D, int HB>
+template <int D, int HB, int HR>
 cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     CUtensorMap mk, mv;
     const uint64_t rows = (uint64_t)p.num_pages * p.Hkv << p.page_shift;
@@ -468,9 +479,9 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
         return cudaErrorInvalidValue;
     // (d = 64: the MMA's unread rows reach one sub-tile past the last V tile)
     constexpr uint32_t smem = Lay<D, HB>::bytes + (D == 64 ? kSub : 0) + 1024;
-    auto *kernel = paged_decode_tc_kernel<D, HB>;
+    auto *kernel = paged_decode_tc_kernel<D, HB, HR>;
     static_assert(smem <= 229000, "shared memory");
-    const cudaError_t e = allow_smem<paged_decode_tc_kernel<D, HB>>(smem);
+    const cudaError_t e = allow_smem<paged_decode_tc_kernel<D, HB, HR>>(smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(grid), 384, smem, st, 1, mk, mv, p);
 }
@@ -478,8 +489,12 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_decode_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st) {
-    if (d == 64) return HB == 16 ? launch<64, 16>(p, grid, st) : launch<64, 32>(p, grid, st);
-    return HB == 16 ? launch<128, 16>(p, grid, st) : launch<128, 32>(p, grid, st);
+    if (d == 64) {
+        if (p.G <= 8) return launch<64, 16, 8>(p, grid, st);
+        return HB == 16 ? launch<64, 16, 16>(p, grid, st) : launch<64, 32, 32>(p, grid, st);
+    }
+    if (p.G <= 8) return launch<128, 16, 8>(p, grid, st);
+    return HB == 16 ? launch<128, 16, 16>(p, grid, st) : launch<128, 32, 32>(p, grid, st);
 }
 
 }  // namespace kda

@@ -176,6 +176,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr));
 }
+// The same, 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+        : "r"(taddr));
+}
 // 16 lanes x 32 columns in the layout of four 16 x 8 accumulator tiles: of tile
 // i, thread t holds row t / 4, columns 8 i + 2 (t % 4) and + 1 in r[4 i], r[4 i + 1]
 // and the same columns of row t / 4 + 8 in r[4 i + 2], r[4 i + 3].
