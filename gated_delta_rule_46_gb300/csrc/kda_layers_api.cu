@@ -171,9 +171,9 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
     const int64_t e = elem(dtype);
     if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return KDA_ERR_INVALID_ARG;
-    const size_t need =
-        kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype);
-    if (!aligned(workspace, 16) || (need > 0 && (!workspace || workspace_bytes < need))) return KDA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype))
+        return KDA_ERR_INVALID_ARG;
     kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
                              seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
                              static_cast<float *>(workspace), false, 0, status};

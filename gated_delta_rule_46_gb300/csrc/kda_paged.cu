@@ -82,23 +82,68 @@ cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t 
 }
 
 // ---------------------------------------------------------------------------
-// CUDA-core form (float32 caches, d = 32, pages of under eight tokens): tiles of
-// 64 tokens in shared memory as float32.  Bound by shared memory, from where each
-// product takes an operand; it reads a float32 cache at 31 % of the copy rate.
+// CUDA-core form (float32 caches, d = 32, pages of under eight tokens): d / 8
+// lanes share a token, eight channels each of its key, its value, the queries
+// and the outputs of HB heads, all in registers; a warp works on 256 / d tokens
+// at a time and on U such rounds between corrections of its maximum.  A round's
+// keys are reloaded as soon as its scores are out, and its values as soon as
+// they are summed up, so that loads are always under way.  Lane groups and warps
+// keep maxima, sums and outputs of their own, which are joined once per item.
+//   64 rows of 8192 float32 tokens, 8 key-value heads of 128 channels, 4 query
+// heads each, take 783 us: 5.5 TB/s, 81 % of the copy rate.  With 8 query heads each
+// it is 59 %, as then two rounds are all that the registers hold and the FMAs of a
+// byte are twice as many; bf16 pages of 4 tokens, 52 %.
 // ---------------------------------------------------------------------------
-constexpr int kHB = 16;        // query heads per item
 constexpr int kTile = 64;
 
+// Eight channels of a row as they are loaded: of lane l of the d / 8 that share it.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParams p) {
-    constexpr int TILE = kTile, LD = D + 4, NG = 256 / D, NA = kHB / NG;
-    extern __shared__ float sm[];
-    float *sK = sm, *sV = sK + TILE * LD, *sQ = sV + TILE * D, *sS = sQ + kHB * D;   // sS [kHB][TILE]
-    float *sM = sS + kHB * TILE, *sL = sM + kHB, *sC = sL + kHB;                     // max, sum, correction
+struct Ch8;
+template <int D>
+struct Ch8<float, D> {
+    float4 a = {}, b = {};
+    static __device__ int channel(int l, int e) { return (e & 4) * (D / 8) + l * 4 + (e & 3); }
+    __device__ void load(const float *row, int l) {
+        a = *reinterpret_cast<const float4 *>(row + l * 4);
+        b = *reinterpret_cast<const float4 *>(row + D / 2 + l * 4);
+    }
+    __device__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <int D>
+struct Ch8<__nv_bfloat16, D> {
+    uint4 u = {};
+    static __device__ int channel(int l, int e) { return l * 8 + e; }
+    __device__ void load(const __nv_bfloat16 *row, int l) { u = *reinterpret_cast<const uint4 *>(row + l * 8); }
+    __device__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <typename T, int D, int HB>
+struct Simt {
+    static constexpr int WARPS = HB == 4 ? 10 : 8;                         // registers for as many
+    static constexpr int U = HB == 4 || sizeof(T) == 2 ? 4 : 2;            // rounds between corrections
+    static constexpr int LPT = D / 8, TPW = 32 / LPT;                      // lanes per token, tokens per warp
+    static constexpr uint32_t smem = sizeof(float) * WARPS * HB * (D + 2);
+};
+
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_simt_kernel(const PagedParams p) {
+    using S = Simt<T, D, HB>;
+    constexpr int TILE = kTile, U = S::U, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
+    extern __shared__ float sm[];                     // of each warp: m and l [HB], outputs [HB][D]
     __shared__ int64_t s_sum[257];
     __shared__ int s_n;
-    const int tid = threadIdx.x, lane = tid & 31, wy = tid >> 5;
-    const int nb = (p.G + kHB - 1) / kHB, items = p.Hkv * nb;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l8 = lane % LPT;
+    const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
@@ -112,114 +157,166 @@ __global__ void __launch_bounds__(256) paged_decode_simt_kernel(const PagedParam
     int64_t tile = (w - sp.cum * items) - item * nt;
     const float sc2 = p.scale * kLog2E;
     const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
-    const int col = tid % D, hg = tid / D;
 
     while (w < w1) {
         const int len = clamp_len(p, n, tid == 0 && item == 0 && tile == 0);
-        const int kvh = item / nb, g0 = (item % nb) * kHB, hb = min(kHB, p.G - g0);
+        const int kvh = item / nb, g0 = (item % nb) * HB, hb = min(HB, p.G - g0);
         const int hq0 = kvh * p.G + g0;
         const int64_t first = tile, last = min(nt, tile + (w1 - w));      // tiles [first, last) of the item
-        __syncthreads();
-        for (int i = tid; i < hb * D; i += 256)
-            sQ[i] = to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)hq0 * D + i]) * sc2;
-        if (tid < kHB) { sM[tid] = -INFINITY; sL[tid] = 0.f; }
-        float acc[NA];
+        const int end = (int)min(last * TILE, (int64_t)len);
+        const int32_t *table = p.table + (int64_t)n * p.max_pages;
+        int t = (int)(first * TILE) + warp * S::TPW + lane / LPT;         // this lane's token of the first round
+
+        float q[HB][8];
 #pragma unroll
-        for (int i = 0; i < NA; ++i) acc[i] = 0.f;
-        for (; tile < last; ++tile) {
-            const int t0 = (int)(tile * TILE);
-            __syncthreads();
-            for (int i = tid; i < TILE * (D / 4); i += 256) {
-                const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-                float kk[4] = {}, vv[4] = {};
-                if (t0 + r < len) {
-                    const int pg = p.table[(int64_t)n * p.max_pages + ((t0 + r) >> p.page_shift)];
-                    if (pg >= 0 && pg < p.num_pages) {
-                        const int64_t at = (((((int64_t)pg * p.Hkv + kvh) << p.page_shift) +
-                                             ((t0 + r) & ((1 << p.page_shift) - 1))) * D) + c;
+        for (int h = 0; h < HB; ++h)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) { kk[e] = to_f32(kc[at + e]); vv[e] = to_f32(vc[at + e]); }
-                    } else {
-                        if (c == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
-                    }
-                }
+            for (int e = 0; e < 8; ++e)
+                q[h][e] = h < hb ? to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)(hq0 + h) * D +
+                                                                      Ch8<T, D>::channel(l8, e)]) * sc2
+                                 : 0.f;
+        float m[HB], l[HB], acc[HB][8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) { sK[r * LD + c + e] = kk[e]; sV[r * D + c + e] = vv[e]; }
-            }
-            __syncthreads();
-            {   // scores: thread = token x every fourth head
-                const int j = tid & 63;
-                bool ok = t0 + j < len;
-                if (ok) {
-                    const int pg = p.table[(int64_t)n * p.max_pages + ((t0 + j) >> p.page_shift)];
-                    ok = pg >= 0 && pg < p.num_pages;
-                }
-                for (int g = tid >> 6; g < hb; g += 4) {
-                    float a = 0.f;
-#pragma unroll 8
-                    for (int c = 0; c < D; c += 4) {
-                        float x[4], y[4];
-                        tc::ld4(sQ + g * D + c, x);
-                        tc::ld4(sK + j * LD + c, y);
-                        a = fmaf(x[0], y[0], a); a = fmaf(x[1], y[1], a);
-                        a = fmaf(x[2], y[2], a); a = fmaf(x[3], y[3], a);
-                    }
-                    sS[g * TILE + j] = ok ? a : -INFINITY;
-                }
-            }
-            __syncthreads();
-            for (int g = wy; g < hb; g += 8) {   // softmax of one head per warp
-                const float s0 = sS[g * TILE + lane], s1 = sS[g * TILE + 32 + lane];
-                float m = fmaxf(s0, s1);
+        for (int h = 0; h < HB; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float mo = sM[g], mn = fmaxf(mo, m);
-                // a tile with nothing in it leaves everything as it is
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                const float p0 = exp2f(s0 - mu), p1 = exp2f(s1 - mu);
-                float l = p0 + p1;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                sS[g * TILE + lane] = p0;
-                sS[g * TILE + 32 + lane] = p1;
-                __syncwarp();
-                if (lane == 0) {
-                    const float f = exp2f(mo - mu);
-                    sC[g] = f;
-                    sM[g] = mn;
-                    sL[g] = sL[g] * f + l;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < NA; ++i) {
-                const int g = hg + i * NG;
-                if (g >= hb) break;
-                float a = acc[i] * sC[g];
-#pragma unroll 8
-                for (int j = 0; j < TILE; ++j) a = fmaf(sS[g * TILE + j], sV[j * D + col], a);
-                acc[i] = a;
-            }
+            for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
         }
-        __syncthreads();
-        if (first == 0 && last == nt) {
+
+        // pages of the U rounds from token t on (-1: no token), and rows of a cache on them
+        auto pages = [&](int t, int (&pg)[U]) {
 #pragma unroll
-            for (int i = 0; i < NA; ++i) {
-                const int g = hg + i * NG;
-                if (g >= hb) break;
-                const float l = sL[g];
-                static_cast<T *>(p.out)[((int64_t)n * p.Hq + hq0 + g) * D + col] =
-                    from_f32<T>(l > 0.f ? acc[i] / l : (l == 0.f ? 0.f : l));
-                if (col == 0 && p.lse) p.lse[(int64_t)n * p.Hq + hq0 + g] = (sM[g] + log2f(l)) / kLog2E;
+            for (int u = 0; u < U; ++u) {
+                pg[u] = -1;
+                if (t + u * STEP < end) {
+                    pg[u] = table[(t + u * STEP) >> p.page_shift];
+                    if (pg[u] < 0 || pg[u] >= p.num_pages) {
+                        if (l8 == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+                        pg[u] = -1;
+                    }
+                }
             }
-        } else {
-            float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, kHB);
+        };
+        auto fetch = [&](const T *cache, int t, const int (&pg)[U], Ch8<T, D> (&x)[U]) {
 #pragma unroll
-            for (int i = 0; i < NA; ++i) {
-                const int g = hg + i * NG;
-                if (g >= hb) break;
-                part[kHB * 2 + g * D + col] = acc[i];
-                if (col == 0) { part[2 * g] = sM[g]; part[2 * g + 1] = sL[g]; }
+            for (int u = 0; u < U; ++u) {
+                x[u] = Ch8<T, D>();
+                if (pg[u] >= 0)
+                    x[u].load(cache + (((((int64_t)pg[u] * p.Hkv + kvh) << p.page_shift) +
+                                        ((t + u * STEP) & ((1 << p.page_shift) - 1))) * D), l8);
+            }
+        };
+        Ch8<T, D> k[U], v[U];
+        int pg[U], pn[U];
+        pages(t, pg);
+        fetch(kc, t, pg, k);
+        fetch(vc, t, pg, v);
+        pages(t + U * STEP, pn);
+        // the rounds of a warp's lanes are the same in number: the shuffles are the whole warp's
+        const int t0 = (int)(first * TILE) + warp * S::TPW;
+        for (int r = t0; r < end; r += U * STEP, t += U * STEP) {
+            float s[U][HB];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8];
+                k[u].get(x);
+#pragma unroll
+                for (int h = 0; h < HB; ++h) {
+                    float a = x[0] * q[h][0];
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) a = fmaf(x[e], q[h][e], a);
+                    s[u][h] = a;
+                }
+            }
+            fetch(kc, t + U * STEP, pn, k);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < HB; ++h) {
+#pragma unroll
+                    for (int o = 1; o < LPT; o <<= 1) s[u][h] += __shfl_xor_sync(0xffffffffu, s[u][h], o);
+                    if (pg[u] < 0) s[u][h] = -INFINITY;
+                }
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+                float mn = m[h];
+#pragma unroll
+                for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u][h]);
+                // rounds without a token leave everything as it is
+                const float mu = mn == -INFINITY ? 0.f : mn, f = tc::ex2(m[h] - mu);
+                m[h] = mn;
+                l[h] *= f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[h][e] *= f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    s[u][h] = tc::ex2(s[u][h] - mu);
+                    l[h] += s[u][h];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8];
+                v[u].get(x);
+#pragma unroll
+                for (int h = 0; h < HB; ++h)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(s[u][h], x[e], acc[h][e]);
+            }
+            fetch(vc, t + U * STEP, pn, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u) pg[u] = pn[u];
+            pages(t + 2 * U * STEP, pn);
+        }
+
+        // join the warp's lane groups, then the warps
+#pragma unroll
+        for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+                const float mo = __shfl_xor_sync(0xffffffffu, m[h], o), lo = __shfl_xor_sync(0xffffffffu, l[h], o);
+                const float mn = fmaxf(m[h], mo), mu = mn == -INFINITY ? 0.f : mn;
+                const float f = tc::ex2(m[h] - mu), fo = tc::ex2(mo - mu);
+                m[h] = mn;
+                l[h] = fmaf(l[h], f, lo * fo);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[h][e] = fmaf(acc[h][e], f, __shfl_xor_sync(0xffffffffu, acc[h][e], o) * fo);
+            }
+        __syncthreads();                              // the item before is written
+        float *mine = sm + warp * HB * (D + 2);
+        if (lane < LPT)
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+                if (lane == 0) { mine[2 * h] = m[h]; mine[2 * h + 1] = l[h]; }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mine[2 * HB + h * D + Ch8<T, D>::channel(l8, e)] = acc[h][e];
+            }
+        __syncthreads();
+        const bool whole = first == 0 && last == nt;
+        float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
+        for (int i = tid; i < hb * D; i += NT) {
+            const int h = i / D, c = i % D;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < S::WARPS; ++x) mx = fmaxf(mx, sm[x * HB * (D + 2) + 2 * h]);
+            const float mu = mx == -INFINITY ? 0.f : mx;
+            float ls = 0.f, a = 0.f;
+#pragma unroll
+            for (int x = 0; x < S::WARPS; ++x) {
+                const float *o = sm + x * HB * (D + 2);
+                const float f = tc::ex2(o[2 * h] - mu);
+                ls = fmaf(o[2 * h + 1], f, ls);
+                a = fmaf(o[2 * HB + h * D + c], f, a);
+            }
+            if (whole) {
+                static_cast<T *>(p.out)[((int64_t)n * p.Hq + hq0 + h) * D + c] =
+                    from_f32<T>(ls > 0.f ? a / ls : (ls == 0.f ? 0.f : ls));
+                if (c == 0 && p.lse) p.lse[(int64_t)n * p.Hq + hq0 + h] = (mx + log2f(ls)) / kLog2E;
+            } else {
+                part[HB * 2 + h * D + c] = a;
+                if (c == 0) { part[2 * h] = mx; part[2 * h + 1] = ls; }
             }
         }
         w += last - first;
@@ -316,35 +413,40 @@ static int grid_tc(int N, int64_t max_tokens, int Hkv, int G) {
     const int HB = heads_tc(G);
     return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc, sm_count());
 }
+// Query heads per item of the CUDA-core form: what its registers hold.
+static int heads_simt(int G) { return G <= 4 ? 4 : 8; }
 static int grid_simt(int N, int64_t max_tokens, int Hkv, int G) {
-    return grid_for(N, max_tokens, Hkv * ((G + kHB - 1) / kHB), kTile, 2 * sm_count());
+    const int HB = heads_simt(G);
+    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTile, sm_count());
 }
 
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
     const int G = Hq / Hkv;
-    if (max_tokens <= (kTile < kTileTc ? kTile : kTileTc)) return 0;      // one tile: nothing to join
+    if (max_tokens <= (kTile < kTileTc ? kTile : kTileTc)) return 16;     // one tile: nothing to join
     const size_t tc = (size_t)grid_tc(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_tc(G));
-    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G) * 2 * part_floats(d, kHB);
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_simt(G));
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 
-template <typename T, int D>
+template <typename T, int D, int HB>
 static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
+    using S = Simt<T, D, HB>;
     p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile;
-    const size_t smem = sizeof(float) * (kTile * (D + 4) + kTile * D + kHB * D + kHB * kTile + 3 * kHB);
-    cudaError_t e = allow_smem<paged_decode_simt_kernel<T, D>>((uint32_t)smem);
+    auto *kernel = paged_decode_simt_kernel<T, D, HB>;
+    cudaError_t e = allow_smem<paged_decode_simt_kernel<T, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
     const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
-    if ((e = launch_dependent(paged_decode_simt_kernel<T, D>, dim3(grid), 256, smem, st, 1, p)) != cudaSuccess) return e;
-    return launch_join<T, D, kTile, kHB>(p, grid, st);
+    if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
+    return launch_join<T, D, kTile, HB>(p, grid, st);
 }
 
 template <typename T>
 static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) {
+    const bool four = heads_simt(p.G) == 4;
     switch (d) {
-        case 32: return paged_simt<T, 32>(p, st);
-        case 64: return paged_simt<T, 64>(p, st);
-        case 128: return paged_simt<T, 128>(p, st);
+        case 32: return four ? paged_simt<T, 32, 4>(p, st) : paged_simt<T, 32, 8>(p, st);
+        case 64: return four ? paged_simt<T, 64, 4>(p, st) : paged_simt<T, 64, 8>(p, st);
+        case 128: return four ? paged_simt<T, 128, 4>(p, st) : paged_simt<T, 128, 8>(p, st);
     }
     return cudaErrorInvalidValue;
 }

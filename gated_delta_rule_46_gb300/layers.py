@@ -277,10 +277,9 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
         new.append(lse)
     if workspace is None:
         size = _fn("kda_paged_decode_workspace_size")(N, cols * ps, Hq, Hkv, d, code)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-            new.append(workspace)
-    size = 0 if workspace is None else _dims(workspace, "workspace", 1)[0]
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        new.append(workspace)
+    size = _dims(workspace, "workspace", 1)[0]
     _call("kda_paged_decode", dev, stream, new, q.data_ptr(), ldq, kp, vp, P, ps, tp, cols,
           _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
           d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),

@@ -130,7 +130,7 @@ kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t
                               int d, kda_dtype_t dtype, uint32_t *status, kda_stream_t stream);
 
 /* Workspace of kda_paged_decode (its partial results) for sequences of up to
- * max_tokens = max_pages page_size tokens; 0 where none of them can be split. */
+ * max_tokens = max_pages page_size tokens. */
 size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq, int Hkv, int d,
                                        kda_dtype_t dtype);
 
@@ -147,8 +147,7 @@ size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq,
  *                table's end, both recorded in *status
  *   out          [num_seqs, Hq, d] of dtype (written)
  *   lse          [num_seqs, Hq] float32 (written), or NULL
- *   workspace    16-byte aligned, kda_paged_decode_workspace_size() bytes; may be
- *                NULL where that is 0
+ *   workspace    16-byte aligned, kda_paged_decode_workspace_size() bytes
  * Tokens on a page whose id lies outside the cache are recorded and left out.
  * A table covers at most 2^30 tokens per sequence.
  */

@@ -273,7 +273,7 @@ def test_refusals():
     with pytest.raises(KDAError):
         paged_decode(q, kc[:, :, :12].contiguous(), vc[:, :, :12].contiguous(), table, n)   # page size 12
     with pytest.raises(KDAError):
-        paged_decode(q, kc, vc, table.repeat(1, 40), n, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
+        paged_decode(q, kc, vc, table, n, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
     k = torch.zeros(1, 2, 64, dtype=BF, device=dev)
     with pytest.raises(ValueError):
         paged_append(k, k, kc[:, :1].contiguous(), vc, table, n)
