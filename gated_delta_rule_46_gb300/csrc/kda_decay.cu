@@ -17,7 +17,6 @@ namespace kda {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) decay_segments_kernel(const DecaySegs p, const float *__restrict__ log_decay,
                                                              const float *__restrict__ init, int state) {
-    ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int n = (int)((unsigned)blockIdx.y / (unsigned)p.H), h = (int)blockIdx.y - n * p.H;
     int bos, eos, before = 0;
@@ -34,6 +33,7 @@ __global__ void __launch_bounds__(256) decay_segments_kernel(const DecaySegs p, 
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) s = *reinterpret_cast<const float4 *>(init + (int64_t)blockIdx.y * state + at);
     float4 *cell = reinterpret_cast<float4 *>(p.cells + ((int64_t)before * p.H + h) * state + at);
+    ptx::pdl_wait();        // the cells; the inputs were complete before the state pass let this kernel start
     // eight loads under way at a time: a store may not be overtaken by the loads after it
     constexpr int B = 8;
     for (int g0 = 0; g0 < segs; g0 += B) {

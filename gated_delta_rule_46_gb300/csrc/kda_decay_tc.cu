@@ -16,11 +16,13 @@
 // are split into three bf16 terms (24 bits) whose products accumulate in
 // float32, from zero in every chunk, before one float32 addition to the state.
 //
-// Roles of the 20 warps of a CTA (one CTA per SM): 0 and 1 take P out of TMEM; 2
-// loads by TMA, up to three chunks ahead, and issues the state's product; 3 issues
-// Q K^T, S^T Q^T and V^T P^T; 4-7 write the output; 8-11 split the decayed keys;
-// 12-19 hold the state, 64 key channels of one value channel per thread, and leave
-// its bf16 copy in TMEM, where the MMA takes it from.  mbarriers link them.
+// Roles of the 20 warps of a CTA (one CTA per SM): 0 and 1 take P out of TMEM, and a
+// thread of 0 loads by TMA, up to three chunks ahead; 2 issues the state's product; 3
+// issues Q K^T, S^T Q^T and V^T P^T; 4-7 write the output; 8-11 split the decayed
+// keys; 12-19 hold the state, 64 key channels of one value channel per thread, and
+// leave its bf16 copy in TMEM, where the MMA takes it from.  mbarriers link them.
+// The state pass of a segmented batch writes no output: there 4-11 split the keys and
+// 3 loads.
 //
 // What bounds it: a token of one head moves 4 d bf16 values and no more; with 128
 // channels that is 64 KB per chunk, 1.5 us at a CTA's share of the copy rate.  It
@@ -268,85 +270,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
-    ptx::pdl_wait();
+    // In the output pass over segments only the state's warps wait for the kernel before: all that it writes is their
+    // start states, and what came before the state pass was complete before any block of that pass let this one start.
+    const bool early = OUT && p.g.len > 0;
+    if (!early) ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     bool ok = true;
     Walk<D, OUT> walk;
     Item x;
+    // Loads the next chunk (one thread); false at the end, or if its stage does not get free.
+    int ls = 0, lround = 0, lt = 0, lt1 = 0, lcol = 0;
+    auto load = [&]() -> bool {
+        while (lt >= lt1) {
+            Item y;
+            if (!walk.next(p, y, false)) return false;
+            lt = y.t0;
+            lt1 = y.t1;
+            lcol = y.head * D;
+        }
+        if (lround > 0 && !wait_on(&bar[L::FREE + ls], lround - 1)) {
+            ok = false;
+            return false;
+        }
+        uint64_t *full = &bar[L::LD + ls];
+        uint8_t *st = sm + ls * L::stage;
+        ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
+#pragma unroll 1
+        for (int h = 0; h < HV; ++h) {
+            const int col = lcol + h * 64;
+            ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, lt, full);
+            if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, lt, full);
+            ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, lt, full);
+        }
+        lt += C;
+        if (++ls == NS) { ls = 0; ++lround; }
+        return true;
+    };
     // 96 registers a thread at launch (61,440); of the five warpgroups' 480 the state's two take 120 each
     if (warp < 4) {
         ptx::regs_dec<80>();
-        if (warp == 2 || (!OUT && warp == 3)) {                       // ---- loads, and the state's product
-            // one thread does whichever of the two can go ahead; without the output's products, one thread each
-            const bool loads = OUT || warp == 2, mults = OUT || warp == 3;
-            const int total = chunks_of<D, OUT>(p, loads);
+        if (warp == 2) {                                              // ---- the state's product
+            const int total = chunks_of<D, OUT>(p, true);
             if (ptx::elect_one()) {
                 const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
                 const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
-                int lc = 0, dc = 0, half = 0;                         // next chunk to load; next half chunk to multiply
-                int ls = 0, lp = 0, ds = 0, dp = 0;                   // their stages and rounds
-                int b = 0, bp = 0;                                    // the product's buffer and round
-                int t = 0, t1 = 0, col0 = 0;
-                long long since = clock64();
-                while ((mults ? dc : lc) < total) {
-                    bool did = false;
-                    if (loads && lc < total && (lp == 0 || ptx::mbar_test(&bar[L::FREE + ls], (lp - 1) & 1))) {
-                        while (t >= t1) {
-                            walk.next(p, x, false);
-                            t = x.t0;
-                            t1 = x.t1;
-                            col0 = x.head * D;
-                        }
-                        uint64_t *full = &bar[L::LD + ls];
-                        uint8_t *st = sm + ls * L::stage;
-                        ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
-    #pragma unroll 1
-                        for (int h = 0; h < HV; ++h) {
-                            const int col = col0 + h * 64;
-                            ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, t, full);
-                            if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, t, full);
-                            ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, t, full);
-                        }
-                        t += C;
-                        ++lc;
-                        if (++ls == NS) { ls = 0; ++lp; }
-                        did = true;
-                    }
-                    if (mults && ptx::mbar_test(&bar[L::TF + 2 * ds + half], dp & 1) &&
-                        (half == 1 || bp == 0 || ptx::mbar_test(&bar[L::DSFREE + b], (bp - 1) & 1))) {
+                int s = 0, sp = 0, b = 0, bp = 0;                     // the chunk's stage, the product's buffer; their rounds
+                for (int c = 0; c < total && ok; ++c) {
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        if (!wait_on(&bar[L::TF + 2 * s + half], sp) ||
+                            (half == 0 && bp > 0 && !wait_on(&bar[L::DSFREE + b], bp - 1))) { ok = false; break; }
                         ptx::tc_fence_after_sync();
                         const uint64_t a = dt + (b * 3 * L::term + half * 4096) / 16;
-                        const uint64_t v = sdesc_mn_sw128(base + ds * L::stage + L::v, kTile) + half * (4096 >> 4);
-    #pragma unroll 2
+                        const uint64_t v = sdesc_mn_sw128(base + s * L::stage + L::v, kTile) + half * (4096 >> 4);
+#pragma unroll 2
                         for (int e = 0; e < 6; ++e)
-                            ptx::mma_bf16_ss(tmem + tm_ds(b), v + (e & 1) * (2048 >> 4), a + ((e >> 1) * L::term + (e & 1) * 2048) / 16,
-                                             id, half > 0 || e > 0);
+                            ptx::mma_bf16_ss(tmem + tm_ds(b), v + (e & 1) * (2048 >> 4),
+                                             a + ((e >> 1) * L::term + (e & 1) * 2048) / 16, id, half > 0 || e > 0);
                         ptx::mma_commit(&bar[L::DSH + 2 * b + half]);
-                        if (half == 1) {
-                            ptx::mma_commit(&bar[L::DS + b]);
-                            ptx::mma_commit(&bar[L::FREE + ds]);
-                            ++dc;
-                            if (++ds == NS) { ds = 0; ++dp; }
-                            if (++b == NB) { b = 0; ++bp; }
-                        }
-                        half ^= 1;
-                        did = true;
                     }
-                    const long long now = clock64();
-                    if (did) since = now;
-                    else if (now - since > kWaitBudget) { ok = false; break; }
+                    ptx::mma_commit(&bar[L::DS + b]);
+                    ptx::mma_commit(&bar[L::FREE + s]);
+                    if (++s == NS) { s = 0; ++sp; }
+                    if (++b == NB) { b = 0; ++bp; }
                 }
             }
+        } else if (!OUT && warp == 3) {                               // ---- loads of the state pass
+            if (ptx::elect_one())
+                while (load()) {}
         } else if (warp < 2) {                                        // ---- P: thread = token of the chunk
             if (OUT) {
                 const int i = threadIdx.x;
                 int c = 0;
-                while (ok && walk.next(p, x, false)) {
+                Walk<D, OUT> mine;                                    // (`walk` is the loads')
+                if (i == 0)
+                    while (lround == 0 && load()) {}
+                __syncwarp();
+                while (ok && mine.next(p, x, false)) {
                     const float l2 = log2_decay(p, x.head);
                     for (int t = x.t0, t1 = x.t1; t < t1; t += C, ++c) {
                         const int b = c & 1;
+                        // P is a chunk ahead of its use: there is time to wait for the stage of two chunks ago
+                        if (c >= 2 && i == 0) load();
                         // the output products of two chunks ago have read this buffer, and so has their output if it had to
-                        ok = warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
+                        ok = __all_sync(0xffffffffu, ok) && warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
                         if (!ok) break;
                         ptx::tc_fence_after_sync();
                         uint8_t *sp = sm + L::P + b * kTile;
@@ -577,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {                                                      // ---- the state: lane = value channel
         ptx::regs_inc<120>();
+        if (early) ptx::pdl_wait();
         if ((warp & 3) * 32 < D) {
             constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
             const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;

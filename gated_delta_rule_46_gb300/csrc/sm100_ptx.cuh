@@ -176,6 +176,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr));
 }
+// Uses of r do not move before this point: what a load from TMEM brings is there only after its wait.
+__device__ __forceinline__ void keep(float (&r)[16]) {
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]));
+}
 // The same, 8 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
     uint32_t *u = reinterpret_cast<uint32_t *>(r);
