@@ -24,15 +24,18 @@
 // The state pass of a segmented batch writes no output: there 4-11 split the keys and
 // 3 loads.
 //
-// What bounds it: a token of one head moves 4 d bf16 values and no more; with 128
-// channels that is 64 KB per chunk, 1.5 us at a CTA's share of the copy rate.  It
-// takes 1.8: 133k ragged tokens of 32 heads run in 805 us, 5.5 TB/s.  No unit is full
-// (tensor pipe 38 %, issue slots 57 %, shared memory 36 %): what is left is each
-// chunk's chain from the state through its product with q to the next state, and the
-// roles in each other's way.  d = 64: 697 us for as many tokens and heads.  Measured
-// before, at that batch: S's copy in shared memory, which leaves room for two stages
-// of loads, 1034 us (917 in TMEM); waits that are calls, 1173; all warps at 96
-// registers, 918 (810).
+// What bounds it, of a chunk with 128 channels: its 64 KB from and to HBM are 1.5 us
+// at a CTA's share of the copy rate, and its traffic in shared memory about 2,700
+// cycles, 1.4 us: the MMAs' operands 1,470 (state's product 770, its V read once per
+// term), the keys' terms 510, TMA in and out 510, P and the output 190.  Together they
+// take 1.8: 133k ragged tokens of 32 heads run in 805 us, 5.5 TB/s, with the tensor
+// pipe 38 % and the issue slots 57 % busy, and the two threads that issue MMAs are
+// held up by them nearly all of the time.  d = 64: 697 us for as many tokens and heads.
+//   Measured at that batch, where not noted: S's copy in shared memory, which leaves
+// room for two stages of loads, 1034 us (917 in TMEM); waits that are calls, 1173; all
+// warps at 96 registers, 918 (810); loads by an output warp 884, in pieces between the
+// state's products 1079, keys and values in stages of their own 826; the output's
+// next part out of TMEM ahead, 811.
 #include <cuda.h>
 
 #include "kda_decay.cuh"

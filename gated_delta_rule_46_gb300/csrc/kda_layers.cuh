@@ -118,6 +118,29 @@ inline cudaError_t allow_smem(uint32_t bytes) {
     return e;
 }
 
+// Clusters of S <= 8 CTAs of `Kernel` that run at a time on the current device, always asked for with the same block and
+// shared memory: it depends on how many SMs each of the GPU's clusters of SMs has, so it is the driver that knows.
+template <auto Kernel>
+inline int cluster_room(int S, unsigned block, uint32_t smem) {
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = known[dev][S].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) known[dev][S].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Launches `kernel` so that its start may overlap the end of the kernel before
 // it in the stream: the kernel calls griddepcontrol.wait before it touches
 // anything that another kernel writes, and so does every one of its blocks

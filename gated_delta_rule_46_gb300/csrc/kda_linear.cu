@@ -520,11 +520,17 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     constexpr uint32_t kRoom = 200 * 1024;      // all of an SM's: the weights under way are what hides HBM's latency
     rp.stages = (int)(kRoom / stage) < 12 ? (int)(kRoom / stage) : 12;
     const int64_t tiles = ((p.N + 127) / 128) * ((p.M + rp.NT - 1) / rp.NT);
-    // Split K over a cluster while one CTA per SM still has room for it and each keeps at least four steps.  64 x 4096
-    // x 4096 (32 tiles): S = 4 takes 10.6 us; with two smaller CTAs per SM S = 4 takes 11.2 and S = 8 11.9.
-    const int64_t slots = sm_count(), kbs = (p.K + kBK - 1) / kBK;
-    rp.S = 1;
-    while (rp.S < 8 && tiles * rp.S * 2 <= slots && kbs / (rp.S * 2) >= 4) rp.S *= 2;
+    const cudaError_t e = allow_smem<linear_rows_kernel<ACT, F32, LOAD>>(kRoom + 1024);
+    if (e != cudaSuccess) return e;
+    // Split K over the largest cluster of which all tiles' run at a time, one CTA per SM, with at least four steps for
+    // each CTA.  64 x 4096 x 4096 (32 tiles): S = 4 takes 10.6 us; with two smaller CTAs per SM S = 4 takes 11.2 and S =
+    // 8 11.9.  64 x 5120 x 4096 (40 tiles): S = 3 takes 12.7, S = 2 14.7; 64 x 2560 x 4096 (20 tiles): S = 7, of which
+    // no more than 15 run at a time, 16.0, S = 4 9.4.
+    const int64_t kbs = (p.K + kBK - 1) / kBK;
+    rp.S = 8;
+    while (rp.S > 1 && (kbs / rp.S < 4 || tiles > cluster_room<linear_rows_kernel<ACT, F32, LOAD>>(
+                                                      rp.S, LOAD ? 448 : 192, kRoom + 1024)))
+        --rp.S;
     uint32_t smem = rp.stages * stage;
     if (rp.S > 1 && smem < (uint32_t)rp.NT * 512u) smem = rp.NT * 512u;
     smem += 1024;
@@ -533,8 +539,6 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
                   !make_map_2d(&mx, p.x, true, p.M, p.K, p.ldx * 2, rp.NT)))
         return cudaErrorInvalidValue;
     auto *kernel = linear_rows_kernel<ACT, F32, LOAD>;
-    const cudaError_t e = allow_smem<linear_rows_kernel<ACT, F32, LOAD>>(kRoom + 1024);
-    if (e != cudaSuccess) return e;
     const int64_t mt = (p.M + rp.NT - 1) / rp.NT;
     return launch_dependent(kernel, dim3((unsigned)((p.N + 127) / 128 * rp.S), (unsigned)mt), LOAD ? 448 : 192, smem, st,
                             rp.S, mw, mx, rp);
