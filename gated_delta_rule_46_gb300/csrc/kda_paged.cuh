@@ -21,10 +21,12 @@ struct Split {
     int n;            // sequence
 };
 
-__device__ __forceinline__ int clamp_len(const PagedParams &p, int n, bool tell) {
-    int len = p.lens[n];
+__device__ __forceinline__ int clamped(const PagedParams &p, int len) {
     const int64_t cap = (int64_t)p.max_pages << p.page_shift;
-    const int c = len < 0 ? 0 : (len > cap ? (int)cap : len);
+    return len < 0 ? 0 : (len > cap ? (int)cap : len);
+}
+__device__ __forceinline__ int clamp_len(const PagedParams &p, int n, bool tell) {
+    const int len = p.lens[n], c = clamped(p, len);
     if (tell && c != len) report_status(p.status, KDA_ERR_INVALID_ARG);
     return c;
 }

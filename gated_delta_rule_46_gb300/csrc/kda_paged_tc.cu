@@ -61,16 +61,19 @@ struct Lay {
 };
 
 // The tiles of this CTA in order: (sequence, item, tile); every role walks its
-// own copy.
+// own copy.  The next sequence's length is read a sequence ahead.
 struct Walk {
     int64_t w, w1, nt, tile;
-    int n, item, items;
+    int n, item, items, len, raw, ahead;      // len: raw, clamped to the table
     __device__ void start(const PagedParams &p, const Split &sp, int items_) {
         items = items_;
         w = (int64_t)blockIdx.x * sp.W / sp.g;
         w1 = (int64_t)(blockIdx.x + 1) * sp.W / sp.g;
         n = sp.n;
-        nt = tiles_of<TILE>(p, n);
+        raw = p.lens[n];
+        len = clamped(p, raw);
+        ahead = n + 1 < p.N ? p.lens[n + 1] : 0;
+        nt = (len + TILE - 1) / TILE;
         item = (int)((w - sp.cum * items) / nt);
         tile = (w - sp.cum * items) - item * nt;
     }
@@ -82,7 +85,12 @@ struct Walk {
         tile = 0;
         if (++item == items) {
             item = 0;
-            do { ++n; nt = tiles_of<TILE>(p, n); } while (nt == 0);
+            do {
+                raw = ahead;
+                len = clamped(p, raw);
+                ahead = ++n + 1 < p.N ? p.lens[n + 1] : 0;
+            } while (len == 0 && n < p.N);
+            nt = (len + TILE - 1) / TILE;
         }
     }
 };
@@ -179,41 +187,46 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
 
     if (warp == 0) {                                              // ---- loads: lane = page of the tile
-        int t = 0;
-        while (ok && wk.more()) {
-            const int len = clamp_len(p, wk.n, lane == 0);
-            const int kvh = wk.item / nb;
-            const int64_t first = wk.tile, last = wk.last();
-            for (int64_t i = first; i < last; ++i, ++t) {
-                const int at = (int)(i * TILE) + lane * rows;     // this page's first token of the tile
-                int page = -1;
-                if (lane < pieces && at < len) {
-                    page = p.table[(int64_t)wk.n * p.max_pages + (at >> p.page_shift)];
-                    if (page < 0 || page >= p.num_pages) {
-                        report_status(p.status, KDA_ERR_INVALID_ARG);
-                        page = -1;
-                    }
-                }
-                const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t bytes = (uint32_t)__popc(mask) * rows * 128u * HALVES;
-                const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at & ((1 << p.page_shift) - 1)));
-                const int s = t % NS;
-                for (int kv = 0; kv < 2; ++kv) {
-                    uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
-                    if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
-                    uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * 128;
-                    if (lane == 0) {
-                        if (kv == 0) s_mask[t & 7] = mask;
-                        ptx::mbar_arrive_expect_tx(full, bytes);
-                    }
-                    __syncwarp();
-                    if (page >= 0)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h) ptx::tma_load_2d(dst + h * kSub, kv ? &mv : &mk, h * 64, y, full);
-                }
-                if (!ok) break;
+        // a tile's page is looked up while the tile before it is loaded
+        int64_t i = wk.tile, first = i, last = wk.last();
+        auto lookup = [&](int at) {
+            return lane < pieces && at < wk.len ? p.table[(int64_t)wk.n * p.max_pages + (at >> p.page_shift)] : 0;
+        };
+        int told = -1, at = (int)(i * TILE) + lane * rows, id = lookup(at);     // at: this page's first token of the tile
+        for (int t = 0; ok && wk.more(); ++t) {
+            if (wk.n != told) {
+                told = wk.n;
+                if (lane == 0 && wk.raw != wk.len) report_status(p.status, KDA_ERR_INVALID_ARG);
             }
-            wk.next_item(p, last - first);
+            const int kvh = wk.item / nb, at0 = at;
+            int page = -1;
+            if (lane < pieces && at < wk.len) {
+                if (id >= 0 && id < p.num_pages) page = id;
+                else report_status(p.status, KDA_ERR_INVALID_ARG);
+            }
+            if (++i == last) {
+                wk.next_item(p, last - first);
+                if (wk.more()) { first = i = wk.tile; last = wk.last(); }
+            }
+            at = (int)(i * TILE) + lane * rows;
+            id = wk.more() ? lookup(at) : 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+            const uint32_t bytes = (uint32_t)__popc(mask) * rows * 128u * HALVES;
+            const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at0 & ((1 << p.page_shift) - 1)));
+            const int s = t % NS;
+            for (int kv = 0; kv < 2; ++kv) {
+                uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
+                if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
+                uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * 128;
+                if (lane == 0) {
+                    if (kv == 0) s_mask[t & 7] = mask;
+                    ptx::mbar_arrive_expect_tx(full, bytes);
+                }
+                __syncwarp();
+                if (page >= 0)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) ptx::tma_load_2d(dst + h * kSub, kv ? &mv : &mk, h * 64, y, full);
+            }
         }
     } else if (warp == 1) {                                       // ---- MMAs
         if (ptx::elect_one()) {
@@ -260,7 +273,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 2) {                                       // ---- rows of V without a token
         int t = 0;
         while (ok && wk.more()) {
-            const int len = clamp_len(p, wk.n, false);
+            const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
             for (int64_t i = first; i < last; ++i, ++t) {
                 const int s = t % NS;
@@ -290,8 +303,6 @@ __global__ void __launch_bounds__(384, 1)
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
-            if (item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
-            if (!ok) break;
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
             // eight channels per lane and step, all loads first
@@ -306,6 +317,8 @@ __global__ void __launch_bounds__(384, 1)
                     else u[i] = load8(q + j * 8);
                 }
             }
+            if (item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
+            if (!ok) break;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int j = lane + i * 32, h = j / (D / 8), c = j % (D / 8);
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(384, 1)
               *sums = reinterpret_cast<float *>(sm + L::SUM), *maxs = sums + 8 * HB;
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
-            const int len = clamp_len(p, wk.n, false);
+            const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
             float m[HR], l[HR];
 #pragma unroll
@@ -391,7 +404,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (j == 0)
 #pragma unroll
-                for (int h = 0; h < HR; ++h) maxs[ib * HB + h] = m[h];
+                for (int h = 0; h < HR; h += 4)
+                    *reinterpret_cast<float4 *>(maxs + ib * HB + h) = make_float4(m[h], m[h + 1], m[h + 2], m[h + 3]);
             warp_arrive(&bar[IREADY + ib]);
             ++item_no;
             wk.next_item(p, last - first);
@@ -432,23 +446,40 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             const bool whole = first == 0 && last == wk.nt;
             float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
+            // head d's sum and maximum by thread d; outputs by all, with a sum that is 0 or at least 1 (a maximum's own
+            // weight), or infinite or NaN
+            if (d < hb) {
+                const float l = (sums[ib * 4 * HB + d] + sums[(ib * 4 + 1) * HB + d]) +
+                                (sums[(ib * 4 + 2) * HB + d] + sums[(ib * 4 + 3) * HB + d]);
+                const float m = maxs[ib * HB + d];
+                if (!whole) { part[2 * d] = m; part[2 * d + 1] = l; }
+                else if (p.lse) p.lse[row0 + d] = (m + log2f(l)) / kLog2E;
+            }
+            float l[HR];
+            if (whole) {
 #pragma unroll
-            for (int h = 0; h < HR; ++h) {
-                if (h >= hb) break;
-                const float l = (sums[ib * 4 * HB + h] + sums[(ib * 4 + 1) * HB + h]) +
-                                (sums[(ib * 4 + 2) * HB + h] + sums[(ib * 4 + 3) * HB + h]);
-                const float m = maxs[ib * HB + h];
-                if (whole) {
-                    if (d < D)
-                        static_cast<__nv_bfloat16 *>(p.out)[(row0 + h) * D + d] =
-                            __float2bfloat16_rn(l > 0.f ? acc[h] / l : (l == 0.f ? 0.f : l));
-                    if (d == 0 && p.lse) p.lse[row0 + h] = (m + log2f(l)) / kLog2E;
-                } else {
-                    if (d < D) part[HB * 2 + h * D + d] = acc[h];
-                    if (d == 0) { part[2 * h] = m; part[2 * h + 1] = l; }
+                for (int h = 0; h < HR; h += 4) {
+                    float x[4][4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) ld4(sums + (ib * 4 + w) * HB + h, x[w]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) l[h + e] = (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
                 }
             }
             warp_arrive(&bar[IFREE + ib]);
+            if (d < D) {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row0 * D + d;
+                if (whole) {
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+                        if (h < hb)
+                            out[h * D] = __float2bfloat16_rn(l[h] > 0.f ? __fdividef(acc[h], l[h]) : (l[h] == 0.f ? 0.f : l[h]));
+                } else {
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+                        if (h < hb) part[HB * 2 + h * D + d] = acc[h];
+                }
+            }
             ++item_no;
             wk.next_item(p, last - first);
         }
