@@ -72,9 +72,10 @@ struct AppendParams {
     int num_seqs, Hkv;
     int64_t total;
     int row_bytes;                  // d x element size: one head of one token
+    int lanes_log2;                 // lanes per token (of the launch's choosing)
     uint32_t *status;
 };
-cudaError_t launch_paged_append(const AppendParams &p, bool vec16, cudaStream_t st);
+cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st);
 
 struct PagedParams {
     const void *q;

@@ -142,7 +142,7 @@ kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t
         return KDA_ERR_INVALID_ARG;
     const kda::AppendParams p{k, v, ldk * e, ldv * e, k_cache, v_cache, num_pages, page_shift(page_size),
                               page_table, max_pages, start_pos, cu_seqlens, num_seqs, Hkv, total_tokens,
-                              (int)(d * e), status};
+                              (int)(d * e), 0, status};
     const bool vec16 = aligned(k, 16) && aligned(v, 16) && (ldk * e) % 16 == 0 && (ldv * e) % 16 == 0;
     return from_cuda(kda::launch_paged_append(p, vec16, reinterpret_cast<cudaStream_t>(stream)));
 }
