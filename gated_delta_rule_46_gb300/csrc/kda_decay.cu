@@ -59,8 +59,8 @@ cudaError_t launch_decay_segments(const DecaySegs &p, const float *log_decay, co
 }
 
 // ---------------------------------------------------------------------------
-// float32 chunk kernel (float32 inputs, and head sizes and alignments that the
-// tensor-core kernel does not take): one CTA per (sequence or segment, head, JB
+// float32 chunk kernel (float32 inputs, and bf16 rows that no 16-byte copy can
+// start on): one CTA per (sequence or segment, head, JB
 // value channels), tokens in chunks of C = 32.  The value channels (columns of
 // S) do not mix, so a chain splits exactly over them; the C x C products q . k
 // are repeated per block.  Per chunk, all sums in float32 registers:

@@ -1,5 +1,5 @@
 // kda_decay_tc.cu -- the chunked form of linear attention with one decay per
-// head (bf16, dk = dv = 128 or 64) on the tensor cores.
+// head (bf16) on the tensor cores, in tiles of D = 64 or 128 channels for dk, dv <= D.
 //
 // Per chain (sequence, head), in chunks of C = 64 tokens with n of them real,
 // start state S and lambda = exp(log_decay):
@@ -28,9 +28,9 @@
 // at a CTA's share of the copy rate, and its traffic in shared memory about 2,700
 // cycles, 1.4 us: the MMAs' operands 1,470 (state's product 770, its V read once per
 // term), the keys' terms 510, TMA in and out 510, P and the output 190.  Together they
-// take 1.8: 133k ragged tokens of 32 heads run in 805 us, 5.5 TB/s, with the tensor
+// take 1.8: 133k ragged tokens of 32 heads run in 803 us, 5.5 TB/s, with the tensor
 // pipe 38 % and the issue slots 57 % busy, and the two threads that issue MMAs are
-// held up by them nearly all of the time.  d = 64: 697 us for as many tokens and heads.
+// held up by them nearly all of the time.  d = 64: 635 us for as many tokens and heads.
 //   Measured at that batch, where not noted: S's copy in shared memory, which leaves
 // room for two stages of loads, 1034 us (917 in TMEM); waits that are calls, 1173; all
 // warps at 96 registers, 918 (810); loads by an output warp 884, in pieces between the
@@ -101,6 +101,7 @@ struct Params {
     int64_t ldv;
     const int32_t *order;       // longest-first order of the sequences, or nullptr
     int expire;                 // test support
+    int dk, dv;                 // at most D
 };
 
 // One piece of a chain: tokens [t0, t1) of one head.
@@ -112,11 +113,11 @@ struct Item {
 };
 
 // Walks this CTA's items in order; every role walks its own copy.
-template <int D, bool OUT>
+template <int D, bool OUT, bool FULL>
 struct Walk {
     unsigned it = 0;
     __device__ __forceinline__ bool next(const Params &p, Item &x, bool tell) {
-        constexpr int64_t kState = (int64_t)D * D;
+        const int64_t kState = FULL ? (int64_t)D * D : (int64_t)p.dk * p.dv;
         const unsigned H = (unsigned)p.g.H;
         if (p.g.len == 0) {
             // rows of gridDim.x chains, dealt out forwards and backwards in turn: with the longest first, every
@@ -156,9 +157,9 @@ struct Walk {
 };
 
 // Chunks of all of a CTA's items.
-template <int D, bool OUT>
+template <int D, bool OUT, bool FULL>
 __device__ __forceinline__ int chunks_of(const Params &p, bool tell) {
-    Walk<D, OUT> walk;
+    Walk<D, OUT, FULL> walk;
     Item x;
     int total = 0;
     while (walk.next(p, x, tell)) total += (x.t1 - x.t0 + C - 1) / C;
@@ -221,11 +222,12 @@ __device__ __forceinline__ void split3(const uint4 &k, float w, uint4 &t1, uint4
     cut(t3);
 }
 
-// sum_{s <= i} P_is v_sj for token i of the chunk at token t and the channel that
-// is element `at` of a row, v from global memory.
-__device__ __forceinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int at, int i) {
+// sum_{s <= i} P_is v_sj for token i of the chunk at token t and value channel j
+// of a head, v from global memory.
+__device__ __forceinline__ float real_pairs(const Params &p, const uint8_t *sp, int t, int t1, int head, int j, int i) {
     float y = 0.f;
-    if (t + i >= t1) return y;
+    if (t + i >= t1 || j >= p.dv) return y;
+    const int at = head * p.dv + j;
 #pragma unroll 1
     for (int s = 0; s <= i; ++s)
         y = fmaf(to_f32(*reinterpret_cast<const __nv_bfloat16 *>(sp + swz(i, s >> 3) + (s & 7) * 2)),
@@ -233,7 +235,10 @@ __device__ __forceinline__ float real_pairs(const Params &p, const uint8_t *sp, 
     return y;
 }
 
-template <int D, bool OUT>
+// FULL: dk = dv = D, 2-D tensor maps [token][head, channel]; else 3-D maps, which give zeros for the channels that are not
+// there, and states of dk x dv (32 x 32, 32 prompts of up to 2048 tokens, 16 heads: 93 us, 501 on the CUDA cores; 64 x
+// 128: 122 us, 1418; full heads by 3-D maps: 823 us for the ragged batch above, 803 by 2-D ones).
+template <int D, bool OUT, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Params p) {
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(sm);
+    const int dk = FULL ? D : p.dk, dv = FULL ? D : p.dv;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
@@ -279,17 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!early) ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     bool ok = true;
-    Walk<D, OUT> walk;
+    Walk<D, OUT, FULL> walk;
     Item x;
     // Loads the next chunk (one thread); false at the end, or if its stage does not get free.
-    int ls = 0, lround = 0, lt = 0, lt1 = 0, lcol = 0;
+    int ls = 0, lround = 0, lt = 0, lt1 = 0, lhead = 0;
     auto load = [&]() -> bool {
         while (lt >= lt1) {
             Item y;
             if (!walk.next(p, y, false)) return false;
             lt = y.t0;
             lt1 = y.t1;
-            lcol = y.head * D;
+            lhead = y.head;
         }
         if (lround > 0 && !wait_on(&bar[L::FREE + ls], lround - 1)) {
             ok = false;
@@ -300,10 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive_expect_tx(full, (OUT ? 3 : 2) * HV * kTile);
 #pragma unroll 1
         for (int h = 0; h < HV; ++h) {
-            const int col = lcol + h * 64;
-            ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, lt, full);
-            if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, lt, full);
-            ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, lt, full);
+            if (FULL) {
+                const int col = lhead * D + h * 64;
+                ptx::tma_load_2d(st + L::k + h * L::half, &mk, col, lt, full);
+                if (OUT) ptx::tma_load_2d(st + L::q + h * L::half, &mq, col, lt, full);
+                ptx::tma_load_2d(st + L::v + h * kTile, &mv, col, lt, full);
+            } else {
+                ptx::tma_load_3d(st + L::k + h * L::half, &mk, h * 64, lhead, lt, full);
+                if (OUT) ptx::tma_load_3d(st + L::q + h * L::half, &mq, h * 64, lhead, lt, full);
+                ptx::tma_load_3d(st + L::v + h * kTile, &mv, h * 64, lhead, lt, full);
+            }
         }
         lt += C;
         if (++ls == NS) { ls = 0; ++lround; }
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         ptx::regs_dec<80>();
         if (warp == 2) {                                              // ---- the state's product
-            const int total = chunks_of<D, OUT>(p, true);
+            const int total = chunks_of<D, OUT, FULL>(p, true);
             if (ptx::elect_one()) {
                 const uint32_t id = ptx::idesc_bf16_f32(128, D) | kAMn | kBMn;
                 const uint64_t dt = sdesc_mn_sw128(base + L::T, kTile);
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (OUT) {
                 const int i = threadIdx.x;
                 int c = 0;
-                Walk<D, OUT> mine;                                    // (`walk` is the loads')
+                Walk<D, OUT, FULL> mine;                                    // (`walk` is the loads')
                 if (i == 0)
                     while (lround == 0 && load()) {}
                 __syncwarp();
@@ -361,18 +373,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after_sync();
                         uint8_t *sp = sm + L::P + b * kTile;
                         // (columns 32-63 of rows 0-31 are never written: zero from the start)
-    #pragma unroll 1
+#pragma unroll 1
                         for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 32) {
                             float d[32];
                             ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
                             const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
                             ptx::tmem_ld_wait();
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
                             if (j0 == 32 * warp)
-    #pragma unroll
+#pragma unroll
                                 for (int e = 0; e < 32; ++e) d[e] = e <= lane ? d[e] : 0.f;
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 32; e += 8) st_chunk(sp, swz(i, (j0 + e) >> 3), d + e);
                         }
                         ptx::fence_async_smem();
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (OUT && warp == 3) {                                // ---- Q K^T, S^T Q^T, V^T P^T
-            const int total = chunks_of<D, OUT>(p, false);
+            const int total = chunks_of<D, OUT, FULL>(p, false);
             if (ptx::elect_one()) {
                 const uint32_t id = ptx::idesc_bf16_f32(128, 64);
                 int s = 0, sp = 0, ns = 0, np = 0;                    // this chunk's stage and round, the next one's
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (c >= 2 && !wait_on(&bar[L::OFREE + b], phase ^ 1))) { ok = false; break; }
                         ptx::tc_fence_after_sync();
                         const uint64_t q = ptx::sdesc_kmajor_sw128(st + L::q);
-    #pragma unroll 2
+#pragma unroll 2
                         for (int k = 0; k < D / 16; ++k)
                             ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * L::half + (k & 3) * 32) >> 4),
                                              id, k > 0);
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // The next chunk's scores go ahead of this chunk's output if its tiles are here, else after it: their
                     // load may be waiting for this very chunk's stage.
                     bool todo = c + 1 < total;
-    #pragma unroll 1
+#pragma unroll 1
                     for (int pass = 0; pass < 2; ++pass) {
                         if (todo && (pass == 1 || c < 0 || ptx::mbar_test(&bar[L::LD + ns], np & 1))) {
                             todo = false;
@@ -414,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t sn = base + ns * L::stage;
                             // rows 0-63: Q K^T; rows 64-127 (K K^T) are not read
                             const uint64_t q = ptx::sdesc_kmajor_sw128(sn + L::q), kd = ptx::sdesc_kmajor_sw128(sn + L::k);
-    #pragma unroll 2
+#pragma unroll 2
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
                                 ptx::mma_bf16_ss(tmem + TM_P, q + at, kd + at, id, k > 0);
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             !wait_on(&bar[L::TF + 2 * s + 1], sp)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
                         const uint64_t a = sdesc_mn_sw128(st + L::v, kTile), pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
-    #pragma unroll 2
+#pragma unroll 2
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
                         ptx::mma_commit(&bar[L::OD + b]);
@@ -478,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (probe != 0.f)
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                o[e] = real_pairs(p, sp, t, t1, head * D + j0 + (lane >> 2) + ((e >> 1) & 1) * 8, ic + (e >> 2) * 8 + (e & 1));
+                                o[e] = real_pairs(p, sp, t, t1, head, j0 + (lane >> 2) + ((e >> 1) & 1) * 8,
+                                                  ic + (e >> 2) * 8 + (e & 1));
                         uint32_t u[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -500,14 +513,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int on = min(t1 - t, C);
                     if (on == C) {
                         if (tid == 0) {
-                            ptx::tma_store_2d(&mo, head * D, t, so);
-                            if (HV == 2) ptx::tma_store_2d(&mo, head * D + 64, t, so + kTile);
+                            if (FULL) {
+                                ptx::tma_store_2d(&mo, head * D, t, so);
+                                if (HV == 2) ptx::tma_store_2d(&mo, head * D + 64, t, so + kTile);
+                            } else {
+                                ptx::tma_store_3d(&mo, 0, head, t, so);
+                                if (HV == 2 && dv > 64) ptx::tma_store_3d(&mo, 64, head, t, so + kTile);
+                            }
                             ptx::bulk_commit();
                         }
                     } else {
                         for (int i = tid; i < on * (D / 8); i += 128) {
                             const int r = i / (D / 8), ch = i % (D / 8);
-                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.g.H + head) * D + ch * 8) =
+                            if (ch * 8 >= dv) continue;
+                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(t + r) * p.g.H + head) * dv + ch * 8) =
                                 *reinterpret_cast<const uint4 *>(so + (ch >> 3) * kTile + swz(r, ch & 7));
                         }
                         asm volatile("bar.sync 1, 128;" ::: "memory");   // read before the next chunk's tile
@@ -591,18 +610,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((warp & 3) * 32 < D) {
             constexpr int KC = D / 2;                                     // key channels k0 .. k0 + KC - 1 per thread
             const int q = warp & 3, k0 = ((warp - 12) >> 2) * KC;
-            const int64_t mine = (int64_t)k0 * D + q * 32 + lane;
+            const int mine = k0 * dv + q * 32 + lane, rows = q * 32 + lane < dv ? dk - k0 : 0;
             const uint32_t at = tmem + ((uint32_t)q << 21);
             int c = 0;
             while (ok && walk.next(p, x, false)) {
                 const float l2 = log2_decay(p, x.head);
-                const float *from = x.from;
+                // (the real state's rows and columns only)
+                const float *from = x.from + mine;
+                const int have = x.from ? rows : 0;
                 float s[KC];
-    #pragma unroll
-                for (int e = 0; e < KC; ++e) s[e] = from ? from[mine + e * D] : 0.f;
+#pragma unroll
+                for (int e = 0; e < KC; ++e) {
+                    s[e] = (FULL ? x.from != nullptr : e < have) ? *from : 0.f;
+                    from += dv;
+                }
                 auto copy_out = [&](int e) {       // 16 channels as bf16 pairs
                     uint32_t u[8];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = pack_bf16(s[e + 2 * i], s[e + 2 * i + 1]);
                     ptx::tmem_st8(at + TM_S + (k0 + e) / 2, u);
                 };
@@ -611,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c > 0) ok = warp_wait(&bar[L::QS], c - 1);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < KC; e += 16) copy_out(e);
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before_sync();
@@ -625,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after_sync();
                     const uint32_t ds = at + tm_ds(c & (NB - 1)) + k0;
                     // 32 columns at a time: the next product may overwrite them as soon as the last have been read
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < KC; e += 32) {
                         float d[32];
                         ptx::tmem_ld16(ds + e, *reinterpret_cast<float(*)[16]>(d));
@@ -635,14 +659,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::tc_fence_before_sync();
                             warp_arrive(&bar[L::DSFREE + (c & (NB - 1))]);
                         }
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 32; ++i) s[e + i] = fmaf(f, s[e + i], d[i]);
                     }
                     if (more) {
                         ok = warp_wait(&bar[L::QS], c);
                         if (!ok) break;
                         ptx::tc_fence_after_sync();
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < KC; e += 16) copy_out(e);
                         ptx::tmem_st_wait();
                         ptx::tc_fence_before_sync();
@@ -650,9 +674,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                if (x.to)
-    #pragma unroll
-                    for (int e = 0; e < KC; ++e) x.to[mine + e * D] = s[e];
+                if (x.to) {
+                    float *to = x.to + mine;
+#pragma unroll
+                    for (int e = 0; e < KC; ++e) {
+                        if (FULL || e < rows) *to = s[e];
+                        to += dv;
+                    }
+                }
             }
         }
     }
@@ -679,19 +708,22 @@ size_t cells_at(int N) { return (kOrderAt + sizeof(int32_t) * (size_t)N + 1023) 
 
 }  // namespace
 
-size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D) {
+size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int dk, int dv) {
     const int len = decay_segment_tokens(total, N, H, sm_count(), kCost);
     if (len == 0 && (N == 1 || (int64_t)N * H <= sm_count())) return 0;
-    return cells_at(N) + decay_cells_bytes(total, N, H, len, D, D);
+    return cells_at(N) + decay_cells_bytes(total, N, H, len, dk, dv);
 }
 
-template <int D>
-static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t workspace_bytes, cudaStream_t st) {
+template <int D, bool FULL>
+static cudaError_t launch_tc(const DecayParams &d, int dk, int dv, void *workspace, size_t workspace_bytes, cudaStream_t st) {
     constexpr uint32_t kSmem = Lay<D, true>::bytes, kSmemState = Lay<D, false>::bytes;
     CUtensorMap mq, mk, mv, mo;
-    const uint64_t T = (uint64_t)d.total, cols = (uint64_t)d.H * D;
-    if (!make_map_2d(&mq, d.q, true, T, cols, d.ldq * 2, C) || !make_map_2d(&mk, d.k, true, T, cols, d.ldk * 2, C) ||
-        !make_map_2d(&mv, d.v, true, T, cols, d.ldv * 2, C) || !make_map_2d(&mo, d.out, true, T, cols, cols * 2, C))
+    const uint64_t T = (uint64_t)d.total, H = (uint64_t)d.H;
+    auto map = [&](CUtensorMap *m, const void *base, int d, uint64_t row_bytes) {
+        return FULL ? make_map_2d(m, base, true, T, H * d, row_bytes, C) : make_map_heads(m, base, T, H, d, row_bytes, C);
+    };
+    if (!map(&mq, d.q, dk, d.ldq * 2) || !map(&mk, d.k, dk, d.ldk * 2) || !map(&mv, d.v, dv, d.ldv * 2) ||
+        !map(&mo, d.out, dv, H * dv * 2))
         return cudaErrorInvalidValue;
     const int sms = sm_count();
     Params p{{d.cu_seqlens, d.num_seqs, d.H, d.total, 0, 0, nullptr, d.status},
@@ -703,12 +735,14 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
              static_cast<const __nv_bfloat16 *>(d.v),
              d.ldv,
              nullptr,
-             take_layers_expire(KDA_TESTING_DECAY)};
-    cudaError_t e = allow_smem<decay_chunk_kernel<D, true>>(kSmem);
-    if (e == cudaSuccess) e = allow_smem<decay_chunk_kernel<D, false>>(kSmemState);
+             take_layers_expire(KDA_TESTING_DECAY),
+             dk,
+             dv};
+    cudaError_t e = allow_smem<decay_chunk_kernel<D, true, FULL>>(kSmem);
+    if (e == cudaSuccess) e = allow_smem<decay_chunk_kernel<D, false, FULL>>(kSmemState);
     if (e != cudaSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, D);
+    const bool room = ws && workspace_bytes >= decay_prefill_tc_workspace(d.total, d.num_seqs, d.H, dk, dv);
     const int64_t chains = (int64_t)d.num_seqs * d.H;
     const int len = room ? decay_segment_tokens(d.total, d.num_seqs, d.H, sms, kCost) : 0;
     if (len) {
@@ -717,10 +751,10 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
         p.g.cap = (int)(d.total / len) + d.num_seqs;
         const int64_t items = (int64_t)p.g.cap * d.H;
         const dim3 grid((unsigned)(items < sms ? items : sms));
-        if ((e = launch_dependent(decay_chunk_kernel<D, false>, grid, kThreads, kSmemState, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
+        if ((e = launch_dependent(decay_chunk_kernel<D, false, FULL>, grid, kThreads, kSmemState, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
             return e;
-        if ((e = launch_decay_segments(p.g, d.log_decay, d.init, D, D, st)) != cudaSuccess) return e;
-        return launch_dependent(decay_chunk_kernel<D, true>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
+        if ((e = launch_decay_segments(p.g, d.log_decay, d.init, dk, dv, st)) != cudaSuccess) return e;
+        return launch_dependent(decay_chunk_kernel<D, true, FULL>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
     }
     if (room && chains > sms && d.num_seqs > 1) {
         int32_t *order = reinterpret_cast<int32_t *>(ws + kOrderAt);
@@ -729,12 +763,16 @@ static cudaError_t launch_tc(const DecayParams &d, void *workspace, size_t works
             return e;
         p.order = order;
     }
-    return launch_dependent(decay_chunk_kernel<D, true>, dim3((unsigned)(chains < sms ? chains : sms)), kThreads, kSmem, st, 1, mq,
+    return launch_dependent(decay_chunk_kernel<D, true, FULL>, dim3((unsigned)(chains < sms ? chains : sms)), kThreads, kSmem, st, 1, mq,
                             mk, mv, mo, p);
 }
 
-cudaError_t launch_decay_prefill_tc(const DecayParams &d, int D, void *workspace, size_t workspace_bytes, cudaStream_t st) {
-    return D == 64 ? launch_tc<64>(d, workspace, workspace_bytes, st) : launch_tc<128>(d, workspace, workspace_bytes, st);
+cudaError_t launch_decay_prefill_tc(const DecayParams &d, int dk, int dv, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t st) {
+    if (dk == dv && dk == 128) return launch_tc<128, true>(d, dk, dv, workspace, workspace_bytes, st);
+    if (dk == dv && dk == 64) return launch_tc<64, true>(d, dk, dv, workspace, workspace_bytes, st);
+    return dk <= 64 && dv <= 64 ? launch_tc<64, false>(d, dk, dv, workspace, workspace_bytes, st)
+                                : launch_tc<128, false>(d, dk, dv, workspace, workspace_bytes, st);
 }
 
 }  // namespace kda

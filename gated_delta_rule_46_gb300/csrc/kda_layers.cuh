@@ -40,9 +40,10 @@ struct DecayParams {
     void *out;
     uint32_t *status;
 };
-// bf16, dk = dv = D = 64 or 128, total > 0, rows that start on 16-byte boundaries
-size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int D);
-cudaError_t launch_decay_prefill_tc(const DecayParams &p, int D, void *workspace, size_t workspace_bytes, cudaStream_t st);
+// bf16, total > 0, rows that start on 16-byte boundaries
+size_t decay_prefill_tc_workspace(int64_t total, int N, int H, int dk, int dv);
+cudaError_t launch_decay_prefill_tc(const DecayParams &p, int dk, int dv, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t st);
 size_t decay_prefill_simt_workspace(int64_t total, int N, int H, int dk, int dv);
 cudaError_t launch_decay_prefill_simt(const DecayParams &p, int dk, int dv, bool bf16, void *workspace,
                                       size_t workspace_bytes, cudaStream_t st);

@@ -67,8 +67,8 @@ size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int 
         !dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv))
         return 0;
     size_t bytes = kda::decay_prefill_simt_workspace(total_tokens, num_seqs, H, dk, dv);
-    if (dtype == KDA_BF16 && dk == dv && dk >= 64) {
-        const size_t tc = kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H, dk);
+    if (dtype == KDA_BF16) {
+        const size_t tc = kda::decay_prefill_tc_workspace(total_tokens, num_seqs, H, dk, dv);
         if (tc > bytes) bytes = tc;
     }
     return (bytes + 255) & ~size_t(255);
@@ -95,9 +95,9 @@ kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_
     const kda::DecayParams p{q, k, v, ldq, ldk, ldv, log_decay, cu_seqlens, num_seqs, H, total_tokens, scale,
                              initial_state, final_state, out, status};
     // TMA copies start on 16-byte boundaries
-    if (dtype == KDA_BF16 && dk == dv && dk >= 64 && total_tokens > 0 && aligned(q, 16) && aligned(k, 16) &&
+    if (dtype == KDA_BF16 && total_tokens > 0 && aligned(q, 16) && aligned(k, 16) &&
         aligned(v, 16) && aligned(out, 16) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0)
-        return from_cuda(kda::launch_decay_prefill_tc(p, dk, workspace, workspace_bytes,
+        return from_cuda(kda::launch_decay_prefill_tc(p, dk, dv, workspace, workspace_bytes,
                                                       reinterpret_cast<cudaStream_t>(stream)));
     return from_cuda(kda::launch_decay_prefill_simt(p, dk, dv, dtype == KDA_BF16, workspace, workspace_bytes,
                                                     reinterpret_cast<cudaStream_t>(stream)));
