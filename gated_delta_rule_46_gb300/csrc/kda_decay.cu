@@ -69,10 +69,12 @@ cudaError_t launch_decay_segments(const DecaySegs &p, const float *log_decay, co
 //          256 / (2 JB) thread groups and joined through shared memory
 //   S      rows x 4 columns per thread, in registers; a copy in shared memory
 //          for the next chunk's S^T q
-// The next chunk's q, k and v are loaded into registers meanwhile.  Bound by the
-// FMAs and the shared-memory reads that feed them (issue slots 62 % busy, two CTAs
-// per SM): 4096 tokens of 16 heads, d = 128, take 268 us in segments (0.27 TB/s and
-// 22 TFLOP/s with the repeated passes), 64 tokens of 2 heads, d = 32, 7.5 us.
+// The next chunk's q, k and v are loaded into registers meanwhile.  Bound by shared
+// memory (its pipe is 80 % busy, the issue slots 62 %, two CTAs per SM): a 16-byte load
+// takes four of its cycles however much of it is shared between lanes, and eight of
+// them feed 64 FMAs of a thread; tiles twice as large do not fit beside the state.
+// 4096 tokens of 16 heads, d = 128, take 268 us in segments, 64 tokens of 2 heads, d =
+// 32, 7.5 us.
 // ---------------------------------------------------------------------------
 struct DecaySimtParams {
     DecaySegs g;

@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // P is a chunk ahead of its use: there is time to wait for the stage of two chunks ago
                         if (c >= 2 && i == 0) load();
                         // the output products of two chunks ago have read this buffer, and so has their output if it had to
-                        ok = __all_sync(0xffffffffu, ok) && warp_wait(&bar[L::QK + b], c >> 1) && (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
+                        ok = __all_sync(0xffffffffu, ok) && warp_wait(&bar[L::QK + b], c >> 1) &&
+                             (c < 2 || warp_wait(&bar[L::OFREE + b], (c >> 1) - 1));
                         if (!ok) break;
                         ptx::tc_fence_after_sync();
                         uint8_t *sp = sm + L::P + b * kTile;
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t q = ptx::sdesc_kmajor_sw128(st + L::q);
 #pragma unroll 2
                         for (int k = 0; k < D / 16; ++k)
-                            ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8, q + (((k >> 2) * L::half + (k & 3) * 32) >> 4),
-                                             id, k > 0);
+                            ptx::mma_bf16_ts(tmem + tm_qs(b), tmem + TM_S + k * 8,
+                                             q + (((k >> 2) * L::half + (k & 3) * 32) >> 4), id, k > 0);
                         ptx::mma_commit(&bar[L::QS]);
                         if (!wait_on(&bar[L::PREADY + b], phase)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
@@ -437,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait_on(&bar[L::TF + 2 * s], sp) ||                  // (V's tail is clean)
                             !wait_on(&bar[L::TF + 2 * s + 1], sp)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
-                        const uint64_t a = sdesc_mn_sw128(st + L::v, kTile), pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
+                        const uint64_t a = sdesc_mn_sw128(st + L::v, kTile);
+                        const uint64_t pb = ptx::sdesc_kmajor_sw128(base + L::P + b * kTile);
 #pragma unroll 2
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_bf16_ss(tmem + tm_pv(b), a + k * (2048 >> 4), pb + k * 2, id | kAMn, k > 0);
@@ -496,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 f = *reinterpret_cast<const float2 *>(pwo + ic + e * 8);
-                            u[2 * e] = pack_bf16(fmaf(a[4 * e], f.x, o[4 * e]) * p.scale, fmaf(a[4 * e + 1], f.y, o[4 * e + 1]) * p.scale);
+                            u[2 * e] = pack_bf16(fmaf(a[4 * e], f.x, o[4 * e]) * p.scale,
+                                                 fmaf(a[4 * e + 1], f.y, o[4 * e + 1]) * p.scale);
                             u[2 * e + 1] = pack_bf16(fmaf(a[4 * e + 2], f.x, o[4 * e + 2]) * p.scale,
                                                      fmaf(a[4 * e + 3], f.y, o[4 * e + 3]) * p.scale);
                         }
@@ -751,8 +754,8 @@ static cudaError_t launch_tc(const DecayParams &d, int dk, int dv, void *workspa
         p.g.cap = (int)(d.total / len) + d.num_seqs;
         const int64_t items = (int64_t)p.g.cap * d.H;
         const dim3 grid((unsigned)(items < sms ? items : sms));
-        if ((e = launch_dependent(decay_chunk_kernel<D, false, FULL>, grid, kThreads, kSmemState, st, 1, mq, mk, mv, mo, p)) != cudaSuccess)
-            return e;
+        e = launch_dependent(decay_chunk_kernel<D, false, FULL>, grid, kThreads, kSmemState, st, 1, mq, mk, mv, mo, p);
+        if (e != cudaSuccess) return e;
         if ((e = launch_decay_segments(p.g, d.log_decay, d.init, dk, dv, st)) != cudaSuccess) return e;
         return launch_dependent(decay_chunk_kernel<D, true, FULL>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
     }
@@ -763,8 +766,8 @@ static cudaError_t launch_tc(const DecayParams &d, int dk, int dv, void *workspa
             return e;
         p.order = order;
     }
-    return launch_dependent(decay_chunk_kernel<D, true, FULL>, dim3((unsigned)(chains < sms ? chains : sms)), kThreads, kSmem, st, 1, mq,
-                            mk, mv, mo, p);
+    const dim3 grid((unsigned)(chains < sms ? chains : sms));
+    return launch_dependent(decay_chunk_kernel<D, true, FULL>, grid, kThreads, kSmem, st, 1, mq, mk, mv, mo, p);
 }
 
 cudaError_t launch_decay_prefill_tc(const DecayParams &d, int dk, int dv, void *workspace, size_t workspace_bytes,

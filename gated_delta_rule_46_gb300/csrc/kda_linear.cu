@@ -505,7 +505,8 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)pp.tiles_m * pp.tiles_n;
     const int pairs = sm_count() / 2;
-    return launch_dependent(kernel, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), 320, L::bytes, st, 2, mx, mw, mo, mr, pp);
+    return launch_dependent(kernel, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), 320, L::bytes, st, 2, mx, mw, mo, mr,
+                            pp);
 }
 
 template <int ACT, bool F32, int LOAD>

@@ -78,7 +78,8 @@ struct Walk {
         tile = (w - sp.cum * items) - item * nt;
     }
     __device__ bool more() const { return w < w1; }
-    __device__ int64_t last() const { return nt < tile + (w1 - w) ? nt : tile + (w1 - w); }   // end of this CTA's part of the item
+    // end of this CTA's part of the item
+    __device__ int64_t last() const { return nt < tile + (w1 - w) ? nt : tile + (w1 - w); }
     __device__ void next_item(const PagedParams &p, int64_t done) {
         w += done;
         if (w >= w1) return;
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(384, 1)
                 if (!ptx::mbar_wait(&bar[KFULL + s], (t / NS) & 1, kWaitBudget)) return false;
                 if (t >= 2 && !ptx::mbar_wait(&bar[PREADY + b], ((t >> 1) - 1) & 1, kWaitBudget)) return false;
                 ptx::tc_fence_after_sync();
-                mma_k<D / 16>(tm_s(b), base + L::K + s * L::tile, kSub, base + L::Q + (item_no & 1) * L::q_bytes, HB * 128, id_s, false);
+                mma_k<D / 16>(tm_s(b), base + L::K + s * L::tile, kSub, base + L::Q + (item_no & 1) * L::q_bytes, HB * 128,
+                              id_s, false);
                 ptx::mma_commit(&bar[SD + b]);
                 ptx::mma_commit(&bar[KFREE + s]);
                 if (++i == last) {
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t pb = ptx::sdesc_kmajor_sw128(base + L::P + b * L::p_bytes);
 #pragma unroll
                 for (int k = 0; k < TILE / 16; ++k)
-                    ptx::mma_bf16_ss(tm_o(b), a + k * (2048 >> 4), pb + (((k >> 2) * (HB * 128) + (k & 3) * 32) >> 4), id_o, k > 0);
+                    ptx::mma_bf16_ss(tm_o(b), a + k * (2048 >> 4), pb + (((k >> 2) * (HB * 128) + (k & 3) * 32) >> 4), id_o,
+                                     k > 0);
                 ptx::mma_commit(&bar[PVD + b]);
                 ptx::mma_commit(&bar[VFREE + s]);
             }
@@ -304,7 +307,8 @@ __global__ void __launch_bounds__(384, 1)
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
+            const __nv_bfloat16 *q =
+                static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
             // eight channels per lane and step, all loads first
             constexpr int PER = HR * D / 256;
             uint4 u[PER];
@@ -473,7 +477,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int h = 0; h < HR; ++h)
                         if (h < hb)
-                            out[h * D] = __float2bfloat16_rn(l[h] > 0.f ? __fdividef(acc[h], l[h]) : (l[h] == 0.f ? 0.f : l[h]));
+                            out[h * D] = __float2bfloat16_rn(l[h] > 0.f ? __fdividef(acc[h], l[h])
+                                                                        : (l[h] == 0.f ? 0.f : l[h]));
                 } else {
 #pragma unroll
                     for (int h = 0; h < HR; ++h)
