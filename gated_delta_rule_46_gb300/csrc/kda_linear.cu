@@ -64,8 +64,8 @@ Tail tail(const LinearParams &p) {
 // MMA's N, a multiple of 16), over its share of K; the S CTAs of a cluster
 // share one tile and add their sums up in order of rank, each for its part of
 // the rows.  Warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-5 read TMEM.
-// With LOAD = 1 (rows that no TMA copy can start on) warps 6-13 load instead,
-// element by element, into the same swizzled layout.
+// With LOAD = 1 (rows that no TMA copy can start on) warps 6-13 load instead, by
+// way of registers, into the same swizzled layout.
 // ---------------------------------------------------------------------------
 constexpr int kBK = 64;                     // K per stage: one 128-byte swizzled row
 constexpr uint32_t kABytes = 128 * 128;     // 128 rows
@@ -88,6 +88,25 @@ __device__ __forceinline__ void put(const Tail &t, int64_t m, int64_t n, float y
         if (t.residual) y += to_f32(static_cast<const __nv_bfloat16 *>(t.residual)[at]);
         static_cast<__nv_bfloat16 *>(t.out)[at] = __float2bfloat16_rn(y);
     }
+}
+
+// The eight elements from address a on, out of the two 16-byte words that hold them.
+__device__ __forceinline__ uint4 shifted(const uint4 &x, const uint4 &y, uint32_t a) {
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = a & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = a & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], w[i + 1], a & 2 ? 0x5432 : 0x3210);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Elements p[0] .. p[n - 1] of eight one by one, zeros for the others.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p, int n) {
+    uint32_t e[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) e[c] = c < n ? __bfloat16_as_ushort(p[c]) : 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
 template <int ACT, bool F32, int LOAD>
@@ -165,22 +184,47 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
             const int s = i % p.stages;
             uint4 v[12];
-#pragma unroll
-            for (int j = 0; j < 12; ++j) {
-                const int id = tid + j * 256;
-                if (id >= chunks) break;
-                const int row = id >> 3;
+            // Eight elements at a time from any even address: where all are there, and the two 16-byte words that hold them
+            // lie within x or w, by those words, six pieces' loads at a time; else one by one.  4096^2 x 4095: 801 us (one
+            // by one throughout 2479; 81 by TMA with K = 4096), 64 x 4096 x 4095: 30 (68; 10).
+            auto piece = [&](int j, int &n, uintptr_t &a, bool &words) {
+                const int id = tid + j * 256, row = id >> 3;
                 const int64_t k0 = (int64_t)kb * kBK + (id & 7) * 8;
                 const bool isw = row < 128;
                 const int64_t r = isw ? f0 + row : m0 + row - 128;
-                const __nv_bfloat16 *src = isw ? p.w + r * p.t.K : p.x + r * p.ldx;
-                const bool in = r < (isw ? p.t.N : p.t.M);
-                uint16_t e[8];
+                const __nv_bfloat16 *begin = isw ? p.w : p.x;
+                const int64_t ld = isw ? p.t.K : p.ldx, rows = isw ? p.t.N : p.t.M;
+                n = id < chunks && r < rows ? (int)max((int64_t)0, min((int64_t)8, p.t.K - k0)) : 0;
+                a = reinterpret_cast<uintptr_t>(begin + r * ld + k0);
+                const uintptr_t lo = a & ~uintptr_t(15);
+                words = n == 8 && lo >= reinterpret_cast<uintptr_t>(begin) &&
+                        lo + 32 <= reinterpret_cast<uintptr_t>(begin + (rows - 1) * ld + p.t.K);
+            };
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    e[c] = in && k0 + c < p.t.K ? __bfloat16_as_ushort(src[k0 + c]) : (uint16_t)0;
-                v[j] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                  e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+            for (int j0 = 0; j0 < 12; j0 += 6) {
+                if (j0 * 256 >= chunks) break;
+                uint4 y[6];
+#pragma unroll
+                for (int j = 0; j < 6; ++j) {
+                    int n;
+                    uintptr_t a;
+                    bool words;
+                    piece(j0 + j, n, a, words);
+                    const uint4 *lo = reinterpret_cast<const uint4 *>(a & ~uintptr_t(15));
+                    if (words) {
+                        v[j0 + j] = lo[0];
+                        y[j] = lo[1];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 6; ++j) {
+                    int n;
+                    uintptr_t a;
+                    bool words;
+                    piece(j0 + j, n, a, words);
+                    if (words) v[j0 + j] = shifted(v[j0 + j], y[j], (uint32_t)a);
+                    else v[j0 + j] = load8(reinterpret_cast<const __nv_bfloat16 *>(a), n);
+                }
             }
             if (i >= p.stages && !ptx::mbar_wait(&empty[s], ((i / p.stages) - 1) & 1, kWaitBudget)) { ok = false; break; }
 #pragma unroll

@@ -55,8 +55,8 @@ typedef enum {
  *   out       [M, N] of out_dtype (KDA_BF16 or KDA_F32), dense (written)
  * Products are summed in float32 and rounded once, after the residual.  Any
  * M, N >= 0 and K >= 1 below 2^31, any row stride and alignment of elements; K a
- * multiple of 8 with 16-byte aligned rows is loaded by TMA, anything else element
- * by element.
+ * multiple of 8 with 16-byte aligned rows is loaded by TMA, anything else by way
+ * of registers, which is several times slower.
  */
 kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *bias,
                         const void *residual, void *out, int64_t M, int64_t N, int64_t K,
