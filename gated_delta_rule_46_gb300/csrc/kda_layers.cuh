@@ -121,7 +121,7 @@ inline cudaError_t allow_smem(uint32_t bytes) {
 }
 
 // Clusters of S <= 8 CTAs of `Kernel` that run at a time on the current device, always asked for with the same block and
-// shared memory: it depends on how many SMs each of the GPU's clusters of SMs has, so it is the driver that knows.
+// shared memory: it depends on how many SMs each of the GPU's clusters of SMs has, so the runtime is asked.
 template <auto Kernel>
 inline int cluster_room(int S, unsigned block, uint32_t smem) {
     static std::atomic<int> known[64][9];

@@ -11,7 +11,8 @@
 // by reading w: 64 x 16384 x 8192 takes 46 us (5.9 TB/s), 64 x 4096 x 4096 11.5 us,
 // of which the 34 MB are 5; launch, the first load and the join are the rest.
 // Every sum is held in float32 (TMEM, and the join of a cluster's parts in order
-// of rank, so that results do not depend on timing); the one rounding is out's own.
+// of rank, so that results do not depend on timing; a float32 output in several
+// parts); the one rounding to fewer bits is out's own.
 #include <cuda.h>
 
 #include "kda_layers.cuh"
@@ -75,6 +76,7 @@ struct RowsParams {
     const __nv_bfloat16 *x, *w;   // LOAD = 1
     int64_t ldx;
     int NT, stages, S;
+    int sums;             // accumulators in TMEM, taken in turn
 };
 
 template <int ACT, bool F32>
@@ -90,6 +92,22 @@ __device__ __forceinline__ void put(const Tail &t, int64_t m, int64_t n, float y
     }
 }
 
+// 16 columns of the `sums` accumulators, `apart` columns from one to the next, added up.
+template <bool F32>
+__device__ __forceinline__ void load_sums(uint32_t at, int apart, int sums, float (&d)[16]) {
+    ptx::tmem_ld16(at, d);
+    ptx::tmem_ld_wait();
+    ptx::keep(d);
+    if constexpr (F32)
+        for (int i = 1; i < sums; ++i) {
+            float x[16];
+            ptx::tmem_ld16(at + i * apart, x);
+            ptx::tmem_ld_wait();
+            ptx::keep(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) d[e] += x[e];
+        }
+}
 // The eight elements from address a on, out of the two 16-byte words that hold them.
 __device__ __forceinline__ uint4 shifted(const uint4 &x, const uint4 &y, uint32_t a) {
     uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -123,8 +141,9 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     const int f0 = (int)(blockIdx.x / p.S) * 128, m0 = (int)blockIdx.y * p.NT;
     const int kb_all = (p.t.K + kBK - 1) / kBK;
     const int kb0 = (int)((int64_t)kb_all * rank / p.S), kb1 = (int)((int64_t)kb_all * (rank + 1) / p.S);
+    const int sums = F32 ? p.sums : 1;
     uint32_t cols = 32;
-    while (cols < (uint32_t)p.NT) cols <<= 1;
+    while (cols < (uint32_t)(p.NT * sums)) cols <<= 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -174,7 +193,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
                 if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kWaitBudget)) { ok = false; break; }
                 ptx::tc_fence_after_sync();
                 const uint32_t a = ptx::smem_addr(sm + s * stage_bytes);
-                mma_k<4>(tmem, a, 0, a + kABytes, 0, idesc, i > 0);
+                mma_k<4>(tmem + (F32 ? (i % sums) * p.NT : 0), a, 0, a + kABytes, 0, idesc, i >= sums);
                 ptx::mma_commit(&empty[s]);
             }
             if (ok) ptx::mma_commit(&done);
@@ -260,8 +279,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
         if (reader && !s_abort) {
             for (int c0 = 0; c0 < rows; c0 += 16) {
                 float d[16];
-                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
-                ptx::tmem_ld_wait();
+                load_sums<F32>(tmem + ((uint32_t)q << 21) + c0, p.NT, min(sums, kb1 - kb0), d);
                 if (f < p.t.N)
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
@@ -275,8 +293,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
         if (reader) {
             for (int c0 = 0; c0 < rows; c0 += 16) {
                 float d[16];
-                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
-                ptx::tmem_ld_wait();
+                load_sums<F32>(tmem + ((uint32_t)q << 21) + c0, p.NT, min(sums, kb1 - kb0), d);
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     if (c0 + c < rows) part[(c0 + c) * 128 + q * 32 + lane] = d[c];
@@ -356,6 +373,10 @@ __global__ void __launch_bounds__(320)
     const uint32_t rank = ptx::cluster_rank();
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
     const int tiles = p.tiles_m * p.tiles_n, kbs = (p.t.K + kBK - 1) / kBK;
+    // A float32 output is summed in passes of 512 products, which the epilogue adds up: the MMAs' own float32 sums lose up
+    // to an ulp at each step, always towards zero (rounding to bf16 hides that).  3812 x 5166 x 2244 in one sum is 1.3e-6
+    // off, in passes 5e-7, a float32 product 4e-7; 4096 x 4096 x 8192 takes 240 us, 158 with a bf16 output.
+    const int per = F32 ? 8 : kbs, passes = F32 ? (kbs + per - 1) / per : 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -412,11 +433,13 @@ __global__ void __launch_bounds__(320)
             const uint32_t idesc = ptx::idesc_bf16_f32(256, BN);
             int it = 0, n = 0;
             if (p.t.expire && pair == 0) ok = ptx::mbar_wait(&tfull[0], 0, kTestWait);
-            for (int i = pair; i < tiles && ok; i += pairs, ++n) {
+            // all passes of a tile, then the next tile's
+            for (int i = pair * passes; i < tiles * passes && ok; i += (i + 1) % passes ? 1 : (pairs - 1) * passes + 1, ++n) {
                 const int b = n & 1;
                 if (n >= 2 && !ptx::mbar_wait_cluster(&tempty[b], ((n >> 1) - 1) & 1, kWaitBudget)) { ok = false; break; }
                 ptx::tc_fence_after_sync();
-                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                const int k0 = (i % passes) * per, k1 = min(kbs, k0 + per);
+                for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = it % kStages;
                     if (!ptx::mbar_wait_cluster(&full[s], (it / kStages) & 1, kWaitBudget)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
@@ -424,7 +447,7 @@ __global__ void __launch_bounds__(320)
                     const uint64_t da = ptx::sdesc_kmajor_sw128(a), db = ptx::sdesc_kmajor_sw128(a + kABytes);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16_ss_pair(tmem + b * BN, da + k * 2, db + k * 2, idesc, kb > 0 || k > 0);
+                        ptx::mma_bf16_ss_pair(tmem + b * BN, da + k * 2, db + k * 2, idesc, kb > k0 || k > 0);
                     ptx::mma_commit_pair(&empty[s]);
                 }
                 if (ok) ptx::mma_commit_pair(&tfull[b]);
@@ -438,16 +461,37 @@ __global__ void __launch_bounds__(320)
         int n = 0;
         uint32_t rphase = 0;
         for (int i = pair; i < tiles && ok; i += pairs, ++n) {
-            const int b = n & 1;
             int tm, tn;
             tile_at(p, i, tm, tn);
             const int m0 = tm * 256 + (int)rank * 128, n0 = tn * BN + g * (BN / 2);
+            float sum[F32 ? BN / 2 : 1];
+            if constexpr (F32) {
+                for (int pass = 0; pass + 1 < passes && ok; ++pass, ++n) {
+                    const int b = n & 1;
+                    ok = !ptx::bar_any(g + 1, 128, !ptx::mbar_wait_cluster(&tfull[b], (n >> 1) & 1, kWaitBudget));
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < BN / 2; c += 16) {
+                        float d[16];
+                        ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c, d);
+                        ptx::tmem_ld_wait();
+                        ptx::keep(d);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[c + e] = pass ? sum[c + e] + d[e] : d[e];
+                    }
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&tempty[b], 0));
+                }
+                if (!ok) break;
+            }
+            const int b = n & 1;
             // the group goes on, or gives up, as one
             ok = !ptx::bar_any(g + 1, 128, !ptx::mbar_wait_cluster(&tfull[b], (n >> 1) & 1, kWaitBudget));
             if (!ok) break;
             ptx::tc_fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < CHUNKS; ++c) {
+            auto chunk = [&](const int c) {
                 const int nc = n0 + c * CW;
                 // the staging tile is free once its last store has read it
                 if (lead) {
@@ -463,6 +507,11 @@ __global__ void __launch_bounds__(320)
                     ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c * CW + 32,
                                    *reinterpret_cast<float(*)[32]>(d + 32));
                 ptx::tmem_ld_wait();
+                if constexpr (F32) {
+                    if (passes > 1)
+#pragma unroll
+                        for (int j = 0; j < CW; ++j) d[j] += sum[c * CW + j];
+                }
                 if (c == CHUNKS - 1) {
                     ptx::tc_fence_before_sync();
                     __syncwarp();
@@ -511,11 +560,17 @@ __global__ void __launch_bounds__(320)
                 }
                 ptx::fence_async_smem();
                 ok = !ptx::bar_any(g + 1, 128, !ok);
-                if (!ok) break;
-                if (lead) {
+                if (ok && lead) {
                     ptx::tma_store_2d(&mo, nc, m0, st);
                     ptx::bulk_commit();
                 }
+            };
+            if constexpr (F32) {       // the sums are registers: unrolled
+                chunk(0);
+                if (ok) chunk(1);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < CHUNKS && ok; ++c) chunk(c);
             }
         }
         if (lead) ptx::bulk_wait_all();
@@ -560,7 +615,11 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     rp.x = p.x;
     rp.w = p.w;
     rp.ldx = p.ldx;
-    rp.NT = p.M < 256 ? (int)((p.M + 15) / 16) * 16 : 256;
+    // A float32 output is summed in several accumulators in turn, 512 products each (see linear_pair_kernel) or 1024 where
+    // TMEM holds no more of them; that leaves fewer rows of x per CTA for large K.
+    const int64_t kbs = (p.K + kBK - 1) / kBK;
+    const int most = !F32 || kbs <= 32 ? 256 : (kbs <= 64 ? 128 : 64);
+    rp.NT = p.M < most ? (int)((p.M + 15) / 16) * 16 : most;
     const uint32_t stage = kABytes + rp.NT * 128;
     constexpr uint32_t kRoom = 200 * 1024;      // all of an SM's: the weights under way are what hides HBM's latency
     rp.stages = (int)(kRoom / stage) < 12 ? (int)(kRoom / stage) : 12;
@@ -571,11 +630,12 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     // each CTA.  64 x 4096 x 4096 (32 tiles): S = 4 takes 10.6 us; with two smaller CTAs per SM S = 4 takes 11.2 and S =
     // 8 11.9.  64 x 5120 x 4096 (40 tiles): S = 3 takes 12.7, S = 2 14.7; 64 x 2560 x 4096 (20 tiles): S = 7, of which
     // no more than 15 run at a time, 16.0, S = 4 9.4.
-    const int64_t kbs = (p.K + kBK - 1) / kBK;
     rp.S = 8;
     while (rp.S > 1 && (kbs / rp.S < 4 || tiles > cluster_room<linear_rows_kernel<ACT, F32, LOAD>>(
                                                       rp.S, LOAD ? 448 : 192, kRoom + 1024)))
         --rp.S;
+    const int64_t need = ((kbs + rp.S - 1) / rp.S + 7) / 8;
+    rp.sums = !F32 ? 1 : (int)(need < 512 / rp.NT ? need : 512 / rp.NT);
     uint32_t smem = rp.stages * stage;
     if (rp.S > 1 && smem < (uint32_t)rp.NT * 512u) smem = rp.NT * 512u;
     smem += 1024;
@@ -600,8 +660,10 @@ cudaError_t launch_act(const LinearParams &p, cudaStream_t st) {
     // Tiles of 256 x 256 where they give more than half of the pairs work (256 x 16384 x 4096: 31 us, 38 by rows; 1024 x
     // 4096 x 4096: 25 us, 32 by rows), of 256 x 128 where those do (512 x 4096 x 4096: 21 us, 24 either way; 1024^3: 8.5
     // us, 10.4 by rows).  With fewer, splitting K beats both (256 x 4096 x 4096: 16 us, 20 in pairs).
+    // (A float32 output's epilogue holds its sums in registers, 128 columns' worth.)
     const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256), pairs = sm_count() / 2;
-    if (store && p.M > 128 && tiles * 2 > pairs) return launch_pair<ACT, F32, 256>(p, st);
+    if constexpr (!F32)
+        if (store && p.M > 128 && tiles * 2 > pairs) return launch_pair<ACT, F32, 256>(p, st);
     if (store && p.M > 256 && tiles * 5 > pairs) return launch_pair<ACT, F32, 128>(p, st);
     return launch_rows<ACT, F32, 0>(p, st);
 }

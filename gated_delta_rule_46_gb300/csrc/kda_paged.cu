@@ -399,7 +399,8 @@ static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) 
                             p, grid);
 }
 
-// Query heads per item of the tensor-core form: one pass over the cache for up to 32 of them.
+// Query heads per item of the tensor-core form: one pass over the cache for up to 32 of them (64 rows of 8192 tokens, 2
+// key-value heads, 32 query heads each: 97 us, 163 in two passes of 16).
 static int heads_tc(int G) { return G <= 16 ? 16 : 32; }
 
 // The tensor-core form: its TMA copies take whole 8-row groups of a page, and
@@ -418,7 +419,8 @@ static int grid_tc(int N, int64_t max_tokens, int Hkv, int G) {
     const int HB = heads_tc(G);
     return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc, sm_count());
 }
-// Query heads per item of the CUDA-core form: what its registers hold.
+// Query heads per item of the CUDA-core form: what its registers hold, and four where there are no more (float32, 64 rows
+// of 8192 tokens, 2 key-value heads, 4 query heads each: 208 us, 279 in items of eight).
 static int heads_simt(int G) { return G <= 4 ? 4 : 8; }
 static int grid_simt(int N, int64_t max_tokens, int Hkv, int G) {
     const int HB = heads_simt(G);
