@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float d[32];
                             ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
                             const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
-                            ptx::tmem_ld_wait();
+                            ptx::tmem_ld_wait(d);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
                             if (j0 == 32 * warp)
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float a[16], o[16];
                         ptx::tmem_ld_tiles4(at + tm_qs(b), a);
                         ptx::tmem_ld_tiles4(at + tm_pv(b), o);
-                        ptx::tmem_ld_wait();
+                        ptx::tmem_ld_wait(a, o);
                         const int ic = i0 + 2 * (lane & 3);          // this thread's first token
                         // an infinity or NaN in v shows in its channel at every token, as P's zeros for later tokens turn
                         // it into NaN: there the sums are taken again over the real pairs
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float d[32];
                         ptx::tmem_ld16(ds + e, *reinterpret_cast<float(*)[16]>(d));
                         ptx::tmem_ld16(ds + e + 16, *reinterpret_cast<float(*)[16]>(d + 16));
-                        ptx::tmem_ld_wait();
+                        ptx::tmem_ld_wait(d);
                         if (e + 32 == KC) {
                             ptx::tc_fence_before_sync();
                             warp_arrive(&bar[L::DSFREE + (c & (NB - 1))]);

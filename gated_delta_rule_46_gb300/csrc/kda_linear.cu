@@ -96,14 +96,12 @@ __device__ __forceinline__ void put(const Tail &t, int64_t m, int64_t n, float y
 template <bool F32>
 __device__ __forceinline__ void load_sums(uint32_t at, int apart, int sums, float (&d)[16]) {
     ptx::tmem_ld16(at, d);
-    ptx::tmem_ld_wait();
-    ptx::keep(d);
+    ptx::tmem_ld_wait(d);
     if constexpr (F32)
         for (int i = 1; i < sums; ++i) {
             float x[16];
             ptx::tmem_ld16(at + i * apart, x);
-            ptx::tmem_ld_wait();
-            ptx::keep(x);
+            ptx::tmem_ld_wait(x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) d[e] += x[e];
         }
@@ -475,8 +473,7 @@ __global__ void __launch_bounds__(320)
                     for (int c = 0; c < BN / 2; c += 16) {
                         float d[16];
                         ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c, d);
-                        ptx::tmem_ld_wait();
-                        ptx::keep(d);
+                        ptx::tmem_ld_wait(d);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) sum[c + e] = pass ? sum[c + e] + d[e] : d[e];
                     }
@@ -506,7 +503,7 @@ __global__ void __launch_bounds__(320)
                 if constexpr (!F32)
                     ptx::tmem_ld32(tmem + ((uint32_t)q << 21) + b * BN + g * (BN / 2) + c * CW + 32,
                                    *reinterpret_cast<float(*)[32]>(d + 32));
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(d);
                 if constexpr (F32) {
                     if (passes > 1)
 #pragma unroll

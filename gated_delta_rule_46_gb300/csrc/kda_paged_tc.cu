@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int h = 0; h < HR; h += W) {
                         float v[W];
                         tmem_load(tm_s(b) + ((uint32_t)q << 21) + h, v);
-                        ptx::tmem_ld_wait();
+                        ptx::tmem_ld_wait(v);
                         const bool in = (int)(i * TILE) + j < len &&
                                         (*static_cast<volatile uint32_t *>(&s_mask[t & 7]) >> (j / rows) & 1);
 #pragma unroll
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_load(tm_o(b) + ((uint32_t)q << 21) + h, v);
 #pragma unroll
                     for (int e = 0; e < W; e += 8) ld8(sf + b * HB + h + e, f + e);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(v);
 #pragma unroll
                     for (int e = 0; e < W; ++e) acc[h + e] = fmaf(acc[h + e], f[e], v[e]);
                 }

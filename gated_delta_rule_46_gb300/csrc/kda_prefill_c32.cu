@@ -185,7 +185,7 @@ __device__ __forceinline__ void save_state(const Ctx &x, float *dst) {
         float X[32];
         const int c0 = 64 * x.half + 32 * m;
         ptx::tmem_ld32(x.lane_base + TM_S + c0, X);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(X);
 #pragma unroll
         for (int i = 0; i < 32; ++i) dst[(int64_t)(c0 + i) * D + x.ch] = X[i];
     }
@@ -200,7 +200,7 @@ __device__ __forceinline__ void scale_state(const Ctx &x, int c_lo, int n) {
         ptx::tmem_ld32(x.lane_base + TM_S + c0, X);
 #pragma unroll
         for (int i = 0; i < 32; i += 8) ld8(x.s_gamma + c0 + i, g + i);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(X);
 #pragma unroll
         for (int i = 0; i < 32; ++i) X[i] *= g[i];
         ptx::tmem_st32(x.lane_base + TM_S + c0, X);
@@ -341,7 +341,7 @@ __device__ __forceinline__ void phase_rhs(const Ctx &x, int nvalid) {
         const float vv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(vb + swz(s, jc) + jo));
         r[i] = s < nvalid ? vv : 0.f;
     }
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(KS);
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] -= KS[i];
     st_chunk(x.sm + R_RU, swz(j, 2 * x.half), r);
@@ -360,7 +360,7 @@ __device__ __forceinline__ void phase_extract(const Ctx &x) {
     // half 0: s = 0..15 sits in column 0.. (tile 0) or 16.. (tile 1); half 1: s = 16..31 in column 32..
     ptx::tmem_ld16(x.lane_base + TM_G + (x.half ? 32 : 0), X);
     ptx::tmem_ld16(x.lane_base + TM_G + 16, Y);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(X, Y);
     const float bt = x.s_beta[t];
     float vals[16];
 #pragma unroll
@@ -522,7 +522,7 @@ __device__ __forceinline__ void phase_T_single(const Ctx &x) {
 __device__ __forceinline__ void phase_u_out(const Ctx &x) {
     float U[16];
     ptx::tmem_ld16(x.lane_base + TM_U + 16 * x.half, U);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(U);
     st_chunk(x.sm + R_RU, swz(x.ch, 2 * x.half), U);
     st_chunk(x.sm + R_RU, swz(x.ch, 2 * x.half + 1), U + 8);
 }
@@ -534,14 +534,14 @@ __device__ __forceinline__ void phase_state_out(const Ctx &x) {
     for (int m = 0; m < 2; ++m) {
         float X[32];
         ptx::tmem_ld32(x.lane_base + TM_S + 64 * x.half + 32 * m, X);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(X);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4)
             st_chunk(x.sm + R_ST + x.half * 16384, swz(x.ch, 4 * m + q4), &X[8 * q4]);
     }
     float O[16];
     ptx::tmem_ld16(x.lane_base + TM_D1 + 32 + 16 * x.half, O);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(O);
     const int j = x.ch;
     const uint32_t obox = R_OST + (uint32_t)(j >> 6) * 4096u;
     const uint32_t jc = (uint32_t)((j & 63) >> 3), jo = (uint32_t)(j & 7) * 2u;
@@ -557,7 +557,7 @@ __device__ __forceinline__ void phase_state_out(const Ctx &x) {
 __device__ __forceinline__ void phase_o_out(const Ctx &x) {
     float O[16];
     ptx::tmem_ld16(x.lane_base + TM_D1 + 32 + 16 * x.half, O);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(O);
     const int j = x.ch;
     const uint32_t obox = R_OST + (uint32_t)(j >> 6) * 4096u;
     const uint32_t jc = (uint32_t)((j & 63) >> 3), jo = (uint32_t)(j & 7) * 2u;

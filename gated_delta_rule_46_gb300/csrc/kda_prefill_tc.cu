@@ -329,7 +329,7 @@ __device__ __forceinline__ void phase_extract_PL(const Ctx &x, uint32_t off_pb,
         const bool loadX = cg <= 2 * m, loadY = cg <= 2 * m + 1;   // warp-uniform
         if (loadX) ptx::tmem_ld16(lane_base + TM_G + tile_off(2 * m) + colbase, X);
         if (loadY) ptx::tmem_ld16(lane_base + TM_G + tile_off(2 * m + 1) + colbase, Y);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(X, Y);
         const bool have = cg <= a;
         const float bt = s_beta[t];
         float dg[16];
@@ -558,7 +558,7 @@ __device__ __forceinline__ void phase_rhs_w8(const Ctx &x, uint32_t tm_ks, uint3
     ptx::tmem_ld32(x.lane_base + tm_ks + 32 * half, KS);
 #pragma unroll
     for (int c4 = 0; c4 < 4; ++c4) ld_chunk(x.sm + off_vt, swz(x.ch, 4 * half + c4), vt + 8 * c4);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(KS);
 #pragma unroll
     for (int i = 0; i < 32; ++i) vt[i] -= KS[i];
 #pragma unroll
@@ -594,7 +594,7 @@ __device__ __forceinline__ void load_state(const Ctx &x, const float *src, uint3
 __device__ __forceinline__ void save_state(const Ctx &x, float *dst, uint32_t tm_s) {
     float X[32];
     ptx::tmem_ld32(x.lane_base + tm_s + 32 * x.cg, X);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(X);
 #pragma unroll
     for (int i = 0; i < 32; ++i) dst[(int64_t)(32 * x.cg + i) * D + x.ch] = X[i];
 }
@@ -606,7 +606,7 @@ __device__ __forceinline__ void phase_rhs(const Ctx &x, uint32_t tm_ks, uint32_t
     ptx::tmem_ld16(x.lane_base + tm_ks + 16 * x.cg, KS);
     ld_chunk(x.sm + off_vt, swz(x.ch, 2 * x.cg), vt);
     ld_chunk(x.sm + off_vt, swz(x.ch, 2 * x.cg + 1), vt + 8);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(KS);
 #pragma unroll
     for (int i = 0; i < 16; ++i) vt[i] -= KS[i];
     st_chunk(x.sm + off_ru, swz(x.ch, 2 * x.cg), vt);
@@ -621,7 +621,7 @@ __device__ __forceinline__ void scale_state_cols(const Ctx &x, uint32_t tm_s, co
     ptx::tmem_ld32(x.lane_base + tm_s + 32 * cg, Sx);
     const float *g = gamma + 32 * cg;
     ld8(g, gm); ld8(g + 8, gm + 8); ld8(g + 16, gm + 16); ld8(g + 24, gm + 24);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(Sx);
 #pragma unroll
     for (int i = 0; i < 32; ++i) Sx[i] *= gm[i];
     ptx::tmem_st32(x.lane_base + tm_s + 32 * cg, Sx);
@@ -634,7 +634,7 @@ __device__ __forceinline__ void scale_state(const Ctx &x, uint32_t tm_s, const f
 __device__ __forceinline__ void u_out(const Ctx &x, uint32_t tm_u, uint32_t off_ru) {
     float U[16];
     ptx::tmem_ld16(x.lane_base + tm_u + 16 * x.cg, U);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(U);
     st_chunk(x.sm + off_ru, swz(x.ch, 2 * x.cg), U);
     st_chunk(x.sm + off_ru, swz(x.ch, 2 * x.cg + 1), U + 8);
 }
@@ -646,7 +646,7 @@ __device__ __forceinline__ void phase_state_out(const Ctx &x, uint32_t tm_s, uin
     float X[32], O[16];
     ptx::tmem_ld32(x.lane_base + tm_s + 32 * x.cg, X);
     ptx::tmem_ld16(x.lane_base + tm_o + 16 * x.cg, O);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(X, O);
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4)
         st_chunk(x.sm + off_st + (x.cg >> 1) * 16384, swz(x.ch, 4 * (x.cg & 1) + q4), &X[8 * q4]);
@@ -1197,7 +1197,7 @@ __device__ __forceinline__ void phase_wu_out(const Ctx &x) {
     if (x.qw < 2) {
         float Wr[32];
         ptx::tmem_ld32(x.lane_base + TM_W + 32 * x.cg, Wr);   // W[t][32 cg + i], t = ch
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(Wr);
 #pragma unroll
         for (int i = 0; i < 32; ++i) Wr[i] = -Wr[i];
         uint8_t *nw = x.sm + OFF_NW_INTRA + (x.cg >> 1) * 8192;
@@ -1206,7 +1206,7 @@ __device__ __forceinline__ void phase_wu_out(const Ctx &x) {
     }
     float Ut[16];
     ptx::tmem_ld16(x.lane_base + TM_UT + 16 * x.cg, Ut);   // U~^T[j][16 cg + i], j = ch
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(Ut);
     st_chunk(x.sm + OFF_UT_INTRA, swz(x.ch, 2 * x.cg), Ut);
     st_chunk(x.sm + OFF_UT_INTRA, swz(x.ch, 2 * x.cg + 1), Ut + 8);
 }
@@ -1765,7 +1765,7 @@ constexpr size_t MAP_CELL = 2 * 65536;   // segment-map mode: float32 S0, then f
 __device__ __forceinline__ void save_m_tile(const Ctx &x, uint8_t *dst, uint32_t tm_m) {
     float X[32];
     ptx::tmem_ld32(x.lane_base + tm_m + 32 * x.cg, X);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(X);
     const int m = x.ch;
     uint8_t *kb = dst + (m >> 6) * 16384;
     const uint32_t mc = (uint32_t)((m & 63) >> 3), mo = (uint32_t)(m & 7) * 2u;
@@ -1816,7 +1816,7 @@ __device__ __forceinline__ void preload_u64(const Ctx &x, uint32_t tm_u, const u
 __device__ __forceinline__ void state_to_bf16(const Ctx &x, uint32_t tm_s, uint32_t off_st) {
     float X[32];
     ptx::tmem_ld32(x.lane_base + tm_s + 32 * x.cg, X);
-    ptx::tmem_ld_wait();
+    ptx::tmem_ld_wait(X);
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4)
         st_chunk(x.sm + off_st + (x.cg >> 1) * 16384, swz(x.ch, 4 * (x.cg & 1) + q4), &X[8 * q4]);
@@ -2082,7 +2082,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap tm_s0, const __grid_cons
     };
     auto save = [&](int g, uint32_t buf, float (&Y)[SCAN_JB]) {   // S_in(g) block out of TMEM buffer buf
         ptx::tmem_ld32(lane_base + buf, Y);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(Y);
 #pragma unroll
         for (int i = 0; i < SCAN_JB / 4; ++i)
             *reinterpret_cast<float4 *>(sm + SC_OUT + swz(c, i)) =
@@ -2154,7 +2154,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap tm_s0, const __grid_cons
             bulk_load(sm + SC_MB + k * 32768, cells + (size_t)(g + 2) * SEG_CELL + SEG_MT, 32768, bar_mb + k);
         if (g + 3 < nseg) ++mb_issued[k];
         ptx::tmem_ld32(lane_base + dk, X);   // S_in(g + 1): the next step's operand
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(X);
         scan_block_to_bf16(sm + SC_SB, c, X);
     }
     if (tid == 0) ptx::bulk_wait_read();

@@ -189,11 +189,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr));
 }
-// Uses of r do not move before this point: what a load from TMEM brings is there only after its wait.
-__device__ __forceinline__ void keep(float (&r)[16]) {
-    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]));
-}
 // The same, 8 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
     uint32_t *u = reinterpret_cast<uint32_t *>(r);
@@ -260,8 +255,22 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8])
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait() {
+// No use of r moves before this point.
+template <int N>
+__device__ __forceinline__ void keep(float (&r)[N]) {
+    static_assert(N % 8 == 0, "whole loads");
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
+                     "+f"(r[i + 6]), "+f"(r[i + 7]));
+}
+// Waits for this thread's loads from TMEM.  What they bring is in the registers r only from here on, and to the compiler
+// a load and its wait are instructions without a connection: the registers are tied to the wait.
+template <int... N>
+__device__ __forceinline__ void tmem_ld_wait(float (&...r)[N]) {
+    static_assert(sizeof...(N) > 0, "what was loaded");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    (keep(r), ...);
 }
 
 // ----------------------------------------------------------------- tcgen05.mma
