@@ -378,10 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j0 = 0; j0 < 32 * (warp + 1); j0 += 32) {
                             float d[32];
                             ptx::tmem_ld32(tmem + ((uint32_t)warp << 21) + TM_P + j0, d);
-                            const float a0 = l2 * (float)(i - j0);               // lambda^{i - j} = 2^{a0 - l2 (j - j0)}
+                            // lambda^{i - j} = 2^{l2 (i - j)}, the difference first: on the diagonal it is exactly 0, and
+                            // the weight 1, however large l2 is
+                            const float a0 = (float)(i - j0);
                             ptx::tmem_ld_wait(d);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) d[e] *= ex2(fmaf(-(float)e, l2, a0));
+                            for (int e = 0; e < 32; ++e) d[e] *= ex2(l2 * (a0 - (float)e));
                             if (j0 == 32 * warp)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) d[e] = e <= lane ? d[e] : 0.f;
