@@ -66,9 +66,10 @@ __device__ __forceinline__ bool find_segment(const DecaySegs &p, unsigned seg, S
     return false;
 }
 
-// 2^(l2 n) with l2 no lower than -16384: exactly 0 for n >= 1 there, and 1 for n = 0.
+// 2^(l2 n) with l2 no lower than -16384: exactly 0 for n >= 1 there, and 1 for n = 0.  A NaN stays one.
 __device__ __forceinline__ float decay_log2(const float *log_decay, int head) {
-    return fmaxf(log_decay[head] * kLog2E, -16384.f);
+    const float l2 = log_decay[head] * kLog2E;
+    return l2 < -16384.f ? -16384.f : l2;
 }
 
 // Tokens per segment in whole chunks, or 0 for whole chains.  Segments cost a

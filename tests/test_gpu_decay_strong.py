@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from gated_delta_rule_46_gb300 import decay_prefill
+from gated_delta_rule_46_gb300 import decay_decode, decay_prefill
 from gpu_util import need_gpu
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,32 @@ def test_output_is_the_token_s_own_value(dtype, dk, dv, lens):
     want = torch.zeros_like(fin)
     want[:, :, 5] = v[cu[1:].long() - 1].float()
     assert torch.equal(fin, want)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 64)])
+@pytest.mark.parametrize("lens", [[130, 0, 5], [2500], [40] * 50])
+def test_a_nan_decay_is_not_taken_for_a_number(dtype, d, lens):
+    """exp(NaN) S is NaN from the first token on; the other heads and the sequences without tokens are as before."""
+    dev = need_gpu()
+    T, g = sum(lens), torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn(T, 3, d, generator=g).to(dtype).to(dev) / d ** 0.25 for _ in range(3))
+    cu = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device=dev)
+    init = torch.randn(len(lens), 3, d, d, generator=g).to(dev)
+    rates = torch.tensor([-0.5, -0.25, -1.0], device=dev)
+    clean, cfin = decay_prefill(q, k, v, rates, cu, init)
+    rates[1] = math.nan
+    out, fin = decay_prefill(q, k, v, rates, cu, init)
+    assert torch.isnan(out[:, 1]).all()
+    assert torch.equal(out[:, ::2], clean[:, ::2]) and torch.equal(fin[:, ::2], cfin[:, ::2])
+    for i, n in enumerate(lens):
+        assert torch.isnan(fin[i, 1]).all() if n else torch.equal(fin[i, 1], init[i, 1])
+
+
+def test_decode_agrees():
+    dev = need_gpu()
+    H, d = len(RATES) + 1, 64
+    q = _unit(2, H, d, F32, dev)
+    v = torch.randn(2, H, d, generator=torch.Generator().manual_seed(3)).to(dev)
+    pool = torch.randn(2, H, d, d, generator=torch.Generator().manual_seed(4)).to(dev)
+    out = decay_decode(q, q, v, torch.tensor(RATES + [math.nan], device=dev), pool)
+    assert torch.equal(out[:, :-1], v[:, :-1]) and torch.isnan(out[:, -1]).all()
