@@ -26,6 +26,8 @@ struct LinearParams {
     uint32_t *status;
 };
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t st);
+// gridDim.y of the largest launch of its few-rows kernel
+int64_t linear_row_tiles(int64_t M, int64_t K, bool f32);
 
 struct DecayParams {
     const void *q, *k, *v;

@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "kda_layers.cuh"
+#include "kda_testing.h"
 
 namespace kda {
 static std::atomic<int> g_layers_expire{0};
@@ -59,6 +60,10 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
     const kda::LinearParams p{static_cast<const __nv_bfloat16 *>(x), ldx, static_cast<const __nv_bfloat16 *>(w),
                               bias, residual, out, M, N, K, act, out_dtype == KDA_F32, status};
     return from_cuda(kda::launch_linear(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t kda_testing_linear_row_tiles(int64_t M, int64_t K, kda_dtype_t out_dtype) {
+    return M > 0 && K > 0 ? kda::linear_row_tiles(M, K, out_dtype == KDA_F32) : 0;
 }
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,

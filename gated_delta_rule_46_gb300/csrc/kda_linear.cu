@@ -605,6 +605,15 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
                             pp);
 }
 
+// Rows of x per CTA.  A float32 output is summed in several accumulators in turn, 512 products each (see
+// linear_pair_kernel) or 1024 where TMEM holds no more of them; that leaves fewer rows of x per CTA for large K.
+constexpr int kLeastTile = 64;              // where there are as many rows
+int rows_tile(int64_t M, int64_t K, bool f32) {
+    const int64_t kbs = (K + kBK - 1) / kBK;
+    const int most = !f32 || kbs <= 32 ? 256 : (kbs <= 64 ? 128 : kLeastTile);
+    return M < most ? (int)((M + 15) / 16) * 16 : most;
+}
+
 template <int ACT, bool F32, int LOAD>
 cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     RowsParams rp{};
@@ -612,11 +621,8 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     rp.x = p.x;
     rp.w = p.w;
     rp.ldx = p.ldx;
-    // A float32 output is summed in several accumulators in turn, 512 products each (see linear_pair_kernel) or 1024 where
-    // TMEM holds no more of them; that leaves fewer rows of x per CTA for large K.
     const int64_t kbs = (p.K + kBK - 1) / kBK;
-    const int most = !F32 || kbs <= 32 ? 256 : (kbs <= 64 ? 128 : 64);
-    rp.NT = p.M < most ? (int)((p.M + 15) / 16) * 16 : most;
+    rp.NT = rows_tile(p.M, p.K, F32);
     const uint32_t stage = kABytes + rp.NT * 128;
     constexpr uint32_t kRoom = 200 * 1024;      // all of an SM's: the weights under way are what hides HBM's latency
     rp.stages = (int)(kRoom / stage) < 12 ? (int)(kRoom / stage) : 12;
@@ -680,11 +686,17 @@ cudaError_t launch_slice(const LinearParams &p, cudaStream_t st) {
     }
 }
 
+// M is worked on in slices: row tiles are the grid's y, which goes up to 65535, and whole pair tiles fill a slice.
+constexpr int64_t kSlice = int64_t(65535) * kLeastTile / 256 * 256;
+
 }  // namespace
 
+int64_t linear_row_tiles(int64_t M, int64_t K, bool f32) {
+    const int64_t m = M < kSlice ? M : kSlice, tile = rows_tile(m, K, f32);
+    return (m + tile - 1) / tile;
+}
+
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t st) {
-    // M in slices of 2^23 rows: the grid's limit in y, and 32-bit tile coordinates
-    constexpr int64_t kSlice = int64_t(1) << 23;
     for (int64_t m0 = 0; m0 < p.M; m0 += kSlice) {
         LinearParams s = p;
         s.M = p.M - m0 < kSlice ? p.M - m0 : kSlice;

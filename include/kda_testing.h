@@ -1,10 +1,13 @@
 /*
  * kda_testing.h -- test support of the GB300 KDA library.  The pages have no
  * counterpart to anything here: it exists so that a test can exercise the
- * library's failure handling without faulting, trapping or hanging a GPU.
+ * library's failure handling without faulting, trapping or hanging a GPU, and
+ * look at a launch without making it.
  */
 #ifndef KDA_GB300_TESTING_H
 #define KDA_GB300_TESTING_H
+
+#include "kda.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -39,6 +42,13 @@ extern "C" {
  * waits for it run out in earnest, after about a second.
  */
 void kda_testing_expire_next_wait(int kernels);
+
+/*
+ * kda_testing_linear_row_tiles -- the largest gridDim.y of the launches that
+ * kda_linear makes for M rows and K products where it takes them by rows: at
+ * most 65535.  Touches no device.
+ */
+int64_t kda_testing_linear_row_tiles(int64_t M, int64_t K, kda_dtype_t out_dtype);
 
 #ifdef __cplusplus
 }
