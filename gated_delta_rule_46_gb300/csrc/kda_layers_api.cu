@@ -172,7 +172,8 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
     if (ldq < (int64_t)Hq * d) return KDA_ERR_INVALID_ARG;
     if (num_seqs == 0) return KDA_OK;
     if (!q || !seq_lens || !out) return KDA_ERR_INVALID_ARG;
-    if (max_pages > 0 && num_pages > 0 && (!k_cache || !v_cache || !page_table)) return KDA_ERR_INVALID_ARG;
+    // (a page's id is read before it is compared with num_pages)
+    if (max_pages > 0 && (!page_table || (num_pages > 0 && (!k_cache || !v_cache)))) return KDA_ERR_INVALID_ARG;
     const int64_t e = elem(dtype);
     if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return KDA_ERR_INVALID_ARG;

@@ -141,7 +141,8 @@ size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq,
  *     out = softmax(scale q K^T) V,   lse = log sum exp(scale q K^T)
  *   q            [num_seqs, Hq, d] of dtype, row stride ldq; query head h reads
  *                key-value head h / (Hq / Hkv); Hq is a multiple of Hkv
- *   k_cache, v_cache, page_table: as for kda_paged_append
+ *   k_cache, v_cache, page_table: as for kda_paged_append; the caches may be
+ *                NULL where num_pages is 0, the table where max_pages is
  *   seq_lens     [num_seqs] int32, device; 0 gives zero outputs and lse -inf.  A
  *                negative length counts as 0 and one past the table as the
  *                table's end, both recorded in *status
