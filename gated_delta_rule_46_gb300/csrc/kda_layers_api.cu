@@ -33,6 +33,9 @@ bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
 int64_t elem(kda_dtype_t t) { return t == KDA_BF16 ? 2 : 4; }
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// float32 and int32 values, and the status word
+template <typename... P>
+bool words(const P *...p) { return (aligned(p, 4) && ...); }
 kda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 // log2 of a page size, or -1 where it is not a power of two up to 1024
@@ -54,7 +57,7 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
     if (M >= kMax31 || N >= kMax31 || K >= kMax31) return KDA_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return KDA_OK;
     if (!x || !w || !out) return KDA_ERR_INVALID_ARG;
-    if (!aligned(x, 2) || !aligned(w, 2) || !aligned(bias, 4) || !aligned(out, elem(out_dtype)) ||
+    if (!aligned(x, 2) || !aligned(w, 2) || !words(bias, status) || !aligned(out, elem(out_dtype)) ||
         !aligned(residual, elem(out_dtype)))
         return KDA_ERR_INVALID_ARG;
     const kda::LinearParams p{static_cast<const __nv_bfloat16 *>(x), ldx, static_cast<const __nv_bfloat16 *>(w),
@@ -95,7 +98,7 @@ kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_
     if (total_tokens > 0 && (!q || !k || !v || !out)) return KDA_ERR_INVALID_ARG;
     if (!aligned(q, elem(dtype)) || !aligned(k, elem(dtype)) || !aligned(v, elem(dtype)) ||
         !aligned(out, elem(dtype)) || !aligned(initial_state, 16) || !aligned(final_state, 16) ||
-        !aligned(workspace, 16))
+        !aligned(workspace, 16) || !words(log_decay, cu_seqlens, status))
         return KDA_ERR_INVALID_ARG;
     const kda::DecayParams p{q, k, v, ldq, ldk, ldv, log_decay, cu_seqlens, num_seqs, H, total_tokens, scale,
                              initial_state, final_state, out, status};
@@ -121,7 +124,7 @@ kda_status_t kda_decay_decode(const void *q, int64_t ldq, const void *k, int64_t
     if (!slot_ids && pool_size < N) return KDA_ERR_INVALID_ARG;
     if (!q || !k || !v || !log_decay || !state_pool || !out) return KDA_ERR_INVALID_ARG;
     if (!aligned(q, elem(dtype)) || !aligned(k, elem(dtype)) || !aligned(v, elem(dtype)) ||
-        !aligned(out, elem(dtype)) || !aligned(state_pool, 16))
+        !aligned(out, elem(dtype)) || !aligned(state_pool, 16) || !words(log_decay, slot_ids, status))
         return KDA_ERR_INVALID_ARG;
     const kda::DecayStepParams p{q, k, v, ldq, ldk, ldv, log_decay, state_pool, pool_size, slot_ids,
                                  out, N, H, scale, status};
@@ -143,7 +146,8 @@ kda_status_t kda_paged_append(const void *k, int64_t ldk, const void *v, int64_t
     if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
     if (!k || !v || !k_cache || !v_cache || !page_table || !start_pos) return KDA_ERR_INVALID_ARG;
     const int64_t e = elem(dtype);
-    if (!aligned(k, e) || !aligned(v, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    if (!aligned(k, e) || !aligned(v, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !words(page_table, start_pos, cu_seqlens, status))
         return KDA_ERR_INVALID_ARG;
     const kda::AppendParams p{k, v, ldk * e, ldv * e, k_cache, v_cache, num_pages, page_shift(page_size),
                               page_table, max_pages, start_pos, cu_seqlens, num_seqs, Hkv, total_tokens,
@@ -175,7 +179,8 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
     // (a page's id is read before it is compared with num_pages)
     if (max_pages > 0 && (!page_table || (num_pages > 0 && (!k_cache || !v_cache)))) return KDA_ERR_INVALID_ARG;
     const int64_t e = elem(dtype);
-    if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !words(page_table, seq_lens, lse, status))
         return KDA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) ||
         workspace_bytes < kda_paged_decode_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype))

@@ -12,7 +12,7 @@
  *
  * The conventions of kda.h hold: device pointers owned by the caller, calls
  * asynchronous on `stream`, argument errors found on the host before anything
- * is launched, no device memory allocated, no call traps.  Three more:
+ * is launched, no device memory allocated, no call traps.  Four more:
  *   - Per-token tensors [T, H, d] that are read (q, k, v, x) take a row stride
  *     (ld*, in elements, at least H d; a row is dense), so slices of one fused
  *     projection are passed as they are.  Rows past 2^31 elements are fine.
@@ -24,6 +24,8 @@
  *     KDA_ERR_DEVICE_TIMEOUT) is recorded in it, and kda_check_device_status
  *     reads it.  What is malformed is treated as absent: it is never read or
  *     written.
+ *   - Every pointer is aligned to its elements (status to 4 bytes), and further
+ *     where stated; KDA_ERR_INVALID_ARG otherwise.
  *   - A row's result depends on that row's inputs alone: infinities and NaN in
  *     other sequences, in later tokens, or in cache slots that no token was
  *     written to do not reach it.

@@ -12,3 +12,17 @@ INV = kda.KDA_ERR_INVALID_ARG
 def test_a_table_is_read_even_if_the_cache_has_no_pages(kw):
     """Ids are looked up before they are compared with the number of pages."""
     assert _attend(**kw) == INV
+
+
+@pytest.mark.parametrize("call,names", [
+    (_linear, ["status"]),
+    (_prefill, ["ld", "cu", "status"]),
+    (_decode, ["ld", "slots", "status"]),
+    (_append, ["table", "start", "cu", "status"]),
+    (_attend, ["table", "lens", "lse", "status"]),
+])
+def test_four_byte_values_off_their_alignment(call, names):
+    """Their loads, and the status word's atomic, would be misaligned addresses on the device."""
+    for name in names:
+        for off in (1, 2, 3):
+            assert call(**{name: A + off}) == INV, (name, off)
