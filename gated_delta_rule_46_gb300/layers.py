@@ -6,8 +6,9 @@ As in ``kda``, every step runs in the CUDA library; this module checks shapes,
 dtypes, devices and strides, passes pointers and the stream, and turns a non-OK
 status into ``KDAError``.  Inputs [T, H, d] may be slices of a wider row-major
 tensor (a fused projection): a row (the last two axes) is dense, the rows any
-stride apart.  Outputs and workspaces that a call allocates belong to the
-stream it runs on.
+stride apart.  Outputs and workspaces that a call allocates come from the memory
+of the stream it runs on (`stream`, or torch's current one); outputs may be used
+on the current stream as well, once it waits for `stream`.
 """
 from __future__ import annotations
 
@@ -106,17 +107,36 @@ def _code(dtype, name):
     return c
 
 
-def _call(name, device, stream, allocated, *args):
-    """Runs `name` on `device` and `stream` (torch's current one by default) and
-    hands what was allocated for the call over to that stream."""
+def _empty(stream, shape, dtype, device):
+    """A new tensor for a call on `stream`, out of that stream's memory: what the current
+    stream has freed may still be in use by kernels that `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _size(name, device, *args):
+    """Workspace bytes on `device`, whose number of SMs they depend on."""
+    if device.index == torch.cuda.current_device():
+        return _fn(name)(*args)
+    with torch.cuda.device(device):
+        return _fn(name)(*args)
+
+
+def _call(name, device, stream, outputs, *args):
+    """Runs `name` on `device` and `stream` (torch's current one by default); `outputs`
+    were allocated for the call, and the current stream may use them too."""
     index = device.index
     if stream is None:
         raw = _raw_stream(index)
     else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the inputs on {device}")
         raw = stream.cuda_stream
         if raw != _raw_stream(index):
-            for t in allocated:
-                t.record_stream(stream)
+            for t in outputs:
+                t.record_stream(torch.cuda.current_stream(device))
     if index == torch.cuda.current_device():
         st = _fn(name)(*args, raw)
     else:
@@ -147,7 +167,7 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, out_dtype=None,
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     new = []
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+        out = _empty(stream, (M, N), torch.bfloat16 if out_dtype is None else out_dtype, dev)
         new.append(out)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -182,16 +202,15 @@ def decay_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, final_stat
     cp = _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
     new = []
     if final_state is None and want_final_state:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _empty(stream, (N, H, dk, dv), torch.float32, dev)
         new.append(final_state)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=dt, device=dev)
+        out = _empty(stream, (T, H, dv), dt, dev)
         new.append(out)
     if workspace is None:
-        size = _fn("kda_decay_prefill_workspace_size")(T, N, H, dk, dv, code)
+        size = _size("kda_decay_prefill_workspace_size", dev, T, N, H, dk, dv, code)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-            new.append(workspace)
+            workspace = _empty(stream, size, torch.uint8, dev)
     size = 0 if workspace is None else _dims(workspace, "workspace", 1)[0]
     wp = _dense(workspace, "workspace", (size,), torch.uint8, dev)
     _call("kda_decay_prefill", dev, stream, new, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, lp, cp, N, T,
@@ -217,7 +236,7 @@ def decay_decode(q, k, v, log_decay, state_pool, slot_ids=None, out=None, scale=
     P = _dims(state_pool, "state_pool", 4)[0]
     new = []
     if out is None:
-        out = torch.empty((N, H, dv), dtype=dt, device=dev)
+        out = _empty(stream, (N, H, dv), dt, dev)
         new.append(out)
     _call("kda_decay_decode", dev, stream, new, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
           _dense(log_decay, "log_decay", (H,), torch.float32, dev),
@@ -270,15 +289,14 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
     tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
     new = []
     if out is None:
-        out = torch.empty((N, Hq, d), dtype=dt, device=dev)
+        out = _empty(stream, (N, Hq, d), dt, dev)
         new.append(out)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        lse = _empty(stream, (N, Hq), torch.float32, dev)
         new.append(lse)
     if workspace is None:
-        size = _fn("kda_paged_decode_workspace_size")(N, cols * ps, Hq, Hkv, d, code)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        new.append(workspace)
+        size = _size("kda_paged_decode_workspace_size", dev, N, cols * ps, Hq, Hkv, d, code)
+        workspace = _empty(stream, size, torch.uint8, dev)
     size = _dims(workspace, "workspace", 1)[0]
     _call("kda_paged_decode", dev, stream, new, q.data_ptr(), ldq, kp, vp, P, ps, tp, cols,
           _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
