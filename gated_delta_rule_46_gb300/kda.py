@@ -116,6 +116,23 @@ def _check(t, name, shape=None, dtype=None, device=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _empty(stream, shape, dtype, device):
+    """A new tensor for a call on `stream`, out of that stream's memory: what the current
+    stream has freed may still be in use by kernels that `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(stream, shape, dtype, device):
+    """The same for an output: the current stream may use it too, once it waits for `stream`."""
+    t = _empty(stream, shape, dtype, device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _on(device):
     """Makes `device` current for a call: the library launches on the current
     device and takes torch's current stream of that device."""
@@ -133,7 +150,7 @@ def gate(z: torch.Tensor, A: torch.Tensor, g_out: torch.Tensor | None = None, st
     T, H, dk = z.shape
     _check(A, "A", (H, dk), torch.float32, z.device)
     if g_out is None:
-        g_out = torch.empty((T, H, dk), dtype=torch.float32, device=z.device)
+        g_out = _result(stream, (T, H, dk), torch.float32, z.device)
     _check(g_out, "g_out", (T, H, dk), torch.float32, z.device)
     with _on(z.device):
         _raise(lib().kda_gate(_ptr(z), _dtype_code(z), _ptr(A), _ptr(g_out), T, H, dk,
@@ -169,15 +186,15 @@ def chunk_prefill(q, k, v, z, A, beta, cu_seqlens, initial_state=None, final_sta
     if initial_state is not None:
         _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     if final_state is None and want_final_state:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _result(stream, (N, H, dk, dv), torch.float32, dev)
     if final_state is not None:
         _check(final_state, "final_state", (N, H, dk, dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+        out = _result(stream, (T, H, dv), q.dtype, dev)
     _check(out, "out", (T, H, dv), q.dtype, dev)
     wsb = workspace_size(T, N, H, dk, dv, q.dtype)
     if workspace is None:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, wsb, torch.uint8, dev)
     _check(workspace, "workspace", None, torch.uint8, dev)
     with _on(dev):
         st = lib().kda_chunk_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
@@ -212,15 +229,16 @@ def chunk_prefill_logdecay(q, k, v, g, beta, cu_seqlens, initial_state=None, fin
     if initial_state is not None:
         _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     if final_state is None and want_final_state:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _result(stream, (N, H, dk, dv), torch.float32, dev)
     if final_state is not None:
         _check(final_state, "final_state", (N, H, dk, dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+        out = _result(stream, (T, H, dv), q.dtype, dev)
     _check(out, "out", (T, H, dv), q.dtype, dev)
     if workspace is None:
-        workspace = torch.zeros(logdecay_workspace_size(T, N, H, dk, dv, q.dtype), dtype=torch.uint8,
-                                device=dev)
+        workspace = _empty(stream, logdecay_workspace_size(T, N, H, dk, dv, q.dtype), torch.uint8, dev)
+        with torch.cuda.stream(stream):           # (None: no change)
+            workspace.zero_()
     _check(workspace, "workspace", None, torch.uint8, dev)
     with _on(dev):
         st = lib().kda_chunk_prefill_logdecay(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -255,7 +273,7 @@ def decode_tokens(q, k, v, z, A, beta, state_pool, slot_ids=None, out=None, stat
     if slot_ids is not None:
         _check(slot_ids, "slot_ids", (N,), torch.int32, dev)
     if out is None:
-        out = torch.empty((N, n, H, dv), dtype=q.dtype, device=dev)
+        out = _result(stream, (N, n, H, dv), q.dtype, dev)
     _check(out, "out", (N, n, H, dv), q.dtype, dev)
     if status is not None:
         _check(status, "status", None, None, dev)
@@ -314,7 +332,7 @@ def decode_step(q, k, v, z, A, beta, state, out=None, stream=None):
     _check(beta, "beta", (N, H), torch.float32, dev)
     _check(state, "state", (N, H, dk, dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
+        out = _result(stream, (N, H, dv), q.dtype, dev)
     _check(out, "out", (N, H, dv), q.dtype, dev)
     with _on(dev):
         st = lib().kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
@@ -349,10 +367,10 @@ def chunk_prefill_noalloc(q, k, v, z, A, beta, cu_seqlens, initial_state=None, f
     if initial_state is not None:
         _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     if final_state is None:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _result(stream, (N, H, dk, dv), torch.float32, dev)
     _check(final_state, "final_state", (N, H, dk, dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+        out = _result(stream, (T, H, dv), q.dtype, dev)
     _check(out, "out", (T, H, dv), q.dtype, dev)
     with _on(dev):   # the scratch address and the stream are the current device's
         st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(cu_seqlens), N, T,
@@ -391,14 +409,13 @@ def segment_map(q, k, v, z, A, beta, cu_seqlens, M=None, b=None, workspace=None,
     _check(cu_seqlens, "cu_seqlens", None, torch.int32, dev)
     N = cu_seqlens.shape[0] - 1
     if M is None:
-        M = torch.empty((N, H, dk, dk), dtype=torch.float32, device=dev)
+        M = _result(stream, (N, H, dk, dk), torch.float32, dev)
     if b is None:
-        b = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        b = _result(stream, (N, H, dk, dv), torch.float32, dev)
     _check(M, "M", (N, H, dk, dk), torch.float32, dev)
     _check(b, "b", (N, H, dk, dv), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(segment_map_workspace_size(T, N, H, dk, dv, q.dtype), dtype=torch.uint8,
-                                device=dev)
+        workspace = _empty(stream, segment_map_workspace_size(T, N, H, dk, dv, q.dtype), torch.uint8, dev)
     _check(workspace, "workspace", None, torch.uint8, dev)
     with _on(dev):
         st = lib().kda_segment_map(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
@@ -424,7 +441,7 @@ def state_compose(M, b, initial_state=None, states=None, stream=None):
     if initial_state is not None:
         _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     if states is None:
-        states = torch.empty((R + 1, N, H, dk, dv), dtype=torch.float32, device=dev)
+        states = _result(stream, (R + 1, N, H, dk, dv), torch.float32, dev)
     _check(states, "states", (R + 1, N, H, dk, dv), torch.float32, dev)
     with _on(dev):
         st = lib().kda_state_compose(_ptr(M), _ptr(b), R, N, H, dk, dv, _ptr(initial_state),

@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from .kda import KDA_BF16, KDA_F32, KDA_OK, KDAError, lib
+from .kda import KDA_BF16, KDA_F32, KDA_OK, KDAError, _empty, lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "sigmoid": 4}
 _CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
@@ -105,15 +105,6 @@ def _code(dtype, name):
     if c is None:
         raise TypeError(f"{name}: unsupported dtype {dtype}")
     return c
-
-
-def _empty(stream, shape, dtype, device):
-    """A new tensor for a call on `stream`, out of that stream's memory: what the current
-    stream has freed may still be in use by kernels that `stream` does not wait for."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _size(name, device, *args):
