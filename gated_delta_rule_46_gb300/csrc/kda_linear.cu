@@ -29,12 +29,34 @@ using namespace tc;
 constexpr long long kWaitBudget = 2000000000LL;   // cycles (about one second)
 constexpr long long kDrain = 20000000LL;          // cycles (about ten milliseconds)
 
+// GELU's Phi, with its relative precision in the lower tail too, where (1 + erf) / 2
+// cancels (5 % off at y = -5, 0 below -5.5).  Phi(-a) = e^{-a^2 / 2} R(a): R, Mills'
+// ratio over sqrt(2 pi), is smooth in t = 1 / (1 + 0.26 a) all the way to a = inf, where
+// it is a multiple of t; R / t is taken from a polynomial of degree 8 in t, fitted by
+// reweighted least squares to a relative error of 3e-8.  Rounding makes that 4e-7 up
+// to |y| = 1, 1.5e-6 to 5 and 5e-6 to 10 (the exponent's ulp).  8192 x 8192 x 512 in
+// bf16: 117-135 us; 140-163 with erff, 240-296 with erfcf, 65-80 without an activation.
+__device__ __forceinline__ float normal_cdf(float y) {
+    const float t = rcp(fmaf(0.26f, fabsf(y), 1.f));
+    float q = 0.030235235f;
+    q = fmaf(q, t, -0.15151833f);
+    q = fmaf(q, t, 0.24878243f);
+    q = fmaf(q, t, -0.14784548f);
+    q = fmaf(q, t, 0.15879746f);
+    q = fmaf(q, t, 0.051948357f);
+    q = fmaf(q, t, 0.102792896f);
+    q = fmaf(q, t, 0.10305038f);
+    q = fmaf(q, t, 0.103757054f);
+    const float p = q * t * ex2(-0.5f * kLog2E * y * y);
+    return y < 0.f ? p : 1.f - p;
+}
+
 // The activation on the float32 sum.  sigmoid and silu are written with
 // exp(-y): it overflows to +inf for very negative y, where both then give 0.
 template <int ACT>
 __device__ __forceinline__ float activate(float y) {
     if constexpr (ACT == KDA_ACT_RELU) return y > 0.f ? y : (y != y ? y : 0.f);
-    if constexpr (ACT == KDA_ACT_GELU) return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
+    if constexpr (ACT == KDA_ACT_GELU) return y * normal_cdf(y);
     if constexpr (ACT == KDA_ACT_SILU) return __fdividef(y, 1.f + __expf(-y));
     if constexpr (ACT == KDA_ACT_SIGMOID) return __fdividef(1.f, 1.f + __expf(-y));
     return y;
