@@ -27,7 +27,7 @@ struct LinearParams {
 };
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t st);
 // gridDim.y of the largest launch of its few-rows kernel
-int64_t linear_row_tiles(int64_t M, int64_t K, bool f32);
+int64_t linear_row_tiles(int64_t M);
 
 struct DecayParams {
     const void *q, *k, *v;

@@ -66,7 +66,7 @@ kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *
 }
 
 int64_t kda_testing_linear_row_tiles(int64_t M, int64_t K, kda_dtype_t out_dtype) {
-    return M > 0 && K > 0 ? kda::linear_row_tiles(M, K, out_dtype == KDA_F32) : 0;
+    return M > 0 && K > 0 && dtype_ok(out_dtype) ? kda::linear_row_tiles(M) : 0;
 }
 
 size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int H, int dk, int dv,

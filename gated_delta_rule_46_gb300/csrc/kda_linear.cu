@@ -98,7 +98,7 @@ struct RowsParams {
     const __nv_bfloat16 *x, *w;   // LOAD = 1
     int64_t ldx;
     int NT, stages, S;
-    int sums;             // accumulators in TMEM, taken in turn
+    int per, parts;       // K steps of one part of the sum; accumulators for the parts after the first
 };
 
 template <int ACT, bool F32>
@@ -114,20 +114,6 @@ __device__ __forceinline__ void put(const Tail &t, int64_t m, int64_t n, float y
     }
 }
 
-// 16 columns of the `sums` accumulators, `apart` columns from one to the next, added up.
-template <bool F32>
-__device__ __forceinline__ void load_sums(uint32_t at, int apart, int sums, float (&d)[16]) {
-    ptx::tmem_ld16(at, d);
-    ptx::tmem_ld_wait(d);
-    if constexpr (F32)
-        for (int i = 1; i < sums; ++i) {
-            float x[16];
-            ptx::tmem_ld16(at + i * apart, x);
-            ptx::tmem_ld_wait(x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) d[e] += x[e];
-        }
-}
 // The eight elements from address a on, out of the two 16-byte words that hold them.
 __device__ __forceinline__ uint4 shifted(const uint4 &x, const uint4 &y, uint32_t a) {
     uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -148,11 +134,11 @@ __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p, int n) {
 }
 
 template <int ACT, bool F32, int LOAD>
-__global__ void __launch_bounds__(LOAD ? 448 : 192)
+__global__ void __launch_bounds__(LOAD ? 448 : 192, 1)
     linear_rows_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                        const RowsParams p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[12], empty[12], done;
+    __shared__ uint64_t full[12], empty[12], done, pfull[2], pfree[2];
     __shared__ uint32_t s_tmem, s_abort;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,9 +147,11 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     const int f0 = (int)(blockIdx.x / p.S) * 128, m0 = (int)blockIdx.y * p.NT;
     const int kb_all = (p.t.K + kBK - 1) / kBK;
     const int kb0 = (int)((int64_t)kb_all * rank / p.S), kb1 = (int)((int64_t)kb_all * (rank + 1) / p.S);
-    const int sums = F32 ? p.sums : 1;
+    // The sum is taken in parts of `per` K steps: the first in the result's own accumulator, the others in `parts` more by
+    // turns, from where the epilogue's warps add them to it.
+    const int steps = kb1 - kb0, passes = F32 ? (steps + p.per - 1) / p.per : 1;
     uint32_t cols = 32;
-    while (cols < (uint32_t)(p.NT * sums)) cols <<= 1;
+    while (cols < (uint32_t)(p.NT * (1 + p.parts))) cols <<= 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -171,6 +159,10 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
             ptx::mbar_init(&empty[i], 1);
         }
         ptx::mbar_init(&done, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&pfull[i], 1);
+            ptx::mbar_init(&pfree[i], 4);        // the epilogue's warps
+        }
         ptx::fence_mbar_init();
         s_abort = 0;
         if (!LOAD) {
@@ -208,13 +200,23 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
         if (ptx::elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_f32(128, p.NT);
             if (p.t.expire && blockIdx.x + blockIdx.y == 0) ok = ptx::mbar_wait(&done, 0, kTestWait);
-            for (int kb = kb0, i = 0; kb < kb1 && ok; ++kb, ++i) {
-                const int s = i % p.stages;
-                if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kWaitBudget)) { ok = false; break; }
+            for (int pass = 0, i = 0; pass < passes && ok; ++pass) {
+                const int b = pass > 0 ? (pass - 1) % p.parts : 0, end = F32 ? min(steps, i + p.per) : steps;
+                if (pass > p.parts && !ptx::mbar_wait(&pfree[b], ((pass - 1) / p.parts - 1) & 1, kWaitBudget)) {
+                    ok = false;
+                    break;
+                }
                 ptx::tc_fence_after_sync();
-                const uint32_t a = ptx::smem_addr(sm + s * stage_bytes);
-                mma_k<4>(tmem + (F32 ? (i % sums) * p.NT : 0), a, 0, a + kABytes, 0, idesc, i >= sums);
-                ptx::mma_commit(&empty[s]);
+                const uint32_t to = tmem + (pass > 0 ? (1 + b) * p.NT : 0);
+                for (bool first = true; i < end; ++i, first = false) {
+                    const int s = i % p.stages;
+                    if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kWaitBudget)) { ok = false; break; }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t a = ptx::smem_addr(sm + s * stage_bytes);
+                    mma_k<4>(to, a, 0, a + kABytes, 0, idesc, !first);
+                    ptx::mma_commit(&empty[s]);
+                }
+                if (ok && pass > 0) ptx::mma_commit(&pfull[b]);
             }
             if (ok) ptx::mma_commit(&done);
         }
@@ -283,9 +285,32 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     const int q = warp & 3;                      // TMEM lane quarter of this warp
     float bias = 0.f;
     const int f = f0 + q * 32 + lane;
+    const int rows = min(p.NT, p.t.M - m0);
     if (reader) {
         if (p.t.bias && f < p.t.N) bias = p.t.bias[f];
-        ok = ptx::mbar_wait(&done, 0, kWaitBudget);
+        if constexpr (F32)
+            for (int pass = 1; pass < passes; ++pass) {
+                // (a part's barrier stands for all products before it too)
+                const int b = (pass - 1) % p.parts;
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&pfull[b], ((pass - 1) / p.parts) & 1, kWaitBudget));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t at = tmem + ((uint32_t)q << 21);
+                for (int c0 = 0; c0 < rows; c0 += 16) {
+                    float d[16], x[16];
+                    ptx::tmem_ld16(at + c0, d);
+                    ptx::tmem_ld16(at + (1 + b) * p.NT + c0, x);
+                    ptx::tmem_ld_wait(d, x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) d[e] += x[e];
+                    ptx::tmem_st16(at + c0, d);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&pfree[b]);
+            }
+        ok = ok && ptx::mbar_wait(&done, 0, kWaitBudget);
         ptx::tc_fence_after_sync();
     }
     if (!ok) {
@@ -294,12 +319,12 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
     }
     __syncthreads();
     if (s_abort) drain();
-    const int rows = min(p.NT, p.t.M - m0);
     if (p.S == 1) {
         if (reader && !s_abort) {
             for (int c0 = 0; c0 < rows; c0 += 16) {
                 float d[16];
-                load_sums<F32>(tmem + ((uint32_t)q << 21) + c0, p.NT, min(sums, kb1 - kb0), d);
+                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
+                ptx::tmem_ld_wait(d);
                 if (f < p.t.N)
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
@@ -313,7 +338,8 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192)
         if (reader) {
             for (int c0 = 0; c0 < rows; c0 += 16) {
                 float d[16];
-                load_sums<F32>(tmem + ((uint32_t)q << 21) + c0, p.NT, min(sums, kb1 - kb0), d);
+                ptx::tmem_ld16(tmem + ((uint32_t)q << 21) + c0, d);
+                ptx::tmem_ld_wait(d);
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     if (c0 + c < rows) part[(c0 + c) * 128 + q * 32 + lane] = d[c];
@@ -627,14 +653,9 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
                             pp);
 }
 
-// Rows of x per CTA.  A float32 output is summed in several accumulators in turn, 512 products each (see
-// linear_pair_kernel) or 1024 where TMEM holds no more of them; that leaves fewer rows of x per CTA for large K.
-constexpr int kLeastTile = 64;              // where there are as many rows
-int rows_tile(int64_t M, int64_t K, bool f32) {
-    const int64_t kbs = (K + kBK - 1) / kBK;
-    const int most = !f32 || kbs <= 32 ? 256 : (kbs <= 64 ? 128 : kLeastTile);
-    return M < most ? (int)((M + 15) / 16) * 16 : most;
-}
+// Rows of x per CTA.
+constexpr int kRowsTile = 256;
+int rows_tile(int64_t M) { return M < kRowsTile ? (int)((M + 15) / 16) * 16 : kRowsTile; }
 
 template <int ACT, bool F32, int LOAD>
 cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
@@ -644,7 +665,7 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     rp.w = p.w;
     rp.ldx = p.ldx;
     const int64_t kbs = (p.K + kBK - 1) / kBK;
-    rp.NT = rows_tile(p.M, p.K, F32);
+    rp.NT = rows_tile(p.M);
     const uint32_t stage = kABytes + rp.NT * 128;
     constexpr uint32_t kRoom = 200 * 1024;      // all of an SM's: the weights under way are what hides HBM's latency
     rp.stages = (int)(kRoom / stage) < 12 ? (int)(kRoom / stage) : 12;
@@ -659,8 +680,12 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
     while (rp.S > 1 && (kbs / rp.S < 4 || tiles > cluster_room<linear_rows_kernel<ACT, F32, LOAD>>(
                                                       rp.S, LOAD ? 448 : 192, kRoom + 1024)))
         --rp.S;
-    const int64_t need = ((kbs + rp.S - 1) / rp.S + 7) / 8;
-    rp.sums = !F32 ? 1 : (int)(need < 512 / rp.NT ? need : 512 / rp.NT);
+    // A float32 output is summed in parts of 512 products (see linear_pair_kernel), up to two of them under way beside the
+    // result as far as TMEM holds them.
+    const int64_t steps = (kbs + rp.S - 1) / rp.S, room = 512 / rp.NT - 1 < 2 ? 512 / rp.NT - 1 : 2;
+    rp.per = 8;
+    const int64_t after = F32 ? (steps + rp.per - 1) / rp.per - 1 : 0;
+    rp.parts = (int)(after < room ? after : room);
     uint32_t smem = rp.stages * stage;
     if (rp.S > 1 && smem < (uint32_t)rp.NT * 512u) smem = rp.NT * 512u;
     smem += 1024;
@@ -708,13 +733,14 @@ cudaError_t launch_slice(const LinearParams &p, cudaStream_t st) {
     }
 }
 
-// M is worked on in slices: row tiles are the grid's y, which goes up to 65535, and whole pair tiles fill a slice.
-constexpr int64_t kSlice = int64_t(65535) * kLeastTile / 256 * 256;
+// M is worked on in slices of whole tiles: row tiles are the grid's y, which goes up to 65535.
+constexpr int64_t kSlice = int64_t(1) << 22;
+static_assert(kSlice / kRowsTile <= 65535 && kSlice % kRowsTile == 0, "slice");
 
 }  // namespace
 
-int64_t linear_row_tiles(int64_t M, int64_t K, bool f32) {
-    const int64_t m = M < kSlice ? M : kSlice, tile = rows_tile(m, K, f32);
+int64_t linear_row_tiles(int64_t M) {
+    const int64_t m = M < kSlice ? M : kSlice, tile = rows_tile(m);
     return (m + tile - 1) / tile;
 }
 
