@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192, 1)
     const int kb0 = (int)((int64_t)kb_all * rank / p.S), kb1 = (int)((int64_t)kb_all * (rank + 1) / p.S);
     // The sum is taken in parts of `per` K steps: the first in the result's own accumulator, the others in `parts` more by
     // turns, from where the epilogue's warps add them to it.
-    const int steps = kb1 - kb0, passes = F32 ? (steps + p.per - 1) / p.per : 1;
+    const int steps = kb1 - kb0, passes = (steps + p.per - 1) / p.per;
     uint32_t cols = 32;
     while (cols < (uint32_t)(p.NT * (1 + p.parts))) cols <<= 1;
 
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192, 1)
             const uint32_t idesc = ptx::idesc_bf16_f32(128, p.NT);
             if (p.t.expire && blockIdx.x + blockIdx.y == 0) ok = ptx::mbar_wait(&done, 0, kTestWait);
             for (int pass = 0, i = 0; pass < passes && ok; ++pass) {
-                const int b = pass > 0 ? (pass - 1) % p.parts : 0, end = F32 ? min(steps, i + p.per) : steps;
+                const int b = pass > 0 ? (pass - 1) % p.parts : 0, end = min(steps, i + p.per);
                 if (pass > p.parts && !ptx::mbar_wait(&pfree[b], ((pass - 1) / p.parts - 1) & 1, kWaitBudget)) {
                     ok = false;
                     break;
@@ -288,28 +288,27 @@ __global__ void __launch_bounds__(LOAD ? 448 : 192, 1)
     const int rows = min(p.NT, p.t.M - m0);
     if (reader) {
         if (p.t.bias && f < p.t.N) bias = p.t.bias[f];
-        if constexpr (F32)
-            for (int pass = 1; pass < passes; ++pass) {
-                // (a part's barrier stands for all products before it too)
-                const int b = (pass - 1) % p.parts;
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&pfull[b], ((pass - 1) / p.parts) & 1, kWaitBudget));
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
-                const uint32_t at = tmem + ((uint32_t)q << 21);
-                for (int c0 = 0; c0 < rows; c0 += 16) {
-                    float d[16], x[16];
-                    ptx::tmem_ld16(at + c0, d);
-                    ptx::tmem_ld16(at + (1 + b) * p.NT + c0, x);
-                    ptx::tmem_ld_wait(d, x);
+        for (int pass = 1; pass < passes; ++pass) {
+            // (a part's barrier stands for all products before it too)
+            const int b = (pass - 1) % p.parts;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&pfull[b], ((pass - 1) / p.parts) & 1, kWaitBudget));
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            const uint32_t at = tmem + ((uint32_t)q << 21);
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                float d[16], x[16];
+                ptx::tmem_ld16(at + c0, d);
+                ptx::tmem_ld16(at + (1 + b) * p.NT + c0, x);
+                ptx::tmem_ld_wait(d, x);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) d[e] += x[e];
-                    ptx::tmem_st16(at + c0, d);
-                }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&pfree[b]);
+                for (int e = 0; e < 16; ++e) d[e] += x[e];
+                ptx::tmem_st16(at + c0, d);
             }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&pfree[b]);
+        }
         ok = ok && ptx::mbar_wait(&done, 0, kWaitBudget);
         ptx::tc_fence_after_sync();
     }
@@ -653,6 +652,10 @@ cudaError_t launch_pair(const LinearParams &p, cudaStream_t st) {
                             pp);
 }
 
+// Most products of one sum in the tensor cores for a bf16 output: each step of 16 loses up to an ulp of it, 2^-23,
+// together 2^-11 where the output's rounding takes 2^-9.
+constexpr int kPart = 65536;
+
 // Rows of x per CTA.
 constexpr int kRowsTile = 256;
 int rows_tile(int64_t M) { return M < kRowsTile ? (int)((M + 15) / 16) * 16 : kRowsTile; }
@@ -681,10 +684,10 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t st) {
                                                       rp.S, LOAD ? 448 : 192, kRoom + 1024)))
         --rp.S;
     // A float32 output is summed in parts of 512 products (see linear_pair_kernel), up to two of them under way beside the
-    // result as far as TMEM holds them.
+    // result as far as TMEM holds them; a bf16 output in parts of kPart.
     const int64_t steps = (kbs + rp.S - 1) / rp.S, room = 512 / rp.NT - 1 < 2 ? 512 / rp.NT - 1 : 2;
-    rp.per = 8;
-    const int64_t after = F32 ? (steps + rp.per - 1) / rp.per - 1 : 0;
+    rp.per = F32 ? 8 : kPart / kBK;
+    const int64_t after = (steps + rp.per - 1) / rp.per - 1;
     rp.parts = (int)(after < room ? after : room);
     uint32_t smem = rp.stages * stage;
     if (rp.S > 1 && smem < (uint32_t)rp.NT * 512u) smem = rp.NT * 512u;
@@ -711,7 +714,10 @@ cudaError_t launch_act(const LinearParams &p, cudaStream_t st) {
     // 4096 x 4096: 25 us, 32 by rows), of 256 x 128 where those do (512 x 4096 x 4096: 21 us, 24 either way; 1024^3: 8.5
     // us, 10.4 by rows).  With fewer, splitting K beats both (256 x 4096 x 4096: 16 us, 20 in pairs).
     // (A float32 output's epilogue holds its sums in registers, 128 columns' worth.)
+    // K past kPart goes by rows, where the sums of a bf16 output too are taken in parts (600 x 2048 x 65600: 200 us, and 281
+    // in pairs with 65536 products; 2048 x 4096: 728 and 613).
     const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256), pairs = sm_count() / 2;
+    if (!F32 && p.K > kPart) return launch_rows<ACT, F32, 0>(p, st);
     if constexpr (!F32)
         if (store && p.M > 128 && tiles * 2 > pairs) return launch_pair<ACT, F32, 256>(p, st);
     if (store && p.M > 256 && tiles * 5 > pairs) return launch_pair<ACT, F32, 128>(p, st);
