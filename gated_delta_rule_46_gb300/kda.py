@@ -133,6 +133,13 @@ def _result(stream, shape, dtype, device):
     return t
 
 
+def _record(stream, *tensors):
+    """What a call on `stream` reads and writes may be freed before it has run there."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _on(device):
     """Makes `device` current for a call: the library launches on the current
     device and takes torch's current stream of that device."""
@@ -152,6 +159,8 @@ def gate(z: torch.Tensor, A: torch.Tensor, g_out: torch.Tensor | None = None, st
     if g_out is None:
         g_out = _result(stream, (T, H, dk), torch.float32, z.device)
     _check(g_out, "g_out", (T, H, dk), torch.float32, z.device)
+    if stream is not None:
+        _record(stream, z, A, g_out)
     with _on(z.device):
         _raise(lib().kda_gate(_ptr(z), _dtype_code(z), _ptr(A), _ptr(g_out), T, H, dk,
                               _stream(stream)), "kda_gate")
@@ -196,6 +205,8 @@ def chunk_prefill(q, k, v, z, A, beta, cu_seqlens, initial_state=None, final_sta
     if workspace is None:
         workspace = _empty(stream, wsb, torch.uint8, dev)
     _check(workspace, "workspace", None, torch.uint8, dev)
+    if stream is not None:
+        _record(stream, q, k, v, z, A, beta, cu_seqlens, initial_state, final_state, out, workspace)
     with _on(dev):
         st = lib().kda_chunk_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
                                      _ptr(cu_seqlens), N, T, H, dk, dv, _dtype_code(q),
@@ -240,6 +251,8 @@ def chunk_prefill_logdecay(q, k, v, g, beta, cu_seqlens, initial_state=None, fin
         with torch.cuda.stream(stream):           # (None: no change)
             workspace.zero_()
     _check(workspace, "workspace", None, torch.uint8, dev)
+    if stream is not None:
+        _record(stream, q, k, v, g, beta, cu_seqlens, initial_state, final_state, out, workspace)
     with _on(dev):
         st = lib().kda_chunk_prefill_logdecay(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                               _ptr(cu_seqlens), N, T, H, dk, dv, _dtype_code(q),
@@ -277,6 +290,8 @@ def decode_tokens(q, k, v, z, A, beta, state_pool, slot_ids=None, out=None, stat
     _check(out, "out", (N, n, H, dv), q.dtype, dev)
     if status is not None:
         _check(status, "status", None, None, dev)
+    if stream is not None:
+        _record(stream, q, k, v, z, A, beta, state_pool, slot_ids, out, status)
     with _on(dev):
         st = lib().kda_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
                                      _ptr(state_pool), state_pool.shape[0], _ptr(slot_ids), _ptr(out),
@@ -298,6 +313,8 @@ def state_slots_copy(state_pool, slot_ids, states, to_pool=True, status=None, st
     _check(states, "states", (N, H, dk, dv), torch.float32, dev)
     if status is not None:
         _check(status, "status", None, None, dev)
+    if stream is not None:
+        _record(stream, state_pool, slot_ids, states, status)
     with _on(dev):
         st = lib().kda_state_slots_copy(_ptr(state_pool), P, _ptr(slot_ids), _ptr(states), N, H, dk,
                                         dv, 1 if to_pool else 0, _ptr(status), _stream(stream))
@@ -334,6 +351,8 @@ def decode_step(q, k, v, z, A, beta, state, out=None, stream=None):
     if out is None:
         out = _result(stream, (N, H, dv), q.dtype, dev)
     _check(out, "out", (N, H, dv), q.dtype, dev)
+    if stream is not None:
+        _record(stream, q, k, v, z, A, beta, state, out)
     with _on(dev):
         st = lib().kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
                                    _ptr(state), _ptr(out), N, H, dk, dv, _dtype_code(q),
@@ -372,6 +391,8 @@ def chunk_prefill_noalloc(q, k, v, z, A, beta, cu_seqlens, initial_state=None, f
     if out is None:
         out = _result(stream, (T, H, dv), q.dtype, dev)
     _check(out, "out", (T, H, dv), q.dtype, dev)
+    if stream is not None:
+        _record(stream, q, k, v, z, A, beta, cu_seqlens, initial_state, final_state, out)
     with _on(dev):   # the scratch address and the stream are the current device's
         st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(cu_seqlens), N, T,
                 H, dk, dv, _dtype_code(q), _ptr(initial_state), _ptr(final_state), _ptr(out),
@@ -417,6 +438,8 @@ def segment_map(q, k, v, z, A, beta, cu_seqlens, M=None, b=None, workspace=None,
     if workspace is None:
         workspace = _empty(stream, segment_map_workspace_size(T, N, H, dk, dv, q.dtype), torch.uint8, dev)
     _check(workspace, "workspace", None, torch.uint8, dev)
+    if stream is not None:
+        _record(stream, q, k, v, z, A, beta, cu_seqlens, M, b, workspace)
     with _on(dev):
         st = lib().kda_segment_map(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta),
                                    _ptr(cu_seqlens), N, T, H, dk, dv, _dtype_code(q), _ptr(M), _ptr(b),
@@ -443,6 +466,8 @@ def state_compose(M, b, initial_state=None, states=None, stream=None):
     if states is None:
         states = _result(stream, (R + 1, N, H, dk, dv), torch.float32, dev)
     _check(states, "states", (R + 1, N, H, dk, dv), torch.float32, dev)
+    if stream is not None:
+        _record(stream, M, b, initial_state, states)
     with _on(dev):
         st = lib().kda_state_compose(_ptr(M), _ptr(b), R, N, H, dk, dv, _ptr(initial_state),
                                      _ptr(states), _stream(stream))

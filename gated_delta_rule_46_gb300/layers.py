@@ -8,7 +8,8 @@ status into ``KDAError``.  Inputs [T, H, d] may be slices of a wider row-major
 tensor (a fused projection): a row (the last two axes) is dense, the rows any
 stride apart.  Outputs and workspaces that a call allocates come from the memory
 of the stream it runs on (`stream`, or torch's current one); outputs may be used
-on the current stream as well, once it waits for `stream`.
+on the current stream as well, once it waits for `stream`, and any tensor of the
+call may be dropped before the call has run.
 """
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ import ctypes
 
 import torch
 
-from .kda import KDA_BF16, KDA_F32, KDA_OK, KDAError, _empty, lib
+from .kda import KDA_BF16, KDA_F32, KDA_OK, KDAError, _empty, _record, lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "sigmoid": 4}
 _CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
@@ -166,6 +167,8 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, out_dtype=None,
     _call("kda_linear", dev, stream, new, x.data_ptr(), ldx, wp, _dense(bias, "bias", (N,), torch.float32, dev),
           _dense(residual, "residual", (M, N), out.dtype, dev), _dense(out, "out", (M, N), out.dtype, dev), M, N, K,
           ACTIVATIONS[act], code, _status(status, dev))
+    if stream is not None:
+        _record(stream, x, w, bias, residual, out, status)
     return out
 
 
@@ -209,6 +212,8 @@ def decay_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, final_stat
           _dense(final_state, "final_state", (N, H, dk, dv), torch.float32, dev),
           _dense(out, "out", (T, H, dv), dt, dev), wp, size,
           _status(status, dev))
+    if stream is not None:
+        _record(stream, q, k, v, log_decay, cu_seqlens, initial_state, final_state, out, workspace, status)
     return out, final_state
 
 
@@ -234,6 +239,8 @@ def decay_decode(q, k, v, log_decay, state_pool, slot_ids=None, out=None, scale=
           _dense(state_pool, "state_pool", (P, H, dk, dv), torch.float32, dev), P,
           _dense(slot_ids, "slot_ids", (N,), torch.int32, dev), _dense(out, "out", (N, H, dv), dt, dev), N, H, dk,
           dv, code, scale, _status(status, dev))
+    if stream is not None:
+        _record(stream, q, k, v, log_decay, state_pool, slot_ids, out, status)
     return out
 
 
@@ -255,6 +262,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, start_pos, cu_seqlens=None,
     _call("kda_paged_append", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, P, ps, tp, cols,
           _dense(start_pos, "start_pos", (N,), torch.int32, dev),
           _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, d, code, _status(status, dev))
+    if stream is not None:
+        _record(stream, k, v, k_cache, v_cache, page_table, start_pos, cu_seqlens, status)
 
 
 def paged_decode_workspace_size(num_seqs, max_tokens, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
@@ -294,4 +303,6 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
           d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),
           _dense(lse, "lse", (N, Hq), torch.float32, dev), _dense(workspace, "workspace", (size,), torch.uint8, dev),
           size, _status(status, dev))
+    if stream is not None:
+        _record(stream, q, k_cache, v_cache, page_table, seq_lens, out, lse, workspace, status)
     return (out, lse) if return_lse else out

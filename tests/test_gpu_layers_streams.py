@@ -73,3 +73,40 @@ def test_results_that_the_current_stream_still_reads(name):
         other = [torch.full((n,), 7, dtype=torch.uint8, device=dev) for n in sizes for _ in range(2)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want)) and len(other)
+
+
+def _args(name, dev):
+    """The call with copies of its inputs, and these copies."""
+    g = torch.Generator(device=dev).manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    if name == "linear":
+        return linear, [rnd(2048, 256).to(BF), rnd(1024, 256).to(BF), rnd(1024), rnd(2048, 1024).to(BF)]
+    if name == "decay_prefill":
+        return (lambda *a, **kw: decay_prefill(*a, want_final_state=False, **kw)[0],
+                [0.3 * rnd(4096, 4, 128).to(BF) for _ in range(3)] +
+                [-rnd(4).abs(), torch.tensor([0, 4096], dtype=torch.int32, device=dev), rnd(1, 4, 128, 128)])
+    if name == "decay_decode":
+        return decay_decode, [0.3 * rnd(2048, 4, 64) for _ in range(3)] + [-rnd(4).abs(), rnd(2048, 4, 64, 64),
+                                                                           torch.arange(2048, dtype=torch.int32, device=dev)]
+    table = torch.randperm(512, generator=torch.Generator().manual_seed(2)).to(torch.int32).reshape(4, 128).to(dev)
+    return paged_decode, [rnd(4, 256, 128).to(BF), rnd(512, 8, 64, 128).to(BF), rnd(512, 8, 64, 128).to(BF), table,
+                          torch.tensor([8000, 5, 8192, 700], dtype=torch.int32, device=dev)]
+
+
+@pytest.mark.parametrize("name", ["linear", "decay_prefill", "decay_decode", "paged_decode"])
+def test_inputs_that_are_dropped_before_the_call_has_run(name):
+    dev = need_gpu()
+    f, args = _args(name, dev)
+    want = f(*(t.clone() for t in args)).clone()
+    s = torch.cuda.Stream()
+    given = [t.clone() for t in args]
+    sizes = [t.numel() * t.element_size() for t in given]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(DELAY)
+    got = f(*given, stream=s)
+    del given
+    other = [torch.full((n,), 255, dtype=torch.uint8, device=dev) for n in sizes for _ in range(2)]     # NaN as numbers
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(other)

@@ -78,3 +78,29 @@ def test_results_that_the_current_stream_still_reads(name):
         other = [torch.full((n,), 7, dtype=torch.uint8, device=dev) for n in sizes for _ in range(2)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want)) and len(other)
+
+
+@pytest.mark.parametrize("name", ["chunk_prefill", "decode_tokens", "segment_map"])
+def test_inputs_that_are_dropped_before_the_call_has_run(name):
+    dev = need_gpu()
+    w = inputs.custom([3000, 1096], H=4, dk=128, dv=128, dtype=torch.bfloat16)
+    d = {n: (t.to(dev) if t is not None else None) for n, t in inputs.prefill_inputs(w).items()}
+    order = [d[n] for n in ("q", "k", "v", "z", "A", "beta", "cu_seqlens")]
+    f = {"chunk_prefill": lambda *a, **kw: K.chunk_prefill(*a, **kw)[0], "segment_map": lambda *a, **kw: K.segment_map(*a, **kw)[1],
+         "decode_tokens": lambda *a, **kw: K.decode_tokens(*a, **kw)}[name]
+    if name == "decode_tokens":
+        order = [t[:1024].unsqueeze(1).contiguous() for t in order[:4]] + [d["A"], d["beta"][:1024].unsqueeze(1).contiguous(),
+                                                                          torch.ones(1024, 4, 128, 128, device=dev)]
+    want = f(*(t.clone() for t in order)).clone()
+    s = torch.cuda.Stream()
+    given = [t.clone() for t in order]
+    sizes = [t.numel() * t.element_size() for t in given]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(DELAY)
+    got = f(*given, stream=s)
+    del given
+    other = [torch.full((n,), 255, dtype=torch.uint8, device=dev) for n in sizes for _ in range(2)]     # NaN as numbers
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(other)
