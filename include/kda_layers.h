@@ -28,7 +28,8 @@
  *     where stated; KDA_ERR_INVALID_ARG otherwise.
  *   - A row's result depends on that row's inputs alone: infinities and NaN in
  *     other sequences, in later tokens, or in cache slots that no token was
- *     written to do not reach it.
+ *     written to do not reach it.  (Its own infinities may give NaN where the
+ *     formula has an infinity.)
  */
 #ifndef KDA_GB300_LAYERS_H
 #define KDA_GB300_LAYERS_H
@@ -55,10 +56,16 @@ typedef enum {
  *   residual  [M, N] of out_dtype, dense, or NULL; it may be the same buffer
  *             as out
  *   out       [M, N] of out_dtype (KDA_BF16 or KDA_F32), dense (written)
- * Products are summed in float32 and rounded once, after the residual.  Any
- * M, N >= 0 and K >= 1 below 2^31, any row stride and alignment of elements; K a
- * multiple of 8 with 16-byte aligned rows is loaded by TMA, anything else by way
- * of registers, which is several times slower.
+ * Products are summed in float32 and rounded once, after the residual.  The
+ * tensor cores' own sums lose up to an ulp, 2^-23, at each step of 16 products:
+ * a float32 output is summed there in parts of 512 products, which are added in
+ * float32, a bf16 output in parts of up to 65536 (2^-11 of the result at most,
+ * where its rounding takes 2^-9).
+ * Any M, N >= 0 and K >= 1 below 2^31, any row stride and alignment of elements.
+ * K a multiple of 8 with 16-byte aligned rows is loaded by TMA, anything else by
+ * way of registers: three times slower for few rows, ten times for thousands.
+ * Out and residual with 16-byte aligned rows are stored and loaded by TMA for
+ * many rows, others take about twice the time.
  */
 kda_status_t kda_linear(const void *x, int64_t ldx, const void *w, const float *bias,
                         const void *residual, void *out, int64_t M, int64_t N, int64_t K,
@@ -79,7 +86,8 @@ size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int 
  *     S_t = exp(log_decay) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
  *   q, k           [total_tokens, H, dk], v [total_tokens, H, dv], of dtype, row
  *                  strides ldq, ldk, ldv
- *   log_decay      [H] float32, device; <= 0 for a decay, -inf for no memory
+ *   log_decay      [H] float32, device; <= 0 for a decay, -inf for no memory, NaN
+ *                  for NaN from the first token on
  *   cu_seqlens     [num_seqs + 1] int32, device, as for kda_chunk_prefill
  *   initial_state  [num_seqs, H, dk, dv] float32, or NULL for zeros
  *   final_state    [num_seqs, H, dk, dv] float32 (written), or NULL; it may be
@@ -87,7 +95,11 @@ size_t kda_decay_prefill_workspace_size(int64_t total_tokens, int num_seqs, int 
  *   out            [total_tokens, H, dv] of dtype (written)
  *   workspace      16-byte aligned, or NULL; with fewer bytes than the size
  *                  above the call runs every chain in one piece
- * dk, dv in {32, 64, 128}.  States are float32 throughout.
+ * dk, dv in {32, 64, 128}.  States, and what is added to them, are float32
+ * throughout.  Of a bf16 call's outputs the weights lambda^(i-j) q_i . k_j within
+ * a chunk of 64 tokens, and the copy of the state that multiplies q, are rounded
+ * to bf16 (2^-9 of each, as the output's own rounding) for the tensor cores;
+ * rows that no 16-byte copy can start on are worked on in float32.
  */
 kda_status_t kda_decay_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk,
                                const void *v, int64_t ldv, const float *log_decay,
@@ -151,6 +163,10 @@ size_t kda_paged_decode_workspace_size(int num_seqs, int64_t max_tokens, int Hq,
  *   out          [num_seqs, Hq, d] of dtype (written)
  *   lse          [num_seqs, Hq] float32 (written), or NULL
  *   workspace    16-byte aligned, kda_paged_decode_workspace_size() bytes
+ * Scores, maxima and sums are float32.  With bf16 caches of 64 or 128 channels and
+ * pages of at least eight tokens the softmax weights are rounded to bf16 (2^-9 of
+ * each, as the output's own rounding) for their product with V, though not for
+ * their sum.
  * Tokens on a page whose id lies outside the cache are recorded and left out.
  * A table covers at most 2^30 tokens per sequence.
  */
