@@ -11,8 +11,8 @@
 // by reading w: 64 x 16384 x 8192 takes 46 us (5.9 TB/s), 64 x 4096 x 4096 11.5 us,
 // of which the 34 MB are 5; launch, the first load and the join are the rest.
 // Every sum is held in float32 (TMEM, and the join of a cluster's parts in order
-// of rank, so that results do not depend on timing; a float32 output, and any at very long K, in several
-// parts); the one rounding to fewer bits is out's own.
+// of rank, so that results do not depend on timing; a float32 output, and any at very
+// long K, in several parts); the one rounding to fewer bits is out's own.
 #include <cuda.h>
 
 #include "kda_layers.cuh"
