@@ -85,6 +85,7 @@ const char *kda_status_string(kda_status_t status) {
         case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: unsupported shape or dtype";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA: CUDA call or launch failed";
         case KDA_ERR_DEVICE_TIMEOUT: return "KDA_ERR_DEVICE_TIMEOUT: device-side wait expired";
+        case KDA_ERR_NO_PAGES: return "KDA_ERR_NO_PAGES: no free page left";
     }
     return "KDA_ERR_UNKNOWN";
 }

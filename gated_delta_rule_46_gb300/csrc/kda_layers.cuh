@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -96,9 +97,30 @@ struct PagedParams {
     bool lone;                      // no item has more than one tile: nothing to join
     int expire;                     // test support
     uint32_t *status;
+    const float *ks, *vs;           // e4m3 caches: [num_pages][Hkv][page_size / block]
+    int block_shift;
 };
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
 cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st);
+// an e4m3 cache; bf16: the queries and outputs
+size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
+cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaStream_t st);
+
+struct AppendQ8Params {
+    const void *k, *v;
+    int64_t ldk, ldv;               // row strides, elements
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+    int num_pages, page_shift, block_shift;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *start, *cu_seqlens;
+    int num_seqs, Hkv;
+    int64_t total;
+    uint32_t *status;
+};
+// vec16: rows that 16-byte loads can start on
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, int d, bool bf16, bool vec16, cudaStream_t st);
 
 // Number of SMs of the current device.
 int sm_count();
@@ -169,5 +191,14 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned bl
 }
 
 constexpr float kLog2E = 1.4426950408889634f;
+
+// Two e4m3 codes, low byte first.
+__device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t u) {
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3)));
+}
+// The nearest codes, ties to the even one; past the largest value, 448, that one; NaN stays NaN.
+__device__ __forceinline__ uint16_t f2_to_e4m3x2(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
 
 }  // namespace kda

@@ -131,18 +131,37 @@ struct Ch8<__nv_bfloat16, D> {
         }
     }
 };
+template <int D>
+struct Ch8<__nv_fp8_e4m3, D> {
+    uint2 u = {};
+    static __device__ int channel(int l, int e) { return l * 8 + e; }
+    __device__ void load(const __nv_fp8_e4m3 *row, int l) {
+        u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(row) + l * 8);
+    }
+    __device__ void get(float (&x)[8]) const {
+        const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = e4m3x2_to_f2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
 
-template <typename T, int D, int HB>
+// T: queries and outputs; C: the cache.
+template <typename C, int D, int HB>
 struct Simt {
     static constexpr int WARPS = HB == 4 ? 10 : 8;                         // registers for as many
-    static constexpr int U = HB == 4 || sizeof(T) == 2 ? 4 : 2;            // rounds between corrections
+    static constexpr int U = HB == 4 || sizeof(C) <= 2 ? 4 : 2;            // rounds between corrections
     static constexpr int LPT = D / 8, TPW = 32 / LPT;                      // lanes per token, tokens per warp
     static constexpr uint32_t smem = sizeof(float) * WARPS * HB * (D + 2);
 };
 
-template <typename T, int D, int HB>
-__global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_simt_kernel(const PagedParams p) {
-    using S = Simt<T, D, HB>;
+template <typename T, typename C, int D, int HB>
+__global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_simt_kernel(const PagedParams p) {
+    using S = Simt<C, D, HB>;
+    constexpr bool kScaled = sizeof(C) == 1;          // codes with a scale for each block of tokens
     constexpr int TILE = kTile, U = S::U, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
     extern __shared__ float sm[];                     // of each warp: m and l [HB], outputs [HB][D]
     __shared__ int64_t s_sum[257];
@@ -161,7 +180,7 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
     int item = (int)((w - sp.cum * items) / nt);
     int64_t tile = (w - sp.cum * items) - item * nt;
     const float sc2 = p.scale * kLog2E;
-    const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
+    const C *kc = static_cast<const C *>(p.kc), *vc = static_cast<const C *>(p.vc);
 
     while (w < w1) {
         const int len = clamp_len(p, n, tid == 0 && item == 0 && tile == 0);
@@ -178,7 +197,7 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 q[h][e] = h < hb ? to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)(hq0 + h) * D +
-                                                                      Ch8<T, D>::channel(l8, e)]) * sc2
+                                                                      Ch8<C, D>::channel(l8, e)]) * sc2
                                  : 0.f;
         float m[HB], l[HB], acc[HB][8];
 #pragma unroll
@@ -203,20 +222,25 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
                 }
             }
         };
-        auto fetch = [&](const T *cache, int t, const int (&pg)[U], Ch8<T, D> (&x)[U]) {
+        auto fetch = [&](const C *cache, const float *scale, int t, const int (&pg)[U], Ch8<C, D> (&x)[U], float (&f)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                x[u] = Ch8<T, D>();
-                if (pg[u] >= 0)
-                    x[u].load(cache + (((((int64_t)pg[u] * p.Hkv + kvh) << p.page_shift) +
-                                        ((t + u * STEP) & ((1 << p.page_shift) - 1))) * D), l8);
+                x[u] = Ch8<C, D>();
+                f[u] = 0.f;
+                if (pg[u] >= 0) {
+                    const int64_t row = ((((int64_t)pg[u] * p.Hkv + kvh) << p.page_shift) +
+                                         ((t + u * STEP) & ((1 << p.page_shift) - 1)));
+                    x[u].load(cache + row * D, l8);
+                    if constexpr (kScaled) f[u] = scale[row >> p.block_shift];
+                }
             }
         };
-        Ch8<T, D> k[U], v[U];
+        Ch8<C, D> k[U], v[U];
+        float fk[U], fv[U];                               // (of scaled caches)
         int pg[U], pn[U];
         pages(t, pg);
-        fetch(kc, t, pg, k);
-        fetch(vc, t, pg, v);
+        fetch(kc, p.ks, t, pg, k, fk);
+        fetch(vc, p.vs, t, pg, v, fv);
         pages(t + U * STEP, pn);
         // the rounds of a warp's lanes are the same in number: the shuffles are the whole warp's
         const int t0 = (int)(first * TILE) + warp * S::TPW;
@@ -231,10 +255,10 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
                     float a = x[0] * q[h][0];
 #pragma unroll
                     for (int e = 1; e < 8; ++e) a = fmaf(x[e], q[h][e], a);
-                    s[u][h] = a;
+                    s[u][h] = kScaled ? a * fk[u] : a;
                 }
             }
-            fetch(kc, t + U * STEP, pn, k);
+            fetch(kc, p.ks, t + U * STEP, pn, k, fk);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -265,11 +289,13 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
                 float x[8];
                 v[u].get(x);
 #pragma unroll
-                for (int h = 0; h < HB; ++h)
+                for (int h = 0; h < HB; ++h) {
+                    const float w = kScaled ? s[u][h] * fv[u] : s[u][h];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(s[u][h], x[e], acc[h][e]);
+                    for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(w, x[e], acc[h][e]);
+                }
             }
-            fetch(vc, t + U * STEP, pn, v);
+            fetch(vc, p.vs, t + U * STEP, pn, v, fv);
 #pragma unroll
             for (int u = 0; u < U; ++u) pg[u] = pn[u];
             pages(t + 2 * U * STEP, pn);
@@ -296,7 +322,7 @@ __global__ void __launch_bounds__(Simt<T, D, HB>::WARPS * 32, 1) paged_decode_si
             for (int h = 0; h < HB; ++h) {
                 if (lane == 0) { mine[2 * h] = m[h]; mine[2 * h + 1] = l[h]; }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mine[2 * HB + h * D + Ch8<T, D>::channel(l8, e)] = acc[h][e];
+                for (int e = 0; e < 8; ++e) mine[2 * HB + h * D + Ch8<C, D>::channel(l8, e)] = acc[h][e];
             }
         __syncthreads();
         const bool whole = first == 0 && last == nt;
@@ -435,25 +461,25 @@ size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, 
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 
-template <typename T, int D, int HB>
+template <typename T, typename C, int D, int HB>
 static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
-    using S = Simt<T, D, HB>;
+    using S = Simt<C, D, HB>;
     p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile;
-    auto *kernel = paged_decode_simt_kernel<T, D, HB>;
-    cudaError_t e = allow_smem<paged_decode_simt_kernel<T, D, HB>>(S::smem);
+    auto *kernel = paged_decode_simt_kernel<T, C, D, HB>;
+    cudaError_t e = allow_smem<paged_decode_simt_kernel<T, C, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
     const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
     if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
     return launch_join<T, D, kTile, HB>(p, grid, st);
 }
 
-template <typename T>
+template <typename T, typename C = T>
 static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) {
     const bool four = heads_simt(p.G) == 4;
     switch (d) {
-        case 32: return four ? paged_simt<T, 32, 4>(p, st) : paged_simt<T, 32, 8>(p, st);
-        case 64: return four ? paged_simt<T, 64, 4>(p, st) : paged_simt<T, 64, 8>(p, st);
-        case 128: return four ? paged_simt<T, 128, 4>(p, st) : paged_simt<T, 128, 8>(p, st);
+        case 32: return four ? paged_simt<T, C, 32, 4>(p, st) : paged_simt<T, C, 32, 8>(p, st);
+        case 64: return four ? paged_simt<T, C, 64, 4>(p, st) : paged_simt<T, C, 64, 8>(p, st);
+        case 128: return four ? paged_simt<T, C, 128, 4>(p, st) : paged_simt<T, C, 128, 8>(p, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -471,6 +497,14 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
                         : launch_join<__nv_bfloat16, 64, kTileTc, 32>(pt, grid, st);
     return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16>(pt, grid, st)
                     : launch_join<__nv_bfloat16, 128, kTileTc, 32>(pt, grid, st);
+}
+
+size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
+    return paged_decode_workspace_bytes(N, max_tokens, Hq, Hkv, d);
+}
+
+cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
+    return bf16 ? paged_dispatch<__nv_bfloat16, __nv_fp8_e4m3>(p, d, st) : paged_dispatch<float, __nv_fp8_e4m3>(p, d, st);
 }
 
 }  // namespace kda

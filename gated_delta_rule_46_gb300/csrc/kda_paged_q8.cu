@@ -1,0 +1,278 @@
+// kda_paged_q8.cu -- new tokens into a paged key-value cache in 8 bits.
+//
+// A block of B tokens of one head has a scale s and e4m3 codes c; a value is c s.
+// Scales are powers of two, the least with amax <= 448 s: the codes have four
+// significant bits whatever s is, so nothing is lost by it but the chance of a
+// finer last step below 2^-6 s, and every product and quotient with s is exact:
+// a code is the value rounded once, and codes whose scale doubles stay as they
+// are in value unless they fall below 2^-6 of the new one.
+//
+// A block that holds earlier tokens keeps its scale unless the new ones need a
+// larger one; then its earlier codes are rounded again, to the new scale.
+#include "kda_layers.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int WARPS = 8, ROWS = 16;               // of a CTA; tokens of a block that one warp works on
+
+// The least power of two s with a <= 448 s (448 = 1.75 2^8), and 2^-126 at least: both s and 1 / s are normal.
+__device__ __forceinline__ float scale_for(float a) {
+    const int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;       // biased exponent
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+constexpr float kLeast = 0x1p-126f, kMost = 0x1p126f;                      // scales that an earlier call can have left
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }   // of 2^e
+
+// Eight values of a row as they are loaded.
+template <typename T, bool VEC>
+struct Row8 {
+    uint4 u[sizeof(T) / 2] = {};
+    __device__ void load(const T *p) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+        } else if constexpr (sizeof(T) == 4) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+            u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+            u[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+    }
+    __device__ void get(float (&x)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (a saturating conversion takes infinities for large numbers)
+        const float a = fabsf(x[2 * i]) < INFINITY ? x[2 * i] * inv : NAN;
+        const float b = fabsf(x[2 * i + 1]) < INFINITY ? x[2 * i + 1] * inv : NAN;
+        c[i] = f2_to_e4m3x2(a, b);
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+__device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
+    const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = e4m3x2_to_f2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+// Tokens and blocks of sequence i; what is malformed has none.
+struct Seq {
+    int t0, start, n, blocks;
+};
+__device__ __forceinline__ Seq sequence(const AppendQ8Params &p, int i) {
+    Seq s{i, p.start[i], 1, 0};
+    bool bad = s.start < 0;
+    if (p.cu_seqlens) {
+        s.t0 = p.cu_seqlens[i];
+        const int end = p.cu_seqlens[i + 1];
+        s.n = end - s.t0;
+        bad = bad || s.t0 < 0 || end < s.t0 || end > p.total;
+    }
+    // (positions past 2^31 are past any table)
+    if (bad || (int64_t)s.start + s.n > 0x7fffffff) s.n = bad ? 0 : 0x7fffffff - s.start;
+    if (s.n > 0) s.blocks = ((s.start + s.n - 1) >> p.block_shift) - (s.start >> p.block_shift) + 1;
+    return s;
+}
+
+// One unit is a block of a sequence, a head, and keys or values; the units of all sequences in order are dealt out evenly.
+// B / 16 warps share a unit, 16 tokens each.
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const AppendQ8Params p) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = ROWS / RPS;        // lanes per row, rows per step, steps
+    __shared__ int64_t s_sum[WARPS + 1];
+    __shared__ int s_n;
+    __shared__ float s_max[2][WARPS];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tasks = 2 * p.Hkv, share = (1 << p.block_shift) / ROWS;     // warps of a unit
+    const int per = WARPS / share, mine = warp / share, part = warp % share;
+
+    // ---- this CTA's units [u0, u1), the sequence in which they start and the blocks before it
+    int64_t total = p.num_seqs, cum = 0;
+    int n = 0;
+    if (p.cu_seqlens) {
+        const int each = (p.num_seqs + WARPS * 32 - 1) / (WARPS * 32);
+        const int n0 = min(p.num_seqs, tid * each), n1 = min(p.num_seqs, n0 + each);
+        int64_t x = 0;
+        for (int i = n0; i < n1; ++i) x += sequence(p, i).blocks;
+        const int64_t own = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_sum[warp] = x;
+        if (tid == 0) s_n = p.num_seqs;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+        for (int i = 0; i < WARPS; ++i) {
+            if (i < warp) before += s_sum[i];
+            total += s_sum[i];
+        }
+        const int64_t b0 = (int64_t)blockIdx.x * (total * tasks) / gridDim.x / tasks;
+        int64_t c = before + x - own;
+        if (b0 >= c && b0 < c + own)
+            for (int i = n0; i < n1; ++i) {
+                const int b = sequence(p, i).blocks;
+                if (b0 < c + b) {
+                    s_n = i;
+                    s_sum[WARPS] = c;
+                    break;
+                }
+                c += b;
+            }
+        __syncthreads();
+        n = s_n;
+        cum = s_sum[WARPS];
+        if (blockIdx.x == 0) {
+            for (int i = tid; i < p.num_seqs; i += WARPS * 32) {
+                const int t0 = p.cu_seqlens[i], end = p.cu_seqlens[i + 1];
+                if (p.start[i] < 0 || t0 < 0 || end < t0 || end > p.total || (int64_t)p.start[i] + (end - t0) > 0x7fffffff)
+                    report_status(p.status, KDA_ERR_INVALID_ARG);
+            }
+            if (tid == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.num_seqs] != p.total))
+                report_status(p.status, KDA_ERR_INVALID_ARG);
+        }
+    }
+    const int64_t units = total * tasks;
+    const int64_t u0 = (int64_t)blockIdx.x * units / gridDim.x, u1 = (int64_t)(blockIdx.x + 1) * units / gridDim.x;
+    if (u0 >= u1) return;
+    int64_t blk = (u0 + mine) / tasks;                // block of all sequences, and the unit within it
+    int task = (int)(u0 + mine - blk * tasks);
+    if (!p.cu_seqlens) n = (int)blk, cum = blk;
+    Seq s{};
+    if (blk < total) s = sequence(p, n);
+    if (!p.cu_seqlens) s.blocks = 1;                  // (of a malformed one too: a sequence is its own block here)
+
+    const int row0 = part * ROWS + lane / LPR, ch = (lane % LPR) * 8;     // first row of the block, first channel
+    const T *in[2] = {static_cast<const T *>(p.k), static_cast<const T *>(p.v)};
+    const int ps = 1 << p.page_shift;
+    for (int64_t u = u0, round = 0; u < u1; u += per, ++round) {
+        // ---- the block: rows [from, to) of it are new, [0, from) hold earlier tokens
+        int from = 0, to = 0;
+        int64_t at = 0;                               // its first row in the cache
+        float was = 0.f;
+        const bool v = task >= p.Hkv;
+        const int h = v ? task - p.Hkv : task;
+        Row8<T, VEC> x[STEPS];
+        if (u + mine < u1) {
+            while (blk >= cum + s.blocks) {
+                cum += s.blocks;
+                s = sequence(p, ++n);
+                if (!p.cu_seqlens) s.blocks = 1;
+            }
+            const int pos = ((s.start >> p.block_shift) + (int)(blk - cum)) << p.block_shift;
+            const int page_i = pos >> p.page_shift;
+            const int page = s.n > 0 && page_i < p.max_pages ? p.table[(int64_t)n * p.max_pages + page_i] : -1;
+            if (page >= 0 && page < p.num_pages) {
+                from = max(s.start - pos, 0);
+                to = min(1 << p.block_shift, s.start + s.n - pos);
+                at = (((int64_t)page * p.Hkv + h) << p.page_shift) + (pos & (ps - 1));
+                if (from > 0) was = (v ? p.vs : p.ks)[at >> p.block_shift];
+                const T *src = in[v] + ((int64_t)s.t0 + pos - s.start) * (v ? p.ldv : p.ldk) + (int64_t)h * D + ch;
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int r = row0 + i * RPS;
+                    if (r >= from && r < to) x[i].load(src + r * (v ? p.ldv : p.ldk));
+                }
+            } else if (lane == 0 && part == 0) {
+                report_status(p.status, KDA_ERR_INVALID_ARG);
+            }
+        }
+        // ---- its largest finite value, and the scale
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            float f[8];
+            x[i].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]) < INFINITY ? fabsf(f[e]) : 0.f);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (share > 1) {
+            if (lane == 0) s_max[round & 1][warp] = amax;
+            __syncthreads();
+            for (int i = 0; i < share; ++i) amax = fmaxf(amax, s_max[round & 1][mine * share + i]);
+        } else {
+            __syncwarp();                             // (every lane has read the scale that one writes)
+        }
+        if (from < to) {
+            float scale = scale_for(amax);
+            bool again = false;                       // earlier codes are rounded to a new scale
+            if (from > 0) {
+                if (was >= kLeast && was <= kMost) {
+                    scale = fmaxf(scale, __uint_as_float((__float_as_uint(was) + 0x7fffffu) & 0xff800000u));
+                    again = scale != was;
+                } else if (lane == 0 && part == 0) {
+                    report_status(p.status, KDA_ERR_INVALID_ARG);
+                }
+            }
+            uint8_t *dst = (v ? p.vc : p.kc) + at * D + ch;
+            const float inv = inverse(scale);
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int r = row0 + i * RPS;
+                float f[8];
+                if (r >= from && r < to) {
+                    x[i].get(f);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8(f, inv);
+                } else if (again && r < from) {
+                    decode8(*reinterpret_cast<const uint2 *>(dst + r * D), f);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8(f, was * inv);
+                }
+            }
+            if (lane == 0 && part == 0) (v ? p.vs : p.ks)[at >> p.block_shift] = scale;
+        }
+        for (task += per; task >= tasks; task -= tasks) ++blk;
+    }
+}
+
+template <typename T, int D, bool VEC>
+cudaError_t launch(const AppendQ8Params &p, cudaStream_t st) {
+    const int B = 1 << p.block_shift, per = WARPS / (B / ROWS);
+    // at most two blocks of a sequence are not whole
+    const int64_t blocks = p.cu_seqlens ? p.total / B + 2 * (int64_t)min((int64_t)p.num_seqs, p.total) : p.num_seqs;
+    const int64_t most = (blocks * 2 * p.Hkv + per - 1) / per, room = (int64_t)sm_count() * 4;
+    return launch_dependent(paged_append_q8_kernel<T, D, VEC>, dim3((unsigned)(most < room ? most : room)), WARPS * 32, 0, st, 1,
+                            p);
+}
+template <typename T, bool VEC>
+cudaError_t launch_d(const AppendQ8Params &p, int d, cudaStream_t st) {
+    return d == 32 ? launch<T, 32, VEC>(p, st) : d == 64 ? launch<T, 64, VEC>(p, st) : launch<T, 128, VEC>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, int d, bool bf16, bool vec16, cudaStream_t st) {
+    if (bf16) return vec16 ? launch_d<__nv_bfloat16, true>(p, d, st) : launch_d<__nv_bfloat16, false>(p, d, st);
+    return vec16 ? launch_d<float, true>(p, d, st) : launch_d<float, false>(p, d, st);
+}
+
+}  // namespace kda

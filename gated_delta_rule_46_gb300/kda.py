@@ -16,7 +16,7 @@ import torch
 
 from . import build as _build
 
-KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT = range(5)
+KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT, KDA_ERR_NO_PAGES = range(6)
 KDA_F32, KDA_BF16 = 0, 1
 # kernels of the tensor-core prefill, as named by include/kda_testing.h
 KDA_TESTING_FUSED, KDA_TESTING_INTRA, KDA_TESTING_SEGMENT, KDA_TESTING_SCAN, KDA_TESTING_STATE = (

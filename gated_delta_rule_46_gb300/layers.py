@@ -30,6 +30,15 @@ _SIGNATURES = {
     "kda_paged_append": (_I, [_P, _L, _P, _L, _P, _P, _I, _I, _P, _I, _P, _P, _I, _L, _I, _I, _I, _P, _P]),
     "kda_paged_decode_workspace_size": (_Z, [_I, _L, _I, _I, _I, _I]),
     "kda_paged_decode": (_I, [_P, _L, _P, _P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _Z, _P, _P]),
+    "kda_paged_append_q8": (_I, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I, _L, _I, _I, _I, _P, _P]),
+    "kda_paged_decode_q8_workspace_size": (_Z, [_I, _L, _I, _I, _I, _I]),
+    "kda_paged_decode_q8": (_I, [_P, _L, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _Z, _P, _P]),
+    "kda_pages_resize_workspace_size": (_Z, [_I, _I, _I]),
+    "kda_pages_resize": (_I, [_P, _I, _I, _P, _P, _I, _P, _I, _P, _Z, _P, _P]),
+    "kda_pages_fork_workspace_size": (_Z, [_I, _I, _I]),
+    "kda_pages_fork": (_I, [_P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P, _P, _I, _I, _P, _Z, _P, _P]),
+    "kda_pages_compact_workspace_size": (_Z, [_I]),
+    "kda_pages_compact": (_I, [_P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _Z, _P, _P]),
 }
 _fns: dict = {}
 # torch's current stream of a device as an integer, without building a Stream object
@@ -305,4 +314,75 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
           size, _status(status, dev))
     if stream is not None:
         _record(stream, q, k_cache, v_cache, page_table, seq_lens, out, lse, workspace, status)
+    return (out, lse) if return_lse else out
+
+
+def _cache_q8(k_cache, v_cache, k_scale, v_scale, H, d, dev):
+    """The shapes and pointers of a cache in 8 bits: pages, page size, block, and four pointers."""
+    P, _, ps, _ = _dims(k_cache, "k_cache", 4)
+    kp = _dense(k_cache, "k_cache", (P, H, ps, d), torch.float8_e4m3fn, dev)
+    vp = _dense(v_cache, "v_cache", (P, H, ps, d), torch.float8_e4m3fn, dev)
+    blocks = _dims(k_scale, "k_scale", 3)[2]
+    if blocks == 0 or ps % blocks:
+        raise ValueError(f"k_scale has {blocks} blocks for pages of {ps} tokens")
+    return (P, ps, ps // blocks, kp, vp, _dense(k_scale, "k_scale", (P, H, blocks), torch.float32, dev),
+            _dense(v_scale, "v_scale", (P, H, blocks), torch.float32, dev))
+
+
+def paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start_pos, cu_seqlens=None, status=None,
+                    stream=None):
+    """paged_append into a cache in 8 bits: k_cache, v_cache [P, Hkv, page_size, d] e4m3, k_scale, v_scale [P, Hkv,
+    page_size / block] f32 with a power of two for each block of 16, 32, 64 or 128 tokens (a value is its code times
+    its block's scale).  A partly filled block's scale grows where new tokens need it, and its codes follow."""
+    dev = _cuda(k, "k")
+    dt = k.dtype
+    code = _code(dt, "k")
+    T, H, d = _dims(k, "k", 3)
+    ldk = _rows(k, "k", (T, H, d), H * d, dt, dev)
+    ldv = _rows(v, "v", (T, H, d), H * d, dt, dev)
+    P, ps, block, kp, vp, ksp, vsp = _cache_q8(k_cache, v_cache, k_scale, v_scale, H, d, dev)
+    N, cols = _dims(page_table, "page_table", 2)
+    tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
+    _call("kda_paged_append_q8", dev, stream, (), k.data_ptr(), ldk, v.data_ptr(), ldv, kp, vp, ksp, vsp, P, ps, block, tp,
+          cols, _dense(start_pos, "start_pos", (N,), torch.int32, dev),
+          _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, d, code, _status(status, dev))
+    if stream is not None:
+        _record(stream, k, v, k_cache, v_cache, k_scale, v_scale, page_table, start_pos, cu_seqlens, status)
+
+
+def paged_decode_q8_workspace_size(num_seqs, max_tokens, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of paged_decode_q8 for tables of max_tokens = max_pages * page_size tokens."""
+    return int(_fn("kda_paged_decode_q8_workspace_size")(num_seqs, max_tokens, Hq, Hkv, d, _code(dtype, "dtype")))
+
+
+def paged_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, scale=None, out=None, lse=None,
+                    return_lse=False, workspace=None, status=None, stream=None):
+    """paged_decode over a cache in 8 bits (as for paged_append_q8).  q [N, Hq, d] bf16 or f32, as out."""
+    dev = _cuda(q, "q")
+    dt = q.dtype
+    code = _code(dt, "q")
+    N, Hq, d = _dims(q, "q", 3)
+    ldq = _rows(q, "q", (N, Hq, d), Hq * d, dt, dev)
+    Hkv = _dims(k_cache, "k_cache", 4)[1]
+    P, ps, block, kp, vp, ksp, vsp = _cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    cols = _dims(page_table, "page_table", 2)[1]
+    tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
+    new = []
+    if out is None:
+        out = _empty(stream, (N, Hq, d), dt, dev)
+        new.append(out)
+    if lse is None and return_lse:
+        lse = _empty(stream, (N, Hq), torch.float32, dev)
+        new.append(lse)
+    if workspace is None:
+        size = _size("kda_paged_decode_q8_workspace_size", dev, N, cols * ps, Hq, Hkv, d, code)
+        workspace = _empty(stream, size, torch.uint8, dev)
+    size = _dims(workspace, "workspace", 1)[0]
+    _call("kda_paged_decode_q8", dev, stream, new, q.data_ptr(), ldq, kp, vp, ksp, vsp, P, ps, block, tp, cols,
+          _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
+          d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),
+          _dense(lse, "lse", (N, Hq), torch.float32, dev), _dense(workspace, "workspace", (size,), torch.uint8, dev),
+          size, _status(status, dev))
+    if stream is not None:
+        _record(stream, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, lse, workspace, status)
     return (out, lse) if return_lse else out

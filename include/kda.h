@@ -53,7 +53,8 @@ typedef enum {
     KDA_ERR_INVALID_ARG = 1,    /* null pointer, negative size, misaligned buffer */
     KDA_ERR_UNSUPPORTED = 2,    /* valid but unsupported shape or dtype */
     KDA_ERR_CUDA = 3,           /* a CUDA runtime/driver call or launch failed */
-    KDA_ERR_DEVICE_TIMEOUT = 4  /* a device-side bounded wait expired */
+    KDA_ERR_DEVICE_TIMEOUT = 4, /* a device-side bounded wait expired */
+    KDA_ERR_NO_PAGES = 5        /* found on the device: a cache has no free page left (kda_pages.h) */
 } kda_status_t;
 
 typedef enum {

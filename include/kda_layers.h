@@ -9,6 +9,9 @@
  *     decay decode    the same for one new token per sequence
  *     paged append    keys and values of new tokens into the pages of a cache
  *     paged decode    softmax attention of one new token over that cache
+ *     append q8, decode q8    the same with the cache in 8 bits
+ *
+ * (kda_pages.h hands the cache's pages out.)
  *
  * The conventions of kda.h hold: device pointers owned by the caller, calls
  * asynchronous on `stream`, argument errors found on the host before anything
@@ -176,6 +179,52 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
                               int d, kda_dtype_t dtype, float scale, void *out, float *lse,
                               void *workspace, size_t workspace_bytes, uint32_t *status,
                               kda_stream_t stream);
+
+/*
+ * kda_paged_append_q8 -- kda_paged_append into a cache in 8 bits: e4m3 codes with a
+ * scale for each block of `block` tokens of one head; a value is its code times
+ * its block's scale.
+ *   k_cache, v_cache  [num_pages, Hkv, page_size, d] e4m3 (no infinities, largest 448),
+ *                     16-byte aligned
+ *   k_scale, v_scale  [num_pages, Hkv, page_size / block] float32
+ *   block             16, 32, 64 or 128, at most page_size
+ * and the rest as for kda_paged_append (k and v are of dtype).  The scale of a
+ * block is the least power of two s, of 2^-126 at least, with |x| <= 448 s for its
+ * tokens' finite values x; a code is x / s rounded once, to four significant bits
+ * (2^-4 of the value at most, or 2^-10 s below 2^-6 s).  Infinities become NaN.
+ * A block with tokens from before the call, at positions below start_pos, keeps
+ * its scale unless the new tokens need a larger one; then the earlier codes are
+ * rounded again, to the new scale (which changes those below 2^-6 of it alone, by
+ * 2^-10 of it at most).  Such a block's scale has to be one that a call left, or
+ * any other from 2^-126 to 2^126, which is rounded up to a power of two; another is
+ * recorded in *status and the block's scale taken from the new tokens alone.  A
+ * block that starts at or behind start_pos is begun afresh, whatever it holds.
+ * What lies in a block behind the new tokens is left.
+ */
+kda_status_t kda_paged_append_q8(const void *k, int64_t ldk, const void *v, int64_t ldv, void *k_cache,
+                                 void *v_cache, float *k_scale, float *v_scale, int num_pages,
+                                 int page_size, int block, const int32_t *page_table, int max_pages,
+                                 const int32_t *start_pos, const int32_t *cu_seqlens, int num_seqs,
+                                 int64_t total_tokens, int Hkv, int d, kda_dtype_t dtype,
+                                 uint32_t *status, kda_stream_t stream);
+
+/* Workspace of kda_paged_decode_q8, as kda_paged_decode_workspace_size. */
+size_t kda_paged_decode_q8_workspace_size(int num_seqs, int64_t max_tokens, int Hq, int Hkv, int d,
+                                          kda_dtype_t dtype);
+
+/*
+ * kda_paged_decode_q8 -- kda_paged_decode over a cache in 8 bits (q and out are of
+ * dtype, the cache as for kda_paged_append_q8, with any finite scales):
+ *     s_t = scale k_scale_t (q . k_t),   out = sum_t softmax(s)_t v_scale_t v_t
+ * Scores, maxima and sums are float32.
+ */
+kda_status_t kda_paged_decode_q8(const void *q, int64_t ldq, const void *k_cache, const void *v_cache,
+                                 const float *k_scale, const float *v_scale, int num_pages,
+                                 int page_size, int block, const int32_t *page_table, int max_pages,
+                                 const int32_t *seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                                 kda_dtype_t dtype, float scale, void *out, float *lse,
+                                 void *workspace, size_t workspace_bytes, uint32_t *status,
+                                 kda_stream_t stream);
 
 #ifdef __cplusplus
 }
