@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libkda_gb300.so")
 SOURCES = ["kda_api.cu", "kda_simt.cu", "kda_prefill_tc.cu", "kda_noalloc.cu", "kda_decode_pool.cu",
            "kda_compose.cu", "kda_chunk_simt.cu", "kda_prefill_c32.cu", "kda_layers_api.cu",
            "kda_linear.cu", "kda_decay.cu", "kda_decay_tc.cu", "kda_paged.cu", "kda_paged_tc.cu",
-           "kda_paged_q8.cu", "kda_pages.cu"]
+           "kda_paged_q8.cu", "kda_paged_q8_tc.cu", "kda_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

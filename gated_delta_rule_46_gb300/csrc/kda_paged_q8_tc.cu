@@ -1,0 +1,531 @@
+// kda_paged_q8_tc.cu -- attention of one token per sequence over a paged cache in
+// 8 bits on the tensor cores (bf16 queries and outputs).
+//
+// As in kda_paged_tc.cu the cached tokens are the M side of both products, so that
+// the codes go from HBM to the MMAs without passing through registers:
+//   S^T [128 tokens x N] = K Q^T,    O^T [d x N] = V^T P^T
+// on e4m3 operands.  K and V are e4m3 as they lie in the cache.  Q and the weights P,
+// which need more than e4m3's four significant bits, take two columns each:
+//   x = hi + lo,   hi = e4m3(x),   lo = e4m3(x - hi)      (lo scaled by a power of two)
+// which is exact for a bf16 query down to 2^-21 of its head's largest channel, and
+// keeps eight bits of a weight, as bf16 would.  The products of the two parts are
+// added in float32.  N = 2 HB for HB heads; with up to 8 of them, 16, the least there is.
+//
+// A token's scale of K multiplies its row of S^T.  Its scale of V goes into its
+// weight: with the tile's largest score m and largest scale of V u,
+//   P = 256 e^{s - m} v_scale / u,   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
+// so that the weights use e4m3's range from the tile's own maximum on (an error below
+// 2^-23 of that, whatever the rest of the row holds), and tiles do not wait for each
+// other's maxima: two groups of softmax warps work on tiles in turn.
+//
+// Roles of the 16 warps: 0 loads (pages by TMA, scales by 4-byte copies), 1 issues
+// the S^T MMAs, 2 zeroes rows of V that hold no token and issues the O^T MMAs, 3 splits
+// and stages Q, 4-7 and 8-11 run the softmax of even and odd tiles (thread = token),
+// 12-15 keep the running output (thread = channel) in float32 registers.
+#include <cuda.h>
+
+#include "kda_paged_tc.cuh"
+#include "kda_tmap.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+using namespace paged;
+
+constexpr int NSMAX = 12;                         // stages of the K and of the V ring, at most
+constexpr int SB = 4, RING = 16;                  // S^T buffers; tiles whose scales and page masks are kept
+constexpr int QRING = 8;                          // items whose queries' factors are kept
+// A page mask or scales of tile t are read before O^T of tile t is issued, which V's stage of tile t + NS waits for, and
+// are written again for tile t + RING > t + NS.  An item's factors are read before the S^T buffer of its last tile of either
+// parity is given back, which tile t + SB waits for: long before the eighth item after it.
+static_assert(RING > NSMAX + 1 && QRING >= SB + 4, "rings");
+
+enum Bar { KFULL, KFREE = KFULL + NSMAX, VFULL = KFREE + NSMAX, VFREE = VFULL + NSMAX, SCALES = VFREE + NSMAX, SD = SCALES + RING,
+           SFREE = SD + SB, PREADY = SFREE + SB, PVD = PREADY + 2, OFREE = PVD + 2, QFULL = OFREE + 2, QFREE = QFULL + 2,
+           IREADY = QFREE + 2, IFREE = IREADY + 2, NBAR = IFREE + 2 };
+
+template <int D, int HB>
+struct Lay {
+    static constexpr int N = 2 * HB;
+    static constexpr uint32_t tile = TILE * D;
+    // about 190 KB of stages where there is room for as much
+    static constexpr int NS = D == 128 ? (HB == 32 ? 5 : 6) : D == 64 && HB == 32 ? 10 : NSMAX;
+    // (V first: with d < 128 the MMA's rows past d read what lies behind a stage, which no one looks at)
+    static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_bytes = N * D;
+    static constexpr uint32_t P = (Q + 2 * q_bytes + 1023) / 1024 * 1024, p_bytes = N * TILE;
+    static constexpr uint32_t SC = P + 2 * p_bytes;                  // float: scales of K [RING][8], of V [RING][8]
+    static constexpr uint32_t QS = SC + 2 * RING * 8 * 4;            // factors of the queries [QRING][HB]
+    static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [2][HB], u / 256 [2] (padded to 4)
+    static constexpr uint32_t RED = M + 2 * HB * 4 + 16;             // maxima of the warps [2][2][4][HB]
+    static constexpr uint32_t SUM = RED + 16 * HB * 4;               // sums of the item [2][8][HB], maxima [2][2][HB]
+    static constexpr uint32_t bytes = SUM + 20 * HB * 4;
+    static constexpr uint32_t cols = HB == 8 ? 128 : HB == 16 ? 256 : 512;   // TMEM: SB + 2 buffers of N columns
+};
+
+// Byte offset of the 16-byte chunk of a row, swizzled as TMA does it.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
+    return (uint32_t)(row * D + ((chunk ^ (D == 128 ? row & 7 : D == 64 ? row >> 1 & 3 : row >> 2 & 1)) << 4));
+}
+
+// 2^e with a <= 448 2^e, and its inverse; at least 2^-126.
+__device__ __forceinline__ float power_for(float a) {
+    const int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+
+// Columns [c, c + 8) and [HB + c, HB + c + 8) of a buffer, for the caller to wait for.
+template <int HB>
+__device__ __forceinline__ void load_parts(uint32_t addr, int c, float (&hi)[8], float (&lo)[8]) {
+    ptx::tmem_ld8(addr + c, hi);
+    ptx::tmem_ld8(addr + HB + c, lo);
+}
+
+template <int D, int HB>
+__global__ void __launch_bounds__(512, 1)
+    paged_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedParams p) {
+    using L = Lay<D, HB>;
+    constexpr int NS = L::NS;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar[NBAR];
+    __shared__ int64_t s_sum[257];
+    __shared__ int s_n;
+    __shared__ uint32_t s_tmem, s_abort, s_mask[RING];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = ptx::smem_addr(sm);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
+
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
+    const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    empty_sequences<__nv_bfloat16, TILE>(p, D);
+    if ((int)blockIdx.x >= sp.g) return;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NBAR; ++i) {
+            int count = 1;
+            if (i >= SCALES && i < SD) count = 32;
+            else if (i >= IREADY && i < IFREE) count = 8;
+            else if ((i >= SFREE && i < PVD) || (i >= OFREE && i < QFULL) || i >= IFREE) count = 4;
+            ptx::mbar_init(&bar[i], count);
+        }
+        ptx::fence_mbar_init();
+        s_abort = 0;
+        ptx::prefetch_tensormap(&mk);
+        ptx::prefetch_tensormap(&mv);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&s_tmem, L::cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    auto tm_s = [&](int b) { return tmem + b * L::N; };
+    auto tm_o = [&](int b) { return tmem + (SB + b) * L::N; };
+    Walk wk;
+    wk.start(p, sp, items);
+    const int rows = min(TILE, 1 << p.page_shift);        // tokens of a tile that one page holds
+    const int pieces = TILE / rows, rows_shift = 31 - __clz(rows);
+    float *const sc = reinterpret_cast<float *>(sm + L::SC), *const qs = reinterpret_cast<float *>(sm + L::QS),
+                 *const sm_m = reinterpret_cast<float *>(sm + L::M), *const sums = reinterpret_cast<float *>(sm + L::SUM);
+    bool ok = true;
+
+    if (warp == 0) {                                              // ---- loads: lane = page of the tile
+        // a tile's page is looked up while the tile before it is loaded
+        int64_t i = wk.tile, first = i, last = wk.last();
+        auto lookup = [&](int at) {
+            return lane < pieces && at < wk.len ? p.table[(int64_t)wk.n * p.max_pages + (at >> p.page_shift)] : 0;
+        };
+        const int per = 1 << (p.page_shift - p.block_shift);      // scales of a page and head
+        int told = -1, at = (int)(i * TILE) + lane * rows, id = lookup(at);     // at: this page's first token of the tile
+        for (int t = 0; ok && wk.more(); ++t) {
+            if (wk.n != told) {
+                told = wk.n;
+                if (lane == 0 && wk.raw != wk.len) report_status(p.status, KDA_ERR_INVALID_ARG);
+            }
+            const int kvh = wk.item / nb, at0 = at;
+            int page = -1;
+            if (lane < pieces && at < wk.len) {
+                if (id >= 0 && id < p.num_pages) page = id;
+                else report_status(p.status, KDA_ERR_INVALID_ARG);
+            }
+            // scales: lanes 0-7 those of K, 8-15 those of V, of the block of tokens that starts at `from`
+            const int from = (int)(i * TILE) + ((lane & 7) << p.block_shift), off = (lane & 7) << p.block_shift;
+            const int of = __shfl_sync(0xffffffffu, page, (off >> rows_shift) & 31);
+            const bool block = lane < 16 && off < TILE && from < wk.len && of >= 0;
+            if (++i == last) {
+                wk.next_item(p, last - first);
+                if (wk.more()) { first = i = wk.tile; last = wk.last(); }
+            }
+            at = (int)(i * TILE) + lane * rows;
+            id = wk.more() ? lookup(at) : 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+            const uint32_t bytes = (uint32_t)__popc(mask) * rows * D;
+            const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at0 & ((1 << p.page_shift) - 1)));
+            const int s = t % NS, r = t % RING;
+            for (int kv = 0; kv < 2; ++kv) {
+                uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
+                if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
+                uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * D;
+                if (lane == 0) {
+                    if (kv == 0) s_mask[r] = mask;
+                    ptx::mbar_arrive_expect_tx(full, bytes);
+                }
+                __syncwarp();
+                if (page >= 0) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
+                if (kv == 0) {
+                    const float *src = lane < 8 ? p.ks : p.vs;
+                    if (block)
+                        src += ((int64_t)of * p.Hkv + kvh) * per + ((from & ((1 << p.page_shift) - 1)) >> p.block_shift);
+                    if (lane < 16) ptx::cp_async4(sc + (lane >> 3) * RING * 8 + r * 8 + (lane & 7), src, block);
+                    ptx::cp_async_arrive(&bar[SCALES + r]);
+                }
+            }
+        }
+    } else if (warp == 1) {                                       // ---- S^T
+        if (ptx::elect_one()) {
+            int item_no = 0;
+            constexpr uint32_t id_s = ptx::idesc_e4m3_f32(128, L::N, false);
+            if (p.expire && blockIdx.x == 0) ok = ptx::mbar_wait(&bar[PVD], 0, kTestWait);
+            for (int t = 0; ok && wk.more();) {
+                const int64_t first = wk.tile, last = wk.last();
+                const int ib = item_no & 1;
+                ok = ptx::mbar_wait(&bar[QFULL + ib], (item_no >> 1) & 1, kWaitBudget);
+                const uint64_t q = ptx::sdesc_rows<D>(base + L::Q + ib * L::q_bytes);
+                for (int64_t i = first; i < last && ok; ++i, ++t) {
+                    const int s = t % NS, b = t % SB;
+                    ok = ptx::mbar_wait(&bar[KFULL + s], (t / NS) & 1, kWaitBudget) &&
+                         (t < SB || ptx::mbar_wait(&bar[SFREE + b], (t / SB - 1) & 1, kWaitBudget));
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t k = ptx::sdesc_rows<D>(base + L::K + s * L::tile);
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) ptx::mma_f8_ss(tm_s(b), k + j * 2, q + j * 2, id_s, j > 0);
+                    ptx::mma_commit(&bar[SD + b]);
+                    ptx::mma_commit(&bar[KFREE + s]);
+                }
+                ptx::mma_commit(&bar[QFREE + ib]);
+                ++item_no;
+                wk.next_item(p, last - first);
+            }
+        }
+    } else if (warp == 2) {                                       // ---- rows of V without a token, O^T
+        constexpr uint32_t id_o = ptx::idesc_e4m3_f32(128, L::N, true);
+        for (int t = 0; ok && wk.more();) {
+            const int len = wk.len;
+            const int64_t first = wk.tile, last = wk.last();
+            for (int64_t i = first; i < last; ++i, ++t) {
+                const int s = t % NS, b = t & 1;
+                ok = warp_wait(&bar[VFULL + s], t / NS);
+                if (!ok) break;
+                const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[t % RING]);
+                const int left = len - (int)(i * TILE);
+                if (left < TILE || __popc(mask) < pieces) {
+                    // (a weight of 0 does not silence a NaN) 16 bytes a lane and step, whole rows
+                    const int from = __popc(mask) < pieces ? 0 : min(max(left, 0), TILE);
+                    for (int j = from * (D / 16) + lane; j < TILE * (D / 16); j += 32) {
+                        const int r = j / (D / 16);
+                        if (r < left && (mask >> (r >> rows_shift) & 1)) continue;
+                        *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + j * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    ptx::fence_async_smem();
+                    __syncwarp();
+                }
+                ok = warp_wait(&bar[PREADY + b], t >> 1);         // (which says that O^T's buffer is free too)
+                if (!ok) break;
+                if (ptx::elect_one()) {
+                    ptx::tc_fence_after_sync();
+                    const uint64_t v = ptx::sdesc_rows<D>(base + L::V + s * L::tile, L::tile);
+                    const uint64_t w = ptx::sdesc_rows<128>(base + L::P + b * L::p_bytes);
+#pragma unroll
+                    for (int j = 0; j < TILE / 32; ++j) ptx::mma_f8_ss(tm_o(b), v + j * (32 * D >> 4), w + j * 2, id_o, j > 0);
+                    ptx::mma_commit(&bar[PVD + b]);
+                    ptx::mma_commit(&bar[VFREE + s]);
+                }
+                __syncwarp();
+            }
+            wk.next_item(p, last - first);
+        }
+    } else if (warp == 3) {                                       // ---- Q
+        int item_no = 0;
+        const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
+        constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = HB / RPS < 1 ? 1 : HB / RPS;     // lanes per head, heads at a time
+        const int c = lane % LPR;
+        while (ok && wk.more()) {
+            const int64_t first = wk.tile, last = wk.last();
+            const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
+            uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
+            const __nv_bfloat16 *q =
+                static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
+            uint4 u[STEPS];
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int h = i * RPS + lane / LPR;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (h < hb) {
+                    if (q16) u[i] = *reinterpret_cast<const uint4 *>(q + h * D + c * 8);
+                    else u[i] = load8(q + h * D + c * 8);
+                }
+            }
+            if (item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int h = i * RPS + lane / LPR;
+                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                float x[8], a = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+                    a = fmaxf(a, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
+                }
+#pragma unroll
+                for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const float f = power_for(a), inv = __uint_as_float((254u << 23) - __float_as_uint(f));
+                uint32_t hi[2] = {}, lo[2] = {};
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    // (a saturating conversion takes infinities for large numbers)
+                    const float y0 = fabsf(x[e]) < INFINITY ? x[e] * inv : NAN, y1 = fabsf(x[e + 1]) < INFINITY ? x[e + 1] * inv : NAN;
+                    const uint16_t ch = f2_to_e4m3x2(y0, y1);
+                    const float2 b = e4m3x2_to_f2(ch);
+                    hi[e >> 2] |= (uint32_t)ch << (8 * (e & 2));
+                    lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(16.f * (y0 - b.x), 16.f * (y1 - b.y)) << (8 * (e & 2));
+                }
+                if (h < HB) {
+                    *reinterpret_cast<uint2 *>(dst + swizzled<D>(h, c >> 1) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(dst + swizzled<D>(HB + h, c >> 1) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+                    if (c == 0) qs[(item_no % QRING) * HB + h] = f * (p.scale * kLog2E);
+                }
+            }
+            ptx::fence_async_smem();
+            warp_arrive(&bar[QFULL + (item_no & 1)]);
+            ++item_no;
+            wk.next_item(p, last - first);
+        }
+    } else if (warp < 12) {                                       // ---- softmax: thread = token of the tile
+        const int wg = (warp - 4) >> 2, q = warp & 3, j = q * 32 + lane;
+        int t = 0, item_no = 0;
+        while (ok && wk.more()) {
+            const int len = wk.len;
+            const int64_t first = wk.tile, last = wk.last();
+            float m[HB], l[HB];
+#pragma unroll
+            for (int h = 0; h < HB; ++h) { m[h] = -INFINITY; l[h] = 0.f; }
+            for (int64_t i = first; i < last; ++i, ++t) {
+                if ((t & 1) != wg) continue;
+                const int sb = t % SB, r = t % RING, turn = t >> 1;
+                float *red = reinterpret_cast<float *>(sm + L::RED) + (wg * 2 + (turn & 1)) * 4 * HB;
+                ok = warp_wait(&bar[SCALES + r], t / RING) && warp_wait(&bar[SD + sb], t / SB);
+                float s[HB], weight = 0.f, unit = 0.f;
+                if (ok) {
+                    ptx::tc_fence_after_sync();
+                    const bool in = (int)(i * TILE) + j < len &&
+                                    (*static_cast<volatile uint32_t *>(&s_mask[r]) >> (j >> rows_shift) & 1);
+                    const float fk = sc[r * 8 + (j >> p.block_shift)];
+                    // the tile's largest scale of V (2^-100 at least), and this token's share of it
+                    const float *fv = sc + RING * 8 + r * 8;
+                    float v[8];
+                    ld8(fv, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) unit = fmaxf(unit, e << p.block_shift < TILE ? fabsf(v[e]) : 0.f);
+                    unit = fmaxf(unit, 0x1p-100f);
+                    weight = in ? fv[j >> p.block_shift] * (256.f / unit) : 0.f;
+#pragma unroll
+                    for (int h = 0; h < HB; h += 8) {
+                        float hi[8], lo[8], f[8];
+                        load_parts<HB>(tm_s(sb) + ((uint32_t)q << 21), h, hi, lo);
+                        ld8(qs + (item_no % QRING) * HB + h, f);
+                        ptx::tmem_ld_wait(hi, lo);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) s[h + e] = hi[e] = in ? fmaf(lo[e], 0.0625f, hi[e]) * fk * f[e] : -INFINITY;
+                        const float mx = reduce_lanes(hi, lane, [](float x, float y) { return fmaxf(x, y); });
+                        if (lane % 4 == 0) red[q * HB + h + lane / 4] = mx;
+                    }
+                    ptx::tc_fence_before_sync();
+                    warp_arrive(&bar[SFREE + sb]);
+                    // the weights and maxima of two tiles ago have been used
+                    ok = t < 2 || warp_wait(&bar[OFREE + wg], turn - 1);
+                }
+                ok = !ptx::bar_any(1 + wg, 128, !ok);
+                if (!ok) break;
+                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (j & 15);
+#pragma unroll
+                for (int h = 0; h < HB; h += 4) {
+                    float mt[4], w[4];
+                    ld4(red + h, mt);
+#pragma unroll
+                    for (int x = 1; x < 4; ++x) {
+                        float o[4];
+                        ld4(red + x * HB + h, o);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mt[e] = fmaxf(mt[e], o[e]);
+                    }
+                    if (j == 0) *reinterpret_cast<float4 *>(sm_m + wg * HB + h) = make_float4(mt[0], mt[1], mt[2], mt[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float mn = fmaxf(m[h + e], mt[e]), mu = mn == -INFINITY ? 0.f : mn;
+                        const float own = ex2(s[h + e] - (mt[e] == -INFINITY ? 0.f : mt[e]));
+                        l[h + e] = fmaf(l[h + e], ex2(m[h + e] - mu), own * ex2(mt[e] - mu));
+                        m[h + e] = mn;
+                        w[e] = own * weight;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const uint16_t hi = f2_to_e4m3x2(w[e], w[e + 1]);
+                        const float2 b = e4m3x2_to_f2(hi);
+                        const uint16_t lo = f2_to_e4m3x2(32.f * (w[e] - b.x), 32.f * (w[e + 1] - b.y));
+                        w8[swizzled<128>(h + e, j >> 4)] = (uint8_t)hi;
+                        w8[swizzled<128>(h + e + 1, j >> 4)] = (uint8_t)(hi >> 8);
+                        w8[swizzled<128>(HB + h + e, j >> 4)] = (uint8_t)lo;
+                        w8[swizzled<128>(HB + h + e + 1, j >> 4)] = (uint8_t)(lo >> 8);
+                    }
+                }
+                if (j == 0) sm_m[2 * HB + wg] = unit * 0x1p-8f;
+                ptx::fence_async_smem();
+                ptx::tc_fence_before_sync();
+                warp_arrive(&bar[PREADY + wg]);
+            }
+            if (!ok) break;
+            const int ib = item_no & 1;
+            ok = item_no < 2 || warp_wait(&bar[IFREE + ib], (item_no >> 1) - 1);
+            ok = !ptx::bar_any(1 + wg, 128, !ok);
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < HB; h += 8) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = l[h + e];
+                const float sum = reduce_lanes(v, lane, [](float x, float y) { return x + y; });
+                if (lane % 4 == 0) sums[(ib * 8 + wg * 4 + q) * HB + h + lane / 4] = sum;
+            }
+            if (j == 0)
+#pragma unroll
+                for (int h = 0; h < HB; h += 4)
+                    *reinterpret_cast<float4 *>(sums + 16 * HB + (ib * 2 + wg) * HB + h) = make_float4(m[h], m[h + 1], m[h + 2], m[h + 3]);
+            warp_arrive(&bar[IREADY + ib]);
+            ++item_no;
+            wk.next_item(p, last - first);
+        }
+    } else {                                                      // ---- output: thread = channel
+        const int q = warp & 3, d = q * 32 + lane;
+        int t = 0, item_no = 0;
+        while (ok && wk.more()) {
+            const int64_t first = wk.tile, last = wk.last();
+            const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
+            const int64_t row0 = (int64_t)wk.n * p.Hq + (int64_t)kvh * p.G + g0;
+            float acc[HB], m[HB];
+#pragma unroll
+            for (int h = 0; h < HB; ++h) { acc[h] = 0.f; m[h] = -INFINITY; }
+            for (int64_t i = first; i < last; ++i, ++t) {
+                const int b = t & 1;
+                ok = warp_wait(&bar[PVD + b], t >> 1);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const float unit = sm_m[2 * HB + b];
+#pragma unroll
+                for (int h = 0; h < HB; h += 8) {
+                    float hi[8], lo[8], mt[8];
+                    load_parts<HB>(tm_o(b) + ((uint32_t)q << 21), h, hi, lo);
+                    ld8(sm_m + b * HB + h, mt);
+                    ptx::tmem_ld_wait(hi, lo);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float mn = fmaxf(m[h + e], mt[e]), mu = mn == -INFINITY ? 0.f : mn;
+                        const float v = fmaf(lo[e], 0.03125f, hi[e]) * (ex2(mt[e] - mu) * unit);
+                        acc[h + e] = fmaf(acc[h + e], ex2(m[h + e] - mu), v);
+                        m[h + e] = mn;
+                    }
+                }
+                ptx::tc_fence_before_sync();
+                warp_arrive(&bar[OFREE + b]);
+            }
+            if (!ok) break;
+            const int ib = item_no & 1;
+            ok = warp_wait(&bar[IREADY + ib], item_no >> 1);
+            if (!ok) break;
+            const bool whole = first == 0 && last == wk.nt;
+            float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
+            // the sum of head h, which both groups of softmax warps have a part of
+            auto sum = [&](int h, float m) {
+                const float mu = m == -INFINITY ? 0.f : m;
+                float l = 0.f;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float *x = sums + (ib * 8 + g * 4) * HB + h;
+                    l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(sums[16 * HB + (ib * 2 + g) * HB + h] - mu), l);
+                }
+                return l;
+            };
+            if (d < hb) {
+                const float mh = fmaxf(sums[16 * HB + ib * 2 * HB + d], sums[16 * HB + (ib * 2 + 1) * HB + d]), l = sum(d, mh);
+                if (!whole) { part[2 * d] = mh; part[2 * d + 1] = l; }
+                else if (p.lse) p.lse[row0 + d] = (mh + log2f(l)) / kLog2E;
+            }
+            float l[HB];
+            if (whole)
+#pragma unroll
+                for (int h = 0; h < HB; ++h) l[h] = sum(h, m[h]);
+            warp_arrive(&bar[IFREE + ib]);
+            if (d < D) {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row0 * D + d;
+                if (whole) {
+#pragma unroll
+                    for (int h = 0; h < HB; ++h)
+                        if (h < hb)
+                            out[h * D] = __float2bfloat16_rn(l[h] > 0.f ? __fdividef(acc[h], l[h])
+                                                                        : (l[h] == 0.f ? 0.f : l[h]));
+                } else {
+#pragma unroll
+                    for (int h = 0; h < HB; ++h)
+                        if (h < hb) part[HB * 2 + h * D + d] = acc[h];
+                }
+            }
+            ++item_no;
+            wk.next_item(p, last - first);
+        }
+    }
+    if (!ok) {
+        s_abort = 1;
+        report_status(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    }
+    __syncthreads();
+    if (s_abort) {      // every copy and MMA in flight lands before the memory is given back
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrain) {}
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, L::cols);
+    }
+}
+
+template <int D, int HB>
+cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    const uint64_t rows = (uint64_t)p.num_pages * p.Hkv << p.page_shift;
+    const uint32_t box = p.page_shift < 7 ? 1u << p.page_shift : TILE;
+    if (!make_map_bytes(&mk, p.kc, rows, D, box) || !make_map_bytes(&mv, p.vc, rows, D, box)) return cudaErrorInvalidValue;
+    constexpr uint32_t smem = Lay<D, HB>::bytes + 1024;
+    static_assert(smem <= 227 * 1024 - 4096, "shared memory");    // (beside the static part)
+    const cudaError_t e = allow_smem<paged_decode_q8_tc_kernel<D, HB>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), 512, smem, st, 1, mk, mv, p);
+}
+template <int D>
+cudaError_t launch_h(const PagedParams &p, int HB, int grid, cudaStream_t st) {
+    return HB == 8 ? launch<D, 8>(p, grid, st) : HB == 16 ? launch<D, 16>(p, grid, st) : launch<D, 32>(p, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_q8_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st) {
+    return d == 32 ? launch_h<32>(p, HB, grid, st) : d == 64 ? launch_h<64>(p, HB, grid, st) : launch_h<128>(p, HB, grid, st);
+}
+
+}  // namespace kda

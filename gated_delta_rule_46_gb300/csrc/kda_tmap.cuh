@@ -37,6 +37,19 @@ inline bool make_map_2d(CUtensorMap *m, const void *base, bool bf16, uint64_t ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A dense [rows][D] tensor of bytes, D = 32, 64 or 128, in boxes of whole rows with the swizzle of their size.
+inline bool make_map_bytes(CUtensorMap *m, const void *base, uint64_t rows, int D, uint32_t box_rows) {
+    const TmapEncode enc = tmap_encode();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, rows}, strides[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {(cuuint32_t)D, box_rows}, one[2] = {1, 1};
+    const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A bf16 [tokens][heads][d] tensor, tokens row_bytes apart (a multiple of 16), in boxes of one head's 64 channels x
 // box_tokens; channels outside read as zeros and are not written.
 inline bool make_map_heads(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t heads, uint64_t d, uint64_t row_bytes,

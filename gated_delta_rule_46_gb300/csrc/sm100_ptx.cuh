@@ -157,6 +157,18 @@ __device__ __forceinline__ void discard_l2(const void *p) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(p)) : "memory");
 }
 
+// ----------------------------------------------------------------- small asynchronous copies
+// Four bytes, or zeros where `is` is false (src is not read then).
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, bool is) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(is ? 4 : 0)
+                 : "memory");
+}
+// One of the barrier's arrivals, once this thread's copies of that kind so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // ----------------------------------------------------------------- TMEM
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -308,6 +320,29 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
            | ((uint32_t)(N >> 3) << 17)           // N / 8
            | ((uint32_t)(M >> 4) << 24);          // M / 16
 }
+// The same layouts with rows of ROW = 128, 64 or 32 bytes and the swizzle of that
+// size: the 16-byte chunk index XOR-ed with row % 8, row / 2 % 4 or row / 4 % 2, 8-row
+// groups 8 ROW bytes apart.  As a K-major operand (rows along M or N) or, with
+// `lead` bytes from each ROW bytes of M to the next, an M-major one (rows along K).
+template <int ROW>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lead = 16) {
+    static_assert(ROW == 128 || ROW == 64 || ROW == 32, "a swizzle's size");
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((8u * ROW) >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)(ROW == 128 ? 2u : ROW == 64 ? 4u : 6u) << 61;
+    return d;
+}
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B, f32 accumulate, dense, shape
+// M x N, K = 32; B is K-major, A too or M-major (a_rows_k).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_rows_k) {
+    return (1u << 4)                              // D format: f32 (A and B format 0: e4m3)
+           | ((uint32_t)a_rows_k << 15)
+           | ((uint32_t)(N >> 3) << 17)
+           | ((uint32_t)(M >> 4) << 24);
+}
 // One lane of a converged warp.  Code under it stays warp-uniform for the
 // compiler, so MMA descriptors live in uniform registers: one thread then issues
 // an M = 128 MMA every 47 cycles at N = 64 and 61 at N = 128, against 73 for
@@ -331,7 +366,17 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same with A in tensor memory: lane = row, two consecutive K elements per
+// The same for 8-bit floating-point operands, 32 of K at a time.
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The bf16 form with A in tensor memory: lane = row, two consecutive K elements per
 // 32-bit column.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
