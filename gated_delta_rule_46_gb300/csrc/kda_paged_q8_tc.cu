@@ -5,18 +5,20 @@
 // the codes go from HBM to the MMAs without passing through registers:
 //   S^T [128 tokens x N] = K Q^T,    O^T [d x N] = V^T P^T
 // on e4m3 operands.  K and V are e4m3 as they lie in the cache.  Q and the weights P,
-// which need more than e4m3's four significant bits, take two columns each:
-//   x = hi + lo,   hi = e4m3(x),   lo = e4m3(x - hi)      (lo scaled by a power of two)
-// which is exact for a bf16 query down to 2^-21 of its head's largest channel, and
-// keeps eight bits of a weight, as bf16 would.  The products of the two parts are
-// added in float32.  N = 2 HB for HB heads; with up to 8 of them, 16, the least there is.
+// which need more than e4m3's four significant bits, come in two parts,
+//   x = hi + lo,   hi = e4m3(x),   lo = e4m3(x - hi)
+// whose products are added up in the same accumulators.  With the largest of a head's
+// channels at 224 or more that is exact for a bf16 query down to 2^-11 of it, and off
+// by 2^-10, 2^-18 of the largest, below; of a weight it keeps eight bits, as bf16 would.
 //
 // A token's scale of K multiplies its row of S^T.  Its scale of V goes into its
 // weight: with the tile's largest score m and largest scale of V u,
 //   P = 256 e^{s - m} v_scale / u,   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
 // so that the weights use e4m3's range from the tile's own maximum on (an error below
-// 2^-23 of that, whatever the rest of the row holds), and tiles do not wait for each
-// other's maxima: two groups of softmax warps work on tiles in turn.
+// 2^-18 of that, whatever the rest of the row holds), and tiles do not wait for each
+// other's maxima: two groups of softmax warps work on tiles in turn.  What is the same for
+// all tokens of a tile (maxima, their exponentials) is worked out by a lane per head and
+// read by the others as vectors.
 //
 // Roles of the 16 warps: 0 loads (pages by TMA, scales by 4-byte copies), 1 issues
 // the S^T MMAs, 2 zeroes rows of V that hold no token and issues the O^T MMAs, 3 splits
@@ -37,8 +39,9 @@ constexpr int NSMAX = 12;                         // stages of the K and of the 
 constexpr int SB = 4, RING = 16;                  // S^T buffers; tiles whose scales and page masks are kept
 constexpr int QRING = 8;                          // items whose queries' factors are kept
 // A page mask or scales of tile t are read before O^T of tile t is issued, which V's stage of tile t + NS waits for, and
-// are written again for tile t + RING > t + NS.  An item's factors are read before the S^T buffer of its last tile of either
-// parity is given back, which tile t + SB waits for: long before the eighth item after it.
+// are written again for tile t + RING > t + NS.  An item's factors are written again once S^T of the sixth item after it
+// is done; a tile of either parity among its last two waited for the S^T buffer of one that the same softmax warps came to
+// after this item.
 static_assert(RING > NSMAX + 1 && QRING >= SB + 4, "rings");
 
 enum Bar { KFULL, KFREE = KFULL + NSMAX, VFULL = KFREE + NSMAX, VFREE = VFULL + NSMAX, SCALES = VFREE + NSMAX, SD = SCALES + RING,
@@ -47,20 +50,21 @@ enum Bar { KFULL, KFREE = KFULL + NSMAX, VFULL = KFREE + NSMAX, VFREE = VFULL + 
 
 template <int D, int HB>
 struct Lay {
-    static constexpr int N = 2 * HB;
+    static constexpr int N = HB < 16 ? 16 : HB;                      // the MMAs' columns; those past HB reach no one
     static constexpr uint32_t tile = TILE * D;
     // about 190 KB of stages where there is room for as much
     static constexpr int NS = D == 128 ? (HB == 32 ? 5 : 6) : D == 64 && HB == 32 ? 10 : NSMAX;
     // (V first: with d < 128 the MMA's rows past d read what lies behind a stage, which no one looks at)
-    static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_bytes = N * D;
-    static constexpr uint32_t P = (Q + 2 * q_bytes + 1023) / 1024 * 1024, p_bytes = N * TILE;
+    static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_part = N * D, q_bytes = 2 * q_part;
+    static constexpr uint32_t P = Q + 2 * q_bytes, p_part = N * TILE, p_bytes = 2 * p_part;
     static constexpr uint32_t SC = P + 2 * p_bytes;                  // float: scales of K [RING][8], of V [RING][8]
     static constexpr uint32_t QS = SC + 2 * RING * 8 * 4;            // factors of the queries [QRING][HB]
     static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [2][HB], u / 256 [2] (padded to 4)
     static constexpr uint32_t RED = M + 2 * HB * 4 + 16;             // maxima of the warps [2][2][4][HB]
     static constexpr uint32_t SUM = RED + 16 * HB * 4;               // sums of the item [2][8][HB], maxima [2][2][HB]
-    static constexpr uint32_t bytes = SUM + 20 * HB * 4;
-    static constexpr uint32_t cols = HB == 8 ? 128 : HB == 16 ? 256 : 512;   // TMEM: SB + 2 buffers of N columns
+    static constexpr uint32_t STAT = SUM + 20 * HB * 4;              // of each of warps 4-15: [4][HB]
+    static constexpr uint32_t bytes = STAT + 12 * 4 * HB * 4;
+    static constexpr uint32_t cols = N == 16 ? 128 : 256;            // TMEM: SB + 2 buffers of N columns
 };
 
 // Byte offset of the 16-byte chunk of a row, swizzled as TMA does it.
@@ -75,11 +79,13 @@ __device__ __forceinline__ float power_for(float a) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Columns [c, c + 8) and [HB + c, HB + c + 8) of a buffer, for the caller to wait for.
-template <int HB>
-__device__ __forceinline__ void load_parts(uint32_t addr, int c, float (&hi)[8], float (&lo)[8]) {
-    ptx::tmem_ld8(addr + c, hi);
-    ptx::tmem_ld8(addr + HB + c, lo);
+// Two weights in two parts each.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 w = __floats2half2_rn(x, y);
+    const uint16_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(w), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    hi = h;
+    lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r), __NV_SATFINITE, __NV_E4M3);
 }
 
 template <int D, int HB>
@@ -195,6 +201,7 @@ __global__ void __launch_bounds__(512, 1)
                 const int ib = item_no & 1;
                 ok = ptx::mbar_wait(&bar[QFULL + ib], (item_no >> 1) & 1, kWaitBudget);
                 const uint64_t q = ptx::sdesc_rows<D>(base + L::Q + ib * L::q_bytes);
+                constexpr int J = D / 32;
                 for (int64_t i = first; i < last && ok; ++i, ++t) {
                     const int s = t % NS, b = t % SB;
                     ok = ptx::mbar_wait(&bar[KFULL + s], (t / NS) & 1, kWaitBudget) &&
@@ -203,7 +210,8 @@ __global__ void __launch_bounds__(512, 1)
                     ptx::tc_fence_after_sync();
                     const uint64_t k = ptx::sdesc_rows<D>(base + L::K + s * L::tile);
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j) ptx::mma_f8_ss(tm_s(b), k + j * 2, q + j * 2, id_s, j > 0);
+                    for (int j = 0; j < 2 * J; ++j)
+                        ptx::mma_f8_ss(tm_s(b), k + j % J * 2, q + j / J * (L::q_part >> 4) + j % J * 2, id_s, j > 0);
                     ptx::mma_commit(&bar[SD + b]);
                     ptx::mma_commit(&bar[KFREE + s]);
                 }
@@ -239,9 +247,11 @@ __global__ void __launch_bounds__(512, 1)
                 if (ptx::elect_one()) {
                     ptx::tc_fence_after_sync();
                     const uint64_t v = ptx::sdesc_rows<D>(base + L::V + s * L::tile, L::tile);
-                    const uint64_t w = ptx::sdesc_rows<128>(base + L::P + b * L::p_bytes);
+                    const uint64_t w = ptx::sdesc_plain_n(base + L::P + b * L::p_bytes, 8 * L::N, 128);
+                    constexpr int J = TILE / 32;
 #pragma unroll
-                    for (int j = 0; j < TILE / 32; ++j) ptx::mma_f8_ss(tm_o(b), v + j * (32 * D >> 4), w + j * 2, id_o, j > 0);
+                    for (int j = 0; j < 2 * J; ++j)
+                        ptx::mma_f8_ss(tm_o(b), v + j % J * (32 * D >> 4), w + j * (32 * L::N >> 4), id_o, j > 0);
                     ptx::mma_commit(&bar[PVD + b]);
                     ptx::mma_commit(&bar[VFREE + s]);
                 }
@@ -254,6 +264,7 @@ __global__ void __launch_bounds__(512, 1)
         const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
         constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = HB / RPS < 1 ? 1 : HB / RPS;     // lanes per head, heads at a time
         const int c = lane % LPR;
+        const float sc2 = fabsf(p.scale) * kLog2E;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
@@ -284,7 +295,8 @@ __global__ void __launch_bounds__(512, 1)
                 }
 #pragma unroll
                 for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                const float f = power_for(a), inv = __uint_as_float((254u << 23) - __float_as_uint(f));
+                // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
+                const float f = power_for(a), inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
                 uint32_t hi[2] = {}, lo[2] = {};
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -293,12 +305,12 @@ __global__ void __launch_bounds__(512, 1)
                     const uint16_t ch = f2_to_e4m3x2(y0, y1);
                     const float2 b = e4m3x2_to_f2(ch);
                     hi[e >> 2] |= (uint32_t)ch << (8 * (e & 2));
-                    lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(16.f * (y0 - b.x), 16.f * (y1 - b.y)) << (8 * (e & 2));
+                    lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(y0 - b.x, y1 - b.y) << (8 * (e & 2));
                 }
                 if (h < HB) {
                     *reinterpret_cast<uint2 *>(dst + swizzled<D>(h, c >> 1) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(dst + swizzled<D>(HB + h, c >> 1) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
-                    if (c == 0) qs[(item_no % QRING) * HB + h] = f * (p.scale * kLog2E);
+                    *reinterpret_cast<uint2 *>(dst + L::q_part + swizzled<D>(h, c >> 1) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+                    if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
                 }
             }
             ptx::fence_async_smem();
@@ -308,13 +320,15 @@ __global__ void __launch_bounds__(512, 1)
         }
     } else if (warp < 12) {                                       // ---- softmax: thread = token of the tile
         const int wg = (warp - 4) >> 2, q = warp & 3, j = q * 32 + lane;
+        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - 4) * 4 * HB;
+        const int hl = lane < HB ? lane : 0;                      // this lane's head, of what is one for all tokens
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
             const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
-            float m[HB], l[HB];
+            float m = -INFINITY, l[HB];
 #pragma unroll
-            for (int h = 0; h < HB; ++h) { m[h] = -INFINITY; l[h] = 0.f; }
+            for (int h = 0; h < HB; ++h) l[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
                 if ((t & 1) != wg) continue;
                 const int sb = t % SB, r = t % RING, turn = t >> 1;
@@ -336,13 +350,12 @@ __global__ void __launch_bounds__(512, 1)
                     weight = in ? fv[j >> p.block_shift] * (256.f / unit) : 0.f;
 #pragma unroll
                     for (int h = 0; h < HB; h += 8) {
-                        float hi[8], lo[8], f[8];
-                        load_parts<HB>(tm_s(sb) + ((uint32_t)q << 21), h, hi, lo);
-                        ld8(qs + (item_no % QRING) * HB + h, f);
-                        ptx::tmem_ld_wait(hi, lo);
+                        float x[8];
+                        ptx::tmem_ld8(tm_s(sb) + ((uint32_t)q << 21) + h, x);
+                        ptx::tmem_ld_wait(x);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s[h + e] = hi[e] = in ? fmaf(lo[e], 0.0625f, hi[e]) * fk * f[e] : -INFINITY;
-                        const float mx = reduce_lanes(hi, lane, [](float x, float y) { return fmaxf(x, y); });
+                        for (int e = 0; e < 8; ++e) s[h + e] = x[e] = in ? x[e] * fk : -INFINITY;
+                        const float mx = reduce_lanes(x, lane, [](float x, float y) { return fmaxf(x, y); });
                         if (lane % 4 == 0) red[q * HB + h + lane / 4] = mx;
                     }
                     ptx::tc_fence_before_sync();
@@ -352,41 +365,61 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 ok = !ptx::bar_any(1 + wg, 128, !ok);
                 if (!ok) break;
-                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (j & 15);
+                {   // a lane per head: its factor, the tile's maximum, what that is to the sums so far
+                    const float mt = fmaxf(fmaxf(red[hl], red[HB + hl]), fmaxf(red[2 * HB + hl], red[3 * HB + hl]));
+                    const float f = qs[(item_no % QRING) * HB + hl], top = mt == -INFINITY ? mt : mt * f;
+                    const float mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn, less = ex2(m - mu);
+                    if (lane < HB) {
+                        st[hl] = f;
+                        st[HB + hl] = top == -INFINITY ? 0.f : top;
+                        st[2 * HB + hl] = ex2(top - mu);
+                        st[3 * HB + hl] = less;
+                        if (q == 0) sm_m[wg * HB + hl] = top;
+                    }
+                    const bool any = __any_sync(0xffffffffu, less != 1.f && m != -INFINITY);
+                    m = mn;
+                    __syncwarp();
+                    if (any)
+#pragma unroll
+                        for (int h = 0; h < HB; h += 4) {
+                            float x[4];
+                            ld4(st + 3 * HB + h, x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) l[h + e] *= x[e];
+                        }
+                }
+                uint32_t hi[HB / 4], lo[HB / 4];
 #pragma unroll
                 for (int h = 0; h < HB; h += 4) {
-                    float mt[4], w[4];
-                    ld4(red + h, mt);
-#pragma unroll
-                    for (int x = 1; x < 4; ++x) {
-                        float o[4];
-                        ld4(red + x * HB + h, o);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mt[e] = fmaxf(mt[e], o[e]);
-                    }
-                    if (j == 0) *reinterpret_cast<float4 *>(sm_m + wg * HB + h) = make_float4(mt[0], mt[1], mt[2], mt[3]);
+                    float f[4], top[4], g[4], w[4];
+                    ld4(st + h, f);
+                    ld4(st + HB + h, top);
+                    ld4(st + 2 * HB + h, g);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float mn = fmaxf(m[h + e], mt[e]), mu = mn == -INFINITY ? 0.f : mn;
-                        const float own = ex2(s[h + e] - (mt[e] == -INFINITY ? 0.f : mt[e]));
-                        l[h + e] = fmaf(l[h + e], ex2(m[h + e] - mu), own * ex2(mt[e] - mu));
-                        m[h + e] = mn;
+                        const float own = ex2(fmaf(s[h + e], f[e], -top[e]));
+                        l[h + e] = fmaf(own, g[e], l[h + e]);
                         w[e] = own * weight;
                     }
+                    uint32_t h0, h1, l0, l1;
+                    split2(w[0], w[1], h0, l0);
+                    split2(w[2], w[3], h1, l1);
+                    hi[h / 4] = h0 | h1 << 16;
+                    lo[h / 4] = l0 | l1 << 16;
+                }
+                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (j >> 3) * 8 * L::N + (j & 7) * 16;
+                if constexpr (HB == 8) {
+                    *reinterpret_cast<uint2 *>(w8) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(w8 + L::p_part) = make_uint2(lo[0], lo[1]);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const uint16_t hi = f2_to_e4m3x2(w[e], w[e + 1]);
-                        const float2 b = e4m3x2_to_f2(hi);
-                        const uint16_t lo = f2_to_e4m3x2(32.f * (w[e] - b.x), 32.f * (w[e + 1] - b.y));
-                        w8[swizzled<128>(h + e, j >> 4)] = (uint8_t)hi;
-                        w8[swizzled<128>(h + e + 1, j >> 4)] = (uint8_t)(hi >> 8);
-                        w8[swizzled<128>(HB + h + e, j >> 4)] = (uint8_t)lo;
-                        w8[swizzled<128>(HB + h + e + 1, j >> 4)] = (uint8_t)(lo >> 8);
+                    for (int h = 0; h < HB / 4; h += 4) {
+                        *reinterpret_cast<uint4 *>(w8 + h * 32) = make_uint4(hi[h], hi[h + 1], hi[h + 2], hi[h + 3]);
+                        *reinterpret_cast<uint4 *>(w8 + L::p_part + h * 32) = make_uint4(lo[h], lo[h + 1], lo[h + 2], lo[h + 3]);
                     }
                 }
                 if (j == 0) sm_m[2 * HB + wg] = unit * 0x1p-8f;
                 ptx::fence_async_smem();
-                ptx::tc_fence_before_sync();
                 warp_arrive(&bar[PREADY + wg]);
             }
             if (!ok) break;
@@ -402,45 +435,50 @@ __global__ void __launch_bounds__(512, 1)
                 const float sum = reduce_lanes(v, lane, [](float x, float y) { return x + y; });
                 if (lane % 4 == 0) sums[(ib * 8 + wg * 4 + q) * HB + h + lane / 4] = sum;
             }
-            if (j == 0)
-#pragma unroll
-                for (int h = 0; h < HB; h += 4)
-                    *reinterpret_cast<float4 *>(sums + 16 * HB + (ib * 2 + wg) * HB + h) = make_float4(m[h], m[h + 1], m[h + 2], m[h + 3]);
+            if (q == 0 && lane < HB) sums[16 * HB + (ib * 2 + wg) * HB + lane] = m;
             warp_arrive(&bar[IREADY + ib]);
             ++item_no;
             wk.next_item(p, last - first);
         }
     } else {                                                      // ---- output: thread = channel
         const int q = warp & 3, d = q * 32 + lane;
+        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - 4) * 4 * HB;
+        const int hl = lane < HB ? lane : 0;
+        const bool works = q * 32 < D;                            // (rows of O^T past d reach no one)
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
             const int64_t row0 = (int64_t)wk.n * p.Hq + (int64_t)kvh * p.G + g0;
-            float acc[HB], m[HB];
+            float acc[HB], m = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < HB; ++h) { acc[h] = 0.f; m[h] = -INFINITY; }
+            for (int h = 0; h < HB; ++h) acc[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
                 const int b = t & 1;
                 ok = warp_wait(&bar[PVD + b], t >> 1);
                 if (!ok) break;
-                ptx::tc_fence_after_sync();
-                const float unit = sm_m[2 * HB + b];
-#pragma unroll
-                for (int h = 0; h < HB; h += 8) {
-                    float hi[8], lo[8], mt[8];
-                    load_parts<HB>(tm_o(b) + ((uint32_t)q << 21), h, hi, lo);
-                    ld8(sm_m + b * HB + h, mt);
-                    ptx::tmem_ld_wait(hi, lo);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float mn = fmaxf(m[h + e], mt[e]), mu = mn == -INFINITY ? 0.f : mn;
-                        const float v = fmaf(lo[e], 0.03125f, hi[e]) * (ex2(mt[e] - mu) * unit);
-                        acc[h + e] = fmaf(acc[h + e], ex2(m[h + e] - mu), v);
-                        m[h + e] = mn;
+                if (works) {
+                    ptx::tc_fence_after_sync();
+                    const float top = sm_m[b * HB + hl], mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn;
+                    __syncwarp();                                 // (the factors before have been read)
+                    if (lane < HB) {
+                        st[hl] = ex2(m - mu);
+                        st[HB + hl] = ex2(top - mu) * sm_m[2 * HB + b];
                     }
+                    m = mn;
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < HB; h += 8) {
+                        float v[8], f[8], g[8];
+                        ptx::tmem_ld8(tm_o(b) + ((uint32_t)q << 21) + h, v);
+                        ld8(st + h, f);
+                        ld8(st + HB + h, g);
+                        ptx::tmem_ld_wait(v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[h + e] = fmaf(acc[h + e], f[e], v[e] * g[e]);
+                    }
+                    ptx::tc_fence_before_sync();
                 }
-                ptx::tc_fence_before_sync();
                 warp_arrive(&bar[OFREE + b]);
             }
             if (!ok) break;
@@ -449,35 +487,34 @@ __global__ void __launch_bounds__(512, 1)
             if (!ok) break;
             const bool whole = first == 0 && last == wk.nt;
             float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
-            // the sum of head h, which both groups of softmax warps have a part of
-            auto sum = [&](int h, float m) {
-                const float mu = m == -INFINITY ? 0.f : m;
+            {   // a lane per head: the sum, which both groups of softmax warps have a part of
+                const float *ms = sums + 16 * HB + ib * 2 * HB + hl;
+                const float mh = fmaxf(ms[0], ms[HB]), mu = mh == -INFINITY ? 0.f : mh;
                 float l = 0.f;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float *x = sums + (ib * 8 + g * 4) * HB + h;
-                    l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(sums[16 * HB + (ib * 2 + g) * HB + h] - mu), l);
+                    const float *x = sums + (ib * 8 + g * 4) * HB + hl;
+                    l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(ms[g * HB] - mu), l);
                 }
-                return l;
-            };
-            if (d < hb) {
-                const float mh = fmaxf(sums[16 * HB + ib * 2 * HB + d], sums[16 * HB + (ib * 2 + 1) * HB + d]), l = sum(d, mh);
-                if (!whole) { part[2 * d] = mh; part[2 * d + 1] = l; }
-                else if (p.lse) p.lse[row0 + d] = (mh + log2f(l)) / kLog2E;
+                __syncwarp();
+                if (lane < HB) st[2 * HB + hl] = l;
+                if (q == 0 && lane < hb) {
+                    if (!whole) { part[2 * lane] = mh; part[2 * lane + 1] = l; }
+                    else if (p.lse) p.lse[row0 + lane] = (mh + log2f(l)) / kLog2E;
+                }
+                __syncwarp();
             }
-            float l[HB];
-            if (whole)
-#pragma unroll
-                for (int h = 0; h < HB; ++h) l[h] = sum(h, m[h]);
             warp_arrive(&bar[IFREE + ib]);
-            if (d < D) {
+            if (works) {
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row0 * D + d;
+                // (a sum is 0 or at least 1, a maximum's own weight, or infinite or NaN)
                 if (whole) {
 #pragma unroll
                     for (int h = 0; h < HB; ++h)
-                        if (h < hb)
-                            out[h * D] = __float2bfloat16_rn(l[h] > 0.f ? __fdividef(acc[h], l[h])
-                                                                        : (l[h] == 0.f ? 0.f : l[h]));
+                        if (h < hb) {
+                            const float l = st[2 * HB + h];
+                            out[h * D] = __float2bfloat16_rn(l > 0.f ? __fdividef(acc[h], l) : (l == 0.f ? 0.f : l));
+                        }
                 } else {
 #pragma unroll
                     for (int h = 0; h < HB; ++h)

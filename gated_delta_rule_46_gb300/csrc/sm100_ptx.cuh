@@ -335,11 +335,17 @@ __device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lead = 1
     d |= (uint64_t)(ROW == 128 ? 2u : ROW == 64 ? 4u : 6u) << 61;
     return d;
 }
+// An N-major operand without a swizzle: 16 bytes of N for each of 8 rows along K in 128
+// contiguous bytes, `next_k` bytes to the next 8 rows, `next_n` to the next 16 bytes.
+__device__ __forceinline__ uint64_t sdesc_plain_n(uint32_t saddr, uint32_t next_k, uint32_t next_n) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((next_k >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((next_n >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46;
+}
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B, f32 accumulate, dense, shape
-// M x N, K = 32; B is K-major, A too or M-major (a_rows_k).
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_rows_k) {
+// M x N, K = 32, both operands K-major, or with rows along K (M- and N-major).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool rows_k) {
     return (1u << 4)                              // D format: f32 (A and B format 0: e4m3)
-           | ((uint32_t)a_rows_k << 15)
+           | ((rows_k ? 3u : 0u) << 15)
            | ((uint32_t)(N >> 3) << 17)
            | ((uint32_t)(M >> 4) << 24);
 }
