@@ -20,10 +20,11 @@
 // all tokens of a tile (maxima, their exponentials) is worked out by a lane per head and
 // read by the others as vectors.
 //
-// Roles of the 16 warps: 0 loads (pages by TMA, scales by 4-byte copies), 1 issues
-// the S^T MMAs, 2 zeroes rows of V that hold no token and issues the O^T MMAs, 3 splits
-// and stages Q, 4-7 and 8-11 run the softmax of even and odd tiles (thread = token),
-// 12-15 keep the running output (thread = channel) in float32 registers.
+// Roles of the 20 warps: 0-3 load tiles in turn (pages by TMA, scales by 4-byte copies),
+// 4 issues the S^T MMAs, 5 zeroes rows of V that hold no token and issues the O^T MMAs,
+// 6 splits and stages Q, 8-11 and 12-15 run the softmax of even and odd tiles (thread =
+// token), 16-19 keep the running output (thread = channel) in float32 registers.  Items
+// of 32 heads have one warp that loads, as their softmax takes 128 registers a thread.
 #include <cuda.h>
 
 #include "kda_paged_tc.cuh"
@@ -37,34 +38,41 @@ using namespace paged;
 
 constexpr int NSMAX = 12;                         // stages of the K and of the V ring, at most
 constexpr int SB = 4, RING = 16;                  // S^T buffers; tiles whose scales and page masks are kept
-constexpr int QRING = 8;                          // items whose queries' factors are kept
-// A page mask or scales of tile t are read before O^T of tile t is issued, which V's stage of tile t + NS waits for, and
-// are written again for tile t + RING > t + NS.  An item's factors are written again once S^T of the sixth item after it
-// is done; a tile of either parity among its last two waited for the S^T buffer of one that the same softmax warps came to
-// after this item.
-static_assert(RING > NSMAX + 1 && QRING >= SB + 4, "rings");
+constexpr int QRING = 16;                         // items whose queries' factors are kept
+constexpr int NG = 2;                             // groups of softmax warps (three: the same times)
+constexpr int LMAX = 4;                           // warps that load, at most
+// A page mask or scales of tile t are read before O^T of tile t is issued, which V's stage of tile t + NS waits for; the warp
+// that writes them again, for tile t + RING, has loaded tile t + RING - LMAX >= t + NS before.  An item's factors are written
+// again once S^T of the item QRING - 2 behind it is done: of its last tiles one for each group of softmax warps waited for an
+// S^T buffer that the group gave back after this item.
+static_assert(RING >= NSMAX + LMAX && QRING >= SB + NG + 2, "rings");
 
 enum Bar { KFULL, KFREE = KFULL + NSMAX, VFULL = KFREE + NSMAX, VFREE = VFULL + NSMAX, SCALES = VFREE + NSMAX, SD = SCALES + RING,
-           SFREE = SD + SB, PREADY = SFREE + SB, PVD = PREADY + 2, OFREE = PVD + 2, QFULL = OFREE + 2, QFREE = QFULL + 2,
+           SFREE = SD + SB, PREADY = SFREE + SB, PVD = PREADY + NG, OFREE = PVD + NG, QFULL = OFREE + NG, QFREE = QFULL + 2,
            IREADY = QFREE + 2, IFREE = IREADY + 2, NBAR = IFREE + 2 };
 
 template <int D, int HB>
 struct Lay {
     static constexpr int N = HB < 16 ? 16 : HB;                      // the MMAs' columns; those past HB reach no one
+    // roles, by their first warps; 32 heads need the registers of 16 warps
+    static constexpr int LOADERS = HB == 32 ? 1 : LMAX;
+    static constexpr int MMA_S = LOADERS, MMA_O = LOADERS + 1, STAGE_Q = LOADERS + 2, SOFTMAX = LOADERS == 1 ? 4 : 8;
+    static constexpr int OUT = SOFTMAX + 4 * NG, THREADS = 32 * (OUT + 4);
     static constexpr uint32_t tile = TILE * D;
     // about 190 KB of stages where there is room for as much
     static constexpr int NS = D == 128 ? (HB == 32 ? 5 : 6) : D == 64 && HB == 32 ? 10 : NSMAX;
     // (V first: with d < 128 the MMA's rows past d read what lies behind a stage, which no one looks at)
     static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_part = N * D, q_bytes = 2 * q_part;
     static constexpr uint32_t P = Q + 2 * q_bytes, p_part = N * TILE, p_bytes = 2 * p_part;
-    static constexpr uint32_t SC = P + 2 * p_bytes;                  // float: scales of K [RING][8], of V [RING][8]
+    static constexpr uint32_t SC = P + NG * p_bytes;                 // float: scales of K [RING][8], of V [RING][8]
     static constexpr uint32_t QS = SC + 2 * RING * 8 * 4;            // factors of the queries [QRING][HB]
-    static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [2][HB], u / 256 [2] (padded to 4)
-    static constexpr uint32_t RED = M + 2 * HB * 4 + 16;             // maxima of the warps [2][2][4][HB]
-    static constexpr uint32_t SUM = RED + 16 * HB * 4;               // sums of the item [2][8][HB], maxima [2][2][HB]
-    static constexpr uint32_t STAT = SUM + 20 * HB * 4;              // of each of warps 4-15: [4][HB]
-    static constexpr uint32_t bytes = STAT + 12 * 4 * HB * 4;
-    static constexpr uint32_t cols = N == 16 ? 128 : 256;            // TMEM: SB + 2 buffers of N columns
+    static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [NG][HB], u / 256 [NG] (padded to 4)
+    static constexpr uint32_t RED = M + NG * HB * 4 + 16;            // maxima of the warps [NG][2][4][HB]
+    static constexpr uint32_t SUM = RED + NG * 8 * HB * 4;           // sums of the item [2][4 NG][HB], maxima [2][NG][HB]
+    static constexpr uint32_t STAT = SUM + 10 * NG * HB * 4;         // of each softmax and output warp: [4][HB]
+    static constexpr uint32_t bytes = STAT + (4 * NG + 4) * 4 * HB * 4;
+    static constexpr uint32_t cols = N == 16 ? 128 : 256;            // TMEM: SB + NG buffers of N columns
+    static_assert((SB + NG) * N <= cols, "tensor memory");
 };
 
 // Byte offset of the 16-byte chunk of a row, swizzled as TMA does it.
@@ -89,10 +97,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 }
 
 template <int D, int HB>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     paged_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedParams p) {
     using L = Lay<D, HB>;
-    constexpr int NS = L::NS;
+    constexpr int NS = L::NS, LOADERS = L::LOADERS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[NBAR];
     __shared__ int64_t s_sum[257];
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
             if (i >= SCALES && i < SD) count = 32;
-            else if (i >= IREADY && i < IFREE) count = 8;
+            else if (i >= IREADY && i < IFREE) count = 4 * NG;
             else if ((i >= SFREE && i < PVD) || (i >= OFREE && i < QFULL) || i >= IFREE) count = 4;
             ptx::mbar_init(&bar[i], count);
         }
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(512, 1)
         ptx::prefetch_tensormap(&mk);
         ptx::prefetch_tensormap(&mv);
     }
-    if (warp == 1) {
+    if (warp == L::MMA_S) {
         ptx::tmem_alloc(&s_tmem, L::cols);
         ptx::tmem_relinquish();
     }
@@ -139,59 +147,55 @@ __global__ void __launch_bounds__(512, 1)
                  *const sm_m = reinterpret_cast<float *>(sm + L::M), *const sums = reinterpret_cast<float *>(sm + L::SUM);
     bool ok = true;
 
-    if (warp == 0) {                                              // ---- loads: lane = page of the tile
-        // a tile's page is looked up while the tile before it is loaded
-        int64_t i = wk.tile, first = i, last = wk.last();
-        auto lookup = [&](int at) {
-            return lane < pieces && at < wk.len ? p.table[(int64_t)wk.n * p.max_pages + (at >> p.page_shift)] : 0;
-        };
+    if (warp < LOADERS) {                                         // ---- loads: lane = page of the tile
         const int per = 1 << (p.page_shift - p.block_shift);      // scales of a page and head
-        int told = -1, at = (int)(i * TILE) + lane * rows, id = lookup(at);     // at: this page's first token of the tile
-        for (int t = 0; ok && wk.more(); ++t) {
-            if (wk.n != told) {
-                told = wk.n;
-                if (lane == 0 && wk.raw != wk.len) report_status(p.status, KDA_ERR_INVALID_ARG);
-            }
-            const int kvh = wk.item / nb, at0 = at;
-            int page = -1;
-            if (lane < pieces && at < wk.len) {
-                if (id >= 0 && id < p.num_pages) page = id;
-                else report_status(p.status, KDA_ERR_INVALID_ARG);
-            }
-            // scales: lanes 0-7 those of K, 8-15 those of V, of the block of tokens that starts at `from`
-            const int from = (int)(i * TILE) + ((lane & 7) << p.block_shift), off = (lane & 7) << p.block_shift;
-            const int of = __shfl_sync(0xffffffffu, page, (off >> rows_shift) & 31);
-            const bool block = lane < 16 && off < TILE && from < wk.len && of >= 0;
-            if (++i == last) {
-                wk.next_item(p, last - first);
-                if (wk.more()) { first = i = wk.tile; last = wk.last(); }
-            }
-            at = (int)(i * TILE) + lane * rows;
-            id = wk.more() ? lookup(at) : 0;
-            const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-            const uint32_t bytes = (uint32_t)__popc(mask) * rows * D;
-            const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at0 & ((1 << p.page_shift) - 1)));
-            const int s = t % NS, r = t % RING;
-            for (int kv = 0; kv < 2; ++kv) {
-                uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
-                if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
-                uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * D;
-                if (lane == 0) {
-                    if (kv == 0) s_mask[r] = mask;
-                    ptx::mbar_arrive_expect_tx(full, bytes);
+        int t0 = 0;                                               // tiles before the item
+        while (ok && wk.more()) {
+            const int64_t first = wk.tile, last = wk.last();
+            const int kvh = wk.item / nb, len = wk.len;
+            const int32_t *table = p.table + (int64_t)wk.n * p.max_pages;
+            if (threadIdx.x == 0 && wk.raw != len) report_status(p.status, KDA_ERR_INVALID_ARG);
+            for (int64_t i = first + ((warp - t0) & (LOADERS - 1)); i < last; i += LOADERS) {
+                const int t = t0 + (int)(i - first), s = t % NS, r = t % RING;
+                const int at = (int)(i * TILE) + lane * rows;     // this page's first token of the tile
+                int page = -1;
+                if (lane < pieces && at < len) {
+                    page = table[at >> p.page_shift];
+                    if (page < 0 || page >= p.num_pages) {
+                        report_status(p.status, KDA_ERR_INVALID_ARG);
+                        page = -1;
+                    }
                 }
-                __syncwarp();
-                if (page >= 0) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
-                if (kv == 0) {
-                    const float *src = lane < 8 ? p.ks : p.vs;
-                    if (block)
-                        src += ((int64_t)of * p.Hkv + kvh) * per + ((from & ((1 << p.page_shift) - 1)) >> p.block_shift);
-                    if (lane < 16) ptx::cp_async4(sc + (lane >> 3) * RING * 8 + r * 8 + (lane & 7), src, block);
-                    ptx::cp_async_arrive(&bar[SCALES + r]);
+                const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t bytes = (uint32_t)__popc(mask) * rows * D;
+                const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at & ((1 << p.page_shift) - 1)));
+                // scales: lanes 0-7 those of K, 8-15 those of V, of the block of tokens that starts at `from`
+                const int off = (lane & 7) << p.block_shift, from = (int)(i * TILE) + off;
+                const int of = __shfl_sync(0xffffffffu, page, (off >> rows_shift) & 31);
+                const bool block = lane < 16 && off < TILE && from < len && of >= 0;
+                const float *src = lane < 8 ? p.ks : p.vs;
+                if (block) src += ((int64_t)of * p.Hkv + kvh) * per + ((from & ((1 << p.page_shift) - 1)) >> p.block_shift);
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
+                    if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
+                    uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * D;
+                    if (lane == 0) {
+                        if (kv == 0) s_mask[r] = mask;
+                        ptx::mbar_arrive_expect_tx(full, bytes);
+                    }
+                    __syncwarp();
+                    if (page >= 0) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
+                    if (kv == 0) {
+                        if (lane < 16) ptx::cp_async4(sc + (lane >> 3) * RING * 8 + r * 8 + (lane & 7), src, block);
+                        ptx::cp_async_arrive(&bar[SCALES + r]);
+                    }
                 }
+                if (!ok) break;
             }
+            t0 += (int)(last - first);
+            wk.next_item(p, last - first);
         }
-    } else if (warp == 1) {                                       // ---- S^T
+    } else if (warp == L::MMA_S) {                                // ---- S^T
         if (ptx::elect_one()) {
             int item_no = 0;
             constexpr uint32_t id_s = ptx::idesc_e4m3_f32(128, L::N, false);
@@ -220,13 +224,13 @@ __global__ void __launch_bounds__(512, 1)
                 wk.next_item(p, last - first);
             }
         }
-    } else if (warp == 2) {                                       // ---- rows of V without a token, O^T
+    } else if (warp == L::MMA_O) {                                // ---- rows of V without a token, O^T
         constexpr uint32_t id_o = ptx::idesc_e4m3_f32(128, L::N, true);
         for (int t = 0; ok && wk.more();) {
             const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
             for (int64_t i = first; i < last; ++i, ++t) {
-                const int s = t % NS, b = t & 1;
+                const int s = t % NS, b = t % NG;
                 ok = warp_wait(&bar[VFULL + s], t / NS);
                 if (!ok) break;
                 const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[t % RING]);
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(512, 1)
                     ptx::fence_async_smem();
                     __syncwarp();
                 }
-                ok = warp_wait(&bar[PREADY + b], t >> 1);         // (which says that O^T's buffer is free too)
+                ok = warp_wait(&bar[PREADY + b], t / NG);         // (which says that O^T's buffer is free too)
                 if (!ok) break;
                 if (ptx::elect_one()) {
                     ptx::tc_fence_after_sync();
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(512, 1)
             }
             wk.next_item(p, last - first);
         }
-    } else if (warp == 3) {                                       // ---- Q
+    } else if (warp == L::STAGE_Q) {                              // ---- Q
         int item_no = 0;
         const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
         constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = HB / RPS < 1 ? 1 : HB / RPS;     // lanes per head, heads at a time
@@ -271,56 +275,62 @@ __global__ void __launch_bounds__(512, 1)
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
             const __nv_bfloat16 *q =
                 static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
-            uint4 u[STEPS];
+            constexpr int U = STEPS < 4 ? STEPS : 4;              // loads under way
+            for (int i0 = 0; i0 < STEPS; i0 += U) {
+                uint4 u[U];
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int h = i * RPS + lane / LPR;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (h < hb) {
-                    if (q16) u[i] = *reinterpret_cast<const uint4 *>(q + h * D + c * 8);
-                    else u[i] = load8(q + h * D + c * 8);
+                for (int i = 0; i < U; ++i) {
+                    const int h = (i0 + i) * RPS + lane / LPR;
+                    u[i] = make_uint4(0, 0, 0, 0);
+                    if (h < hb) {
+                        if (q16) u[i] = *reinterpret_cast<const uint4 *>(q + h * D + c * 8);
+                        else u[i] = load8(q + h * D + c * 8);
+                    }
+                }
+                if (i0 == 0 && item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int h = (i0 + i) * RPS + lane / LPR;
+                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    float x[8], a = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+                        a = fmaxf(a, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
+                    }
+#pragma unroll
+                    for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                    // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
+                    const float f = power_for(a), inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
+                    uint32_t hi[2] = {}, lo[2] = {};
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        // (a saturating conversion takes infinities for large numbers)
+                        const float y0 = fabsf(x[e]) < INFINITY ? x[e] * inv : NAN;
+                        const float y1 = fabsf(x[e + 1]) < INFINITY ? x[e + 1] * inv : NAN;
+                        const uint16_t ch = f2_to_e4m3x2(y0, y1);
+                        const float2 b = e4m3x2_to_f2(ch);
+                        hi[e >> 2] |= (uint32_t)ch << (8 * (e & 2));
+                        lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(y0 - b.x, y1 - b.y) << (8 * (e & 2));
+                    }
+                    if (h < HB) {
+                        uint8_t *to = dst + swizzled<D>(h, c >> 1) + (c & 1) * 8;
+                        *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(to + L::q_part) = make_uint2(lo[0], lo[1]);
+                        if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
+                    }
                 }
             }
-            if (item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
             if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int h = i * RPS + lane / LPR;
-                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                float x[8], a = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-                    a = fmaxf(a, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
-                }
-#pragma unroll
-                for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
-                const float f = power_for(a), inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
-                uint32_t hi[2] = {}, lo[2] = {};
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    // (a saturating conversion takes infinities for large numbers)
-                    const float y0 = fabsf(x[e]) < INFINITY ? x[e] * inv : NAN, y1 = fabsf(x[e + 1]) < INFINITY ? x[e + 1] * inv : NAN;
-                    const uint16_t ch = f2_to_e4m3x2(y0, y1);
-                    const float2 b = e4m3x2_to_f2(ch);
-                    hi[e >> 2] |= (uint32_t)ch << (8 * (e & 2));
-                    lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(y0 - b.x, y1 - b.y) << (8 * (e & 2));
-                }
-                if (h < HB) {
-                    *reinterpret_cast<uint2 *>(dst + swizzled<D>(h, c >> 1) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(dst + L::q_part + swizzled<D>(h, c >> 1) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
-                    if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
-                }
-            }
             ptx::fence_async_smem();
             warp_arrive(&bar[QFULL + (item_no & 1)]);
             ++item_no;
             wk.next_item(p, last - first);
         }
-    } else if (warp < 12) {                                       // ---- softmax: thread = token of the tile
-        const int wg = (warp - 4) >> 2, q = warp & 3, j = q * 32 + lane;
-        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - 4) * 4 * HB;
+    } else if (warp >= L::SOFTMAX && warp < L::OUT) {             // ---- softmax: thread = token of the tile
+        const int wg = (warp - L::SOFTMAX) >> 2, q = warp & 3, j = q * 32 + lane;
+        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - L::SOFTMAX) * 4 * HB;
         const int hl = lane < HB ? lane : 0;                      // this lane's head, of what is one for all tokens
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
@@ -330,8 +340,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int h = 0; h < HB; ++h) l[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
-                if ((t & 1) != wg) continue;
-                const int sb = t % SB, r = t % RING, turn = t >> 1;
+                if (t % NG != wg) continue;
+                const int sb = t % SB, r = t % RING, turn = t / NG;
                 float *red = reinterpret_cast<float *>(sm + L::RED) + (wg * 2 + (turn & 1)) * 4 * HB;
                 ok = warp_wait(&bar[SCALES + r], t / RING) && warp_wait(&bar[SD + sb], t / SB);
                 float s[HB], weight = 0.f, unit = 0.f;
@@ -355,13 +365,17 @@ __global__ void __launch_bounds__(512, 1)
                         ptx::tmem_ld_wait(x);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) s[h + e] = x[e] = in ? x[e] * fk : -INFINITY;
-                        const float mx = reduce_lanes(x, lane, [](float x, float y) { return fmaxf(x, y); });
-                        if (lane % 4 == 0) red[q * HB + h + lane / 4] = mx;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = ptx::warp_max(x[e]);
+                        if (lane == 0) {
+                            *reinterpret_cast<float4 *>(red + q * HB + h) = make_float4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<float4 *>(red + q * HB + h + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                        }
                     }
                     ptx::tc_fence_before_sync();
                     warp_arrive(&bar[SFREE + sb]);
-                    // the weights and maxima of two tiles ago have been used
-                    ok = t < 2 || warp_wait(&bar[OFREE + wg], turn - 1);
+                    // the weights and maxima of this group's last tile have been used
+                    ok = t < NG || warp_wait(&bar[OFREE + wg], turn - 1);
                 }
                 ok = !ptx::bar_any(1 + wg, 128, !ok);
                 if (!ok) break;
@@ -418,7 +432,7 @@ __global__ void __launch_bounds__(512, 1)
                         *reinterpret_cast<uint4 *>(w8 + L::p_part + h * 32) = make_uint4(lo[h], lo[h + 1], lo[h + 2], lo[h + 3]);
                     }
                 }
-                if (j == 0) sm_m[2 * HB + wg] = unit * 0x1p-8f;
+                if (j == 0) sm_m[NG * HB + wg] = unit * 0x1p-8f;
                 ptx::fence_async_smem();
                 warp_arrive(&bar[PREADY + wg]);
             }
@@ -433,16 +447,16 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = l[h + e];
                 const float sum = reduce_lanes(v, lane, [](float x, float y) { return x + y; });
-                if (lane % 4 == 0) sums[(ib * 8 + wg * 4 + q) * HB + h + lane / 4] = sum;
+                if (lane % 4 == 0) sums[((ib * NG + wg) * 4 + q) * HB + h + lane / 4] = sum;
             }
-            if (q == 0 && lane < HB) sums[16 * HB + (ib * 2 + wg) * HB + lane] = m;
+            if (q == 0 && lane < HB) sums[(8 * NG + ib * NG + wg) * HB + lane] = m;
             warp_arrive(&bar[IREADY + ib]);
             ++item_no;
             wk.next_item(p, last - first);
         }
-    } else {                                                      // ---- output: thread = channel
+    } else if (warp >= L::OUT) {                                  // ---- output: thread = channel
         const int q = warp & 3, d = q * 32 + lane;
-        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - 4) * 4 * HB;
+        float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - L::SOFTMAX) * 4 * HB;
         const int hl = lane < HB ? lane : 0;
         const bool works = q * 32 < D;                            // (rows of O^T past d reach no one)
         int t = 0, item_no = 0;
@@ -454,8 +468,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int h = 0; h < HB; ++h) acc[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
-                const int b = t & 1;
-                ok = warp_wait(&bar[PVD + b], t >> 1);
+                const int b = t % NG;
+                ok = warp_wait(&bar[PVD + b], t / NG);
                 if (!ok) break;
                 if (works) {
                     ptx::tc_fence_after_sync();
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(512, 1)
                     __syncwarp();                                 // (the factors before have been read)
                     if (lane < HB) {
                         st[hl] = ex2(m - mu);
-                        st[HB + hl] = ex2(top - mu) * sm_m[2 * HB + b];
+                        st[HB + hl] = ex2(top - mu) * sm_m[NG * HB + b];
                     }
                     m = mn;
                     __syncwarp();
@@ -487,13 +501,15 @@ __global__ void __launch_bounds__(512, 1)
             if (!ok) break;
             const bool whole = first == 0 && last == wk.nt;
             float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
-            {   // a lane per head: the sum, which both groups of softmax warps have a part of
-                const float *ms = sums + 16 * HB + ib * 2 * HB + hl;
-                const float mh = fmaxf(ms[0], ms[HB]), mu = mh == -INFINITY ? 0.f : mh;
-                float l = 0.f;
+            {   // a lane per head: the sum, which every group of softmax warps has a part of
+                const float *ms = sums + (8 + ib) * NG * HB + hl;
+                float mh = ms[0], l = 0.f;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float *x = sums + (ib * 8 + g * 4) * HB + hl;
+                for (int g = 1; g < NG; ++g) mh = fmaxf(mh, ms[g * HB]);
+                const float mu = mh == -INFINITY ? 0.f : mh;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float *x = sums + (ib * NG + g) * 4 * HB + hl;
                     l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(ms[g * HB] - mu), l);
                 }
                 __syncwarp();
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == LOADERS) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, L::cols);
     }
@@ -552,7 +568,7 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");    // (beside the static part)
     const cudaError_t e = allow_smem<paged_decode_q8_tc_kernel<D, HB>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), 512, smem, st, 1, mk, mv, p);
+    return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), Lay<D, HB>::THREADS, smem, st, 1, mk, mv, p);
 }
 template <int D>
 cudaError_t launch_h(const PagedParams &p, int HB, int grid, cudaStream_t st) {

@@ -402,6 +402,13 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
         : "memory");
 }
 
+// The largest of a warp's numbers (NaN only where all are).
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Named barrier over `n` threads; true for all of them if `x` is for any.
 __device__ __forceinline__ bool bar_any(int id, int n, bool x) {
     uint32_t r;
