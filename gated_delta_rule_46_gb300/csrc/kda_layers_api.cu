@@ -51,6 +51,11 @@ int block_shift(int block, int page_size) {
     return block >= 16 && block <= 128 && block <= page_size ? page_shift(block) : -1;
 }
 
+// a workspace of `need` bytes, where any are needed
+bool workspace_ok(const void *workspace, size_t bytes, size_t need) {
+    return aligned(workspace, 16) && (need == 0 || (workspace && bytes >= need));
+}
+
 bool pools_ok(void *const *pools, const int64_t *page_bytes, int n) {
     if (n > 0 && (!pools || !page_bytes)) return false;
     for (int i = 0; i < n; ++i)
@@ -259,8 +264,8 @@ kda_status_t kda_paged_decode_q8(const void *q, int64_t ldq, const void *k_cache
     if (!aligned(q, e) || !aligned(out, e) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !words(k_scale, v_scale, page_table, seq_lens, lse, status))
         return KDA_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < kda_paged_decode_q8_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype))
+    if (!workspace_ok(workspace, workspace_bytes,
+                      kda_paged_decode_q8_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype)))
         return KDA_ERR_INVALID_ARG;
     kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
                        seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
@@ -280,10 +285,9 @@ kda_status_t kda_pages_resize(int32_t *page_table, int num_rows, int max_pages, 
     if (num_rows < 0 || max_pages < 0 || num_pages < 0) return KDA_ERR_INVALID_ARG;
     if (page_shift(page_size) < 0 || !table_ok(num_rows, max_pages)) return KDA_ERR_UNSUPPORTED;
     if (num_rows == 0) return KDA_OK;
-    if (!held || !tokens || (max_pages > 0 && !page_table) || (num_pages > 0 && (!refs || !workspace)))
-        return KDA_ERR_INVALID_ARG;
-    if (!words(page_table, held, refs, tokens, status) || !aligned(workspace, 16) ||
-        workspace_bytes < kda::pages_resize_workspace_bytes(num_pages))
+    if (!held || !tokens || (max_pages > 0 && !page_table) || (num_pages > 0 && !refs)) return KDA_ERR_INVALID_ARG;
+    if (!words(page_table, held, refs, tokens, status) ||
+        !workspace_ok(workspace, workspace_bytes, kda::pages_resize_workspace_bytes(num_pages)))
         return KDA_ERR_INVALID_ARG;
     const kda::PageTable p{page_table, num_rows, max_pages, held, refs, num_pages, page_shift(page_size), status};
     return from_cuda(kda::launch_pages_resize(p, tokens, workspace, reinterpret_cast<cudaStream_t>(stream)));

@@ -508,7 +508,7 @@ static int grid_q8(int N, int64_t max_tokens, int Hkv, int G) {
 
 size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
     const size_t simt = paged_decode_workspace_bytes(N, max_tokens, Hq, Hkv, d);
-    if (max_tokens <= kTile) return simt;
+    if (max_tokens <= kTile) return 0;            // (an item is one tile in either form: nothing to join)
     const int G = Hq / Hkv;
     const size_t tc = sizeof(float) * grid_q8(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_q8(G));
     return tc > simt ? tc : simt;

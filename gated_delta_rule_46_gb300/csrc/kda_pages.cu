@@ -29,6 +29,7 @@ struct Scan {
 };
 struct Ranks {
     int before, total;              // in the warps before this one; in all
+    int cta;                        // in the CTAs before this one
 };
 
 __device__ __forceinline__ int lanes_before(int x, int lane, int &sum) {
@@ -48,7 +49,7 @@ __device__ Ranks scan_cta(Scan &s, int mine) {
     __syncthreads();
     if (lane == 0) s.warp_sum[warp] = mine;
     __syncthreads();
-    Ranks r;
+    Ranks r{};
     const int x = lanes_before(s.warp_sum[lane], lane, r.total);
     r.before = __shfl_sync(0xffffffffu, x, warp);
     return r;
@@ -66,9 +67,10 @@ __device__ Ranks scan_cluster(Scan &s, int mine, int &turn) {
     r.total = 0;
 #pragma unroll
     for (int i = 0; i < CL; ++i) {
-        if (i < rank) r.before += all[i];
+        if (i < rank) r.cta += all[i];
         r.total += all[i];
     }
+    r.before += r.cta;
     return r;
 }
 
@@ -92,29 +94,58 @@ struct Flat {
     }
 };
 
-// The lowest pages that no one holds, up to `need` of them, into list; how many there are.  Cluster-wide.
-__device__ int take_free(const PageTable &p, int need, int32_t *list, Scan &s, int &turn) {
+// A list that the whole cluster writes and reads: in its CTAs' shared memory, or in device memory where it is longer.
+constexpr int kListShift = 13;                    // entries of a CTA
+constexpr int kListMost = CL << kListShift;
+struct List {
+    int32_t *device, *shared;                     // (shared: at the same place in every CTA, or null)
+    __device__ void put(int i, int x) const {
+        if (shared)
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(
+                             ptx::map_to_rank(shared + (i & ((1 << kListShift) - 1)), i >> kListShift)), "r"(x) : "memory");
+        else
+            device[i] = x;
+    }
+    __device__ int get(int i) const {
+        if (!shared) return ldcg(device + i);
+        int x;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                     : "=r"(x)
+                     : "r"(ptx::map_to_rank(shared + (i & ((1 << kListShift) - 1)), i >> kListShift))
+                     : "memory");
+        return x;
+    }
+};
+
+// The lowest pages that no one holds, up to `need` of them, into list; how many there are.  Cluster-wide.  A warp looks
+// at up to 1024 pages in a row at a time, and lane j keeps which of the j-th 32 are free: one sum over the cluster for
+// up to 262,144 pages.
+__device__ int take_free(const PageTable &p, int need, const List &list, Scan &s, int &turn) {
     constexpr int J = 8;                          // loads under way per thread
     const int lane = threadIdx.x & 31, gw = (int)ptx::cluster_rank() * NW + (threadIdx.x >> 5);
+    const int groups = min(32, (int)(((int64_t)p.num_pages + CL * NW * 32 - 1) / (CL * NW * 32)));
     int found = 0;
-    for (int64_t p0 = 0; p0 < p.num_pages && found < need; p0 += CL * NW * 32 * J) {
-        const int64_t at = p0 + gw * (32 * J) + lane;
-        unsigned b[J];
-        int count = 0;
+    for (int64_t p0 = 0; p0 < p.num_pages && found < need; p0 += CL * NW * 32 * groups) {
+        const int64_t at = p0 + (int64_t)gw * 32 * groups + lane;
+        unsigned mine = 0;
+        for (int g = 0; g < groups; g += J) {
+            bool b[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) b[j] = at + j * 32 < p.num_pages ? ldcg(p.refs + at + j * 32) == 0 : 0;
+            for (int j = 0; j < J; ++j)
+                b[j] = g + j < groups && at + (g + j) * 32 < p.num_pages && ldcg(p.refs + at + (g + j) * 32) == 0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            b[j] = __ballot_sync(0xffffffffu, b[j]);
-            count += __popc(b[j]);
+            for (int j = 0; j < J; ++j) {
+                const unsigned x = __ballot_sync(0xffffffffu, b[j]);
+                if (lane == g + j) mine = x;
+            }
         }
-        const Ranks r = scan_cluster(s, count, turn);
-        int k = found + r.before;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int mine = k + __popc(b[j] & ((1u << lane) - 1));
-            if ((b[j] >> lane & 1) && mine < need) list[mine] = (int)(at + j * 32);
-            k += __popc(b[j]);
+        int sum;
+        const int before = lanes_before(__popc(mine), lane, sum);
+        const Ranks r = scan_cluster(s, sum, turn);
+        for (int g = 0; g < groups; ++g) {
+            const unsigned b = __shfl_sync(0xffffffffu, mine, g);
+            const int k = found + r.before + __shfl_sync(0xffffffffu, before, g) + __popc(b & ((1u << lane) - 1));
+            if ((b >> lane & 1) && k < need) list.put(k, (int)(at + g * 32));
         }
         found += r.total;
     }
@@ -149,9 +180,12 @@ __device__ __forceinline__ Change change(const PageTable &p, const int32_t *toke
     return {held, want};
 }
 
-__global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, const int32_t *tokens, int32_t *list) {
+__global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, const int32_t *tokens, int32_t *workspace) {
+    constexpr int U = 8;                          // pages under way per thread
     __shared__ Scan s;
     __shared__ Flat flat;
+    __shared__ int s_first[NT];                   // each row's first entry that changes
+    __shared__ int32_t s_list[1 << kListShift];
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     ptx::cluster_sync();                          // all CTAs are there to be written to
@@ -164,16 +198,27 @@ __global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, 
     for (int64_t c = r0; c < r1; c += NT) {
         Change x{0, 0};
         if (c + tid < r1) x = change(p, tokens, (int)(c + tid), true);
+        __syncthreads();                          // (the rows before are done with)
+        s_first[tid] = x.want;
         const int total = flat.fill(s, max(0, x.held - x.want));
-        for (int i = tid; i < total; i += NT) {
-            const int row = flat.row(i);
-            const int64_t r = c + row;
-            const int e = change(p, tokens, (int)r, false).want + i - flat.before[row];
-            int32_t *entry = p.table + r * p.max_pages + e;
-            give_back(p, *entry);
-            *entry = -1;
+        for (int i0 = tid; i0 < total; i0 += U * NT) {
+            int id[U];
+            int32_t *entry[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * NT;
+                if (i >= total) break;
+                const int row = flat.row(i);
+                entry[u] = p.table + (c + row) * p.max_pages + s_first[row] + i - flat.before[row];
+                id[u] = *entry[u];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u * NT >= total) break;
+                *entry[u] = -1;
+                give_back(p, id[u]);
+            }
         }
-        __syncthreads();                          // (held is read above)
         if (x.want < x.held) p.held[c + tid] = x.want;
         int sum;
         lanes_before(max(0, x.want - x.held), tid & 31, sum);
@@ -181,28 +226,84 @@ __global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, 
     }
     const Ranks all = scan_cluster(s, need, turn);
     if (all.total == 0) return;                   // (the same in all CTAs)
-    const Ranks cta = scan_cta(s, need);
-    int base = all.before - cta.before;           // needed by the CTAs before this one
+    int base = all.cta;                           // needed by the CTAs before this one
+    const List list{workspace, min(all.total, p.num_pages) <= kListMost ? s_list : nullptr};
     const int got = take_free(p, all.total, list, s, turn);
 
     for (int64_t c = r0; c < r1; c += NT) {
         Change x{0, 0};
         if (c + tid < r1) x = change(p, tokens, (int)(c + tid), false);
-        const int mine = max(0, x.want - x.held), total = flat.fill(s, mine);
-        for (int i = tid; i < total && base + i < got; i += NT) {
-            const int row = flat.row(i);
-            const int64_t r = c + row;
-            const int page = ldcg(list + base + i);
-            p.table[r * p.max_pages + ldcg(p.held + r) + i - flat.before[row]] = page;
-            p.refs[page] = 1;
+        __syncthreads();
+        s_first[tid] = x.held;
+        const int mine = max(0, x.want - x.held), total = flat.fill(s, mine), most = min(total, got - base);
+        for (int i0 = tid; i0 < most; i0 += U * NT) {
+            int page[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * NT < most) page[u] = list.get(base + i0 + u * NT);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * NT;
+                if (i >= most) break;
+                const int row = flat.row(i);
+                p.table[(c + row) * p.max_pages + s_first[row] + i - flat.before[row]] = page[u];
+                p.refs[page[u]] = 1;
+            }
         }
-        __syncthreads();                          // (held is read above)
         if (mine > 0) {
             const int have = min(mine, max(0, got - base - flat.before[tid]));
             if (have < mine) report_status(p.status, KDA_ERR_NO_PAGES);
             p.held[c + tid] = x.held + have;
         }
         base += total;
+    }
+    ptx::cluster_sync();                          // (the others read this CTA's part of the list)
+}
+
+// ---------------------------------------------------------------------------
+// Copies of pages in all pools, a unit of up to 16 KB of one page at a time.  Sources
+// are pages in use and destinations free ones, so no order is needed.
+// ---------------------------------------------------------------------------
+constexpr int kUnit = 16384, kCopyThreads = 256;
+constexpr int64_t kMostAtOnce = 1 << 19;          // bytes of pages that the planning kernel copies by itself
+
+
+// By T threads, with U loads under way in each.
+template <typename V, int T, int U>
+__device__ __forceinline__ void copy_unit(uint8_t *dst, const uint8_t *src, int bytes, int thread) {
+    const int n = bytes / (int)sizeof(V);
+    for (int i0 = thread; i0 < n; i0 += U * T) {
+        V x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * T < n) x[u] = reinterpret_cast<const V *>(src)[i0 + u * T];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * T < n) reinterpret_cast<V *>(dst)[i0 + u * T] = x[u];
+    }
+}
+
+// The part of group `group` of `groups` groups of T threads.
+template <int T, int U>
+__device__ __forceinline__ void copy_pages(const Pools &pools, const int32_t *from, const int32_t *to, int count, int group,
+                                           int groups) {
+    const int per = pools.first[pools.n], thread = threadIdx.x % T;
+    for (int64_t u = group; u < (int64_t)count * per; u += groups) {
+        const int pair = (int)(u / per), at = (int)(u - (int64_t)pair * per);
+        int lo = 0, hi = pools.n;                 // the pool of the unit
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pools.first[mid] <= at) lo = mid; else hi = mid;
+        }
+        const int64_t size = pools.bytes[lo], off = (int64_t)(at - pools.first[lo]) * kUnit;
+        uint8_t *base = pools.base[lo];
+        uint8_t *dst = base + ldcg(to + pair) * size + off;
+        const uint8_t *src = base + ldcg(from + pair) * size + off;
+        const int bytes = (int)min((int64_t)kUnit, size - off);
+        const uint64_t odd = reinterpret_cast<uint64_t>(base) | (uint64_t)size;
+        if (odd % 16 == 0) copy_unit<uint4, T, U>(dst, src, bytes, thread);
+        else if (odd % 4 == 0) copy_unit<uint32_t, T, U>(dst, src, bytes, thread);
+        else copy_unit<uint8_t, T, U>(dst, src, bytes, thread);
     }
 }
 
@@ -234,8 +335,30 @@ __device__ int4 fork_pair(const PageTable &p, const int32_t *lens, const int32_t
     return bad ? make_int4(-1, b, 0, -1) : make_int4(a, b, len, page);
 }
 
+// The destinations' rows of the table, an entry at a time.
+__device__ __forceinline__ void fork_rows(const PageTable &p, int forks, const ForkPlan &f, int64_t thread, int64_t threads) {
+    for (int64_t x = thread; x < (int64_t)forks * p.max_pages; x += threads) {
+        const int i = (int)(x / p.max_pages), e = (int)(x - (int64_t)i * p.max_pages);
+        const int4 r = __ldcg(f.rows + i);
+        if (r.x < 0 || e > r.z || (e == r.z && r.w < 0)) continue;
+        int id = r.w;
+        if (e < r.z) {
+            id = p.table[(int64_t)r.x * p.max_pages + e];
+            if (id >= 0 && id < p.num_pages) {
+                atomicAdd(p.refs + id, 1);
+            } else {
+                report_status(p.status, KDA_ERR_INVALID_ARG);
+                id = -1;
+            }
+        }
+        p.table[(int64_t)r.y * p.max_pages + e] = id;
+    }
+}
+
+// copy: the pools are copied here too.
 __global__ void __launch_bounds__(NT, 1)
-    pages_fork_kernel(const PageTable p, int32_t *lens, const int32_t *src, const int32_t *dst, int forks, const ForkPlan f) {
+    pages_fork_kernel(const __grid_constant__ Pools pools, const PageTable p, int32_t *lens, const int32_t *src,
+                      const int32_t *dst, int forks, const ForkPlan f, bool copy) {
     __shared__ Scan s;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
@@ -261,9 +384,9 @@ __global__ void __launch_bounds__(NT, 1)
         if (c + tid < i1) f.rows[c + tid] = x = fork_pair(p, lens, src, dst, f, (int)(c + tid));
         need += __popc(__ballot_sync(0xffffffffu, x.w >= 0));
     }
-    const Ranks all = scan_cluster(s, need, turn), cta = scan_cta(s, need);
-    int base = all.before - cta.before;
-    const int got = take_free(p, all.total, f.list, s, turn);
+    const Ranks all = scan_cluster(s, need, turn);
+    int base = all.cta;
+    const int got = take_free(p, all.total, List{f.list, nullptr}, s, turn);
     if (rank == 0 && tid == 0) *f.count = got;
     for (int64_t c = i0; c < i1; c += NT) {
         int4 x = make_int4(-1, 0, 0, -1);
@@ -293,6 +416,11 @@ __global__ void __launch_bounds__(NT, 1)
         }
         base += r.total;
     }
+    if (copy) {
+        ptx::cluster_sync();                      // the plan is there for all
+        fork_rows(p, forks, f, rank * NT + tid, CL * NT);
+        copy_pages<64, 8>(pools, f.from, f.to, got, (rank * NT + tid) / 64, CL * NT / 64);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -304,7 +432,20 @@ struct CompactPlan {
     int32_t *map, *live;            // (the caller's)
 };
 
-__global__ void __launch_bounds__(NT, 1) pages_compact_kernel(const PageTable p, const CompactPlan f) {
+// The table, an entry at a time.
+__device__ __forceinline__ void compact_rows(const PageTable &p, const CompactPlan &f, int64_t thread, int64_t threads) {
+    for (int64_t x = thread; x < (int64_t)p.rows * p.max_pages; x += threads) {
+        const int id = p.table[x];
+        if (id < 0) continue;
+        const int to = id < p.num_pages ? ldcg(f.map + id) : -1;
+        if (to < 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+        if (to != id) p.table[x] = to;
+    }
+}
+
+// copy: the pools are copied here too.
+__global__ void __launch_bounds__(NT, 1)
+    pages_compact_kernel(const __grid_constant__ Pools pools, const PageTable p, const CompactPlan f, bool copy) {
     __shared__ Scan s;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
@@ -360,47 +501,11 @@ __global__ void __launch_bounds__(NT, 1) pages_compact_kernel(const PageTable p,
         *f.count = m.total;
         *f.live = live;
     }
-}
-
-// ---------------------------------------------------------------------------
-// Copies of pages in all pools, a unit of up to 16 KB of one page at a time.  Sources
-// are pages in use and destinations free ones, so no order is needed.
-// ---------------------------------------------------------------------------
-constexpr int kUnit = 16384, kCopyThreads = 256;
-
-template <typename V>
-__device__ __forceinline__ void copy_unit(uint8_t *dst, const uint8_t *src, int bytes) {
-    constexpr int U = 4;
-    const int n = bytes / (int)sizeof(V);
-    for (int i0 = threadIdx.x; i0 < n; i0 += U * kCopyThreads) {
-        V x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * kCopyThreads < n) x[u] = reinterpret_cast<const V *>(src)[i0 + u * kCopyThreads];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * kCopyThreads < n) reinterpret_cast<V *>(dst)[i0 + u * kCopyThreads] = x[u];
-    }
-}
-
-__device__ void copy_pages(const Pools &pools, const int32_t *from, const int32_t *to, int count) {
-    const int per = pools.first[pools.n];
-    for (int64_t u = blockIdx.x; u < (int64_t)count * per; u += gridDim.x) {
-        const int pair = (int)(u / per), at = (int)(u - (int64_t)pair * per);
-        int lo = 0, hi = pools.n;                 // the pool of the unit
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pools.first[mid] <= at) lo = mid; else hi = mid;
-        }
-        const int64_t size = pools.bytes[lo], off = (int64_t)(at - pools.first[lo]) * kUnit;
-        uint8_t *base = pools.base[lo];
-        uint8_t *dst = base + to[pair] * size + off;
-        const uint8_t *src = base + from[pair] * size + off;
-        const int bytes = (int)min((int64_t)kUnit, size - off);
-        const uint64_t odd = reinterpret_cast<uint64_t>(base) | (uint64_t)size;
-        if (odd % 16 == 0) copy_unit<uint4>(dst, src, bytes);
-        else if (odd % 4 == 0) copy_unit<uint32_t>(dst, src, bytes);
-        else copy_unit<uint8_t>(dst, src, bytes);
+    if (copy) {
+        ptx::cluster_sync();                      // the plan is there for all
+        const int thread = (int)ptx::cluster_rank() * NT + threadIdx.x;
+        compact_rows(p, f, thread, CL * NT);
+        copy_pages<64, 8>(pools, f.from, f.to, m.total, thread / 64, CL * NT / 64);
     }
 }
 
@@ -409,41 +514,35 @@ __global__ void __launch_bounds__(kCopyThreads)
     pages_fork_copy_kernel(const __grid_constant__ Pools pools, const PageTable p, int forks, const ForkPlan f, bool first) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    if (first)
-        for (int64_t x = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; x < (int64_t)forks * p.max_pages;
-             x += (int64_t)gridDim.x * kCopyThreads) {
-            const int i = (int)(x / p.max_pages), e = (int)(x - (int64_t)i * p.max_pages);
-            const int4 r = f.rows[i];
-            if (r.x < 0 || e > r.z || (e == r.z && r.w < 0)) continue;
-            int id = r.w;
-            if (e < r.z) {
-                id = p.table[(int64_t)r.x * p.max_pages + e];
-                if (id >= 0 && id < p.num_pages) {
-                    atomicAdd(p.refs + id, 1);
-                } else {
-                    report_status(p.status, KDA_ERR_INVALID_ARG);
-                    id = -1;
-                }
-            }
-            p.table[(int64_t)r.y * p.max_pages + e] = id;
-        }
-    copy_pages(pools, f.from, f.to, *f.count);
+    if (first) fork_rows(p, forks, f, (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, (int64_t)gridDim.x * kCopyThreads);
+    copy_pages<kCopyThreads, 4>(pools, f.from, f.to, *f.count, blockIdx.x, gridDim.x);
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
     pages_compact_copy_kernel(const __grid_constant__ Pools pools, const PageTable p, const CompactPlan f, bool first) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    if (first)
-        for (int64_t x = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; x < (int64_t)p.rows * p.max_pages;
-             x += (int64_t)gridDim.x * kCopyThreads) {
-            const int id = p.table[x];
-            if (id < 0) continue;
-            const int to = id < p.num_pages ? f.map[id] : -1;
-            if (to < 0) report_status(p.status, KDA_ERR_INVALID_ARG);
-            if (to != id) p.table[x] = to;
-        }
-    copy_pages(pools, f.from, f.to, *f.count);
+    if (first) compact_rows(p, f, (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, (int64_t)gridDim.x * kCopyThreads);
+    copy_pages<kCopyThreads, 4>(pools, f.from, f.to, *f.count, blockIdx.x, gridDim.x);
+}
+
+Pools some_pools(void *const *base, const int64_t *bytes, int n) {
+    Pools pools{};
+    pools.n = n;
+    for (int i = 0; i < n; ++i) {
+        pools.base[i] = static_cast<uint8_t *>(base[i]);
+        pools.bytes[i] = bytes[i];
+        pools.first[i + 1] = pools.first[i] + (int)((bytes[i] + kUnit - 1) / kUnit);
+    }
+    return pools;
+}
+
+// Up to half a megabyte the planning kernel's eight CTAs copy sooner than a second launch would.
+bool copied_at_once(const int64_t *bytes, int n, int64_t others, int64_t pairs) {
+    if (n > kPoolsPerLaunch || others > (1 << 16)) return false;
+    int64_t page = 0;
+    for (int i = 0; i < n; ++i) page += bytes[i] < kMostAtOnce ? bytes[i] : kMostAtOnce;
+    return page == 0 || pairs <= kMostAtOnce / page;
 }
 
 // Calls launch(pools, grid, first) for all pools, at most kPoolsPerLaunch of them at a time, and once where there are none.
@@ -451,13 +550,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 template <typename F>
 cudaError_t launch_copies(void *const *base, const int64_t *bytes, int n, int64_t others, int64_t pairs, F &&launch) {
     for (int at = 0; at == 0 || at < n; at += kPoolsPerLaunch) {
-        Pools pools{};
-        pools.n = n - at < kPoolsPerLaunch ? n - at : kPoolsPerLaunch;
-        for (int i = 0; i < pools.n; ++i) {
-            pools.base[i] = static_cast<uint8_t *>(base[at + i]);
-            pools.bytes[i] = bytes[at + i];
-            pools.first[i + 1] = pools.first[i] + (int)((bytes[at + i] + kUnit - 1) / kUnit);
-        }
+        const Pools pools = some_pools(base + at, bytes + at, n - at < kPoolsPerLaunch ? n - at : kPoolsPerLaunch);
         const int64_t units = pairs * pools.first[pools.n], work = (others + kCopyThreads - 1) / kCopyThreads;
         const int64_t most = units > work ? units : work, room = (int64_t)sm_count() * 8;
         const cudaError_t e = launch(pools, dim3((unsigned)(most < 1 ? 1 : (most < room ? most : room))), at == 0);
@@ -470,7 +563,7 @@ size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
 
 }  // namespace
 
-size_t pages_resize_workspace_bytes(int num_pages) { return up16(4 * (size_t)num_pages); }
+size_t pages_resize_workspace_bytes(int num_pages) { return num_pages <= kListMost ? 0 : up16(4 * (size_t)num_pages); }
 
 cudaError_t launch_pages_resize(const PageTable &p, const int32_t *tokens, void *workspace, cudaStream_t st) {
     return launch_dependent(pages_resize_kernel, dim3(CL), NT, 0, st, CL, p, tokens, static_cast<int32_t *>(workspace));
@@ -495,8 +588,10 @@ cudaError_t launch_pages_fork(void *const *pools, const int64_t *page_bytes, int
     f.from = piece(4 * (size_t)forks);
     f.to = piece(4 * (size_t)forks);
     f.rows = reinterpret_cast<int4 *>(piece(16 * (size_t)forks));
-    const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(CL), NT, 0, st, CL, p, lens, src, dst, forks, f);
-    if (e != cudaSuccess) return e;
+    const bool once = copied_at_once(page_bytes, num_pools, (int64_t)forks * p.max_pages, forks);
+    const Pools now = some_pools(pools, page_bytes, once ? num_pools : 0);
+    const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(CL), NT, 0, st, CL, now, p, lens, src, dst, forks, f, once);
+    if (e != cudaSuccess || once) return e;
     return launch_copies(pools, page_bytes, num_pools, (int64_t)forks * p.max_pages, forks,
                          [&](const Pools &some, dim3 grid, bool first) {
                              return launch_dependent(pages_fork_copy_kernel, grid, kCopyThreads, 0, st, 1, some, p, forks, f,
@@ -515,9 +610,12 @@ cudaError_t launch_pages_compact(void *const *pools, const int64_t *page_bytes, 
     f.to = reinterpret_cast<int32_t *>(w + 16 + up16(4 * (size_t)p.num_pages));
     f.map = page_map;
     f.live = live;
-    const cudaError_t e = launch_dependent(pages_compact_kernel, dim3(CL), NT, 0, st, CL, p, f);
-    if (e != cudaSuccess) return e;
-    return launch_copies(pools, page_bytes, num_pools, (int64_t)p.rows * p.max_pages, p.num_pages,
+    // (no more pages move than half of them)
+    const bool once = copied_at_once(page_bytes, num_pools, (int64_t)p.rows * p.max_pages, p.num_pages / 2);
+    const Pools now = some_pools(pools, page_bytes, once ? num_pools : 0);
+    const cudaError_t e = launch_dependent(pages_compact_kernel, dim3(CL), NT, 0, st, CL, now, p, f, once);
+    if (e != cudaSuccess || once) return e;
+    return launch_copies(pools, page_bytes, num_pools, (int64_t)p.rows * p.max_pages, p.num_pages / 2,
                          [&](const Pools &some, dim3 grid, bool first) {
                              return launch_dependent(pages_compact_copy_kernel, grid, kCopyThreads, 0, st, 1, some, p, f, first);
                          });

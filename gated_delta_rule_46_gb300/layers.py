@@ -14,6 +14,7 @@ call may be dropped before the call has run.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -44,6 +45,7 @@ _fns: dict = {}
 # torch's current stream of a device as an integer, without building a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _fn(name):
@@ -117,10 +119,9 @@ def _code(dtype, name):
     return c
 
 
+@functools.lru_cache(maxsize=4096)
 def _size(name, device, *args):
     """Workspace bytes on `device`, whose number of SMs they depend on."""
-    if device.index == torch.cuda.current_device():
-        return _fn(name)(*args)
     with torch.cuda.device(device):
         return _fn(name)(*args)
 
@@ -138,7 +139,7 @@ def _call(name, device, stream, outputs, *args):
         if raw != _raw_stream(index):
             for t in outputs:
                 t.record_stream(torch.cuda.current_stream(device))
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = _fn(name)(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -367,22 +368,30 @@ def paged_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
     P, ps, block, kp, vp, ksp, vsp = _cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
     cols = _dims(page_table, "page_table", 2)[1]
     tp = _dense(page_table, "page_table", (N, cols), torch.int32, dev)
-    new = []
+    new, lsep, wp = [], None, None
     if out is None:
         out = _empty(stream, (N, Hq, d), dt, dev)
+        outp = out.data_ptr()
         new.append(out)
-    if lse is None and return_lse:
+    else:
+        outp = _dense(out, "out", (N, Hq, d), dt, dev)
+    if lse is not None:
+        lsep = _dense(lse, "lse", (N, Hq), torch.float32, dev)
+    elif return_lse:
         lse = _empty(stream, (N, Hq), torch.float32, dev)
+        lsep = lse.data_ptr()
         new.append(lse)
-    if workspace is None:
+    if workspace is not None:
+        size = _dims(workspace, "workspace", 1)[0]
+        wp = _dense(workspace, "workspace", (size,), torch.uint8, dev)
+    else:
         size = _size("kda_paged_decode_q8_workspace_size", dev, N, cols * ps, Hq, Hkv, d, code)
-        workspace = _empty(stream, size, torch.uint8, dev)
-    size = _dims(workspace, "workspace", 1)[0]
+        if size:
+            workspace = _empty(stream, size, torch.uint8, dev)
+            wp = workspace.data_ptr()
     _call("kda_paged_decode_q8", dev, stream, new, q.data_ptr(), ldq, kp, vp, ksp, vsp, P, ps, block, tp, cols,
           _dense(seq_lens, "seq_lens", (N,), torch.int32, dev), N, Hq, Hkv, d, code,
-          d ** -0.5 if scale is None else scale, _dense(out, "out", (N, Hq, d), dt, dev),
-          _dense(lse, "lse", (N, Hq), torch.float32, dev), _dense(workspace, "workspace", (size,), torch.uint8, dev),
-          size, _status(status, dev))
+          d ** -0.5 if scale is None else scale, outp, lsep, wp, size, _status(status, dev))
     if stream is not None:
         _record(stream, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, lse, workspace, status)
     return (out, lse) if return_lse else out

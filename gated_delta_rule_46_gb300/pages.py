@@ -9,12 +9,12 @@ it is 0).  Checks, streams and errors are as in ``layers``.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 
 import torch
 
 from .kda import _empty, _record
-from .layers import _call, _cuda, _dense, _dims, _fn, _status
+from .layers import _call, _cuda, _dense, _dims, _size, _status
 
 
 def _state(page_table, held, refs):
@@ -27,8 +27,16 @@ def _state(page_table, held, refs):
 
 
 def _pools(pools, P, dev):
-    """Host arrays of the pools' addresses and of the bytes of a page in each."""
-    ptrs, sizes = (ctypes.c_void_p * len(pools))(), (ctypes.c_int64 * len(pools))()
+    """The pools' addresses and the bytes of a page in each, as arrays on the host."""
+    index = dev.index
+    for t in pools:
+        if not (type(t) is torch.Tensor and t.get_device() == index and t.is_contiguous() and t.dim() and t.shape[0] == P):
+            _check_pools(pools, P, dev)
+            break
+    return array("Q", [t.data_ptr() for t in pools]), array("q", [t.nbytes // P if P else 0 for t in pools])
+
+
+def _check_pools(pools, P, dev):
     for i, t in enumerate(pools):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"pools[{i}] must be a torch.Tensor")
@@ -38,16 +46,18 @@ def _pools(pools, P, dev):
             raise ValueError(f"pools[{i}] has shape {tuple(t.shape)}, expected {P} pages")
         if not t.is_contiguous():
             raise ValueError(f"pools[{i}] must be contiguous")
-        ptrs[i] = t.data_ptr()
-        sizes[i] = t.numel() // P * t.element_size() if P else 0
-    return ptrs, sizes
 
 
 def _workspace(workspace, name, stream, dev, *sizes):
-    if workspace is None:
-        workspace = _empty(stream, int(_fn(name)(*sizes)), torch.uint8, dev)
-    n = _dims(workspace, "workspace", 1)[0]
-    return workspace, _dense(workspace, "workspace", (n,), torch.uint8, dev), n
+    """The workspace (a new one for None, where one is needed), its pointer and its bytes."""
+    if workspace is not None:
+        n = _dims(workspace, "workspace", 1)[0]
+        return workspace, _dense(workspace, "workspace", (n,), torch.uint8, dev), n
+    n = _size(name, dev, *sizes)
+    if n == 0:
+        return None, None, 0
+    workspace = _empty(stream, n, torch.uint8, dev)
+    return workspace, workspace.data_ptr(), n
 
 
 def pages_resize(page_table, held, refs, tokens, page_size, workspace=None, status=None, stream=None):
@@ -69,7 +79,7 @@ def pages_fork(pools, page_table, held, refs, lens, src, dst, page_size, workspa
     F = _dims(src, "src", 1)[0]
     ptrs, sizes = _pools(pools, P, dev)
     workspace, wp, size = _workspace(workspace, "kda_pages_fork_workspace_size", stream, dev, N, cols, F)
-    _call("kda_pages_fork", dev, stream, (), ptrs, sizes, len(pools), tp, N, cols, hp, rp, P,
+    _call("kda_pages_fork", dev, stream, (), ptrs.buffer_info()[0], sizes.buffer_info()[0], len(pools), tp, N, cols, hp, rp, P,
           _dense(lens, "lens", (N,), torch.int32, dev), _dense(src, "src", (F,), torch.int32, dev),
           _dense(dst, "dst", (F,), torch.int32, dev), F, page_size, wp, size, _status(status, dev))
     if stream is not None:
@@ -86,15 +96,20 @@ def pages_compact(pools, page_table, refs, page_map=None, live=None, workspace=N
     new = []
     if page_map is None:
         page_map = _empty(stream, (P,), torch.int32, dev)
+        mp = page_map.data_ptr()
         new.append(page_map)
+    else:
+        mp = _dense(page_map, "page_map", (P,), torch.int32, dev)
     if live is None:
         live = _empty(stream, (1,), torch.int32, dev)
+        lp = live.data_ptr()
         new.append(live)
+    else:
+        lp = _dense(live, "live", (1,), torch.int32, dev)
     workspace, wp, size = _workspace(workspace, "kda_pages_compact_workspace_size", stream, dev, P)
-    _call("kda_pages_compact", dev, stream, new, ptrs, sizes, len(pools),
+    _call("kda_pages_compact", dev, stream, new, ptrs.buffer_info()[0], sizes.buffer_info()[0], len(pools),
           _dense(page_table, "page_table", (N, cols), torch.int32, dev), N, cols,
-          _dense(refs, "refs", (P,), torch.int32, dev), P, _dense(page_map, "page_map", (P,), torch.int32, dev),
-          _dense(live, "live", (1,), torch.int32, dev), wp, size, _status(status, dev))
+          _dense(refs, "refs", (P,), torch.int32, dev), P, mp, lp, wp, size, _status(status, dev))
     if stream is not None:
         _record(stream, *pools, page_table, refs, page_map, live, workspace, status)
     return page_map, live

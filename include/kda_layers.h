@@ -208,7 +208,8 @@ kda_status_t kda_paged_append_q8(const void *k, int64_t ldk, const void *v, int6
                                  int64_t total_tokens, int Hkv, int d, kda_dtype_t dtype,
                                  uint32_t *status, kda_stream_t stream);
 
-/* Workspace of kda_paged_decode_q8, as kda_paged_decode_workspace_size. */
+/* Workspace of kda_paged_decode_q8, as kda_paged_decode_workspace_size; none (0, and the
+ * workspace may be NULL) where max_tokens is at most 64. */
 size_t kda_paged_decode_q8_workspace_size(int num_seqs, int64_t max_tokens, int Hq, int Hkv, int d,
                                           kda_dtype_t dtype);
 

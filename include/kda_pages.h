@@ -35,7 +35,8 @@
 extern "C" {
 #endif
 
-/* Workspace bytes of kda_pages_resize; 0 for sizes that it refuses. */
+/* Workspace bytes of kda_pages_resize: 0 (and the workspace may be NULL) for pools of up to 65536 pages, and for sizes
+ * that it refuses. */
 size_t kda_pages_resize_workspace_size(int num_rows, int max_pages, int num_pages);
 
 /*

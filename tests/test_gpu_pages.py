@@ -284,7 +284,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         pages_resize(table.t(), i(4), refs, i(4), 16)
     with pytest.raises(KDAError):
-        pages_resize(table, held, refs, i(3), 16, workspace=torch.zeros(8, dtype=torch.uint8, device=dev))
+        pages_resize(table, held, i(70000), i(3), 16, workspace=torch.zeros(8, dtype=torch.uint8, device=dev))
     pool = torch.zeros(9, 4, device=dev)
     for bad in (pool[:8], pool.cpu(), pool.t().contiguous().t()):
         with pytest.raises(ValueError):

@@ -53,7 +53,7 @@ def _resize(**kw):
 
 @pytest.mark.parametrize("kw,want", [(dict(n=-1), INV), (dict(P=-1), INV), (dict(ps=3), UNS), (dict(ps=2048), UNS), (dict(n=0), OK),
                                      (dict(held=None), INV), (dict(refs=None), INV), (dict(tokens=A + 2), INV),
-                                     (dict(ws=A + 8), INV), (dict(wsb=35), INV), (dict(ws=None), INV), (dict(table=None), INV),
+                                     (dict(ws=A + 8), INV), (dict(wsb=4 * 70000 - 1, P=70000), INV), (dict(ws=None, P=70000), INV), (dict(table=None), INV),
                                      (dict(n=1 << 16, cols=1 << 15), UNS)])
 def test_resize(kw, want):
     assert _resize(**kw) == want
@@ -96,12 +96,14 @@ def test_compact(kw, want):
 
 def test_workspace_sizes():
     size = lambda name, *a: layers._fn(name)(*a)  # noqa: E731
-    assert size("kda_pages_resize_workspace_size", 4, 5, 1000) >= 4000
+    assert size("kda_pages_resize_workspace_size", 4, 5, 65537) >= 4 * 65537
+    assert size("kda_pages_resize_workspace_size", 4, 5, 65536) == 0
     assert size("kda_pages_resize_workspace_size", 1 << 16, 1 << 15, 9) == 0
     assert size("kda_pages_fork_workspace_size", 10, 5, 7) > 0 and size("kda_pages_fork_workspace_size", 10, 5, -1) == 0
     assert size("kda_pages_compact_workspace_size", 1000) >= 8000 and size("kda_pages_compact_workspace_size", -1) == 0
     ws = layers.paged_decode_q8_workspace_size
     assert ws(4, 1000, 8, 2, 128) > 0 and ws(4, 1000, 8, 3, 128) == 0 and ws(0, 1000, 8, 2, 128) == 0
+    assert ws(4, 64, 8, 2, 128) == 0 and ws(4, 65, 8, 2, 128) > 0
 
 
 def test_status_string():
