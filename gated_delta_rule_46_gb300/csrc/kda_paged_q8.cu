@@ -42,6 +42,14 @@ struct Row8 {
             u[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
         }
     }
+    // The largest magnitude's bits, of two values in halves for bf16, and as a float's at the end: what is not finite is
+    // larger than what is.  (Two instructions for two bf16, where a comparison with infinity takes six.)
+    __device__ void top(uint32_t &m) const {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i) m = sizeof(T) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+    }
+    static __device__ uint32_t joined(uint32_t m) { return sizeof(T) == 4 ? m : max(m << 16, m & 0xffff0000u); }
     __device__ void get(float (&x)[8]) const {
         if constexpr (sizeof(T) == 4) {
             const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
@@ -58,13 +66,17 @@ struct Row8 {
     }
 };
 
+// ODD: infinities, which a saturating conversion takes for large numbers, become NaN.
+template <bool ODD>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (a saturating conversion takes infinities for large numbers)
-        const float a = fabsf(x[2 * i]) < INFINITY ? x[2 * i] * inv : NAN;
-        const float b = fabsf(x[2 * i + 1]) < INFINITY ? x[2 * i + 1] * inv : NAN;
+        float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+        if constexpr (ODD) {
+            if (!(fabsf(x[2 * i]) < INFINITY)) a = NAN;
+            if (!(fabsf(x[2 * i + 1]) < INFINITY)) b = NAN;
+        }
         c[i] = f2_to_e4m3x2(a, b);
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
@@ -99,9 +111,17 @@ __device__ __forceinline__ Seq sequence(const AppendQ8Params &p, int i) {
 }
 
 // One unit is a block of a sequence, a head, and keys or values; the units of all sequences in order are dealt out evenly.
-// B / 16 warps share a unit, 16 tokens each.
+// B / 16 warps share a unit, 16 tokens each; the one token of a sequence without cu_seqlens is one warp's.
+//
+// Instructions bound it next to HBM: what a value costs is kept to two and a half (its share of a maximum over the bits of
+// two values at a time, half a multiplication's and a conversion's), and registers to what lets as many CTAs run as these
+// need to overlap: 131k tokens of 8 heads of 128 channels take 131 us (6.2 TB/s) with three CTAs of an SM, 145 with two,
+// 151 with four; float32 108 with two, 133 with three.  Copying a warp's next units to shared memory ahead gains nothing.
+template <typename T, int D>
+constexpr int kCtas = ROWS * D * sizeof(T) > 4096 ? 2 : ROWS * D * sizeof(T) > 2048 ? 3 : 4;
+
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const AppendQ8Params p) {
+__global__ void __launch_bounds__(WARPS * 32, kCtas<T, D>) paged_append_q8_kernel(const AppendQ8Params p) {
     constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = ROWS / RPS;        // lanes per row, rows per step, steps
     __shared__ int64_t s_sum[WARPS + 1];
     __shared__ int s_n;
@@ -109,7 +129,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tasks = 2 * p.Hkv, share = (1 << p.block_shift) / ROWS;     // warps of a unit
+    const int tasks = 2 * p.Hkv, share = p.cu_seqlens ? (1 << p.block_shift) / ROWS : 1;      // warps of a unit
     const int per = WARPS / share, mine = warp / share, part = warp % share;
 
     // ---- this CTA's units [u0, u1), the sequence in which they start and the blocks before it
@@ -170,7 +190,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
     if (blk < total) s = sequence(p, n);
     if (!p.cu_seqlens) s.blocks = 1;                  // (of a malformed one too: a sequence is its own block here)
 
-    const int row0 = part * ROWS + lane / LPR, ch = (lane % LPR) * 8;     // first row of the block, first channel
+    const int lane_row = lane / LPR, ch = (lane % LPR) * 8;
     const T *in[2] = {static_cast<const T *>(p.k), static_cast<const T *>(p.v)};
     const int ps = 1 << p.page_shift;
     for (int64_t u = u0, round = 0; u < u1; u += per, ++round) {
@@ -178,6 +198,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
         int from = 0, to = 0;
         int64_t at = 0;                               // its first row in the cache
         float was = 0.f;
+        int row0 = part * ROWS + lane_row;            // this lane's first row
         const bool v = task >= p.Hkv;
         const int h = v ? task - p.Hkv : task;
         Row8<T, VEC> x[STEPS];
@@ -193,6 +214,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
             if (page >= 0 && page < p.num_pages) {
                 from = max(s.start - pos, 0);
                 to = min(1 << p.block_shift, s.start + s.n - pos);
+                if (!p.cu_seqlens) row0 = (from & ~(ROWS - 1)) + lane_row;
                 at = (((int64_t)page * p.Hkv + h) << p.page_shift) + (pos & (ps - 1));
                 if (from > 0) was = (v ? p.vs : p.ks)[at >> p.block_shift];
                 const T *src = in[v] + ((int64_t)s.t0 + pos - s.start) * (v ? p.ldv : p.ldk) + (int64_t)h * D + ch;
@@ -206,16 +228,23 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
             }
         }
         // ---- its largest finite value, and the scale
-        float amax = 0.f;
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            float f[8];
-            x[i].get(f);
+        for (int i = 0; i < STEPS; ++i) x[i].top(top);
+        top = __reduce_max_sync(0xffffffffu, Row8<T, VEC>::joined(top));
+        const bool odd = top >= 0x7f800000u;          // (the same in all lanes)
+        float amax = __uint_as_float(top);
+        if (odd) {
+            amax = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]) < INFINITY ? fabsf(f[e]) : 0.f);
+            for (int i = 0; i < STEPS; ++i) {
+                float f[8];
+                x[i].get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]) < INFINITY ? fabsf(f[e]) : 0.f);
+            }
+            amax = ptx::warp_max(amax);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (share > 1) {
             if (lane == 0) s_max[round & 1][warp] = amax;
             __syncthreads();
@@ -242,12 +271,18 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
                 float f[8];
                 if (r >= from && r < to) {
                     x[i].get(f);
-                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8(f, inv);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = odd ? encode8<true>(f, inv) : encode8<false>(f, inv);
                 } else if (again && r < from) {
                     decode8(*reinterpret_cast<const uint2 *>(dst + r * D), f);
-                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8(f, was * inv);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8<true>(f, was * inv);
                 }
             }
+            if (again && !p.cu_seqlens)               // what lies before this warp's rows
+                for (int r = lane_row; r < row0 - lane_row; r += RPS) {
+                    float f[8];
+                    decode8(*reinterpret_cast<const uint2 *>(dst + r * D), f);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8<true>(f, was * inv);
+                }
             if (lane == 0 && part == 0) (v ? p.vs : p.ks)[at >> p.block_shift] = scale;
         }
         for (task += per; task >= tasks; task -= tasks) ++blk;
@@ -256,10 +291,10 @@ __global__ void __launch_bounds__(WARPS * 32) paged_append_q8_kernel(const Appen
 
 template <typename T, int D, bool VEC>
 cudaError_t launch(const AppendQ8Params &p, cudaStream_t st) {
-    const int B = 1 << p.block_shift, per = WARPS / (B / ROWS);
+    const int B = 1 << p.block_shift, per = p.cu_seqlens ? WARPS / (B / ROWS) : WARPS;
     // at most two blocks of a sequence are not whole
     const int64_t blocks = p.cu_seqlens ? p.total / B + 2 * (int64_t)min((int64_t)p.num_seqs, p.total) : p.num_seqs;
-    const int64_t most = (blocks * 2 * p.Hkv + per - 1) / per, room = (int64_t)sm_count() * 4;
+    const int64_t most = (blocks * 2 * p.Hkv + per - 1) / per, room = (int64_t)sm_count() * kCtas<T, D>;
     return launch_dependent(paged_append_q8_kernel<T, D, VEC>, dim3((unsigned)(most < room ? most : room)), WARPS * 32, 0, st, 1,
                             p);
 }

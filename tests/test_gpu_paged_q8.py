@@ -158,6 +158,37 @@ def test_append_scale_of_a_partly_filled_block():
         ref.same("codes", got[0], want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,B", [(128, 128), (64, 64), (32, 32), (128, 16)])
+def test_append_one_token_rescales_its_block(dtype, d, B):
+    """A token anywhere in a block whose scale it outgrows, and in one that it does not."""
+    dev = need_gpu()
+    start = [0, 1, 5, 15, 16, 17, 31, 32, 47, 63, 64, 100, 111, 112, 126, 127]
+    n = len(start)
+    k, v, kc, vc, ks, vs, table = _case(dtype, 2, d, 128, B, [1] * n, start, d + B)
+    ks, vs = ks * 2.0 ** -6, vs * torch.exp2(torch.arange(vs.shape[0]) % 2 * 8.0 - 6)[:, None, None]
+    _append(k, v, kc, vc, ks, vs, table, start, [1] * n, dev, one=True)
+
+
+def test_append_bf16_that_is_not_finite():
+    """Infinities and NaN in bf16 blocks of one token, of some and of all of a block's warps."""
+    dev = need_gpu()
+    d, ps, n = 64, 64, 64
+    g = torch.Generator().manual_seed(5)
+    for B in (16, 64):
+        x = torch.randn(3 * n, 1, d, generator=g).to(BF)
+        x[3, 0, 7], x[20, 0, 63], x[40, 0, 0], x[41] = math.inf, -math.inf, math.nan, math.nan
+        x[64:128] = math.nan
+        x[130, 0, 2], x[131] = 2.0 ** -133, 3e38
+        kc, ks = _codes(4, 1, ps, d, B, 2)
+        table = torch.arange(3, dtype=torch.int32)[None]
+        _append(x, x.flip(0).contiguous(), kc, kc, ks, ks, table, [0], [3 * n], dev)
+        rows = x[[0, 3, 20, 41, 130, 131]].contiguous()
+        six = torch.arange(6, dtype=torch.int32)[:, None].contiguous()
+        kc, ks = _codes(6, 1, ps, d, B, 3)
+        _append(rows, rows, kc, kc, ks, ks, six, [0, 17, 40, 33, 63, 5], [1] * 6, dev, one=True)
+
+
 def test_append_in_pieces_and_at_once():
     """The same scales; the same codes but below 2^-6 of the scale, where re-rounding may move them by one step."""
     dev = need_gpu()
