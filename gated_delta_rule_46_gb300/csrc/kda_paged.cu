@@ -501,24 +501,24 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
 
 // The 8-bit cache.  Query heads per item of its tensor-core form: half of the MMAs' columns.
 static int heads_q8(int G) { return G <= 8 ? 8 : (G <= 16 ? 16 : 32); }
-static int grid_q8(int N, int64_t max_tokens, int Hkv, int G) {
+static int grid_q8(int N, int64_t max_tokens, int Hkv, int G, int d) {
     const int HB = heads_q8(G);
-    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc, sm_count());
+    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc * tokens_per_row(d, HB), sm_count());
 }
 
 size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
     const size_t simt = paged_decode_workspace_bytes(N, max_tokens, Hq, Hkv, d);
     if (max_tokens <= kTile) return 0;            // (an item is one tile in either form: nothing to join)
     const int G = Hq / Hkv;
-    const size_t tc = sizeof(float) * grid_q8(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_q8(G));
+    const size_t tc = sizeof(float) * grid_q8(N, max_tokens, Hkv, G, d) * 2 * part_floats(d, heads_q8(G));
     return tc > simt ? tc : simt;
 }
 
 template <int D>
 static cudaError_t join_q8(const PagedParams &p, int HB, int grid, cudaStream_t st) {
-    return HB == 8    ? launch_join<__nv_bfloat16, D, kTileTc, 8>(p, grid, st)
-           : HB == 16 ? launch_join<__nv_bfloat16, D, kTileTc, 16>(p, grid, st)
-                      : launch_join<__nv_bfloat16, D, kTileTc, 32>(p, grid, st);
+    return HB == 8    ? launch_join<__nv_bfloat16, D, kTileTc * tokens_per_row(D, 8), 8>(p, grid, st)
+           : HB == 16 ? launch_join<__nv_bfloat16, D, kTileTc * tokens_per_row(D, 16), 16>(p, grid, st)
+                      : launch_join<__nv_bfloat16, D, kTileTc * tokens_per_row(D, 32), 32>(p, grid, st);
 }
 
 cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
@@ -526,10 +526,10 @@ cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaS
     const bool tc = bf16 && p.num_pages > 0 && p.max_pages > 0 &&
                     ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
     if (!tc) return bf16 ? paged_dispatch<__nv_bfloat16, __nv_fp8_e4m3>(p, d, st) : paged_dispatch<float, __nv_fp8_e4m3>(p, d, st);
-    const int HB = heads_q8(p.G), grid = grid_q8(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
+    const int HB = heads_q8(p.G), grid = grid_q8(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, d);
     PagedParams pt = p;
     pt.expire = take_layers_expire(KDA_TESTING_PAGED);
-    pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc;
+    pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc * tokens_per_row(d, HB);
     const cudaError_t e = launch_paged_decode_q8_tc(pt, d, HB, grid, st);
     if (e != cudaSuccess) return e;
     return d == 32 ? join_q8<32>(pt, HB, grid, st) : d == 64 ? join_q8<64>(pt, HB, grid, st) : join_q8<128>(pt, HB, grid, st);

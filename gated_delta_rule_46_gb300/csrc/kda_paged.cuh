@@ -110,7 +110,8 @@ __host__ __device__ constexpr int part_floats(int d, int HB) { return HB * (d + 
 // grid it runs on, with HB query heads per item.
 cudaError_t launch_paged_decode_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st);
 constexpr int kTileTc = 128;
-// e4m3 caches with bf16 queries
+// e4m3 caches with bf16 queries; tokens of a row of its tiles, which have 128
+constexpr int tokens_per_row(int d, int HB) { return d < 128 && HB <= 16 ? 2 : 1; }
 cudaError_t launch_paged_decode_q8_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st);
 
 }  // namespace kda

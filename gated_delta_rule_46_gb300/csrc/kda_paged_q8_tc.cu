@@ -3,28 +3,35 @@
 //
 // As in kda_paged_tc.cu the cached tokens are the M side of both products, so that
 // the codes go from HBM to the MMAs without passing through registers:
-//   S^T [128 tokens x N] = K Q^T,    O^T [d x N] = V^T P^T
-// on e4m3 operands.  K and V are e4m3 as they lie in the cache.  Q and the weights P,
-// which need more than e4m3's four significant bits, come in two parts,
+//   S^T [128 rows x N] = K Q^T,    O^T [row bytes x N] = V^T P^T
+// on e4m3 operands.  K and V are e4m3 as they lie in the cache, in rows of one token or,
+// for up to 64 channels and 16 heads, of F = 2: a tile is 128 rows either way, and what a
+// tile costs whatever it holds (waits, maxima, an MMA's 47 cycles of issue) is spent on
+// twice the tokens.  Tokens e = 0, 1 of the rows have N columns of their own: S^T of e is
+// the product with the e-th half of K's rows, and of O^T's columns of e only the e-th half
+// of the rows is looked at, the sum of a token's weights and the other's values being noise.
+//
+// Q and the weights P, which need more than e4m3's four significant bits, come in two parts,
 //   x = hi + lo,   hi = e4m3(x),   lo = e4m3(x - hi)
-// whose products are added up in the same accumulators.  With the largest of a head's
-// channels at 224 or more that is exact for a bf16 query down to 2^-11 of it, and off
-// by 2^-10, 2^-18 of the largest, below; of a weight it keeps eight bits, as bf16 would.
+// whose products are added up: in the same accumulators, and for up to 8 heads, where an
+// MMA's 16 columns have room for both parts, in neighbouring columns.  With the largest of
+// a head's channels at 224 or more that is exact for a bf16 query down to 2^-11 of it, and
+// off by 2^-10, 2^-18 of the largest, below; of a weight it keeps eight bits, as bf16 would.
 //
 // A token's scale of K multiplies its row of S^T.  Its scale of V goes into its
 // weight: with the tile's largest score m and largest scale of V u,
 //   P = 256 e^{s - m} v_scale / u,   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
 // so that the weights use e4m3's range from the tile's own maximum on (an error below
 // 2^-18 of that, whatever the rest of the row holds), and tiles do not wait for each
-// other's maxima: two groups of softmax warps work on tiles in turn.  What is the same for
-// all tokens of a tile (maxima, their exponentials) is worked out by a lane per head and
-// read by the others as vectors.
+// other's maxima: two groups of softmax warps work on tiles in turn.  A softmax thread has
+// four rows and a quarter of the heads (TMEM's 16 x 256-bit reads), so that what is one for
+// all tokens (maxima, their exponentials; worked out by a lane per head) is a vector or two.
 //
 // Roles of the 20 warps: 0-3 load tiles in turn (pages by TMA, scales by 4-byte copies),
 // 4 issues the S^T MMAs, 5 zeroes rows of V that hold no token and issues the O^T MMAs,
-// 6 splits and stages Q, 8-11 and 12-15 run the softmax of even and odd tiles (thread =
-// token), 16-19 keep the running output (thread = channel) in float32 registers.  Items
-// of 32 heads have one warp that loads, as their softmax takes 128 registers a thread.
+// 6 splits and stages Q, 8-11 and 12-15 run the softmax of even and odd tiles, 16-19 keep
+// the running output (thread = row of O^T) in float32 registers.  Items of 32 heads have one
+// warp that loads, as their softmax takes 128 registers a thread.
 #include <cuda.h>
 
 #include "kda_paged_tc.cuh"
@@ -53,27 +60,37 @@ enum Bar { KFULL, KFREE = KFULL + NSMAX, VFULL = KFREE + NSMAX, VFREE = VFULL + 
 
 template <int D, int HB>
 struct Lay {
-    static constexpr int N = HB < 16 ? 16 : HB;                      // the MMAs' columns; those past HB reach no one
+    static constexpr int F = tokens_per_row(D, HB), RB = D * F;      // tokens and bytes of a row
+    static constexpr int TOK = TILE * F, NBK = TOK / 16;             // tokens and, at most, blocks of a tile
+    static constexpr bool BOTH = HB == 8;                            // both parts in the columns
+    static constexpr int QN = BOTH ? 16 : HB, N = F * QN;            // columns of a token of the rows, of all
+    static constexpr int PARTS = BOTH ? 1 : 2, HT = HB / 4;          // rounds of MMAs; heads of a softmax thread
     // roles, by their first warps; 32 heads need the registers of 16 warps
     static constexpr int LOADERS = HB == 32 ? 1 : LMAX;
     static constexpr int MMA_S = LOADERS, MMA_O = LOADERS + 1, STAGE_Q = LOADERS + 2, SOFTMAX = LOADERS == 1 ? 4 : 8;
     static constexpr int OUT = SOFTMAX + 4 * NG, THREADS = 32 * (OUT + 4);
-    static constexpr uint32_t tile = TILE * D;
+    static constexpr uint32_t tile = TILE * RB;
     // about 190 KB of stages where there is room for as much
-    static constexpr int NS = D == 128 ? (HB == 32 ? 5 : 6) : D == 64 && HB == 32 ? 10 : NSMAX;
-    // (V first: with d < 128 the MMA's rows past d read what lies behind a stage, which no one looks at)
-    static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_part = N * D, q_bytes = 2 * q_part;
-    static constexpr uint32_t P = Q + 2 * q_bytes, p_part = N * TILE, p_bytes = 2 * p_part;
-    static constexpr uint32_t SC = P + NG * p_bytes;                 // float: scales of K [RING][8], of V [RING][8]
-    static constexpr uint32_t QS = SC + 2 * RING * 8 * 4;            // factors of the queries [QRING][HB]
+    static constexpr int NS = RB == 128 ? (HB == 32 || (HB == 16 && F == 2) ? 5 : 6) : RB == 64 ? (HB == 8 ? NSMAX : 10) : NSMAX;
+    // (V first: with rows of less than 128 bytes the MMA's rows past them read what lies behind a stage, which no one looks at)
+    static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_part = QN * D, q_bytes = PARTS * q_part;
+    static constexpr uint32_t P = Q + 2 * q_bytes, p_part = N * TILE, p_bytes = PARTS * p_part;
+    static constexpr uint32_t SC = P + NG * p_bytes;                 // float: scales of K [RING][NBK], of V [RING][NBK]
+    static constexpr uint32_t QS = SC + 2 * RING * NBK * 4;          // factors of the queries [QRING][HB]
     static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [NG][HB], u / 256 [NG] (padded to 4)
     static constexpr uint32_t RED = M + NG * HB * 4 + 16;            // maxima of the warps [NG][2][4][HB]
     static constexpr uint32_t SUM = RED + NG * 8 * HB * 4;           // sums of the item [2][4 NG][HB], maxima [2][NG][HB]
     static constexpr uint32_t STAT = SUM + 10 * NG * HB * 4;         // of each softmax and output warp: [4][HB]
-    static constexpr uint32_t bytes = STAT + (4 * NG + 4) * 4 * HB * 4;
-    static constexpr uint32_t cols = N == 16 ? 128 : 256;            // TMEM: SB + NG buffers of N columns
+    static constexpr uint32_t X = STAT + (4 * NG + 4) * 4 * HB * 4;  // outputs of an item's tokens e, F == 2: [HB][RB]
+    static constexpr uint32_t bytes = X + (F == 2 ? HB * RB * 4 : 0);
+    static constexpr uint32_t cols = (SB + NG) * N <= 128 ? 128 : 256;   // TMEM: SB + NG buffers of N columns
     static_assert((SB + NG) * N <= cols, "tensor memory");
 };
+// The column of S^T, and the row of Q's stage, of head h: a softmax thread finds its HT heads in a row in its own columns.
+template <int HB>
+__device__ __forceinline__ int column(int h) {
+    return HB == 8 ? h : HB == 16 ? 8 * (h >> 1 & 1) + 2 * (h >> 2) + (h & 1) : 8 * (h >> 1 & 3) + 2 * (h >> 3) + (h & 1);
+}
 
 // Byte offset of the 16-byte chunk of a row, swizzled as TMA does it.
 template <int D>
@@ -96,11 +113,43 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r), __NV_SATFINITE, __NV_E4M3);
 }
 
+// N values per lane, combined over the lanes with the same lane % 4: lane i ends with value `mine` of them.
+template <int N, typename Op>
+__device__ __forceinline__ float reduce_rows(float (&v)[N], int lane, int &mine, Op op) {
+    mine = 0;
+#pragma unroll
+    for (int n = N, bit = 16; bit >= 4; bit >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & bit;
+            mine += up ? n : 0;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+        }
+    }
+    return v[0];
+}
+template <int N>
+__device__ __forceinline__ void ld_heads(const float *p, float (&x)[N]) {
+    if constexpr (N == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x; x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) ld4(p + i, x + i);
+    }
+}
+
 template <int D, int HB>
 __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     paged_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedParams p) {
     using L = Lay<D, HB>;
-    constexpr int NS = L::NS, LOADERS = L::LOADERS;
+    constexpr int NS = L::NS, LOADERS = L::LOADERS, F = L::F, FS = F - 1, TOK = L::TOK;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[NBAR];
     __shared__ int64_t s_sum[257];
@@ -113,8 +162,8 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
 
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
-    const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    empty_sequences<__nv_bfloat16, TILE>(p, D);
+    const Split sp = find_split<TOK>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    empty_sequences<__nv_bfloat16, TOK>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBAR; ++i) {
@@ -139,9 +188,9 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     const uint32_t tmem = s_tmem;
     auto tm_s = [&](int b) { return tmem + b * L::N; };
     auto tm_o = [&](int b) { return tmem + (SB + b) * L::N; };
-    Walk wk;
+    WalkOf<TOK> wk;
     wk.start(p, sp, items);
-    const int rows = min(TILE, 1 << p.page_shift);        // tokens of a tile that one page holds
+    const int rows = min(TILE, 1 << (p.page_shift - FS)); // of a tile that one page holds
     const int pieces = TILE / rows, rows_shift = 31 - __clz(rows);
     float *const sc = reinterpret_cast<float *>(sm + L::SC), *const qs = reinterpret_cast<float *>(sm + L::QS),
                  *const sm_m = reinterpret_cast<float *>(sm + L::M), *const sums = reinterpret_cast<float *>(sm + L::SUM);
@@ -157,7 +206,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             if (threadIdx.x == 0 && wk.raw != len) report_status(p.status, KDA_ERR_INVALID_ARG);
             for (int64_t i = first + ((warp - t0) & (LOADERS - 1)); i < last; i += LOADERS) {
                 const int t = t0 + (int)(i - first), s = t % NS, r = t % RING;
-                const int at = (int)(i * TILE) + lane * rows;     // this page's first token of the tile
+                const int at = (int)(i * TOK) + lane * rows * F;  // this page's first token of the tile
                 int page = -1;
                 if (lane < pieces && at < len) {
                     page = table[at >> p.page_shift];
@@ -167,26 +216,30 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t bytes = (uint32_t)__popc(mask) * rows * D;
-                const int y = (int)(((((int64_t)page * p.Hkv) + kvh) << p.page_shift) + (at & ((1 << p.page_shift) - 1)));
-                // scales: lanes 0-7 those of K, 8-15 those of V, of the block of tokens that starts at `from`
-                const int off = (lane & 7) << p.block_shift, from = (int)(i * TILE) + off;
-                const int of = __shfl_sync(0xffffffffu, page, (off >> rows_shift) & 31);
-                const bool block = lane < 16 && off < TILE && from < len && of >= 0;
-                const float *src = lane < 8 ? p.ks : p.vs;
-                if (block) src += ((int64_t)of * p.Hkv + kvh) * per + ((from & ((1 << p.page_shift) - 1)) >> p.block_shift);
+                // (rows before the first read as zeros, as those of a page that is missing)
+                const int y = page < 0 ? -TILE : (int)((((((int64_t)page * p.Hkv) + kvh) << p.page_shift) +
+                                                        (at & ((1 << p.page_shift) - 1))) >> FS);
+                // scales: a lane for each block of tokens
+                const int off = lane << p.block_shift, from = (int)(i * TOK) + off;
+                const int of = __shfl_sync(0xffffffffu, page, (off >> FS >> rows_shift) & 31);
+                const bool block = off < TOK && from < len && of >= 0;
+                const int64_t at_scale =
+                    block ? ((int64_t)of * p.Hkv + kvh) * per + ((from & ((1 << p.page_shift) - 1)) >> p.block_shift) : 0;
                 for (int kv = 0; kv < 2; ++kv) {
                     uint64_t *full = &bar[(kv ? VFULL : KFULL) + s], *free = &bar[(kv ? VFREE : KFREE) + s];
                     if (t >= NS && !warp_wait(free, t / NS - 1)) { ok = false; break; }
-                    uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * D;
+                    uint8_t *dst = sm + (kv ? L::V : L::K) + s * L::tile + lane * rows * L::RB;
                     if (lane == 0) {
                         if (kv == 0) s_mask[r] = mask;
-                        ptx::mbar_arrive_expect_tx(full, bytes);
+                        ptx::mbar_arrive_expect_tx(full, L::tile);
                     }
                     __syncwarp();
-                    if (page >= 0) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
+                    if (lane < pieces) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
                     if (kv == 0) {
-                        if (lane < 16) ptx::cp_async4(sc + (lane >> 3) * RING * 8 + r * 8 + (lane & 7), src, block);
+                        if (lane < L::NBK) {
+                            ptx::cp_async4(sc + r * L::NBK + lane, p.ks + at_scale, block);
+                            ptx::cp_async4(sc + (RING + r) * L::NBK + lane, p.vs + at_scale, block);
+                        }
                         ptx::cp_async_arrive(&bar[SCALES + r]);
                     }
                 }
@@ -198,7 +251,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     } else if (warp == L::MMA_S) {                                // ---- S^T
         if (ptx::elect_one()) {
             int item_no = 0;
-            constexpr uint32_t id_s = ptx::idesc_e4m3_f32(128, L::N, false);
+            constexpr uint32_t id_s = ptx::idesc_e4m3_f32(128, L::QN, false);
             if (p.expire && blockIdx.x == 0) ok = ptx::mbar_wait(&bar[PVD], 0, kTestWait);
             for (int t = 0; ok && wk.more();) {
                 const int64_t first = wk.tile, last = wk.last();
@@ -212,10 +265,13 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                          (t < SB || ptx::mbar_wait(&bar[SFREE + b], (t / SB - 1) & 1, kWaitBudget));
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
-                    const uint64_t k = ptx::sdesc_rows<D>(base + L::K + s * L::tile);
+                    const uint64_t k = ptx::sdesc_rows<L::RB>(base + L::K + s * L::tile);
 #pragma unroll
-                    for (int j = 0; j < 2 * J; ++j)
-                        ptx::mma_f8_ss(tm_s(b), k + j % J * 2, q + j / J * (L::q_part >> 4) + j % J * 2, id_s, j > 0);
+                    for (int j = 0; j < F * L::PARTS * J; ++j) {
+                        const int e = j / (L::PARTS * J), part = j / J % L::PARTS;
+                        ptx::mma_f8_ss(tm_s(b) + e * L::QN, k + (e * D >> 4) + j % J * 2, q + part * (L::q_part >> 4) + j % J * 2,
+                                       id_s, j % (L::PARTS * J) > 0);
+                    }
                     ptx::mma_commit(&bar[SD + b]);
                     ptx::mma_commit(&bar[KFREE + s]);
                 }
@@ -233,16 +289,11 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 const int s = t % NS, b = t % NG;
                 ok = warp_wait(&bar[VFULL + s], t / NS);
                 if (!ok) break;
-                const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[t % RING]);
-                const int left = len - (int)(i * TILE);
-                if (left < TILE || __popc(mask) < pieces) {
-                    // (a weight of 0 does not silence a NaN) 16 bytes a lane and step, whole rows
-                    const int from = __popc(mask) < pieces ? 0 : min(max(left, 0), TILE);
-                    for (int j = from * (D / 16) + lane; j < TILE * (D / 16); j += 32) {
-                        const int r = j / (D / 16);
-                        if (r < left && (mask >> (r >> rows_shift) & 1)) continue;
-                        *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + j * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                const int left = len - (int)(i * TOK);
+                if (left < TOK) {       // (a weight of 0 does not silence a NaN) 16 bytes a lane and step
+                    constexpr int C = L::RB / 16;
+                    for (int j = left * (D / 16) + lane; j < TILE * C; j += 32)
+                        *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + swizzled<L::RB>(j / C, j % C)) = make_uint4(0, 0, 0, 0);
                     ptx::fence_async_smem();
                     __syncwarp();
                 }
@@ -250,12 +301,12 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 if (!ok) break;
                 if (ptx::elect_one()) {
                     ptx::tc_fence_after_sync();
-                    const uint64_t v = ptx::sdesc_rows<D>(base + L::V + s * L::tile, L::tile);
+                    const uint64_t v = ptx::sdesc_rows<L::RB>(base + L::V + s * L::tile, L::tile);
                     const uint64_t w = ptx::sdesc_plain_n(base + L::P + b * L::p_bytes, 8 * L::N, 128);
                     constexpr int J = TILE / 32;
 #pragma unroll
-                    for (int j = 0; j < 2 * J; ++j)
-                        ptx::mma_f8_ss(tm_o(b), v + j % J * (32 * D >> 4), w + j * (32 * L::N >> 4), id_o, j > 0);
+                    for (int j = 0; j < L::PARTS * J; ++j)
+                        ptx::mma_f8_ss(tm_o(b), v + j % J * (32 * L::RB >> 4), w + j * (32 * L::N >> 4), id_o, j > 0);
                     ptx::mma_commit(&bar[PVD + b]);
                     ptx::mma_commit(&bar[VFREE + s]);
                 }
@@ -315,9 +366,10 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(y0 - b.x, y1 - b.y) << (8 * (e & 2));
                     }
                     if (h < HB) {
-                        uint8_t *to = dst + swizzled<D>(h, c >> 1) + (c & 1) * 8;
-                        *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(to + L::q_part) = make_uint2(lo[0], lo[1]);
+                        const int n = column<HB>(h);
+                        *reinterpret_cast<uint2 *>(dst + swizzled<D>(n, c >> 1) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+                        uint8_t *low = dst + (L::BOTH ? swizzled<D>(8 + n, c >> 1) : L::q_part + swizzled<D>(n, c >> 1));
+                        *reinterpret_cast<uint2 *>(low + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
                         if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
                     }
                 }
@@ -328,50 +380,85 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             ++item_no;
             wk.next_item(p, last - first);
         }
-    } else if (warp >= L::SOFTMAX && warp < L::OUT) {             // ---- softmax: thread = token of the tile
-        const int wg = (warp - L::SOFTMAX) >> 2, q = warp & 3, j = q * 32 + lane;
+    } else if (warp >= L::SOFTMAX && warp < L::OUT) {             // ---- softmax
+        // row k of this thread: 32 q + lane / 4 + 8 k; its heads: lane % 4 * HT and on
+        constexpr int HT = L::HT, NT = L::N / 8;
+        const int wg = (warp - L::SOFTMAX) >> 2, q = warp & 3, row0 = q * 32 + (lane >> 2), h0 = (lane & 3) * HT;
         float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - L::SOFTMAX) * 4 * HB;
         const int hl = lane < HB ? lane : 0;                      // this lane's head, of what is one for all tokens
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
             const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
-            float m = -INFINITY, l[HB];
+            float m = -INFINITY, l[HT];
 #pragma unroll
-            for (int h = 0; h < HB; ++h) l[h] = 0.f;
+            for (int h = 0; h < HT; ++h) l[h] = 0.f;
             for (int64_t i = first; i < last; ++i, ++t) {
                 if (t % NG != wg) continue;
                 const int sb = t % SB, r = t % RING, turn = t / NG;
                 float *red = reinterpret_cast<float *>(sm + L::RED) + (wg * 2 + (turn & 1)) * 4 * HB;
                 ok = warp_wait(&bar[SCALES + r], t / RING) && warp_wait(&bar[SD + sb], t / SB);
-                float s[HB], weight = 0.f, unit = 0.f;
+                float x[F * HT][4], weight[4], unit = 0.f;        // scores of token e, head h: x[e * HT + h]
                 if (ok) {
                     ptx::tc_fence_after_sync();
-                    const bool in = (int)(i * TILE) + j < len &&
-                                    (*static_cast<volatile uint32_t *>(&s_mask[r]) >> (j >> rows_shift) & 1);
-                    const float fk = sc[r * 8 + (j >> p.block_shift)];
-                    // the tile's largest scale of V (2^-100 at least), and this token's share of it
-                    const float *fv = sc + RING * 8 + r * 8;
-                    float v[8];
-                    ld8(fv, v);
+                    float raw[2][4 * NT];                         // lanes 0-15 and 16-31 of the warp's part of TMEM
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) unit = fmaxf(unit, e << p.block_shift < TILE ? fabsf(v[e]) : 0.f);
-                    unit = fmaxf(unit, 0x1p-100f);
-                    weight = in ? fv[j >> p.block_shift] * (256.f / unit) : 0.f;
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t from = tm_s(sb) + ((uint32_t)q << 21) + ((uint32_t)half << 20);
+                        if constexpr (NT == 2) ptx::tmem_ld_tiles2(from, raw[half]);
+                        else ptx::tmem_ld_tiles4(from, raw[half]);
+                    }
+                    const float *fk = sc + r * L::NBK, *fv = sc + (RING + r) * L::NBK;
+                    float f[4];
 #pragma unroll
-                    for (int h = 0; h < HB; h += 8) {
-                        float x[8];
-                        ptx::tmem_ld8(tm_s(sb) + ((uint32_t)q << 21) + h, x);
-                        ptx::tmem_ld_wait(x);
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = (row0 + 8 * k) * F >> p.block_shift;
+                        f[k] = fk[at];
+                        weight[k] = fv[at];
+                    }
+                    // the tile's largest scale of V, 2^-100 at least (where a block has no token its scale is 0)
+                    unit = fmaxf(ptx::warp_max(fabsf(lane < (TOK >> p.block_shift) ? fv[lane] : 0.f)), 0x1p-100f);
+                    const float share = 256.f / unit;
+                    ptx::tmem_ld_wait(raw[0], raw[1]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s[h + e] = x[e] = in ? x[e] * fk : -INFINITY;
+                    for (int k = 0; k < 4; ++k) {
+                        weight[k] *= share;
+                        auto column = [&](int tile, int b) { return raw[k >> 1][4 * tile + 2 * (k & 1) + b]; };
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = ptx::warp_max(x[e]);
-                        if (lane == 0) {
-                            *reinterpret_cast<float4 *>(red + q * HB + h) = make_float4(x[0], x[1], x[2], x[3]);
-                            *reinterpret_cast<float4 *>(red + q * HB + h + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                        for (int e = 0; e < F; ++e)
+#pragma unroll
+                            for (int h = 0; h < HT; ++h)
+                                x[e * HT + h][k] = f[k] * (L::BOTH ? column(2 * e, h) + column(2 * e + 1, h)
+                                                                   : column(e * (L::QN / 8) + (h >> 1), h & 1));
+                    }
+                    const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[r]);
+                    const int left = len - (int)(i * TOK);
+                    if (left < TOK || __popc(mask) < pieces) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = row0 + 8 * k;
+                            const bool page = mask >> (row >> rows_shift) & 1;
+#pragma unroll
+                            for (int e = 0; e < F; ++e) {
+                                const bool in = page && row * F + e < left;
+#pragma unroll
+                                for (int h = 0; h < HT; ++h) x[e * HT + h][k] = in ? x[e * HT + h][k] : -INFINITY;
+                            }
+                            if (!page) weight[k] = 0.f;
                         }
                     }
+                    float mx[HT];
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        mx[h] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < F; ++e)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mx[h] = fmaxf(mx[h], x[e * HT + h][k]);
+                    }
+                    int mine;
+                    const float top = reduce_rows(mx, lane, mine, [](float a, float b) { return fmaxf(a, b); });
+                    red[q * HB + h0 + mine] = top;
                     ptx::tc_fence_before_sync();
                     warp_arrive(&bar[SFREE + sb]);
                     // the weights and maxima of this group's last tile have been used
@@ -393,46 +480,49 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     const bool any = __any_sync(0xffffffffu, less != 1.f && m != -INFINITY);
                     m = mn;
                     __syncwarp();
-                    if (any)
+                    if (any) {
+                        float y[HT];
+                        ld_heads(st + 3 * HB + h0, y);
 #pragma unroll
-                        for (int h = 0; h < HB; h += 4) {
-                            float x[4];
-                            ld4(st + 3 * HB + h, x);
+                        for (int h = 0; h < HT; ++h) l[h] *= y[h];
+                    }
+                }
+                float f[HT], top[HT], g[HT];
+                ld_heads(st + h0, f);
+                ld_heads(st + HB + h0, top);
+                ld_heads(st + 2 * HB + h0, g);
+                constexpr int WB = L::BOTH ? 1 : HT / 4;          // 16-byte columns of a token, a word of this thread in each
+                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (4 * q + (lane >> 3)) * 8 * L::N + (lane & 7) * 16;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) l[h + e] *= x[e];
+                for (int e = 0; e < F; ++e)
+#pragma unroll
+                    for (int blk = 0; blk < WB; ++blk) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float w[4];
+#pragma unroll
+                            for (int j = 0; j < (L::BOTH ? 2 : 4); ++j) {
+                                const int h = 4 * blk + j;
+                                const float own = ex2(fmaf(x[e * HT + h][k], f[h], -top[h]));
+                                l[h] = fmaf(own, g[h], l[h]);
+                                w[j] = own * weight[k];
+                            }
+                            uint32_t h0_, l0_, h1_, l1_;
+                            split2(w[0], w[1], h0_, l0_);
+                            if constexpr (L::BOTH) {
+                                hi[k] = h0_ | l0_ << 16;
+                            } else {
+                                split2(w[2], w[3], h1_, l1_);
+                                hi[k] = h0_ | h1_ << 16;
+                                lo[k] = l0_ | l1_ << 16;
+                            }
                         }
-                }
-                uint32_t hi[HB / 4], lo[HB / 4];
-#pragma unroll
-                for (int h = 0; h < HB; h += 4) {
-                    float f[4], top[4], g[4], w[4];
-                    ld4(st + h, f);
-                    ld4(st + HB + h, top);
-                    ld4(st + 2 * HB + h, g);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float own = ex2(fmaf(s[h + e], f[e], -top[e]));
-                        l[h + e] = fmaf(own, g[e], l[h + e]);
-                        w[e] = own * weight;
+                        uint8_t *to = w8 + (e * WB + blk) * 128;
+                        ptx::stmatrix4(ptx::smem_addr(to), hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (!L::BOTH) ptx::stmatrix4(ptx::smem_addr(to + L::p_part), lo[0], lo[1], lo[2], lo[3]);
                     }
-                    uint32_t h0, h1, l0, l1;
-                    split2(w[0], w[1], h0, l0);
-                    split2(w[2], w[3], h1, l1);
-                    hi[h / 4] = h0 | h1 << 16;
-                    lo[h / 4] = l0 | l1 << 16;
-                }
-                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (j >> 3) * 8 * L::N + (j & 7) * 16;
-                if constexpr (HB == 8) {
-                    *reinterpret_cast<uint2 *>(w8) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(w8 + L::p_part) = make_uint2(lo[0], lo[1]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < HB / 4; h += 4) {
-                        *reinterpret_cast<uint4 *>(w8 + h * 32) = make_uint4(hi[h], hi[h + 1], hi[h + 2], hi[h + 3]);
-                        *reinterpret_cast<uint4 *>(w8 + L::p_part + h * 32) = make_uint4(lo[h], lo[h + 1], lo[h + 2], lo[h + 3]);
-                    }
-                }
-                if (j == 0) sm_m[NG * HB + wg] = unit * 0x1p-8f;
+                if (q == 0 && lane == 0) sm_m[NG * HB + wg] = unit * 0x1p-8f;
                 ptx::fence_async_smem();
                 warp_arrive(&bar[PREADY + wg]);
             }
@@ -441,24 +531,20 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             ok = item_no < 2 || warp_wait(&bar[IFREE + ib], (item_no >> 1) - 1);
             ok = !ptx::bar_any(1 + wg, 128, !ok);
             if (!ok) break;
-#pragma unroll
-            for (int h = 0; h < HB; h += 8) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = l[h + e];
-                const float sum = reduce_lanes(v, lane, [](float x, float y) { return x + y; });
-                if (lane % 4 == 0) sums[((ib * NG + wg) * 4 + q) * HB + h + lane / 4] = sum;
-            }
+            int mine;
+            const float sum = reduce_rows(l, lane, mine, [](float a, float b) { return a + b; });
+            sums[((ib * NG + wg) * 4 + q) * HB + h0 + mine] = sum;
             if (q == 0 && lane < HB) sums[(8 * NG + ib * NG + wg) * HB + lane] = m;
             warp_arrive(&bar[IREADY + ib]);
             ++item_no;
             wk.next_item(p, last - first);
         }
-    } else if (warp >= L::OUT) {                                  // ---- output: thread = channel
-        const int q = warp & 3, d = q * 32 + lane;
+    } else if (warp >= L::OUT) {                                  // ---- output: thread = row of O^T
+        const int q = warp & 3, row = q * 32 + lane, e = row / D, d = row % D;
         float *const st = reinterpret_cast<float *>(sm + L::STAT) + (warp - L::SOFTMAX) * 4 * HB;
+        float *const xch = reinterpret_cast<float *>(sm + L::X);
         const int hl = lane < HB ? lane : 0;
-        const bool works = q * 32 < D;                            // (rows of O^T past d reach no one)
+        const bool works = q * 32 < L::RB;                        // (rows of O^T past a row's bytes reach no one)
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
@@ -473,6 +559,10 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 if (!ok) break;
                 if (works) {
                     ptx::tc_fence_after_sync();
+                    const uint32_t from = tm_o(b) + ((uint32_t)q << 21) + (F == 2 ? (uint32_t)e * L::QN : 0u);
+                    float v[L::QN];
+                    if constexpr (L::QN == 16) ptx::tmem_ld16(from, v);
+                    else ptx::tmem_ld32(from, v);
                     const float top = sm_m[b * HB + hl], mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn;
                     __syncwarp();                                 // (the factors before have been read)
                     if (lane < HB) {
@@ -481,23 +571,40 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     m = mn;
                     __syncwarp();
+                    ptx::tmem_ld_wait(v);
 #pragma unroll
-                    for (int h = 0; h < HB; h += 8) {
-                        float v[8], f[8], g[8];
-                        ptx::tmem_ld8(tm_o(b) + ((uint32_t)q << 21) + h, v);
-                        ld8(st + h, f);
-                        ld8(st + HB + h, g);
-                        ptx::tmem_ld_wait(v);
+                    for (int h = 0; h < HB; h += 4) {
+                        float f[4], g[4];
+                        ld4(st + h, f);
+                        ld4(st + HB + h, g);
+                        // heads h to h + 3 in the columns that the softmax threads write
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[h + e] = fmaf(acc[h + e], f[e], v[e] * g[e]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float y = HB == 8    ? v[2 * h + 4 * (j >> 1) + (j & 1)] + v[2 * h + 4 * (j >> 1) + (j & 1) + 2]
+                                            : HB == 16 ? v[h + j]
+                                                       : v[16 * (h >> 2 & 1) + 4 * (h >> 3) + j];
+                            acc[h + j] = fmaf(acc[h + j], f[j], y * g[j]);
+                        }
                     }
                     ptx::tc_fence_before_sync();
                 }
                 warp_arrive(&bar[OFREE + b]);
             }
-            if (!ok) break;
             const int ib = item_no & 1;
-            ok = warp_wait(&bar[IREADY + ib], item_no >> 1);
+            ok = ok && warp_wait(&bar[IREADY + ib], item_no >> 1);
+            if constexpr (F == 2) {      // tokens e = 0 and 1 of the rows together, half of the heads each
+                if (ok && works)
+#pragma unroll
+                    for (int h = 0; h < HB; ++h) xch[h * L::RB + row] = acc[h];
+                ok = !ptx::bar_any(1 + NG, 128, !ok);
+                if (ok && works)
+#pragma unroll
+                    for (int h = 0; h < HB / 2; ++h) {
+                        const float *x = xch + (e * (HB / 2) + h) * L::RB + d;
+                        acc[h] = x[0] + x[D];
+                    }
+                ptx::bar_any(1 + NG, 128, false);                 // (what is written next has been read)
+            }
             if (!ok) break;
             const bool whole = first == 0 && last == wk.nt;
             float *part = p.part + ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * part_floats(D, HB);
@@ -522,19 +629,21 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             }
             warp_arrive(&bar[IFREE + ib]);
             if (works) {
+                constexpr int HM = HB / F;                        // heads of this thread
+                const int h1 = F == 2 ? e * HM : 0;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row0 * D + d;
                 // (a sum is 0 or at least 1, a maximum's own weight, or infinite or NaN)
                 if (whole) {
 #pragma unroll
-                    for (int h = 0; h < HB; ++h)
-                        if (h < hb) {
-                            const float l = st[2 * HB + h];
-                            out[h * D] = __float2bfloat16_rn(l > 0.f ? __fdividef(acc[h], l) : (l == 0.f ? 0.f : l));
+                    for (int h = 0; h < HM; ++h)
+                        if (h1 + h < hb) {
+                            const float l = st[2 * HB + h1 + h];
+                            out[(h1 + h) * D] = __float2bfloat16_rn(l > 0.f ? __fdividef(acc[h], l) : (l == 0.f ? 0.f : l));
                         }
                 } else {
 #pragma unroll
-                    for (int h = 0; h < HB; ++h)
-                        if (h < hb) part[HB * 2 + h * D + d] = acc[h];
+                    for (int h = 0; h < HM; ++h)
+                        if (h1 + h < hb) part[HB * 2 + (h1 + h) * D + d] = acc[h];
                 }
             }
             ++item_no;
@@ -561,14 +670,16 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
 template <int D, int HB>
 cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     CUtensorMap mk, mv;
-    const uint64_t rows = (uint64_t)p.num_pages * p.Hkv << p.page_shift;
-    const uint32_t box = p.page_shift < 7 ? 1u << p.page_shift : TILE;
-    if (!make_map_bytes(&mk, p.kc, rows, D, box) || !make_map_bytes(&mv, p.vc, rows, D, box)) return cudaErrorInvalidValue;
-    constexpr uint32_t smem = Lay<D, HB>::bytes + 1024;
+    using L = Lay<D, HB>;
+    const int shift = p.page_shift - (L::F - 1);
+    const uint64_t rows = (uint64_t)p.num_pages * p.Hkv << shift;
+    const uint32_t box = shift < 7 ? 1u << shift : TILE;
+    if (!make_map_bytes(&mk, p.kc, rows, L::RB, box) || !make_map_bytes(&mv, p.vc, rows, L::RB, box)) return cudaErrorInvalidValue;
+    constexpr uint32_t smem = L::bytes + 1024;
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");    // (beside the static part)
     const cudaError_t e = allow_smem<paged_decode_q8_tc_kernel<D, HB>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), Lay<D, HB>::THREADS, smem, st, 1, mk, mv, p);
+    return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), L::THREADS, smem, st, 1, mk, mv, p);
 }
 template <int D>
 cudaError_t launch_h(const PagedParams &p, int HB, int grid, cudaStream_t st) {

@@ -15,7 +15,8 @@ constexpr long long kDrain = 20000000LL;
 
 // The tiles of this CTA in order: (sequence, item, tile); every role walks its
 // own copy.  The next sequence's length is read a sequence ahead.
-struct Walk {
+template <int TILE>
+struct WalkOf {
     int64_t w, w1, nt, tile;
     int n, item, items, len, raw, ahead;      // len: raw, clamped to the table
     __device__ void start(const PagedParams &p, const Split &sp, int items_) {
@@ -48,6 +49,8 @@ struct Walk {
         }
     }
 };
+
+using Walk = WalkOf<TILE>;
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, int phase) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, kWaitBudget));

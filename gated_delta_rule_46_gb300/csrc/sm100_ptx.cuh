@@ -231,6 +231,21 @@ __device__ __forceinline__ void tmem_ld_tiles4(uint32_t taddr, float (&r)[16]) {
           "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr));
 }
+// The same of two tiles.
+__device__ __forceinline__ void tmem_ld_tiles2(uint32_t taddr, float (&r)[8]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+        : "r"(taddr));
+}
+// Four 8 x 8 tiles of 16-bit values: thread t holds columns 2 (t % 4) and + 1 of row t / 4 of each, and gives the
+// address of row t % 8 (16 bytes) of the stored tile t / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
 // Four 8 x 8 tiles of 16-bit values in that layout, stored transposed: thread t
 // gives the address of row t % 8 (16 bytes) of the stored tile t / 8.
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
