@@ -29,7 +29,7 @@
 //
 // Roles of the 20 warps: 0-3 load tiles in turn (pages by TMA, scales by 4-byte copies),
 // 4 issues the S^T MMAs, 5 zeroes rows of V that hold no token and issues the O^T MMAs,
-// 6 splits and stages Q, 8-11 and 12-15 run the softmax of even and odd tiles, 16-19 keep
+// 6 and 7 split and stage Q of items in turn, 8-11 and 12-15 run the softmax of even and odd tiles, 16-19 keep
 // the running output (thread = row of O^T) in float32 registers.  Items of 32 heads have one
 // warp that loads, as their softmax takes 128 registers a thread.
 #include <cuda.h>
@@ -68,6 +68,7 @@ struct Lay {
     // roles, by their first warps; 32 heads need the registers of 16 warps
     static constexpr int LOADERS = HB == 32 ? 1 : LMAX;
     static constexpr int MMA_S = LOADERS, MMA_O = LOADERS + 1, STAGE_Q = LOADERS + 2, SOFTMAX = LOADERS == 1 ? 4 : 8;
+    static constexpr int STAGERS = SOFTMAX - STAGE_Q;                // warps that stage Q, items in turn
     static constexpr int OUT = SOFTMAX + 4 * NG, THREADS = 32 * (OUT + 4);
     static constexpr uint32_t tile = TILE * RB;
     // about 190 KB of stages where there is room for as much
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
         int t0 = 0;                                               // tiles before the item
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
-            const int kvh = wk.item / nb, len = wk.len;
+            const int kvh = nb == 1 ? wk.item : wk.item / nb, len = wk.len;
             const int32_t *table = p.table + (int64_t)wk.n * p.max_pages;
             if (threadIdx.x == 0 && wk.raw != len) report_status(p.status, KDA_ERR_INVALID_ARG);
             for (int64_t i = first + ((warp - t0) & (LOADERS - 1)); i < last; i += LOADERS) {
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             }
             wk.next_item(p, last - first);
         }
-    } else if (warp == L::STAGE_Q) {                              // ---- Q
+    } else if (warp < L::SOFTMAX) {                               // ---- Q
         int item_no = 0;
         const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
         constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = HB / RPS < 1 ? 1 : HB / RPS;     // lanes per head, heads at a time
@@ -322,11 +323,16 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
         const float sc2 = fabsf(p.scale) * kLog2E;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
-            const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
+            const int kvh = nb == 1 ? wk.item : wk.item / nb, g0 = (wk.item - kvh * nb) * HB, hb = min(HB, p.G - g0);
+            if (item_no % L::STAGERS != warp - L::STAGE_Q) {
+                ++item_no;
+                wk.next_item(p, last - first);
+                continue;
+            }
             uint8_t *dst = sm + L::Q + (item_no & 1) * L::q_bytes;
             const __nv_bfloat16 *q =
                 static_cast<const __nv_bfloat16 *>(p.q) + (int64_t)wk.n * p.ldq + ((int64_t)kvh * p.G + g0) * D;
-            constexpr int U = STEPS < 4 ? STEPS : 4;              // loads under way
+            constexpr int U = STEPS < 8 ? STEPS : 8;              // loads under way
             for (int i0 = 0; i0 < STEPS; i0 += U) {
                 uint4 u[U];
 #pragma unroll
@@ -340,36 +346,54 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 }
                 if (i0 == 0 && item_no >= 2) ok = warp_wait(&bar[QFREE + (item_no & 1)], (item_no >> 1) - 1);
                 if (!ok) break;
+                // each head's largest magnitude, by its bits, of two values at a time; what is not finite is larger still
+                uint32_t top[U];
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    top[i] = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                      __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
+#pragma unroll
+                for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+                    for (int i = 0; i < U; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    top[i] = max(top[i] << 16, top[i] & 0xffff0000u);
+                    odd |= top[i] >= 0x7f800000u;
+                }
+                if (__any_sync(0xffffffffu, odd))                 // what is not finite becomes NaN, the rest as without it
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, m = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t half = w[e >> 1] >> (16 * (e & 1)) & 0x7fffu;
+                            if (half >= 0x7f80u) w[e >> 1] |= 0x7fffu << (16 * (e & 1));
+                            else m = max(m, half);
+                        }
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        top[i] = m << 16;
+                    }
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const int h = (i0 + i) * RPS + lane / LPR;
-                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                    float x[8], a = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-                        a = fmaxf(a, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
-                    }
-#pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
                     // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
-                    const float f = power_for(a), inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
-                    uint32_t hi[2] = {}, lo[2] = {};
+                    const float f = power_for(__uint_as_float(top[i]));
+                    const float inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
+                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        // (a saturating conversion takes infinities for large numbers)
-                        const float y0 = fabsf(x[e]) < INFINITY ? x[e] * inv : NAN;
-                        const float y1 = fabsf(x[e + 1]) < INFINITY ? x[e + 1] * inv : NAN;
-                        const uint16_t ch = f2_to_e4m3x2(y0, y1);
-                        const float2 b = e4m3x2_to_f2(ch);
-                        hi[e >> 2] |= (uint32_t)ch << (8 * (e & 2));
-                        lo[e >> 2] |= (uint32_t)f2_to_e4m3x2(y0 - b.x, y1 - b.y) << (8 * (e & 2));
-                    }
+                    for (int e = 0; e < 4; ++e)     // (exact in float16 but for what is below 2^-23 of the largest)
+                        split2(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
                     if (h < HB) {
                         const int n = column<HB>(h);
-                        *reinterpret_cast<uint2 *>(dst + swizzled<D>(n, c >> 1) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
                         uint8_t *low = dst + (L::BOTH ? swizzled<D>(8 + n, c >> 1) : L::q_part + swizzled<D>(n, c >> 1));
-                        *reinterpret_cast<uint2 *>(low + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+                        *reinterpret_cast<uint2 *>(dst + swizzled<D>(n, c >> 1) + (c & 1) * 8) =
+                            make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                        *reinterpret_cast<uint2 *>(low + (c & 1) * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                         if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
                     }
                 }
@@ -548,7 +572,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
         int t = 0, item_no = 0;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
-            const int kvh = wk.item / nb, g0 = (wk.item % nb) * HB, hb = min(HB, p.G - g0);
+            const int kvh = nb == 1 ? wk.item : wk.item / nb, g0 = (wk.item - kvh * nb) * HB, hb = min(HB, p.G - g0);
             const int64_t row0 = (int64_t)wk.n * p.Hq + (int64_t)kvh * p.G + g0;
             float acc[HB], m = -INFINITY;
 #pragma unroll
@@ -620,7 +644,8 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(ms[g * HB] - mu), l);
                 }
                 __syncwarp();
-                if (lane < HB) st[2 * HB + hl] = l;
+                // (a sum is 0, without a token, or at least 1, a maximum's own weight, or infinite or NaN)
+                if (lane < HB) st[2 * HB + hl] = l > 0.f ? __fdividef(1.f, l) : l;
                 if (q == 0 && lane < hb) {
                     if (!whole) { part[2 * lane] = mh; part[2 * lane + 1] = l; }
                     else if (p.lse) p.lse[row0 + lane] = (mh + log2f(l)) / kLog2E;
@@ -632,14 +657,15 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 constexpr int HM = HB / F;                        // heads of this thread
                 const int h1 = F == 2 ? e * HM : 0;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row0 * D + d;
-                // (a sum is 0 or at least 1, a maximum's own weight, or infinite or NaN)
                 if (whole) {
 #pragma unroll
-                    for (int h = 0; h < HM; ++h)
-                        if (h1 + h < hb) {
-                            const float l = st[2 * HB + h1 + h];
-                            out[(h1 + h) * D] = __float2bfloat16_rn(l > 0.f ? __fdividef(acc[h], l) : (l == 0.f ? 0.f : l));
-                        }
+                    for (int h = 0; h < HM; h += 4) {
+                        float l[4];
+                        ld4(st + 2 * HB + h1 + h, l);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (h1 + h + j < hb) out[(h1 + h + j) * D] = __float2bfloat16_rn(acc[h + j] * l[j]);
+                    }
                 } else {
 #pragma unroll
                     for (int h = 0; h < HM; ++h)
