@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     __shared__ int s_n;
     const int n = blockIdx.x, hq = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, U = 8;
+    ptx::pdl_launch_dependents();    // what follows waits for this grid's end
     T *out = static_cast<T *>(p.out);
     const int64_t nt = tiles_of<TILE>(p, n);
     if (nt == 0) {
@@ -391,23 +392,48 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     if (b0 == b1) return;
     // CTA b0 starts the item (slot 1), the others go on with it (slot 0)
     auto part = [&](int b) { return p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB); };
-    float m = -INFINITY;
-    for (int b = b0 + lane; b <= b1; b += 32) m = fmaxf(m, part(b)[2 * g]);
+    // (maxima and sums lie in pairs, outputs 16 bytes apart: a part starts on 16 bytes)
+    auto pair = [&](int b) { return b <= b1 ? *reinterpret_cast<const float2 *>(part(b) + 2 * g) : make_float2(-INFINITY, 0.f); };
+    auto rows = [&](int b, float (&x)[E]) {
+        const float *from = part(b) + HB * 2 + g * D + lane * E;
+        if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(from);
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        } else if constexpr (E == 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(from);
+            x[0] = v.x; x[1] = v.y;
+        } else {
+            x[0] = *from;
+        }
+    };
+    float x[U][E];                   // the first parts are on their way while the maxima are joined
+    const float2 first = pair(b0 + lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (b0 + u <= b1) rows(b0 + u, x[u]);
+    float m = first.x;
+    for (int b = b0 + 32 + lane; b <= b1; b += 32) m = fmaxf(m, pair(b).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float mu = m == -INFINITY ? 0.f : m;
     float l = 0.f, a[E] = {};
     for (int c0 = b0; c0 <= b1; c0 += 32) {
-        const int b = c0 + lane;
-        const float f = b <= b1 ? exp2f(part(b)[2 * g] - mu) : 0.f;
-        l += b <= b1 ? part(b)[2 * g + 1] * f : 0.f;
+        const float2 ml = c0 == b0 ? first : pair(c0 + lane);
+        const float f = c0 + lane <= b1 ? exp2f(ml.x - mu) : 0.f;
+        l += c0 + lane <= b1 ? ml.y * f : 0.f;
         const int cnt = min(32, b1 - c0 + 1);
-#pragma unroll 8
-        for (int i = 0; i < cnt; ++i) {
-            const float *x = part(c0 + i) + HB * 2 + g * D + lane * E;
-            const float w = __shfl_sync(0xffffffffu, f, i);
+        for (int i0 = 0; i0 < cnt; i0 += U) {
+            if (c0 != b0 || i0 > 0)
 #pragma unroll
-            for (int j = 0; j < E; ++j) a[j] = fmaf(x[j], w, a[j]);
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u < cnt) rows(c0 + i0 + u, x[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < cnt) {
+                    const float w = __shfl_sync(0xffffffffu, f, i0 + u);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) a[j] = fmaf(x[u][j], w, a[j]);
+                }
         }
     }
 #pragma unroll
