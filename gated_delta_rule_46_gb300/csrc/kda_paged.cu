@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     if (hq >= p.Hq) return;
     const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / HB, g = gi % HB;
     const int64_t s = sp.cum * items + item * nt, e = s + nt;
-    const int b0 = (int)(((s + 1) * sp.g - 1) / sp.W), b1 = (int)((e * sp.g - 1) / sp.W);
+    const int b0 = (int)quotient((s + 1) * sp.g - 1, sp.W), b1 = (int)quotient(e * sp.g - 1, sp.W);
     if (b0 == b1) return;
     // CTA b0 starts the item (slot 1), the others go on with it (slot 0)
     auto part = [&](int b) { return p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB); };

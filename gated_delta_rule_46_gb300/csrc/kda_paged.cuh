@@ -31,6 +31,11 @@ __device__ __forceinline__ int clamp_len(const PagedParams &p, int n, bool tell)
     return c;
 }
 
+// a / b of numbers >= 0, in 32 bits where they fit (64-bit division is a long loop).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Tiles of one item of sequence n.
 template <int TILE>
 __device__ __forceinline__ int64_t tiles_of(const PagedParams &p, int n) {
@@ -68,7 +73,7 @@ __device__ Split find_split(const PagedParams &p, int items, int grid, int b, in
     r.n = n;
     r.cum = 0;
     if (b >= 0 && b >= r.g) return r;
-    const int64_t w0 = b >= 0 ? (int64_t)b * r.W / r.g : 0;
+    const int64_t w0 = b >= 0 ? quotient((int64_t)b * r.W, r.g) : 0;
     for (int i = n0; i < n1; ++i) {
         const int64_t ti = tiles_of<TILE>(p, i);
         if (b >= 0 ? (w0 >= c * items && w0 < (c + ti) * items) : i == n) {

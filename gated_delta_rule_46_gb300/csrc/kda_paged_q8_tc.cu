@@ -161,24 +161,25 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
 
+    if (threadIdx.x < NBAR) {         // what needs nothing of the kernels before overlaps them
+        const int i = threadIdx.x;
+        int count = 1;
+        if (i >= SCALES && i < SD) count = 32;
+        else if (i >= IREADY && i < IFREE) count = 4 * NG;
+        else if ((i >= SFREE && i < PVD) || (i >= OFREE && i < QFULL) || i >= IFREE) count = 4;
+        ptx::mbar_init(&bar[i], count);
+        ptx::fence_mbar_init();
+    }
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        ptx::prefetch_tensormap(&mk);
+        ptx::prefetch_tensormap(&mv);
+    }
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TOK>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
     empty_sequences<__nv_bfloat16, TOK>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NBAR; ++i) {
-            int count = 1;
-            if (i >= SCALES && i < SD) count = 32;
-            else if (i >= IREADY && i < IFREE) count = 4 * NG;
-            else if ((i >= SFREE && i < PVD) || (i >= OFREE && i < QFULL) || i >= IFREE) count = 4;
-            ptx::mbar_init(&bar[i], count);
-        }
-        ptx::fence_mbar_init();
-        s_abort = 0;
-        ptx::prefetch_tensormap(&mk);
-        ptx::prefetch_tensormap(&mv);
-    }
     if (warp == L::MMA_S) {
         ptx::tmem_alloc(&s_tmem, L::cols);
         ptx::tmem_relinquish();

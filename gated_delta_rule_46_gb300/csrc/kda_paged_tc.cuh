@@ -21,14 +21,14 @@ struct WalkOf {
     int n, item, items, len, raw, ahead;      // len: raw, clamped to the table
     __device__ void start(const PagedParams &p, const Split &sp, int items_) {
         items = items_;
-        w = (int64_t)blockIdx.x * sp.W / sp.g;
-        w1 = (int64_t)(blockIdx.x + 1) * sp.W / sp.g;
+        w = quotient((int64_t)blockIdx.x * sp.W, sp.g);
+        w1 = quotient((int64_t)(blockIdx.x + 1) * sp.W, sp.g);
         n = sp.n;
         raw = p.lens[n];
         len = clamped(p, raw);
         ahead = n + 1 < p.N ? p.lens[n + 1] : 0;
         nt = (len + TILE - 1) / TILE;
-        item = (int)((w - sp.cum * items) / nt);
+        item = (int)quotient(w - sp.cum * items, nt);
         tile = (w - sp.cum * items) - item * nt;
     }
     __device__ bool more() const { return w < w1; }
