@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     __shared__ int s_n;
     const int n = blockIdx.x, hq = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
-    constexpr int E = D / 32, U = 8;
+    constexpr int E = D / 32, U = 16;
     ptx::pdl_launch_dependents();    // what follows waits for this grid's end
     T *out = static_cast<T *>(p.out);
     const int64_t nt = tiles_of<TILE>(p, n);
