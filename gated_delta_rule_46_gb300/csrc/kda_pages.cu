@@ -153,12 +153,15 @@ __device__ int take_free(const PageTable &p, int need, const List &list, Scan &s
     return min(found, need);
 }
 
-// One holder of a page less; a page that had none is left so.
+// One holder of a page less; a page that had none is left so, and so is a count below 0.
 __device__ __forceinline__ void give_back(const PageTable &p, int id) {
     if (id < 0) return;
     if (id >= p.num_pages) {
         report_status(p.status, KDA_ERR_INVALID_ARG);
-    } else if (atomicSub(p.refs + id, 1) <= 0) {
+        return;
+    }
+    if (ldcg(p.refs + id) < 0) return;
+    if (atomicSub(p.refs + id, 1) <= 0) {
         atomicAdd(p.refs + id, 1);
         report_status(p.status, KDA_ERR_INVALID_ARG);
     }
@@ -345,7 +348,8 @@ __device__ __forceinline__ void fork_rows(const PageTable &p, int forks, const F
         if (e < r.z) {
             id = p.table[(int64_t)r.x * p.max_pages + e];
             if (id >= 0 && id < p.num_pages) {
-                atomicAdd(p.refs + id, 1);
+                // (a count below 0 is not kept: it would come to 0, and the page be handed out)
+                if (ldcg(p.refs + id) >= 0) atomicAdd(p.refs + id, 1);
             } else {
                 report_status(p.status, KDA_ERR_INVALID_ARG);
                 id = -1;

@@ -199,7 +199,9 @@ kda_status_t kda_paged_decode(const void *q, int64_t ldq, const void *k_cache, c
  * any other from 2^-126 to 2^126, which is rounded up to a power of two; another is
  * recorded in *status and the block's scale taken from the new tokens alone.  A
  * block that starts at or behind start_pos is begun afresh, whatever it holds.
- * What lies in a block behind the new tokens is left.
+ * What lies in a block behind the new tokens is left.  No two sequences of a call
+ * write to the same page (kda_pages_fork copies a page that rows would share and
+ * write to).
  */
 kda_status_t kda_paged_append_q8(const void *k, int64_t ldk, const void *v, int64_t ldv, void *k_cache,
                                  void *v_cache, float *k_scale, float *v_scale, int num_pages,

@@ -13,7 +13,9 @@
  *   held        [num_rows] int32: pages that each row holds
  *   refs        [num_pages] int32: how many table entries (and other holders, which
  *               the caller may add) hold each page.  A page is free where it is 0;
- *               a negative count keeps it from ever being handed out
+ *               a negative count keeps it from ever being handed out, and these
+ *               calls leave it as it is (pages of the caller's own, which rows may
+ *               share for good)
  * All start as -1, 0 and 0.  Free pages are handed out lowest first, rows and
  * pairs served in order: results depend on the arguments alone.
  *

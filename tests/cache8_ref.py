@@ -105,9 +105,9 @@ class Pages:
             if w is not None and w < self.held[i]:
                 for e in range(w, self.held[i]):
                     p, self.table[i][e] = self.table[i][e], -1
-                    if p >= len(self.refs) or (p >= 0 and self.refs[p] <= 0):
+                    if p >= len(self.refs) or (p >= 0 and self.refs[p] == 0):
                         self.errors.add("arg")
-                    elif p >= 0:
+                    elif p >= 0 and self.refs[p] > 0:
                         self.refs[p] -= 1
                 self.held[i] = w
         free = self.free()
@@ -156,7 +156,7 @@ class Pages:
             for e in range(n // self.ps):
                 p = self.table[a][e]
                 if 0 <= p < len(self.refs):
-                    self.refs[p] += 1
+                    self.refs[p] += self.refs[p] >= 0
                 else:
                     self.errors.add("arg")
                     p = -1

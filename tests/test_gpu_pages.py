@@ -109,6 +109,23 @@ def test_resize_malformed():
     assert 3 not in b.table[0].tolist()
 
 
+def test_pages_kept_from_use_are_shared():
+    """A negative count stays what it is: rows that share such a page give it back, and it is never handed out."""
+    dev = need_gpu()
+    b = Both(6, 4, 14, 16, dev)
+    b.m.refs[2] = b.m.refs[5] = -1
+    b.m.refs[7] = -2 ** 31
+    b.m.table[0][:3], b.m.held[0] = [2, 7, 5], 3
+    b.lens[0] = 40
+    b.load()
+    b.fork([0, 0, 0], [1, 2, 3])
+    b.resize([-1, 0, 60, 16, 64, 64])
+    b.resize([0] * 6)
+    assert b.refs.tolist() == [0, 0, -1, 0, 0, -1, 0, -2 ** 31] + [0] * 6
+    b.resize([64] * 6)
+    assert not {2, 5, 7} & set(b.table.flatten().tolist())
+
+
 @pytest.mark.parametrize("rows,cols,pages,ps", [(1, 1, 1, 1), (3000, 3, 5000, 64), (17, 5000, 70001, 1), (9000, 20, 140000, 1024)])
 def test_resize_sizes(rows, cols, pages, ps):
     """More rows and pages than one round of the kernel takes, rows of thousands of pages, pages of one token."""
