@@ -153,18 +153,23 @@ __device__ int take_free(const PageTable &p, int need, const List &list, Scan &s
     return min(found, need);
 }
 
-// One holder of a page less; a page that had none is left so, and so is a count below 0.
-__device__ __forceinline__ void give_back(const PageTable &p, int id) {
-    if (id < 0) return;
-    if (id >= p.num_pages) {
-        report_status(p.status, KDA_ERR_INVALID_ARG);
-        return;
-    }
-    if (ldcg(p.refs + id) < 0) return;
-    if (atomicSub(p.refs + id, 1) <= 0) {
-        atomicAdd(p.refs + id, 1);
-        report_status(p.status, KDA_ERR_INVALID_ARG);
-    }
+// One holder less for each of the pages; one that had none is left so, and so is a count below 0.  (Loads and atomics go
+// ahead of what is done with their results, so that all of a thread's are under way at a time.)
+template <int U>
+__device__ __forceinline__ void give_back(const PageTable &p, const int (&id)[U]) {
+    int count[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) count[u] = id[u] >= 0 && id[u] < p.num_pages ? ldcg(p.refs + id[u]) : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (count[u] >= 0) count[u] = atomicSub(p.refs + id[u], 1);
+        else count[u] = id[u] < p.num_pages ? 1 : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (count[u] <= 0) {
+            if (id[u] < p.num_pages) atomicAdd(p.refs + id[u], 1);
+            report_status(p.status, KDA_ERR_INVALID_ARG);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -210,17 +215,17 @@ __global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * NT;
-                if (i >= total) break;
+                id[u] = -1;
+                entry[u] = nullptr;
+                if (i >= total) continue;
                 const int row = flat.row(i);
                 entry[u] = p.table + (c + row) * p.max_pages + s_first[row] + i - flat.before[row];
                 id[u] = *entry[u];
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u * NT >= total) break;
-                *entry[u] = -1;
-                give_back(p, id[u]);
-            }
+            for (int u = 0; u < U; ++u)
+                if (entry[u]) *entry[u] = -1;
+            give_back(p, id);
         }
         if (x.want < x.held) p.held[c + tid] = x.want;
         int sum;
