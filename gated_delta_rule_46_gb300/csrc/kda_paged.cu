@@ -98,10 +98,18 @@ cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st) {
 // heads each, take 783 us: 5.5 TB/s, 81 % of the copy rate.  With 8 query heads each
 // it is 59 %, as then two rounds are all that the registers hold and the FMAs of a
 // byte are twice as many; bf16 pages of 4 tokens, 52 %.
+//   A cache in 8 bits with float32 queries keeps float32's precision here, which the
+// tensor cores' two e4m3 parts do not.  Its lanes take sixteen channels each, for loads
+// of 16 bytes, half of the shuffles and products two at a time, and items of up to four
+// heads: 64 rows of up to 4096 tokens, 8 key-value heads of 128 channels, take 107 us
+// with 1 query head each (219 with eight channels and items of four heads), 186 with 4
+// (228) and 351 with 8 (332 in items of eight heads), 0.37, 0.21 and 0.11 of the copy
+// rate: conversions and products of a byte bound it, and each item's first loads and
+// joins, which nothing overlaps.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;
 
-// Eight channels of a row as they are loaded: of lane l of the d / 8 that share it.
+// Channels of a row as they are loaded, eight or, of e4m3, sixteen: of lane l of those that share it.
 template <typename T, int D>
 struct Ch8;
 template <int D>
@@ -133,15 +141,15 @@ struct Ch8<__nv_bfloat16, D> {
 };
 template <int D>
 struct Ch8<__nv_fp8_e4m3, D> {
-    uint2 u = {};
-    static __device__ int channel(int l, int e) { return l * 8 + e; }
+    uint4 u = {};
+    static __device__ int channel(int l, int e) { return l * 16 + e; }
     __device__ void load(const __nv_fp8_e4m3 *row, int l) {
-        u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(row) + l * 8);
+        u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(row) + l * 16);
     }
-    __device__ void get(float (&x)[8]) const {
-        const uint32_t w[2] = {u.x, u.y};
+    __device__ void get(float (&x)[16]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const float2 f = e4m3x2_to_f2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
             x[2 * i] = f.x;
             x[2 * i + 1] = f.y;
@@ -149,12 +157,44 @@ struct Ch8<__nv_fp8_e4m3, D> {
     }
 };
 
+// Sums of products over a lane's channels, and products added to its outputs; of sixteen channels two at a time.
+template <int CH>
+__device__ __forceinline__ float dot(const float (&x)[CH], const float (&q)[CH]) {
+    if constexpr (CH == 16) {
+        float2 a = __fmul2_rn(make_float2(x[0], x[1]), make_float2(q[0], q[1]));
+#pragma unroll
+        for (int e = 2; e < CH; e += 2) a = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(q[e], q[e + 1]), a);
+        return a.x + a.y;
+    } else {
+        float a = x[0] * q[0];
+#pragma unroll
+        for (int e = 1; e < CH; ++e) a = fmaf(x[e], q[e], a);
+        return a;
+    }
+}
+template <int CH>
+__device__ __forceinline__ void add(float (&acc)[CH], float w, const float (&x)[CH]) {
+    if constexpr (CH == 16) {
+#pragma unroll
+        for (int e = 0; e < CH; e += 2) {
+            const float2 a = __ffma2_rn(make_float2(w, w), make_float2(x[e], x[e + 1]), make_float2(acc[e], acc[e + 1]));
+            acc[e] = a.x;
+            acc[e + 1] = a.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < CH; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    }
+}
+
 // T: queries and outputs; C: the cache.
 template <typename C, int D, int HB>
 struct Simt {
-    static constexpr int WARPS = HB == 4 ? 10 : 8;                         // registers for as many
-    static constexpr int U = HB == 4 || sizeof(C) <= 2 ? 4 : 2;            // rounds between corrections
-    static constexpr int LPT = D / 8, TPW = 32 / LPT;                      // lanes per token, tokens per warp
+    static constexpr int CH = sizeof(C) == 1 ? 16 : 8;                     // channels of a lane
+    // registers for as many
+    static constexpr int WARPS = CH == 16 ? (HB == 4 ? 8 : HB == 2 ? 12 : 16) : HB == 4 ? 10 : 8;
+    static constexpr int U = HB <= 4 || sizeof(C) <= 2 ? 4 : 2;            // rounds between corrections
+    static constexpr int LPT = D / CH, TPW = 32 / LPT;                     // lanes per token, tokens per warp
     static constexpr uint32_t smem = sizeof(float) * WARPS * HB * (D + 2);
 };
 
@@ -162,7 +202,7 @@ template <typename T, typename C, int D, int HB>
 __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_simt_kernel(const PagedParams p) {
     using S = Simt<C, D, HB>;
     constexpr bool kScaled = sizeof(C) == 1;          // codes with a scale for each block of tokens
-    constexpr int TILE = kTile, U = S::U, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
+    constexpr int TILE = kTile, U = S::U, CH = S::CH, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
     extern __shared__ float sm[];                     // of each warp: m and l [HB], outputs [HB][D]
     __shared__ int64_t s_sum[257];
     __shared__ int s_n;
@@ -180,6 +220,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
     int item = (int)((w - sp.cum * items) / nt);
     int64_t tile = (w - sp.cum * items) - item * nt;
     const float sc2 = p.scale * kLog2E;
+    const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 4 == 0;
     const C *kc = static_cast<const C *>(p.kc), *vc = static_cast<const C *>(p.vc);
 
     while (w < w1) {
@@ -191,21 +232,36 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
         const int32_t *table = p.table + (int64_t)n * p.max_pages;
         int t = (int)(first * TILE) + warp * S::TPW + lane / LPT;         // this lane's token of the first round
 
-        float q[HB][8];
+        float q[HB][CH];
+        if (kScaled && sizeof(T) == 4 && q16) {           // (a lane's channels are neighbours)
 #pragma unroll
-        for (int h = 0; h < HB; ++h)
+            for (int h = 0; h < HB; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                q[h][e] = h < hb ? to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)(hq0 + h) * D +
-                                                                      Ch8<C, D>::channel(l8, e)]) * sc2
-                                 : 0.f;
-        float m[HB], l[HB], acc[HB][8];
+                for (int e = 0; e < CH; e += 4) {
+                    const float4 x = h < hb ? *reinterpret_cast<const float4 *>(static_cast<const T *>(p.q) + (int64_t)n * p.ldq +
+                                                                                (int64_t)(hq0 + h) * D + l8 * CH + e)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    q[h][e] = x.x * sc2;
+                    q[h][e + 1] = x.y * sc2;
+                    q[h][e + 2] = x.z * sc2;
+                    q[h][e + 3] = x.w * sc2;
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int e = 0; e < CH; ++e)
+                    q[h][e] = h < hb ? to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)(hq0 + h) * D +
+                                                                          Ch8<C, D>::channel(l8, e)]) * sc2
+                                     : 0.f;
+        }
+        float m[HB], l[HB], acc[HB][CH];
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
             m[h] = -INFINITY;
             l[h] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
+            for (int e = 0; e < CH; ++e) acc[h][e] = 0.f;
         }
 
         // pages of the U rounds from token t on (-1: no token), and rows of a cache on them
@@ -248,13 +304,11 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
             float s[U][HB];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float x[8];
+                float x[CH];
                 k[u].get(x);
 #pragma unroll
                 for (int h = 0; h < HB; ++h) {
-                    float a = x[0] * q[h][0];
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) a = fmaf(x[e], q[h][e], a);
+                    const float a = dot(x, q[h]);
                     s[u][h] = kScaled ? a * fk[u] : a;
                 }
             }
@@ -277,7 +331,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
                 m[h] = mn;
                 l[h] *= f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[h][e] *= f;
+                for (int e = 0; e < CH; ++e) acc[h][e] *= f;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     s[u][h] = tc::ex2(s[u][h] - mu);
@@ -286,14 +340,10 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float x[8];
+                float x[CH];
                 v[u].get(x);
 #pragma unroll
-                for (int h = 0; h < HB; ++h) {
-                    const float w = kScaled ? s[u][h] * fv[u] : s[u][h];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(w, x[e], acc[h][e]);
-                }
+                for (int h = 0; h < HB; ++h) add(acc[h], kScaled ? s[u][h] * fv[u] : s[u][h], x);
             }
             fetch(vc, p.vs, t + U * STEP, pn, v, fv);
 #pragma unroll
@@ -312,7 +362,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
                 m[h] = mn;
                 l[h] = fmaf(l[h], f, lo * fo);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < CH; ++e)
                     acc[h][e] = fmaf(acc[h][e], f, __shfl_xor_sync(0xffffffffu, acc[h][e], o) * fo);
             }
         __syncthreads();                              // the item before is written
@@ -322,7 +372,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
             for (int h = 0; h < HB; ++h) {
                 if (lane == 0) { mine[2 * h] = m[h]; mine[2 * h + 1] = l[h]; }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mine[2 * HB + h * D + Ch8<C, D>::channel(l8, e)] = acc[h][e];
+                for (int e = 0; e < CH; ++e) mine[2 * HB + h * D + Ch8<C, D>::channel(l8, e)] = acc[h][e];
             }
         __syncthreads();
         const bool whole = first == 0 && last == nt;
@@ -346,7 +396,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_si
                     from_f32<T>(ls > 0.f ? a / ls : (ls == 0.f ? 0.f : ls));
                 if (c == 0 && p.lse) p.lse[(int64_t)n * p.Hq + hq0 + h] = (mx + log2f(ls)) / kLog2E;
             } else {
-                part[HB * 2 + h * D + c] = a;
+                part[part_head(HB) + h * D + c] = a;
                 if (c == 0) { part[2 * h] = mx; part[2 * h + 1] = ls; }
             }
         }
@@ -395,7 +445,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     // (maxima and sums lie in pairs, outputs 16 bytes apart: a part starts on 16 bytes)
     auto pair = [&](int b) { return b <= b1 ? *reinterpret_cast<const float2 *>(part(b) + 2 * g) : make_float2(-INFINITY, 0.f); };
     auto rows = [&](int b, float (&x)[E]) {
-        const float *from = part(b) + HB * 2 + g * D + lane * E;
+        const float *from = part(b) + part_head(HB) + g * D + lane * E;
         if constexpr (E == 4) {
             const float4 v = *reinterpret_cast<const float4 *>(from);
             x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
@@ -474,8 +524,7 @@ static int grid_tc(int N, int64_t max_tokens, int Hkv, int G) {
 // Query heads per item of the CUDA-core form: what its registers hold, and four where there are no more (float32, 64 rows
 // of 8192 tokens, 2 key-value heads, 4 query heads each: 208 us, 279 in items of eight).
 static int heads_simt(int G) { return G <= 4 ? 4 : 8; }
-static int grid_simt(int N, int64_t max_tokens, int Hkv, int G) {
-    const int HB = heads_simt(G);
+static int grid_simt(int N, int64_t max_tokens, int Hkv, int G, int HB) {
     return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTile, sm_count());
 }
 
@@ -483,7 +532,7 @@ size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, 
     const int G = Hq / Hkv;
     if (max_tokens <= (kTile < kTileTc ? kTile : kTileTc)) return 16;     // one tile: nothing to join
     const size_t tc = (size_t)grid_tc(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_tc(G));
-    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_simt(G));
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, heads_simt(G)) * 2 * part_floats(d, heads_simt(G));
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 
@@ -494,18 +543,18 @@ static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
     auto *kernel = paged_decode_simt_kernel<T, C, D, HB>;
     cudaError_t e = allow_smem<paged_decode_simt_kernel<T, C, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
-    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
+    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, HB);
     if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
     return launch_join<T, D, kTile, HB>(p, grid, st);
 }
 
-template <typename T, typename C = T>
+template <typename T>
 static cudaError_t paged_dispatch(const PagedParams &p, int d, cudaStream_t st) {
     const bool four = heads_simt(p.G) == 4;
     switch (d) {
-        case 32: return four ? paged_simt<T, C, 32, 4>(p, st) : paged_simt<T, C, 32, 8>(p, st);
-        case 64: return four ? paged_simt<T, C, 64, 4>(p, st) : paged_simt<T, C, 64, 8>(p, st);
-        case 128: return four ? paged_simt<T, C, 128, 4>(p, st) : paged_simt<T, C, 128, 8>(p, st);
+        case 32: return four ? paged_simt<T, T, 32, 4>(p, st) : paged_simt<T, T, 32, 8>(p, st);
+        case 64: return four ? paged_simt<T, T, 64, 4>(p, st) : paged_simt<T, T, 64, 8>(p, st);
+        case 128: return four ? paged_simt<T, T, 128, 4>(p, st) : paged_simt<T, T, 128, 8>(p, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -532,12 +581,25 @@ static int grid_q8(int N, int64_t max_tokens, int Hkv, int G, int d) {
     return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTileTc * tokens_per_row(d, HB), sm_count());
 }
 
+// Of its CUDA-core form: the four that the registers hold with sixteen channels a lane, or the one or two that there are.
+static int heads_simt_q8(int G) { return G <= 2 ? G : 4; }
+template <typename T, int D>
+static cudaError_t paged_simt_q8(const PagedParams &p, cudaStream_t st) {
+    using C = __nv_fp8_e4m3;
+    const int HB = heads_simt_q8(p.G);
+    return HB == 1 ? paged_simt<T, C, D, 1>(p, st) : HB == 2 ? paged_simt<T, C, D, 2>(p, st) : paged_simt<T, C, D, 4>(p, st);
+}
+template <typename T>
+static cudaError_t paged_dispatch_q8(const PagedParams &p, int d, cudaStream_t st) {
+    return d == 32 ? paged_simt_q8<T, 32>(p, st) : d == 64 ? paged_simt_q8<T, 64>(p, st) : paged_simt_q8<T, 128>(p, st);
+}
+
 size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
-    const size_t simt = paged_decode_workspace_bytes(N, max_tokens, Hq, Hkv, d);
     if (max_tokens <= kTile) return 0;            // (an item is one tile in either form: nothing to join)
-    const int G = Hq / Hkv;
-    const size_t tc = sizeof(float) * grid_q8(N, max_tokens, Hkv, G, d) * 2 * part_floats(d, heads_q8(G));
-    return tc > simt ? tc : simt;
+    const int G = Hq / Hkv, HB = heads_simt_q8(G);
+    const size_t tc = (size_t)grid_q8(N, max_tokens, Hkv, G, d) * 2 * part_floats(d, heads_q8(G));
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, HB) * 2 * part_floats(d, HB);
+    return sizeof(float) * (tc > simt ? tc : simt);
 }
 
 template <int D>
@@ -551,7 +613,7 @@ cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaS
     // (row coordinates of TMA copies are 32-bit)
     const bool tc = bf16 && p.num_pages > 0 && p.max_pages > 0 &&
                     ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
-    if (!tc) return bf16 ? paged_dispatch<__nv_bfloat16, __nv_fp8_e4m3>(p, d, st) : paged_dispatch<float, __nv_fp8_e4m3>(p, d, st);
+    if (!tc) return bf16 ? paged_dispatch_q8<__nv_bfloat16>(p, d, st) : paged_dispatch_q8<float>(p, d, st);
     const int HB = heads_q8(p.G), grid = grid_q8(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, d);
     PagedParams pt = p;
     pt.expire = take_layers_expire(KDA_TESTING_PAGED);

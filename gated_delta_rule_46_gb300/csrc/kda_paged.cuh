@@ -108,8 +108,9 @@ __device__ __forceinline__ void empty_sequences(const PagedParams &p, int D) {
 }
 
 // One partial result of an item of HB query heads: m, l (base-2 logarithms) per
-// head, then a[d] per head.
-__host__ __device__ constexpr int part_floats(int d, int HB) { return HB * (d + 2); }
+// head, then, from 16 bytes on, a[d] per head.
+__host__ __device__ constexpr int part_head(int HB) { return (HB * 2 + 3) & ~3; }
+__host__ __device__ constexpr int part_floats(int d, int HB) { return part_head(HB) + HB * d; }
 
 // bf16, d = 64 or 128, pages of at least 8 tokens: the tensor-core form and the
 // grid it runs on, with HB query heads per item.
