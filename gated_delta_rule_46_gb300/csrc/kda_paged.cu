@@ -187,19 +187,22 @@ __device__ __forceinline__ void add(float (&acc)[CH], float w, const float (&x)[
     }
 }
 
+constexpr int ctas_q8(int HB) { return HB == 4 ? 2 : HB == 2 ? 3 : 4; }
+
 // T: queries and outputs; C: the cache.
 template <typename C, int D, int HB>
 struct Simt {
     static constexpr int CH = sizeof(C) == 1 ? 16 : 8;                     // channels of a lane
     // registers for as many
-    static constexpr int WARPS = CH == 16 ? (HB == 4 ? 8 : HB == 2 ? 12 : 16) : HB == 4 ? 10 : 8;
+    static constexpr int CTAS = CH == 16 ? ctas_q8(HB) : 1;                // of an SM
+    static constexpr int WARPS = CH == 16 ? 4 : HB == 4 ? 10 : 8;
     static constexpr int U = HB <= 4 || sizeof(C) <= 2 ? 4 : 2;            // rounds between corrections
     static constexpr int LPT = D / CH, TPW = 32 / LPT;                     // lanes per token, tokens per warp
     static constexpr uint32_t smem = sizeof(float) * WARPS * HB * (D + 2);
 };
 
 template <typename T, typename C, int D, int HB>
-__global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, 1) paged_decode_simt_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CTAS) paged_decode_simt_kernel(const PagedParams p) {
     using S = Simt<C, D, HB>;
     constexpr bool kScaled = sizeof(C) == 1;          // codes with a scale for each block of tokens
     constexpr int TILE = kTile, U = S::U, CH = S::CH, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
@@ -524,15 +527,15 @@ static int grid_tc(int N, int64_t max_tokens, int Hkv, int G) {
 // Query heads per item of the CUDA-core form: what its registers hold, and four where there are no more (float32, 64 rows
 // of 8192 tokens, 2 key-value heads, 4 query heads each: 208 us, 279 in items of eight).
 static int heads_simt(int G) { return G <= 4 ? 4 : 8; }
-static int grid_simt(int N, int64_t max_tokens, int Hkv, int G, int HB) {
-    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTile, sm_count());
+static int grid_simt(int N, int64_t max_tokens, int Hkv, int G, int HB, int ctas) {
+    return grid_for(N, max_tokens, Hkv * ((G + HB - 1) / HB), kTile, sm_count() * ctas);
 }
 
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
     const int G = Hq / Hkv;
     if (max_tokens <= (kTile < kTileTc ? kTile : kTileTc)) return 16;     // one tile: nothing to join
     const size_t tc = (size_t)grid_tc(N, max_tokens, Hkv, G) * 2 * part_floats(d, heads_tc(G));
-    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, heads_simt(G)) * 2 * part_floats(d, heads_simt(G));
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, heads_simt(G), 1) * 2 * part_floats(d, heads_simt(G));
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 
@@ -543,7 +546,7 @@ static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
     auto *kernel = paged_decode_simt_kernel<T, C, D, HB>;
     cudaError_t e = allow_smem<paged_decode_simt_kernel<T, C, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
-    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, HB);
+    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, HB, S::CTAS);
     if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
     return launch_join<T, D, kTile, HB>(p, grid, st);
 }
@@ -598,7 +601,7 @@ size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hk
     if (max_tokens <= kTile) return 0;            // (an item is one tile in either form: nothing to join)
     const int G = Hq / Hkv, HB = heads_simt_q8(G);
     const size_t tc = (size_t)grid_q8(N, max_tokens, Hkv, G, d) * 2 * part_floats(d, heads_q8(G));
-    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, HB) * 2 * part_floats(d, HB);
+    const size_t simt = (size_t)grid_simt(N, max_tokens, Hkv, G, HB, ctas_q8(HB)) * 2 * part_floats(d, HB);
     return sizeof(float) * (tc > simt ? tc : simt);
 }
 

@@ -42,16 +42,16 @@ __device__ __forceinline__ int64_t tiles_of(const PagedParams &p, int n) {
     return (clamp_len(p, n, false) + TILE - 1) / TILE;
 }
 
-// Block-wide (the first 256 threads scan): the totals, and with b >= 0 the sequence in which
+// Block-wide (256 threads scan, or all where there are less): the totals, and with b >= 0 the sequence in which
 // CTA b's first tile lies; with b < 0 the sums before sequence `n`.
 template <int TILE>
 __device__ Split find_split(const PagedParams &p, int items, int grid, int b, int n, int64_t *s_sum /* 257 */,
                             int *s_n) {
-    const int tid = threadIdx.x;
-    const int per = (p.N + 255) / 256, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    const int tid = threadIdx.x, scan = min(256, (int)blockDim.x);
+    const int per = (p.N + scan - 1) / scan, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
     int64_t mine = 0;
     for (int i = n0; i < n1; ++i) mine += tiles_of<TILE>(p, i);
-    // inclusive scan over the 256 threads: within warps, then over the 8 warp sums
+    // inclusive scan over the threads: within warps, then over the warps' sums
     int64_t x = mine;
     const int lane = tid & 31, w = tid >> 5;
 #pragma unroll
@@ -62,7 +62,7 @@ __device__ Split find_split(const PagedParams &p, int items, int grid, int b, in
     if (lane == 31) s_sum[w] = x;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < scan / 32; ++i) {
         if (i < w) before += s_sum[i];
         total += s_sum[i];
     }
