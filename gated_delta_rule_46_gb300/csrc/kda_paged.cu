@@ -87,7 +87,7 @@ cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// CUDA-core form (float32 caches, d = 32, pages of under eight tokens): d / 8
+// CUDA-core form (float32 caches, d = 32, pages of under eight tokens; caches in 8 bits with float32 queries): d / 8
 // lanes share a token, eight channels each of its key, its value, the queries
 // and the outputs of HB heads, all in registers; a warp works on 256 / d tokens
 // at a time and on U such rounds between corrections of its maximum.  A round's
@@ -100,12 +100,13 @@ cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st) {
 // byte are twice as many; bf16 pages of 4 tokens, 52 %.
 //   A cache in 8 bits with float32 queries keeps float32's precision here, which the
 // tensor cores' two e4m3 parts do not.  Its lanes take sixteen channels each, for loads
-// of 16 bytes, half of the shuffles and products two at a time, and items of up to four
-// heads: 64 rows of up to 4096 tokens, 8 key-value heads of 128 channels, take 107 us
-// with 1 query head each (219 with eight channels and items of four heads), 186 with 4
-// (228) and 351 with 8 (332 in items of eight heads), 0.37, 0.21 and 0.11 of the copy
-// rate: conversions and products of a byte bound it, and each item's first loads and
-// joins, which nothing overlaps.
+// of 16 bytes, half of the shuffles and products two at a time; items have up to four
+// heads, and CTAs four warps, of which an SM holds two to four, so that one's first loads
+// and joins overlap another's tokens.  64 rows of up to 4096 tokens, 8 key-value heads of
+// 128 channels, take 72 us with 1 query head each (107 in one CTA of 16 warps an SM, 219
+// with eight channels a lane), 146 with 4 (186, 228), 274 with 8 (351, 332) and 527 with
+// 16: 0.55, 0.27, 0.15 and 0.08 of the copy rate.  Conversions and products of a byte
+// bound it (issue slots 52 % busy with the two warps a scheduler that registers allow).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;
 
