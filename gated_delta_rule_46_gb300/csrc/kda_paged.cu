@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
-    const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
+    const Split sp = find_split<TILE, (NT < 256 ? NT : 256)>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
     empty_sequences<T, TILE>(p, D);
     if ((int)blockIdx.x >= sp.g) return;
-    int64_t w = (int64_t)blockIdx.x * sp.W / sp.g;
-    const int64_t w1 = (int64_t)(blockIdx.x + 1) * sp.W / sp.g;
+    int64_t w = quotient((int64_t)blockIdx.x * sp.W, sp.g);
+    const int64_t w1 = quotient((int64_t)(blockIdx.x + 1) * sp.W, sp.g);
     int n = sp.n;
     int64_t nt = tiles_of<TILE>(p, n);
-    int item = (int)((w - sp.cum * items) / nt);
+    int item = (int)quotient(w - sp.cum * items, nt);
     int64_t tile = (w - sp.cum * items) - item * nt;
     const float sc2 = p.scale * kLog2E;
     const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 4 == 0;

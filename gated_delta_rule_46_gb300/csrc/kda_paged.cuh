@@ -42,13 +42,13 @@ __device__ __forceinline__ int64_t tiles_of(const PagedParams &p, int n) {
     return (clamp_len(p, n, false) + TILE - 1) / TILE;
 }
 
-// Block-wide (256 threads scan, or all where there are less): the totals, and with b >= 0 the sequence in which
+// Block-wide (the first SCAN threads scan): the totals, and with b >= 0 the sequence in which
 // CTA b's first tile lies; with b < 0 the sums before sequence `n`.
-template <int TILE>
+template <int TILE, int SCAN = 256>
 __device__ Split find_split(const PagedParams &p, int items, int grid, int b, int n, int64_t *s_sum /* 257 */,
                             int *s_n) {
-    const int tid = threadIdx.x, scan = min(256, (int)blockDim.x);
-    const int per = (p.N + scan - 1) / scan, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    const int tid = threadIdx.x;
+    const int per = (p.N + SCAN - 1) / SCAN, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
     int64_t mine = 0;
     for (int i = n0; i < n1; ++i) mine += tiles_of<TILE>(p, i);
     // inclusive scan over the threads: within warps, then over the warps' sums
@@ -62,7 +62,8 @@ __device__ Split find_split(const PagedParams &p, int items, int grid, int b, in
     if (lane == 31) s_sum[w] = x;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int i = 0; i < scan / 32; ++i) {
+#pragma unroll
+    for (int i = 0; i < SCAN / 32; ++i) {
         if (i < w) before += s_sum[i];
         total += s_sum[i];
     }
