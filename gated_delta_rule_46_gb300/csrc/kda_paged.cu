@@ -215,8 +215,10 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE, (NT < 256 ? NT : 256)>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    empty_sequences<T, TILE>(p, D);
-    if ((int)blockIdx.x >= sp.g) return;
+    if ((int)blockIdx.x >= sp.g) {
+        empty_sequences<T>(p, D);
+        return;
+    }
     int64_t w = quotient((int64_t)blockIdx.x * sp.W, sp.g);
     const int64_t w1 = quotient((int64_t)(blockIdx.x + 1) * sp.W, sp.g);
     int n = sp.n;
@@ -413,37 +415,43 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
             }
         }
     }
+    empty_sequences<T>(p, D);
 }
 
 // ---------------------------------------------------------------------------
-// Join: one warp per sequence and query head, eight heads per CTA.  Heads whose
-// item one CTA had whole are done already; a sequence without tokens gets
-// zeros.  A long row has a part from nearly every CTA: their maxima and sums
-// are read a part per lane and joined by shuffles, then the weighted rows are
-// summed in order, with as many loads under way as the unrolling gives.
+// Join: a CTA for each border between two CTAs' tiles.  An item that its border
+// is the first to cut is joined there, a warp per head; so there are as many CTAs
+// as items can be cut, whatever the batch (256 rows of up to 600 tokens, 16 query
+// heads: 93 us with a CTA for every row and eight heads, 87 so).  A long row has a
+// part from nearly every CTA: their maxima and sums are read a part per lane and
+// joined by shuffles, then the weighted rows are summed in order, with as many
+// loads under way as the unrolling gives.
 // ---------------------------------------------------------------------------
 template <typename T, int D, int TILE, int HB>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int grid) {
     __shared__ int64_t s_sum[257];
     __shared__ int s_n;
-    const int n = blockIdx.x, hq = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int b = blockIdx.x + 1, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     constexpr int E = D / 32, U = 16;
     ptx::pdl_launch_dependents();    // what follows waits for this grid's end
-    T *out = static_cast<T *>(p.out);
-    const int64_t nt = tiles_of<TILE>(p, n);
-    if (nt == 0) {
-        ptx::pdl_wait();         // this grid's end stands for the one before it too
-        if (blockIdx.y == 0) empty_sequence<T>(p, n, D);
-        return;
+    const Split sp = find_split<TILE>(p, items, grid, b, 0, s_sum, &s_n);
+    // the item of the border's tile, from tile s on
+    int64_t s = 0, nt = 0;
+    int item = 0;
+    bool cut = b < sp.g;
+    if (cut) {
+        const int64_t w = quotient((int64_t)b * sp.W, sp.g), at = w - sp.cum * items;
+        nt = tiles_of<TILE>(p, sp.n);
+        item = (int)quotient(at, nt);
+        s = sp.cum * items + item * nt;
+        cut = w > s && quotient((int64_t)(b - 1) * sp.W, sp.g) <= s;
     }
-    const Split sp = find_split<TILE>(p, items, grid, -1, n, s_sum, &s_n);
-    ptx::pdl_wait();             // the partial results
-    if (hq >= p.Hq) return;
-    const int kvh = hq / p.G, gi = hq % p.G, item = kvh * nb + gi / HB, g = gi % HB;
-    const int64_t s = sp.cum * items + item * nt, e = s + nt;
-    const int b0 = (int)quotient((s + 1) * sp.g - 1, sp.W), b1 = (int)quotient(e * sp.g - 1, sp.W);
-    if (b0 == b1) return;
+    ptx::pdl_wait();                 // the partial results; this grid's end stands for the one before it too
+    const int kvh = item / nb, g0 = (item - kvh * nb) * HB, hq = kvh * p.G + g0 + h;
+    if (!cut || h >= min(HB, p.G - g0)) return;
+    const int n = sp.n, g = h, b0 = b - 1, b1 = (int)quotient((s + nt) * sp.g - 1, sp.W);
+    T *out = static_cast<T *>(p.out);
     // CTA b0 starts the item (slot 1), the others go on with it (slot 0)
     auto part = [&](int b) { return p.part + ((int64_t)b * 2 + (b == b0 ? 1 : 0)) * part_floats(D, HB); };
     // (maxima and sums lie in pairs, outputs 16 bytes apart: a part starts on 16 bytes)
@@ -500,9 +508,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
 
 template <typename T, int D, int TILE, int HB>
 static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) {
-    if (p.lone) return cudaSuccess;
-    return launch_dependent(paged_join_kernel<T, D, TILE, HB>, dim3((unsigned)p.N, (unsigned)((p.Hq + 7) / 8)), 256, 0, st, 1,
-                            p, grid);
+    if (p.lone || grid == 1) return cudaSuccess;
+    const int heads = p.G < HB ? p.G : HB;
+    return launch_dependent(paged_join_kernel<T, D, TILE, HB>, dim3((unsigned)grid - 1, (unsigned)((heads + 7) / 8)), 256, 0, st,
+                            1, p, grid);
 }
 
 // Query heads per item of the tensor-core form: one pass over the cache for up to 32 of them (64 rows of 8192 tokens, 2

@@ -90,22 +90,22 @@ __device__ Split find_split(const PagedParams &p, int items, int grid, int b, in
     return r;
 }
 
-// Zero outputs and lse = -inf of sequence n, which has no tokens (block-wide).
+// Zero outputs and lse = -inf of the sequences without tokens, a warp at a time.
 template <typename T>
-__device__ __forceinline__ void empty_sequence(const PagedParams &p, int n, int D) {
-    clamp_len(p, n, threadIdx.x == 0);
-    T *out = static_cast<T *>(p.out) + (int64_t)n * p.Hq * D;
-    for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x) out[i] = from_f32<T>(0.f);
-    if (p.lse)
-        for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) p.lse[(int64_t)n * p.Hq + i] = -INFINITY;
-}
-
-// Those of all empty sequences, where no join kernel follows to write them.
-template <typename T, int TILE>
 __device__ __forceinline__ void empty_sequences(const PagedParams &p, int D) {
-    if (p.lone)
-        for (int n = blockIdx.x; n < p.N; n += gridDim.x)
-            if (tiles_of<TILE>(p, n) == 0) empty_sequence<T>(p, n, D);
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    // (the last CTAs first: they have no tiles where there are few)
+    for (int64_t n0 = ((int64_t)(gridDim.x - 1 - blockIdx.x) * warps + (threadIdx.x >> 5)) * 32; n0 < p.N;
+         n0 += (int64_t)gridDim.x * warps * 32) {
+        const int len = n0 + lane < p.N ? clamp_len(p, (int)n0 + lane, true) : 1;
+        for (uint32_t left = __ballot_sync(0xffffffffu, len == 0); left; left &= left - 1) {
+            const int64_t n = n0 + __ffs(left) - 1;
+            T *out = static_cast<T *>(p.out) + n * p.Hq * D;
+            for (int i = lane; i < p.Hq * D; i += 32) out[i] = from_f32<T>(0.f);
+            if (p.lse)
+                for (int i = lane; i < p.Hq; i += 32) p.lse[n * p.Hq + i] = -INFINITY;
+        }
+    }
 }
 
 // One partial result of an item of HB query heads: m, l (base-2 logarithms) per

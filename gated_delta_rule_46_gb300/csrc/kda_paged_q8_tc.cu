@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TOK>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    empty_sequences<__nv_bfloat16, TOK>(p, D);
-    if ((int)blockIdx.x >= sp.g) return;
+    if ((int)blockIdx.x >= sp.g) {
+        empty_sequences<__nv_bfloat16>(p, D);
+        return;
+    }
     if (warp == L::MMA_S) {
         ptx::tmem_alloc(&s_tmem, L::cols);
         ptx::tmem_relinquish();
@@ -689,6 +691,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             wk.next_item(p, last - first);
         }
     }
+    empty_sequences<__nv_bfloat16>(p, D);
     if (!ok) {
         s_abort = 1;
         report_status(p.status, KDA_ERR_DEVICE_TIMEOUT);
