@@ -306,9 +306,10 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 ok = warp_wait(&bar[VFULL + s], t / NS);
                 if (!ok) break;
                 const int left = len - (int)(i * TOK);
-                if (left < TOK) {       // (a weight of 0 does not silence a NaN) 16 bytes a lane and step
+                if (left < TOK) {       // (a weight of 0 does not silence a NaN) 16 bytes a lane and step, to the page's end
                     constexpr int C = L::RB / 16;
-                    for (int j = left * (D / 16) + lane; j < TILE * C; j += 32)
+                    const int end = min(TILE, ((left + F - 1) / F + rows - 1) & ~(rows - 1)) * C;
+                    for (int j = left * (D / 16) + lane; j < end; j += 32)
                         *reinterpret_cast<uint4 *>(sm + L::V + s * L::tile + swizzled<L::RB>(j / C, j % C)) = make_uint4(0, 0, 0, 0);
                     ptx::fence_async_smem();
                     __syncwarp();
