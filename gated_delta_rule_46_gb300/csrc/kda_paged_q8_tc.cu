@@ -34,13 +34,14 @@
 // warp that loads, as their softmax takes 128 registers a thread.
 //
 // Measured (8 key-value heads unless said): 64 rows of up to 16384 tokens, 4 query heads of
-// 128 channels each, 173 us, 0.91 of the copy rate; one row of 131072, 54 us (0.74), of which
-// about 15 are the start, the first loads' latency and the join; with 16 query heads and up
-// to 8192 tokens 100 us (0.80), 4 query heads of 64 channels 94 us (0.84), of 32 channels
-// 85 (0.47); 128 rows of up to 8192, 4 key-value heads with 16 query heads of 64 channels,
-// 70-73 us (0.55).  What bounds the last is the softmax: 450 instructions a thread and tile
+// 128 channels each, 173 us, 0.91 of the copy rate; one row of 131072, 51 us (0.77), of which
+// about 12 are the start, the first loads' latency and the join; with 16 query heads and up
+// to 8192 tokens 95 us (0.83), 4 query heads of 64 channels 91 us (0.87), of 32 channels
+// 86 (0.46); 128 rows of up to 8192, 4 key-value heads with 16 query heads of 64 channels,
+// 69-71 us (0.56); 256 rows of up to 128 tokens 27 us.  What bounds the last is the softmax: 450 instructions a thread and tile
 // of 256 tokens, each seven cycles after the one before with two such warps a scheduler.  A
-// third group of softmax warps spills registers (73 -> 85 us); moving what is freed from the
+// third group of softmax warps spills registers (73 -> 85 us), and gains nothing where the
+// scores are read from TMEM twice to need fewer (70.5 -> 73.4); moving what is freed from the
 // load and MMA warps to them with setmaxnreg makes no difference to the compiler (103 us).
 // Freeing stages by the consumers instead of a second commit: 141 -> 152 us (4 heads, 64
 // channels, in rows of one token).
@@ -58,7 +59,7 @@ using namespace paged;
 constexpr int NSMAX = 12;                         // stages of the K and of the V ring, at most
 constexpr int SB = 4, RING = 16;                  // S^T buffers; tiles whose scales and page masks are kept
 constexpr int QRING = 16;                         // items whose queries' factors are kept
-constexpr int NG = 2;                             // groups of softmax warps (three: the same times)
+constexpr int NG = 2;                             // groups of softmax warps
 constexpr int LMAX = 4;                           // warps that load, at most
 // A page mask or scales of tile t are read before O^T of tile t is issued, which V's stage of tile t + NS waits for; the warp
 // that writes them again, for tile t + RING, has loaded tile t + RING - LMAX >= t + NS before.  An item's factors are written

@@ -10,11 +10,14 @@ it is 0).  Checks, streams and errors are as in ``layers``.
 from __future__ import annotations
 
 from array import array
+from operator import attrgetter
 
 import torch
 
 from .kda import _empty, _record
 from .layers import _call, _cuda, _dense, _dims, _size, _status
+
+_Tensor, _shape, _nbytes = torch.Tensor, attrgetter("shape"), attrgetter("nbytes")
 
 
 def _state(page_table, held, refs):
@@ -27,13 +30,16 @@ def _state(page_table, held, refs):
 
 
 def _pools(pools, P, dev):
-    """The pools' addresses and the bytes of a page in each, as arrays on the host."""
-    index = dev.index
-    for t in pools:
-        if not (type(t) is torch.Tensor and t.get_device() == index and t.is_contiguous() and t.dim() and t.shape[0] == P):
-            _check_pools(pools, P, dev)
-            break
-    return array("Q", [t.data_ptr() for t in pools]), array("q", [t.nbytes // P if P else 0 for t in pools])
+    """The pools' addresses and the bytes of a page in each, as arrays on the host.  (A model's layers have dozens of
+    pools: each check runs over all of them at once.)"""
+    try:
+        plain = (set(map(type, pools)) <= {_Tensor} and set(map(_Tensor.get_device, pools)) <= {dev.index}
+                 and {s[0] for s in map(_shape, pools)} <= {P} and all(map(_Tensor.is_contiguous, pools)))
+    except IndexError:                                                   # a tensor without axes
+        plain = False
+    if not plain:
+        _check_pools(pools, P, dev)
+    return array("Q", map(_Tensor.data_ptr, pools)), array("q", [n // P for n in map(_nbytes, pools)] if P else [0] * len(pools))
 
 
 def _check_pools(pools, P, dev):
