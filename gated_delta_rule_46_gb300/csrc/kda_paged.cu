@@ -104,8 +104,8 @@ cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st) {
 // heads, and CTAs four warps, of which an SM holds two to four, so that one's first loads
 // and joins overlap another's tokens.  64 rows of up to 4096 tokens, 8 key-value heads of
 // 128 channels, take 72 us with 1 query head each (107 in one CTA of 16 warps an SM, 219
-// with eight channels a lane), 146 with 4 (186, 228), 274 with 8 (351, 332) and 527 with
-// 16: 0.55, 0.27, 0.15 and 0.08 of the copy rate.  Conversions and products of a byte
+// with eight channels a lane), 142 with 4 (186, 228), 263 with 8 (351, 332) and 503 with
+// 16: 0.55, 0.28, 0.15 and 0.08 of the copy rate.  Conversions and products of a byte
 // bound it (issue slots 52 % busy with the two warps a scheduler that registers allow).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
 // Join: a CTA for each border between two CTAs' tiles.  An item that its border
 // is the first to cut is joined there, a warp per head; so there are as many CTAs
 // as items can be cut, whatever the batch (256 rows of up to 600 tokens, 16 query
-// heads: 93 us with a CTA for every row and eight heads, 87 so).  A long row has a
+// heads: 93 us with a CTA for every row and eight heads, 80 so).  A long row has a
 // part from nearly every CTA: their maxima and sums are read a part per lane and
 // joined by shuffles, then the weighted rows are summed in order, with as many
 // loads under way as the unrolling gives.
