@@ -110,26 +110,31 @@ __device__ __forceinline__ Seq sequence(const AppendQ8Params &p, int i) {
     return s;
 }
 
-// One unit is a block of a sequence, a head, and keys or values; the units of all sequences in order are dealt out evenly.
+// One unit is a block of a sequence, a head, and keys or values, or both where the registers hold them; the units of all
+// sequences in order are dealt out evenly.
 // B / 16 warps share a unit, 16 tokens each; the one token of a sequence without cu_seqlens is one warp's.
 //
 // Instructions bound it next to HBM: what a value costs is kept to two and a half (its share of a maximum over the bits of
 // two values at a time, half a multiplication's and a conversion's), and registers to what lets as many CTAs run as these
-// need to overlap: 131k tokens of 8 heads of 128 channels take 131 us (6.2 TB/s) with three CTAs of an SM, 145 with two,
-// 151 with four; float32 108 with two, 133 with three.  Copying a warp's next units to shared memory ahead gains nothing.
+// need to overlap: 131k tokens of 8 heads of 128 channels take 128 us (6.4 TB/s) with three CTAs of an SM, 145 with two,
+// 151 with four; float32 105 with two, 133 with three.  Keys and values in one unit: 73 us instead of 79 with 64 channels,
+// 43 instead of 57 with 32.  Copying a warp's next units to shared memory ahead gains nothing.
 template <typename T, int D>
-constexpr int kCtas = ROWS * D * sizeof(T) > 4096 ? 2 : ROWS * D * sizeof(T) > 2048 ? 3 : 4;
+constexpr int kBoth = ROWS * D * sizeof(T) > 2048 ? 1 : 2;                // keys, or keys and values, of a unit
+template <typename T, int D>
+constexpr int kCtas = ROWS * D * sizeof(T) > 4096 ? 2 : ROWS * D * sizeof(T) >= 2048 ? 3 : 4;
 
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, kCtas<T, D>) paged_append_q8_kernel(const AppendQ8Params p) {
     constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = ROWS / RPS;        // lanes per row, rows per step, steps
     __shared__ int64_t s_sum[WARPS + 1];
     __shared__ int s_n;
-    __shared__ float s_max[2][WARPS];
+    constexpr int KV = kBoth<T, D>;
+    __shared__ float s_max[2][KV][WARPS];
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tasks = 2 * p.Hkv, share = p.cu_seqlens ? (1 << p.block_shift) / ROWS : 1;      // warps of a unit
+    const int tasks = 2 / KV * p.Hkv, share = p.cu_seqlens ? (1 << p.block_shift) / ROWS : 1;      // warps of a unit
     const int per = WARPS / share, mine = warp / share, part = warp % share;
 
     // ---- this CTA's units [u0, u1), the sequence in which they start and the blocks before it
@@ -191,17 +196,16 @@ __global__ void __launch_bounds__(WARPS * 32, kCtas<T, D>) paged_append_q8_kerne
     if (!p.cu_seqlens) s.blocks = 1;                  // (of a malformed one too: a sequence is its own block here)
 
     const int lane_row = lane / LPR, ch = (lane % LPR) * 8;
-    const T *in[2] = {static_cast<const T *>(p.k), static_cast<const T *>(p.v)};
     const int ps = 1 << p.page_shift;
     for (int64_t u = u0, round = 0; u < u1; u += per, ++round) {
         // ---- the block: rows [from, to) of it are new, [0, from) hold earlier tokens
         int from = 0, to = 0;
         int64_t at = 0;                               // its first row in the cache
-        float was = 0.f;
+        float was[KV] = {};                           // scales before
         int row0 = part * ROWS + lane_row;            // this lane's first row
-        const bool v = task >= p.Hkv;
-        const int h = v ? task - p.Hkv : task;
-        Row8<T, VEC> x[STEPS];
+        const int h = task >= p.Hkv ? task - p.Hkv : task;
+        auto value = [&](int kv) { return KV == 2 ? kv == 1 : task >= p.Hkv; };
+        Row8<T, VEC> x[KV][STEPS];
         if (u + mine < u1) {
             while (blk >= cum + s.blocks) {
                 cum += s.blocks;
@@ -216,75 +220,90 @@ __global__ void __launch_bounds__(WARPS * 32, kCtas<T, D>) paged_append_q8_kerne
                 to = min(1 << p.block_shift, s.start + s.n - pos);
                 if (!p.cu_seqlens) row0 = (from & ~(ROWS - 1)) + lane_row;
                 at = (((int64_t)page * p.Hkv + h) << p.page_shift) + (pos & (ps - 1));
-                if (from > 0) was = (v ? p.vs : p.ks)[at >> p.block_shift];
-                const T *src = in[v] + ((int64_t)s.t0 + pos - s.start) * (v ? p.ldv : p.ldk) + (int64_t)h * D + ch;
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = row0 + i * RPS;
-                    if (r >= from && r < to) x[i].load(src + r * (v ? p.ldv : p.ldk));
+                for (int kv = 0; kv < KV; ++kv) {
+                    const bool v = value(kv);
+                    if (from > 0) was[kv] = (v ? p.vs : p.ks)[at >> p.block_shift];
+                    const int64_t ld = v ? p.ldv : p.ldk;
+                    const T *src = static_cast<const T *>(v ? p.v : p.k) + ((int64_t)s.t0 + pos - s.start) * ld + (int64_t)h * D + ch;
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        const int r = row0 + i * RPS;
+                        if (r >= from && r < to) x[kv][i].load(src + r * ld);
+                    }
                 }
             } else if (lane == 0 && part == 0) {
                 report_status(p.status, KDA_ERR_INVALID_ARG);
             }
         }
-        // ---- its largest finite value, and the scale
-        uint32_t top = 0;
+        // ---- the largest finite values, and the scales
+        float amax[KV];
+        bool odd[KV];                                 // (the same in all lanes)
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) x[i].top(top);
-        top = __reduce_max_sync(0xffffffffu, Row8<T, VEC>::joined(top));
-        const bool odd = top >= 0x7f800000u;          // (the same in all lanes)
-        float amax = __uint_as_float(top);
-        if (odd) {
-            amax = 0.f;
+        for (int kv = 0; kv < KV; ++kv) {
+            uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                float f[8];
-                x[i].get(f);
+            for (int i = 0; i < STEPS; ++i) x[kv][i].top(top);
+            top = __reduce_max_sync(0xffffffffu, Row8<T, VEC>::joined(top));
+            odd[kv] = top >= 0x7f800000u;
+            amax[kv] = __uint_as_float(top);
+            if (odd[kv]) {
+                float a = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]) < INFINITY ? fabsf(f[e]) : 0.f);
+                for (int i = 0; i < STEPS; ++i) {
+                    float f[8];
+                    x[kv][i].get(f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]) < INFINITY ? fabsf(f[e]) : 0.f);
+                }
+                amax[kv] = ptx::warp_max(a);
             }
-            amax = ptx::warp_max(amax);
+            if (share > 1 && lane == 0) s_max[round & 1][kv][warp] = amax[kv];
         }
         if (share > 1) {
-            if (lane == 0) s_max[round & 1][warp] = amax;
             __syncthreads();
-            for (int i = 0; i < share; ++i) amax = fmaxf(amax, s_max[round & 1][mine * share + i]);
-        } else {
-            __syncwarp();                             // (every lane has read the scale that one writes)
-        }
-        if (from < to) {
-            float scale = scale_for(amax);
-            bool again = false;                       // earlier codes are rounded to a new scale
-            if (from > 0) {
-                if (was >= kLeast && was <= kMost) {
-                    scale = fmaxf(scale, __uint_as_float((__float_as_uint(was) + 0x7fffffu) & 0xff800000u));
-                    again = scale != was;
-                } else if (lane == 0 && part == 0) {
-                    report_status(p.status, KDA_ERR_INVALID_ARG);
-                }
-            }
-            uint8_t *dst = (v ? p.vc : p.kc) + at * D + ch;
-            const float inv = inverse(scale);
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int r = row0 + i * RPS;
-                float f[8];
-                if (r >= from && r < to) {
-                    x[i].get(f);
-                    *reinterpret_cast<uint2 *>(dst + r * D) = odd ? encode8<true>(f, inv) : encode8<false>(f, inv);
-                } else if (again && r < from) {
-                    decode8(*reinterpret_cast<const uint2 *>(dst + r * D), f);
-                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8<true>(f, was * inv);
+            for (int kv = 0; kv < KV; ++kv)
+                for (int i = 0; i < share; ++i) amax[kv] = fmaxf(amax[kv], s_max[round & 1][kv][mine * share + i]);
+        } else {
+            __syncwarp();                             // (every lane has read the scales that one writes)
+        }
+        if (from < to)
+#pragma unroll
+            for (int kv = 0; kv < KV; ++kv) {
+                const bool v = value(kv);
+                float scale = scale_for(amax[kv]);
+                bool again = false;                   // earlier codes are rounded to a new scale
+                if (from > 0) {
+                    if (was[kv] >= kLeast && was[kv] <= kMost) {
+                        scale = fmaxf(scale, __uint_as_float((__float_as_uint(was[kv]) + 0x7fffffu) & 0xff800000u));
+                        again = scale != was[kv];
+                    } else if (lane == 0 && part == 0) {
+                        report_status(p.status, KDA_ERR_INVALID_ARG);
+                    }
                 }
-            }
-            if (again && !p.cu_seqlens)               // what lies before this warp's rows
-                for (int r = lane_row; r < row0 - lane_row; r += RPS) {
+                uint8_t *dst = (v ? p.vc : p.kc) + at * D + ch;
+                const float inv = inverse(scale);
+                auto round_again = [&](int r) {
                     float f[8];
                     decode8(*reinterpret_cast<const uint2 *>(dst + r * D), f);
-                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8<true>(f, was * inv);
+                    *reinterpret_cast<uint2 *>(dst + r * D) = encode8<true>(f, was[kv] * inv);
+                };
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int r = row0 + i * RPS;
+                    if (r >= from && r < to) {
+                        float f[8];
+                        x[kv][i].get(f);
+                        *reinterpret_cast<uint2 *>(dst + r * D) = odd[kv] ? encode8<true>(f, inv) : encode8<false>(f, inv);
+                    } else if (again && r < from) {
+                        round_again(r);
+                    }
                 }
-            if (lane == 0 && part == 0) (v ? p.vs : p.ks)[at >> p.block_shift] = scale;
-        }
+                if (again && !p.cu_seqlens)           // what lies before this warp's rows
+                    for (int r = lane_row; r < row0 - lane_row; r += RPS) round_again(r);
+                if (lane == 0 && part == 0) (v ? p.vs : p.ks)[at >> p.block_shift] = scale;
+            }
         for (task += per; task >= tasks; task -= tasks) ++blk;
     }
 }
@@ -294,7 +313,7 @@ cudaError_t launch(const AppendQ8Params &p, cudaStream_t st) {
     const int B = 1 << p.block_shift, per = p.cu_seqlens ? WARPS / (B / ROWS) : WARPS;
     // at most two blocks of a sequence are not whole
     const int64_t blocks = p.cu_seqlens ? p.total / B + 2 * (int64_t)min((int64_t)p.num_seqs, p.total) : p.num_seqs;
-    const int64_t most = (blocks * 2 * p.Hkv + per - 1) / per, room = (int64_t)sm_count() * kCtas<T, D>;
+    const int64_t most = (blocks * (2 / kBoth<T, D>) * p.Hkv + per - 1) / per, room = (int64_t)sm_count() * kCtas<T, D>;
     return launch_dependent(paged_append_q8_kernel<T, D, VEC>, dim3((unsigned)(most < room ? most : room)), WARPS * 32, 0, st, 1,
                             p);
 }

@@ -164,15 +164,6 @@ __device__ __forceinline__ void cp_async4(void *dst, const void *src, bool is) {
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(is ? 4 : 0)
                  : "memory");
 }
-// 16 bytes, and groups of a thread's copies: wait leaves the last N of them under way.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // One of the barrier's arrivals, once this thread's copies of that kind so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
