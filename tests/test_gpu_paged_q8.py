@@ -403,6 +403,66 @@ def test_decode_bad_pages_and_lengths(dtype):
     layers_ref.close("lse", lse, rl)
 
 
+FORMS = [(32, 3), (32, 16), (32, 20), (64, 8), (64, 11), (64, 33), (128, 8), (128, 16), (128, 24)]
+
+
+@pytest.mark.parametrize("d,G", FORMS)
+@pytest.mark.parametrize("ps,B", [(1024, 128), (1024, 16), (16, 16), (128, 32)])
+def test_decode_lengths_of_every_form(d, G, ps, B):
+    """Rows of one and two tokens, that end next to a tile's, a page's and a block's end, and a row without any."""
+    dev = need_gpu()
+    lens = [1, 2, 0, 15, 17, 127, 128, 129, 255, 256, 257, 511, 513, 1023, 1025, 31]
+    _decode(_cache(lens, 1, G, d, ps, B, BF, d + G + ps), lens, dev)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,G", FORMS)
+def test_decode_missing_pages_of_every_form(dtype, d, G):
+    """Pages that are missing at the front, in the middle and at the end of a tile, several in a row, and all of a tile."""
+    dev = need_gpu()
+    lens = [700, 600, 520, 90, 530]
+    q, kc, vc, ks, vs, table = _cache(lens, 2, G, d, 16, 16, dtype, d + G)
+    P = kc.shape[0]
+    for row, cols in enumerate(([0], [3, 4, 5, 31], range(16, 33), range(6), [1, 2, 7, 8, 15, 16, 32, 33])):
+        for i in cols:
+            table[row, i] = (-1, P, 1 << 30, -2 ** 31)[i % 4]
+    status = torch.zeros(4, dtype=torch.int32, device=dev)
+    out, lse = _decode((q, kc, vc, ks, vs, table), lens, dev, status=status)
+    assert not out[3].any() and torch.isneginf(lse[3]).all()
+    assert check_device_status(status) == kda.KDA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,G", FORMS)
+def test_decode_values_of_their_own_of_every_form(dtype, d, G):
+    """NaN in a row's own tokens, next to others' in a row of the tile, stays in that row's heads and channels."""
+    dev = need_gpu()
+    lens = [200, 150, 90, 60]
+    c = _cache(lens, 2, G, d, 32, 16, dtype, d + G + 1)
+    plain, _ = _decode(c, lens, dev)
+    q, kc, vc, ks, vs, table = (t.clone() for t in c)
+    kc.view(torch.uint8)[int(table[0, 2]), 0, 3, 5] = 0x7F
+    vc.view(torch.uint8)[int(table[1, 1]), 1, 4, 7] = 0xFF
+    vc.view(torch.uint8)[int(table[3, 1]), 0, 27, d - 1] = 0x7F          # the last token
+    q[2, 1, 4] = math.inf
+    q[2, 2 * G - 1, d - 1] = math.nan
+    out, _ = _decode((q, kc, vc, ks, vs, table), lens, dev, check=False)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, :G], bad[1, G:, 7], bad[2, 1], bad[2, 2 * G - 1], bad[3, :G, d - 1] = True, True, True, True, True
+    bad |= torch.isnan(plain)                                            # (a few of the random codes are NaN)
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], plain[~bad])
+
+
+@pytest.mark.parametrize("d,G", FORMS)
+def test_decode_many_short_rows_of_every_form(d, G):
+    """Items of one tile and of a few, whole and cut, more of them than CTAs."""
+    dev = need_gpu()
+    g = torch.Generator().manual_seed(d + G)
+    lens = [int(n) for n in torch.randint(0, 700, (90,), generator=g)]
+    _decode(_cache(lens, 2, G, d, 64, 32, BF, d + G + 2), lens, dev)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_decode_query_rows_of_a_wider_product(dtype):
     dev = need_gpu()
