@@ -320,14 +320,22 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
 
 def _cache_q8(k_cache, v_cache, k_scale, v_scale, H, d, dev):
     """The shapes and pointers of a cache in 8 bits: pages, page size, block, and four pointers."""
-    P, _, ps, _ = _dims(k_cache, "k_cache", 4)
-    kp = _dense(k_cache, "k_cache", (P, H, ps, d), torch.float8_e4m3fn, dev)
-    vp = _dense(v_cache, "v_cache", (P, H, ps, d), torch.float8_e4m3fn, dev)
-    blocks = _dims(k_scale, "k_scale", 3)[2]
-    if blocks == 0 or ps % blocks:
-        raise ValueError(f"k_scale has {blocks} blocks for pages of {ps} tokens")
-    return (P, ps, ps // blocks, kp, vp, _dense(k_scale, "k_scale", (P, H, blocks), torch.float32, dev),
-            _dense(v_scale, "v_scale", (P, H, blocks), torch.float32, dev))
+    shape, blocks = _dims(k_cache, "k_cache", 4), _dims(k_scale, "k_scale", 3)
+    P, _, ps, _ = shape
+    n, index, f8, f32 = blocks[2], dev.index, torch.float8_e4m3fn, torch.float32
+    if (type(k_cache) is type(v_cache) is type(k_scale) is type(v_scale) is torch.Tensor and shape == (P, H, ps, d)
+            and blocks == (P, H, n) and v_cache.shape == shape and v_scale.shape == blocks
+            and k_cache.dtype is v_cache.dtype is f8 and k_scale.dtype is v_scale.dtype is f32
+            and k_cache.get_device() == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == index
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and n and ps % n == 0):
+        return P, ps, ps // n, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+    # which of it is wrong (a subclass of Tensor is not)
+    kp, vp = (_dense(t, name, (P, H, ps, d), f8, dev) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")))
+    if n == 0 or ps % n:
+        raise ValueError(f"k_scale has {n} blocks for pages of {ps} tokens")
+    ksp, vsp = (_dense(t, name, (P, H, n), f32, dev) for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+    return P, ps, ps // n, kp, vp, ksp, vsp
 
 
 def paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start_pos, cu_seqlens=None, status=None,
