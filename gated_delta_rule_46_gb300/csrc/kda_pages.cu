@@ -13,8 +13,8 @@
 //
 // The chain of steps bounds the bookkeeping: a resize that changes hardly anything takes
 // 5 us on the device, one that gives back or hands out 65000 pages 14 (eight SMs' scattered
-// atomics and stores); a fork of four rows 9, a compaction of a hundred pages 7.  Copies run
-// at 5.7 to 6.1 TB/s (192 forks of 1.5 MB: 97 us; 880 MB compacted: 289 us).
+// atomics and stores); a fork of four rows 9, a compaction of a hundred pages 7.  With their
+// copies 192 forks of 1.5 MB take 104 us (0.84 of the copy rate), 870 MB compacted 269 (0.95).
 #include "kda_pages.cuh"
 #include "sm100_ptx.cuh"
 
@@ -274,34 +274,35 @@ __global__ void __launch_bounds__(NT, 1) pages_resize_kernel(const PageTable p, 
 }
 
 // ---------------------------------------------------------------------------
-// Copies of pages in all pools, a unit of up to 16 KB of one page at a time.  Sources
+// Copies of pages in all pools, a unit of up to 4 KB of one page at a time by each warp,
+// all of whose loads are under way at once (units of 16 KB by a CTA leave it waiting for
+// a page's scales of a few bytes as long as for its keys: 290 us instead of 273).  Sources
 // are pages in use and destinations free ones, so no order is needed.
 // ---------------------------------------------------------------------------
-constexpr int kUnit = 16384, kCopyThreads = 256;
+constexpr int kUnit = 4096, kCopyThreads = 256;
 constexpr int64_t kMostAtOnce = 1 << 19;          // bytes of pages that the planning kernel copies by itself
 
 
-// By T threads, with U loads under way in each.
-template <typename V, int T, int U>
-__device__ __forceinline__ void copy_unit(uint8_t *dst, const uint8_t *src, int bytes, int thread) {
+template <typename V>
+__device__ __forceinline__ void copy_unit(uint8_t *dst, const uint8_t *src, int bytes) {
+    constexpr int U = 8;                          // loads under way per lane
     const int n = bytes / (int)sizeof(V);
-    for (int i0 = thread; i0 < n; i0 += U * T) {
+    for (int i0 = threadIdx.x & 31; i0 < n; i0 += U * 32) {
         V x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i0 + u * T < n) x[u] = reinterpret_cast<const V *>(src)[i0 + u * T];
+            if (i0 + u * 32 < n) x[u] = reinterpret_cast<const V *>(src)[i0 + u * 32];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i0 + u * T < n) reinterpret_cast<V *>(dst)[i0 + u * T] = x[u];
+            if (i0 + u * 32 < n) reinterpret_cast<V *>(dst)[i0 + u * 32] = x[u];
     }
 }
 
-// The part of group `group` of `groups` groups of T threads.
-template <int T, int U>
-__device__ __forceinline__ void copy_pages(const Pools &pools, const int32_t *from, const int32_t *to, int count, int group,
-                                           int groups) {
-    const int per = pools.first[pools.n], thread = threadIdx.x % T;
-    for (int64_t u = group; u < (int64_t)count * per; u += groups) {
+// The part of warp `warp` of `warps`.
+__device__ __forceinline__ void copy_pages(const Pools &pools, const int32_t *from, const int32_t *to, int count, int warp,
+                                           int warps) {
+    const int per = pools.first[pools.n];
+    for (int64_t u = warp; u < (int64_t)count * per; u += warps) {
         const int pair = (int)(u / per), at = (int)(u - (int64_t)pair * per);
         int lo = 0, hi = pools.n;                 // the pool of the unit
         while (hi - lo > 1) {
@@ -314,9 +315,9 @@ __device__ __forceinline__ void copy_pages(const Pools &pools, const int32_t *fr
         const uint8_t *src = base + ldcg(from + pair) * size + off;
         const int bytes = (int)min((int64_t)kUnit, size - off);
         const uint64_t odd = reinterpret_cast<uint64_t>(base) | (uint64_t)size;
-        if (odd % 16 == 0) copy_unit<uint4, T, U>(dst, src, bytes, thread);
-        else if (odd % 4 == 0) copy_unit<uint32_t, T, U>(dst, src, bytes, thread);
-        else copy_unit<uint8_t, T, U>(dst, src, bytes, thread);
+        if (odd % 16 == 0) copy_unit<uint4>(dst, src, bytes);
+        else if (odd % 4 == 0) copy_unit<uint32_t>(dst, src, bytes);
+        else copy_unit<uint8_t>(dst, src, bytes);
     }
 }
 
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (copy) {
         ptx::cluster_sync();                      // the plan is there for all
         fork_rows(p, forks, f, rank * NT + tid, CL * NT);
-        copy_pages<64, 8>(pools, f.from, f.to, got, (rank * NT + tid) / 64, CL * NT / 64);
+        copy_pages(pools, f.from, f.to, got, (rank * NT + tid) / 32, CL * NW);
     }
 }
 
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(NT, 1)
         ptx::cluster_sync();                      // the plan is there for all
         const int thread = (int)ptx::cluster_rank() * NT + threadIdx.x;
         compact_rows(p, f, thread, CL * NT);
-        copy_pages<64, 8>(pools, f.from, f.to, m.total, thread / 64, CL * NT / 64);
+        copy_pages(pools, f.from, f.to, m.total, thread / 32, CL * NW);
     }
 }
 
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     if (first) fork_rows(p, forks, f, (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, (int64_t)gridDim.x * kCopyThreads);
-    copy_pages<kCopyThreads, 4>(pools, f.from, f.to, *f.count, blockIdx.x, gridDim.x);
+    copy_pages(pools, f.from, f.to, *f.count, (blockIdx.x * kCopyThreads + threadIdx.x) / 32, gridDim.x * (kCopyThreads / 32));
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     if (first) compact_rows(p, f, (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, (int64_t)gridDim.x * kCopyThreads);
-    copy_pages<kCopyThreads, 4>(pools, f.from, f.to, *f.count, blockIdx.x, gridDim.x);
+    copy_pages(pools, f.from, f.to, *f.count, (blockIdx.x * kCopyThreads + threadIdx.x) / 32, gridDim.x * (kCopyThreads / 32));
 }
 
 Pools some_pools(void *const *base, const int64_t *bytes, int n) {
@@ -560,13 +561,15 @@ bool copied_at_once(const int64_t *bytes, int n, int64_t others, int64_t pairs) 
 }
 
 // Calls launch(pools, grid, first) for all pools, at most kPoolsPerLaunch of them at a time, and once where there are none.
-// others: threads' worth of other work; pairs: pages to copy, at most.
+// others: threads' worth of other work; pairs: pages to copy, at most; ctas: of an SM, at most (three run at a time).  More
+// even out what each takes (half of a batch compacted: 273 us with 8, 267 with 24, 264 with 48); where it is not known how
+// many pages move, those that find nothing to do cost as well (two pages of 4000: 11.8, 13.5 and 17.2 us).
 template <typename F>
-cudaError_t launch_copies(void *const *base, const int64_t *bytes, int n, int64_t others, int64_t pairs, F &&launch) {
+cudaError_t launch_copies(void *const *base, const int64_t *bytes, int n, int64_t others, int64_t pairs, int ctas, F &&launch) {
     for (int at = 0; at == 0 || at < n; at += kPoolsPerLaunch) {
         const Pools pools = some_pools(base + at, bytes + at, n - at < kPoolsPerLaunch ? n - at : kPoolsPerLaunch);
-        const int64_t units = pairs * pools.first[pools.n], work = (others + kCopyThreads - 1) / kCopyThreads;
-        const int64_t most = units > work ? units : work, room = (int64_t)sm_count() * 8;
+        const int64_t units = (pairs * pools.first[pools.n] + kCopyThreads / 32 - 1) / (kCopyThreads / 32), work = (others + kCopyThreads - 1) / kCopyThreads;
+        const int64_t most = units > work ? units : work, room = (int64_t)sm_count() * ctas;
         const cudaError_t e = launch(pools, dim3((unsigned)(most < 1 ? 1 : (most < room ? most : room))), at == 0);
         if (e != cudaSuccess) return e;
     }
@@ -606,7 +609,7 @@ cudaError_t launch_pages_fork(void *const *pools, const int64_t *page_bytes, int
     const Pools now = some_pools(pools, page_bytes, once ? num_pools : 0);
     const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(CL), NT, 0, st, CL, now, p, lens, src, dst, forks, f, once);
     if (e != cudaSuccess || once) return e;
-    return launch_copies(pools, page_bytes, num_pools, (int64_t)forks * p.max_pages, forks,
+    return launch_copies(pools, page_bytes, num_pools, (int64_t)forks * p.max_pages, forks, 24,
                          [&](const Pools &some, dim3 grid, bool first) {
                              return launch_dependent(pages_fork_copy_kernel, grid, kCopyThreads, 0, st, 1, some, p, forks, f,
                                                      first);
@@ -629,7 +632,7 @@ cudaError_t launch_pages_compact(void *const *pools, const int64_t *page_bytes, 
     const Pools now = some_pools(pools, page_bytes, once ? num_pools : 0);
     const cudaError_t e = launch_dependent(pages_compact_kernel, dim3(CL), NT, 0, st, CL, now, p, f, once);
     if (e != cudaSuccess || once) return e;
-    return launch_copies(pools, page_bytes, num_pools, (int64_t)p.rows * p.max_pages, p.num_pages / 2,
+    return launch_copies(pools, page_bytes, num_pools, (int64_t)p.rows * p.max_pages, p.num_pages / 2, 16,
                          [&](const Pools &some, dim3 grid, bool first) {
                              return launch_dependent(pages_compact_copy_kernel, grid, kCopyThreads, 0, st, 1, some, p, f, first);
                          });
