@@ -457,13 +457,13 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         f[k] = fk[at];
                         weight[k] = fv[at];
                     }
-                    // the tile's largest scale of V, 2^-100 at least (where a block has no token its scale is 0)
-                    unit = fmaxf(ptx::warp_max(fabsf(lane < (TOK >> p.block_shift) ? fv[lane] : 0.f)), 0x1p-100f);
-                    const float share = 256.f / unit;
+                    // the tile's largest scale of V, 2^-126 at least (where a block has no token its scale is 0)
+                    unit = fmaxf(ptx::warp_max(fabsf(lane < (TOK >> p.block_shift) ? fv[lane] : 0.f)), 0x1p-126f);
+                    const float share = 1.f / unit;
                     ptx::tmem_ld_wait(raw[0], raw[1]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        weight[k] *= share;
+                        weight[k] = weight[k] * share * 256.f;       // (256 / unit can be infinite)
                         auto column = [&](int tile, int b) { return raw[k >> 1][4 * tile + 2 * (k & 1) + b]; };
 #pragma unroll
                         for (int e = 0; e < F; ++e)
