@@ -12,18 +12,24 @@
 // of the rows is looked at, the sum of a token's weights and the other's values being noise.
 //
 // Q and the weights P, which need more than e4m3's four significant bits, come in two parts,
-//   x = hi + lo,   hi = e4m3(x),   lo = e4m3(x - hi)
-// whose products are added up: in the same accumulators, and for up to 8 heads, where an
-// MMA's 16 columns have room for both parts, in neighbouring columns.  With the largest of
-// a head's channels at 224 or more that is exact for a bf16 query down to 2^-11 of it, and
-// off by 2^-10, 2^-18 of the largest, below; of a weight it keeps eight bits, as bf16 would.
+//   x = hi + lo / f,   hi = e4m3(x),   lo = e4m3(f (x - hi))
+// whose products are added up.  For Q f is 1, and they share accumulators, or for up to 8
+// heads, where an MMA's 16 columns have room for both parts, are in neighbouring columns.  With
+// the largest of a head's channels at 224 or more that is exact for a bf16 query down to 2^-11
+// of it, and off by 2^-10, 2^-18 of the largest, below.  For P, at most 256, f is 32, and the
+// parts have columns of their own: eight bits of a weight are kept, as bf16 would, down to
+// 2^-10 of the largest, and 2^-23 of that (2^-15 of 256) below.
 //
 // A token's scale of K multiplies its row of S^T.  Its scale of V goes into its
-// weight: with the tile's largest score m and largest scale of V u,
-//   P = 256 e^{s - m} v_scale / u,   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
-// so that the weights use e4m3's range from the tile's own maximum on (an error below
-// 2^-18 of that, whatever the rest of the row holds), and tiles do not wait for each
-// other's maxima: two groups of softmax warps work on tiles in turn.  A softmax thread has
+// weight: with the tile's largest scale of V u and largest product of both m,
+//   m = max s + log v_scale / u,   P = 256 e^{s - m} v_scale / u,
+//   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
+// so that the weights use e4m3's range from the tile's largest on, whatever the rest of the row
+// holds and whichever tokens the largest score and the largest scale belong to.  Tiles do not
+// wait for each other's maxima: two groups of softmax warps work on tiles in turn.  Where a tile's
+// scales are within a factor of 4, as they mostly are, m is its largest score, which is as much
+// off at most (an error of 2^-21 of the largest); it is never taken more than 40 (base 2) below
+// the largest score, so that sums of e^{s - m} stay finite.  A softmax thread has
 // four rows and a quarter of the heads (TMEM's 16 x 256-bit reads), so that what is one for
 // all tokens (maxima, their exponentials; worked out by a lane per head) is a vector or two.
 //
@@ -77,7 +83,8 @@ struct Lay {
     static constexpr int TOK = TILE * F, NBK = TOK / 16;             // tokens and, at most, blocks of a tile
     static constexpr bool BOTH = HB == 8;                            // both parts in the columns
     static constexpr int QN = BOTH ? 16 : HB, N = F * QN;            // columns of a token of the rows, of all
-    static constexpr int PARTS = BOTH ? 1 : 2, HT = HB / 4;          // rounds of MMAs; heads of a softmax thread
+    static constexpr int PARTS = BOTH ? 1 : 2, HT = HB / 4;          // rounds of S^T's MMAs; heads of a softmax thread
+    static constexpr int ON = BOTH ? N : 2 * N;                      // columns of P and O^T: both parts
     // roles, by their first warps; 32 heads need the registers of 16 warps
     static constexpr int LOADERS = HB == 32 ? 1 : LMAX;
     static constexpr int MMA_S = LOADERS, MMA_O = LOADERS + 1, STAGE_Q = LOADERS + 2, SOFTMAX = LOADERS == 1 ? 4 : 8;
@@ -88,7 +95,7 @@ struct Lay {
     static constexpr int NS = RB == 128 ? (HB == 32 || (HB == 16 && F == 2) ? 5 : 6) : RB == 64 ? (HB == 8 ? NSMAX : 10) : NSMAX;
     // (V first: with rows of less than 128 bytes the MMA's rows past them read what lies behind a stage, which no one looks at)
     static constexpr uint32_t V = 0, K = NS * tile, Q = 2 * NS * tile, q_part = QN * D, q_bytes = PARTS * q_part;
-    static constexpr uint32_t P = Q + 2 * q_bytes, p_part = N * TILE, p_bytes = PARTS * p_part;
+    static constexpr uint32_t P = Q + 2 * q_bytes, p_bytes = ON * TILE;
     static constexpr uint32_t SC = P + NG * p_bytes;                 // float: scales of K [RING][NBK], of V [RING][NBK]
     static constexpr uint32_t QS = SC + 2 * RING * NBK * 4;          // factors of the queries [QRING][HB]
     static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [NG][HB], u / 256 [NG] (padded to 4)
@@ -97,13 +104,20 @@ struct Lay {
     static constexpr uint32_t STAT = SUM + 10 * NG * HB * 4;         // of each softmax and output warp: [4][HB]
     static constexpr uint32_t X = STAT + (4 * NG + 4) * 4 * HB * 4;  // outputs of an item's tokens e, F == 2: [HB][RB]
     static constexpr uint32_t bytes = X + (F == 2 ? HB * RB * 4 : 0);
-    static constexpr uint32_t cols = (SB + NG) * N <= 128 ? 128 : 256;   // TMEM: SB + NG buffers of N columns
-    static_assert((SB + NG) * N <= cols, "tensor memory");
+    static constexpr uint32_t cols = SB * N + NG * ON <= 128 ? 128 : 256;    // TMEM: SB buffers of S^T, NG of O^T
+    static_assert(SB * N + NG * ON <= cols, "tensor memory");
 };
 // The column of S^T, and the row of Q's stage, of head h: a softmax thread finds its HT heads in a row in its own columns.
 template <int HB>
 __device__ __forceinline__ int column(int h) {
     return HB == 8 ? h : HB == 16 ? 8 * (h >> 1 & 1) + 2 * (h >> 2) + (h & 1) : 8 * (h >> 1 & 3) + 2 * (h >> 3) + (h & 1);
+}
+
+// The column of O^T that the softmax threads write head h to (up to 8 heads: its first part, the second is two behind it).
+template <int HB>
+__device__ __forceinline__ constexpr int out_column(int h) {
+    const int j = h & 3;
+    return HB == 8 ? 2 * (h - j) + 4 * (j >> 1) + (j & 1) : HB == 16 ? h : 16 * (h >> 2 & 1) + 4 * (h >> 3) + j;
 }
 
 // Byte offset of the 16-byte chunk of a row, swizzled as TMA does it.
@@ -118,11 +132,14 @@ __device__ __forceinline__ float power_for(float a) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Two weights in two parts each.
+// Two values in two parts each; of weights, which come kLow times too large, the second stays so.  (What the first
+// leaves of a weight, at most 256, is at most 8.)
+constexpr float kLow = 32.f, kTop = 13.f;         // 2^13 = 256 kLow: the largest weight
+template <bool WEIGHT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    const __half2 w = __floats2half2_rn(x, y);
-    const uint16_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(w), __NV_SATFINITE, __NV_E4M3);
-    const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    const __half2 w = __floats2half2_rn(x, y), first = WEIGHT ? __hmul2(w, __float2half2_rn(1.f / kLow)) : w;
+    const uint16_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(first), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hfma2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)), __float2half2_rn(WEIGHT ? -kLow : -1.f), w);
     hi = h;
     lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r), __NV_SATFINITE, __NV_E4M3);
 }
@@ -204,7 +221,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
     auto tm_s = [&](int b) { return tmem + b * L::N; };
-    auto tm_o = [&](int b) { return tmem + (SB + b) * L::N; };
+    auto tm_o = [&](int b) { return tmem + SB * L::N + b * L::ON; };
     WalkOf<TOK> wk;
     wk.start(p, sp, items);
     const int rows = min(TILE, 1 << (p.page_shift - FS)); // of a tile that one page holds
@@ -298,7 +315,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
             }
         }
     } else if (warp == L::MMA_O) {                                // ---- rows of V without a token, O^T
-        constexpr uint32_t id_o = ptx::idesc_e4m3_f32(128, L::N, true);
+        constexpr uint32_t id_o = ptx::idesc_e4m3_f32(128, L::ON, true);
         for (int t = 0; ok && wk.more();) {
             const int len = wk.len;
             const int64_t first = wk.tile, last = wk.last();
@@ -320,11 +337,11 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 if (ptx::elect_one()) {
                     ptx::tc_fence_after_sync();
                     const uint64_t v = ptx::sdesc_rows<L::RB>(base + L::V + s * L::tile, L::tile);
-                    const uint64_t w = ptx::sdesc_plain_n(base + L::P + b * L::p_bytes, 8 * L::N, 128);
+                    const uint64_t w = ptx::sdesc_plain_n(base + L::P + b * L::p_bytes, 8 * L::ON, 128);
                     constexpr int J = TILE / 32;
 #pragma unroll
-                    for (int j = 0; j < L::PARTS * J; ++j)
-                        ptx::mma_f8_ss(tm_o(b), v + j % J * (32 * L::RB >> 4), w + j * (32 * L::N >> 4), id_o, j > 0);
+                    for (int j = 0; j < J; ++j)
+                        ptx::mma_f8_ss(tm_o(b), v + j * (32 * L::RB >> 4), w + j * (32 * L::ON >> 4), id_o, j > 0);
                     ptx::mma_commit(&bar[PVD + b]);
                     ptx::mma_commit(&bar[VFREE + s]);
                 }
@@ -404,7 +421,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)     // (exact in float16 but for what is below 2^-23 of the largest)
-                        split2(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+                        split2<false>(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
                     if (h < HB) {
                         const int n = column<HB>(h);
                         uint8_t *low = dst + (L::BOTH ? swizzled<D>(8 + n, c >> 1) : L::q_part + swizzled<D>(n, c >> 1));
@@ -440,6 +457,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 float *red = reinterpret_cast<float *>(sm + L::RED) + (wg * 2 + (turn & 1)) * 4 * HB;
                 ok = warp_wait(&bar[SCALES + r], t / RING) && warp_wait(&bar[SD + sb], t / SB);
                 float x[F * HT][4], weight[4], unit = 0.f;        // scores of token e, head h: x[e * HT + h]
+                bool apart = false;
                 if (ok) {
                     ptx::tc_fence_after_sync();
                     float raw[2][4 * NT];                         // lanes 0-15 and 16-31 of the warp's part of TMEM
@@ -459,11 +477,11 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     // the tile's largest scale of V, 2^-126 at least (where a block has no token its scale is 0)
                     unit = fmaxf(ptx::warp_max(fabsf(lane < (TOK >> p.block_shift) ? fv[lane] : 0.f)), 0x1p-126f);
-                    const float share = 1.f / unit;
+                    const float share = __fdividef(1.f, unit);     // (the factor of 2^13 comes with the exponentials)
                     ptx::tmem_ld_wait(raw[0], raw[1]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        weight[k] = weight[k] * share * 256.f;       // (256 / unit can be infinite)
+                        weight[k] *= share;
                         auto column = [&](int tile, int b) { return raw[k >> 1][4 * tile + 2 * (k & 1) + b]; };
 #pragma unroll
                         for (int e = 0; e < F; ++e)
@@ -474,6 +492,11 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     const uint32_t mask = *static_cast<volatile uint32_t *>(&s_mask[r]);
                     const int left = len - (int)(i * TOK);
+                    {
+                        const int token = lane << p.block_shift;  // of a block; does it have one, on a page that is there?
+                        const bool is = token < min(left, TOK) && (mask >> (token >> FS >> rows_shift & 31) & 1);
+                        apart = __any_sync(0xffffffffu, is && fabsf(fv[lane]) < 0.25f * unit);
+                    }
                     if (left < TOK || __popc(mask) < pieces) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -490,12 +513,25 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     float mx[HT];
 #pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        mx[h] = -INFINITY;
+                    for (int h = 0; h < HT; ++h) mx[h] = -INFINITY;
+                    if (!apart) {
 #pragma unroll
-                        for (int e = 0; e < F; ++e)
+                        for (int h = 0; h < HT; ++h)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) mx[h] = fmaxf(mx[h], x[e * HT + h][k]);
+                            for (int e = 0; e < F; ++e)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) mx[h] = fmaxf(mx[h], x[e * HT + h][k]);
+                    } else {                                      // (the queries' factors were there before S^T)
+                        float f[HT];
+                        ld_heads(qs + (item_no % QRING) * HB + h0, f);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float low = fmaxf(__log2f(fabsf(weight[k])), -40.f);
+#pragma unroll
+                            for (int h = 0; h < HT; ++h)
+#pragma unroll
+                                for (int e = 0; e < F; ++e) mx[h] = fmaxf(mx[h], fmaf(x[e * HT + h][k], f[h], low));
+                        }
                     }
                     int mine;
                     const float top = reduce_rows(mx, lane, mine, [](float a, float b) { return fmaxf(a, b); });
@@ -509,12 +545,12 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 if (!ok) break;
                 {   // a lane per head: its factor, the tile's maximum, what that is to the sums so far
                     const float mt = fmaxf(fmaxf(red[hl], red[HB + hl]), fmaxf(red[2 * HB + hl], red[3 * HB + hl]));
-                    const float f = qs[(item_no % QRING) * HB + hl], top = mt == -INFINITY ? mt : mt * f;
+                    const float f = qs[(item_no % QRING) * HB + hl], top = mt == -INFINITY || apart ? mt : mt * f;
                     const float mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn, less = ex2(m - mu);
                     if (lane < HB) {
                         st[hl] = f;
-                        st[HB + hl] = top == -INFINITY ? 0.f : top;
-                        st[2 * HB + hl] = ex2(top - mu);
+                        st[HB + hl] = top == -INFINITY ? 0.f : top - kTop;
+                        st[2 * HB + hl] = ex2(top - kTop - mu);
                         st[3 * HB + hl] = less;
                         if (q == 0) sm_m[wg * HB + hl] = top;
                     }
@@ -533,7 +569,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 ld_heads(st + HB + h0, top);
                 ld_heads(st + 2 * HB + h0, g);
                 constexpr int WB = L::BOTH ? 1 : HT / 4;          // 16-byte columns of a token, a word of this thread in each
-                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (4 * q + (lane >> 3)) * 8 * L::N + (lane & 7) * 16;
+                uint8_t *w8 = sm + L::P + wg * L::p_bytes + (4 * q + (lane >> 3)) * 8 * L::ON + (lane & 7) * 16;
 #pragma unroll
                 for (int e = 0; e < F; ++e)
 #pragma unroll
@@ -550,18 +586,18 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                                 w[j] = own * weight[k];
                             }
                             uint32_t h0_, l0_, h1_, l1_;
-                            split2(w[0], w[1], h0_, l0_);
+                            split2<true>(w[0], w[1], h0_, l0_);
                             if constexpr (L::BOTH) {
                                 hi[k] = h0_ | l0_ << 16;
                             } else {
-                                split2(w[2], w[3], h1_, l1_);
+                                split2<true>(w[2], w[3], h1_, l1_);
                                 hi[k] = h0_ | h1_ << 16;
                                 lo[k] = l0_ | l1_ << 16;
                             }
                         }
                         uint8_t *to = w8 + (e * WB + blk) * 128;
                         ptx::stmatrix4(ptx::smem_addr(to), hi[0], hi[1], hi[2], hi[3]);
-                        if constexpr (!L::BOTH) ptx::stmatrix4(ptx::smem_addr(to + L::p_part), lo[0], lo[1], lo[2], lo[3]);
+                        if constexpr (!L::BOTH) ptx::stmatrix4(ptx::smem_addr(to + 8 * L::N), lo[0], lo[1], lo[2], lo[3]);
                     }
                 if (q == 0 && lane == 0) sm_m[NG * HB + wg] = unit * 0x1p-8f;
                 ptx::fence_async_smem();
@@ -601,9 +637,12 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 if (works) {
                     ptx::tc_fence_after_sync();
                     const uint32_t from = tm_o(b) + ((uint32_t)q << 21) + (F == 2 ? (uint32_t)e * L::QN : 0u);
-                    float v[L::QN];
-                    if constexpr (L::QN == 16) ptx::tmem_ld16(from, v);
-                    else ptx::tmem_ld32(from, v);
+                    float v[16], x[16];                           // 16 columns of both parts (up to 8 heads: v has both)
+                    auto load = [&](int c) {
+                        ptx::tmem_ld16(from + c, v);
+                        if constexpr (!L::BOTH) ptx::tmem_ld16(from + L::N + c, x);
+                    };
+                    load(0);
                     const float top = sm_m[b * HB + hl], mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn;
                     __syncwarp();                                 // (the factors before have been read)
                     if (lane < HB) {
@@ -612,19 +651,23 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     m = mn;
                     __syncwarp();
-                    ptx::tmem_ld_wait(v);
 #pragma unroll
-                    for (int h = 0; h < HB; h += 4) {
-                        float f[4], g[4];
-                        ld4(st + h, f);
-                        ld4(st + HB + h, g);
-                        // heads h to h + 3 in the columns that the softmax threads write
+                    for (int c = 0; c < L::QN; c += 16) {
+                        if (c > 0) load(c);
+                        if constexpr (L::BOTH) ptx::tmem_ld_wait(v);
+                        else ptx::tmem_ld_wait(v, x);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float y = HB == 8    ? v[2 * h + 4 * (j >> 1) + (j & 1)] + v[2 * h + 4 * (j >> 1) + (j & 1) + 2]
-                                            : HB == 16 ? v[h + j]
-                                                       : v[16 * (h >> 2 & 1) + 4 * (h >> 3) + j];
-                            acc[h + j] = fmaf(acc[h + j], f[j], y * g[j]);
+                        for (int h = 0; h < HB; h += 4) {
+                            if (out_column<HB>(h) / 16 != c / 16) continue;
+                            float f[4], g[4];
+                            ld4(st + h, f);
+                            ld4(st + HB + h, g);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int at = out_column<HB>(h + j) % 16;
+                                const float y = fmaf(L::BOTH ? v[at + 2] : x[at], 1.f / kLow, v[at]);
+                                acc[h + j] = fmaf(acc[h + j], f[j], y * g[j]);
+                            }
                         }
                     }
                     ptx::tc_fence_before_sync();
@@ -661,7 +704,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     l = fmaf((x[0] + x[HB]) + (x[2 * HB] + x[3 * HB]), ex2(ms[g * HB] - mu), l);
                 }
                 __syncwarp();
-                // (a sum is 0, without a token, or at least 1, a maximum's own weight, or infinite or NaN)
+                // (a sum is 0, without a token, or about 1 at least, where m is, or infinite or NaN)
                 if (lane < HB) st[2 * HB + hl] = l > 0.f ? __fdividef(1.f, l) : l;
                 if (q == 0 && lane < hb) {
                     if (!whole) { part[2 * lane] = mh; part[2 * lane + 1] = l; }

@@ -217,13 +217,15 @@ size_t kda_paged_decode_q8_workspace_size(int num_seqs, int64_t max_tokens, int 
 
 /*
  * kda_paged_decode_q8 -- kda_paged_decode over a cache in 8 bits (q and out are of
- * dtype, the cache as for kda_paged_append_q8, with any finite scales):
+ * dtype, the cache as for kda_paged_append_q8, with any scales, for bf16 of up to
+ * 2^100 for K and 2^126 for V):
  *     s_t = scale k_scale_t (q . k_t),   out = sum_t softmax(s)_t v_scale_t v_t
  * Scores, maxima and sums are float32.  For bf16 the products are of e4m3 numbers on
  * the tensor cores: a query is the sum of two, exact down to 2^-11 of its head's
- * largest channel and off by 2^-18 of that below, and a softmax weight, with its
- * scale of V, the sum of two, which keeps eight bits, or 2^-18 of the largest of 128
- * to 256 neighbouring tokens.
+ * largest channel and off by 2^-18 of that below, and the product of a softmax weight
+ * and its scale of V the sum of two, off by 2^-8 of itself at most or 2^-21 of the
+ * largest such product of 128 to 256 neighbouring tokens (and 2^-61 of their largest
+ * weight times their largest scale, where those are not one token's).
  */
 kda_status_t kda_paged_decode_q8(const void *q, int64_t ldq, const void *k_cache, const void *v_cache,
                                  const float *k_scale, const float *v_scale, int num_pages,
