@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
     int64_t nt = tiles_of<TILE>(p, n);
     int item = (int)quotient(w - sp.cum * items, nt);
     int64_t tile = (w - sp.cum * items) - item * nt;
-    const float sc2 = p.scale * kLog2E;
+    // (a cache's scales can make up for a scale so small that the product of the two constants would not be precise)
+    const float sc2 = kScaled ? p.scale : p.scale * kLog2E, sc1 = kScaled ? kLog2E : 1.f;
     const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 4 == 0;
     const C *kc = static_cast<const C *>(p.kc), *vc = static_cast<const C *>(p.vc);
 
@@ -247,10 +248,10 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
                     const float4 x = h < hb ? *reinterpret_cast<const float4 *>(static_cast<const T *>(p.q) + (int64_t)n * p.ldq +
                                                                                 (int64_t)(hq0 + h) * D + l8 * CH + e)
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                    q[h][e] = x.x * sc2;
-                    q[h][e + 1] = x.y * sc2;
-                    q[h][e + 2] = x.z * sc2;
-                    q[h][e + 3] = x.w * sc2;
+                    q[h][e] = x.x * sc2 * sc1;
+                    q[h][e + 1] = x.y * sc2 * sc1;
+                    q[h][e + 2] = x.z * sc2 * sc1;
+                    q[h][e + 3] = x.w * sc2 * sc1;
                 }
         } else {
 #pragma unroll
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
 #pragma unroll
                 for (int e = 0; e < CH; ++e)
                     q[h][e] = h < hb ? to_f32(static_cast<const T *>(p.q)[(int64_t)n * p.ldq + (int64_t)(hq0 + h) * D +
-                                                                          Ch8<C, D>::channel(l8, e)]) * sc2
+                                                                          Ch8<C, D>::channel(l8, e)]) * sc2 * sc1
                                      : 0.f;
         }
         float m[HB], l[HB], acc[HB][CH];

@@ -354,7 +354,6 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
         const bool q16 = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 8 == 0;
         constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = HB / RPS < 1 ? 1 : HB / RPS;     // lanes per head, heads at a time
         const int c = lane % LPR;
-        const float sc2 = fabsf(p.scale) * kLog2E;
         while (ok && wk.more()) {
             const int64_t first = wk.tile, last = wk.last();
             const int kvh = nb == 1 ? wk.item : wk.item / nb, g0 = (wk.item - kvh * nb) * HB, hb = min(HB, p.G - g0);
@@ -416,7 +415,9 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     const int h = (i0 + i) * RPS + lane / LPR;
                     // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
                     const float f = power_for(__uint_as_float(top[i]));
-                    const float inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)), p.scale);
+                    // (a factor below 2^-126, of a scale of 0 too, would leave none to tell masked tokens by: it goes with them)
+                    const float factor = f * fabsf(p.scale) * kLog2E, least = factor < 0x1p-126f ? factor * 0x1p126f : 1.f;
+                    const float inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)) * least, p.scale);
                     const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         *reinterpret_cast<uint2 *>(dst + swizzled<D>(n, c >> 1) + (c & 1) * 8) =
                             make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
                         *reinterpret_cast<uint2 *>(low + (c & 1) * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                        if (c == 0) qs[(item_no % QRING) * HB + h] = f * sc2 < 0x1p-126f ? 0x1p-126f : f * sc2;
+                        if (c == 0) qs[(item_no % QRING) * HB + h] = factor < 0x1p-126f ? 0x1p-126f : factor;
                     }
                 }
             }
