@@ -94,17 +94,21 @@ struct PagedParams {
     void *out;
     float *lse;
     float *part;                    // partial results (workspace)
-    bool lone;                      // no item has more than one tile: nothing to join
+    bool lone;                      // no item has more than one tile, or the grid one CTA: nothing to join
     int expire;                     // test support
     uint32_t *status;
-    const float *ks, *vs;           // e4m3 caches: [num_pages][Hkv][page_size / block]
+};
+// An e4m3 cache.  (Parameters of their own: with three words more in PagedParams the kernels of float32 caches, which have
+// no use for them, spill 204 bytes instead of 88.)
+struct PagedQ8Params : PagedParams {
+    const float *ks, *vs;           // [num_pages][Hkv][page_size / block]
     int block_shift;
 };
 size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
 cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStream_t st);
-// an e4m3 cache; bf16: the queries and outputs
+// bf16: the queries and outputs
 size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d);
-cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_paged_decode_q8(const PagedQ8Params &p, int d, bool bf16, cudaStream_t st);
 
 struct AppendQ8Params {
     const void *k, *v;

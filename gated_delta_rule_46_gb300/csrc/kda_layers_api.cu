@@ -267,10 +267,10 @@ kda_status_t kda_paged_decode_q8(const void *q, int64_t ldq, const void *k_cache
     if (!workspace_ok(workspace, workspace_bytes,
                       kda_paged_decode_q8_workspace_size(num_seqs, (int64_t)max_pages * page_size, Hq, Hkv, d, dtype)))
         return KDA_ERR_INVALID_ARG;
-    kda::PagedParams p{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
-                       seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
-                       static_cast<float *>(workspace), false, 0, status, k_scale, v_scale,
-                       block_shift(block, page_size)};
+    kda::PagedQ8Params p{{q, ldq, k_cache, v_cache, num_pages, page_shift(page_size), page_table, max_pages,
+                          seq_lens, num_seqs, Hq, Hkv, Hq / Hkv, scale, out, lse,
+                          static_cast<float *>(workspace), false, 0, status},
+                         k_scale, v_scale, block_shift(block, page_size)};
     return from_cuda(kda::launch_paged_decode_q8(p, d, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 

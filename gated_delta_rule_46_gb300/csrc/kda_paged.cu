@@ -6,6 +6,8 @@
 // summed up by m = max s_t, l = sum e^{s_t - m} and a = sum e^{s_t - m} v_t; two
 // parts join as m = max(m1, m2), l = l1 e^{m1-m} + l2 e^{m2-m}, a likewise, and
 // the whole gives out = a / l, lse = m + log l.
+#include <type_traits>
+
 #include "kda_paged.cuh"
 #include "kda_tc_util.cuh"
 #include "kda_testing.h"
@@ -194,6 +196,7 @@ constexpr int ctas_q8(int HB) { return HB == 4 ? 2 : HB == 2 ? 3 : 4; }
 template <typename C, int D, int HB>
 struct Simt {
     static constexpr int CH = sizeof(C) == 1 ? 16 : 8;                     // channels of a lane
+    using Params = std::conditional_t<sizeof(C) == 1, PagedQ8Params, PagedParams>;
     // registers for as many
     static constexpr int CTAS = CH == 16 ? ctas_q8(HB) : 1;                // of an SM
     static constexpr int WARPS = CH == 16 ? 4 : HB == 4 ? 10 : 8;
@@ -203,7 +206,7 @@ struct Simt {
 };
 
 template <typename T, typename C, int D, int HB>
-__global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CTAS) paged_decode_simt_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CTAS) paged_decode_simt_kernel(const typename Simt<C, D, HB>::Params p) {
     using S = Simt<C, D, HB>;
     constexpr bool kScaled = sizeof(C) == 1;          // codes with a scale for each block of tokens
     constexpr int TILE = kTile, U = S::U, CH = S::CH, LPT = S::LPT, STEP = S::WARPS * S::TPW, NT = S::WARPS * 32;
@@ -215,10 +218,8 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE, (NT < 256 ? NT : 256)>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    if ((int)blockIdx.x >= sp.g) {
-        empty_sequences<T>(p, D);
-        return;
-    }
+    if (p.lone) empty_sequences_first<T, TILE>(p, D);     // (no join kernel follows to write them)
+    if ((int)blockIdx.x >= sp.g) return;
     int64_t w = quotient((int64_t)blockIdx.x * sp.W, sp.g);
     const int64_t w1 = quotient((int64_t)(blockIdx.x + 1) * sp.W, sp.g);
     int n = sp.n;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
                 }
             }
         };
-        auto fetch = [&](const C *cache, const float *scale, int t, const int (&pg)[U], Ch8<C, D> (&x)[U], float (&f)[U]) {
+        auto fetch = [&](const C *cache, [[maybe_unused]] const float *scale, int t, const int (&pg)[U], Ch8<C, D> (&x)[U], float (&f)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 x[u] = Ch8<C, D>();
@@ -302,8 +303,13 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
         float fk[U], fv[U];                               // (of scaled caches)
         int pg[U], pn[U];
         pages(t, pg);
-        fetch(kc, p.ks, t, pg, k, fk);
-        fetch(vc, p.vs, t, pg, v, fv);
+        const float *ks = nullptr, *vs = nullptr;
+        if constexpr (kScaled) {
+            ks = p.ks;
+            vs = p.vs;
+        }
+        fetch(kc, ks, t, pg, k, fk);
+        fetch(vc, vs, t, pg, v, fv);
         pages(t + U * STEP, pn);
         // the rounds of a warp's lanes are the same in number: the shuffles are the whole warp's
         const int t0 = (int)(first * TILE) + warp * S::TPW;
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
                     s[u][h] = kScaled ? a * fk[u] : a;
                 }
             }
-            fetch(kc, p.ks, t + U * STEP, pn, k, fk);
+            fetch(kc, ks, t + U * STEP, pn, k, fk);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
 #pragma unroll
                 for (int h = 0; h < HB; ++h) add(acc[h], kScaled ? s[u][h] * fv[u] : s[u][h], x);
             }
-            fetch(vc, p.vs, t + U * STEP, pn, v, fv);
+            fetch(vc, vs, t + U * STEP, pn, v, fv);
 #pragma unroll
             for (int u = 0; u < U; ++u) pg[u] = pn[u];
             pages(t + 2 * U * STEP, pn);
@@ -416,19 +422,21 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
             }
         }
     }
-    empty_sequences<T>(p, D);
 }
 
 // ---------------------------------------------------------------------------
 // Join: a CTA for each border between two CTAs' tiles.  An item that its border
 // is the first to cut is joined there, a warp per head; so there are as many CTAs
 // as items can be cut, whatever the batch (256 rows of up to 600 tokens, 16 query
-// heads: 93 us with a CTA for every row and eight heads, 80 so).  A long row has a
+// heads: 93 us with a CTA for every row and eight heads, 80 so; it takes 1.5 us longer itself).  A long row has a
 // part from nearly every CTA: their maxima and sums are read a part per lane and
 // joined by shuffles, then the weighted rows are summed in order, with as many
 // loads under way as the unrolling gives.
 // ---------------------------------------------------------------------------
-template <typename T, int D, int TILE, int HB>
+// EMPTY: sequences without tokens are written here too, beside the attention kernel, whose registers they would take
+// (64 rows of 8192 float32 tokens, 4 query heads each: 850 us with them at its end, 785 so).  The kernels before
+// that one have ended when this one starts, as it lets it start after its own wait for them.
+template <typename T, int D, int TILE, int HB, bool EMPTY>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int grid) {
     __shared__ int64_t s_sum[257];
     __shared__ int s_n;
@@ -436,6 +444,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
     constexpr int E = D / 32, U = 16;
     ptx::pdl_launch_dependents();    // what follows waits for this grid's end
+    if (EMPTY && blockIdx.y == 0) empty_sequences<T>(p, D);
     const Split sp = find_split<TILE>(p, items, grid, b, 0, s_sum, &s_n);
     // the item of the border's tile, from tile s on
     int64_t s = 0, nt = 0;
@@ -507,11 +516,11 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) / kLog2E;
 }
 
-template <typename T, int D, int TILE, int HB>
+template <typename T, int D, int TILE, int HB, bool EMPTY = false>
 static cudaError_t launch_join(const PagedParams &p, int grid, cudaStream_t st) {
     if (p.lone || grid == 1) return cudaSuccess;
     const int heads = p.G < HB ? p.G : HB;
-    return launch_dependent(paged_join_kernel<T, D, TILE, HB>, dim3((unsigned)grid - 1, (unsigned)((heads + 7) / 8)), 256, 0, st,
+    return launch_dependent(paged_join_kernel<T, D, TILE, HB, EMPTY>, dim3((unsigned)grid - 1, (unsigned)((heads + 7) / 8)), 256, 0, st,
                             1, p, grid);
 }
 
@@ -551,15 +560,15 @@ size_t paged_decode_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, 
 }
 
 template <typename T, typename C, int D, int HB>
-static cudaError_t paged_simt(PagedParams p, cudaStream_t st) {
+static cudaError_t paged_simt(typename Simt<C, D, HB>::Params p, cudaStream_t st) {
     using S = Simt<C, D, HB>;
-    p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile;
+    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, HB, S::CTAS);
+    p.lone = ((int64_t)p.max_pages << p.page_shift) <= kTile || grid == 1;
     auto *kernel = paged_decode_simt_kernel<T, C, D, HB>;
     cudaError_t e = allow_smem<paged_decode_simt_kernel<T, C, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
-    const int grid = grid_simt(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, HB, S::CTAS);
     if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
-    return launch_join<T, D, kTile, HB>(p, grid, st);
+    return launch_join<T, D, kTile, HB, true>(p, grid, st);
 }
 
 template <typename T>
@@ -578,14 +587,14 @@ cudaError_t launch_paged_decode(const PagedParams &p, int d, bool bf16, cudaStre
     const int HB = heads_tc(p.G), grid = grid_tc(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G);
     PagedParams pt = p;
     pt.expire = take_layers_expire(KDA_TESTING_PAGED);
-    pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc;
+    pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc || grid == 1;
     const cudaError_t e = launch_paged_decode_tc(pt, d, HB, grid, st);
     if (e != cudaSuccess) return e;
     if (d == 64)
-        return HB == 16 ? launch_join<__nv_bfloat16, 64, kTileTc, 16>(pt, grid, st)
-                        : launch_join<__nv_bfloat16, 64, kTileTc, 32>(pt, grid, st);
-    return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16>(pt, grid, st)
-                    : launch_join<__nv_bfloat16, 128, kTileTc, 32>(pt, grid, st);
+        return HB == 16 ? launch_join<__nv_bfloat16, 64, kTileTc, 16, true>(pt, grid, st)
+                        : launch_join<__nv_bfloat16, 64, kTileTc, 32, true>(pt, grid, st);
+    return HB == 16 ? launch_join<__nv_bfloat16, 128, kTileTc, 16, true>(pt, grid, st)
+                    : launch_join<__nv_bfloat16, 128, kTileTc, 32, true>(pt, grid, st);
 }
 
 // The 8-bit cache.  Query heads per item of its tensor-core form: half of the MMAs' columns.
@@ -598,13 +607,13 @@ static int grid_q8(int N, int64_t max_tokens, int Hkv, int G, int d) {
 // Of its CUDA-core form: the four that the registers hold with sixteen channels a lane, or the one or two that there are.
 static int heads_simt_q8(int G) { return G <= 2 ? G : 4; }
 template <typename T, int D>
-static cudaError_t paged_simt_q8(const PagedParams &p, cudaStream_t st) {
+static cudaError_t paged_simt_q8(const PagedQ8Params &p, cudaStream_t st) {
     using C = __nv_fp8_e4m3;
     const int HB = heads_simt_q8(p.G);
     return HB == 1 ? paged_simt<T, C, D, 1>(p, st) : HB == 2 ? paged_simt<T, C, D, 2>(p, st) : paged_simt<T, C, D, 4>(p, st);
 }
 template <typename T>
-static cudaError_t paged_dispatch_q8(const PagedParams &p, int d, cudaStream_t st) {
+static cudaError_t paged_dispatch_q8(const PagedQ8Params &p, int d, cudaStream_t st) {
     return d == 32 ? paged_simt_q8<T, 32>(p, st) : d == 64 ? paged_simt_q8<T, 64>(p, st) : paged_simt_q8<T, 128>(p, st);
 }
 
@@ -623,13 +632,13 @@ static cudaError_t join_q8(const PagedParams &p, int HB, int grid, cudaStream_t 
                       : launch_join<__nv_bfloat16, D, kTileTc * tokens_per_row(D, 32), 32>(p, grid, st);
 }
 
-cudaError_t launch_paged_decode_q8(const PagedParams &p, int d, bool bf16, cudaStream_t st) {
+cudaError_t launch_paged_decode_q8(const PagedQ8Params &p, int d, bool bf16, cudaStream_t st) {
     // (row coordinates of TMA copies are 32-bit)
     const bool tc = bf16 && p.num_pages > 0 && p.max_pages > 0 &&
                     ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
     if (!tc) return bf16 ? paged_dispatch_q8<__nv_bfloat16>(p, d, st) : paged_dispatch_q8<float>(p, d, st);
     const int HB = heads_q8(p.G), grid = grid_q8(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, d);
-    PagedParams pt = p;
+    PagedQ8Params pt = p;
     pt.expire = take_layers_expire(KDA_TESTING_PAGED);
     pt.lone = ((int64_t)p.max_pages << p.page_shift) <= kTileTc * tokens_per_row(d, HB);
     const cudaError_t e = launch_paged_decode_q8_tc(pt, d, HB, grid, st);

@@ -108,6 +108,20 @@ __device__ __forceinline__ void empty_sequences(const PagedParams &p, int D) {
     }
 }
 
+// The same by the whole of a CTA that has one in its turn, before anything else: for kernels that have no registers to
+// spare for it at their end.
+template <typename T, int TILE>
+__device__ __forceinline__ void empty_sequences_first(const PagedParams &p, int D) {
+    for (int n = blockIdx.x; n < p.N; n += gridDim.x)
+        if (tiles_of<TILE>(p, n) == 0) {
+            clamp_len(p, n, threadIdx.x == 0);
+            T *out = static_cast<T *>(p.out) + (int64_t)n * p.Hq * D;
+            for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x) out[i] = from_f32<T>(0.f);
+            if (p.lse)
+                for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) p.lse[(int64_t)n * p.Hq + i] = -INFINITY;
+        }
+}
+
 // One partial result of an item of HB query heads: m, l (base-2 logarithms) per
 // head, then, from 16 bytes on, a[d] per head.
 __host__ __device__ constexpr int part_head(int HB) { return (HB * 2 + 3) & ~3; }
@@ -119,6 +133,6 @@ cudaError_t launch_paged_decode_tc(const PagedParams &p, int d, int HB, int grid
 constexpr int kTileTc = 128;
 // e4m3 caches with bf16 queries; tokens of a row of its tiles, which have 128
 constexpr int tokens_per_row(int d, int HB) { return d < 128 && HB <= 16 ? 2 : 1; }
-cudaError_t launch_paged_decode_q8_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_q8_tc(const PagedQ8Params &p, int d, int HB, int grid, cudaStream_t st);
 
 }  // namespace kda

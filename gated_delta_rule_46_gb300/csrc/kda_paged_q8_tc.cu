@@ -178,7 +178,7 @@ __device__ __forceinline__ void ld_heads(const float *p, float (&x)[N]) {
 
 template <int D, int HB>
 __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
-    paged_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedParams p) {
+    paged_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const PagedQ8Params p) {
     using L = Lay<D, HB>;
     constexpr int NS = L::NS, LOADERS = L::LOADERS, F = L::F, FS = F - 1, TOK = L::TOK;
     extern __shared__ uint8_t smem_raw[];
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
 }
 
 template <int D, int HB>
-cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
+cudaError_t launch(const PagedQ8Params &p, int grid, cudaStream_t st) {
     CUtensorMap mk, mv;
     using L = Lay<D, HB>;
     const int shift = p.page_shift - (L::F - 1);
@@ -770,13 +770,13 @@ cudaError_t launch(const PagedParams &p, int grid, cudaStream_t st) {
     return launch_dependent(paged_decode_q8_tc_kernel<D, HB>, dim3(grid), L::THREADS, smem, st, 1, mk, mv, p);
 }
 template <int D>
-cudaError_t launch_h(const PagedParams &p, int HB, int grid, cudaStream_t st) {
+cudaError_t launch_h(const PagedQ8Params &p, int HB, int grid, cudaStream_t st) {
     return HB == 8 ? launch<D, 8>(p, grid, st) : HB == 16 ? launch<D, 16>(p, grid, st) : launch<D, 32>(p, grid, st);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_decode_q8_tc(const PagedParams &p, int d, int HB, int grid, cudaStream_t st) {
+cudaError_t launch_paged_decode_q8_tc(const PagedQ8Params &p, int d, int HB, int grid, cudaStream_t st) {
     return d == 32 ? launch_h<32>(p, HB, grid, st) : d == 64 ? launch_h<64>(p, HB, grid, st) : launch_h<128>(p, HB, grid, st);
 }
 

@@ -88,10 +88,8 @@ __global__ void __launch_bounds__(384, 1)
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    if ((int)blockIdx.x >= sp.g) {
-        empty_sequences<__nv_bfloat16>(p, D);
-        return;
-    }
+    if (p.lone) empty_sequences_first<__nv_bfloat16, TILE>(p, D);     // (no join kernel follows to write them)
+    if ((int)blockIdx.x >= sp.g) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBAR; ++i) {
             const bool four = (i >= PREADY && i < PREADY + 2) || (i >= OFREE && i < OFREE + 2) || i >= IREADY;
@@ -420,7 +418,6 @@ __global__ void __launch_bounds__(384, 1)
             wk.next_item(p, last - first);
         }
     }
-    empty_sequences<__nv_bfloat16>(p, D);
     if (!ok) {
         s_abort = 1;
         report_status(p.status, KDA_ERR_DEVICE_TIMEOUT);
