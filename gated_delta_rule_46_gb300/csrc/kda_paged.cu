@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
         int t = (int)(first * TILE) + warp * S::TPW + lane / LPT;         // this lane's token of the first round
 
         float q[HB][CH];
-        if (kScaled && sizeof(T) == 4 && q16) {           // (a lane's channels are neighbours)
+        if (kScaled && q16) {           // (a lane's channels are neighbours)
 #pragma unroll
             for (int h = 0; h < HB; ++h)
 #pragma unroll
@@ -606,15 +606,27 @@ static int grid_q8(int N, int64_t max_tokens, int Hkv, int G, int d) {
 
 // Of its CUDA-core form: the four that the registers hold with sixteen channels a lane, or the one or two that there are.
 static int heads_simt_q8(int G) { return G <= 2 ? G : 4; }
-template <typename T, int D>
+template <int D>
 static cudaError_t paged_simt_q8(const PagedQ8Params &p, cudaStream_t st) {
     using C = __nv_fp8_e4m3;
     const int HB = heads_simt_q8(p.G);
-    return HB == 1 ? paged_simt<T, C, D, 1>(p, st) : HB == 2 ? paged_simt<T, C, D, 2>(p, st) : paged_simt<T, C, D, 4>(p, st);
+    return HB == 1   ? paged_simt<float, C, D, 1>(p, st)
+           : HB == 2 ? paged_simt<float, C, D, 2>(p, st) : paged_simt<float, C, D, 4>(p, st);
 }
+
+// A cache without a page: no row has a token that could be read (its tensors have no address to make a map of either).
 template <typename T>
-static cudaError_t paged_dispatch_q8(const PagedQ8Params &p, int d, cudaStream_t st) {
-    return d == 32 ? paged_simt_q8<T, 32>(p, st) : d == 64 ? paged_simt_q8<T, 64>(p, st) : paged_simt_q8<T, 128>(p, st);
+__global__ void __launch_bounds__(256) paged_no_page_kernel(const PagedParams p, int D) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); n < p.N; n += (int64_t)gridDim.x * 8) {
+        if (lane == 0 && p.lens[n] != 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+        T *out = static_cast<T *>(p.out) + n * p.Hq * D;
+        for (int i = lane; i < p.Hq * D; i += 32) out[i] = from_f32<T>(0.f);
+        if (p.lse)
+            for (int i = lane; i < p.Hq; i += 32) p.lse[n * p.Hq + i] = -INFINITY;
+    }
 }
 
 size_t paged_decode_q8_workspace_bytes(int N, int64_t max_tokens, int Hq, int Hkv, int d) {
@@ -633,10 +645,12 @@ static cudaError_t join_q8(const PagedParams &p, int HB, int grid, cudaStream_t 
 }
 
 cudaError_t launch_paged_decode_q8(const PagedQ8Params &p, int d, bool bf16, cudaStream_t st) {
-    // (row coordinates of TMA copies are 32-bit)
-    const bool tc = bf16 && p.num_pages > 0 && p.max_pages > 0 &&
-                    ((int64_t)p.num_pages * p.Hkv << p.page_shift) < (int64_t(1) << 31);
-    if (!tc) return bf16 ? paged_dispatch_q8<__nv_bfloat16>(p, d, st) : paged_dispatch_q8<float>(p, d, st);
+    if (p.num_pages == 0 || p.max_pages == 0) {
+        const int64_t ctas = ((int64_t)p.N + 7) / 8, most = 8 * (int64_t)sm_count();
+        return launch_dependent(bf16 ? paged_no_page_kernel<__nv_bfloat16> : paged_no_page_kernel<float>,
+                                dim3((unsigned)(ctas < most ? ctas : most)), 256, 0, st, 1, static_cast<const PagedParams &>(p), d);
+    }
+    if (!bf16) return d == 32 ? paged_simt_q8<32>(p, st) : d == 64 ? paged_simt_q8<64>(p, st) : paged_simt_q8<128>(p, st);
     const int HB = heads_q8(p.G), grid = grid_q8(p.N, (int64_t)p.max_pages << p.page_shift, p.Hkv, p.G, d);
     PagedQ8Params pt = p;
     pt.expire = take_layers_expire(KDA_TESTING_PAGED);

@@ -250,9 +250,8 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-                // (rows before the first read as zeros, as those of a page that is missing)
-                const int y = page < 0 ? -TILE : (int)((((((int64_t)page * p.Hkv) + kvh) << p.page_shift) +
-                                                        (at & ((1 << p.page_shift) - 1))) >> FS);
+                // (a page before the first reads as zeros, as one that is missing)
+                const int y = (at & ((1 << p.page_shift) - 1)) >> FS;
                 // scales: a lane for each block of tokens
                 const int off = lane << p.block_shift, from = (int)(i * TOK) + off;
                 const int of = __shfl_sync(0xffffffffu, page, (off >> FS >> rows_shift) & 31);
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         ptx::mbar_arrive_expect_tx(full, L::tile);
                     }
                     __syncwarp();
-                    if (lane < pieces) ptx::tma_load_2d(dst, kv ? &mv : &mk, 0, y, full);
+                    if (lane < pieces) ptx::tma_load_4d(dst, kv ? &mv : &mk, 0, y, kvh, page, full);
                     if (kv == 0) {
                         if (lane < L::NBK) {
                             ptx::cp_async4(sc + r * L::NBK + lane, p.ks + at_scale, block);
@@ -760,9 +759,9 @@ cudaError_t launch(const PagedQ8Params &p, int grid, cudaStream_t st) {
     CUtensorMap mk, mv;
     using L = Lay<D, HB>;
     const int shift = p.page_shift - (L::F - 1);
-    const uint64_t rows = (uint64_t)p.num_pages * p.Hkv << shift;
     const uint32_t box = shift < 7 ? 1u << shift : TILE;
-    if (!make_map_bytes(&mk, p.kc, rows, L::RB, box) || !make_map_bytes(&mv, p.vc, rows, L::RB, box)) return cudaErrorInvalidValue;
+    for (const bool v : {false, true})
+        if (!make_map_pages(v ? &mv : &mk, v ? p.vc : p.kc, p.num_pages, p.Hkv, 1ull << shift, L::RB, box)) return cudaErrorInvalidValue;
     constexpr uint32_t smem = L::bytes + 1024;
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");    // (beside the static part)
     const cudaError_t e = allow_smem<paged_decode_q8_tc_kernel<D, HB>>(smem);

@@ -37,15 +37,18 @@ inline bool make_map_2d(CUtensorMap *m, const void *base, bool bf16, uint64_t ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A dense [rows][D] tensor of bytes, D = 32, 64 or 128, in boxes of whole rows with the swizzle of their size.
-inline bool make_map_bytes(CUtensorMap *m, const void *base, uint64_t rows, int D, uint32_t box_rows) {
+// A dense [pages][heads][rows][D] tensor of bytes, D = 32, 64 or 128, in boxes of whole rows with the swizzle of their
+// size.  (An axis each: rows of all pages counted in one would pass the 31 bits of a coordinate.)
+inline bool make_map_pages(CUtensorMap *m, const void *base, uint64_t pages, uint64_t heads, uint64_t rows, int D,
+                           uint32_t box_rows) {
     const TmapEncode enc = tmap_encode();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)D, rows}, strides[1] = {(cuuint64_t)D};
-    const cuuint32_t box[2] = {(cuuint32_t)D, box_rows}, one[2] = {1, 1};
+    const cuuint64_t dims[4] = {(cuuint64_t)D, rows, heads, pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)D, D * rows, D * rows * heads};
+    const cuuint32_t box[4] = {(cuuint32_t)D, box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
     const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                   : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, one,
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
