@@ -5,7 +5,8 @@ device and in the order of the stream.
 The state is three int32 tensors of the caller's: page_table [N, max_pages] (as
 for ``paged_append``; starts as -1), held [N] (pages that each row holds; starts
 as 0) and refs [P] (holders of each page; starts as 0, and a page is free where
-it is 0).  Checks, streams and errors are as in ``layers``.
+it is 0; a negative count, of a page of the caller's own, stays what it is).  Checks,
+streams and errors are as in ``layers``.
 """
 from __future__ import annotations
 
@@ -93,7 +94,7 @@ def pages_fork(pools, page_table, held, refs, lens, src, dst, page_size, workspa
 
 
 def pages_compact(pools, page_table, refs, page_map=None, live=None, workspace=None, status=None, stream=None):
-    """Moves the pages in use to the lowest ids in every tensor [P, ...] of `pools`, and the table (or None) and the
+    """Moves the pages in use (refs not 0) to the lowest ids in every tensor [P, ...] of `pools`, and the table (or None) and the
     counts with them.  Returns (page_map [P] int32: each page's new id, -1 for a free one; live [1] int32: pages in use)."""
     dev = _cuda(refs, "refs")
     P = _dims(refs, "refs", 1)[0]

@@ -13,9 +13,11 @@
  *   held        [num_rows] int32: pages that each row holds
  *   refs        [num_pages] int32: how many table entries (and other holders, which
  *               the caller may add) hold each page.  A page is free where it is 0;
- *               a negative count keeps it from ever being handed out, and these
- *               calls leave it as it is (pages of the caller's own, which rows may
- *               share for good)
+ *               a negative count keeps it from ever being handed out, and no call
+ *               changes the count (pages of the caller's own, which rows may share
+ *               for good); kda_pages_compact moves such a page as any other in use,
+ *               and its count with it, so that an id held outside the table has to
+ *               follow page_map
  * All start as -1, 0 and 0.  Free pages are handed out lowest first, rows and
  * pairs served in order: results depend on the arguments alone.
  *
@@ -93,9 +95,9 @@ kda_status_t kda_pages_fork(void *const *pools, const int64_t *page_bytes, int n
 size_t kda_pages_compact_workspace_size(int num_pages);
 
 /*
- * kda_pages_compact -- moves the pages in use (refs not 0) to the front of all
- * pools: of L of them, those with ids of L and more go, in order, to the free ones
- * below L; the others stay.  Table and counts follow.
+ * kda_pages_compact -- moves the pages in use (refs not 0, negative ones among them)
+ * to the front of all pools: of L of them, those with ids of L and more go, in order, to
+ * the free ones below L; the others stay.  Table and counts follow.
  *   pools, page_bytes: as for kda_pages_fork
  *   page_map    [num_pages] int32 (written): the new id of each page, -1 for one
  *               that was free
