@@ -21,11 +21,19 @@ from .layers import _call, _cuda, _dense, _dims, _size, _status
 _Tensor, _shape, _nbytes = torch.Tensor, attrgetter("shape"), attrgetter("nbytes")
 
 
-def _state(page_table, held, refs):
+def _fits(*sizes):
+    """The C interface's sizes are 32-bit: a larger one would be cut short on its way."""
+    for n in sizes:
+        if not 0 <= n < 1 << 31:
+            raise ValueError(f"a size of {n} is out of range")
+
+
+def _state(page_table, held, refs, page_size):
     """Device, rows, columns and pages, and the three pointers."""
     dev = _cuda(page_table, "page_table")
     N, cols = _dims(page_table, "page_table", 2)
     P = _dims(refs, "refs", 1)[0]
+    _fits(N, cols, P, page_size)
     return (dev, N, cols, P, _dense(page_table, "page_table", (N, cols), torch.int32, dev),
             _dense(held, "held", (N,), torch.int32, dev), _dense(refs, "refs", (P,), torch.int32, dev))
 
@@ -70,7 +78,7 @@ def _workspace(workspace, name, stream, dev, *sizes):
 def pages_resize(page_table, held, refs, tokens, page_size, workspace=None, status=None, stream=None):
     """Row i gets or gives back pages so that it holds those of tokens[i] tokens (int32; 0 ends the row, a negative
     number leaves it).  Free pages are handed out lowest first; held[i] says what a row has where they run out."""
-    dev, N, cols, P, tp, hp, rp = _state(page_table, held, refs)
+    dev, N, cols, P, tp, hp, rp = _state(page_table, held, refs, page_size)
     workspace, wp, size = _workspace(workspace, "kda_pages_resize_workspace_size", stream, dev, N, cols, P)
     _call("kda_pages_resize", dev, stream, (), tp, N, cols, hp, rp, P, _dense(tokens, "tokens", (N,), torch.int32, dev),
           page_size, wp, size, _status(status, dev))
@@ -82,7 +90,7 @@ def pages_fork(pools, page_table, held, refs, lens, src, dst, page_size, workspa
     """Row dst[i] goes on from the tokens of row src[i] (int32; negative: padding): it shares that row's full pages, and
     a partly filled last page is copied to a free one in every tensor [P, ...] of `pools`.  lens [N] int32: tokens of
     each row; lens[dst[i]] becomes lens[src[i]].  A destination holds no pages before, and is no other pair's row."""
-    dev, N, cols, P, tp, hp, rp = _state(page_table, held, refs)
+    dev, N, cols, P, tp, hp, rp = _state(page_table, held, refs, page_size)
     F = _dims(src, "src", 1)[0]
     ptrs, sizes = _pools(pools, P, dev)
     workspace, wp, size = _workspace(workspace, "kda_pages_fork_workspace_size", stream, dev, N, cols, F)
@@ -99,6 +107,7 @@ def pages_compact(pools, page_table, refs, page_map=None, live=None, workspace=N
     dev = _cuda(refs, "refs")
     P = _dims(refs, "refs", 1)[0]
     N, cols = (0, 0) if page_table is None else _dims(page_table, "page_table", 2)
+    _fits(N, cols, P)
     ptrs, sizes = _pools(pools, P, dev)
     new = []
     if page_map is None:
