@@ -196,6 +196,13 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned bl
 
 constexpr float kLog2E = 1.4426950408889634f;
 
+// The least power of two s with a <= 448 s (448 = 1.75 2^8, e4m3's largest value), and 2^-126 at least: s and 1 / s are
+// normal numbers.
+__device__ __forceinline__ float scale_for(float a) {
+    const int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;       // biased exponent
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }   // of 2^e
 // Two e4m3 codes, low byte first.
 __device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t u) {
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3)));

@@ -17,13 +17,7 @@ namespace {
 
 constexpr int WARPS = 8, ROWS = 16;               // of a CTA; tokens of a block that one warp works on
 
-// The least power of two s with a <= 448 s (448 = 1.75 2^8), and 2^-126 at least: both s and 1 / s are normal.
-__device__ __forceinline__ float scale_for(float a) {
-    const int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;       // biased exponent
-    return __uint_as_float((uint32_t)max(e, 1) << 23);
-}
 constexpr float kLeast = 0x1p-126f, kMost = 0x1p126f;                      // scales that an earlier call can have left
-__device__ __forceinline__ float inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }   // of 2^e
 
 // Eight values of a row as they are loaded.
 template <typename T, bool VEC>

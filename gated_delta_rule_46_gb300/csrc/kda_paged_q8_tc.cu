@@ -126,12 +126,6 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
     return (uint32_t)(row * D + ((chunk ^ (D == 128 ? row & 7 : D == 64 ? row >> 1 & 3 : row >> 2 & 1)) << 4));
 }
 
-// 2^e with a <= 448 2^e, and its inverse; at least 2^-126.
-__device__ __forceinline__ float power_for(float a) {
-    const int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;
-    return __uint_as_float((uint32_t)max(e, 1) << 23);
-}
-
 // Two values in two parts each; of weights, which come kLow times too large, the second stays so.  (What the first
 // leaves of a weight, at most 256, is at most 8.)
 constexpr float kLow = 32.f, kTop = 13.f;         // 2^13 = 256 kLow: the largest weight
@@ -413,10 +407,10 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                 for (int i = 0; i < U; ++i) {
                     const int h = (i0 + i) * RPS + lane / LPR;
                     // (a negative scale's sign goes with the queries, so that the largest product is the largest score)
-                    const float f = power_for(__uint_as_float(top[i]));
+                    const float f = scale_for(__uint_as_float(top[i]));
                     // (a factor below 2^-126, of a scale of 0 too, would leave none to tell masked tokens by: it goes with them)
                     const float factor = f * fabsf(p.scale) * kLog2E, least = factor < 0x1p-126f ? factor * 0x1p126f : 1.f;
-                    const float inv = copysignf(__uint_as_float((254u << 23) - __float_as_uint(f)) * least, p.scale);
+                    const float inv = copysignf(inverse(f) * least, p.scale);
                     const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
