@@ -16,18 +16,18 @@
 // whose products are added up.  For Q f is 1, and they share accumulators, or for up to 8
 // heads, where an MMA's 16 columns have room for both parts, are in neighbouring columns.  With
 // the largest of a head's channels at 224 or more that is exact for a bf16 query down to 2^-11
-// of it, and off by 2^-10, 2^-18 of the largest, below.  For P, at most 256, f is 32, and the
+// of it, and off by 2^-10, 2^-18 of the largest, below.  For P, at most 128, f is 32, and the
 // parts have columns of their own: eight bits of a weight are kept, as bf16 would, down to
-// 2^-10 of the largest, and 2^-23 of that (2^-15 of 256) below.
+// 2^-14 of the largest, and 2^-22 of that (2^-15 of 128) below.
 //
 // A token's scale of K multiplies its row of S^T.  Its scale of V goes into its
 // weight: with the tile's largest scale of V u and largest product of both m,
-//   m = max s + log v_scale / u,   P = 256 e^{s - m} v_scale / u,
-//   O = O_before e^{m_before - m_now} + u / 256 e^{m - m_now} V^T P
+//   m = max s + log v_scale / u,   P = 128 e^{s - m} v_scale / u,
+//   O = O_before e^{m_before - m_now} + u / 128 e^{m - m_now} V^T P
 // so that the weights use e4m3's range from the tile's largest on, whatever the rest of the row
 // holds and whichever tokens the largest score and the largest scale belong to.  Tiles do not
 // wait for each other's maxima: two groups of softmax warps work on tiles in turn.  Where a tile's
-// scales are within a factor of 4, as they mostly are, m is its largest score, which is as much
+// scales are within a factor of 2, as they mostly are, m is its largest score, which is as much
 // off at most (an error of 2^-21 of the largest); it is never taken more than 40 (base 2) below
 // the largest score, so that sums of e^{s - m} stay finite.  A softmax thread has
 // four rows and a quarter of the heads (TMEM's 16 x 256-bit reads), so that what is one for
@@ -98,7 +98,7 @@ struct Lay {
     static constexpr uint32_t P = Q + 2 * q_bytes, p_bytes = ON * TILE;
     static constexpr uint32_t SC = P + NG * p_bytes;                 // float: scales of K [RING][NBK], of V [RING][NBK]
     static constexpr uint32_t QS = SC + 2 * RING * NBK * 4;          // factors of the queries [QRING][HB]
-    static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [NG][HB], u / 256 [NG] (padded to 4)
+    static constexpr uint32_t M = QS + QRING * HB * 4;               // maxima of the tile [NG][HB], u [NG] (padded to 4)
     static constexpr uint32_t RED = M + NG * HB * 4 + 16;            // maxima of the warps [NG][2][4][HB]
     static constexpr uint32_t SUM = RED + NG * 8 * HB * 4;           // sums of the item [2][4 NG][HB], maxima [2][NG][HB]
     static constexpr uint32_t STAT = SUM + 10 * NG * HB * 4;         // of each softmax and output warp: [4][HB]
@@ -127,8 +127,11 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
 }
 
 // Two values in two parts each; of weights, which come kLow times too large, the second stays so.  (What the first
-// leaves of a weight, at most 256, is at most 8.)
-constexpr float kLow = 32.f, kTop = 13.f;         // 2^13 = 256 kLow: the largest weight
+// leaves of a weight, at most 256 with all rounding, is at most 8.)
+constexpr float kLow = 32.f;
+// Exponents of the largest weights, which scales of V then bring to 2^12 = 128 kLow.  (Taken from a score as large as 2^26 a
+// 16 leaves no rounding; and where the score itself is off by up to 1, from 2^24 on, a weight of 256 still has both parts.)
+constexpr float kTop = 16.f, kShare = 0.0625f;
 template <bool WEIGHT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     const __half2 w = __floats2half2_rn(x, y), first = WEIGHT ? __hmul2(w, __float2half2_rn(1.f / kLow)) : w;
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     }
                     // the tile's largest scale of V, 2^-126 at least (where a block has no token its scale is 0)
                     unit = fmaxf(ptx::warp_max(fabsf(lane < (TOK >> p.block_shift) ? fv[lane] : 0.f)), 0x1p-126f);
-                    const float share = __fdividef(1.f, unit);     // (the factor of 2^13 comes with the exponentials)
+                    const float share = __fdividef(kShare, unit);
                     ptx::tmem_ld_wait(raw[0], raw[1]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     {
                         const int token = lane << p.block_shift;  // of a block; does it have one, on a page that is there?
                         const bool is = token < min(left, TOK) && (mask >> (token >> FS >> rows_shift & 31) & 1);
-                        apart = __any_sync(0xffffffffu, is && fabsf(fv[lane]) < 0.25f * unit);
+                        apart = __any_sync(0xffffffffu, is && fabsf(fv[lane]) < 0.5f * unit);
                     }
                     if (left < TOK || __popc(mask) < pieces) {
 #pragma unroll
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         ld_heads(qs + (item_no % QRING) * HB + h0, f);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float low = fmaxf(__log2f(fabsf(weight[k])), -40.f);
+                            const float low = fmaxf(__log2f(fabsf(weight[k]) * (1.f / kShare)), -40.f);
 #pragma unroll
                             for (int h = 0; h < HT; ++h)
 #pragma unroll
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         st[3 * HB + hl] = less;
                         if (q == 0) sm_m[wg * HB + hl] = top;
                     }
-                    const bool any = __any_sync(0xffffffffu, less != 1.f && m != -INFINITY);
+                    const bool any = __any_sync(0xffffffffu, (less != 1.f && m != -INFINITY));
                     m = mn;
                     __syncwarp();
                     if (any) {
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                         ptx::stmatrix4(ptx::smem_addr(to), hi[0], hi[1], hi[2], hi[3]);
                         if constexpr (!L::BOTH) ptx::stmatrix4(ptx::smem_addr(to + 8 * L::N), lo[0], lo[1], lo[2], lo[3]);
                     }
-                if (q == 0 && lane == 0) sm_m[NG * HB + wg] = unit * 0x1p-8f;
+                if (q == 0 && lane == 0) sm_m[NG * HB + wg] = unit;
                 ptx::fence_async_smem();
                 warp_arrive(&bar[PREADY + wg]);
             }
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(Lay<D, HB>::THREADS, 1)
                     __syncwarp();                                 // (the factors before have been read)
                     if (lane < HB) {
                         st[hl] = ex2(m - mu);
-                        st[HB + hl] = ex2(top - mu) * sm_m[NG * HB + b];
+                        st[HB + hl] = ex2(top - kTop - mu) * (kLow / kShare) * sm_m[NG * HB + b];
                     }
                     m = mn;
                     __syncwarp();
