@@ -218,8 +218,15 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();     // the join kernel may start: it reads lengths before it waits
     const Split sp = find_split<TILE, (NT < 256 ? NT : 256)>(p, items, gridDim.x, blockIdx.x, 0, s_sum, &s_n);
-    if (p.lone) empty_sequences_first<T, TILE>(p, D);     // (no join kernel follows to write them)
-    if ((int)blockIdx.x >= sp.g) return;
+    if constexpr (kScaled) {          // (with registers to spare, at its end: 4 short rows 4.9 us, 5.3 ahead)
+        if ((int)blockIdx.x >= sp.g) {
+            empty_sequences<T>(p, D);
+            return;
+        }
+    } else {                          // by the join kernel, where one follows
+        if (p.lone) empty_sequences_first<T, TILE>(p, D);
+        if ((int)blockIdx.x >= sp.g) return;
+    }
     int64_t w = quotient((int64_t)blockIdx.x * sp.W, sp.g);
     const int64_t w1 = quotient((int64_t)(blockIdx.x + 1) * sp.W, sp.g);
     int n = sp.n;
@@ -422,6 +429,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
             }
         }
     }
+    if constexpr (kScaled) empty_sequences<T>(p, D);
 }
 
 // ---------------------------------------------------------------------------
@@ -568,7 +576,7 @@ static cudaError_t paged_simt(typename Simt<C, D, HB>::Params p, cudaStream_t st
     cudaError_t e = allow_smem<paged_decode_simt_kernel<T, C, D, HB>>(S::smem);
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(kernel, dim3(grid), S::WARPS * 32, S::smem, st, 1, p)) != cudaSuccess) return e;
-    return launch_join<T, D, kTile, HB, true>(p, grid, st);
+    return launch_join<T, D, kTile, HB, sizeof(C) != 1>(p, grid, st);
 }
 
 template <typename T>
