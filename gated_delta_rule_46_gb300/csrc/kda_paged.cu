@@ -105,9 +105,9 @@ cudaError_t launch_paged_append(AppendParams p, bool vec16, cudaStream_t st) {
 // of 16 bytes, half of the shuffles and products two at a time; items have up to four
 // heads, and CTAs four warps, of which an SM holds two to four, so that one's first loads
 // and joins overlap another's tokens.  64 rows of up to 4096 tokens, 8 key-value heads of
-// 128 channels, take 72 us with 1 query head each (107 in one CTA of 16 warps an SM, 219
-// with eight channels a lane), 142 with 4 (186, 228), 263 with 8 (351, 332) and 503 with
-// 16: 0.55, 0.28, 0.15 and 0.08 of the copy rate.  Conversions and products of a byte
+// 128 channels, take 73 us with 1 query head each (107 in one CTA of 16 warps an SM, 219
+// with eight channels a lane), 142 with 4 (186, 228), 265 with 8 (351, 332) and 503 with
+// 16: 0.54, 0.28, 0.15 and 0.08 of the copy rate.  Conversions and products of a byte
 // bound it (issue slots 52 % busy with the two warps a scheduler that registers allow).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;

@@ -42,15 +42,22 @@
 // Measured (8 key-value heads unless said): 64 rows of up to 16384 tokens, 4 query heads of
 // 128 channels each, 173 us, 0.91 of the copy rate; one row of 131072, 51 us (0.77), of which
 // about 12 are the start, the first loads' latency and the join; with 16 query heads and up
-// to 8192 tokens 95 us (0.83), 4 query heads of 64 channels 91 us (0.87), of 32 channels
-// 86 (0.46); 128 rows of up to 8192, 4 key-value heads with 16 query heads of 64 channels,
-// 69-71 us (0.56); 256 rows of up to 128 tokens 27 us.  What bounds the last is the softmax: 450 instructions a thread and tile
-// of 256 tokens, each seven cycles after the one before with two such warps a scheduler.  A
-// third group of softmax warps spills registers (73 -> 85 us), and gains nothing where the
-// scores are read from TMEM twice to need fewer (70.5 -> 73.4); moving what is freed from the
-// load and MMA warps to them with setmaxnreg makes no difference to the compiler (103 us).
-// Freeing stages by the consumers instead of a second commit: 141 -> 152 us (4 heads, 64
-// channels, in rows of one token).
+// to 8192 tokens 98 us (0.81), 4 query heads of 64 channels 92 us (0.86), of 32 channels
+// 89 (0.45); 128 rows of up to 8192, 4 key-value heads with 16 query heads of 64 channels,
+// 74 us (0.53); 64 rows of up to 16384, 2 key-value heads with 32 query heads of 128 channels 70
+// (0.57), of 64 channels 63 (0.32); 256 rows of up to 128 tokens 28 us.
+// What bounds 16 heads of 64 channels is the softmax: a chain of some 450 instructions a thread and
+// tile of 256 tokens, each about seven cycles after the one before with two such warps a
+// scheduler (issue slots 49 %, no pipe above 40 %).  A third group of softmax warps spills
+// registers (73 -> 85 us), and gains nothing where the scores are read from TMEM twice to need
+// fewer (70.5 -> 73.4); moving what is freed from the load and MMA warps to them with setmaxnreg
+// makes no difference to the compiler (103 us).  Freeing stages by the consumers instead of a
+// second commit: 141 -> 152 us (4 heads, 64 channels, in rows of one token).
+// Second parts of the weights with a step and columns of their own, and the largest product
+// instead of the two maxima, cost 16 heads of 64 channels 70.6 -> 74.4 us, 4 heads of 32 channels
+// 85.8 -> 88.5, short rows 27.4 -> 28.5 and long ones of 128 channels nothing; the reciprocal of u by
+// an IEEE division cost 2 to 4 us more, the weights' power of two at the weights 0.5, room for
+// large scores per tile instead of in the exponents' offset 1 to 3.5 %.
 #include <cuda.h>
 
 #include "kda_paged_tc.cuh"

@@ -23,7 +23,7 @@ extern "C" {
 /* and of the operators in kda_layers.h, where they run on the tensor cores: */
 #define KDA_TESTING_LINEAR 32      /* kda_linear */
 #define KDA_TESTING_DECAY 64       /* kda_decay_prefill */
-#define KDA_TESTING_PAGED 128      /* kda_paged_decode */
+#define KDA_TESTING_PAGED 128      /* kda_paged_decode, kda_paged_decode_q8 */
 
 /*
  * kda_testing_expire_next_wait -- arms a simulated wait expiry for the next
