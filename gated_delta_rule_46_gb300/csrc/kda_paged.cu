@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(Simt<C, D, HB>::WARPS * 32, Simt<C, D, HB>::CT
 // Join: a CTA for each border between two CTAs' tiles.  An item that its border
 // is the first to cut is joined there, a warp per head; so there are as many CTAs
 // as items can be cut, whatever the batch (256 rows of up to 600 tokens, 16 query
-// heads: 93 us with a CTA for every row and eight heads, 80 so; it takes 1.5 us longer itself).  A long row has a
+// heads: 93 us with a CTA for every row and eight heads, 80 so).  A long row has a
 // part from nearly every CTA: their maxima and sums are read a part per lane and
 // joined by shuffles, then the weighted rows are summed in order, with as many
 // loads under way as the unrolling gives.
@@ -450,7 +450,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     __shared__ int s_n;
     const int b = blockIdx.x + 1, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nb = (p.G + HB - 1) / HB, items = p.Hkv * nb;
-    constexpr int E = D / 32, U = 16;
+    // Parts under way: with up to 32 heads, four CTAs a border, registers for four CTAs of an SM count more (64 rows of
+    // 8192 tokens, 2 x 32 heads: 98.2 us with 16, 96.5 with 8; one row of 131072: 41.1, 39.5); with fewer, one row of
+    // 131072 and 8 x 4 heads takes 53.9 with 16, 55.5 with 8.
+    constexpr int E = D / 32, U = HB > 16 ? 8 : 16;
     ptx::pdl_launch_dependents();    // what follows waits for this grid's end
     if (EMPTY && blockIdx.y == 0) empty_sequences<T>(p, D);
     const Split sp = find_split<TILE>(p, items, grid, b, 0, s_sum, &s_n);

@@ -44,8 +44,8 @@
 // about 12 are the start, the first loads' latency and the join; with 16 query heads and up
 // to 8192 tokens 98 us (0.81), 4 query heads of 64 channels 92 us (0.86), of 32 channels
 // 89 (0.45); 128 rows of up to 8192, 4 key-value heads with 16 query heads of 64 channels,
-// 74 us (0.53); 64 rows of up to 16384, 2 key-value heads with 32 query heads of 128 channels 70
-// (0.57), of 64 channels 63 (0.32); 256 rows of up to 128 tokens 28 us.
+// 74 us (0.53); 64 rows of up to 16384, 2 key-value heads with 32 query heads of 128 channels 67
+// (0.59), of 64 channels 62 (0.32); 256 rows of up to 128 tokens 28 us.
 // What bounds 16 heads of 64 channels is the softmax: a chain of some 450 instructions a thread and
 // tile of 256 tokens, each about seven cycles after the one before with two such warps a
 // scheduler (issue slots 49 %, no pipe above 40 %).  A third group of softmax warps spills

@@ -52,6 +52,8 @@ def test_rows_past_31_bits(d, H, ps, B, G):
         wo, wl = ref.decode(q, kc, kc, ks, ks, small, lens, d ** -0.5)
         ref.close("out", out, wo)
         layers_ref.close("lse", lse, wl)
+    del cache
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
